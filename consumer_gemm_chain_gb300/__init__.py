@@ -42,3 +42,22 @@ from .chain import (  # noqa: F401
     cs_tune_size,
     decode_unit,
 )
+from .kv import (  # noqa: F401
+    CS_KV_ADJACENT,
+    CS_KV_HALF,
+    CS_KV_HEAD,
+    CS_KV_TOKEN,
+    KVBatch,
+    KVPlan,
+    cs_attn_cached_forward,
+    cs_kv_abi_version,
+    cs_kv_append,
+    cs_kv_attention,
+    cs_kv_attention_shared,
+    cs_kv_batch,
+    cs_kv_desc_init,
+    cs_kv_destroy,
+    cs_kv_plan,
+    cs_kv_reset,
+    cs_kv_status,
+)

@@ -20,8 +20,8 @@ LIB = os.path.join(LIBDIR, "libcs_chain.so")
 LIB_NOMC = os.path.join(LIBDIR, "libcs_chain_nomc.so")
 # (library, extra nvcc defines)
 VARIANTS = ((LIB, []), (LIB_NOMC, ["-DCS_NO_CLUSTER_MULTICAST"]))
-SOURCES = ["cs_chain.cu", "cs_tune.cpp"]
-DEPS = ["cs_chain.cu", "cs_kernel.cuh", "cs_ptx.cuh", "cs_sched.cuh", "cs_tune.cpp", "cs_tune.h"]
+SOURCES = ["cs_chain.cu", "cs_kv.cu", "cs_tune.cpp"]
+DEPS = ["cs_chain.cu", "cs_kernel.cuh", "cs_kv.cu", "cs_kv_kernel.cuh", "cs_ptx.cuh", "cs_sched.cuh", "cs_tune.cpp", "cs_tune.h"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
 
@@ -36,7 +36,7 @@ def _stale(lib: str) -> bool:
     if not os.path.exists(lib):
         return True
     t = os.path.getmtime(lib)
-    deps = [os.path.join(CSRC, d) for d in DEPS] + [os.path.join(ROOT, "include", "cs_chain.h")]
+    deps = [os.path.join(CSRC, d) for d in DEPS] + [os.path.join(ROOT, "include", h) for h in ("cs_chain.h", "cs_kv.h")]
     return any(os.path.exists(d) and os.path.getmtime(d) > t for d in deps)
 
 

@@ -152,6 +152,8 @@ struct cs_chain_s {
   bool error_latched = false;
 };
 
+const cs_chain_desc* cs_chain_desc_of(cs_chain_t plan) { return &plan->d; }
+
 namespace {
 
 PFN_cuTensorMapEncodeTiled_v12000 get_encode() {

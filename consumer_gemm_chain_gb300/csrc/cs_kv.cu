@@ -1,0 +1,398 @@
+// Host side of the paged key/value cache operators (include/cs_kv.h): plans,
+// argument checks, launches and status.
+#include <cuda.h>
+#include <cuda_runtime.h>
+
+#include <cmath>
+#include <cstring>
+#include <new>
+
+#include "../../include/cs_kv.h"
+#include "cs_kv_kernel.cuh"
+#include "cs_tune.h"  // cs_fail
+
+#define KV_CUDA(call)                                                                              \
+  do {                                                                                             \
+    cudaError_t e_ = (call);                                                                       \
+    if (e_ != cudaSuccess) return cs_fail(CS_ERR_CUDA, "%s: %s", #call, cudaGetErrorString(e_));   \
+  } while (0)
+
+struct cs_kv_s {
+  cs_kv_desc d{};
+  int device = 0, num_sms = 0;
+  uint32_t* ctrl = nullptr;  // error words, then the counters
+  size_t ctrl_words = 0;
+  bool error_latched = false;
+};
+
+namespace {
+
+constexpr int kMaxSeqs = 8192;
+constexpr int kMaxKeys = 1 << 22;
+
+// The plan's device is current while a call of it runs.
+struct DeviceGuard {
+  int was = -1;
+  bool ok = true;
+  explicit DeviceGuard(int device) {
+    int cur = -1;
+    ok = cudaGetDevice(&cur) == cudaSuccess;
+    if (ok && cur != device) {
+      ok = cudaSetDevice(device) == cudaSuccess;
+      was = cur;
+    }
+  }
+  ~DeviceGuard() {
+    if (was >= 0) cudaSetDevice(was);
+  }
+};
+
+cs_status validate(const cs_kv_desc* d) {
+  if (!d) return cs_fail(CS_ERR_INVALID_ARG, "desc is NULL");
+  if (d->dtype != CS_F16 && d->dtype != CS_BF16) return cs_fail(CS_ERR_INVALID_ARG, "bad dtype %d", d->dtype);
+  if (d->heads < 1 || d->heads > 1024) return cs_fail(CS_ERR_INVALID_ARG, "heads=%d (1..1024)", d->heads);
+  if (d->kv_heads < 1 || d->heads % d->kv_heads != 0)
+    return cs_fail(CS_ERR_INVALID_ARG, "kv_heads=%d does not divide heads=%d", d->kv_heads, d->heads);
+  if (d->heads / d->kv_heads > 128)
+    return cs_fail(CS_ERR_UNSUPPORTED, "%d query heads per key head (at most 128)", d->heads / d->kv_heads);
+  if (d->head_dim != 64 && d->head_dim != 128) return cs_fail(CS_ERR_UNSUPPORTED, "head_dim=%d (64 or 128)", d->head_dim);
+  if (d->page_size != 16 && d->page_size != 32 && d->page_size != 64 && d->page_size != 128)
+    return cs_fail(CS_ERR_UNSUPPORTED, "page_size=%d (16, 32, 64 or 128)", d->page_size);
+  if (d->num_pages < 1 || d->num_pages > (1 << 27)) return cs_fail(CS_ERR_INVALID_ARG, "num_pages=%d (1..2^27)", d->num_pages);
+  if (d->cache_layout != CS_KV_TOKEN && d->cache_layout != CS_KV_HEAD)
+    return cs_fail(CS_ERR_INVALID_ARG, "bad cache_layout %d", d->cache_layout);
+  if (d->max_tokens < 1 || d->max_tokens > (1 << 20))
+    return cs_fail(CS_ERR_INVALID_ARG, "max_tokens=%d (1..2^20)", d->max_tokens);
+  if (d->max_seqs < 1 || d->max_seqs > kMaxSeqs) return cs_fail(CS_ERR_INVALID_ARG, "max_seqs=%d (1..%d)", d->max_seqs, kMaxSeqs);
+  if (d->rotary_dim < 0 || d->rotary_dim > d->head_dim || d->rotary_dim % 16 != 0)
+    return cs_fail(CS_ERR_INVALID_ARG, "rotary_dim=%d (a multiple of 16 up to head_dim)", d->rotary_dim);
+  if (d->rotary_pairing != CS_KV_HALF && d->rotary_pairing != CS_KV_ADJACENT)
+    return cs_fail(CS_ERR_INVALID_ARG, "bad rotary_pairing %d", d->rotary_pairing);
+  if (d->window < 0) return cs_fail(CS_ERR_INVALID_ARG, "window=%d", d->window);
+  if (d->sinks < 0) return cs_fail(CS_ERR_INVALID_ARG, "sinks=%d", d->sinks);
+  if (!(d->scale >= 0.0f) || std::isinf(d->scale))
+    return cs_fail(CS_ERR_INVALID_ARG, "scale=%g (positive, or 0 for 1/sqrt(head_dim))", d->scale);
+  if (d->shared != 0 && d->shared != 1) return cs_fail(CS_ERR_INVALID_ARG, "shared=%d (0 or 1)", d->shared);
+  if (d->shared && d->window > 0) return cs_fail(CS_ERR_UNSUPPORTED, "a shared prefix is built without a window");
+  if (d->num_sms < 0) return cs_fail(CS_ERR_INVALID_ARG, "num_sms=%d", d->num_sms);
+  return CS_OK;
+}
+
+bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
+
+// Row stride of a token-indexed tensor `width` wide: the default, or what the caller gave.
+cs_status row_stride(const char* name, long long given, long long width, long long* stride) {
+  *stride = given == 0 ? width : given;
+  if (*stride < width || *stride % 8 != 0 || *stride > (1ll << 32))
+    return cs_fail(CS_ERR_INVALID_ARG, "%s=%lld (0, or a multiple of 8 from %lld on)", name, given, width);
+  return CS_OK;
+}
+
+cs_status check_batch(const cs_kv_s* p, const cs_kv_batch* b) {
+  if (!b) return cs_fail(CS_ERR_INVALID_ARG, "batch is NULL");
+  if (b->tokens < 0 || b->tokens > p->d.max_tokens)
+    return cs_fail(CS_ERR_INVALID_ARG, "tokens=%d (the plan holds %d)", b->tokens, p->d.max_tokens);
+  if (b->seqs < 0 || b->seqs > p->d.max_seqs)
+    return cs_fail(CS_ERR_INVALID_ARG, "seqs=%d (the plan holds %d)", b->seqs, p->d.max_seqs);
+  if (b->max_q < 1) return cs_fail(CS_ERR_INVALID_ARG, "max_q=%d", b->max_q);
+  if (b->table_cols < 0 || static_cast<long long>(b->table_cols) * p->d.page_size > kMaxKeys)
+    return cs_fail(CS_ERR_INVALID_ARG, "table_cols=%d (at most %d keys)", b->table_cols, kMaxKeys);
+  if (b->tokens > 0 && b->seqs > 0 && (!b->cu_q || !b->kv_lens || (!b->page_table && b->table_cols > 0)))
+    return cs_fail(CS_ERR_INVALID_ARG, "cu_q, kv_lens and page_table are required");
+  return CS_OK;
+}
+
+cskv::Batch device_batch(const cs_kv_s* p, const cs_kv_batch* b) {
+  const cs_kv_desc& d = p->d;
+  cskv::Batch B{};
+  B.cu_q = b->cu_q;
+  B.kv_lens = b->kv_lens;
+  B.table = b->page_table;
+  B.tokens = b->tokens;
+  B.seqs = b->seqs;
+  B.max_q = b->max_q;
+  B.table_cols = b->table_cols;
+  B.heads = d.heads;
+  B.kv_heads = d.kv_heads;
+  B.group = d.heads / d.kv_heads;
+  B.page_size = d.page_size;
+  B.page_shift = __builtin_ctz(static_cast<unsigned>(d.page_size));
+  B.num_pages = d.num_pages;
+  B.page_stride = static_cast<long long>(d.page_size) * d.kv_heads * d.head_dim;
+  B.slot_stride = d.cache_layout == CS_KV_TOKEN ? static_cast<long long>(d.kv_heads) * d.head_dim : d.head_dim;
+  B.head_stride = d.cache_layout == CS_KV_TOKEN ? d.head_dim : static_cast<long long>(d.page_size) * d.head_dim;
+  B.ctrl = p->ctrl;
+  return B;
+}
+
+// A launch that may be scheduled while the preceding grid drains: every kernel
+// here waits for that grid (griddepcontrol.wait) before it touches global memory.
+cs_status launch(const void* fn, dim3 grid, int threads, int smem, void* params, cudaStream_t stream) {
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3(threads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  void* args[] = {params};
+  const cudaError_t e = cudaLaunchKernelExC(&cfg, fn, args);
+  if (e != cudaSuccess) return cs_fail(CS_ERR_CUDA, "kernel launch: %s", cudaGetErrorString(e));
+  return CS_OK;
+}
+
+cs_status check_caches(const void* k, const void* v) {
+  if (!k || !v) return cs_fail(CS_ERR_INVALID_ARG, "k_cache and v_cache are required");
+  if (!aligned16(k) || !aligned16(v)) return cs_fail(CS_ERR_INVALID_ARG, "the caches must be 16-byte aligned");
+  return CS_OK;
+}
+
+cs_status check_attn(const cs_kv_s* p, const cs_kv_batch* b, const cs_kv_attn_args* a, cskv::AttnP& k) {
+  if (!a) return cs_fail(CS_ERR_INVALID_ARG, "args is NULL");
+  const long long width = static_cast<long long>(p->d.heads) * p->d.head_dim;
+  std::memset(&k, 0, sizeof(k));
+  cs_status s = check_caches(a->k_cache, a->v_cache);
+  if (s != CS_OK) return s;
+  if ((s = row_stride("q_stride", a->q_stride, width, &k.q_stride)) != CS_OK) return s;
+  if ((s = row_stride("out_stride", a->out_stride, width, &k.out_stride)) != CS_OK) return s;
+  if (b->tokens > 0 && (!a->q || !a->out)) return cs_fail(CS_ERR_INVALID_ARG, "q and out are required");
+  if (!aligned16(a->q) || !aligned16(a->out)) return cs_fail(CS_ERR_INVALID_ARG, "q and out must be 16-byte aligned");
+  if (a->q && a->q == a->out) return cs_fail(CS_ERR_INVALID_ARG, "out must not be q");
+  k.b = device_batch(p, b);
+  k.q = a->q;
+  k.k_cache = a->k_cache;
+  k.v_cache = a->v_cache;
+  k.out = a->out;
+  k.lse = a->lse;
+  k.window = p->d.window;
+  k.sinks = p->d.sinks;
+  const double scale = p->d.scale > 0.0f ? p->d.scale : 1.0 / std::sqrt(static_cast<double>(p->d.head_dim));
+  k.scale_log2 = static_cast<float>(scale * 1.4426950408889634);
+  return CS_OK;
+}
+
+cs_status run_attention(cs_kv_s* p, cskv::AttnP& k, cudaStream_t st) {
+  if (k.b.tokens == 0 || k.b.seqs == 0) return CS_OK;
+  const bool bf16 = p->d.dtype == CS_BF16, wide = p->d.head_dim == 128;
+  const void* fn =
+      bf16 ? (wide ? (const void*)cskv::cs_kv_attn_rows<__nv_bfloat16, 128> : (const void*)cskv::cs_kv_attn_rows<__nv_bfloat16, 64>)
+           : (wide ? (const void*)cskv::cs_kv_attn_rows<__half, 128> : (const void*)cskv::cs_kv_attn_rows<__half, 64>);
+  const long long rows = static_cast<long long>(k.b.tokens) * k.b.heads;
+  return launch(fn, dim3(static_cast<unsigned>((rows + 3) / 4)), 128, 0, &k, st);
+}
+
+cs_status append(cs_kv_s* p, const cs_kv_batch* b, const cs_kv_append_args* a, cudaStream_t st) {
+  if (!a) return cs_fail(CS_ERR_INVALID_ARG, "args is NULL");
+  const cs_kv_desc& d = p->d;
+  cs_status s = check_caches(a->k_cache, a->v_cache);
+  if (s != CS_OK) return s;
+  if (b->tokens > 0 && (!a->qkv || !a->q_out)) return cs_fail(CS_ERR_INVALID_ARG, "qkv and q_out are required");
+  if (!aligned16(a->qkv) || !aligned16(a->q_out)) return cs_fail(CS_ERR_INVALID_ARG, "qkv and q_out must be 16-byte aligned");
+  const long long q_width = static_cast<long long>(d.heads) * d.head_dim;
+  const long long width = q_width + 2ll * d.kv_heads * d.head_dim;
+  cskv::AppendP k;
+  std::memset(&k, 0, sizeof(k));
+  if ((s = row_stride("qkv_stride", a->qkv_stride, width, &k.qkv_stride)) != CS_OK) return s;
+  if ((s = row_stride("q_stride", a->q_stride, q_width, &k.q_stride)) != CS_OK) return s;
+  if (b->tokens > 0 && !(a->q_out == a->qkv && k.q_stride == k.qkv_stride)) {
+    // not in place: the rows must lie apart
+    const char* x0 = static_cast<const char*>(a->qkv);
+    const char* x1 = x0 + 2 * ((b->tokens - 1) * k.qkv_stride + width);
+    const char* y0 = static_cast<const char*>(a->q_out);
+    const char* y1 = y0 + 2 * ((b->tokens - 1) * k.q_stride + q_width);
+    if (x0 < y1 && y0 < x1) return cs_fail(CS_ERR_INVALID_ARG, "q_out overlaps qkv without being its Q part");
+  }
+  if (d.rotary_dim > 0) {
+    if (!a->rope || a->rope_rows < 1) return cs_fail(CS_ERR_INVALID_ARG, "rope is required (rotary_dim=%d)", d.rotary_dim);
+    if (!aligned16(a->rope)) return cs_fail(CS_ERR_INVALID_ARG, "rope must be 16-byte aligned");
+  }
+  if (b->tokens == 0 || b->seqs == 0) return CS_OK;
+  k.b = device_batch(p, b);
+  k.qkv = static_cast<const uint4*>(a->qkv);
+  k.q_out = static_cast<uint4*>(a->q_out);
+  k.k_cache = static_cast<uint4*>(a->k_cache);
+  k.v_cache = static_cast<uint4*>(a->v_cache);
+  k.rope = reinterpret_cast<const float4*>(a->rope);
+  k.positions = a->positions;
+  k.qkv_stride >>= 3;
+  k.q_stride >>= 3;
+  k.rope_rows = a->rope_rows;
+  k.rotary_dim = d.rotary_dim;
+  k.half = d.rotary_pairing == CS_KV_HALF;
+  k.head_chunks = d.head_dim / 8;
+  k.units = (d.heads + 2 * d.kv_heads) * (d.head_dim / 16);
+  k.tokens_per_block = 1;
+  const dim3 grid(b->tokens, 1);
+  const void* fn = d.dtype == CS_BF16 ? (const void*)cskv::cs_kv_append_kernel<__nv_bfloat16>
+                                      : (const void*)cskv::cs_kv_append_kernel<__half>;
+  return launch(fn, grid, cskv::APPEND_THREADS, 0, &k, st);
+}
+
+cs_status begin(cs_kv_s* p, const cs_kv_batch* b) {
+  if (!p) return cs_fail(CS_ERR_INVALID_ARG, "plan is NULL");
+  if (p->error_latched) return cs_fail(CS_ERR_NEEDS_RESET, "plan holds a device error; call cs_kv_reset");
+  return check_batch(p, b);
+}
+
+void free_plan(cs_kv_s* p) {
+  cudaFree(p->ctrl);
+  delete p;
+}
+
+}  // namespace
+
+extern "C" {
+
+int cs_kv_abi_version(void) { return CS_KV_ABI_VERSION; }
+
+cs_status cs_kv_desc_init(cs_kv_desc* d) {
+  if (!d) return cs_fail(CS_ERR_INVALID_ARG, "desc is NULL");
+  std::memset(d, 0, sizeof(*d));
+  d->dtype = CS_F16;
+  d->head_dim = 128;
+  d->page_size = 16;
+  return CS_OK;
+}
+
+cs_status cs_kv_plan(const cs_kv_desc* desc, cs_kv_t* out) {
+  if (!out) return cs_fail(CS_ERR_INVALID_ARG, "out is NULL");
+  *out = nullptr;
+  cs_status s = validate(desc);
+  if (s != CS_OK) return s;
+  int dev = 0, sms = 0, major = 0, minor = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess || cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
+    return cs_fail(CS_ERR_CUDA, "no CUDA device available");
+  cudaDeviceGetAttribute(&major, cudaDevAttrComputeCapabilityMajor, dev);
+  cudaDeviceGetAttribute(&minor, cudaDevAttrComputeCapabilityMinor, dev);
+  if (major * 10 + minor != 103)
+    return cs_fail(CS_ERR_UNSUPPORTED, "device is sm_%d%d; this library is built for sm_103a only", major, minor);
+  cs_kv_s* p = new (std::nothrow) cs_kv_s();
+  if (!p) return cs_fail(CS_ERR_OOM, "host allocation failed");
+  p->d = *desc;
+  p->device = dev;
+  p->num_sms = desc->num_sms > 0 && desc->num_sms < sms ? desc->num_sms : sms;
+  p->ctrl_words = cskv::CTRL_COUNTERS;
+  if (cudaMalloc(reinterpret_cast<void**>(&p->ctrl), p->ctrl_words * 4) != cudaSuccess) {
+    cudaGetLastError();
+    free_plan(p);
+    return cs_fail(CS_ERR_OOM, "cudaMalloc of the plan's workspace failed");
+  }
+  if (cudaMemset(p->ctrl, 0, p->ctrl_words * 4) != cudaSuccess || cudaDeviceSynchronize() != cudaSuccess) {
+    free_plan(p);
+    return cs_fail(CS_ERR_CUDA, "clearing the plan's workspace failed");
+  }
+  *out = p;
+  return CS_OK;
+}
+
+cs_status cs_kv_destroy(cs_kv_t p) {
+  if (!p) return CS_OK;
+  DeviceGuard g(p->device);
+  cudaDeviceSynchronize();
+  free_plan(p);
+  return CS_OK;
+}
+
+cs_status cs_kv_append(cs_kv_t p, const cs_kv_batch* b, const cs_kv_append_args* a, void* stream) {
+  cs_status s = begin(p, b);
+  if (s != CS_OK) return s;
+  DeviceGuard g(p->device);
+  if (!g.ok) return cs_fail(CS_ERR_CUDA, "cannot select the plan's device");
+  return append(p, b, a, static_cast<cudaStream_t>(stream));
+}
+
+cs_status cs_kv_attention(cs_kv_t p, const cs_kv_batch* b, const cs_kv_attn_args* a, void* stream) {
+  cs_status s = begin(p, b);
+  if (s != CS_OK) return s;
+  cskv::AttnP k;
+  if ((s = check_attn(p, b, a, k)) != CS_OK) return s;
+  DeviceGuard g(p->device);
+  if (!g.ok) return cs_fail(CS_ERR_CUDA, "cannot select the plan's device");
+  return run_attention(p, k, static_cast<cudaStream_t>(stream));
+}
+
+cs_status cs_kv_attention_shared(cs_kv_t p, const cs_kv_batch* b, const int32_t* prefix_pages, int prefix_len,
+                                 const cs_kv_attn_args* a, void* stream) {
+  cs_status s = begin(p, b);
+  if (s != CS_OK) return s;
+  if (!p->d.shared) return cs_fail(CS_ERR_INVALID_ARG, "the plan was made without desc.shared");
+  if (prefix_len < 0 || prefix_len > kMaxKeys) return cs_fail(CS_ERR_INVALID_ARG, "prefix_len=%d (0..%d)", prefix_len, kMaxKeys);
+  if (!prefix_pages && prefix_len > 0) return cs_fail(CS_ERR_INVALID_ARG, "prefix_pages is NULL");
+  cskv::AttnP k;
+  if ((s = check_attn(p, b, a, k)) != CS_OK) return s;
+  k.prefix_pages = prefix_pages;
+  k.prefix_len = prefix_len;
+  DeviceGuard g(p->device);
+  if (!g.ok) return cs_fail(CS_ERR_CUDA, "cannot select the plan's device");
+  return run_attention(p, k, static_cast<cudaStream_t>(stream));
+}
+
+cs_status cs_attn_cached_forward(cs_chain_t chain, cs_kv_t p, const cs_kv_batch* b, const cs_attn_args* args,
+                                 const cs_kv_append_args* append_args, void* stream) {
+  cs_status s = begin(p, b);
+  if (s != CS_OK) return s;
+  if (!chain || !args || !append_args) return cs_fail(CS_ERR_INVALID_ARG, "chain, args and append are required");
+  cs_chain_info info;
+  if ((s = cs_chain_query(chain, &info)) != CS_OK) return s;
+  const cs_chain_desc& cd = *cs_chain_desc_of(chain);
+  if (cd.kind != CS_CHAIN_ATTN) return cs_fail(CS_ERR_INVALID_ARG, "chain is not an attention chain");
+  const cs_kv_desc& d = p->d;
+  if (d.dtype != cd.dtype || d.heads != cd.heads || d.kv_heads != cd.heads || d.head_dim != 128)
+    return cs_fail(CS_ERR_INVALID_ARG, "the plans differ: dtype %d/%d, heads %d/%d, kv_heads %d, head_dim %d", cd.dtype, d.dtype,
+                   cd.heads, d.heads, d.kv_heads, d.head_dim);
+  if (b->tokens != cd.M) return cs_fail(CS_ERR_INVALID_ARG, "batch has %d tokens, the chain M=%d", b->tokens, cd.M);
+  // a stage that runs alone does not advance the epoch that its split tiles count by
+  if (info.split_k[0] != 1 || info.split_k[2] != 1 || info.sk_units != 0)
+    return cs_fail(CS_ERR_UNSUPPORTED, "the chain's plan splits K (make it with split_k = 1 and sk_tiles = -1)");
+  cs_kv_append_args ap = *append_args;
+  ap.qkv = info.intermediate[0];
+  ap.q_out = info.intermediate[0];
+  ap.qkv_stride = ap.q_stride = 3ll * cd.F;
+  cs_kv_attn_args at;
+  std::memset(&at, 0, sizeof(at));
+  at.q = info.intermediate[0];
+  at.q_stride = 3ll * cd.F;
+  at.k_cache = ap.k_cache;
+  at.v_cache = ap.v_cache;
+  at.out = info.intermediate[1];
+  if ((s = cs_chain_forward_stage(chain, args, 0, stream)) != CS_OK) return s;
+  if ((s = cs_kv_append(p, b, &ap, stream)) != CS_OK) return s;
+  if ((s = cs_kv_attention(p, b, &at, stream)) != CS_OK) return s;
+  return cs_chain_forward_stage(chain, args, 2, stream);
+}
+
+cs_status cs_kv_status(cs_kv_t p) {
+  if (!p) return cs_fail(CS_ERR_INVALID_ARG, "plan is NULL");
+  DeviceGuard g(p->device);
+  uint32_t w[3];
+  KV_CUDA(cudaMemcpy(w, p->ctrl, sizeof(w), cudaMemcpyDeviceToHost));
+  if (w[cskv::CTRL_ERROR] == 0) return CS_OK;
+  p->error_latched = true;
+  const cs_status code = static_cast<cs_status>(w[cskv::CTRL_ERROR]);
+  const uint32_t i = w[cskv::CTRL_INDEX];
+  switch (w[cskv::CTRL_WHAT]) {
+    case cskv::WHAT_LENGTHS:
+      return cs_fail(code, "cu_q or kv_lens of sequence %u does not fit the call", i);
+    case cskv::WHAT_PAGE:
+      return cs_fail(code, "a page of sequence %u (%u: of the prefix) is not in the pool", i, 0xFFFFFFFFu);
+    case cskv::WHAT_POSITION:
+      return cs_fail(code, "the position of token %u has no row in rope", i);
+    default:
+      return cs_fail(code, "a wait inside a kernel ran out (at %u)", i);
+  }
+}
+
+cs_status cs_kv_reset(cs_kv_t p) {
+  if (!p) return cs_fail(CS_ERR_INVALID_ARG, "plan is NULL");
+  DeviceGuard g(p->device);
+  KV_CUDA(cudaDeviceSynchronize());
+  KV_CUDA(cudaMemset(p->ctrl, 0, p->ctrl_words * 4));
+  KV_CUDA(cudaDeviceSynchronize());
+  p->error_latched = false;
+  return CS_OK;
+}
+
+}  // extern "C"

@@ -1,0 +1,261 @@
+// Kernels of the paged key/value cache operators (include/cs_kv.h).
+#pragma once
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+
+#include <cstdint>
+
+#include "cs_ptx.cuh"
+
+namespace cskv {
+
+// What every kernel of a plan reads: the batch, the cache's geometry and the
+// plan's error words.
+struct Batch {
+  const int* cu_q;
+  const int* kv_lens;
+  const int* table;
+  int tokens, seqs, max_q, table_cols;
+  int heads, kv_heads, group;  // group = heads / kv_heads
+  int page_size, page_shift, num_pages;
+  long long page_stride, slot_stride, head_stride;  // cache strides in elements
+  uint32_t* ctrl;
+};
+
+// ctrl words: first device error (cs_status), what did not fit, and its index
+enum : int { CTRL_ERROR = 0, CTRL_WHAT = 1, CTRL_INDEX = 2, CTRL_COUNTERS = 16 };
+enum : uint32_t { WHAT_LENGTHS = 1, WHAT_PAGE = 2, WHAT_POSITION = 3, WHAT_WAIT = 4 };
+constexpr uint32_t ERR_INVALID = 1, ERR_WATCHDOG = 6;  // cs_status values
+
+static __device__ __noinline__ void record(uint32_t* ctrl, uint32_t code, uint32_t what, uint32_t index) {
+  if (atomicCAS(&ctrl[CTRL_ERROR], 0u, code) == 0u) {
+    ctrl[CTRL_WHAT] = what;
+    ctrl[CTRL_INDEX] = index;
+  }
+}
+
+// Rows [t0, t0 + n) and key count m of sequence b; false (and the device error)
+// where they do not fit the call.
+__device__ __forceinline__ bool sequence(const Batch& B, int b, int& t0, int& n, int& m) {
+  t0 = __ldg(B.cu_q + b);
+  const int t1 = __ldg(B.cu_q + b + 1);
+  m = __ldg(B.kv_lens + b);
+  n = t1 - t0;
+  if (t0 >= 0 && t1 >= t0 && t1 <= B.tokens && n <= B.max_q && m >= 0 && m <= B.table_cols * B.page_size) return true;
+  record(B.ctrl, ERR_INVALID, WHAT_LENGTHS, static_cast<uint32_t>(b));
+  return false;
+}
+
+// The last sequence whose first row is <= t (it holds row t unless t is padding).
+__device__ __forceinline__ int sequence_of(const Batch& B, int t) {
+  int lo = 0, hi = B.seqs;  // cu_q[lo] <= t < cu_q[hi], where they are so at all
+  while (hi - lo > 1) {
+    const int mid = (lo + hi) >> 1;
+    if (__ldg(B.cu_q + mid) <= t)
+      lo = mid;
+    else
+      hi = mid;
+  }
+  return lo;
+}
+
+template <typename T>
+struct Pair;  // two values of the storage type in a 32-bit word
+template <>
+struct Pair<__half> {
+  static __device__ __forceinline__ float2 get(uint32_t w) { return __half22float2(*reinterpret_cast<__half2*>(&w)); }
+  static __device__ __forceinline__ uint32_t put(float a, float b) {
+    __half2 h = __floats2half2_rn(a, b);
+    return *reinterpret_cast<uint32_t*>(&h);
+  }
+};
+template <>
+struct Pair<__nv_bfloat16> {
+  static __device__ __forceinline__ float2 get(uint32_t w) {
+    return __bfloat1622float2(*reinterpret_cast<__nv_bfloat162*>(&w));
+  }
+  static __device__ __forceinline__ uint32_t put(float a, float b) {
+    __nv_bfloat162 h = __floats2bfloat162_rn(a, b);
+    return *reinterpret_cast<uint32_t*>(&h);
+  }
+};
+
+// ---------------------------------------------------------------- append
+// (a, b) -> (a cos - b sin, b cos + a sin) for the rotated pairs of Q and K, a copy
+// for the rest.  A unit is 16 values of one head: the two 8-value chunks whose
+// pairs lie across them (HALF) or two neighbouring chunks (ADJACENT, and what
+// is not rotated).  One thread reads and writes both, so that the rotation
+// may run in place.  Bound by DRAM: every value is read and written once, the
+// rotation's row of a token comes from L1 for all heads but the first.
+struct AppendP {
+  Batch b;
+  const uint4* qkv;
+  uint4* q_out;
+  uint4* k_cache;
+  uint4* v_cache;
+  const float4* rope;
+  const int* positions;
+  long long qkv_stride, q_stride;  // in 16-byte chunks
+  int rope_rows, rotary_dim, half, head_chunks;  // half: HALF pairing; head_chunks = head_dim / 8
+  int tokens_per_block, units;  // units per token
+};
+
+constexpr int APPEND_THREADS = 256;
+constexpr int APPEND_MAX_TOKENS = 32;  // per block
+
+template <typename T>
+__global__ void __launch_bounds__(APPEND_THREADS) cs_kv_append_kernel(const __grid_constant__ AppendP p) {
+  __shared__ long long place[APPEND_MAX_TOKENS];  // element offset of the token's slot in a cache, -1: left out
+  __shared__ int angle[APPEND_MAX_TOKENS];        // its row of the rotation table
+  cs::grid_dep_wait();
+  cs::grid_dep_launch_dependents();
+  const Batch& B = p.b;
+  const int first = blockIdx.x * p.tokens_per_block;
+  const int count = min(p.tokens_per_block, B.tokens - first);
+  if (threadIdx.x < count) {
+    const int t = first + threadIdx.x;
+    const int b = sequence_of(B, t);
+    int t0, n, m;
+    long long at = -1;
+    int row = 0;
+    if (sequence(B, b, t0, n, m) && t >= t0 && t < t0 + n && m - n + t - t0 >= 0) {
+      const int pos = m - n + t - t0;
+      row = p.positions ? __ldg(p.positions + t) : pos;
+      const int page = __ldg(B.table + static_cast<long long>(b) * B.table_cols + (pos >> B.page_shift));
+      if (page < 0 || page >= B.num_pages)
+        record(B.ctrl, ERR_INVALID, WHAT_PAGE, static_cast<uint32_t>(b));
+      else if (p.rotary_dim > 0 && (row < 0 || row >= p.rope_rows))
+        record(B.ctrl, ERR_INVALID, WHAT_POSITION, static_cast<uint32_t>(t));
+      else
+        at = page * B.page_stride + (pos & (B.page_size - 1)) * B.slot_stride;
+    }
+    place[threadIdx.x] = at;
+    angle[threadIdx.x] = row;
+  }
+  __syncthreads();
+  const int per_head = p.head_chunks >> 1;  // units of a head
+  const int turned = p.rotary_dim >> 4;     // of them rotated
+  for (int i = blockIdx.y * blockDim.x + threadIdx.x; i < count * p.units; i += blockDim.x * gridDim.y) {
+    const int k = i / p.units, u = i - k * p.units;
+    const int h = u / per_head, j = u - h * per_head;
+    const long long at = place[k];
+    if (at < 0) continue;
+    const bool rotate = j < turned && h < B.heads + B.kv_heads;
+    const int c0 = rotate && p.half ? j : 2 * j, c1 = rotate && p.half ? j + turned : 2 * j + 1;
+    const uint4* src = p.qkv + (first + k) * p.qkv_stride + h * p.head_chunks;
+    uint4* dst;
+    if (h < B.heads) {
+      dst = p.q_out + (first + k) * p.q_stride + h * p.head_chunks;
+    } else {
+      const bool key = h < B.heads + B.kv_heads;
+      const int kh = h - B.heads - (key ? 0 : B.kv_heads);
+      dst = (key ? p.k_cache : p.v_cache) + ((at + kh * B.head_stride) >> 3);
+    }
+    uint4 x = src[c0], y = src[c1];
+    if (rotate) {
+      const float4* row = p.rope + static_cast<long long>(angle[k]) * (p.rotary_dim >> 2);
+      // 8 cosines, 8 sines: HALF rotates (x[e], y[e]), ADJACENT neighbouring values
+      const float4 ca = __ldg(row + 2 * j), cb = __ldg(row + 2 * j + 1);
+      const float4 sa = __ldg(row + 2 * turned + 2 * j), sb = __ldg(row + 2 * turned + 2 * j + 1);
+      const float c[8] = {ca.x, ca.y, ca.z, ca.w, cb.x, cb.y, cb.z, cb.w};
+      const float s[8] = {sa.x, sa.y, sa.z, sa.w, sb.x, sb.y, sb.z, sb.w};
+      uint32_t* xw = reinterpret_cast<uint32_t*>(&x);
+      uint32_t* yw = reinterpret_cast<uint32_t*>(&y);
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const float2 a = Pair<T>::get(xw[e]), b = Pair<T>::get(yw[e]);
+        if (p.half) {
+          xw[e] = Pair<T>::put(a.x * c[2 * e] - b.x * s[2 * e], a.y * c[2 * e + 1] - b.y * s[2 * e + 1]);
+          yw[e] = Pair<T>::put(b.x * c[2 * e] + a.x * s[2 * e], b.y * c[2 * e + 1] + a.y * s[2 * e + 1]);
+        } else {
+          xw[e] = Pair<T>::put(a.x * c[e] - a.y * s[e], a.y * c[e] + a.x * s[e]);
+          yw[e] = Pair<T>::put(b.x * c[e + 4] - b.y * s[e + 4], b.y * c[e + 4] + b.x * s[e + 4]);
+        }
+      }
+    }
+    dst[c0] = x;
+    dst[c1] = y;
+  }
+}
+
+// ---------------------------------------------------------------- attention
+struct AttnP {
+  Batch b;
+  const void* q;
+  const void* k_cache;
+  const void* v_cache;
+  void* out;
+  float* lse;
+  long long q_stride, out_stride;  // elements
+  int window, sinks;
+  float scale_log2;  // scale * log2(e): scores in base 2
+  const int* prefix_pages;
+  int prefix_len;
+};
+
+// One warp per (token, head): o = sum_j 2^(s_j - max) v_j / sum_j 2^(s_j - max) over
+// the visible keys, one key at a time with the running maximum.
+template <typename T, int D>
+__global__ void __launch_bounds__(128) cs_kv_attn_rows(const __grid_constant__ AttnP p) {
+  cs::grid_dep_wait();
+  cs::grid_dep_launch_dependents();
+  const Batch& B = p.b;
+  const int lane = threadIdx.x & 31;
+  const long long row = static_cast<long long>(blockIdx.x) * 4 + (threadIdx.x >> 5);
+  const int t = static_cast<int>(row / B.heads), h = static_cast<int>(row % B.heads);
+  if (t >= B.tokens) return;
+  const int b = sequence_of(B, t);
+  int t0, n, m;
+  if (!sequence(B, b, t0, n, m) || t < t0 || t >= t0 + n) return;
+  const int pos = m - n + t - t0, kh = h / B.group;
+  constexpr int W = D / 64;  // 32-bit words per lane
+  float q[2 * W], o[2 * W] = {};
+  const uint32_t* qr = reinterpret_cast<const uint32_t*>(static_cast<const T*>(p.q) + t * p.q_stride + h * D);
+#pragma unroll
+  for (int w = 0; w < W; ++w) {
+    const float2 v = Pair<T>::get(qr[lane + 32 * w]);
+    q[2 * w] = v.x * p.scale_log2, q[2 * w + 1] = v.y * p.scale_log2;
+  }
+  float mx = -INFINITY, l = 0.0f;
+  auto keys = [&](const int* pages, int j0, int j1) {
+    for (int j = j0; j < j1; ++j) {
+      const int page = __ldg(pages + (j >> B.page_shift));
+      if (page < 0 || page >= B.num_pages) {
+        record(B.ctrl, ERR_INVALID, WHAT_PAGE, static_cast<uint32_t>(b));
+        continue;
+      }
+      const long long at = page * B.page_stride + (j & (B.page_size - 1)) * B.slot_stride + kh * B.head_stride;
+      const uint32_t* kr = reinterpret_cast<const uint32_t*>(static_cast<const T*>(p.k_cache) + at);
+      const uint32_t* vr = reinterpret_cast<const uint32_t*>(static_cast<const T*>(p.v_cache) + at);
+      float s = 0.0f;
+#pragma unroll
+      for (int w = 0; w < W; ++w) {
+        const float2 k = Pair<T>::get(kr[lane + 32 * w]);
+        s = fmaf(q[2 * w], k.x, fmaf(q[2 * w + 1], k.y, s));
+      }
+#pragma unroll
+      for (int d = 16; d; d >>= 1) s += __shfl_xor_sync(0xFFFFFFFFu, s, d);
+      const float mn = fmaxf(mx, s), f = mx == -INFINITY ? 0.0f : exp2f(mx - mn), e = exp2f(s - mn);
+      l = l * f + e;
+#pragma unroll
+      for (int w = 0; w < W; ++w) {
+        const float2 v = Pair<T>::get(vr[lane + 32 * w]);
+        o[2 * w] = fmaf(o[2 * w], f, e * v.x), o[2 * w + 1] = fmaf(o[2 * w + 1], f, e * v.y);
+      }
+      mx = mn;
+    }
+  };
+  if (p.prefix_len > 0) keys(p.prefix_pages, 0, p.prefix_len);
+  const int* pages = B.table + static_cast<long long>(b) * B.table_cols;
+  const int lo = p.window > 0 ? max(0, pos - p.window + 1) : 0;
+  keys(pages, 0, min(p.sinks, lo));
+  keys(pages, lo, pos + 1);
+  const float inv = l == 0.0f ? 0.0f : 1.0f / l;
+  uint32_t* orow = reinterpret_cast<uint32_t*>(static_cast<T*>(p.out) + t * p.out_stride + h * D);
+#pragma unroll
+  for (int w = 0; w < W; ++w) orow[lane + 32 * w] = Pair<T>::put(o[2 * w] * inv, o[2 * w + 1] * inv);
+  if (p.lse && lane == 0)
+    p.lse[static_cast<long long>(t) * B.heads + h] = l == 0.0f ? -INFINITY : (mx + log2f(l)) * 0.6931471805599453f;
+}
+
+}  // namespace cskv

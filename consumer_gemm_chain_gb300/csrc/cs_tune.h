@@ -1,11 +1,14 @@
-// Internal interface between the plan code (cs_chain.cu) and the tuning table
-// (cs_tune.cpp).  Not part of the C ABI.
+// Internal interface between the plan code (cs_chain.cu), the tuning table
+// (cs_tune.cpp) and the paged-cache operators (cs_kv.cu).  Not part of the C ABI.
 #pragma once
 
 #include "../../include/cs_chain.h"
 
 // Records a status and its message as the thread's last error; returns s.
 cs_status cs_fail(cs_status s, const char* fmt, ...);
+
+// The desc that a plan runs (tuning-table choices applied).
+const cs_chain_desc* cs_chain_desc_of(cs_chain_t plan);
 
 // Looks up the tuning-table entry for a desc run on num_sms SMs.  Returns the
 // entry's index, or -1 when the table is not consulted (desc->tuned < 0, or no
