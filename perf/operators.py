@@ -197,7 +197,7 @@ def prepare(case, seed):
         import consumer_gemm_chain_gb300 as cs
         desc = cs.cs_kv_desc_init(dtype=dt, heads=hq, kv_heads=hk, head_dim=d, page_size=ps, num_pages=pages,
                                   cache_layout=case["layout"], max_tokens=max(1, tokens), max_seqs=case["seqs"],
-                                  rotary_dim=case["rotary_dim"], rotary_pairing=case["pairing"], window=case["window"],
+                                  rotary_dim=min(case["rotary_dim"], d), rotary_pairing=case["pairing"], window=case["window"],
                                   sinks=case["sinks"], shared=1 if case["op"] == "shared" else 0)
         s["plan"] = cs.cs_kv_plan(desc)
         s["batch"] = cs.cs_kv_batch(s["plan"], s["cu_q"], s["kv_lens"], s["table"], tokens=tokens, max_q=max(1, max(q)))
