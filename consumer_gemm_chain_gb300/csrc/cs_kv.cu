@@ -2,13 +2,15 @@
 // argument checks, launches and status.
 #include <cuda.h>
 #include <cuda_runtime.h>
+#include <cudaTypedefs.h>
 
 #include <cmath>
 #include <cstring>
+#include <mutex>
 #include <new>
 
 #include "../../include/cs_kv.h"
-#include "cs_kv_kernel.cuh"
+#include "cs_kv_attn.cuh"
 #include "cs_tune.h"  // cs_fail
 
 #define KV_CUDA(call)                                                                              \
@@ -22,6 +24,8 @@ struct cs_kv_s {
   int device = 0, num_sms = 0;
   uint32_t* ctrl = nullptr;  // error words, then the counters
   size_t ctrl_words = 0;
+  float* part = nullptr;    // pieces of items that several CTAs share
+  float* flat_o = nullptr;  // desc.shared: the prefix's output and log-sum-exp
   bool error_latched = false;
 };
 
@@ -29,6 +33,7 @@ namespace {
 
 constexpr int kMaxSeqs = 8192;
 constexpr int kMaxKeys = 1 << 22;
+constexpr unsigned long long kWaitNs = 2000000000ull;  // limit of every wait inside a kernel
 
 // The plan's device is current while a call of it runs.
 struct DeviceGuard {
@@ -74,6 +79,8 @@ cs_status validate(const cs_kv_desc* d) {
     return cs_fail(CS_ERR_INVALID_ARG, "scale=%g (positive, or 0 for 1/sqrt(head_dim))", d->scale);
   if (d->shared != 0 && d->shared != 1) return cs_fail(CS_ERR_INVALID_ARG, "shared=%d (0 or 1)", d->shared);
   if (d->shared && d->window > 0) return cs_fail(CS_ERR_UNSUPPORTED, "a shared prefix is built without a window");
+  if (static_cast<long long>(d->num_pages) * d->kv_heads * (d->page_size / 8) >= (1ll << 31))
+    return cs_fail(CS_ERR_UNSUPPORTED, "num_pages=%d times %d heads is more than the copies can address", d->num_pages, d->kv_heads);
   if (d->num_sms < 0) return cs_fail(CS_ERR_INVALID_ARG, "num_sms=%d", d->num_sms);
   return CS_OK;
 }
@@ -150,38 +157,95 @@ cs_status check_caches(const void* k, const void* v) {
   return CS_OK;
 }
 
+PFN_cuTensorMapEncodeTiled_v12000 get_encode() {
+  static PFN_cuTensorMapEncodeTiled_v12000 fn = nullptr;
+  static std::once_flag once;
+  std::call_once(once, [] {
+    void* f = nullptr;
+    cudaDriverEntryPointQueryResult q;
+    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &f, 12000, cudaEnableDefault, &q) == cudaSuccess &&
+        q == cudaDriverEntryPointSuccess)
+      fn = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(f);
+  });
+  return fn;
+}
+
+cs_status encode(CUtensorMap* map, int bf16, const void* ptr, int rank, const cuuint64_t* dims, const cuuint64_t* strides,
+                 const cuuint32_t* box, const char* name) {
+  auto enc = get_encode();
+  if (!enc) return cs_fail(CS_ERR_CUDA, "cuTensorMapEncodeTiled is unavailable (driver too old?)");
+  const cuuint32_t ones[5] = {1, 1, 1, 1, 1};
+  const CUresult r = enc(map, bf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, rank,
+                         const_cast<void*>(ptr), dims, strides, box, ones, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                         CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  if (r != CUDA_SUCCESS) return cs_fail(CS_ERR_CUDA, "cuTensorMapEncodeTiled failed (%d) for %s", static_cast<int>(r), name);
+  return CS_OK;
+}
+
+// A cache as [8-slot group][head][64-dimension half][slot of the group][64]: one box is
+// a page's slots of a head.  In the HEAD layout heads are part of the groups' order.
+cs_status encode_cache(const cs_kv_s* p, const cskv::Batch& B, CUtensorMap* map, const void* ptr, const char* name) {
+  const cs_kv_desc& d = p->d;
+  const bool head = d.cache_layout == CS_KV_HEAD;
+  const cuuint64_t groups = static_cast<cuuint64_t>(d.num_pages) * (d.page_size / 8);
+  const cuuint64_t dims[5] = {64, 8, static_cast<cuuint64_t>(d.head_dim / 64), head ? 1 : static_cast<cuuint64_t>(d.kv_heads),
+                              head ? groups * d.kv_heads : groups};
+  const cuuint64_t slot = static_cast<cuuint64_t>(B.slot_stride) * 2;
+  const cuuint64_t strides[4] = {slot, 128, static_cast<cuuint64_t>(B.head_stride) * 2, 8 * slot};
+  const cuuint32_t box[5] = {64, 8, static_cast<cuuint32_t>(d.head_dim / 64), 1, static_cast<cuuint32_t>(d.page_size / 8)};
+  return encode(map, d.dtype == CS_BF16, ptr, 5, dims, strides, box, name);
+}
+
 cs_status check_attn(const cs_kv_s* p, const cs_kv_batch* b, const cs_kv_attn_args* a, cskv::AttnP& k) {
   if (!a) return cs_fail(CS_ERR_INVALID_ARG, "args is NULL");
-  const long long width = static_cast<long long>(p->d.heads) * p->d.head_dim;
+  const cs_kv_desc& d = p->d;
+  const long long width = static_cast<long long>(d.heads) * d.head_dim;
   std::memset(&k, 0, sizeof(k));
   cs_status s = check_caches(a->k_cache, a->v_cache);
   if (s != CS_OK) return s;
-  if ((s = row_stride("q_stride", a->q_stride, width, &k.q_stride)) != CS_OK) return s;
+  long long q_stride = 0;
+  if ((s = row_stride("q_stride", a->q_stride, width, &q_stride)) != CS_OK) return s;
   if ((s = row_stride("out_stride", a->out_stride, width, &k.out_stride)) != CS_OK) return s;
-  if (b->tokens > 0 && (!a->q || !a->out)) return cs_fail(CS_ERR_INVALID_ARG, "q and out are required");
+  if (b->tokens == 0) return CS_OK;
+  if (!a->q || !a->out) return cs_fail(CS_ERR_INVALID_ARG, "q and out are required");
   if (!aligned16(a->q) || !aligned16(a->out)) return cs_fail(CS_ERR_INVALID_ARG, "q and out must be 16-byte aligned");
-  if (a->q && a->q == a->out) return cs_fail(CS_ERR_INVALID_ARG, "out must not be q");
+  if (a->q == a->out) return cs_fail(CS_ERR_INVALID_ARG, "out must not be q");
   k.b = device_batch(p, b);
-  k.q = a->q;
-  k.k_cache = a->k_cache;
-  k.v_cache = a->v_cache;
+  k.c.per_tile = 128 / k.b.group;
+  k.c.per_item = 2 * k.c.per_tile;
+  // a window as long as any sequence hides nothing
+  k.c.window = d.window >= kMaxKeys ? 0 : d.window;
+  k.c.sinks = k.c.window == 0 ? 0 : d.sinks < kMaxKeys ? d.sinks : kMaxKeys;
   k.out = a->out;
   k.lse = a->lse;
-  k.window = p->d.window;
-  k.sinks = p->d.sinks;
-  const double scale = p->d.scale > 0.0f ? p->d.scale : 1.0 / std::sqrt(static_cast<double>(p->d.head_dim));
+  const double scale = d.scale > 0.0f ? d.scale : 1.0 / std::sqrt(static_cast<double>(d.head_dim));
   k.scale_log2 = static_cast<float>(scale * 1.4426950408889634);
-  return CS_OK;
+  k.part = p->part;
+  k.arrivals = p->ctrl + cskv::CTRL_COUNTERS;
+  k.head_groups = d.cache_layout == CS_KV_HEAD ? d.page_size / 8 : 0;
+  k.wait_ns = kWaitNs;
+  const cuuint64_t dims[3] = {static_cast<cuuint64_t>(d.head_dim), static_cast<cuuint64_t>(d.heads),
+                              static_cast<cuuint64_t>(b->tokens)};
+  const cuuint64_t strides[2] = {static_cast<cuuint64_t>(d.head_dim) * 2, static_cast<cuuint64_t>(q_stride) * 2};
+  const cuuint32_t box[3] = {64, static_cast<cuuint32_t>(k.b.group), static_cast<cuuint32_t>(k.c.per_tile)};
+  if ((s = encode(&k.q, d.dtype == CS_BF16, a->q, 3, dims, strides, box, "q")) != CS_OK) return s;
+  if ((s = encode_cache(p, k.b, &k.k, a->k_cache, "k_cache")) != CS_OK) return s;
+  return encode_cache(p, k.b, &k.v, a->v_cache, "v_cache");
+}
+
+const void* attn_kernel(const cs_kv_desc& d, int* smem) {
+  *smem = d.head_dim == 128 ? cskv::AttnShape<128>::SMEM : cskv::AttnShape<64>::SMEM;
+  if (d.dtype == CS_BF16)
+    return d.head_dim == 128 ? (const void*)cskv::cs_kv_attn_kernel<__nv_bfloat16, 128>
+                             : (const void*)cskv::cs_kv_attn_kernel<__nv_bfloat16, 64>;
+  return d.head_dim == 128 ? (const void*)cskv::cs_kv_attn_kernel<__half, 128> : (const void*)cskv::cs_kv_attn_kernel<__half, 64>;
 }
 
 cs_status run_attention(cs_kv_s* p, cskv::AttnP& k, cudaStream_t st) {
   if (k.b.tokens == 0 || k.b.seqs == 0) return CS_OK;
-  const bool bf16 = p->d.dtype == CS_BF16, wide = p->d.head_dim == 128;
-  const void* fn =
-      bf16 ? (wide ? (const void*)cskv::cs_kv_attn_rows<__nv_bfloat16, 128> : (const void*)cskv::cs_kv_attn_rows<__nv_bfloat16, 64>)
-           : (wide ? (const void*)cskv::cs_kv_attn_rows<__half, 128> : (const void*)cskv::cs_kv_attn_rows<__half, 64>);
-  const long long rows = static_cast<long long>(k.b.tokens) * k.b.heads;
-  return launch(fn, dim3(static_cast<unsigned>((rows + 3) / 4)), 128, 0, &k, st);
+  int smem = 0;
+  const void* fn = attn_kernel(p->d, &smem);
+  return launch(fn, dim3(p->num_sms), cskv::ATTN_THREADS, smem, &k, st);
 }
 
 cs_status append(cs_kv_s* p, const cs_kv_batch* b, const cs_kv_append_args* a, cudaStream_t st) {
@@ -239,6 +303,8 @@ cs_status begin(cs_kv_s* p, const cs_kv_batch* b) {
 
 void free_plan(cs_kv_s* p) {
   cudaFree(p->ctrl);
+  cudaFree(p->part);
+  cudaFree(p->flat_o);
   delete p;
 }
 
@@ -274,8 +340,19 @@ cs_status cs_kv_plan(const cs_kv_desc* desc, cs_kv_t* out) {
   p->d = *desc;
   p->device = dev;
   p->num_sms = desc->num_sms > 0 && desc->num_sms < sms ? desc->num_sms : sms;
-  p->ctrl_words = cskv::CTRL_COUNTERS;
-  if (cudaMalloc(reinterpret_cast<void**>(&p->ctrl), p->ctrl_words * 4) != cudaSuccess) {
+  p->ctrl_words = cskv::CTRL_COUNTERS + 2 * static_cast<size_t>(p->num_sms);
+  int smem = 0;
+  const void* fn = attn_kernel(p->d, &smem);
+  if (cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess) {
+    cudaGetLastError();
+    free_plan(p);
+    return cs_fail(CS_ERR_CUDA, "the attention kernel needs %d bytes of shared memory", smem);
+  }
+  const size_t part = static_cast<size_t>(p->num_sms) * 4 * (desc->head_dim / 4 + 1) * 128 * 16;
+  const size_t flat = static_cast<size_t>(desc->max_tokens) * desc->heads * (desc->head_dim + 1) * 4;
+  if (cudaMalloc(reinterpret_cast<void**>(&p->ctrl), p->ctrl_words * 4) != cudaSuccess ||
+      cudaMalloc(reinterpret_cast<void**>(&p->part), part) != cudaSuccess ||
+      (desc->shared && cudaMalloc(reinterpret_cast<void**>(&p->flat_o), flat) != cudaSuccess)) {
     cudaGetLastError();
     free_plan(p);
     return cs_fail(CS_ERR_OOM, "cudaMalloc of the plan's workspace failed");
@@ -323,10 +400,18 @@ cs_status cs_kv_attention_shared(cs_kv_t p, const cs_kv_batch* b, const int32_t*
   if (!prefix_pages && prefix_len > 0) return cs_fail(CS_ERR_INVALID_ARG, "prefix_pages is NULL");
   cskv::AttnP k;
   if ((s = check_attn(p, b, a, k)) != CS_OK) return s;
-  k.prefix_pages = prefix_pages;
-  k.prefix_len = prefix_len;
   DeviceGuard g(p->device);
   if (!g.ok) return cs_fail(CS_ERR_CUDA, "cannot select the plan's device");
+  if (prefix_len > 0) {
+    // all tokens of the batch over the prefix; then every sequence's own keys, which join it
+    k.flat_o = p->flat_o;
+    k.flat_lse = p->flat_o + static_cast<size_t>(p->d.max_tokens) * p->d.heads * p->d.head_dim;
+    k.pages = prefix_pages;
+    k.c.flat = 1;
+    k.c.flat_len = prefix_len;
+    if ((s = run_attention(p, k, static_cast<cudaStream_t>(stream))) != CS_OK) return s;
+    k.c.flat = 0;
+  }
   return run_attention(p, k, static_cast<cudaStream_t>(stream));
 }
 

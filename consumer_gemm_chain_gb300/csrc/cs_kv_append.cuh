@@ -1,9 +1,10 @@
-// Kernels of the paged key/value cache operators (include/cs_kv.h).
+// What the paged key/value cache operators (include/cs_kv.h) share, and the append kernel.
 #pragma once
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
 #include <cstdint>
+#include <type_traits>
 
 #include "cs_ptx.cuh"
 
@@ -176,86 +177,6 @@ __global__ void __launch_bounds__(APPEND_THREADS) cs_kv_append_kernel(const __gr
     dst[c0] = x;
     dst[c1] = y;
   }
-}
-
-// ---------------------------------------------------------------- attention
-struct AttnP {
-  Batch b;
-  const void* q;
-  const void* k_cache;
-  const void* v_cache;
-  void* out;
-  float* lse;
-  long long q_stride, out_stride;  // elements
-  int window, sinks;
-  float scale_log2;  // scale * log2(e): scores in base 2
-  const int* prefix_pages;
-  int prefix_len;
-};
-
-// One warp per (token, head): o = sum_j 2^(s_j - max) v_j / sum_j 2^(s_j - max) over
-// the visible keys, one key at a time with the running maximum.
-template <typename T, int D>
-__global__ void __launch_bounds__(128) cs_kv_attn_rows(const __grid_constant__ AttnP p) {
-  cs::grid_dep_wait();
-  cs::grid_dep_launch_dependents();
-  const Batch& B = p.b;
-  const int lane = threadIdx.x & 31;
-  const long long row = static_cast<long long>(blockIdx.x) * 4 + (threadIdx.x >> 5);
-  const int t = static_cast<int>(row / B.heads), h = static_cast<int>(row % B.heads);
-  if (t >= B.tokens) return;
-  const int b = sequence_of(B, t);
-  int t0, n, m;
-  if (!sequence(B, b, t0, n, m) || t < t0 || t >= t0 + n) return;
-  const int pos = m - n + t - t0, kh = h / B.group;
-  constexpr int W = D / 64;  // 32-bit words per lane
-  float q[2 * W], o[2 * W] = {};
-  const uint32_t* qr = reinterpret_cast<const uint32_t*>(static_cast<const T*>(p.q) + t * p.q_stride + h * D);
-#pragma unroll
-  for (int w = 0; w < W; ++w) {
-    const float2 v = Pair<T>::get(qr[lane + 32 * w]);
-    q[2 * w] = v.x * p.scale_log2, q[2 * w + 1] = v.y * p.scale_log2;
-  }
-  float mx = -INFINITY, l = 0.0f;
-  auto keys = [&](const int* pages, int j0, int j1) {
-    for (int j = j0; j < j1; ++j) {
-      const int page = __ldg(pages + (j >> B.page_shift));
-      if (page < 0 || page >= B.num_pages) {
-        record(B.ctrl, ERR_INVALID, WHAT_PAGE, static_cast<uint32_t>(b));
-        continue;
-      }
-      const long long at = page * B.page_stride + (j & (B.page_size - 1)) * B.slot_stride + kh * B.head_stride;
-      const uint32_t* kr = reinterpret_cast<const uint32_t*>(static_cast<const T*>(p.k_cache) + at);
-      const uint32_t* vr = reinterpret_cast<const uint32_t*>(static_cast<const T*>(p.v_cache) + at);
-      float s = 0.0f;
-#pragma unroll
-      for (int w = 0; w < W; ++w) {
-        const float2 k = Pair<T>::get(kr[lane + 32 * w]);
-        s = fmaf(q[2 * w], k.x, fmaf(q[2 * w + 1], k.y, s));
-      }
-#pragma unroll
-      for (int d = 16; d; d >>= 1) s += __shfl_xor_sync(0xFFFFFFFFu, s, d);
-      const float mn = fmaxf(mx, s), f = mx == -INFINITY ? 0.0f : exp2f(mx - mn), e = exp2f(s - mn);
-      l = l * f + e;
-#pragma unroll
-      for (int w = 0; w < W; ++w) {
-        const float2 v = Pair<T>::get(vr[lane + 32 * w]);
-        o[2 * w] = fmaf(o[2 * w], f, e * v.x), o[2 * w + 1] = fmaf(o[2 * w + 1], f, e * v.y);
-      }
-      mx = mn;
-    }
-  };
-  if (p.prefix_len > 0) keys(p.prefix_pages, 0, p.prefix_len);
-  const int* pages = B.table + static_cast<long long>(b) * B.table_cols;
-  const int lo = p.window > 0 ? max(0, pos - p.window + 1) : 0;
-  keys(pages, 0, min(p.sinks, lo));
-  keys(pages, lo, pos + 1);
-  const float inv = l == 0.0f ? 0.0f : 1.0f / l;
-  uint32_t* orow = reinterpret_cast<uint32_t*>(static_cast<T*>(p.out) + t * p.out_stride + h * D);
-#pragma unroll
-  for (int w = 0; w < W; ++w) orow[lane + 32 * w] = Pair<T>::put(o[2 * w] * inv, o[2 * w + 1] * inv);
-  if (p.lse && lane == 0)
-    p.lse[static_cast<long long>(t) * B.heads + h] = l == 0.0f ? -INFINITY : (mx + log2f(l)) * 0.6931471805599453f;
 }
 
 }  // namespace cskv
