@@ -213,6 +213,7 @@ cs_status check_attn(const cs_kv_s* p, const cs_kv_batch* b, const cs_kv_attn_ar
   k.b = device_batch(p, b);
   k.c.per_tile = 128 / k.b.group;
   k.c.per_item = 2 * k.c.per_tile;
+  k.c.item_cost = 1;
   // a window as long as any sequence hides nothing
   k.c.window = d.window >= kMaxKeys ? 0 : d.window;
   k.c.sinks = k.c.window == 0 ? 0 : d.sinks < kMaxKeys ? d.sinks : kMaxKeys;
@@ -348,7 +349,7 @@ cs_status cs_kv_plan(const cs_kv_desc* desc, cs_kv_t* out) {
     free_plan(p);
     return cs_fail(CS_ERR_CUDA, "the attention kernel needs %d bytes of shared memory", smem);
   }
-  const size_t part = static_cast<size_t>(p->num_sms) * 4 * (desc->head_dim / 4 + 1) * 128 * 16;
+  const size_t part = static_cast<size_t>(p->num_sms) * 6 * (desc->head_dim / 4 + 1) * 128 * 16;
   const size_t flat = static_cast<size_t>(desc->max_tokens) * desc->heads * (desc->head_dim + 1) * 4;
   if (cudaMalloc(reinterpret_cast<void**>(&p->ctrl), p->ctrl_words * 4) != cudaSuccess ||
       cudaMalloc(reinterpret_cast<void**>(&p->part), part) != cudaSuccess ||

@@ -28,7 +28,7 @@ enum : int { CTRL_ERROR = 0, CTRL_WHAT = 1, CTRL_INDEX = 2, CTRL_COUNTERS = 16 }
 enum : uint32_t { WHAT_LENGTHS = 1, WHAT_PAGE = 2, WHAT_POSITION = 3, WHAT_WAIT = 4 };
 constexpr uint32_t ERR_INVALID = 1, ERR_WATCHDOG = 6;  // cs_status values
 
-static __device__ __noinline__ void record(uint32_t* ctrl, uint32_t code, uint32_t what, uint32_t index) {
+__device__ __forceinline__ void record(uint32_t* ctrl, uint32_t code, uint32_t what, uint32_t index) {
   if (atomicCAS(&ctrl[CTRL_ERROR], 0u, code) == 0u) {
     ctrl[CTRL_WHAT] = what;
     ctrl[CTRL_INDEX] = index;

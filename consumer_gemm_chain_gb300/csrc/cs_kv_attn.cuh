@@ -21,6 +21,7 @@ struct Cut {
   int per_tile;   // tokens of a 128-row tile: 128 / group, rounded down
   int per_item;   // tokens of an item: two tiles
   int window, sinks;
+  int item_cost;  // what starting and ending an item costs, in key tiles
   int flat;       // every row sees keys 0 .. flat_len - 1 of one common table (a shared prefix)
   int flat_len;
 };
@@ -84,12 +85,13 @@ __device__ __forceinline__ unsigned long long floor_sum(unsigned n, unsigned m, 
   return ans;
 }
 
-// Key tiles of the first k items of a sequence (of one key head).
-__device__ __forceinline__ unsigned long long tiles_before(const Cut& C, const Seq& s, int k) {
+// Units of the first k items of a sequence (of one key head): their key tiles, and
+// item_cost for each.
+__device__ __forceinline__ unsigned long long units_before(const Cut& C, const Seq& s, int k) {
   if (k == 0) return 0;
-  if (C.flat) return static_cast<unsigned long long>(k) * static_cast<unsigned>(item_tiles(C, s, 0));
+  if (C.flat) return static_cast<unsigned long long>(k) * static_cast<unsigned>(item_tiles(C, s, 0) + C.item_cost);
   const int full = min(k, items_of(C, s) - 1);  // the last item may hold fewer tokens
-  unsigned long long sum = 0;
+  unsigned long long sum = static_cast<unsigned long long>(k) * C.item_cost;
   if (k > full) sum += item_tiles(C, s, full);
   if (full > 0) {
     const int base = s.m - s.n, P = C.per_item;
@@ -116,18 +118,20 @@ struct Seg {
   __device__ __forceinline__ int key0(int k) const { return (k < sinks ? k : lo / KT + k - sinks) * KT; }
 };
 
-// Where a CTA's range begins and ends; every warp role walks it by itself.
+// Where a CTA's range of units begins and ends; every warp role walks it by itself.
 struct Range {
   unsigned long long x0, x1, total, rem;
   int ctas;
   int b, kvh, item, off;
   __device__ __forceinline__ unsigned long long begin_of(unsigned c) const { return total * c / ctas; }
-  // the CTA whose range holds tile x
+  // the CTA whose range holds unit x
   __device__ __forceinline__ unsigned cta_of(unsigned long long x) const {
     return static_cast<unsigned>(((x + 1) * ctas + total - 1) / total - 1);
   }
 };
 
+// An item's units are item_cost of overhead and then its tiles; a range that ends
+// in the overhead leaves all tiles to the next CTA.
 struct Walk {
   unsigned long long x, x1;
   int b, kvh, item, off, items;
@@ -137,34 +141,39 @@ struct Walk {
     if (x < x1 && load_seq(B, C, b, s)) items = items_of(C, s);
   }
   __device__ __forceinline__ bool next(const Batch& B, const Cut& C, Seg& g) {
-    if (x >= x1) return false;
-    if (item == items) {
-      item = 0;
-      if (++kvh == B.kv_heads) {
-        kvh = 0;
-        const int seqs = C.flat ? 1 : B.seqs;
-        do {
-          if (++b >= seqs) return false;
-          items = load_seq(B, C, b, s) ? items_of(C, s) : 0;
-        } while (items == 0);
+    while (x < x1) {
+      if (item == items) {
+        item = 0;
+        if (++kvh == B.kv_heads) {
+          kvh = 0;
+          const int seqs = C.flat ? 1 : B.seqs;
+          do {
+            if (++b >= seqs) return false;
+            items = load_seq(B, C, b, s) ? items_of(C, s) : 0;
+          } while (items == 0);
+        }
       }
+      const int units = item_tiles(C, s, item) + C.item_cost;
+      const unsigned long long left = x1 - x;
+      const int to = static_cast<unsigned long long>(units - off) <= left ? units : off + static_cast<int>(left);
+      g.x = x - off + C.item_cost;
+      g.k0 = max(0, off - C.item_cost);
+      g.k1 = to - C.item_cost;
+      g.item = item;
+      x += to - off;
+      off = 0;
+      ++item;
+      if (g.k1 <= g.k0) continue;
+      g.s = s;
+      g.b = b;
+      g.kvh = kvh;
+      g.tiles = units - C.item_cost;
+      g.lo = item_lo(C, s, g.item);
+      g.hi = item_hi(C, s, g.item);
+      g.sinks = sink_tiles(C, g.lo);
+      return true;
     }
-    g.s = s;
-    g.b = b;
-    g.kvh = kvh;
-    g.item = item;
-    g.lo = item_lo(C, s, item);
-    g.hi = item_hi(C, s, item);
-    g.sinks = sink_tiles(C, g.lo);
-    g.tiles = item_tiles(C, s, item);
-    g.k0 = off;
-    g.x = x - off;
-    const unsigned long long left = x1 - x;
-    g.k1 = static_cast<unsigned long long>(g.tiles - off) <= left ? g.tiles : off + static_cast<int>(left);
-    x += g.k1 - g.k0;
-    off = 0;
-    ++item;
-    return true;
+    return false;
   }
 };
 
@@ -178,7 +187,7 @@ __device__ __forceinline__ void find_range(const Batch& B, const Cut& C, Range* 
   unsigned long long mine = 0;
   Seq s;
   for (int b = b0; b < b1; ++b)
-    if (load_seq(B, C, b, s)) mine += tiles_before(C, s, items_of(C, s));
+    if (load_seq(B, C, b, s)) mine += units_before(C, s, items_of(C, s));
   unsigned long long incl = mine;
 #pragma unroll
   for (int d = 1; d < 32; d <<= 1) {
@@ -209,7 +218,7 @@ __device__ __forceinline__ void find_range(const Batch& B, const Cut& C, Range* 
   if (work && at <= x0 && x0 < incl * B.kv_heads) {
     for (int b = b0; b < b1; ++b) {
       if (!load_seq(B, C, b, s)) continue;
-      const unsigned long long c = tiles_before(C, s, items_of(C, s));
+      const unsigned long long c = units_before(C, s, items_of(C, s));
       if (x0 < at + c * B.kv_heads) {
         r->b = b;
         r->kvh = static_cast<int>((x0 - at) / c);
@@ -221,19 +230,19 @@ __device__ __forceinline__ void find_range(const Batch& B, const Cut& C, Range* 
   }
   __syncthreads();
   if (warp == 0 && work) {
-    // the item that holds tile `rem` of its sequence and head: 32 trials at a time
+    // the item that holds unit `rem` of its sequence and head: 32 trials at a time
     if (load_seq(B, C, r->b, s)) {
       const unsigned long long rem = r->rem;
-      int a = 0, e = items_of(C, s);  // tiles_before(a) <= rem < tiles_before(e)
+      int a = 0, e = items_of(C, s);  // units_before(a) <= rem < units_before(e)
       while (e - a > 1) {
         const int step = (e - a + 31) / 32;
         const int k = a + lane * step;
-        const bool in = k < e && tiles_before(C, s, k) <= rem;
+        const bool in = k < e && units_before(C, s, k) <= rem;
         const int last = 31 - __clz(__ballot_sync(0xFFFFFFFFu, in));
         a += last * step;
         e = min(e, a + step);
       }
-      const int off = static_cast<int>(rem - tiles_before(C, s, a));
+      const int off = static_cast<int>(rem - units_before(C, s, a));
       __syncwarp();
       if (lane == 0) {
         r->item = a;
@@ -254,7 +263,7 @@ struct AttnP {
   float* lse;
   long long out_stride;   // elements
   float scale_log2;       // scale * log2(e): exponents in base 2
-  float* part;            // pieces: [CTA][first, last][tile][D / 4 + 1][128 rows] float4
+  float* part;            // states: [CTA][first piece, last piece, other half][tile][D / 4 + 1][128 rows] float4
   uint32_t* arrivals;     // [CTA][tile] pieces of the item that starts there and ends elsewhere
   float* flat_o;          // [tokens][heads][D], [tokens][heads]: a prefix's normalised output and
   float* flat_lse;        // base-2 log-sum-exp; written with c.flat, else joined in if not null
@@ -262,7 +271,20 @@ struct AttnP {
   unsigned long long wait_ns;
 };
 
-constexpr int ATTN_THREADS = 320;  // two softmax warpgroups, the TMA warp, the MMA warp
+constexpr int ATTN_THREADS = 384;  // two softmax warpgroups; the TMA warp, the MMA warp and two idle ones
+// Registers: 65536 / 384 gives every thread 168 at launch; a softmax thread holds a
+// row of S, so the third warpgroup hands over what it does not need
+// (2 x 216 + 72 = 3 x 168).
+constexpr int SOFTMAX_REGS = 216, OTHER_REGS = 72;
+static_assert(2 * SOFTMAX_REGS + OTHER_REGS <= 3 * 168, "more registers than the launch holds");
+template <int N>
+__device__ __forceinline__ void regs_inc() {
+  asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
+}
+template <int N>
+__device__ __forceinline__ void regs_dec() {
+  asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
+}
 constexpr uint32_t COL_S = 0, COL_O = 256;
 constexpr float RAISE_LOG2 = 8.0f;  // the reference maximum follows a row's when it is exceeded by more than 2^8
 
@@ -277,13 +299,16 @@ struct AttnShape {
 template <int SLOTS>
 struct AttnCtl {
   uint64_t full[SLOTS], empty[SLOTS];
-  uint64_t q_full, q_empty, s_full[2], p_full[2], o_full[2], stored[2], counted[2], drained;
+  uint64_t q_full[2], q_empty[2], s_full[2], p_full[2][2], o_full[2];
+  uint64_t stored[2], counted[2];      // a piece is stored; its arrival is counted
+  uint64_t other_full, other_empty;    // warpgroup 1's half of an item of one row tile
+  uint64_t drained;
   unsigned long long scratch[ATTN_THREADS / 32];
   Range range;
   uint32_t tmem;
   volatile int abort;
   volatile int last[2];
-  int loads, q_loads;  // tiles and queries whose copies were issued
+  int loads, q_loads[2];  // tiles and queries whose copies were issued
 };
 
 __device__ __forceinline__ void tma_5d(void* dst, const CUtensorMap* map, int x, int c1, int c2, int c3, int c4,
@@ -309,6 +334,13 @@ __device__ __forceinline__ void mma_ts(uint32_t d_tmem, uint32_t a_tmem, uint64_
       "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d_tmem),
       "r"(a_tmem), "l"(b_desc), "r"(idesc), "r"(acc)
       : "memory");
+}
+
+// One lane of a converged warp, the same one every time.
+__device__ __forceinline__ bool elect_one() {
+  uint32_t one;
+  asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(one));
+  return one != 0;
 }
 
 // Bounded wait; false when it ran out, here or in another role.
@@ -347,7 +379,8 @@ __device__ void come_to_rest(AttnCtl<SLOTS>* sc, const AttnP& p) {
     const int n = (sc->loads - i + SLOTS - 1) / SLOTS;  // loads into slot i
     if (n > 0) settle(&sc->full[i], (n - 1) & 1);
   }
-  if (sc->q_loads > 0) settle(&sc->q_full, (sc->q_loads - 1) & 1);
+  for (int w = 0; w < 2; ++w)
+    if (sc->q_loads[w] > 0) settle(&sc->q_full[w], (sc->q_loads[w] - 1) & 1);
   settle(&sc->drained, 0);
 }
 
@@ -373,21 +406,23 @@ __device__ bool load_role(const AttnP& p, AttnCtl<AttnShape<D>::SLOTS>* sc, uint
   Walk walk(B, p.c, sc->range);
   Seg g;
   Ring<Sh::SLOTS> rp;
-  uint32_t q_phase = 1;
+  uint32_t q_phase[2] = {1, 1};
   while (walk.next(B, p.c, g)) {
     const int* table = p.c.flat ? p.pages : B.table + static_cast<long long>(g.b) * B.table_cols;
     const bool two = g.s.n - g.item * p.c.per_item > p.c.per_tile;
-    if (!wait_warp(&sc->q_empty, q_phase, sc, p, 1)) return false;
-    q_phase ^= 1u;
-    if (lane == 0) {
-      const int tok = g.s.t0 + g.item * p.c.per_item;
-      const uint32_t bytes = static_cast<uint32_t>(p.c.per_tile) * B.group * D * 2;
-      cs::mbar_arrive_expect_tx(&sc->q_full, two ? 2 * bytes : bytes);
-      for (int w = 0; w < (two ? 2 : 1); ++w)
+    auto queries = [&](int w) {
+      if (!wait_warp(&sc->q_empty[w], q_phase[w], sc, p, 1)) return false;
+      q_phase[w] ^= 1u;
+      if (lane == 0) {
+        cs::mbar_arrive_expect_tx(&sc->q_full[w], static_cast<uint32_t>(p.c.per_tile) * B.group * D * 2);
         for (int h = 0; h < Sh::HALVES; ++h)
-          tma_3d(qbuf + w * Sh::TILE + h * (KT * 128), &p.q, h * 64, g.kvh * B.group, tok + w * p.c.per_tile, &sc->q_full);
-      ++sc->q_loads;
-    }
+          tma_3d(qbuf + w * Sh::TILE + h * (KT * 128), &p.q, h * 64, g.kvh * B.group,
+                 g.s.t0 + g.item * p.c.per_item + w * p.c.per_tile, &sc->q_full[w]);
+        ++sc->q_loads[w];
+      }
+      return true;
+    };
+    if (!queries(0)) return false;
     // the page that this lane brings of tile k, -1: none of its keys is seen
     auto page_of = [&](int k) {
       if (k >= g.k1 || lane >= pages_per_tile) return -1;
@@ -415,6 +450,8 @@ __device__ bool load_role(const AttnP& p, AttnCtl<AttnShape<D>::SLOTS>* sc, uint
           tma_5d(ring + rp.slot * Sh::TILE + lane * (B.page_size * D * 2), half ? &p.v : &p.k, 0, 0, 0, c3, c4,
                  &sc->full[rp.slot]);
         rp.next();
+        // the second row tile's queries, which the last item may still hold, after the first keys
+        if (two && k == g.k0 && half == 0 && !queries(1)) return false;
       }
       page = after;
     }
@@ -422,95 +459,135 @@ __device__ bool load_role(const AttnP& p, AttnCtl<AttnShape<D>::SLOTS>* sc, uint
   return true;
 }
 
-// One thread: S of the two row tiles in turn, each P V between them, so that one
-// tile's softmax runs while the tensor core works for the other.  P takes the
-// place of the first half of S; MMAs execute in the order of their issue.
+// One thread.  Step i computes S_i = Q K^T into S buffer i % 2 and then, one step
+// behind, O += P V of step i - 1, so that the tensor core works for one buffer
+// while the other's softmax runs.  An item of two row tiles takes each key tile in
+// two steps, one per row tile; an item of one row tile takes its key tiles in turn
+// (its two buffers are joined at the end).  P takes the place of the first half of
+// S; MMAs execute in the order of their issue.  The issue must keep ahead of
+// 64 cycles per MMA: addresses and descriptors stay in registers (with the
+// tensor-memory base read from shared memory for every MMA, a prompt of 8192
+// tokens and 32 heads took 638 us instead of 502).
 template <int D>
 __device__ bool mma_role(const AttnP& p, AttnCtl<AttnShape<D>::SLOTS>* sc, uint8_t* qbuf, uint8_t* ring, int bf16) {
   using Sh = AttnShape<D>;
   const uint32_t idesc_s = cs::make_idesc_f16(bf16, 0, 128, KT);
   const uint32_t idesc_o = cs::make_idesc_f16(bf16, 1, 128, D);
+  const uint32_t tm = sc->tmem;
+  const uint64_t q_desc = cs::smem_desc_sw128(cs::smem_u32(qbuf), 16, 1024);
+  const uint64_t k_desc = cs::smem_desc_sw128(cs::smem_u32(ring), 16, Sh::HALVES * 1024);
+  const uint64_t v_desc = cs::smem_desc_sw128(cs::smem_u32(ring), 1024, Sh::HALVES * 1024);
   Walk walk(p.b, p.c, sc->range);
   Seg g;
   Ring<Sh::SLOTS> rk, rv;
   rv.next();
-  uint32_t q_phase = 0, p_phase[2] = {0, 0};
-  const uint32_t qa = cs::smem_u32(qbuf), ra = cs::smem_u32(ring);
-  auto scores = [&](int w) {
-    const uint64_t a = cs::smem_desc_sw128(qa + w * Sh::TILE, 16, 1024);
-    const uint64_t b = cs::smem_desc_sw128(ra + rk.slot * Sh::TILE, 16, Sh::HALVES * 1024);
-#pragma unroll
-    for (int kk = 0; kk < D / 16; ++kk)
-      cs::tc_mma_f16<1>(sc->tmem + COL_S + w * 128, a + (kk >> 2) * (KT * 128 >> 4) + (kk & 3) * 2,
-                        b + (kk >> 2) * (1024 >> 4) + (kk & 3) * 2, idesc_s, kk != 0);
-    cs::tc_commit<1>(&sc->s_full[w]);
-  };
-  auto values = [&](int w, const Ring<Sh::SLOTS>& r, bool acc) {
-    if (!wait(&sc->p_full[w], p_phase[w], sc, p, 3)) return false;
-    p_phase[w] ^= 1u;
-    if (!wait(&sc->full[r.slot], r.phase, sc, p, 4)) return false;
-    cs::tc_fence_after();
-    const uint64_t b = cs::smem_desc_sw128(ra + r.slot * Sh::TILE, 1024, Sh::HALVES * 1024);
-#pragma unroll
-    for (int kk = 0; kk < KT / 16; ++kk)
-      mma_ts(sc->tmem + COL_O + w * D, sc->tmem + COL_S + w * 128 + kk * 8, b + kk * (Sh::HALVES * 2048 >> 4), idesc_o,
-             acc || kk != 0);
-    return true;
-  };
+  uint32_t q_phase = 0, p_phase = 0;  // bit w
   while (walk.next(p.b, p.c, g)) {
     const bool two = g.s.n - g.item * p.c.per_item > p.c.per_tile;
-    if (!wait(&sc->q_full, q_phase, sc, p, 5)) return false;
-    q_phase ^= 1u;
-    Ring<Sh::SLOTS> prev;  // the V tile of the previous key tile
-    for (int k = g.k0; k < g.k1; ++k) {
-      if (!wait(&sc->full[rk.slot], rk.phase, sc, p, 6)) return false;
-      cs::tc_fence_after();
-      scores(0);
-      if (two) {
-        if (k > g.k0) {
-          if (!values(1, prev, k - 1 > g.k0)) return false;
-          cs::tc_commit<1>(&sc->empty[prev.slot]);
+    const int steps = (g.k1 - g.k0) << (two ? 1 : 0);
+    for (int i = 0; i <= steps; ++i) {
+      if (i < steps) {
+        const int w = i & 1, qw = two ? w : 0;
+        if (i < (two ? 2 : 1)) {
+          if (!wait(&sc->q_full[qw], (q_phase >> qw) & 1u, sc, p, 5)) return false;
+          q_phase ^= 1u << qw;
         }
-        scores(1);
+        if (!(two && w) && !wait(&sc->full[rk.slot], rk.phase, sc, p, 6)) return false;
+        cs::tc_fence_after();
+        const uint64_t a = q_desc + qw * (Sh::TILE >> 4), b = k_desc + rk.slot * (Sh::TILE >> 4);
+        const uint32_t d = tm + COL_S + w * 128;
+#pragma unroll
+        for (int kk = 0; kk < D / 16; ++kk)
+          cs::tc_mma_f16<1>(d, a + ((kk >> 2) * (KT * 128 >> 4) + (kk & 3) * 2), b + ((kk >> 2) * (1024 >> 4) + (kk & 3) * 2),
+                            idesc_s, kk != 0);
+        cs::tc_commit<1>(&sc->s_full[w]);
+        if (!two || w) {
+          cs::tc_commit<1>(&sc->empty[rk.slot]);
+          rk.next(), rk.next();
+        }
+        if (i >= steps - (two ? 2 : 1)) cs::tc_commit<1>(&sc->q_empty[qw]);
       }
-      cs::tc_commit<1>(&sc->empty[rk.slot]);
-      if (k + 1 == g.k1) cs::tc_commit<1>(&sc->q_empty);
-      rk.next(), rk.next();
-      if (!values(0, rv, k > g.k0)) return false;
-      if (!two) cs::tc_commit<1>(&sc->empty[rv.slot]);
-      if (k + 1 == g.k1) cs::tc_commit<1>(&sc->o_full[0]);
-      prev = rv;
-      rv.next(), rv.next();
-    }
-    if (two) {
-      if (!values(1, prev, g.k1 - 1 > g.k0)) return false;
-      cs::tc_commit<1>(&sc->empty[prev.slot]);
-      cs::tc_commit<1>(&sc->o_full[1]);
+      if (i > 0) {
+        const int j = i - 1, w = j & 1;
+        if (!(two && w) && !wait(&sc->full[rv.slot], rv.phase, sc, p, 4)) return false;
+        const uint64_t b = v_desc + rv.slot * (Sh::TILE >> 4);
+        const uint32_t d = tm + COL_O + w * D, a = tm + COL_S + w * 128;
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {  // the first 64 keys' weights come before the rest
+          if (!wait(&sc->p_full[w][h], (p_phase >> w) & 1u, sc, p, 3)) return false;
+          cs::tc_fence_after();
+#pragma unroll
+          for (int kk = 4 * h; kk < 4 * h + 4; ++kk)
+            mma_ts(d, a + kk * 8, b + kk * (Sh::HALVES * 2048 >> 4), idesc_o, kk != 0 || j >= 2);
+        }
+        p_phase ^= 1u << w;
+        if (!two || w) {
+          cs::tc_commit<1>(&sc->empty[rv.slot]);
+          rv.next(), rv.next();
+        }
+        if (j >= steps - 2) cs::tc_commit<1>(&sc->o_full[w]);
+      }
     }
   }
   return true;
 }
 
-// Warpgroup w: the softmax of row tile w, one row per thread, and its output.
+// max of three, two multiply-adds and two sums at a time
+__device__ __forceinline__ float max3(float a, float b, float c) {
+  float d;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+  return d;
+}
+__device__ __forceinline__ uint64_t pack64(float a, float b) {
+  uint64_t d;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(d) : "f"(a), "f"(b));
+  return d;
+}
+__device__ __forceinline__ void unpack64(uint64_t x, float& a, float& b) {
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(x));
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t d;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
+  return d;
+}
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
+  uint64_t d;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+  return d;
+}
+
+// Warpgroup w: the softmax of the steps with buffer w, one row per thread, and the output.
 template <typename T, int D>
 __device__ bool softmax_role(const AttnP& p, AttnCtl<AttnShape<D>::SLOTS>* sc, uint8_t* ring, int w) {
   using Sh = AttnShape<D>;
+  constexpr int CH = D / 32;                                      // chunks of 32 columns of O
+  constexpr size_t STATE = static_cast<size_t>(D / 4 + 1) * 128;  // float4s
   const Batch& B = p.b;
-  const int r = threadIdx.x & 127;
+  const int r = threadIdx.x & 127, lane = threadIdx.x & 31;
   const uint32_t lanes = static_cast<uint32_t>(r & ~31) << 16;
   const uint32_t s_tm = sc->tmem + lanes + COL_S + w * 128, o_tm = sc->tmem + lanes + COL_O + w * D;
   const int row_tok = r / B.group, row_head = r - row_tok * B.group;
+  float4* states = reinterpret_cast<float4*>(p.part) + r;
+  auto state = [&](unsigned cta, int which, int tile) { return states + ((static_cast<size_t>(cta) * 3 + which) * 2 + tile) * STATE; };
+  auto read_o = [&](int c, uint32_t (&o)[32]) {
+    cs::tmem_ld32(o_tm + c * 32, o);
+    cs::tc_wait_ld();
+    cs::tc_wait_ld_regs(o);
+  };
+  const uint64_t scale2 = pack64(p.scale_log2, p.scale_log2);
   Walk walk(B, p.c, sc->range);
   Seg g;
-  Ring<Sh::SLOTS> rv;
-  rv.next();
-  uint32_t s_phase = 0, o_phase = 0, j_phase = 0;
+  uint32_t tiles_done = 0;  // key tiles of the segments before this one
+  uint32_t s_phase = 0, o_phase = 0, j_phase = 0, x_phase = 0;
   while (walk.next(B, p.c, g)) {
-    const int first = g.item * p.c.per_item + w * p.c.per_tile;  // the tile's first token
-    if (first >= g.s.n) {  // the item has one tile
-      for (int k = g.k0; k < g.k1; ++k) rv.next(), rv.next();
-      continue;
-    }
+    const int count = g.k1 - g.k0;
+    const uint32_t ring0 = 2 * tiles_done;
+    tiles_done += count;
+    const bool two = g.s.n - g.item * p.c.per_item > p.c.per_tile;
+    if (!two && w >= count) continue;  // one key tile of one row tile: buffer 0 alone
+    const int tile = two ? w : 0;      // this warpgroup's row tile
+    const int first = g.item * p.c.per_item + tile * p.c.per_tile;  // its first token
     const int base = g.s.m - g.s.n;
     const int tok = first + row_tok;
     const bool live = row_tok < p.c.per_tile && tok < g.s.n;
@@ -520,7 +597,8 @@ __device__ bool softmax_role(const AttnP& p, AttnCtl<AttnShape<D>::SLOTS>* sc, u
     const int some = p.c.flat ? g.s.m : base + first + 1;
     const int all_lo = p.c.window > 0 ? max(0, base + first + p.c.per_tile - p.c.window) : 0;
     float m_ref = -INFINITY, l = 0.0f;
-    for (int k = g.k0; k < g.k1; ++k) {
+    for (int k = g.k0 + (two ? 0 : w); k < g.k1; k += two ? 1 : 2) {
+      const bool fresh = k - g.k0 < (two ? 1 : 2);  // O of this buffer holds nothing yet
       const int j0 = g.key0(k);
       if (!wait_warp(&sc->s_full[w], s_phase, sc, p, 7 + w)) return false;
       s_phase ^= 1u;
@@ -545,166 +623,247 @@ __device__ bool softmax_role(const AttnP& p, AttnCtl<AttnShape<D>::SLOTS>* sc, u
 #pragma unroll
       for (int c = 0; c < 4; ++c)
 #pragma unroll
-        for (int t = 0; t < 32; ++t) mx[t & 3] = fmaxf(mx[t & 3], __uint_as_float(v[c][t]));
-      const float m_tile = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * p.scale_log2;
+        for (int t = 0; t < 32; t += 2)
+          mx[(t >> 1) & 3] = max3(mx[(t >> 1) & 3], __uint_as_float(v[c][t]), __uint_as_float(v[c][t + 1]));
+      const float m_tile = max3(fmaxf(mx[0], mx[1]), mx[2], mx[3]) * p.scale_log2;
       // P is taken against a reference that is raised only when a row's maximum
       // exceeds it by more than 2^8 (so P <= 2^8, and rounding to the dtype is as
       // good as at 1); then O and l are scaled down first
       const bool raise = m_tile > m_ref + RAISE_LOG2 || (m_ref == -INFINITY && m_tile > -INFINITY);
       const float m_new = raise ? m_tile : m_ref;
-      if (k > g.k0 && __any_sync(0xFFFFFFFFu, raise)) {
-        // S of this tile was issued after P V of the one before: O is complete
+      if (!fresh && __any_sync(0xFFFFFFFFu, raise)) {
+        // S of this step was issued after P V of the buffer's last one: O is complete
         const float f = raise ? cs::ex2_approx(m_ref - m_new) : 1.0f;
         l *= f;
 #pragma unroll 1
-        for (int c = 0; c < D / 32; ++c) {
+        for (int c = 0; c < CH; ++c) {
           uint32_t o[32];
-          cs::tmem_ld32(o_tm + c * 32, o);
-          cs::tc_wait_ld();
-          cs::tc_wait_ld_regs(o);
+          read_o(c, o);
 #pragma unroll
           for (int t = 0; t < 32; ++t) o[t] = __float_as_uint(__uint_as_float(o[t]) * f);
           cs::tmem_st32(o_tm + c * 32, o);
         }
       }
       m_ref = m_new;
-      const float sub = m_ref == -INFINITY ? 0.0f : -m_ref;
-      float ls[2] = {0.0f, 0.0f};
-#pragma unroll
-      for (int c = 0; c < 2; ++c) {
-        uint32_t pk[32];
-#pragma unroll
-        for (int t = 0; t < 64; t += 2) {
-          const float p0 = cs::ex2_approx(fmaf(__uint_as_float(v[2 * c + (t >> 5)][t & 31]), p.scale_log2, sub));
-          const float p1 = cs::ex2_approx(fmaf(__uint_as_float(v[2 * c + (t >> 5)][(t & 31) + 1]), p.scale_log2, sub));
-          ls[0] += p0;
-          ls[1] += p1;
-          pk[t >> 1] = Pair<T>::put(p0, p1);
-        }
-        cs::tmem_st32(s_tm + c * 32, pk);
-      }
-      l += ls[0] + ls[1];
       // values of keys that no row of the item sees may hold anything: zeros in
-      // their place (the first tile's P V is issued first, so w = 0 does it for both)
-      if (w == 0 && (j0 + KT > g.hi || (j0 < g.lo && j0 + KT > p.c.sinks))) {
-        if (!wait_warp(&sc->full[rv.slot], rv.phase, sc, p, 9)) return false;
+      // their place, before any P V of this tile (row tile 0's is issued first)
+      if (tile == 0 && (j0 + KT > g.hi || (j0 < g.lo && j0 + KT > p.c.sinks))) {
+        const uint32_t at = ring0 + 2 * (k - g.k0) + 1, slot = at % Sh::SLOTS;
+        if (!wait_warp(&sc->full[slot], (at / Sh::SLOTS) & 1u, sc, p, 9)) return false;
         const int j = j0 + r;
         if (j >= g.hi || (j < g.lo && j >= p.c.sinks)) {
-          uint8_t* row = ring + rv.slot * Sh::TILE + (r >> 3) * (Sh::HALVES * 1024) + (r & 7) * 128;
+          uint8_t* row = ring + slot * Sh::TILE + (r >> 3) * (Sh::HALVES * 1024) + (r & 7) * 128;
           for (int h = 0; h < Sh::HALVES; ++h)
 #pragma unroll
             for (int c = 0; c < 8; ++c) *reinterpret_cast<uint4*>(row + h * 1024 + c * 16) = make_uint4(0, 0, 0, 0);
         }
-        cs::fence_proxy_async_shared();
+        cs::fence_proxy_async_shared();  // and all four warps signal before the MMA reads
       }
-      cs::tc_wait_st();
-      cs::tc_fence_before();
-      cs::mbar_arrive(&sc->p_full[w]);
-      rv.next(), rv.next();
+      const float sub = m_ref == -INFINITY ? 0.0f : -m_ref;
+      const uint64_t sub2 = pack64(sub, sub);
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        uint32_t pk[32];
+#pragma unroll
+        for (int t = 0; t < 64; t += 2) {
+          uint32_t& a = v[2 * h + (t >> 5)][t & 31];
+          uint32_t& b = v[2 * h + (t >> 5)][(t & 31) + 1];
+          float x, y;
+          unpack64(fma2(pack64(__uint_as_float(a), __uint_as_float(b)), scale2, sub2), x, y);
+          x = cs::ex2_approx(x);
+          y = cs::ex2_approx(y);
+          pk[t >> 1] = Pair<T>::put(x, y);
+          a = __float_as_uint(x);
+          b = __float_as_uint(y);
+        }
+        cs::tmem_st32(s_tm + h * 32, pk);
+        cs::tc_wait_st();
+        cs::tc_fence_before();
+        __syncwarp();
+        if (lane == 0) cs::mbar_arrive(&sc->p_full[w][h]);
+      }
+      uint64_t ls[2] = {0, 0};
+#pragma unroll
+      for (int c = 0; c < 4; ++c)
+#pragma unroll
+        for (int t = 0; t < 32; t += 2)
+          ls[(t >> 1) & 1] = add2(ls[(t >> 1) & 1], pack64(__uint_as_float(v[c][t]), __uint_as_float(v[c][t + 1])));
+      float l0, l1;
+      unpack64(add2(ls[0], ls[1]), l0, l1);
+      l += l0 + l1;
     }
     if (!wait_warp(&sc->o_full[w], o_phase, sc, p, 10 + w)) return false;
     o_phase ^= 1u;
     cs::tc_fence_after();
-    // this thread's row of O, against m_ref
-    float acc[D];
+    // the state of this row: O (in tensor memory) and l, both against m_ref
+    if (!two && w == 1) {
+      // the other key tiles of warpgroup 0's rows: it joins them
+      if (!wait_warp(&sc->other_empty, x_phase ^ 1u, sc, p, 12)) return false;
+      x_phase ^= 1u;
+      float4* to = state(blockIdx.x, 2, 0);
+#pragma unroll 1
+      for (int c = 0; c < CH; ++c) {
+        uint32_t o[32];
+        read_o(c, o);
+        if (live)
 #pragma unroll
-    for (int c = 0; c < D / 32; ++c) {
-      uint32_t o[32];
-      cs::tmem_ld32(o_tm + c * 32, o);
-      cs::tc_wait_ld();
-      cs::tc_wait_ld_regs(o);
-#pragma unroll
-      for (int t = 0; t < 32; ++t) acc[c * 32 + t] = __uint_as_float(o[t]);
-    }
-    cs::tc_fence_before();
-    if (!g.whole()) {
-      constexpr size_t PIECE = static_cast<size_t>(D / 4 + 1) * 128;  // float4s
-      float4* part = reinterpret_cast<float4*>(p.part);
-      auto piece = [&](unsigned cta, int last) { return part + ((static_cast<size_t>(cta) * 2 + last) * 2 + w) * PIECE + r; };
-      float4* mine = piece(blockIdx.x, sc->range.x0 < g.x);
-#pragma unroll
-      for (int t = 0; t < D / 4; ++t) mine[t * 128] = make_float4(acc[4 * t], acc[4 * t + 1], acc[4 * t + 2], acc[4 * t + 3]);
-      mine[D / 4 * 128] = make_float4(m_ref, l, 0.0f, 0.0f);
-      const unsigned c0 = sc->range.cta_of(g.x), c1 = sc->range.cta_of(g.x + g.tiles - 1);
-      // every thread's stores come before the one arrival at gpu scope; the other
-      // pieces are read after it
-      cs::mbar_arrive(&sc->stored[w]);
-      if (r < 32) {
-        if (!wait_warp(&sc->stored[w], j_phase, sc, p, 12)) return false;
-        if (r == 0) {
-          uint32_t* ctr = p.arrivals + c0 * 2 + w;
-          const uint32_t old = cs::atom_add_acq_rel_gpu(ctr, 1u);
-          sc->last[w] = old == c1 - c0;
-          if (old == c1 - c0) *ctr = 0u;  // for the next call
-          cs::mbar_arrive(&sc->counted[w]);
-        }
-        __syncwarp();
+          for (int t = 0; t < 8; ++t)
+            to[(c * 8 + t) * 128] = make_float4(__uint_as_float(o[4 * t]), __uint_as_float(o[4 * t + 1]),
+                                                __uint_as_float(o[4 * t + 2]), __uint_as_float(o[4 * t + 3]));
       }
-      if (!wait_warp(&sc->counted[w], j_phase, sc, p, 13)) return false;
-      j_phase ^= 1u;
-      const bool last = sc->last[w] != 0;
-      if (!last) continue;
-      m_ref = -INFINITY;
-      for (unsigned c = c0; c <= c1; ++c)
-        m_ref = fmaxf(m_ref, __ldcg(piece(c, sc->range.begin_of(c) < g.x) + D / 4 * 128).x);
-      const float sub = m_ref == -INFINITY ? 0.0f : m_ref;
-      l = 0.0f;
-#pragma unroll
-      for (int t = 0; t < D; ++t) acc[t] = 0.0f;
-      for (unsigned c = c0; c <= c1; ++c) {
-        const float4* src = piece(c, sc->range.begin_of(c) < g.x);
-        const float4 ml = __ldcg(src + D / 4 * 128);
-        const float f = cs::ex2_approx(ml.x - sub);
-        l = fmaf(ml.y, f, l);
-#pragma unroll
-        for (int t = 0; t < D / 4; ++t) {
-          const float4 x = __ldcg(src + t * 128);
-          acc[4 * t] = fmaf(x.x, f, acc[4 * t]);
-          acc[4 * t + 1] = fmaf(x.y, f, acc[4 * t + 1]);
-          acc[4 * t + 2] = fmaf(x.z, f, acc[4 * t + 2]);
-          acc[4 * t + 3] = fmaf(x.w, f, acc[4 * t + 3]);
-        }
-      }
-    }
-    if (!live) continue;
-    const long long row = static_cast<long long>(g.s.t0 + tok) * B.heads + g.kvh * B.group + row_head;
-    if (p.c.flat) {
-      const float inv = 1.0f / l;
-      float4* dst = reinterpret_cast<float4*>(p.flat_o + row * D);
-#pragma unroll
-      for (int t = 0; t < D / 4; ++t)
-        dst[t] = make_float4(acc[4 * t] * inv, acc[4 * t + 1] * inv, acc[4 * t + 2] * inv, acc[4 * t + 3] * inv);
-      p.flat_lse[row] = m_ref + log2f(l);
+      if (live) to[D / 4 * 128] = make_float4(m_ref, l, 0.0f, 0.0f);
+      cs::tc_fence_before();
+      cs::mbar_arrive(&sc->other_full);
       continue;
     }
-    float fold = 0.0f;  // weight of the prefix's output
-    const float4* pre = reinterpret_cast<const float4*>(p.flat_o + row * D);
-    if (p.flat_o) {
-      const float z = p.flat_lse[row];
-      const float m_new = fmaxf(m_ref, z);
-      const float f = m_ref == -INFINITY ? 0.0f : cs::ex2_approx(m_ref - m_new);
-      fold = cs::ex2_approx(z - m_new);
-      l = fmaf(l, f, fold);
-#pragma unroll
-      for (int t = 0; t < D / 4; ++t) {
-        const float4 x = pre[t];
-        acc[4 * t] = fmaf(acc[4 * t], f, fold * x.x);
-        acc[4 * t + 1] = fmaf(acc[4 * t + 1], f, fold * x.y);
-        acc[4 * t + 2] = fmaf(acc[4 * t + 2], f, fold * x.z);
-        acc[4 * t + 3] = fmaf(acc[4 * t + 3], f, fold * x.w);
+    const float4* other = nullptr;
+    float f_own = 1.0f, f_other = 0.0f;
+    if (!two && count > 1) {
+      if (!wait_warp(&sc->other_full, x_phase, sc, p, 13)) return false;
+      x_phase ^= 1u;
+      if (live) {
+        other = state(blockIdx.x, 2, 0);
+        const float4 ml = __ldcg(other + D / 4 * 128);
+        const float m_new = fmaxf(m_ref, ml.x);
+        f_own = m_ref == -INFINITY ? 0.0f : cs::ex2_approx(m_ref - m_new);
+        f_other = ml.x == -INFINITY ? 0.0f : cs::ex2_approx(ml.x - m_new);
+        l = l * f_own + ml.y * f_other;
+        m_ref = m_new;
       }
-      m_ref = m_new;
     }
-    const float inv = l == 0.0f ? 0.0f : 1.0f / l;
-    uint4* dst = reinterpret_cast<uint4*>(static_cast<T*>(p.out) + (g.s.t0 + tok) * p.out_stride +
-                                          (g.kvh * B.group + row_head) * D);
+    // 32 columns of the state, both halves joined
+    auto own_chunk = [&](int c, float (&x)[32]) {
+      uint32_t o[32];
+      read_o(c, o);
 #pragma unroll
-    for (int t = 0; t < D / 8; ++t) {
-      const float* a = acc + 8 * t;
-      dst[t] = make_uint4(Pair<T>::put(a[0] * inv, a[1] * inv), Pair<T>::put(a[2] * inv, a[3] * inv),
-                          Pair<T>::put(a[4] * inv, a[5] * inv), Pair<T>::put(a[6] * inv, a[7] * inv));
+      for (int t = 0; t < 32; ++t) x[t] = __uint_as_float(o[t]);
+      if (other) {
+#pragma unroll
+        for (int t = 0; t < 8; ++t) {
+          const float4 y = __ldcg(other + (c * 8 + t) * 128);
+          x[4 * t] = x[4 * t] * f_own + y.x * f_other;
+          x[4 * t + 1] = x[4 * t + 1] * f_own + y.y * f_other;
+          x[4 * t + 2] = x[4 * t + 2] * f_own + y.z * f_other;
+          x[4 * t + 3] = x[4 * t + 3] * f_own + y.w * f_other;
+        }
+      }
+    };
+    const long long row = static_cast<long long>(g.s.t0 + tok) * B.heads + g.kvh * B.group + row_head;
+    // the row's output from its final state, of which chunk(c, x) gives 32 columns
+    auto finish = [&](auto chunk) {
+      float f = 1.0f, fold = 0.0f;  // weights of the state and of a prefix's output
+      const float4* pre = nullptr;
+      if (live && !p.c.flat && p.flat_o) {
+        pre = reinterpret_cast<const float4*>(p.flat_o + row * D);
+        const float z = p.flat_lse[row];
+        const float m_new = fmaxf(m_ref, z);
+        f = m_ref == -INFINITY ? 0.0f : cs::ex2_approx(m_ref - m_new);
+        fold = z == -INFINITY ? 0.0f : cs::ex2_approx(z - m_new);
+        l = l * f + fold;
+        m_ref = m_new;
+      }
+      const float inv = l == 0.0f ? 0.0f : 1.0f / l;
+#pragma unroll 1
+      for (int c = 0; c < CH; ++c) {
+        float x[32];
+        chunk(c, x);
+        if (!live) continue;
+        if (p.c.flat) {
+          float4* dst = reinterpret_cast<float4*>(p.flat_o + row * D) + c * 8;
+#pragma unroll
+          for (int t = 0; t < 8; ++t)
+            dst[t] = make_float4(x[4 * t] * inv, x[4 * t + 1] * inv, x[4 * t + 2] * inv, x[4 * t + 3] * inv);
+          continue;
+        }
+        if (pre) {
+#pragma unroll
+          for (int t = 0; t < 8; ++t) {
+            const float4 y = pre[c * 8 + t];
+            x[4 * t] = x[4 * t] * f + y.x * fold;
+            x[4 * t + 1] = x[4 * t + 1] * f + y.y * fold;
+            x[4 * t + 2] = x[4 * t + 2] * f + y.z * fold;
+            x[4 * t + 3] = x[4 * t + 3] * f + y.w * fold;
+          }
+        }
+        uint4* dst = reinterpret_cast<uint4*>(static_cast<T*>(p.out) + (g.s.t0 + tok) * p.out_stride +
+                                              (g.kvh * B.group + row_head) * D + c * 32);
+#pragma unroll
+        for (int t = 0; t < 4; ++t) {
+          const float* a = x + 8 * t;
+          dst[t] = make_uint4(Pair<T>::put(a[0] * inv, a[1] * inv), Pair<T>::put(a[2] * inv, a[3] * inv),
+                              Pair<T>::put(a[4] * inv, a[5] * inv), Pair<T>::put(a[6] * inv, a[7] * inv));
+        }
+      }
+      if (!live) return;
+      const float lse2 = l == 0.0f ? -INFINITY : m_ref + log2f(l);
+      if (p.c.flat)
+        p.flat_lse[row] = lse2;
+      else if (p.lse)
+        p.lse[row] = lse2 * 0.6931471805599453f;
+    };
+    if (g.whole()) {
+      finish(own_chunk);
+    } else {
+      float4* mine = state(blockIdx.x, sc->range.x0 < g.x, tile);
+#pragma unroll 1
+      for (int c = 0; c < CH; ++c) {
+        float x[32];
+        own_chunk(c, x);
+        if (live)
+#pragma unroll
+          for (int t = 0; t < 8; ++t) mine[(c * 8 + t) * 128] = make_float4(x[4 * t], x[4 * t + 1], x[4 * t + 2], x[4 * t + 3]);
+      }
+      if (live) mine[D / 4 * 128] = make_float4(m_ref, l, 0.0f, 0.0f);
     }
-    if (p.lse) p.lse[row] = l == 0.0f ? -INFINITY : (m_ref + log2f(l)) * 0.6931471805599453f;
+    cs::tc_fence_before();
+    if (!two && count > 1) cs::mbar_arrive(&sc->other_empty);
+    if (g.whole()) continue;
+    // every thread's stores come before the one arrival at gpu scope; the other
+    // pieces are read after it
+    const unsigned c0 = sc->range.cta_of(g.x), c1 = sc->range.cta_of(g.x + g.tiles - 1);
+    cs::mbar_arrive(&sc->stored[w]);
+    if (r < 32) {
+      if (!wait_warp(&sc->stored[w], j_phase, sc, p, 15)) return false;
+      if (r == 0) {
+        uint32_t* ctr = p.arrivals + c0 * 2 + tile;
+        const uint32_t old = cs::atom_add_acq_rel_gpu(ctr, 1u);
+        sc->last[w] = old == c1 - c0;
+        if (old == c1 - c0) *ctr = 0u;  // for the next call
+        cs::mbar_arrive(&sc->counted[w]);
+      }
+      __syncwarp();
+    }
+    if (!wait_warp(&sc->counted[w], j_phase, sc, p, 16)) return false;
+    j_phase ^= 1u;
+    if (sc->last[w] && live) {
+      // the last to arrive joins the pieces in their order
+      auto piece = [&](unsigned c) { return state(c, sc->range.begin_of(c) < g.x, tile); };
+      m_ref = -INFINITY;
+      for (unsigned c = c0; c <= c1; ++c) m_ref = fmaxf(m_ref, __ldcg(piece(c) + D / 4 * 128).x);
+      const float m_all = m_ref == -INFINITY ? 0.0f : m_ref;
+      l = 0.0f;
+      for (unsigned c = c0; c <= c1; ++c) {
+        const float4 ml = __ldcg(piece(c) + D / 4 * 128);
+        l = fmaf(ml.y, cs::ex2_approx(ml.x - m_all), l);
+      }
+      finish([&](int c, float (&x)[32]) {
+#pragma unroll
+        for (int t = 0; t < 32; ++t) x[t] = 0.0f;
+        for (unsigned i = c0; i <= c1; ++i) {
+          const float4* src = piece(i);
+          const float f = cs::ex2_approx(__ldcg(src + D / 4 * 128).x - m_all);
+#pragma unroll
+          for (int t = 0; t < 8; ++t) {
+            const float4 y = __ldcg(src + (c * 8 + t) * 128);
+            x[4 * t] = fmaf(y.x, f, x[4 * t]);
+            x[4 * t + 1] = fmaf(y.y, f, x[4 * t + 1]);
+            x[4 * t + 2] = fmaf(y.z, f, x[4 * t + 2]);
+            x[4 * t + 3] = fmaf(y.w, f, x[4 * t + 3]);
+          }
+        }
+      });
+    }
+    __syncwarp();
   }
   return true;
 }
@@ -725,17 +884,19 @@ __global__ void __launch_bounds__(ATTN_THREADS, 1) cs_kv_attn_kernel(const __gri
       cs::mbar_init(&sc->full[i], 1);
       cs::mbar_init(&sc->empty[i], 1);
     }
-    cs::mbar_init(&sc->q_full, 1);
-    cs::mbar_init(&sc->q_empty, 1);
     for (int w = 0; w < 2; ++w) {
+      cs::mbar_init(&sc->q_full[w], 1);
+      cs::mbar_init(&sc->q_empty[w], 1);
       cs::mbar_init(&sc->s_full[w], 1);
-      cs::mbar_init(&sc->p_full[w], 128);
+      for (int h = 0; h < 2; ++h) cs::mbar_init(&sc->p_full[w][h], 4);  // the warps of a warpgroup
       cs::mbar_init(&sc->o_full[w], 1);
       cs::mbar_init(&sc->stored[w], 128);
       cs::mbar_init(&sc->counted[w], 1);
     }
+    cs::mbar_init(&sc->other_full, 128);
+    cs::mbar_init(&sc->other_empty, 128);
     cs::mbar_init(&sc->drained, 1);
-    sc->abort = sc->loads = sc->q_loads = 0;
+    sc->abort = sc->loads = sc->q_loads[0] = sc->q_loads[1] = 0;
     cs::fence_mbar_init();
     cs::prefetch_tmap(&p.q);
     cs::prefetch_tmap(&p.k);
@@ -752,12 +913,15 @@ __global__ void __launch_bounds__(ATTN_THREADS, 1) cs_kv_attn_kernel(const __gri
   cs::grid_dep_launch_dependents();
   find_range<ATTN_THREADS>(p.b, p.c, &sc->range, sc->scratch);
   constexpr int bf16 = sizeof(T) == 2 && !std::is_same<T, __half>::value;
-  if (warp < 8)
+  if (warp < 8) {
+    regs_inc<SOFTMAX_REGS>();
     softmax_role<T, D>(p, sc, ring, warp >> 2);
-  else if (warp == 8)
-    load_role<D>(p, sc, qbuf, ring);
-  else if ((threadIdx.x & 31) == 0 && !mma_role<D>(p, sc, qbuf, ring, bf16))
-    cs::tc_commit<1>(&sc->drained);
+  } else {
+    regs_dec<OTHER_REGS>();
+    if (warp == 8) load_role<D>(p, sc, qbuf, ring);
+    // `drained`, after a wait that ran out: the MMAs issued so far are done
+    if (warp == 9 && elect_one() && !mma_role<D>(p, sc, qbuf, ring, bf16)) cs::tc_commit<1>(&sc->drained);
+  }
   __syncwarp();
   cs::tc_fence_before();
   __syncthreads();
