@@ -33,7 +33,6 @@ namespace {
 
 constexpr int kMaxSeqs = 8192;
 constexpr int kMaxKeys = 1 << 22;
-constexpr unsigned long long kWaitNs = 2000000000ull;  // limit of every wait inside a kernel
 
 // The plan's device is current while a call of it runs.
 struct DeviceGuard {
@@ -224,7 +223,6 @@ cs_status check_attn(const cs_kv_s* p, const cs_kv_batch* b, const cs_kv_attn_ar
   k.part = p->part;
   k.arrivals = p->ctrl + cskv::CTRL_COUNTERS;
   k.head_groups = d.cache_layout == CS_KV_HEAD ? d.page_size / 8 : 0;
-  k.wait_ns = kWaitNs;
   const cuuint64_t dims[3] = {static_cast<cuuint64_t>(d.head_dim), static_cast<cuuint64_t>(d.heads),
                               static_cast<cuuint64_t>(b->tokens)};
   const cuuint64_t strides[2] = {static_cast<cuuint64_t>(d.head_dim) * 2, static_cast<cuuint64_t>(q_stride) * 2};

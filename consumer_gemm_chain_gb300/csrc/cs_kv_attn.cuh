@@ -62,22 +62,17 @@ __device__ __forceinline__ int item_tiles(const Cut& C, const Seq& s, int item) 
 __device__ __forceinline__ int items_of(const Cut& C, const Seq& s) { return (s.n + C.per_item - 1) / C.per_item; }
 
 // sum over i < n of floor((a i + b) / m), a, b >= 0 (the Euclid-like recurrence for
-// lattice points under a line)
+// lattice points under a line); m a + m fits 32 bits times n
 __device__ __forceinline__ unsigned long long floor_sum(unsigned n, unsigned m, unsigned a, unsigned b) {
   unsigned long long ans = 0;
+#pragma unroll 1
   while (n > 0) {
-    if (a >= m) {
-      ans += static_cast<unsigned long long>(n) * (n - 1) / 2 * (a / m);
-      a %= m;
-    }
-    if (b >= m) {
-      ans += static_cast<unsigned long long>(n) * (b / m);
-      b %= m;
-    }
-    const unsigned long long y = static_cast<unsigned long long>(a) * n + b;
-    if (y < m) break;
-    n = static_cast<unsigned>(y / m);
-    b = static_cast<unsigned>(y % m);
+    ans += static_cast<unsigned long long>(n) * (n - 1) / 2 * (a / m) + static_cast<unsigned long long>(n) * (b / m);
+    a %= m;
+    b %= m;
+    const unsigned y = a * n + b;  // below 128 (n + 1), n <= 2^20 tokens
+    n = y / m;
+    b = y % m;
     const unsigned t = m;
     m = a;
     a = t;
@@ -118,16 +113,11 @@ struct Seg {
   __device__ __forceinline__ int key0(int k) const { return (k < sinks ? k : lo / KT + k - sinks) * KT; }
 };
 
-// Where a CTA's range of units begins and ends; every warp role walks it by itself.
+// Where a CTA's range of units begins and ends (CTA c takes units c * quota and
+// on); every warp role walks it by itself.
 struct Range {
-  unsigned long long x0, x1, total, rem;
-  int ctas;
+  unsigned long long x0, x1, rem, quota;
   int b, kvh, item, off;
-  __device__ __forceinline__ unsigned long long begin_of(unsigned c) const { return total * c / ctas; }
-  // the CTA whose range holds unit x
-  __device__ __forceinline__ unsigned cta_of(unsigned long long x) const {
-    return static_cast<unsigned>(((x + 1) * ctas + total - 1) / total - 1);
-  }
 };
 
 // An item's units are item_cost of overhead and then its tiles; a range that ends
@@ -183,70 +173,78 @@ __device__ __forceinline__ void find_range(const Batch& B, const Cut& C, Range* 
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int seqs = C.flat ? 1 : B.seqs;
   const int per = (seqs + THREADS - 1) / THREADS;
-  const int b0 = min(tid * per, seqs), b1 = min(b0 + per, seqs);
-  unsigned long long mine = 0;
+  const int b0 = min(tid * per, seqs);
+  int b1 = min(b0 + per, seqs);
+  unsigned long long at = 0, x0 = 0;
   Seq s;
-  for (int b = b0; b < b1; ++b)
-    if (load_seq(B, C, b, s)) mine += units_before(C, s, items_of(C, s));
-  unsigned long long incl = mine;
-#pragma unroll
-  for (int d = 1; d < 32; d <<= 1) {
-    const unsigned long long o = __shfl_up_sync(0xFFFFFFFFu, incl, d);
-    if (lane >= d) incl += o;
-  }
-  if (lane == 31) scratch[warp] = incl;
-  __syncthreads();
-  unsigned long long before = 0, total = 0;
-  for (int w = 0; w < THREADS / 32; ++w) {
-    if (w < warp) before += scratch[w];
-    total += scratch[w];
-  }
-  incl += before;
-  total *= B.kv_heads;
-  const unsigned ctas = total < gridDim.x ? static_cast<unsigned>(total) : gridDim.x;
-  const bool work = blockIdx.x < ctas;
-  const unsigned long long x0 = work ? total * blockIdx.x / ctas : 0, x1 = work ? total * (blockIdx.x + 1) / ctas : 0;
-  if (tid == 0) {
-    r->x0 = x0;
-    r->x1 = x1;
-    r->total = total;
-    r->ctas = static_cast<int>(ctas);
-    r->b = r->kvh = r->item = r->off = 0;
-  }
-  __syncthreads();
-  unsigned long long at = (incl - mine) * B.kv_heads;
-  if (work && at <= x0 && x0 < incl * B.kv_heads) {
+  // first the units of all sequences, then, by the thread whose sequences hold unit
+  // x0, the one that holds it
+#pragma unroll 1
+  for (int pass = 0; pass < 2; ++pass) {
+    unsigned long long mine = 0;
+#pragma unroll 1
     for (int b = b0; b < b1; ++b) {
       if (!load_seq(B, C, b, s)) continue;
       const unsigned long long c = units_before(C, s, items_of(C, s));
-      if (x0 < at + c * B.kv_heads) {
+      const unsigned long long in = x0 - at - mine * B.kv_heads;
+      if (pass == 1 && in < c * B.kv_heads) {
         r->b = b;
-        r->kvh = static_cast<int>((x0 - at) / c);
-        r->rem = (x0 - at) % c;
+        r->kvh = static_cast<int>(in / c);
+        r->rem = in - r->kvh * c;
         break;
       }
-      at += c * B.kv_heads;
+      mine += c;
     }
+    if (pass == 1) break;
+    unsigned long long incl = mine;
+#pragma unroll
+    for (int d = 1; d < 32; d <<= 1) {
+      const unsigned long long o = __shfl_up_sync(0xFFFFFFFFu, incl, d);
+      if (lane >= d) incl += o;
+    }
+    if (lane == 31) scratch[warp] = incl;
+    __syncthreads();
+    unsigned long long before = 0, total = 0;
+#pragma unroll 1
+    for (int w = 0; w < THREADS / 32; ++w) {
+      if (w < warp) before += scratch[w];
+      total += scratch[w];
+    }
+    incl = (incl + before) * B.kv_heads;
+    total *= B.kv_heads;
+    const unsigned long long quota = (total + gridDim.x - 1) / gridDim.x;
+    x0 = min(quota * blockIdx.x, total);
+    const unsigned long long x1 = min(x0 + quota, total);
+    if (tid == 0) {
+      r->x0 = x0;
+      r->x1 = x1;
+      r->quota = quota;
+      r->b = r->kvh = r->item = r->off = 0;
+    }
+    __syncthreads();
+    at = incl - mine * B.kv_heads;
+    if (x0 >= x1 || x0 < at || x0 >= incl) b1 = b0;
   }
   __syncthreads();
-  if (warp == 0 && work) {
+  if (warp == 0 && r->x0 < r->x1) {
     // the item that holds unit `rem` of its sequence and head: 32 trials at a time
     if (load_seq(B, C, r->b, s)) {
       const unsigned long long rem = r->rem;
       int a = 0, e = items_of(C, s);  // units_before(a) <= rem < units_before(e)
-      while (e - a > 1) {
+      unsigned long long base = 0;    // units_before(a)
+      do {
         const int step = (e - a + 31) / 32;
         const int k = a + lane * step;
-        const bool in = k < e && units_before(C, s, k) <= rem;
-        const int last = 31 - __clz(__ballot_sync(0xFFFFFFFFu, in));
+        const unsigned long long u = k < e ? units_before(C, s, k) : ~0ull;
+        const int last = 31 - __clz(__ballot_sync(0xFFFFFFFFu, u <= rem));
+        base = __shfl_sync(0xFFFFFFFFu, u, last);
         a += last * step;
         e = min(e, a + step);
-      }
-      const int off = static_cast<int>(rem - units_before(C, s, a));
+      } while (e - a > 1);
       __syncwarp();
       if (lane == 0) {
         r->item = a;
-        r->off = off;
+        r->off = static_cast<int>(rem - base);
       }
     }
   }
@@ -268,13 +266,15 @@ struct AttnP {
   float* flat_o;          // [tokens][heads][D], [tokens][heads]: a prefix's normalised output and
   float* flat_lse;        // base-2 log-sum-exp; written with c.flat, else joined in if not null
   int head_groups;        // 8-slot groups between heads (HEAD layout), 0: heads are a dimension of their own
-  unsigned long long wait_ns;
 };
 
-constexpr int ATTN_THREADS = 384;  // two softmax warpgroups; the TMA warp, the MMA warp and two idle ones
+// Two softmax warpgroups, one per S buffer with a row per thread, and one with the
+// TMA warp, the MMA warp and two idle ones.
+constexpr int ATTN_THREADS = 384;
 // Registers: 65536 / 384 gives every thread 168 at launch; a softmax thread holds a
 // row of S, so the third warpgroup hands over what it does not need
-// (2 x 216 + 72 = 3 x 168).
+// (2 x 216 + 72 = 3 x 168).  Nothing may spill: next to 226 KB of shared memory the
+// L1 holds nearly nothing, and a spilled register comes back from L2.
 constexpr int SOFTMAX_REGS = 216, OTHER_REGS = 72;
 static_assert(2 * SOFTMAX_REGS + OTHER_REGS <= 3 * 168, "more registers than the launch holds");
 template <int N>
@@ -286,6 +286,7 @@ __device__ __forceinline__ void regs_dec() {
   asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
 }
 constexpr uint32_t COL_S = 0, COL_O = 256;
+constexpr int CTL = 1024;  // bytes of the control block
 constexpr float RAISE_LOG2 = 8.0f;  // the reference maximum follows a row's when it is exceeded by more than 2^8
 
 template <int D>
@@ -293,7 +294,7 @@ struct AttnShape {
   static constexpr int HALVES = D / 64;
   static constexpr int TILE = KT * D * 2;              // bytes of a 128-row tile of Q, K or V
   static constexpr int SLOTS = D == 128 ? 5 : 10;      // ring of K and V tiles: 160 KB in flight
-  static constexpr int SMEM = 2 * TILE + SLOTS * TILE + 1024 + 1024;
+  static constexpr int SMEM = 2 * TILE + SLOTS * TILE + 1024 + CTL;
 };
 
 template <int SLOTS>
@@ -343,36 +344,38 @@ __device__ __forceinline__ bool elect_one() {
   return one != 0;
 }
 
-// Bounded wait; false when it ran out, here or in another role.
+// Bounded wait; false when it ran out, here or in another role.  What is waited
+// for is always work of this CTA, microseconds away; a try suspends the thread
+// for a while, so the limit is seconds.  (Kept small: with the slow path's timer and
+// error record inlined everywhere the kernel had 156 KB of code, and its warps
+// waited for instructions.)
+constexpr int WAIT_TRIES = 1 << 22;
 template <typename Ctl>
-__device__ __forceinline__ bool wait(uint64_t* bar, uint32_t parity, Ctl* sc, const AttnP& p, uint32_t where) {
-  if (cs::mbar_try_wait(bar, parity)) return true;
-  const uint64_t t0 = cs::globaltimer();
-  for (uint32_t i = 1;; ++i) {
+__device__ __forceinline__ bool wait(uint64_t* bar, uint32_t parity, Ctl* sc) {
+#pragma unroll 1
+  for (int i = 0; i < WAIT_TRIES; ++i) {
     if (cs::mbar_try_wait(bar, parity)) return true;
     if (sc->abort) return false;
-    if ((i & 63u) == 0u && cs::globaltimer() - t0 > p.wait_ns) {
-      record(p.b.ctrl, ERR_WATCHDOG, WHAT_WAIT, where);
-      sc->abort = 1;
-      return false;
-    }
   }
+  sc->abort = 1;
+  return false;
 }
 
 // The same for a whole warp, which goes on or gives up together.
 template <typename Ctl>
-__device__ __forceinline__ bool wait_warp(uint64_t* bar, uint32_t parity, Ctl* sc, const AttnP& p, uint32_t where) {
-  const bool ok = wait(bar, parity, sc, p, where);
-  return __all_sync(0xFFFFFFFFu, ok);
+__device__ __forceinline__ bool wait_warp(uint64_t* bar, uint32_t parity, Ctl* sc) {
+  if (__all_sync(0xFFFFFFFFu, cs::mbar_try_wait(bar, parity))) return true;
+  return __all_sync(0xFFFFFFFFu, wait(bar, parity, sc));
 }
 
 // After a wait that ran out, one thread: this CTA's copies and MMAs in flight
 // come to rest (again with a limit) before its memory is given back.
 template <int SLOTS>
 __device__ void come_to_rest(AttnCtl<SLOTS>* sc, const AttnP& p) {
-  const uint64_t t0 = cs::globaltimer();
+  record(p.b.ctrl, ERR_WATCHDOG, WHAT_WAIT, blockIdx.x);
+  int tries = 0;
   auto settle = [&](uint64_t* bar, uint32_t parity) {
-    while (!cs::mbar_try_wait(bar, parity) && cs::globaltimer() - t0 < p.wait_ns) {
+    while (!cs::mbar_try_wait(bar, parity) && ++tries < WAIT_TRIES) {
     }
   };
   for (int i = 0; i < SLOTS; ++i) {
@@ -411,7 +414,7 @@ __device__ bool load_role(const AttnP& p, AttnCtl<AttnShape<D>::SLOTS>* sc, uint
     const int* table = p.c.flat ? p.pages : B.table + static_cast<long long>(g.b) * B.table_cols;
     const bool two = g.s.n - g.item * p.c.per_item > p.c.per_tile;
     auto queries = [&](int w) {
-      if (!wait_warp(&sc->q_empty[w], q_phase[w], sc, p, 1)) return false;
+      if (!wait_warp(&sc->q_empty[w], q_phase[w], sc)) return false;
       q_phase[w] ^= 1u;
       if (lane == 0) {
         cs::mbar_arrive_expect_tx(&sc->q_full[w], static_cast<uint32_t>(p.c.per_tile) * B.group * D * 2);
@@ -434,13 +437,15 @@ __device__ bool load_role(const AttnP& p, AttnCtl<AttnShape<D>::SLOTS>* sc, uint
       return -1;
     };
     int page = page_of(g.k0);
+#pragma unroll 1
     for (int k = g.k0; k < g.k1; ++k) {
       const uint32_t boxes = __popc(__ballot_sync(0xFFFFFFFFu, page >= 0));
       const int after = page_of(k + 1);
       const int c3 = p.head_groups ? 0 : g.kvh;
       const int c4 = page * (p.head_groups ? p.head_groups * B.kv_heads : groups) + g.kvh * p.head_groups;
+#pragma unroll 1
       for (int half = 0; half < 2; ++half) {  // K, then V
-        if (!wait_warp(&sc->empty[rp.slot], rp.phase ^ 1u, sc, p, 2)) return false;
+        if (!wait_warp(&sc->empty[rp.slot], rp.phase ^ 1u, sc)) return false;
         if (lane == 0) {
           cs::mbar_arrive_expect_tx(&sc->full[rp.slot], boxes * B.page_size * D * 2);
           ++sc->loads;
@@ -459,15 +464,14 @@ __device__ bool load_role(const AttnP& p, AttnCtl<AttnShape<D>::SLOTS>* sc, uint
   return true;
 }
 
-// One thread.  Step i computes S_i = Q K^T into S buffer i % 2 and then, one step
+// MMA warp.  Step i computes S_i = Q K^T into S buffer i % 2 and then, one step
 // behind, O += P V of step i - 1, so that the tensor core works for one buffer
 // while the other's softmax runs.  An item of two row tiles takes each key tile in
 // two steps, one per row tile; an item of one row tile takes its key tiles in turn
 // (its two buffers are joined at the end).  P takes the place of the first half of
-// S; MMAs execute in the order of their issue.  The issue must keep ahead of
-// 64 cycles per MMA: addresses and descriptors stay in registers (with the
-// tensor-memory base read from shared memory for every MMA, a prompt of 8192
-// tokens and 32 heads took 638 us instead of 502).
+// S; MMAs execute in the order of their issue.  A step's control flow has to
+// take less than its 1024 cycles of MMAs: the whole warp runs it and one lane issues
+// (with one lane running all of it, a step took 1500 cycles).
 template <int D>
 __device__ bool mma_role(const AttnP& p, AttnCtl<AttnShape<D>::SLOTS>* sc, uint8_t* qbuf, uint8_t* ring, int bf16) {
   using Sh = AttnShape<D>;
@@ -477,59 +481,78 @@ __device__ bool mma_role(const AttnP& p, AttnCtl<AttnShape<D>::SLOTS>* sc, uint8
   const uint64_t q_desc = cs::smem_desc_sw128(cs::smem_u32(qbuf), 16, 1024);
   const uint64_t k_desc = cs::smem_desc_sw128(cs::smem_u32(ring), 16, Sh::HALVES * 1024);
   const uint64_t v_desc = cs::smem_desc_sw128(cs::smem_u32(ring), 1024, Sh::HALVES * 1024);
+  const bool leader = elect_one();
   Walk walk(p.b, p.c, sc->range);
   Seg g;
   Ring<Sh::SLOTS> rk, rv;
   rv.next();
   uint32_t q_phase = 0, p_phase = 0;  // bit w
-  while (walk.next(p.b, p.c, g)) {
+  bool ok = true;
+  while (ok && walk.next(p.b, p.c, g)) {
     const bool two = g.s.n - g.item * p.c.per_item > p.c.per_tile;
     const int steps = (g.k1 - g.k0) << (two ? 1 : 0);
-    for (int i = 0; i <= steps; ++i) {
+#pragma unroll 1
+    for (int i = 0; ok && i <= steps; ++i) {
+      const int w = i & 1, v = w ^ 1;  // buffers of this step and the one before
       if (i < steps) {
-        const int w = i & 1, qw = two ? w : 0;
+        const int qw = two ? w : 0;
         if (i < (two ? 2 : 1)) {
-          if (!wait(&sc->q_full[qw], (q_phase >> qw) & 1u, sc, p, 5)) return false;
+          ok = wait_warp(&sc->q_full[qw], (q_phase >> qw) & 1u, sc);
           q_phase ^= 1u << qw;
         }
-        if (!(two && w) && !wait(&sc->full[rk.slot], rk.phase, sc, p, 6)) return false;
+        if (!(two && w)) ok = ok && wait_warp(&sc->full[rk.slot], rk.phase, sc);
+        if (!ok) break;
         cs::tc_fence_after();
-        const uint64_t a = q_desc + qw * (Sh::TILE >> 4), b = k_desc + rk.slot * (Sh::TILE >> 4);
-        const uint32_t d = tm + COL_S + w * 128;
+        if (leader) {
+          uint64_t a = q_desc + qw * (Sh::TILE >> 4), b = k_desc + rk.slot * (Sh::TILE >> 4);
+          const uint32_t d = tm + COL_S + w * 128;
+#pragma unroll 1
+          for (int h = 0; h < Sh::HALVES; ++h, a += KT * 128 >> 4, b += 1024 >> 4)
 #pragma unroll
-        for (int kk = 0; kk < D / 16; ++kk)
-          cs::tc_mma_f16<1>(d, a + ((kk >> 2) * (KT * 128 >> 4) + (kk & 3) * 2), b + ((kk >> 2) * (1024 >> 4) + (kk & 3) * 2),
-                            idesc_s, kk != 0);
-        cs::tc_commit<1>(&sc->s_full[w]);
-        if (!two || w) {
-          cs::tc_commit<1>(&sc->empty[rk.slot]);
-          rk.next(), rk.next();
+            for (int kk = 0; kk < 4; ++kk) cs::tc_mma_f16<1>(d, a + kk * 2, b + kk * 2, idesc_s, h + kk);
+          cs::tc_commit<1>(&sc->s_full[w]);
+          if (!two || w) cs::tc_commit<1>(&sc->empty[rk.slot]);
+          if (i >= steps - (two ? 2 : 1)) cs::tc_commit<1>(&sc->q_empty[qw]);
         }
-        if (i >= steps - (two ? 2 : 1)) cs::tc_commit<1>(&sc->q_empty[qw]);
+        if (!two || w) rk.next(), rk.next();
       }
       if (i > 0) {
-        const int j = i - 1, w = j & 1;
-        if (!(two && w) && !wait(&sc->full[rv.slot], rv.phase, sc, p, 4)) return false;
-        const uint64_t b = v_desc + rv.slot * (Sh::TILE >> 4);
-        const uint32_t d = tm + COL_O + w * D, a = tm + COL_S + w * 128;
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {  // the first 64 keys' weights come before the rest
-          if (!wait(&sc->p_full[w][h], (p_phase >> w) & 1u, sc, p, 3)) return false;
+        if (!(two && v)) ok = wait_warp(&sc->full[rv.slot], rv.phase, sc);
+        uint64_t b = v_desc + rv.slot * (Sh::TILE >> 4);
+        uint32_t a = tm + COL_S + v * 128;
+        const uint32_t d = tm + COL_O + v * D;
+        // the weights of the first 64 keys come before the rest
+#pragma unroll 1
+        for (int h = 0; h < 2; ++h, a += 32, b += Sh::HALVES * 8192 >> 4) {
+          ok = ok && wait_warp(&sc->p_full[v][h], (p_phase >> v) & 1u, sc);
+          if (!ok) break;
           cs::tc_fence_after();
+          if (leader) {
 #pragma unroll
-          for (int kk = 4 * h; kk < 4 * h + 4; ++kk)
-            mma_ts(d, a + kk * 8, b + kk * (Sh::HALVES * 2048 >> 4), idesc_o, kk != 0 || j >= 2);
+            for (int kk = 0; kk < 4; ++kk)
+              mma_ts(d, a + kk * 8, b + kk * (Sh::HALVES * 2048 >> 4), idesc_o, i > 2 || h + kk > 0);
+          }
         }
-        p_phase ^= 1u << w;
-        if (!two || w) {
-          cs::tc_commit<1>(&sc->empty[rv.slot]);
-          rv.next(), rv.next();
+        p_phase ^= 1u << v;
+        if (leader && ok) {
+          if (!two || v) cs::tc_commit<1>(&sc->empty[rv.slot]);
+          if (i > steps - 2) cs::tc_commit<1>(&sc->o_full[v]);
         }
-        if (j >= steps - 2) cs::tc_commit<1>(&sc->o_full[w]);
+        if (!two || v) rv.next(), rv.next();
       }
     }
   }
-  return true;
+  if (!ok && leader) cs::tc_commit<1>(&sc->drained);  // when the MMAs issued so far are done
+  return ok;
+}
+
+// Store 16 consecutive 32-bit columns of this thread's lane.
+__device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t (&r)[16]) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};" ::"r"(taddr),
+      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]),
+      "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
+      : "memory");
 }
 
 // max of three, two multiply-adds and two sums at a time
@@ -557,7 +580,24 @@ __device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
   return d;
 }
 
-// Warpgroup w: the softmax of the steps with buffer w, one row per thread, and the output.
+// x += f * the 32 values of 8 float4s `stride` apart (written by this grid or an earlier one).
+__device__ __forceinline__ void axpy(float (&x)[32], const float4* src, int stride, float f) {
+  float4 y[8];
+#pragma unroll
+  for (int t = 0; t < 8; ++t) y[t] = __ldcg(src + t * stride);
+#pragma unroll
+  for (int t = 0; t < 8; ++t) {
+    x[4 * t] = fmaf(y[t].x, f, x[4 * t]);
+    x[4 * t + 1] = fmaf(y[t].y, f, x[4 * t + 1]);
+    x[4 * t + 2] = fmaf(y[t].z, f, x[4 * t + 2]);
+    x[4 * t + 3] = fmaf(y[t].w, f, x[4 * t + 3]);
+  }
+}
+
+// The bits 0 .. n - 1 (none for n <= 0, all from 32 on).
+__device__ __forceinline__ uint32_t below(int n) { return n >= 32 ? 0xFFFFFFFFu : n <= 0 ? 0u : (1u << n) - 1u; }
+
+// Warpgroup w: the softmax of the steps with S buffer w, one row per thread, and the output.
 template <typename T, int D>
 __device__ bool softmax_role(const AttnP& p, AttnCtl<AttnShape<D>::SLOTS>* sc, uint8_t* ring, int w) {
   using Sh = AttnShape<D>;
@@ -586,7 +626,7 @@ __device__ bool softmax_role(const AttnP& p, AttnCtl<AttnShape<D>::SLOTS>* sc, u
     tiles_done += count;
     const bool two = g.s.n - g.item * p.c.per_item > p.c.per_tile;
     if (!two && w >= count) continue;  // one key tile of one row tile: buffer 0 alone
-    const int tile = two ? w : 0;      // this warpgroup's row tile
+    const int tile = two ? w : 0;      // this buffer's row tile
     const int first = g.item * p.c.per_item + tile * p.c.per_tile;  // its first token
     const int base = g.s.m - g.s.n;
     const int tok = first + row_tok;
@@ -597,10 +637,11 @@ __device__ bool softmax_role(const AttnP& p, AttnCtl<AttnShape<D>::SLOTS>* sc, u
     const int some = p.c.flat ? g.s.m : base + first + 1;
     const int all_lo = p.c.window > 0 ? max(0, base + first + p.c.per_tile - p.c.window) : 0;
     float m_ref = -INFINITY, l = 0.0f;
+#pragma unroll 1
     for (int k = g.k0 + (two ? 0 : w); k < g.k1; k += two ? 1 : 2) {
       const bool fresh = k - g.k0 < (two ? 1 : 2);  // O of this buffer holds nothing yet
       const int j0 = g.key0(k);
-      if (!wait_warp(&sc->s_full[w], s_phase, sc, p, 7 + w)) return false;
+      if (!wait_warp(&sc->s_full[w], s_phase, sc)) return false;
       s_phase ^= 1u;
       cs::tc_fence_after();
       uint32_t v[4][32];
@@ -609,15 +650,15 @@ __device__ bool softmax_role(const AttnP& p, AttnCtl<AttnShape<D>::SLOTS>* sc, u
       cs::tc_wait_ld();
 #pragma unroll
       for (int c = 0; c < 4; ++c) cs::tc_wait_ld_regs(v[c]);
-      if (!(j0 + KT <= some && (j0 >= all_lo || j0 + KT <= p.c.sinks))) {
-        const int rel_end = end - j0, rel_lo = lo - j0, rel_sinks = p.c.sinks - j0;
+      if (__builtin_expect(!(j0 + KT <= some && (j0 >= all_lo || j0 + KT <= p.c.sinks)), 0)) {
 #pragma unroll
-        for (int c = 0; c < 4; ++c)
+        for (int c = 0; c < 4; ++c) {
+          const int j1 = j0 + 32 * c;
+          const uint32_t seen = below(end - j1) & (~below(lo - j1) | below(p.c.sinks - j1));
 #pragma unroll
-          for (int t = 0; t < 32; ++t) {
-            const int j = c * 32 + t;
-            if (j >= rel_end || (j < rel_lo && j >= rel_sinks)) v[c][t] = 0xFF800000u;  // -inf
-          }
+          for (int t = 0; t < 32; ++t)
+            if (!(seen >> t & 1u)) v[c][t] = 0xFF800000u;  // -inf
+        }
       }
       float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
@@ -626,12 +667,12 @@ __device__ bool softmax_role(const AttnP& p, AttnCtl<AttnShape<D>::SLOTS>* sc, u
         for (int t = 0; t < 32; t += 2)
           mx[(t >> 1) & 3] = max3(mx[(t >> 1) & 3], __uint_as_float(v[c][t]), __uint_as_float(v[c][t + 1]));
       const float m_tile = max3(fmaxf(mx[0], mx[1]), mx[2], mx[3]) * p.scale_log2;
-      // P is taken against a reference that is raised only when a row's maximum
-      // exceeds it by more than 2^8 (so P <= 2^8, and rounding to the dtype is as
-      // good as at 1); then O and l are scaled down first
+      // the reference is raised only when a row's maximum exceeds it by more than
+      // 2^8 (so P <= 2^8, and rounding to the dtype is as good as at 1);
+      // then O and l are scaled down first
       const bool raise = m_tile > m_ref + RAISE_LOG2 || (m_ref == -INFINITY && m_tile > -INFINITY);
       const float m_new = raise ? m_tile : m_ref;
-      if (!fresh && __any_sync(0xFFFFFFFFu, raise)) {
+      if (__builtin_expect(!fresh && __any_sync(0xFFFFFFFFu, raise), 0)) {
         // S of this step was issued after P V of the buffer's last one: O is complete
         const float f = raise ? cs::ex2_approx(m_ref - m_new) : 1.0f;
         l *= f;
@@ -647,9 +688,9 @@ __device__ bool softmax_role(const AttnP& p, AttnCtl<AttnShape<D>::SLOTS>* sc, u
       m_ref = m_new;
       // values of keys that no row of the item sees may hold anything: zeros in
       // their place, before any P V of this tile (row tile 0's is issued first)
-      if (tile == 0 && (j0 + KT > g.hi || (j0 < g.lo && j0 + KT > p.c.sinks))) {
+      if (__builtin_expect(tile == 0 && (j0 + KT > g.hi || (j0 < g.lo && j0 + KT > p.c.sinks)), 0)) {
         const uint32_t at = ring0 + 2 * (k - g.k0) + 1, slot = at % Sh::SLOTS;
-        if (!wait_warp(&sc->full[slot], (at / Sh::SLOTS) & 1u, sc, p, 9)) return false;
+        if (!wait_warp(&sc->full[slot], (at / Sh::SLOTS) & 1u, sc)) return false;
         const int j = j0 + r;
         if (j >= g.hi || (j < g.lo && j >= p.c.sinks)) {
           uint8_t* row = ring + slot * Sh::TILE + (r >> 3) * (Sh::HALVES * 1024) + (r & 7) * 128;
@@ -657,48 +698,42 @@ __device__ bool softmax_role(const AttnP& p, AttnCtl<AttnShape<D>::SLOTS>* sc, u
 #pragma unroll
             for (int c = 0; c < 8; ++c) *reinterpret_cast<uint4*>(row + h * 1024 + c * 16) = make_uint4(0, 0, 0, 0);
         }
-        cs::fence_proxy_async_shared();  // and all four warps signal before the MMA reads
+        cs::fence_proxy_async_shared();  // and all warps signal before the MMA reads
       }
       const float sub = m_ref == -INFINITY ? 0.0f : -m_ref;
       const uint64_t sub2 = pack64(sub, sub);
+      uint64_t ls[2] = {0, 0};
 #pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        uint32_t pk[32];
+      for (int c = 0; c < 4; ++c) {
+        uint32_t pk[16];
 #pragma unroll
-        for (int t = 0; t < 64; t += 2) {
-          uint32_t& a = v[2 * h + (t >> 5)][t & 31];
-          uint32_t& b = v[2 * h + (t >> 5)][(t & 31) + 1];
+        for (int t = 0; t < 32; t += 2) {
           float x, y;
-          unpack64(fma2(pack64(__uint_as_float(a), __uint_as_float(b)), scale2, sub2), x, y);
+          unpack64(fma2(pack64(__uint_as_float(v[c][t]), __uint_as_float(v[c][t + 1])), scale2, sub2), x, y);
           x = cs::ex2_approx(x);
           y = cs::ex2_approx(y);
           pk[t >> 1] = Pair<T>::put(x, y);
-          a = __float_as_uint(x);
-          b = __float_as_uint(y);
+          ls[(t >> 1) & 1] = add2(ls[(t >> 1) & 1], pack64(x, y));
         }
-        cs::tmem_st32(s_tm + h * 32, pk);
-        cs::tc_wait_st();
-        cs::tc_fence_before();
-        __syncwarp();
-        if (lane == 0) cs::mbar_arrive(&sc->p_full[w][h]);
+        tmem_st16(s_tm + c * 16, pk);
+        if (c & 1) {
+          cs::tc_wait_st();
+          cs::tc_fence_before();
+          __syncwarp();
+          if (lane == 0) cs::mbar_arrive(&sc->p_full[w][c >> 1]);
+        }
       }
-      uint64_t ls[2] = {0, 0};
-#pragma unroll
-      for (int c = 0; c < 4; ++c)
-#pragma unroll
-        for (int t = 0; t < 32; t += 2)
-          ls[(t >> 1) & 1] = add2(ls[(t >> 1) & 1], pack64(__uint_as_float(v[c][t]), __uint_as_float(v[c][t + 1])));
       float l0, l1;
       unpack64(add2(ls[0], ls[1]), l0, l1);
       l += l0 + l1;
     }
-    if (!wait_warp(&sc->o_full[w], o_phase, sc, p, 10 + w)) return false;
-    o_phase ^= 1u;
+    if (!wait_warp(&sc->o_full[w], o_phase, sc)) return false;
     cs::tc_fence_after();
+    o_phase ^= 1u;
     // the state of this row: O (in tensor memory) and l, both against m_ref
     if (!two && w == 1) {
-      // the other key tiles of warpgroup 0's rows: it joins them
-      if (!wait_warp(&sc->other_empty, x_phase ^ 1u, sc, p, 12)) return false;
+      // the other key tiles of buffer 0's rows, which joins them
+      if (!wait_warp(&sc->other_empty, x_phase ^ 1u, sc)) return false;
       x_phase ^= 1u;
       float4* to = state(blockIdx.x, 2, 0);
 #pragma unroll 1
@@ -709,7 +744,7 @@ __device__ bool softmax_role(const AttnP& p, AttnCtl<AttnShape<D>::SLOTS>* sc, u
 #pragma unroll
           for (int t = 0; t < 8; ++t)
             to[(c * 8 + t) * 128] = make_float4(__uint_as_float(o[4 * t]), __uint_as_float(o[4 * t + 1]),
-                                                __uint_as_float(o[4 * t + 2]), __uint_as_float(o[4 * t + 3]));
+                                                       __uint_as_float(o[4 * t + 2]), __uint_as_float(o[4 * t + 3]));
       }
       if (live) to[D / 4 * 128] = make_float4(m_ref, l, 0.0f, 0.0f);
       cs::tc_fence_before();
@@ -719,7 +754,7 @@ __device__ bool softmax_role(const AttnP& p, AttnCtl<AttnShape<D>::SLOTS>* sc, u
     const float4* other = nullptr;
     float f_own = 1.0f, f_other = 0.0f;
     if (!two && count > 1) {
-      if (!wait_warp(&sc->other_full, x_phase, sc, p, 13)) return false;
+      if (!wait_warp(&sc->other_full, x_phase, sc)) return false;
       x_phase ^= 1u;
       if (live) {
         other = state(blockIdx.x, 2, 0);
@@ -731,137 +766,121 @@ __device__ bool softmax_role(const AttnP& p, AttnCtl<AttnShape<D>::SLOTS>* sc, u
         m_ref = m_new;
       }
     }
-    // 32 columns of the state, both halves joined
-    auto own_chunk = [&](int c, float (&x)[32]) {
-      uint32_t o[32];
-      read_o(c, o);
-#pragma unroll
-      for (int t = 0; t < 32; ++t) x[t] = __uint_as_float(o[t]);
-      if (other) {
-#pragma unroll
-        for (int t = 0; t < 8; ++t) {
-          const float4 y = __ldcg(other + (c * 8 + t) * 128);
-          x[4 * t] = x[4 * t] * f_own + y.x * f_other;
-          x[4 * t + 1] = x[4 * t + 1] * f_own + y.y * f_other;
-          x[4 * t + 2] = x[4 * t + 2] * f_own + y.z * f_other;
-          x[4 * t + 3] = x[4 * t + 3] * f_own + y.w * f_other;
-        }
-      }
-    };
     const long long row = static_cast<long long>(g.s.t0 + tok) * B.heads + g.kvh * B.group + row_head;
-    // the row's output from its final state, of which chunk(c, x) gives 32 columns
-    auto finish = [&](auto chunk) {
-      float f = 1.0f, fold = 0.0f;  // weights of the state and of a prefix's output
-      const float4* pre = nullptr;
-      if (live && !p.c.flat && p.flat_o) {
-        pre = reinterpret_cast<const float4*>(p.flat_o + row * D);
-        const float z = p.flat_lse[row];
-        const float m_new = fmaxf(m_ref, z);
-        f = m_ref == -INFINITY ? 0.0f : cs::ex2_approx(m_ref - m_new);
-        fold = z == -INFINITY ? 0.0f : cs::ex2_approx(z - m_new);
-        l = l * f + fold;
-        m_ref = m_new;
+    const bool whole = g.whole();
+    auto starts_before = [&](unsigned cta) { return sc->range.quota * cta < g.x ? 1 : 0; };
+    unsigned c0 = 0, c1 = 0;  // the CTAs that hold pieces of the item
+    float f = f_own, fold = 0.0f, inv = 1.0f;
+    const float4* pre = nullptr;
+#pragma unroll 1
+    for (int pass = whole ? 1 : 0; pass < 2; ++pass) {  // 0: store this piece; 1: the output
+      if (pass == 1) {
+        if (!whole) {
+          // every thread's stores come before the one arrival at gpu scope; the other
+          // pieces are read after it
+          cs::mbar_arrive(&sc->stored[w]);
+          if (r < 32) {
+            if (!wait_warp(&sc->stored[w], j_phase, sc)) return false;
+            if (r == 0) {
+              uint32_t* ctr = p.arrivals + c0 * 2 + tile;
+              const uint32_t old = cs::atom_add_acq_rel_gpu(ctr, 1u);
+              sc->last[w] = old == c1 - c0;
+              if (old == c1 - c0) *ctr = 0u;  // for the next call
+              cs::mbar_arrive(&sc->counted[w]);
+            }
+            __syncwarp();
+          }
+          if (!wait_warp(&sc->counted[w], j_phase, sc)) return false;
+          j_phase ^= 1u;
+          if (!sc->last[w]) break;
+          // the last to arrive joins the pieces in their order
+          m_ref = -INFINITY;
+          l = 0.0f;
+          if (live) {
+#pragma unroll 1
+            for (unsigned c = c0; c <= c1; ++c) m_ref = fmaxf(m_ref, __ldcg(state(c, starts_before(c), tile) + D / 4 * 128).x);
+#pragma unroll 1
+            for (unsigned c = c0; c <= c1; ++c) {
+              const float4 ml = __ldcg(state(c, starts_before(c), tile) + D / 4 * 128);
+              l = fmaf(ml.y, ml.x == -INFINITY ? 0.0f : cs::ex2_approx(ml.x - m_ref), l);
+            }
+          }
+        }
+        if (live && !p.c.flat && p.flat_o) {  // join the prefix's output
+          pre = reinterpret_cast<const float4*>(p.flat_o + row * D);
+          const float z = p.flat_lse[row];
+          const float m_new = fmaxf(m_ref, z);
+          const float own = m_ref == -INFINITY ? 0.0f : cs::ex2_approx(m_ref - m_new);
+          fold = z == -INFINITY ? 0.0f : cs::ex2_approx(z - m_new);
+          l = l * own + fold;
+          f *= own;
+          f_other *= own;
+          m_ref = m_new;
+        }
+        inv = l == 0.0f ? 0.0f : 1.0f / l;
+      } else {
+        const unsigned me = blockIdx.x, q = static_cast<unsigned>(min(sc->range.quota, 0x80000000ull));
+        const unsigned long long end_x = g.x + g.tiles - 1;
+        c0 = sc->range.x0 > g.x ? me - (static_cast<unsigned>(sc->range.x0 - g.x) + q - 1) / q : me;
+        c1 = end_x >= sc->range.x1 ? me + static_cast<unsigned>(end_x - sc->range.x1) / q + 1 : me;
       }
-      const float inv = l == 0.0f ? 0.0f : 1.0f / l;
+      float4* to = state(blockIdx.x, sc->range.x0 < g.x, tile);
 #pragma unroll 1
       for (int c = 0; c < CH; ++c) {
         float x[32];
-        chunk(c, x);
+        if (pass == 0 || whole) {
+          uint32_t o[32];
+          read_o(c, o);
+#pragma unroll
+          for (int t = 0; t < 32; ++t) x[t] = __uint_as_float(o[t]) * f;
+          if (other) axpy(x, other + c * 8 * 128, 128, f_other);
+        } else if (live) {
+#pragma unroll
+          for (int t = 0; t < 32; ++t) x[t] = 0.0f;
+#pragma unroll 1
+          for (unsigned i = c0; i <= c1; ++i) {
+            const float4* src = state(i, starts_before(i), tile);
+            const float m_i = __ldcg(src + D / 4 * 128).x;
+            axpy(x, src + c * 8 * 128, 128, m_i == -INFINITY ? 0.0f : cs::ex2_approx(m_i - m_ref));
+          }
+        }
         if (!live) continue;
+        if (pass == 0) {
+#pragma unroll
+          for (int t = 0; t < 8; ++t) to[(c * 8 + t) * 128] = make_float4(x[4 * t], x[4 * t + 1], x[4 * t + 2], x[4 * t + 3]);
+          continue;
+        }
+        if (pre) axpy(x, pre + c * 8, 1, fold);
+#pragma unroll
+        for (int t = 0; t < 32; ++t) x[t] *= inv;
         if (p.c.flat) {
           float4* dst = reinterpret_cast<float4*>(p.flat_o + row * D) + c * 8;
 #pragma unroll
-          for (int t = 0; t < 8; ++t)
-            dst[t] = make_float4(x[4 * t] * inv, x[4 * t + 1] * inv, x[4 * t + 2] * inv, x[4 * t + 3] * inv);
-          continue;
-        }
-        if (pre) {
+          for (int t = 0; t < 8; ++t) dst[t] = make_float4(x[4 * t], x[4 * t + 1], x[4 * t + 2], x[4 * t + 3]);
+        } else {
+          uint4* dst = reinterpret_cast<uint4*>(static_cast<T*>(p.out) + (g.s.t0 + tok) * p.out_stride +
+                                                (g.kvh * B.group + row_head) * D + c * 32);
 #pragma unroll
-          for (int t = 0; t < 8; ++t) {
-            const float4 y = pre[c * 8 + t];
-            x[4 * t] = x[4 * t] * f + y.x * fold;
-            x[4 * t + 1] = x[4 * t + 1] * f + y.y * fold;
-            x[4 * t + 2] = x[4 * t + 2] * f + y.z * fold;
-            x[4 * t + 3] = x[4 * t + 3] * f + y.w * fold;
-          }
+          for (int t = 0; t < 4; ++t)
+            dst[t] = make_uint4(Pair<T>::put(x[8 * t], x[8 * t + 1]), Pair<T>::put(x[8 * t + 2], x[8 * t + 3]),
+                                Pair<T>::put(x[8 * t + 4], x[8 * t + 5]), Pair<T>::put(x[8 * t + 6], x[8 * t + 7]));
         }
-        uint4* dst = reinterpret_cast<uint4*>(static_cast<T*>(p.out) + (g.s.t0 + tok) * p.out_stride +
-                                              (g.kvh * B.group + row_head) * D + c * 32);
-#pragma unroll
-        for (int t = 0; t < 4; ++t) {
-          const float* a = x + 8 * t;
-          dst[t] = make_uint4(Pair<T>::put(a[0] * inv, a[1] * inv), Pair<T>::put(a[2] * inv, a[3] * inv),
-                              Pair<T>::put(a[4] * inv, a[5] * inv), Pair<T>::put(a[6] * inv, a[7] * inv));
-        }
-      }
-      if (!live) return;
-      const float lse2 = l == 0.0f ? -INFINITY : m_ref + log2f(l);
-      if (p.c.flat)
-        p.flat_lse[row] = lse2;
-      else if (p.lse)
-        p.lse[row] = lse2 * 0.6931471805599453f;
-    };
-    if (g.whole()) {
-      finish(own_chunk);
-    } else {
-      float4* mine = state(blockIdx.x, sc->range.x0 < g.x, tile);
-#pragma unroll 1
-      for (int c = 0; c < CH; ++c) {
-        float x[32];
-        own_chunk(c, x);
-        if (live)
-#pragma unroll
-          for (int t = 0; t < 8; ++t) mine[(c * 8 + t) * 128] = make_float4(x[4 * t], x[4 * t + 1], x[4 * t + 2], x[4 * t + 3]);
-      }
-      if (live) mine[D / 4 * 128] = make_float4(m_ref, l, 0.0f, 0.0f);
-    }
-    cs::tc_fence_before();
-    if (!two && count > 1) cs::mbar_arrive(&sc->other_empty);
-    if (g.whole()) continue;
-    // every thread's stores come before the one arrival at gpu scope; the other
-    // pieces are read after it
-    const unsigned c0 = sc->range.cta_of(g.x), c1 = sc->range.cta_of(g.x + g.tiles - 1);
-    cs::mbar_arrive(&sc->stored[w]);
-    if (r < 32) {
-      if (!wait_warp(&sc->stored[w], j_phase, sc, p, 15)) return false;
-      if (r == 0) {
-        uint32_t* ctr = p.arrivals + c0 * 2 + tile;
-        const uint32_t old = cs::atom_add_acq_rel_gpu(ctr, 1u);
-        sc->last[w] = old == c1 - c0;
-        if (old == c1 - c0) *ctr = 0u;  // for the next call
-        cs::mbar_arrive(&sc->counted[w]);
       }
       __syncwarp();
-    }
-    if (!wait_warp(&sc->counted[w], j_phase, sc, p, 16)) return false;
-    j_phase ^= 1u;
-    if (sc->last[w] && live) {
-      // the last to arrive joins the pieces in their order
-      auto piece = [&](unsigned c) { return state(c, sc->range.begin_of(c) < g.x, tile); };
-      m_ref = -INFINITY;
-      for (unsigned c = c0; c <= c1; ++c) m_ref = fmaxf(m_ref, __ldcg(piece(c) + D / 4 * 128).x);
-      const float m_all = m_ref == -INFINITY ? 0.0f : m_ref;
-      l = 0.0f;
-      for (unsigned c = c0; c <= c1; ++c) {
-        const float4 ml = __ldcg(piece(c) + D / 4 * 128);
-        l = fmaf(ml.y, cs::ex2_approx(ml.x - m_all), l);
+      if (pass == 0 || whole) {  // O and the other buffer's state are read
+        cs::tc_fence_before();
+        if (!two && count > 1) cs::mbar_arrive(&sc->other_empty);
       }
-      finish([&](int c, float (&x)[32]) {
-#pragma unroll
-        for (int t = 0; t < 32; ++t) x[t] = 0.0f;
-        for (unsigned i = c0; i <= c1; ++i) {
-          const float4* src = piece(i);
-          const float f = cs::ex2_approx(__ldcg(src + D / 4 * 128).x - m_all);
-#pragma unroll
-          for (int t = 0; t < 8; ++t) {
-            const float4 y = __ldcg(src + (c * 8 + t) * 128);
-            x[4 * t] = fmaf(y.x, f, x[4 * t]);
-            x[4 * t + 1] = fmaf(y.y, f, x[4 * t + 1]);
-            x[4 * t + 2] = fmaf(y.z, f, x[4 * t + 2]);
-            x[4 * t + 3] = fmaf(y.w, f, x[4 * t + 3]);
-          }
-        }
-      });
+      if (!live) continue;
+      if (pass == 0) {
+        to[D / 4 * 128] = make_float4(m_ref, l, 0.0f, 0.0f);
+      } else {
+        const float lse2 = l == 0.0f ? -INFINITY : m_ref + log2f(l);
+        if (p.c.flat)
+          p.flat_lse[row] = lse2;
+        else if (p.lse)
+          p.lse[row] = lse2 * 0.6931471805599453f;
+      }
     }
     __syncwarp();
   }
@@ -872,7 +891,7 @@ template <typename T, int D>
 __global__ void __launch_bounds__(ATTN_THREADS, 1) cs_kv_attn_kernel(const __grid_constant__ AttnP p) {
   using Sh = AttnShape<D>;
   using Ctl = AttnCtl<Sh::SLOTS>;
-  static_assert(sizeof(Ctl) <= 1024, "control block");
+  static_assert(sizeof(Ctl) <= CTL, "control block");
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   uint8_t* qbuf = smem;
@@ -888,7 +907,7 @@ __global__ void __launch_bounds__(ATTN_THREADS, 1) cs_kv_attn_kernel(const __gri
       cs::mbar_init(&sc->q_full[w], 1);
       cs::mbar_init(&sc->q_empty[w], 1);
       cs::mbar_init(&sc->s_full[w], 1);
-      for (int h = 0; h < 2; ++h) cs::mbar_init(&sc->p_full[w][h], 4);  // the warps of a warpgroup
+      for (int h = 0; h < 2; ++h) cs::mbar_init(&sc->p_full[w][h], 4);  // the warps of its warpgroup
       cs::mbar_init(&sc->o_full[w], 1);
       cs::mbar_init(&sc->stored[w], 128);
       cs::mbar_init(&sc->counted[w], 1);
@@ -919,8 +938,7 @@ __global__ void __launch_bounds__(ATTN_THREADS, 1) cs_kv_attn_kernel(const __gri
   } else {
     regs_dec<OTHER_REGS>();
     if (warp == 8) load_role<D>(p, sc, qbuf, ring);
-    // `drained`, after a wait that ran out: the MMAs issued so far are done
-    if (warp == 9 && elect_one() && !mma_role<D>(p, sc, qbuf, ring, bf16)) cs::tc_commit<1>(&sc->drained);
+    if (warp == 9) mma_role<D>(p, sc, qbuf, ring, bf16);
   }
   __syncwarp();
   cs::tc_fence_before();
