@@ -269,7 +269,7 @@ struct AttnP {
 };
 
 // Two softmax warpgroups, one per S buffer with a row per thread, and one with the
-// TMA warp, the MMA warp and two idle ones.
+// TMA warp, two MMA warps and an idle one.
 constexpr int ATTN_THREADS = 384;
 // Registers: 65536 / 384 gives every thread 168 at launch; a softmax thread holds a
 // row of S, so the third warpgroup hands over what it does not need
@@ -464,85 +464,90 @@ __device__ bool load_role(const AttnP& p, AttnCtl<AttnShape<D>::SLOTS>* sc, uint
   return true;
 }
 
-// MMA warp.  Step i computes S_i = Q K^T into S buffer i % 2 and then, one step
-// behind, O += P V of step i - 1, so that the tensor core works for one buffer
-// while the other's softmax runs.  An item of two row tiles takes each key tile in
-// two steps, one per row tile; an item of one row tile takes its key tiles in turn
-// (its two buffers are joined at the end).  P takes the place of the first half of
-// S; MMAs execute in the order of their issue.  A step's control flow has to
-// take less than its 1024 cycles of MMAs: the whole warp runs it and one lane issues
-// (with one lane running all of it, a step took 1500 cycles).
+// MMA warp w works for S buffer w: S = Q K^T, then, once the softmax has put P into the
+// first half of S, O += P V.  An item of two row tiles has one for each buffer; of an item
+// of one row tile the buffers take the key tiles in turn (and are joined at the end).
+// The issue of an MMA holds its warp for the 64 cycles that the tensor core works
+// on one, so whatever else the warp does leaves the tensor core idle, unless the other
+// buffer's warp is issuing: with one warp for both buffers a step of 1024 cycles took 2300.
+// A buffer's MMAs are issued by one thread and execute in that order, and no
+// MMA reads what the other buffer's write.
 template <int D>
-__device__ bool mma_role(const AttnP& p, AttnCtl<AttnShape<D>::SLOTS>* sc, uint8_t* qbuf, uint8_t* ring, int bf16) {
+__device__ bool mma_role(const AttnP& p, AttnCtl<AttnShape<D>::SLOTS>* sc, uint8_t* qbuf, uint8_t* ring, int bf16, int w) {
   using Sh = AttnShape<D>;
   const uint32_t idesc_s = cs::make_idesc_f16(bf16, 0, 128, KT);
   const uint32_t idesc_o = cs::make_idesc_f16(bf16, 1, 128, D);
-  const uint32_t tm = sc->tmem;
+  const uint32_t s_tm = sc->tmem + COL_S + w * 128, o_tm = sc->tmem + COL_O + w * D;
   const uint64_t q_desc = cs::smem_desc_sw128(cs::smem_u32(qbuf), 16, 1024);
   const uint64_t k_desc = cs::smem_desc_sw128(cs::smem_u32(ring), 16, Sh::HALVES * 1024);
   const uint64_t v_desc = cs::smem_desc_sw128(cs::smem_u32(ring), 1024, Sh::HALVES * 1024);
   const bool leader = elect_one();
   Walk walk(p.b, p.c, sc->range);
   Seg g;
-  Ring<Sh::SLOTS> rk, rv;
-  rv.next();
-  uint32_t q_phase = 0, p_phase = 0;  // bit w
+  Ring<Sh::SLOTS> r;
+  uint32_t q_phase = 0, p_phase = 0;  // q_phase: bit per query buffer
   bool ok = true;
   while (ok && walk.next(p.b, p.c, g)) {
     const bool two = g.s.n - g.item * p.c.per_item > p.c.per_tile;
-    const int steps = (g.k1 - g.k0) << (two ? 1 : 0);
+    const int qw = two ? w : 0, count = g.k1 - g.k0;
+    const bool any = two || w < count;  // this buffer has key tiles
+    const int last = two ? count - 1 : count - 1 - ((count - 1 - w) & 1);  // the last of them
+    ok = wait_warp(&sc->q_full[qw], (q_phase >> qw) & 1u, sc);
+    if (!ok) break;
+    q_phase ^= two ? 3u : 1u;
+    // both warps give the first queries back, warp 1 at once where it does not read them (the
+    // wait above keeps it from doing so for an item before its queries are loaded)
+    if (leader && w == 1 && (two || !any)) cs::mbar_arrive(&sc->q_empty[0]);
 #pragma unroll 1
-    for (int i = 0; ok && i <= steps; ++i) {
-      const int w = i & 1, v = w ^ 1;  // buffers of this step and the one before
-      if (i < steps) {
-        const int qw = two ? w : 0;
-        if (i < (two ? 2 : 1)) {
-          ok = wait_warp(&sc->q_full[qw], (q_phase >> qw) & 1u, sc);
-          q_phase ^= 1u << qw;
-        }
-        if (!(two && w)) ok = ok && wait_warp(&sc->full[rk.slot], rk.phase, sc);
-        if (!ok) break;
+    for (int t = 0; ok && t < count; ++t) {
+      const bool use = two || (t & 1) == w;
+      ok = wait_warp(&sc->full[r.slot], r.phase, sc);
+      if (!ok) break;
+      if (use) {
         cs::tc_fence_after();
         if (leader) {
-          uint64_t a = q_desc + qw * (Sh::TILE >> 4), b = k_desc + rk.slot * (Sh::TILE >> 4);
-          const uint32_t d = tm + COL_S + w * 128;
+          uint64_t a = q_desc + qw * (Sh::TILE >> 4), b = k_desc + r.slot * (Sh::TILE >> 4);
 #pragma unroll 1
           for (int h = 0; h < Sh::HALVES; ++h, a += KT * 128 >> 4, b += 1024 >> 4)
 #pragma unroll
-            for (int kk = 0; kk < 4; ++kk) cs::tc_mma_f16<1>(d, a + kk * 2, b + kk * 2, idesc_s, h + kk);
+            for (int kk = 0; kk < 4; ++kk) cs::tc_mma_f16<1>(s_tm, a + kk * 2, b + kk * 2, idesc_s, h + kk);
           cs::tc_commit<1>(&sc->s_full[w]);
-          if (!two || w) cs::tc_commit<1>(&sc->empty[rk.slot]);
-          if (i >= steps - (two ? 2 : 1)) cs::tc_commit<1>(&sc->q_empty[qw]);
+          cs::tc_commit<1>(&sc->empty[r.slot]);
+          if (t == last) cs::tc_commit<1>(&sc->q_empty[qw]);
         }
-        if (!two || w) rk.next(), rk.next();
+      } else if (leader) {
+        cs::mbar_arrive(&sc->empty[r.slot]);
       }
-      if (i > 0) {
-        if (!(two && v)) ok = wait_warp(&sc->full[rv.slot], rv.phase, sc);
-        uint64_t b = v_desc + rv.slot * (Sh::TILE >> 4);
-        uint32_t a = tm + COL_S + v * 128;
-        const uint32_t d = tm + COL_O + v * D;
+      r.next();
+      ok = wait_warp(&sc->full[r.slot], r.phase, sc);
+      if (!ok) break;
+      if (use) {
+        uint64_t b = v_desc + r.slot * (Sh::TILE >> 4);
+        uint32_t a = s_tm;
         // the weights of the first 64 keys come before the rest
 #pragma unroll 1
         for (int h = 0; h < 2; ++h, a += 32, b += Sh::HALVES * 8192 >> 4) {
-          ok = ok && wait_warp(&sc->p_full[v][h], (p_phase >> v) & 1u, sc);
+          ok = ok && wait_warp(&sc->p_full[w][h], p_phase, sc);
           if (!ok) break;
           cs::tc_fence_after();
           if (leader) {
 #pragma unroll
             for (int kk = 0; kk < 4; ++kk)
-              mma_ts(d, a + kk * 8, b + kk * (Sh::HALVES * 2048 >> 4), idesc_o, i > 2 || h + kk > 0);
+              mma_ts(o_tm, a + kk * 8, b + kk * (Sh::HALVES * 2048 >> 4), idesc_o, t >= (two ? 1 : 2) || h + kk > 0);
           }
         }
-        p_phase ^= 1u << v;
+        p_phase ^= 1u;
         if (leader && ok) {
-          if (!two || v) cs::tc_commit<1>(&sc->empty[rv.slot]);
-          if (i > steps - 2) cs::tc_commit<1>(&sc->o_full[v]);
+          cs::tc_commit<1>(&sc->empty[r.slot]);
+          if (t == last) cs::tc_commit<1>(&sc->o_full[w]);
         }
-        if (!two || v) rv.next(), rv.next();
+      } else if (leader) {
+        cs::mbar_arrive(&sc->empty[r.slot]);
       }
+      r.next();
     }
   }
-  if (!ok && leader) cs::tc_commit<1>(&sc->drained);  // when the MMAs issued so far are done
+  if (leader) cs::tc_commit<1>(&sc->drained);  // all MMAs of this warp are done
   return ok;
 }
 
@@ -644,28 +649,39 @@ __device__ bool softmax_role(const AttnP& p, AttnCtl<AttnShape<D>::SLOTS>* sc, u
       if (!wait_warp(&sc->s_full[w], s_phase, sc)) return false;
       s_phase ^= 1u;
       cs::tc_fence_after();
-      uint32_t v[4][32];
-#pragma unroll
-      for (int c = 0; c < 4; ++c) cs::tmem_ld32(s_tm + c * 32, v[c]);
-      cs::tc_wait_ld();
-#pragma unroll
-      for (int c = 0; c < 4; ++c) cs::tc_wait_ld_regs(v[c]);
+      // The row is read twice, for its maximum and for its weights: in registers
+      // all along it would need all its 128 values' code in line, and with that the hot loops of
+      // the roles no longer fit the instruction caches next to each other.
+      float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
       if (__builtin_expect(!(j0 + KT <= some && (j0 >= all_lo || j0 + KT <= p.c.sinks)), 0)) {
-#pragma unroll
-        for (int c = 0; c < 4; ++c) {
+#pragma unroll 1
+        for (int c = 0; c < 4; ++c) {  // hidden scores become -inf in place
           const int j1 = j0 + 32 * c;
           const uint32_t seen = below(end - j1) & (~below(lo - j1) | below(p.c.sinks - j1));
+          uint32_t v[32];
+          cs::tmem_ld32(s_tm + c * 32, v);
+          cs::tc_wait_ld();
+          cs::tc_wait_ld_regs(v);
 #pragma unroll
           for (int t = 0; t < 32; ++t)
-            if (!(seen >> t & 1u)) v[c][t] = 0xFF800000u;  // -inf
+            if (!(seen >> t & 1u)) v[t] = 0xFF800000u;
+          cs::tmem_st32(s_tm + c * 32, v);
+        }
+        cs::tc_wait_st();
+      }
+      {
+        uint32_t v[4][32];
+#pragma unroll
+        for (int c = 0; c < 4; ++c) cs::tmem_ld32(s_tm + c * 32, v[c]);
+        cs::tc_wait_ld();
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+          cs::tc_wait_ld_regs(v[c]);
+#pragma unroll
+          for (int t = 0; t < 32; t += 2)
+            mx[(t >> 1) & 3] = max3(mx[(t >> 1) & 3], __uint_as_float(v[c][t]), __uint_as_float(v[c][t + 1]));
         }
       }
-      float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
-#pragma unroll
-      for (int c = 0; c < 4; ++c)
-#pragma unroll
-        for (int t = 0; t < 32; t += 2)
-          mx[(t >> 1) & 3] = max3(mx[(t >> 1) & 3], __uint_as_float(v[c][t]), __uint_as_float(v[c][t + 1]));
       const float m_tile = max3(fmaxf(mx[0], mx[1]), mx[2], mx[3]) * p.scale_log2;
       // the reference is raised only when a row's maximum exceeds it by more than
       // 2^8 (so P <= 2^8, and rounding to the dtype is as good as at 1);
@@ -687,8 +703,8 @@ __device__ bool softmax_role(const AttnP& p, AttnCtl<AttnShape<D>::SLOTS>* sc, u
       }
       m_ref = m_new;
       // values of keys that no row of the item sees may hold anything: zeros in
-      // their place, before any P V of this tile (row tile 0's is issued first)
-      if (__builtin_expect(tile == 0 && (j0 + KT > g.hi || (j0 < g.lo && j0 + KT > p.c.sinks)), 0)) {
+      // their place before this buffer's P V (the other buffer's warps write them as well)
+      if (__builtin_expect(j0 + KT > g.hi || (j0 < g.lo && j0 + KT > p.c.sinks), 0)) {
         const uint32_t at = ring0 + 2 * (k - g.k0) + 1, slot = at % Sh::SLOTS;
         if (!wait_warp(&sc->full[slot], (at / Sh::SLOTS) & 1u, sc)) return false;
         const int j = j0 + r;
@@ -703,25 +719,31 @@ __device__ bool softmax_role(const AttnP& p, AttnCtl<AttnShape<D>::SLOTS>* sc, u
       const float sub = m_ref == -INFINITY ? 0.0f : -m_ref;
       const uint64_t sub2 = pack64(sub, sub);
       uint64_t ls[2] = {0, 0};
+#pragma unroll 1
+      for (int h = 0; h < 2; ++h) {  // 64 keys at a time: P V of the first half starts while the second is computed
+        uint32_t v[2][32];
+        cs::tmem_ld32(s_tm + h * 64, v[0]);
+        cs::tmem_ld32(s_tm + h * 64 + 32, v[1]);
+        cs::tc_wait_ld();
 #pragma unroll
-      for (int c = 0; c < 4; ++c) {
-        uint32_t pk[16];
+        for (int c = 0; c < 2; ++c) {
+          cs::tc_wait_ld_regs(v[c]);
+          uint32_t pk[16];
 #pragma unroll
-        for (int t = 0; t < 32; t += 2) {
-          float x, y;
-          unpack64(fma2(pack64(__uint_as_float(v[c][t]), __uint_as_float(v[c][t + 1])), scale2, sub2), x, y);
-          x = cs::ex2_approx(x);
-          y = cs::ex2_approx(y);
-          pk[t >> 1] = Pair<T>::put(x, y);
-          ls[(t >> 1) & 1] = add2(ls[(t >> 1) & 1], pack64(x, y));
+          for (int t = 0; t < 32; t += 2) {
+            float x, y;
+            unpack64(fma2(pack64(__uint_as_float(v[c][t]), __uint_as_float(v[c][t + 1])), scale2, sub2), x, y);
+            x = cs::ex2_approx(x);
+            y = cs::ex2_approx(y);
+            pk[t >> 1] = Pair<T>::put(x, y);
+            ls[(t >> 1) & 1] = add2(ls[(t >> 1) & 1], pack64(x, y));
+          }
+          tmem_st16(s_tm + h * 32 + c * 16, pk);
         }
-        tmem_st16(s_tm + c * 16, pk);
-        if (c & 1) {
-          cs::tc_wait_st();
-          cs::tc_fence_before();
-          __syncwarp();
-          if (lane == 0) cs::mbar_arrive(&sc->p_full[w][c >> 1]);
-        }
+        cs::tc_wait_st();
+        cs::tc_fence_before();
+        __syncwarp();
+        if (lane == 0) cs::mbar_arrive(&sc->p_full[w][h]);
       }
       float l0, l1;
       unpack64(add2(ls[0], ls[1]), l0, l1);
@@ -901,11 +923,11 @@ __global__ void __launch_bounds__(ATTN_THREADS, 1) cs_kv_attn_kernel(const __gri
   if (threadIdx.x == 0) {
     for (int i = 0; i < Sh::SLOTS; ++i) {
       cs::mbar_init(&sc->full[i], 1);
-      cs::mbar_init(&sc->empty[i], 1);
+      cs::mbar_init(&sc->empty[i], 2);  // both MMA warps
     }
     for (int w = 0; w < 2; ++w) {
       cs::mbar_init(&sc->q_full[w], 1);
-      cs::mbar_init(&sc->q_empty[w], 1);
+      cs::mbar_init(&sc->q_empty[w], w == 0 ? 2 : 1);
       cs::mbar_init(&sc->s_full[w], 1);
       for (int h = 0; h < 2; ++h) cs::mbar_init(&sc->p_full[w][h], 4);  // the warps of its warpgroup
       cs::mbar_init(&sc->o_full[w], 1);
@@ -914,7 +936,7 @@ __global__ void __launch_bounds__(ATTN_THREADS, 1) cs_kv_attn_kernel(const __gri
     }
     cs::mbar_init(&sc->other_full, 128);
     cs::mbar_init(&sc->other_empty, 128);
-    cs::mbar_init(&sc->drained, 1);
+    cs::mbar_init(&sc->drained, 2);
     sc->abort = sc->loads = sc->q_loads[0] = sc->q_loads[1] = 0;
     cs::fence_mbar_init();
     cs::prefetch_tmap(&p.q);
@@ -938,7 +960,7 @@ __global__ void __launch_bounds__(ATTN_THREADS, 1) cs_kv_attn_kernel(const __gri
   } else {
     regs_dec<OTHER_REGS>();
     if (warp == 8) load_role<D>(p, sc, qbuf, ring);
-    if (warp == 9) mma_role<D>(p, sc, qbuf, ring, bf16);
+    if (warp == 9 || warp == 10) mma_role<D>(p, sc, qbuf, ring, bf16, warp - 9);
   }
   __syncwarp();
   cs::tc_fence_before();
