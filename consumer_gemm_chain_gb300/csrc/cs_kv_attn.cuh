@@ -301,6 +301,7 @@ template <int SLOTS>
 struct AttnCtl {
   uint64_t full[SLOTS], empty[SLOTS];
   uint64_t q_full[2], q_empty[2], s_full[2], p_full[2][2], o_full[2];
+  uint64_t v_ready[2];                 // the values of the buffer's tile are there
   uint64_t stored[2], counted[2];      // a piece is stored; its arrival is counted
   uint64_t other_full, other_empty;    // warpgroup 1's half of an item of one row tile
   uint64_t drained;
@@ -484,24 +485,26 @@ __device__ bool mma_role(const AttnP& p, AttnCtl<AttnShape<D>::SLOTS>* sc, uint8
   const bool leader = elect_one();
   Walk walk(p.b, p.c, sc->range);
   Seg g;
+  // Both warps watch every tile arrive, and give back the ones they do not read
+  // too: a barrier's parity tells two phases apart, so no reader may be two behind.
   Ring<Sh::SLOTS> r;
   uint32_t q_phase = 0, p_phase = 0;  // q_phase: bit per query buffer
   bool ok = true;
   while (ok && walk.next(p.b, p.c, g)) {
     const bool two = g.s.n - g.item * p.c.per_item > p.c.per_tile;
     const int qw = two ? w : 0, count = g.k1 - g.k0;
-    const bool any = two || w < count;  // this buffer has key tiles
-    const int last = two ? count - 1 : count - 1 - ((count - 1 - w) & 1);  // the last of them
     ok = wait_warp(&sc->q_full[qw], (q_phase >> qw) & 1u, sc);
     if (!ok) break;
     q_phase ^= two ? 3u : 1u;
     // both warps give the first queries back, warp 1 at once where it does not read them (the
     // wait above keeps it from doing so for an item before its queries are loaded)
-    if (leader && w == 1 && (two || !any)) cs::mbar_arrive(&sc->q_empty[0]);
+    if (leader && w == 1 && (two || count == 1)) cs::mbar_arrive(&sc->q_empty[0]);
+    bool early = false;  // this tile's keys were seen before the last P V
+    int v_late = -1;     // slot of V that the last P V read, to be given back
 #pragma unroll 1
-    for (int t = 0; ok && t < count; ++t) {
+    for (int t = 0; t < count; ++t) {
       const bool use = two || (t & 1) == w;
-      ok = wait_warp(&sc->full[r.slot], r.phase, sc);
+      if (!early) ok = wait_warp(&sc->full[r.slot], r.phase, sc);
       if (!ok) break;
       if (use) {
         cs::tc_fence_after();
@@ -513,38 +516,48 @@ __device__ bool mma_role(const AttnP& p, AttnCtl<AttnShape<D>::SLOTS>* sc, uint8
             for (int kk = 0; kk < 4; ++kk) cs::tc_mma_f16<1>(s_tm, a + kk * 2, b + kk * 2, idesc_s, h + kk);
           cs::tc_commit<1>(&sc->s_full[w]);
           cs::tc_commit<1>(&sc->empty[r.slot]);
-          if (t == last) cs::tc_commit<1>(&sc->q_empty[qw]);
+          if (v_late >= 0) cs::tc_commit<1>(&sc->empty[v_late]);
+          if (t + (two ? 1 : 2) >= count) cs::tc_commit<1>(&sc->q_empty[qw]);
         }
+        v_late = -1;
       } else if (leader) {
         cs::mbar_arrive(&sc->empty[r.slot]);
       }
+      early = false;
       r.next();
       ok = wait_warp(&sc->full[r.slot], r.phase, sc);
       if (!ok) break;
-      if (use) {
-        uint64_t b = v_desc + r.slot * (Sh::TILE >> 4);
-        uint32_t a = s_tm;
-        // the weights of the first 64 keys come before the rest
-#pragma unroll 1
-        for (int h = 0; h < 2; ++h, a += 32, b += Sh::HALVES * 8192 >> 4) {
-          ok = ok && wait_warp(&sc->p_full[w][h], p_phase, sc);
-          if (!ok) break;
-          cs::tc_fence_after();
-          if (leader) {
-#pragma unroll
-            for (int kk = 0; kk < 4; ++kk)
-              mma_ts(o_tm, a + kk * 8, b + kk * (Sh::HALVES * 2048 >> 4), idesc_o, t >= (two ? 1 : 2) || h + kk > 0);
-          }
-        }
-        p_phase ^= 1u;
-        if (leader && ok) {
-          cs::tc_commit<1>(&sc->empty[r.slot]);
-          if (t == last) cs::tc_commit<1>(&sc->o_full[w]);
-        }
-      } else if (leader) {
-        cs::mbar_arrive(&sc->empty[r.slot]);
+      if (!use) {
+        if (leader) cs::mbar_arrive(&sc->empty[r.slot]);
+        r.next();
+        continue;
       }
+      if (leader) cs::mbar_arrive(&sc->v_ready[w]);
+      const int sv = r.slot;
       r.next();
+      // with the next tile's keys there, its S is issued right behind this P V
+      early = two && t + 1 < count && __all_sync(0xFFFFFFFFu, cs::mbar_test_wait(&sc->full[r.slot], r.phase));
+      uint64_t b = v_desc + sv * (Sh::TILE >> 4);
+      uint32_t a = s_tm;
+      // the weights of the first 64 keys come before the rest
+#pragma unroll 1
+      for (int h = 0; h < 2; ++h, a += 32, b += Sh::HALVES * 8192 >> 4) {
+        ok = ok && wait_warp(&sc->p_full[w][h], p_phase, sc);
+        if (!ok) break;
+        cs::tc_fence_after();
+        if (leader) {
+#pragma unroll
+          for (int kk = 0; kk < 4; ++kk)
+            mma_ts(o_tm, a + kk * 8, b + kk * (Sh::HALVES * 2048 >> 4), idesc_o, t >= (two ? 1 : 2) || h + kk > 0);
+        }
+      }
+      if (!ok) break;
+      p_phase ^= 1u;
+      if (early)
+        v_late = sv;
+      else if (leader)
+        cs::tc_commit<1>(&sc->empty[sv]);
+      if (leader && t + (two ? 1 : 2) >= count) cs::tc_commit<1>(&sc->o_full[w]);
     }
   }
   if (leader) cs::tc_commit<1>(&sc->drained);  // all MMAs of this warp are done
@@ -705,8 +718,8 @@ __device__ bool softmax_role(const AttnP& p, AttnCtl<AttnShape<D>::SLOTS>* sc, u
       // values of keys that no row of the item sees may hold anything: zeros in
       // their place before this buffer's P V (the other buffer's warps write them as well)
       if (__builtin_expect(j0 + KT > g.hi || (j0 < g.lo && j0 + KT > p.c.sinks), 0)) {
-        const uint32_t at = ring0 + 2 * (k - g.k0) + 1, slot = at % Sh::SLOTS;
-        if (!wait_warp(&sc->full[slot], (at / Sh::SLOTS) & 1u, sc)) return false;
+        const uint32_t slot = (ring0 + 2 * (k - g.k0) + 1) % Sh::SLOTS;
+        if (!wait_warp(&sc->v_ready[w], s_phase ^ 1u, sc)) return false;
         const int j = j0 + r;
         if (j >= g.hi || (j < g.lo && j >= p.c.sinks)) {
           uint8_t* row = ring + slot * Sh::TILE + (r >> 3) * (Sh::HALVES * 1024) + (r & 7) * 128;
@@ -931,6 +944,7 @@ __global__ void __launch_bounds__(ATTN_THREADS, 1) cs_kv_attn_kernel(const __gri
       cs::mbar_init(&sc->s_full[w], 1);
       for (int h = 0; h < 2; ++h) cs::mbar_init(&sc->p_full[w][h], 4);  // the warps of its warpgroup
       cs::mbar_init(&sc->o_full[w], 1);
+      cs::mbar_init(&sc->v_ready[w], 1);
       cs::mbar_init(&sc->stored[w], 128);
       cs::mbar_init(&sc->counted[w], 1);
     }
