@@ -10,7 +10,7 @@
 #include <new>
 
 #include "../../include/cs_kv.h"
-#include "cs_kv_attn.cuh"
+#include "cs_kv_rows.cuh"
 #include "cs_tune.h"  // cs_fail
 
 #define KV_CUDA(call)                                                                              \
@@ -210,26 +210,27 @@ cs_status check_attn(const cs_kv_s* p, const cs_kv_batch* b, const cs_kv_attn_ar
   if (!aligned16(a->q) || !aligned16(a->out)) return cs_fail(CS_ERR_INVALID_ARG, "q and out must be 16-byte aligned");
   if (a->q == a->out) return cs_fail(CS_ERR_INVALID_ARG, "out must not be q");
   k.b = device_batch(p, b);
-  k.c.per_tile = 128 / k.b.group;
-  k.c.per_item = 2 * k.c.per_tile;
-  k.c.item_cost = 1;
   // a window as long as any sequence hides nothing
   k.c.window = d.window >= kMaxKeys ? 0 : d.window;
   k.c.sinks = k.c.window == 0 ? 0 : d.sinks < kMaxKeys ? d.sinks : kMaxKeys;
+  k.c.item_cost = 1;
   k.out = a->out;
   k.lse = a->lse;
   const double scale = d.scale > 0.0f ? d.scale : 1.0 / std::sqrt(static_cast<double>(d.head_dim));
   k.scale_log2 = static_cast<float>(scale * 1.4426950408889634);
   k.part = p->part;
   k.arrivals = p->ctrl + cskv::CTRL_COUNTERS;
-  k.head_groups = d.cache_layout == CS_KV_HEAD ? d.page_size / 8 : 0;
-  const cuuint64_t dims[3] = {static_cast<cuuint64_t>(d.head_dim), static_cast<cuuint64_t>(d.heads),
-                              static_cast<cuuint64_t>(b->tokens)};
-  const cuuint64_t strides[2] = {static_cast<cuuint64_t>(d.head_dim) * 2, static_cast<cuuint64_t>(q_stride) * 2};
-  const cuuint32_t box[3] = {64, static_cast<cuuint32_t>(k.b.group), static_cast<cuuint32_t>(k.c.per_tile)};
-  if ((s = encode(&k.q, d.dtype == CS_BF16, a->q, 3, dims, strides, box, "q")) != CS_OK) return s;
-  if ((s = encode_cache(p, k.b, &k.k, a->k_cache, "k_cache")) != CS_OK) return s;
-  return encode_cache(p, k.b, &k.v, a->v_cache, "v_cache");
+  k.q_raw = a->q;
+  k.k_raw = a->k_cache;
+  k.v_raw = a->v_cache;
+  k.q_stride = q_stride;
+  k.out_wide = reinterpret_cast<uintptr_t>(a->out) % 32 == 0 && k.out_stride % 16 == 0;
+  return CS_OK;
+}
+
+int rows_grid(const cs_kv_s* p) {
+  const int n = p->num_sms * cskv::ROWS_CTAS;
+  return n < cskv::ROWS_MAX_GRID ? n : cskv::ROWS_MAX_GRID;
 }
 
 const void* attn_kernel(const cs_kv_desc& d, int* smem) {
@@ -240,10 +241,34 @@ const void* attn_kernel(const cs_kv_desc& d, int* smem) {
   return d.head_dim == 128 ? (const void*)cskv::cs_kv_attn_kernel<__half, 128> : (const void*)cskv::cs_kv_attn_kernel<__half, 64>;
 }
 
-cs_status run_attention(cs_kv_s* p, cskv::AttnP& k, cudaStream_t st) {
-  if (k.b.tokens == 0 || k.b.seqs == 0) return CS_OK;
+// Up to 16 rows (tokens x query heads) of a sequence per key head are read by the rows
+// kernel, which is bound by the keys' bytes and has the shorter latency; more by the
+// tensor-core kernel.
+cs_status run_attention(cs_kv_s* p, cskv::AttnP& k, int max_rows, cudaStream_t st) {
+  const cs_kv_desc& d = p->d;
+  const bool bf16 = d.dtype == CS_BF16, wide = d.head_dim == 128;
+  if (max_rows <= cskv::ROWS) {
+    k.c.per_item = cskv::ROWS / k.b.group;
+    k.c.shift = cskv::ROWS_SHIFT;
+    const void* fn = bf16 ? (wide ? (const void*)cskv::cs_kv_rows_kernel<__nv_bfloat16, 128>
+                                  : (const void*)cskv::cs_kv_rows_kernel<__nv_bfloat16, 64>)
+                          : (wide ? (const void*)cskv::cs_kv_rows_kernel<__half, 128> : (const void*)cskv::cs_kv_rows_kernel<__half, 64>);
+    return launch(fn, dim3(rows_grid(p)), cskv::ROWS_THREADS, 0, &k, st);
+  }
+  k.per_tile = 128 / k.b.group;
+  k.c.per_item = 2 * k.per_tile;
+  k.c.shift = 7;
+  k.head_groups = d.cache_layout == CS_KV_HEAD ? d.page_size / 8 : 0;
+  const cuuint64_t dims[3] = {static_cast<cuuint64_t>(d.head_dim), static_cast<cuuint64_t>(d.heads),
+                              static_cast<cuuint64_t>(k.b.tokens)};
+  const cuuint64_t strides[2] = {static_cast<cuuint64_t>(d.head_dim) * 2, static_cast<cuuint64_t>(k.q_stride) * 2};
+  const cuuint32_t box[3] = {64, static_cast<cuuint32_t>(k.b.group), static_cast<cuuint32_t>(k.per_tile)};
+  cs_status s = encode(&k.q, bf16, k.q_raw, 3, dims, strides, box, "q");
+  if (s == CS_OK) s = encode_cache(p, k.b, &k.k, k.k_raw, "k_cache");
+  if (s == CS_OK) s = encode_cache(p, k.b, &k.v, k.v_raw, "v_cache");
+  if (s != CS_OK) return s;
   int smem = 0;
-  const void* fn = attn_kernel(p->d, &smem);
+  const void* fn = attn_kernel(d, &smem);
   return launch(fn, dim3(p->num_sms), cskv::ATTN_THREADS, smem, &k, st);
 }
 
@@ -294,6 +319,12 @@ cs_status append(cs_kv_s* p, const cs_kv_batch* b, const cs_kv_append_args* a, c
   return launch(fn, grid, cskv::APPEND_THREADS, 0, &k, st);
 }
 
+// Rows of one key head that a sequence of n new tokens has.
+int rows_of(const cskv::AttnP& k, int n) {
+  const long long tokens = n < k.b.tokens ? n : k.b.tokens;
+  return static_cast<int>(tokens * k.b.group);
+}
+
 cs_status begin(cs_kv_s* p, const cs_kv_batch* b) {
   if (!p) return cs_fail(CS_ERR_INVALID_ARG, "plan is NULL");
   if (p->error_latched) return cs_fail(CS_ERR_NEEDS_RESET, "plan holds a device error; call cs_kv_reset");
@@ -339,7 +370,8 @@ cs_status cs_kv_plan(const cs_kv_desc* desc, cs_kv_t* out) {
   p->d = *desc;
   p->device = dev;
   p->num_sms = desc->num_sms > 0 && desc->num_sms < sms ? desc->num_sms : sms;
-  p->ctrl_words = cskv::CTRL_COUNTERS + 2 * static_cast<size_t>(p->num_sms);
+  const size_t counters = 2 * static_cast<size_t>(p->num_sms), rows_counters = rows_grid(p);
+  p->ctrl_words = cskv::CTRL_COUNTERS + (counters > rows_counters ? counters : rows_counters);
   int smem = 0;
   const void* fn = attn_kernel(p->d, &smem);
   if (cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess) {
@@ -347,7 +379,9 @@ cs_status cs_kv_plan(const cs_kv_desc* desc, cs_kv_t* out) {
     free_plan(p);
     return cs_fail(CS_ERR_CUDA, "the attention kernel needs %d bytes of shared memory", smem);
   }
+  // states of both kernels: the tensor-core kernel's are the larger
   const size_t part = static_cast<size_t>(p->num_sms) * 6 * (desc->head_dim / 4 + 1) * 128 * 16;
+  static_assert(cskv::ROWS_CTAS * 2 * cskv::ROWS * (64 + 2) * 4 <= 6 * (64 / 4 + 1) * 128 * 16, "workspace");
   const size_t flat = static_cast<size_t>(desc->max_tokens) * desc->heads * (desc->head_dim + 1) * 4;
   if (cudaMalloc(reinterpret_cast<void**>(&p->ctrl), p->ctrl_words * 4) != cudaSuccess ||
       cudaMalloc(reinterpret_cast<void**>(&p->part), part) != cudaSuccess ||
@@ -387,7 +421,8 @@ cs_status cs_kv_attention(cs_kv_t p, const cs_kv_batch* b, const cs_kv_attn_args
   if ((s = check_attn(p, b, a, k)) != CS_OK) return s;
   DeviceGuard g(p->device);
   if (!g.ok) return cs_fail(CS_ERR_CUDA, "cannot select the plan's device");
-  return run_attention(p, k, static_cast<cudaStream_t>(stream));
+  if (b->tokens == 0 || b->seqs == 0) return CS_OK;
+  return run_attention(p, k, rows_of(k, b->max_q), static_cast<cudaStream_t>(stream));
 }
 
 cs_status cs_kv_attention_shared(cs_kv_t p, const cs_kv_batch* b, const int32_t* prefix_pages, int prefix_len,
@@ -401,6 +436,7 @@ cs_status cs_kv_attention_shared(cs_kv_t p, const cs_kv_batch* b, const int32_t*
   if ((s = check_attn(p, b, a, k)) != CS_OK) return s;
   DeviceGuard g(p->device);
   if (!g.ok) return cs_fail(CS_ERR_CUDA, "cannot select the plan's device");
+  if (b->tokens == 0 || b->seqs == 0) return CS_OK;
   if (prefix_len > 0) {
     // all tokens of the batch over the prefix; then every sequence's own keys, which join it
     k.flat_o = p->flat_o;
@@ -408,10 +444,10 @@ cs_status cs_kv_attention_shared(cs_kv_t p, const cs_kv_batch* b, const int32_t*
     k.pages = prefix_pages;
     k.c.flat = 1;
     k.c.flat_len = prefix_len;
-    if ((s = run_attention(p, k, static_cast<cudaStream_t>(stream))) != CS_OK) return s;
+    if ((s = run_attention(p, k, rows_of(k, b->tokens), static_cast<cudaStream_t>(stream))) != CS_OK) return s;
     k.c.flat = 0;
   }
-  return run_attention(p, k, static_cast<cudaStream_t>(stream));
+  return run_attention(p, k, rows_of(k, b->max_q), static_cast<cudaStream_t>(stream));
 }
 
 cs_status cs_attn_cached_forward(cs_chain_t chain, cs_kv_t p, const cs_kv_batch* b, const cs_attn_args* args,

@@ -4,256 +4,19 @@
 // (token, query head) pairs that read that head: S = Q K^T, running row maximum
 // and sum, P = 2^(c S - max), O += P V, and O / sum at the end.
 //
-// Work.  An item is 2 x 128 such rows (whole tokens) of one sequence and key head; it
-// needs one or more tiles of 128 keys.  The tiles of all items, laid end to end, are
-// cut into one equal range per CTA (one CTA per SM): long and short sequences, one or
-// many, prompts and single tokens all load the SMs alike, without a launch per
-// kind.  Items cut by a range's border leave their state (O, max, sum) in the
-// workspace, and the last CTA to arrive joins the pieces in their order, so the
-// result does not depend on who is last.
+// Work.  An item is 2 x 128 such rows (whole tokens), its tiles have 128 keys; one CTA
+// per SM (cs_kv_sched.cuh).
 #pragma once
-#include "cs_kv_append.cuh"
+#include "cs_kv_sched.cuh"
 
 namespace cskv {
 
-// ---------------------------------------------------------------- which tiles
-struct Cut {
-  int per_tile;   // tokens of a 128-row tile: 128 / group, rounded down
-  int per_item;   // tokens of an item: two tiles
-  int window, sinks;
-  int item_cost;  // what starting and ending an item costs, in key tiles
-  int flat;       // every row sees keys 0 .. flat_len - 1 of one common table (a shared prefix)
-  int flat_len;
-};
+constexpr int KT = 128;  // keys per tile (Cut.shift 7)
 
-constexpr int KT = 128;  // keys per tile
-
-struct Seq {
-  int t0, n, m;
-};
-
-// Sequence b of the batch, or with `flat` all tokens of the batch over the prefix.
-__device__ __forceinline__ bool load_seq(const Batch& B, const Cut& C, int b, Seq& s) {
-  if (!C.flat) return sequence(B, b, s.t0, s.n, s.m);
-  s.t0 = __ldg(B.cu_q);
-  const int t1 = __ldg(B.cu_q + B.seqs);
-  s.n = t1 - s.t0;
-  s.m = C.flat_len;
-  if (s.t0 >= 0 && t1 >= s.t0 && t1 <= B.tokens) return true;
-  record(B.ctrl, ERR_INVALID, WHAT_LENGTHS, static_cast<uint32_t>(B.seqs - 1));
-  return false;
-}
-
-// First key of the window of the item's first token (0 without a window), and the
-// end of the keys that its last token sees.
-__device__ __forceinline__ int item_lo(const Cut& C, const Seq& s, int item) {
-  return C.window > 0 ? max(0, s.m - s.n + item * C.per_item - C.window + 1) : 0;
-}
-__device__ __forceinline__ int item_hi(const Cut& C, const Seq& s, int item) {
-  return C.flat ? s.m : max(0, s.m - s.n + min(s.n, (item + 1) * C.per_item));
-}
-// Tiles of the sinks before the window's first tile.
-__device__ __forceinline__ int sink_tiles(const Cut& C, int lo) { return min((C.sinks + KT - 1) / KT, lo / KT); }
-// Key tiles of an item; at least one, so that rows without keys are written too.
-__device__ __forceinline__ int item_tiles(const Cut& C, const Seq& s, int item) {
-  const int lo = item_lo(C, s, item), hi = item_hi(C, s, item);
-  return (max(1, hi) + KT - 1) / KT - lo / KT + sink_tiles(C, lo);
-}
-__device__ __forceinline__ int items_of(const Cut& C, const Seq& s) { return (s.n + C.per_item - 1) / C.per_item; }
-
-// sum over i < n of floor((a i + b) / m), a, b >= 0 (the Euclid-like recurrence for
-// lattice points under a line); m a + m fits 32 bits times n
-__device__ __forceinline__ unsigned long long floor_sum(unsigned n, unsigned m, unsigned a, unsigned b) {
-  unsigned long long ans = 0;
-#pragma unroll 1
-  while (n > 0) {
-    ans += static_cast<unsigned long long>(n) * (n - 1) / 2 * (a / m) + static_cast<unsigned long long>(n) * (b / m);
-    a %= m;
-    b %= m;
-    const unsigned y = a * n + b;  // below 128 (n + 1), n <= 2^20 tokens
-    n = y / m;
-    b = y % m;
-    const unsigned t = m;
-    m = a;
-    a = t;
-  }
-  return ans;
-}
-
-// Units of the first k items of a sequence (of one key head): their key tiles, and
-// item_cost for each.
-__device__ __forceinline__ unsigned long long units_before(const Cut& C, const Seq& s, int k) {
-  if (k == 0) return 0;
-  if (C.flat) return static_cast<unsigned long long>(k) * static_cast<unsigned>(item_tiles(C, s, 0) + C.item_cost);
-  const int full = min(k, items_of(C, s) - 1);  // the last item may hold fewer tokens
-  unsigned long long sum = static_cast<unsigned long long>(k) * C.item_cost;
-  if (k > full) sum += item_tiles(C, s, full);
-  if (full > 0) {
-    const int base = s.m - s.n, P = C.per_item;
-    // sum of ceil(max(1, base + (i + 1) P) / KT)
-    const int early = base < 0 ? min(full, -base / P) : 0;
-    sum += early + floor_sum(full - early, KT, P, base + (early + 1) * P + KT - 1);
-    if (C.window > 0) {
-      // minus what lies between the sinks' tiles and the window's first tile
-      const int b2 = base - C.window + 1 - (C.sinks + KT - 1) / KT * KT;
-      const int k2 = b2 >= 0 ? 0 : (-b2 + P - 1) / P;
-      if (full > k2) sum -= floor_sum(full - k2, KT, P, b2 + k2 * P);
-    }
-  }
-  return sum;
-}
-
-// A piece of work of one CTA: key tiles [k0, k1) of an item.
-struct Seg {
-  Seq s;
-  int b, kvh, item, k0, k1, tiles, lo, hi, sinks;  // sinks: its leading sink tiles
-  unsigned long long x;                            // the item's first tile in the order of all
-  __device__ __forceinline__ bool whole() const { return k0 == 0 && k1 == tiles; }
-  // first key of the k-th tile
-  __device__ __forceinline__ int key0(int k) const { return (k < sinks ? k : lo / KT + k - sinks) * KT; }
-};
-
-// Where a CTA's range of units begins and ends (CTA c takes units c * quota and
-// on); every warp role walks it by itself.
-struct Range {
-  unsigned long long x0, x1, rem, quota;
-  int b, kvh, item, off;
-};
-
-// An item's units are item_cost of overhead and then its tiles; a range that ends
-// in the overhead leaves all tiles to the next CTA.
-struct Walk {
-  unsigned long long x, x1;
-  int b, kvh, item, off, items;
-  Seq s;
-  __device__ __forceinline__ Walk(const Batch& B, const Cut& C, const Range& r)
-      : x(r.x0), x1(r.x1), b(r.b), kvh(r.kvh), item(r.item), off(r.off), items(0) {
-    if (x < x1 && load_seq(B, C, b, s)) items = items_of(C, s);
-  }
-  __device__ __forceinline__ bool next(const Batch& B, const Cut& C, Seg& g) {
-    while (x < x1) {
-      if (item == items) {
-        item = 0;
-        if (++kvh == B.kv_heads) {
-          kvh = 0;
-          const int seqs = C.flat ? 1 : B.seqs;
-          do {
-            if (++b >= seqs) return false;
-            items = load_seq(B, C, b, s) ? items_of(C, s) : 0;
-          } while (items == 0);
-        }
-      }
-      const int units = item_tiles(C, s, item) + C.item_cost;
-      const unsigned long long left = x1 - x;
-      const int to = static_cast<unsigned long long>(units - off) <= left ? units : off + static_cast<int>(left);
-      g.x = x - off + C.item_cost;
-      g.k0 = max(0, off - C.item_cost);
-      g.k1 = to - C.item_cost;
-      g.item = item;
-      x += to - off;
-      off = 0;
-      ++item;
-      if (g.k1 <= g.k0) continue;
-      g.s = s;
-      g.b = b;
-      g.kvh = kvh;
-      g.tiles = units - C.item_cost;
-      g.lo = item_lo(C, s, g.item);
-      g.hi = item_hi(C, s, g.item);
-      g.sinks = sink_tiles(C, g.lo);
-      return true;
-    }
-    return false;
-  }
-};
-
-// Every thread of the block: this CTA's range into *r (shared memory).
-template <int THREADS>
-__device__ __forceinline__ void find_range(const Batch& B, const Cut& C, Range* r, unsigned long long* scratch) {
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const int seqs = C.flat ? 1 : B.seqs;
-  const int per = (seqs + THREADS - 1) / THREADS;
-  const int b0 = min(tid * per, seqs);
-  int b1 = min(b0 + per, seqs);
-  unsigned long long at = 0, x0 = 0;
-  Seq s;
-  // first the units of all sequences, then, by the thread whose sequences hold unit
-  // x0, the one that holds it
-#pragma unroll 1
-  for (int pass = 0; pass < 2; ++pass) {
-    unsigned long long mine = 0;
-#pragma unroll 1
-    for (int b = b0; b < b1; ++b) {
-      if (!load_seq(B, C, b, s)) continue;
-      const unsigned long long c = units_before(C, s, items_of(C, s));
-      const unsigned long long in = x0 - at - mine * B.kv_heads;
-      if (pass == 1 && in < c * B.kv_heads) {
-        r->b = b;
-        r->kvh = static_cast<int>(in / c);
-        r->rem = in - r->kvh * c;
-        break;
-      }
-      mine += c;
-    }
-    if (pass == 1) break;
-    unsigned long long incl = mine;
-#pragma unroll
-    for (int d = 1; d < 32; d <<= 1) {
-      const unsigned long long o = __shfl_up_sync(0xFFFFFFFFu, incl, d);
-      if (lane >= d) incl += o;
-    }
-    if (lane == 31) scratch[warp] = incl;
-    __syncthreads();
-    unsigned long long before = 0, total = 0;
-#pragma unroll 1
-    for (int w = 0; w < THREADS / 32; ++w) {
-      if (w < warp) before += scratch[w];
-      total += scratch[w];
-    }
-    incl = (incl + before) * B.kv_heads;
-    total *= B.kv_heads;
-    const unsigned long long quota = (total + gridDim.x - 1) / gridDim.x;
-    x0 = min(quota * blockIdx.x, total);
-    const unsigned long long x1 = min(x0 + quota, total);
-    if (tid == 0) {
-      r->x0 = x0;
-      r->x1 = x1;
-      r->quota = quota;
-      r->b = r->kvh = r->item = r->off = 0;
-    }
-    __syncthreads();
-    at = incl - mine * B.kv_heads;
-    if (x0 >= x1 || x0 < at || x0 >= incl) b1 = b0;
-  }
-  __syncthreads();
-  if (warp == 0 && r->x0 < r->x1) {
-    // the item that holds unit `rem` of its sequence and head: 32 trials at a time
-    if (load_seq(B, C, r->b, s)) {
-      const unsigned long long rem = r->rem;
-      int a = 0, e = items_of(C, s);  // units_before(a) <= rem < units_before(e)
-      unsigned long long base = 0;    // units_before(a)
-      do {
-        const int step = (e - a + 31) / 32;
-        const int k = a + lane * step;
-        const unsigned long long u = k < e ? units_before(C, s, k) : ~0ull;
-        const int last = 31 - __clz(__ballot_sync(0xFFFFFFFFu, u <= rem));
-        base = __shfl_sync(0xFFFFFFFFu, u, last);
-        a += last * step;
-        e = min(e, a + step);
-      } while (e - a > 1);
-      __syncwarp();
-      if (lane == 0) {
-        r->item = a;
-        r->off = static_cast<int>(rem - base);
-      }
-    }
-  }
-  __syncthreads();
-}
-
-// ---------------------------------------------------------------- the kernel
 struct AttnP {
-  CUtensorMap q, k, v;
+  CUtensorMap q, k, v;    // for cs_kv_attn_kernel
+  const void *q_raw, *k_raw, *v_raw;  // for cs_kv_rows_kernel
+  long long q_stride;
   Batch b;
   Cut c;
   const int* pages;       // flat: the prefix's pages
@@ -265,6 +28,8 @@ struct AttnP {
   uint32_t* arrivals;     // [CTA][tile] pieces of the item that starts there and ends elsewhere
   float* flat_o;          // [tokens][heads][D], [tokens][heads]: a prefix's normalised output and
   float* flat_lse;        // base-2 log-sum-exp; written with c.flat, else joined in if not null
+  int per_tile;           // tokens of a 128-row tile: 128 / group, rounded down; an item has two
+  int out_wide;           // rows of out start on 32-byte boundaries
   int head_groups;        // 8-slot groups between heads (HEAD layout), 0: heads are a dimension of their own
 };
 
@@ -310,6 +75,7 @@ struct AttnCtl {
   uint32_t tmem;
   volatile int abort;
   volatile int last[2];
+  int turn;               // an MMA warp has the tensor core
   int loads, q_loads[2];  // tiles and queries whose copies were issued
 };
 
@@ -388,6 +154,14 @@ __device__ void come_to_rest(AttnCtl<SLOTS>* sc, const AttnP& p) {
   settle(&sc->drained, 0);
 }
 
+// The tensor core for a group of MMAs (given back by clearing sc->turn).
+template <typename Ctl>
+__device__ __forceinline__ void take_turn(Ctl* sc) {
+#pragma unroll 1
+  for (int i = 0; i < WAIT_TRIES && atomicCAS(&sc->turn, 0, 1) != 0 && !sc->abort; ++i) {
+  }
+}
+
 // A position in the ring: slot and the parity of its full barrier's current phase.
 template <int SLOTS>
 struct Ring {
@@ -413,15 +187,15 @@ __device__ bool load_role(const AttnP& p, AttnCtl<AttnShape<D>::SLOTS>* sc, uint
   uint32_t q_phase[2] = {1, 1};
   while (walk.next(B, p.c, g)) {
     const int* table = p.c.flat ? p.pages : B.table + static_cast<long long>(g.b) * B.table_cols;
-    const bool two = g.s.n - g.item * p.c.per_item > p.c.per_tile;
+    const bool two = g.s.n - g.item * p.c.per_item > p.per_tile;
     auto queries = [&](int w) {
       if (!wait_warp(&sc->q_empty[w], q_phase[w], sc)) return false;
       q_phase[w] ^= 1u;
       if (lane == 0) {
-        cs::mbar_arrive_expect_tx(&sc->q_full[w], static_cast<uint32_t>(p.c.per_tile) * B.group * D * 2);
+        cs::mbar_arrive_expect_tx(&sc->q_full[w], static_cast<uint32_t>(p.per_tile) * B.group * D * 2);
         for (int h = 0; h < Sh::HALVES; ++h)
           tma_3d(qbuf + w * Sh::TILE + h * (KT * 128), &p.q, h * 64, g.kvh * B.group,
-                 g.s.t0 + g.item * p.c.per_item + w * p.c.per_tile, &sc->q_full[w]);
+                 g.s.t0 + g.item * p.c.per_item + w * p.per_tile, &sc->q_full[w]);
         ++sc->q_loads[w];
       }
       return true;
@@ -430,7 +204,7 @@ __device__ bool load_role(const AttnP& p, AttnCtl<AttnShape<D>::SLOTS>* sc, uint
     // the page that this lane brings of tile k, -1: none of its keys is seen
     auto page_of = [&](int k) {
       if (k >= g.k1 || lane >= pages_per_tile) return -1;
-      const int j0 = g.key0(k) + (lane << B.page_shift), j1 = j0 + B.page_size;
+      const int j0 = g.key0(p.c, k) + (lane << B.page_shift), j1 = j0 + B.page_size;
       if (j0 >= g.hi || (j1 <= g.lo && j0 >= p.c.sinks)) return -1;
       const int page = __ldg(table + (j0 >> B.page_shift));
       if (page >= 0 && page < B.num_pages) return page;
@@ -491,7 +265,7 @@ __device__ bool mma_role(const AttnP& p, AttnCtl<AttnShape<D>::SLOTS>* sc, uint8
   uint32_t q_phase = 0, p_phase = 0;  // q_phase: bit per query buffer
   bool ok = true;
   while (ok && walk.next(p.b, p.c, g)) {
-    const bool two = g.s.n - g.item * p.c.per_item > p.c.per_tile;
+    const bool two = g.s.n - g.item * p.c.per_item > p.per_tile;
     const int qw = two ? w : 0, count = g.k1 - g.k0;
     ok = wait_warp(&sc->q_full[qw], (q_phase >> qw) & 1u, sc);
     if (!ok) break;
@@ -499,65 +273,75 @@ __device__ bool mma_role(const AttnP& p, AttnCtl<AttnShape<D>::SLOTS>* sc, uint8
     // both warps give the first queries back, warp 1 at once where it does not read them (the
     // wait above keeps it from doing so for an item before its queries are loaded)
     if (leader && w == 1 && (two || count == 1)) cs::mbar_arrive(&sc->q_empty[0]);
-    bool early = false;  // this tile's keys were seen before the last P V
-    int v_late = -1;     // slot of V that the last P V read, to be given back
+    // S of the tile whose keys lie in `slot`; the last one gives the queries back
+    auto scores = [&](int slot, bool last) {
+      uint64_t a = q_desc + qw * (Sh::TILE >> 4), b = k_desc + slot * (Sh::TILE >> 4);
 #pragma unroll 1
-    for (int t = 0; t < count; ++t) {
-      const bool use = two || (t & 1) == w;
-      if (!early) ok = wait_warp(&sc->full[r.slot], r.phase, sc);
-      if (!ok) break;
-      if (use) {
-        cs::tc_fence_after();
-        if (leader) {
-          uint64_t a = q_desc + qw * (Sh::TILE >> 4), b = k_desc + r.slot * (Sh::TILE >> 4);
-#pragma unroll 1
-          for (int h = 0; h < Sh::HALVES; ++h, a += KT * 128 >> 4, b += 1024 >> 4)
+      for (int h = 0; h < Sh::HALVES; ++h, a += KT * 128 >> 4, b += 1024 >> 4)
 #pragma unroll
-            for (int kk = 0; kk < 4; ++kk) cs::tc_mma_f16<1>(s_tm, a + kk * 2, b + kk * 2, idesc_s, h + kk);
-          cs::tc_commit<1>(&sc->s_full[w]);
-          cs::tc_commit<1>(&sc->empty[r.slot]);
-          if (v_late >= 0) cs::tc_commit<1>(&sc->empty[v_late]);
-          if (t + (two ? 1 : 2) >= count) cs::tc_commit<1>(&sc->q_empty[qw]);
+        for (int kk = 0; kk < 4; ++kk) cs::tc_mma_f16<1>(s_tm, a + kk * 2, b + kk * 2, idesc_s, h + kk);
+      cs::tc_commit<1>(&sc->s_full[w]);
+      cs::tc_commit<1>(&sc->empty[slot]);
+      if (last) cs::tc_commit<1>(&sc->q_empty[qw]);
+    };
+    // 64 keys' part of P V
+    auto values = [&](int slot, int h, bool add) {
+      const uint64_t b = v_desc + (slot * (Sh::TILE >> 4) + h * (Sh::HALVES * 8192 >> 4));
+#pragma unroll
+      for (int kk = 0; kk < 4; ++kk)
+        mma_ts(o_tm, s_tm + h * 32 + kk * 8, b + kk * (Sh::HALVES * 2048 >> 4), idesc_o, add || kk > 0);
+    };
+    bool issued = false;  // S of this tile was issued right behind the last P V
+#pragma unroll 1
+    for (int t = 0; ok && t < count; ++t) {
+      const int next = t + (two ? 1 : 2);  // this warp's next tile
+      if (!two && (t & 1) != w) {
+        for (int i = 0; ok && i < 2; ++i) {
+          ok = wait_warp(&sc->full[r.slot], r.phase, sc);
+          if (leader && ok) cs::mbar_arrive(&sc->empty[r.slot]);
+          r.next();
         }
-        v_late = -1;
-      } else if (leader) {
-        cs::mbar_arrive(&sc->empty[r.slot]);
-      }
-      early = false;
-      r.next();
-      ok = wait_warp(&sc->full[r.slot], r.phase, sc);
-      if (!ok) break;
-      if (!use) {
-        if (leader) cs::mbar_arrive(&sc->empty[r.slot]);
-        r.next();
         continue;
       }
-      if (leader) cs::mbar_arrive(&sc->v_ready[w]);
-      const int sv = r.slot;
-      r.next();
-      // with the next tile's keys there, its S is issued right behind this P V
-      early = two && t + 1 < count && __all_sync(0xFFFFFFFFu, cs::mbar_test_wait(&sc->full[r.slot], r.phase));
-      uint64_t b = v_desc + sv * (Sh::TILE >> 4);
-      uint32_t a = s_tm;
-      // the weights of the first 64 keys come before the rest
-#pragma unroll 1
-      for (int h = 0; h < 2; ++h, a += 32, b += Sh::HALVES * 8192 >> 4) {
-        ok = ok && wait_warp(&sc->p_full[w][h], p_phase, sc);
+      if (!issued) {
+        ok = wait_warp(&sc->full[r.slot], r.phase, sc);
         if (!ok) break;
         cs::tc_fence_after();
-        if (leader) {
-#pragma unroll
-          for (int kk = 0; kk < 4; ++kk)
-            mma_ts(o_tm, a + kk * 8, b + kk * (Sh::HALVES * 2048 >> 4), idesc_o, t >= (two ? 1 : 2) || h + kk > 0);
-        }
+        if (leader) scores(r.slot, next >= count);
+        r.next();
       }
+      ok = wait_warp(&sc->full[r.slot], r.phase, sc);
       if (!ok) break;
-      p_phase ^= 1u;
-      if (early)
-        v_late = sv;
-      else if (leader)
+      const int sv = r.slot;
+      r.next();
+      if (leader) cs::mbar_arrive(&sc->v_ready[w]);
+      // with the next tile's keys there, nothing comes between this P V and its S
+      issued = two && next < count && __all_sync(0xFFFFFFFFu, cs::mbar_test_wait(&sc->full[r.slot], r.phase));
+      const int sk = r.slot;
+      const bool add = t >= (two ? 1 : 2);
+      ok = wait_warp(&sc->p_full[w][0], p_phase, sc);  // the weights of the first 64 keys come before the rest
+      if (!ok) break;
+      cs::tc_fence_after();
+      if (leader) values(sv, 0, add);
+      ok = wait_warp(&sc->p_full[w][1], p_phase, sc);
+      if (!ok) break;
+      cs::tc_fence_after();
+      if (leader) {
+        // one buffer's twelve MMAs after the other's: issued side by side, both S would
+        // be done late, both softmaxes run at a time, and the tensor core wait for them
+        // (64 dimensions: an MMA of P V takes half the time and the softmax bounds the rest;
+        // taking turns cost 4 %)
+        if (D == 128 && issued) take_turn(sc);
+        values(sv, 1, true);
+        if (issued) {
+          scores(sk, next + 1 >= count);
+          if (D == 128) atomicExch(&sc->turn, 0);
+        }
         cs::tc_commit<1>(&sc->empty[sv]);
-      if (leader && t + (two ? 1 : 2) >= count) cs::tc_commit<1>(&sc->o_full[w]);
+        if (next >= count) cs::tc_commit<1>(&sc->o_full[w]);
+      }
+      p_phase ^= 1u;
+      if (issued) r.next();
     }
   }
   if (leader) cs::tc_commit<1>(&sc->drained);  // all MMAs of this warp are done
@@ -612,6 +396,12 @@ __device__ __forceinline__ void axpy(float (&x)[32], const float4* src, int stri
   }
 }
 
+__device__ __forceinline__ void st32(void* p, const uint32_t* v) {
+  asm volatile("st.global.v8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"l"(p), "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]),
+               "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7])
+               : "memory");
+}
+
 // The bits 0 .. n - 1 (none for n <= 0, all from 32 on).
 __device__ __forceinline__ uint32_t below(int n) { return n >= 32 ? 0xFFFFFFFFu : n <= 0 ? 0u : (1u << n) - 1u; }
 
@@ -642,31 +432,30 @@ __device__ bool softmax_role(const AttnP& p, AttnCtl<AttnShape<D>::SLOTS>* sc, u
     const int count = g.k1 - g.k0;
     const uint32_t ring0 = 2 * tiles_done;
     tiles_done += count;
-    const bool two = g.s.n - g.item * p.c.per_item > p.c.per_tile;
+    const bool two = g.s.n - g.item * p.c.per_item > p.per_tile;
     if (!two && w >= count) continue;  // one key tile of one row tile: buffer 0 alone
     const int tile = two ? w : 0;      // this buffer's row tile
-    const int first = g.item * p.c.per_item + tile * p.c.per_tile;  // its first token
+    const int first = g.item * p.c.per_item + tile * p.per_tile;  // its first token
     const int base = g.s.m - g.s.n;
     const int tok = first + row_tok;
-    const bool live = row_tok < p.c.per_tile && tok < g.s.n;
+    const bool live = row_tok < p.per_tile && tok < g.s.n;
     const int end = p.c.flat ? g.s.m : live ? base + tok + 1 : 0;  // keys [.., end) are seen
     const int lo = p.c.window > 0 ? max(0, base + tok + 1 - p.c.window) : 0;
     // keys below `some` and from `all_lo` on are seen by every live row
     const int some = p.c.flat ? g.s.m : base + first + 1;
-    const int all_lo = p.c.window > 0 ? max(0, base + first + p.c.per_tile - p.c.window) : 0;
+    const int all_lo = p.c.window > 0 ? max(0, base + first + p.per_tile - p.c.window) : 0;
     float m_ref = -INFINITY, l = 0.0f;
 #pragma unroll 1
     for (int k = g.k0 + (two ? 0 : w); k < g.k1; k += two ? 1 : 2) {
+      // what the tile needs, known before its scores are there
       const bool fresh = k - g.k0 < (two ? 1 : 2);  // O of this buffer holds nothing yet
-      const int j0 = g.key0(k);
+      const int j0 = g.key0(p.c, k);
+      const bool mask = !(j0 + KT <= some && (j0 >= all_lo || j0 + KT <= p.c.sinks));  // some key is hidden from some row
+      const bool unseen = j0 + KT > g.hi || (j0 < g.lo && j0 + KT > p.c.sinks);       // from every row of the item
       if (!wait_warp(&sc->s_full[w], s_phase, sc)) return false;
       s_phase ^= 1u;
       cs::tc_fence_after();
-      // The row is read twice, for its maximum and for its weights: in registers
-      // all along it would need all its 128 values' code in line, and with that the hot loops of
-      // the roles no longer fit the instruction caches next to each other.
-      float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
-      if (__builtin_expect(!(j0 + KT <= some && (j0 >= all_lo || j0 + KT <= p.c.sinks)), 0)) {
+      if (__builtin_expect(mask, 0)) {
 #pragma unroll 1
         for (int c = 0; c < 4; ++c) {  // hidden scores become -inf in place
           const int j1 = j0 + 32 * c;
@@ -682,18 +471,17 @@ __device__ bool softmax_role(const AttnP& p, AttnCtl<AttnShape<D>::SLOTS>* sc, u
         }
         cs::tc_wait_st();
       }
-      {
-        uint32_t v[4][32];
+      uint32_t v[4][32];
 #pragma unroll
-        for (int c = 0; c < 4; ++c) cs::tmem_ld32(s_tm + c * 32, v[c]);
-        cs::tc_wait_ld();
+      for (int c = 0; c < 4; ++c) cs::tmem_ld32(s_tm + c * 32, v[c]);
+      cs::tc_wait_ld();
+      float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
-        for (int c = 0; c < 4; ++c) {
-          cs::tc_wait_ld_regs(v[c]);
+      for (int c = 0; c < 4; ++c) {
+        cs::tc_wait_ld_regs(v[c]);
 #pragma unroll
-          for (int t = 0; t < 32; t += 2)
-            mx[(t >> 1) & 3] = max3(mx[(t >> 1) & 3], __uint_as_float(v[c][t]), __uint_as_float(v[c][t + 1]));
-        }
+        for (int t = 0; t < 32; t += 2)
+          mx[(t >> 1) & 3] = max3(mx[(t >> 1) & 3], __uint_as_float(v[c][t]), __uint_as_float(v[c][t + 1]));
       }
       const float m_tile = max3(fmaxf(mx[0], mx[1]), mx[2], mx[3]) * p.scale_log2;
       // the reference is raised only when a row's maximum exceeds it by more than
@@ -717,7 +505,7 @@ __device__ bool softmax_role(const AttnP& p, AttnCtl<AttnShape<D>::SLOTS>* sc, u
       m_ref = m_new;
       // values of keys that no row of the item sees may hold anything: zeros in
       // their place before this buffer's P V (the other buffer's warps write them as well)
-      if (__builtin_expect(j0 + KT > g.hi || (j0 < g.lo && j0 + KT > p.c.sinks), 0)) {
+      if (__builtin_expect(unseen, 0)) {
         const uint32_t slot = (ring0 + 2 * (k - g.k0) + 1) % Sh::SLOTS;
         if (!wait_warp(&sc->v_ready[w], s_phase ^ 1u, sc)) return false;
         const int j = j0 + r;
@@ -732,31 +520,25 @@ __device__ bool softmax_role(const AttnP& p, AttnCtl<AttnShape<D>::SLOTS>* sc, u
       const float sub = m_ref == -INFINITY ? 0.0f : -m_ref;
       const uint64_t sub2 = pack64(sub, sub);
       uint64_t ls[2] = {0, 0};
-#pragma unroll 1
-      for (int h = 0; h < 2; ++h) {  // 64 keys at a time: P V of the first half starts while the second is computed
-        uint32_t v[2][32];
-        cs::tmem_ld32(s_tm + h * 64, v[0]);
-        cs::tmem_ld32(s_tm + h * 64 + 32, v[1]);
-        cs::tc_wait_ld();
 #pragma unroll
-        for (int c = 0; c < 2; ++c) {
-          cs::tc_wait_ld_regs(v[c]);
-          uint32_t pk[16];
+      for (int c = 0; c < 4; ++c) {  // P V of the first 64 keys starts while the rest is computed
+        uint32_t pk[16];
 #pragma unroll
-          for (int t = 0; t < 32; t += 2) {
-            float x, y;
-            unpack64(fma2(pack64(__uint_as_float(v[c][t]), __uint_as_float(v[c][t + 1])), scale2, sub2), x, y);
-            x = cs::ex2_approx(x);
-            y = cs::ex2_approx(y);
-            pk[t >> 1] = Pair<T>::put(x, y);
-            ls[(t >> 1) & 1] = add2(ls[(t >> 1) & 1], pack64(x, y));
-          }
-          tmem_st16(s_tm + h * 32 + c * 16, pk);
+        for (int t = 0; t < 32; t += 2) {
+          float x, y;
+          unpack64(fma2(pack64(__uint_as_float(v[c][t]), __uint_as_float(v[c][t + 1])), scale2, sub2), x, y);
+          x = cs::ex2_approx(x);
+          y = cs::ex2_approx(y);
+          pk[t >> 1] = Pair<T>::put(x, y);
+          ls[(t >> 1) & 1] = add2(ls[(t >> 1) & 1], pack64(x, y));
         }
-        cs::tc_wait_st();
-        cs::tc_fence_before();
-        __syncwarp();
-        if (lane == 0) cs::mbar_arrive(&sc->p_full[w][h]);
+        tmem_st16(s_tm + c * 16, pk);
+        if (c & 1) {
+          cs::tc_wait_st();
+          cs::tc_fence_before();
+          __syncwarp();
+          if (lane == 0) cs::mbar_arrive(&sc->p_full[w][c >> 1]);
+        }
       }
       float l0, l1;
       unpack64(add2(ls[0], ls[1]), l0, l1);
@@ -895,10 +677,17 @@ __device__ bool softmax_role(const AttnP& p, AttnCtl<AttnShape<D>::SLOTS>* sc, u
         } else {
           uint4* dst = reinterpret_cast<uint4*>(static_cast<T*>(p.out) + (g.s.t0 + tok) * p.out_stride +
                                                 (g.kvh * B.group + row_head) * D + c * 32);
+          uint32_t y[16];
 #pragma unroll
-          for (int t = 0; t < 4; ++t)
-            dst[t] = make_uint4(Pair<T>::put(x[8 * t], x[8 * t + 1]), Pair<T>::put(x[8 * t + 2], x[8 * t + 3]),
-                                Pair<T>::put(x[8 * t + 4], x[8 * t + 5]), Pair<T>::put(x[8 * t + 6], x[8 * t + 7]));
+          for (int t = 0; t < 16; ++t) y[t] = Pair<T>::put(x[2 * t], x[2 * t + 1]);
+          if (p.out_wide) {
+            // a lane's row is another line than its neighbours': whole 32-byte sectors at least
+            st32(dst, y);
+            st32(dst + 2, y + 8);
+          } else {
+#pragma unroll
+            for (int t = 0; t < 4; ++t) dst[t] = make_uint4(y[4 * t], y[4 * t + 1], y[4 * t + 2], y[4 * t + 3]);
+          }
         }
       }
       __syncwarp();
@@ -951,7 +740,7 @@ __global__ void __launch_bounds__(ATTN_THREADS, 1) cs_kv_attn_kernel(const __gri
     cs::mbar_init(&sc->other_full, 128);
     cs::mbar_init(&sc->other_empty, 128);
     cs::mbar_init(&sc->drained, 2);
-    sc->abort = sc->loads = sc->q_loads[0] = sc->q_loads[1] = 0;
+    sc->abort = sc->turn = sc->loads = sc->q_loads[0] = sc->q_loads[1] = 0;
     cs::fence_mbar_init();
     cs::prefetch_tmap(&p.q);
     cs::prefetch_tmap(&p.k);

@@ -1,0 +1,329 @@
+// Attention over the paged cache for few rows per key head (single tokens, or a few):
+// at most 16 (token, query head) rows of a sequence read each key, so the keys' and
+// values' bytes bound it, and for short contexts the latency.
+//
+// An item is the rows of one sequence and key head, a tile 64 keys: 16 for each of a
+// CTA's four warps.  The operands go from global memory to registers as the
+// fragments of m16n8k16 MMAs: the order of the contracted dimensions is free as long
+// as both operands agree on it, so a lane reads 16 consecutive bytes (K: of the key that is its
+// column, V: of its four keys), and no shared memory, copy engine or barrier lies
+// on the way.  Each warp has its own running maximum and sum; the four are
+// joined in shared memory at the end, pieces of an item as in cs_kv_sched.cuh.
+#pragma once
+#include "cs_kv_attn.cuh"
+
+namespace cskv {
+
+constexpr int ROWS = 16;         // rows of an item
+constexpr int ROWS_THREADS = 128;
+constexpr int ROWS_CTAS = 3;     // per SM: 168 registers a thread, 12 warps with 8 KB in flight each
+constexpr int ROWS_MAX_GRID = 512;
+constexpr int ROWS_SHIFT = 6;    // keys of a tile
+
+__device__ __forceinline__ uint4 ld_stream(const void* p) {
+  uint4 v;
+  asm volatile("ld.global.nc.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];"
+               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+               : "l"(p));
+  return v;
+}
+
+template <typename T>
+__device__ __forceinline__ void mma16816(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
+                                         uint32_t b1) {
+  if constexpr (std::is_same<T, __half>::value)
+    asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+                 : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+                 : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+  else
+    asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+                 : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+                 : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+
+template <int D>
+struct RowsShared {
+  Range range;
+  unsigned long long scratch[ROWS_THREADS / 32];
+  int last;
+  float2 ml[4][ROWS];      // each warp's maximum and sum of a row
+  float top[ROWS_THREADS];
+  uint4 q[ROWS][D / 8 + 1];
+  union {
+    float o[4][ROWS][D + 4];                 // each warp's output
+    float weight[ROWS_MAX_GRID][ROWS];       // of the pieces of an item
+  };
+};
+
+template <typename T, int D>
+__global__ void __launch_bounds__(ROWS_THREADS, ROWS_CTAS) cs_kv_rows_kernel(const __grid_constant__ AttnP p) {
+  __shared__ RowsShared<D> sm;
+  cs::grid_dep_wait();
+  cs::grid_dep_launch_dependents();
+  const Batch& B = p.b;
+  find_range<ROWS_THREADS>(B, p.c, &sm.range, sm.scratch);
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, gq = lane >> 2, jq = lane & 3;
+  constexpr int KB = D / 32, VB = D / 64;  // 16-byte pieces of a key per lane, of each of its values
+  const T* kc = static_cast<const T*>(p.k_raw);
+  const T* vc = static_cast<const T*>(p.v_raw);
+  Walk walk(B, p.c, sm.range);
+  Seg g;
+  while (walk.next(B, p.c, g)) {
+    const int first = g.item * p.c.per_item;  // the item's first token
+    const int rows = min(p.c.per_item, g.s.n - first) * B.group;
+    const int* table = p.c.flat ? p.pages : B.table + static_cast<long long>(g.b) * B.table_cols;
+    __syncthreads();  // shared memory of the segment before is read
+    for (int i = tid; i < ROWS * (D / 8); i += ROWS_THREADS) {
+      const int r = i / (D / 8), c = i % (D / 8);
+      uint4 v = make_uint4(0, 0, 0, 0);
+      if (r < rows) {
+        const int t = r / B.group;
+        v = *(reinterpret_cast<const uint4*>(static_cast<const T*>(p.q_raw) + (g.s.t0 + first + t) * p.q_stride +
+                                             (g.kvh * B.group + r - t * B.group) * D) + c);
+      }
+      sm.q[r][c] = v;
+    }
+    // keys [.., end) and from lo on, or below the sinks, are seen by rows gq and gq + 8
+    int end[2], lo[2];
+#pragma unroll
+    for (int x = 0; x < 2; ++x) {
+      const int r = gq + 8 * x, pos = g.s.m - g.s.n + first + r / B.group;
+      end[x] = r >= rows ? 0 : p.c.flat ? g.s.m : pos + 1;
+      lo[x] = p.c.window > 0 ? max(0, pos + 1 - p.c.window) : 0;
+    }
+    auto seen = [&](int key) { return key < g.hi && (key >= g.lo || key < p.c.sinks); };  // by some row
+    // this warp's page of tile k, -1 if none of its keys is seen
+    auto page_of = [&](int k) {
+      if (k >= g.k1) return -1;
+      const int j0 = g.key0(p.c, k) + warp * 16;
+      if (j0 >= g.hi || (j0 + 16 <= g.lo && j0 >= p.c.sinks)) return -1;
+      const int page = __ldg(table + (j0 >> B.page_shift));
+      if (page >= 0 && page < B.num_pages) return page;
+      record(B.ctrl, ERR_INVALID, WHAT_PAGE, p.c.flat ? 0xFFFFFFFFu : static_cast<uint32_t>(g.b));
+      return -1;
+    };
+    uint4 kr[2][KB], vr[4][VB];
+    auto load_k = [&](int k, int page) {
+      const int j0 = g.key0(p.c, k) + warp * 16;
+      const T* at = kc + page * B.page_stride + (j0 & (B.page_size - 1)) * B.slot_stride + g.kvh * B.head_stride + 8 * jq;
+#pragma unroll
+      for (int b = 0; b < 2; ++b) {
+        const bool in = page >= 0 && seen(j0 + 8 * b + gq);
+#pragma unroll
+        for (int i = 0; i < KB; ++i)
+          kr[b][i] = in ? ld_stream(at + (8 * b + gq) * B.slot_stride + 32 * i) : make_uint4(0, 0, 0, 0);
+      }
+    };
+    auto load_v = [&](int k, int page) {
+      const int j0 = g.key0(p.c, k) + warp * 16;
+      const T* at = vc + page * B.page_stride + (j0 & (B.page_size - 1)) * B.slot_stride + g.kvh * B.head_stride + 8 * gq;
+#pragma unroll
+      for (int b = 0; b < 4; ++b) {
+        const int j = 2 * jq + (b & 1) + 8 * (b >> 1);
+        const bool in = page >= 0 && seen(j0 + j);
+#pragma unroll
+        for (int h = 0; h < VB; ++h) vr[b][h] = in ? ld_stream(at + j * B.slot_stride + 64 * h) : make_uint4(0, 0, 0, 0);
+      }
+    };
+    int page = page_of(g.k0);
+    load_k(g.k0, page);
+    load_v(g.k0, page);
+    float o[VB][8][4];
+#pragma unroll
+    for (int h = 0; h < VB; ++h)
+#pragma unroll
+      for (int i = 0; i < 8; ++i)
+#pragma unroll
+        for (int c = 0; c < 4; ++c) o[h][i][c] = 0.0f;
+    float m_ref[2] = {-INFINITY, -INFINITY}, l[2] = {0.0f, 0.0f};
+    __syncthreads();  // the queries are there
+#pragma unroll 1
+    for (int k = g.k0; k < g.k1; ++k) {
+      const int j0 = g.key0(p.c, k) + warp * 16;
+      const int next = page_of(k + 1);
+      float s[2][4] = {};
+#pragma unroll
+      for (int i = 0; i < KB; ++i) {
+        const uint4 qa = sm.q[gq][4 * i + jq], qb = sm.q[gq + 8][4 * i + jq];
+#pragma unroll
+        for (int b = 0; b < 2; ++b) {
+          mma16816<T>(s[b], qa.x, qb.x, qa.y, qb.y, kr[b][i].x, kr[b][i].y);
+          mma16816<T>(s[b], qa.z, qb.z, qa.w, qb.w, kr[b][i].z, kr[b][i].w);
+        }
+      }
+      if (k + 1 < g.k1) load_k(k + 1, next);
+      bool raise = false;
+      float f[2];
+#pragma unroll
+      for (int x = 0; x < 2; ++x) {
+        float mx = -INFINITY;
+#pragma unroll
+        for (int b = 0; b < 2; ++b)
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            const int key = j0 + 8 * b + 2 * jq + e;
+            float& y = s[b][2 * x + e];
+            y = key < end[x] && (key >= lo[x] || key < p.c.sinks) ? y * p.scale_log2 : -INFINITY;
+            mx = fmaxf(mx, y);
+          }
+        mx = fmaxf(mx, __shfl_xor_sync(0xFFFFFFFFu, mx, 1));
+        mx = fmaxf(mx, __shfl_xor_sync(0xFFFFFFFFu, mx, 2));
+        // the reference is raised only when it is exceeded by more than 2^8
+        const bool up = mx > m_ref[x] + RAISE_LOG2 || (m_ref[x] == -INFINITY && mx > -INFINITY);
+        f[x] = up ? cs::ex2_approx(m_ref[x] - mx) : 1.0f;
+        if (up) m_ref[x] = mx;
+        raise |= up;
+      }
+      if (__any_sync(0xFFFFFFFFu, raise)) {
+#pragma unroll
+        for (int h = 0; h < VB; ++h)
+#pragma unroll
+          for (int i = 0; i < 8; ++i)
+#pragma unroll
+            for (int c = 0; c < 4; ++c) o[h][i][c] *= f[c >> 1];
+        l[0] *= f[0];
+        l[1] *= f[1];
+      }
+#pragma unroll
+      for (int x = 0; x < 2; ++x) {
+        const float sub = m_ref[x] == -INFINITY ? 0.0f : m_ref[x];
+#pragma unroll
+        for (int b = 0; b < 2; ++b)
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            s[b][2 * x + e] = cs::ex2_approx(s[b][2 * x + e] - sub);
+            l[x] += s[b][2 * x + e];
+          }
+      }
+      const uint32_t a0 = Pair<T>::put(s[0][0], s[0][1]), a1 = Pair<T>::put(s[0][2], s[0][3]);
+      const uint32_t a2 = Pair<T>::put(s[1][0], s[1][1]), a3 = Pair<T>::put(s[1][2], s[1][3]);
+#pragma unroll
+      for (int h = 0; h < VB; ++h) {
+        const uint32_t* v0 = reinterpret_cast<const uint32_t*>(&vr[0][h]);
+        const uint32_t* v1 = reinterpret_cast<const uint32_t*>(&vr[1][h]);
+        const uint32_t* v2 = reinterpret_cast<const uint32_t*>(&vr[2][h]);
+        const uint32_t* v3 = reinterpret_cast<const uint32_t*>(&vr[3][h]);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {  // column n of this MMA is dimension 8 n + i of the half
+          const uint32_t pick = i & 1 ? 0x7632u : 0x5410u;
+          mma16816<T>(o[h][i], a0, a1, a2, a3, __byte_perm(v0[i >> 1], v1[i >> 1], pick),
+                      __byte_perm(v2[i >> 1], v3[i >> 1], pick));
+        }
+      }
+      if (k + 1 < g.k1) load_v(k + 1, next);
+    }
+    // the four warps' states to shared memory
+#pragma unroll
+    for (int x = 0; x < 2; ++x) {
+      l[x] += __shfl_xor_sync(0xFFFFFFFFu, l[x], 1);
+      l[x] += __shfl_xor_sync(0xFFFFFFFFu, l[x], 2);
+      const int r = gq + 8 * x;
+      if (r < rows) {
+        if (jq == 0) sm.ml[warp][r] = make_float2(m_ref[x], l[x]);
+#pragma unroll
+        for (int h = 0; h < VB; ++h)
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            float4* to = reinterpret_cast<float4*>(&sm.o[warp][r][8 * (2 * jq + e + 8 * h)]);
+            to[0] = make_float4(o[h][0][2 * x + e], o[h][1][2 * x + e], o[h][2][2 * x + e], o[h][3][2 * x + e]);
+            to[1] = make_float4(o[h][4][2 * x + e], o[h][5][2 * x + e], o[h][6][2 * x + e], o[h][7][2 * x + e]);
+          }
+      }
+    }
+    __syncthreads();
+    const int d = tid % D;
+    auto state = [&](unsigned cta, int which, int r) { return p.part + ((static_cast<size_t>(cta) * 2 + which) * ROWS + r) * (D + 2); };
+    // dimension d of row r from its state
+    auto finish = [&](int r, float x, float m, float l) {
+      const int t = r / B.group;
+      const long long row = static_cast<long long>(g.s.t0 + first + t) * B.heads + g.kvh * B.group + r - t * B.group;
+      if (!p.c.flat && p.flat_o) {  // join the prefix's output
+        const float z = p.flat_lse[row], top = fmaxf(m, z);
+        const float own = m == -INFINITY ? 0.0f : cs::ex2_approx(m - top), fold = z == -INFINITY ? 0.0f : cs::ex2_approx(z - top);
+        x = x * own + p.flat_o[row * D + d] * fold;
+        l = l * own + fold;
+        m = top;
+      }
+      const float y = l == 0.0f ? 0.0f : x / l;
+      const float lse2 = l == 0.0f ? -INFINITY : m + log2f(l);
+      if (p.c.flat) {
+        p.flat_o[row * D + d] = y;
+        if (d == 0) p.flat_lse[row] = lse2;
+      } else {
+        T* out = static_cast<T*>(p.out) + (g.s.t0 + first + t) * p.out_stride + (g.kvh * B.group + r - t * B.group) * D;
+        if constexpr (std::is_same<T, __half>::value)
+          out[d] = __float2half(y);
+        else
+          out[d] = __float2bfloat16(y);
+        if (d == 0 && p.lse) p.lse[row] = lse2 * 0.6931471805599453f;
+      }
+    };
+    const bool whole = g.whole();
+    for (int r = tid / D; r < rows; r += ROWS_THREADS / D) {
+      float m = -INFINITY, sum = 0.0f, x = 0.0f;
+#pragma unroll
+      for (int w = 0; w < 4; ++w) m = fmaxf(m, sm.ml[w][r].x);
+#pragma unroll
+      for (int w = 0; w < 4; ++w) {
+        const float2 ml = sm.ml[w][r];
+        const float f = ml.x == -INFINITY ? 0.0f : cs::ex2_approx(ml.x - m);
+        sum = fmaf(ml.y, f, sum);
+        x = fmaf(sm.o[w][r][d], f, x);
+      }
+      if (whole) {
+        finish(r, x, m, sum);
+      } else {
+        float* to = state(blockIdx.x, sm.range.x0 < g.x, r);
+        to[d] = x;
+        if (d == 0) *reinterpret_cast<float2*>(to + D) = make_float2(m, sum);
+      }
+    }
+    if (whole) continue;
+    const unsigned me = blockIdx.x, quota = static_cast<unsigned>(min(sm.range.quota, 0x80000000ull));
+    const unsigned long long end_x = g.x + g.tiles - 1;
+    const unsigned c0 = sm.range.x0 > g.x ? me - (static_cast<unsigned>(sm.range.x0 - g.x) + quota - 1) / quota : me;
+    const unsigned c1 = end_x >= sm.range.x1 ? me + static_cast<unsigned>(end_x - sm.range.x1) / quota + 1 : me;
+    __syncthreads();  // all stores come before the one arrival at gpu scope
+    if (tid == 0) {
+      uint32_t* ctr = p.arrivals + c0;
+      const uint32_t old = cs::atom_add_acq_rel_gpu(ctr, 1u);
+      sm.last = old == c1 - c0;
+      if (old == c1 - c0) *ctr = 0u;  // for the next call
+    }
+    __syncthreads();
+    if (!sm.last) continue;
+    // the last to arrive joins the pieces in their order
+    const int pieces = static_cast<int>(c1 - c0) + 1;
+    auto piece = [&](int i, int r) { return state(c0 + i, sm.range.quota * (c0 + i) < g.x, r); };
+    const int wr = tid % ROWS;  // a row for the weights
+    float m = -INFINITY;
+    if (wr < rows)
+#pragma unroll 4
+      for (int i = tid / ROWS; i < pieces; i += ROWS_THREADS / ROWS) m = fmaxf(m, __ldcg(piece(i, wr) + D));
+    sm.top[tid] = m;
+    __syncthreads();
+#pragma unroll
+    for (int i = 0; i < ROWS_THREADS / ROWS; ++i) m = fmaxf(m, sm.top[i * ROWS + wr]);
+    if (wr < rows)
+      for (int i = tid / ROWS; i < pieces; i += ROWS_THREADS / ROWS) {
+        const float x = __ldcg(piece(i, wr) + D);
+        sm.weight[i][wr] = x == -INFINITY ? 0.0f : cs::ex2_approx(x - m);
+      }
+    __syncthreads();
+    if (tid < ROWS) sm.top[tid] = m;
+    __syncthreads();
+    for (int r = tid / D; r < rows; r += ROWS_THREADS / D) {
+      float x = 0.0f, sum = 0.0f;
+#pragma unroll 8
+      for (int i = 0; i < pieces; ++i) {
+        const float* from = piece(i, r);
+        const float f = sm.weight[i][r];
+        x = fmaf(__ldcg(from + d), f, x);
+        sum = fmaf(__ldcg(from + D + 1), f, sum);
+      }
+      finish(r, x, sm.top[r], sum);
+    }
+  }
+}
+
+}  // namespace cskv
