@@ -182,8 +182,8 @@ cs_status encode(CUtensorMap* map, int bf16, const void* ptr, int rank, const cu
 }
 
 // A cache as [8-slot group][head][64-dimension half][slot of the group][64]: one box is
-// a page's slots of a head.  In the HEAD layout heads are part of the groups' order.
-cs_status encode_cache(const cs_kv_s* p, const cskv::Batch& B, CUtensorMap* map, const void* ptr, const char* name) {
+// some slots of a page, of one head.  In the HEAD layout heads are part of the groups' order.
+cs_status encode_cache(const cs_kv_s* p, const cskv::Batch& B, CUtensorMap* map, const void* ptr, int slots, const char* name) {
   const cs_kv_desc& d = p->d;
   const bool head = d.cache_layout == CS_KV_HEAD;
   const cuuint64_t groups = static_cast<cuuint64_t>(d.num_pages) * (d.page_size / 8);
@@ -191,7 +191,7 @@ cs_status encode_cache(const cs_kv_s* p, const cskv::Batch& B, CUtensorMap* map,
                               head ? groups * d.kv_heads : groups};
   const cuuint64_t slot = static_cast<cuuint64_t>(B.slot_stride) * 2;
   const cuuint64_t strides[4] = {slot, 128, static_cast<cuuint64_t>(B.head_stride) * 2, 8 * slot};
-  const cuuint32_t box[5] = {64, 8, static_cast<cuuint32_t>(d.head_dim / 64), 1, static_cast<cuuint32_t>(d.page_size / 8)};
+  const cuuint32_t box[5] = {64, 8, static_cast<cuuint32_t>(d.head_dim / 64), 1, static_cast<cuuint32_t>(slots / 8)};
   return encode(map, d.dtype == CS_BF16, ptr, 5, dims, strides, box, name);
 }
 
@@ -228,6 +228,17 @@ cs_status check_attn(const cs_kv_s* p, const cs_kv_batch* b, const cs_kv_attn_ar
   return CS_OK;
 }
 
+const void* rows_kernel(const cs_kv_desc& d) {
+  if (d.dtype == CS_BF16)
+    return d.head_dim == 128 ? (const void*)cskv::cs_kv_rows_kernel<__nv_bfloat16, 128>
+                             : (const void*)cskv::cs_kv_rows_kernel<__nv_bfloat16, 64>;
+  return d.head_dim == 128 ? (const void*)cskv::cs_kv_rows_kernel<__half, 128> : (const void*)cskv::cs_kv_rows_kernel<__half, 64>;
+}
+
+int rows_smem(const cs_kv_desc& d) {
+  return d.head_dim == 128 ? sizeof(cskv::RowsShared<128>) + 1024 : sizeof(cskv::RowsShared<64>) + 1024;
+}
+
 int rows_grid(const cs_kv_s* p) {
   const int n = p->num_sms * cskv::ROWS_CTAS;
   return n < cskv::ROWS_MAX_GRID ? n : cskv::ROWS_MAX_GRID;
@@ -246,26 +257,26 @@ const void* attn_kernel(const cs_kv_desc& d, int* smem) {
 // tensor-core kernel.
 cs_status run_attention(cs_kv_s* p, cskv::AttnP& k, int max_rows, cudaStream_t st) {
   const cs_kv_desc& d = p->d;
-  const bool bf16 = d.dtype == CS_BF16, wide = d.head_dim == 128;
+  const bool bf16 = d.dtype == CS_BF16;
+  k.head_groups = d.cache_layout == CS_KV_HEAD ? d.page_size / 8 : 0;
+  cs_status s;
   if (max_rows <= cskv::ROWS) {
     k.c.per_item = cskv::ROWS / k.b.group;
     k.c.shift = cskv::ROWS_SHIFT;
-    const void* fn = bf16 ? (wide ? (const void*)cskv::cs_kv_rows_kernel<__nv_bfloat16, 128>
-                                  : (const void*)cskv::cs_kv_rows_kernel<__nv_bfloat16, 64>)
-                          : (wide ? (const void*)cskv::cs_kv_rows_kernel<__half, 128> : (const void*)cskv::cs_kv_rows_kernel<__half, 64>);
-    return launch(fn, dim3(rows_grid(p)), cskv::ROWS_THREADS, 0, &k, st);
+    if ((s = encode_cache(p, k.b, &k.k, k.k_raw, 16, "k_cache")) != CS_OK) return s;
+    if ((s = encode_cache(p, k.b, &k.v, k.v_raw, 16, "v_cache")) != CS_OK) return s;
+    return launch(rows_kernel(d), dim3(rows_grid(p)), cskv::ROWS_THREADS, rows_smem(d), &k, st);
   }
   k.per_tile = 128 / k.b.group;
   k.c.per_item = 2 * k.per_tile;
   k.c.shift = 7;
-  k.head_groups = d.cache_layout == CS_KV_HEAD ? d.page_size / 8 : 0;
   const cuuint64_t dims[3] = {static_cast<cuuint64_t>(d.head_dim), static_cast<cuuint64_t>(d.heads),
                               static_cast<cuuint64_t>(k.b.tokens)};
   const cuuint64_t strides[2] = {static_cast<cuuint64_t>(d.head_dim) * 2, static_cast<cuuint64_t>(k.q_stride) * 2};
   const cuuint32_t box[3] = {64, static_cast<cuuint32_t>(k.b.group), static_cast<cuuint32_t>(k.per_tile)};
-  cs_status s = encode(&k.q, bf16, k.q_raw, 3, dims, strides, box, "q");
-  if (s == CS_OK) s = encode_cache(p, k.b, &k.k, k.k_raw, "k_cache");
-  if (s == CS_OK) s = encode_cache(p, k.b, &k.v, k.v_raw, "v_cache");
+  s = encode(&k.q, bf16, k.q_raw, 3, dims, strides, box, "q");
+  if (s == CS_OK) s = encode_cache(p, k.b, &k.k, k.k_raw, d.page_size, "k_cache");
+  if (s == CS_OK) s = encode_cache(p, k.b, &k.v, k.v_raw, d.page_size, "v_cache");
   if (s != CS_OK) return s;
   int smem = 0;
   const void* fn = attn_kernel(d, &smem);
@@ -374,10 +385,11 @@ cs_status cs_kv_plan(const cs_kv_desc* desc, cs_kv_t* out) {
   p->ctrl_words = cskv::CTRL_COUNTERS + (counters > rows_counters ? counters : rows_counters);
   int smem = 0;
   const void* fn = attn_kernel(p->d, &smem);
-  if (cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess) {
+  if (cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess ||
+      cudaFuncSetAttribute(rows_kernel(p->d), cudaFuncAttributeMaxDynamicSharedMemorySize, rows_smem(p->d)) != cudaSuccess) {
     cudaGetLastError();
     free_plan(p);
-    return cs_fail(CS_ERR_CUDA, "the attention kernel needs %d bytes of shared memory", smem);
+    return cs_fail(CS_ERR_CUDA, "the attention kernels need %d bytes of shared memory", smem);
   }
   // states of both kernels: the tensor-core kernel's are the larger
   const size_t part = static_cast<size_t>(p->num_sms) * 6 * (desc->head_dim / 4 + 1) * 128 * 16;

@@ -3,30 +3,24 @@
 // values' bytes bound it, and for short contexts the latency.
 //
 // An item is the rows of one sequence and key head, a tile 64 keys: 16 for each of a
-// CTA's four warps.  The operands go from global memory to registers as the
-// fragments of m16n8k16 MMAs: the order of the contracted dimensions is free as long
-// as both operands agree on it, so a lane reads 16 consecutive bytes (K: of the key that is its
-// column, V: of its four keys), and no shared memory, copy engine or barrier lies
-// on the way.  Each warp has its own running maximum and sum; the four are
-// joined in shared memory at the end, pieces of an item as in cs_kv_sched.cuh.
+// CTA's four warps, which has them copied (one TMA box for K, one for V) for itself, so that no
+// barrier of the CTA lies on the way.  The order of the contracted dimensions of a product is
+// free as long as both operands agree on it, so each lane's part of the m16n8k16
+// fragments is 16 consecutive bytes: of K, of the key that is its column; of V, of
+// its four keys.  Each warp has its own running maximum and sum; the four are joined
+// in shared memory at the end, pieces of an item as in cs_kv_sched.cuh.
 #pragma once
+#include <climits>
+
 #include "cs_kv_attn.cuh"
 
 namespace cskv {
 
 constexpr int ROWS = 16;         // rows of an item
 constexpr int ROWS_THREADS = 128;
-constexpr int ROWS_CTAS = 3;     // per SM: 168 registers a thread, 12 warps with 8 KB in flight each
+constexpr int ROWS_CTAS = 3;     // per SM: 12 warps with up to 16 KB in flight each
 constexpr int ROWS_MAX_GRID = 512;
 constexpr int ROWS_SHIFT = 6;    // keys of a tile
-
-__device__ __forceinline__ uint4 ld_stream(const void* p) {
-  uint4 v;
-  asm volatile("ld.global.nc.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];"
-               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
-               : "l"(p));
-  return v;
-}
 
 template <typename T>
 __device__ __forceinline__ void mma16816(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
@@ -42,46 +36,73 @@ __device__ __forceinline__ void mma16816(float (&c)[4], uint32_t a0, uint32_t a1
 }
 
 template <int D>
-struct RowsShared {
-  Range range;
-  unsigned long long scratch[ROWS_THREADS / 32];
-  int last;
-  float2 ml[4][ROWS];      // each warp's maximum and sum of a row
-  float top[ROWS_THREADS];
-  uint4 q[ROWS][D / 8 + 1];
+struct alignas(1024) RowsShared {
+  static constexpr int STAGES = D == 128 ? 2 : 4;  // tiles on their way
   union {
+    // [warp][stage][K, V][8-key group][64-dimension half][key][16-byte piece, at its index ^ key]
+    uint4 kv[4][STAGES][2][2][D / 64][8][8];
     float o[4][ROWS][D + 4];                 // each warp's output
     float weight[ROWS_MAX_GRID][ROWS];       // of the pieces of an item
   };
+  Range range;
+  unsigned long long scratch[ROWS_THREADS / 32];
+  int last, failed;
+  uint64_t full[4][STAGES][2];  // [warp][stage][K, V]
+  float2 ml[4][ROWS];           // each warp's maximum and sum of a row
+  float top[ROWS_THREADS];
+  uint4 q[ROWS][D / 8 + 1];
 };
 
 template <typename T, int D>
 __global__ void __launch_bounds__(ROWS_THREADS, ROWS_CTAS) cs_kv_rows_kernel(const __grid_constant__ AttnP p) {
-  __shared__ RowsShared<D> sm;
+  extern __shared__ __align__(1024) uint8_t rows_smem[];
+  RowsShared<D>& sm =
+      *reinterpret_cast<RowsShared<D>*>((reinterpret_cast<uintptr_t>(rows_smem) + 1023) & ~uintptr_t(1023));
+  constexpr int ST = RowsShared<D>::STAGES;
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < 4 * ST * 2; ++i) cs::mbar_init(&sm.full[0][0][0] + i, 1);
+    sm.failed = 0;
+    cs::fence_mbar_init();
+    cs::prefetch_tmap(&p.k);
+    cs::prefetch_tmap(&p.v);
+  }
   cs::grid_dep_wait();
   cs::grid_dep_launch_dependents();
   const Batch& B = p.b;
   find_range<ROWS_THREADS>(B, p.c, &sm.range, sm.scratch);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, gq = lane >> 2, jq = lane & 3;
-  constexpr int KB = D / 32, VB = D / 64;  // 16-byte pieces of a key per lane, of each of its values
-  const T* kc = static_cast<const T*>(p.k_raw);
-  const T* vc = static_cast<const T*>(p.v_raw);
+  constexpr int KB = D / 32, VB = D / 64;  // 16-byte pieces of a key per lane, of each of its four values
+  uint32_t done = 0;  // tiles that this warp has read
+  // a copy of this warp; one that never comes (an error: the results mean nothing) is waited
+  // for with a limit, once
+  auto arrived = [&](int which, uint32_t n) {
+    uint64_t* bar = &sm.full[warp][n % ST][which];
+#pragma unroll 1
+    for (int i = 0; !cs::mbar_try_wait(bar, n / ST & 1u); ++i)
+      if (i >= WAIT_TRIES) {
+        if (atomicExch(&sm.failed, 1) == 0) record(B.ctrl, ERR_WATCHDOG, WHAT_WAIT, blockIdx.x);
+        break;
+      }
+  };
   Walk walk(B, p.c, sm.range);
   Seg g;
   while (walk.next(B, p.c, g)) {
     const int first = g.item * p.c.per_item;  // the item's first token
     const int rows = min(p.c.per_item, g.s.n - first) * B.group;
     const int* table = p.c.flat ? p.pages : B.table + static_cast<long long>(g.b) * B.table_cols;
+    cs::fence_proxy_async_shared();
     __syncthreads();  // shared memory of the segment before is read
-    for (int i = tid; i < ROWS * (D / 8); i += ROWS_THREADS) {
-      const int r = i / (D / 8), c = i % (D / 8);
-      uint4 v = make_uint4(0, 0, 0, 0);
+    constexpr int QN = ROWS * (D / 8) / ROWS_THREADS;  // 16-byte pieces of the queries per thread
+    uint4 qv[QN];
+#pragma unroll
+    for (int i = 0; i < QN; ++i) {
+      const int x = tid + i * ROWS_THREADS, r = x / (D / 8), c = x % (D / 8);
+      qv[i] = make_uint4(0, 0, 0, 0);
       if (r < rows) {
         const int t = r / B.group;
-        v = *(reinterpret_cast<const uint4*>(static_cast<const T*>(p.q_raw) + (g.s.t0 + first + t) * p.q_stride +
-                                             (g.kvh * B.group + r - t * B.group) * D) + c);
+        qv[i] = *(reinterpret_cast<const uint4*>(static_cast<const T*>(p.q_raw) + (g.s.t0 + first + t) * p.q_stride +
+                                                 (g.kvh * B.group + r - t * B.group) * D) + c);
       }
-      sm.q[r][c] = v;
     }
     // keys [.., end) and from lo on, or below the sinks, are seen by rows gq and gq + 8
     int end[2], lo[2];
@@ -93,41 +114,40 @@ __global__ void __launch_bounds__(ROWS_THREADS, ROWS_CTAS) cs_kv_rows_kernel(con
     }
     auto seen = [&](int key) { return key < g.hi && (key >= g.lo || key < p.c.sinks); };  // by some row
     // this warp's page of tile k, -1 if none of its keys is seen
-    auto page_of = [&](int k) {
+    auto table_of = [&](int k) {
       if (k >= g.k1) return -1;
       const int j0 = g.key0(p.c, k) + warp * 16;
       if (j0 >= g.hi || (j0 + 16 <= g.lo && j0 >= p.c.sinks)) return -1;
       const int page = __ldg(table + (j0 >> B.page_shift));
-      if (page >= 0 && page < B.num_pages) return page;
+      return page < 0 ? INT_MAX : page;
+    };
+    auto checked = [&](int page) {
+      if (page < B.num_pages) return page;
       record(B.ctrl, ERR_INVALID, WHAT_PAGE, p.c.flat ? 0xFFFFFFFFu : static_cast<uint32_t>(g.b));
       return -1;
     };
-    uint4 kr[2][KB], vr[4][VB];
-    auto load_k = [&](int k, int page) {
-      const int j0 = g.key0(p.c, k) + warp * 16;
-      const T* at = kc + page * B.page_stride + (j0 & (B.page_size - 1)) * B.slot_stride + g.kvh * B.head_stride + 8 * jq;
-#pragma unroll
-      for (int b = 0; b < 2; ++b) {
-        const bool in = page >= 0 && seen(j0 + 8 * b + gq);
-#pragma unroll
-        for (int i = 0; i < KB; ++i)
-          kr[b][i] = in ? ld_stream(at + (8 * b + gq) * B.slot_stride + 32 * i) : make_uint4(0, 0, 0, 0);
+    auto load = [&](int which, int k, int page, uint32_t n) {  // n: the warp's tile
+      if (k >= g.k1 || lane != 0) return;
+      uint64_t* bar = &sm.full[warp][n % ST][which];
+      if (page < 0) {  // nothing to read
+        cs::mbar_arrive(bar);
+        return;
       }
+      const int group = ((g.key0(p.c, k) + warp * 16) & (B.page_size - 1)) >> 3;
+      const int c4 = p.head_groups ? (page * B.kv_heads + g.kvh) * p.head_groups + group : page * (B.page_size >> 3) + group;
+      cs::mbar_arrive_expect_tx(bar, 16 * D * 2);
+      tma_5d(&sm.kv[warp][n % ST][which], which ? &p.v : &p.k, 0, 0, 0, p.head_groups ? 0 : g.kvh, c4, bar);
     };
-    auto load_v = [&](int k, int page) {
-      const int j0 = g.key0(p.c, k) + warp * 16;
-      const T* at = vc + page * B.page_stride + (j0 & (B.page_size - 1)) * B.slot_stride + g.kvh * B.head_stride + 8 * gq;
+    int ahead[ST + 1];
 #pragma unroll
-      for (int b = 0; b < 4; ++b) {
-        const int j = 2 * jq + (b & 1) + 8 * (b >> 1);
-        const bool in = page >= 0 && seen(j0 + j);
+    for (int i = 0; i <= ST; ++i) ahead[i] = table_of(g.k0 + i);
 #pragma unroll
-        for (int h = 0; h < VB; ++h) vr[b][h] = in ? ld_stream(at + j * B.slot_stride + 64 * h) : make_uint4(0, 0, 0, 0);
-      }
-    };
-    int page = page_of(g.k0);
-    load_k(g.k0, page);
-    load_v(g.k0, page);
+    for (int i = 0; i < ST; ++i) {
+      const int page = checked(ahead[i]);
+      load(0, g.k0 + i, page, done + i);
+      load(1, g.k0 + i, page, done + i);
+    }
+    int next = ahead[ST];
     float o[VB][8][4];
 #pragma unroll
     for (int h = 0; h < VB; ++h)
@@ -136,22 +156,32 @@ __global__ void __launch_bounds__(ROWS_THREADS, ROWS_CTAS) cs_kv_rows_kernel(con
 #pragma unroll
         for (int c = 0; c < 4; ++c) o[h][i][c] = 0.0f;
     float m_ref[2] = {-INFINITY, -INFINITY}, l[2] = {0.0f, 0.0f};
+#pragma unroll
+    for (int i = 0; i < QN; ++i) {
+      const int x = tid + i * ROWS_THREADS;
+      sm.q[x / (D / 8)][x % (D / 8)] = qv[i];
+    }
     __syncthreads();  // the queries are there
 #pragma unroll 1
     for (int k = g.k0; k < g.k1; ++k) {
       const int j0 = g.key0(p.c, k) + warp * 16;
-      const int next = page_of(k + 1);
+      const int page = checked(next);  // of tile k + ST
+      next = table_of(k + ST + 1);
+      const int stage = done % ST;
+      arrived(0, done);
       float s[2][4] = {};
 #pragma unroll
       for (int i = 0; i < KB; ++i) {
         const uint4 qa = sm.q[gq][4 * i + jq], qb = sm.q[gq + 8][4 * i + jq];
 #pragma unroll
         for (int b = 0; b < 2; ++b) {
-          mma16816<T>(s[b], qa.x, qb.x, qa.y, qb.y, kr[b][i].x, kr[b][i].y);
-          mma16816<T>(s[b], qa.z, qb.z, qa.w, qb.w, kr[b][i].z, kr[b][i].w);
+          const uint4 kr = sm.kv[warp][stage][0][b][i >> 1][gq][(4 * (i & 1) + jq) ^ gq];
+          mma16816<T>(s[b], qa.x, qb.x, qa.y, qb.y, kr.x, kr.y);
+          mma16816<T>(s[b], qa.z, qb.z, qa.w, qb.w, kr.z, kr.w);
         }
       }
-      if (k + 1 < g.k1) load_k(k + 1, next);
+      __syncwarp();
+      load(0, k + ST, page, done + ST);
       bool raise = false;
       float f[2];
 #pragma unroll
@@ -197,12 +227,25 @@ __global__ void __launch_bounds__(ROWS_THREADS, ROWS_CTAS) cs_kv_rows_kernel(con
       }
       const uint32_t a0 = Pair<T>::put(s[0][0], s[0][1]), a1 = Pair<T>::put(s[0][2], s[0][3]);
       const uint32_t a2 = Pair<T>::put(s[1][0], s[1][1]), a3 = Pair<T>::put(s[1][2], s[1][3]);
+      arrived(1, done);
+      // values of keys that no row sees may be anything: zeros instead
+      const bool part = j0 + 16 > g.hi || (j0 < g.lo && j0 + 16 > p.c.sinks);
 #pragma unroll
       for (int h = 0; h < VB; ++h) {
-        const uint32_t* v0 = reinterpret_cast<const uint32_t*>(&vr[0][h]);
-        const uint32_t* v1 = reinterpret_cast<const uint32_t*>(&vr[1][h]);
-        const uint32_t* v2 = reinterpret_cast<const uint32_t*>(&vr[2][h]);
-        const uint32_t* v3 = reinterpret_cast<const uint32_t*>(&vr[3][h]);
+        uint32_t v0[4], v1[4], v2[4], v3[4];
+        *reinterpret_cast<uint4*>(v0) = sm.kv[warp][stage][1][0][h][2 * jq][gq ^ 2 * jq];
+        *reinterpret_cast<uint4*>(v1) = sm.kv[warp][stage][1][0][h][2 * jq + 1][gq ^ (2 * jq + 1)];
+        *reinterpret_cast<uint4*>(v2) = sm.kv[warp][stage][1][1][h][2 * jq][gq ^ 2 * jq];
+        *reinterpret_cast<uint4*>(v3) = sm.kv[warp][stage][1][1][h][2 * jq + 1][gq ^ (2 * jq + 1)];
+        if (part) {
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            if (!seen(j0 + 2 * jq)) v0[e] = 0;
+            if (!seen(j0 + 2 * jq + 1)) v1[e] = 0;
+            if (!seen(j0 + 2 * jq + 8)) v2[e] = 0;
+            if (!seen(j0 + 2 * jq + 9)) v3[e] = 0;
+          }
+        }
 #pragma unroll
         for (int i = 0; i < 8; ++i) {  // column n of this MMA is dimension 8 n + i of the half
           const uint32_t pick = i & 1 ? 0x7632u : 0x5410u;
@@ -210,8 +253,11 @@ __global__ void __launch_bounds__(ROWS_THREADS, ROWS_CTAS) cs_kv_rows_kernel(con
                       __byte_perm(v2[i >> 1], v3[i >> 1], pick));
         }
       }
-      if (k + 1 < g.k1) load_v(k + 1, next);
+      __syncwarp();
+      load(1, k + ST, page, done + ST);
+      ++done;
     }
+    __syncthreads();  // every warp is done with its operands' memory
     // the four warps' states to shared memory
 #pragma unroll
     for (int x = 0; x < 2; ++x) {

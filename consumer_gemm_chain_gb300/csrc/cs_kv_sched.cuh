@@ -162,11 +162,79 @@ struct Walk {
   }
 };
 
-// Every thread of the block: this CTA's range into *r (shared memory).
+// a / b; nearly always both fit 32 bits, where the division is much the shorter
+__device__ __forceinline__ unsigned long long divide(unsigned long long a, unsigned long long b) {
+  if (((a | b) >> 32) == 0) return static_cast<unsigned>(a) / static_cast<unsigned>(b);
+  return a / b;
+}
+
+// One warp, all lanes: the item that holds unit r.rem of sequence s and a key head;
+// 32 trials at a time.
+__device__ __forceinline__ void find_item(const Cut& C, const Seq& s, Range& r) {
+  const int lane = threadIdx.x & 31;
+  int a = 0, e = items_of(C, s);  // units_before(a) <= rem < units_before(e)
+  unsigned long long base = 0;    // units_before(a)
+#pragma unroll 1
+  while (e - a > 1) {
+    const int step = (e - a + 31) / 32;
+    const int k = a + lane * step;
+    const unsigned long long u = k < e ? units_before(C, s, k) : ~0ull;
+    const int last = 31 - __clz(__ballot_sync(0xFFFFFFFFu, u <= r.rem));
+    base = __shfl_sync(0xFFFFFFFFu, u, last);
+    a += last * step;
+    e = min(e, a + step);
+  }
+  r.item = a;
+  r.off = static_cast<int>(r.rem - base);
+}
+
+__device__ __forceinline__ unsigned long long warp_inclusive(unsigned long long x) {
+#pragma unroll
+  for (int d = 1; d < 32; d <<= 1) {
+    const unsigned long long o = __shfl_up_sync(0xFFFFFFFFu, x, d);
+    if ((threadIdx.x & 31) >= d) x += o;
+  }
+  return x;
+}
+
+// This CTA's share of `total` units.
+__device__ __forceinline__ void share(unsigned long long total, Range& r) {
+  r.quota = divide(total + gridDim.x - 1, gridDim.x);
+  r.x0 = min(r.quota * blockIdx.x, total);
+  r.x1 = min(r.x0 + r.quota, total);
+  r.rem = 0;
+  r.b = r.kvh = r.item = r.off = 0;
+}
+
+// Every thread of the block: this CTA's range into *out (shared memory).
 template <int THREADS>
-__device__ __forceinline__ void find_range(const Batch& B, const Cut& C, Range* r, unsigned long long* scratch) {
+__device__ __forceinline__ void find_range(const Batch& B, const Cut& C, Range* out, unsigned long long* scratch) {
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int seqs = C.flat ? 1 : B.seqs;
+  if (seqs <= 32) {  // one sequence per lane of one warp: no barrier but the last
+    if (warp == 0) {
+      Seq s{0, 0, 0};
+      const bool ok = lane < seqs && load_seq(B, C, lane, s);
+      const unsigned long long c = ok ? units_before(C, s, items_of(C, s)) * B.kv_heads : 0;
+      const unsigned long long incl = warp_inclusive(c);
+      Range r;
+      share(__shfl_sync(0xFFFFFFFFu, incl, 31), r);
+      if (r.x0 < r.x1) {
+        r.b = __ffs(__ballot_sync(0xFFFFFFFFu, r.x0 < incl)) - 1;
+        const unsigned long long in = r.x0 - __shfl_sync(0xFFFFFFFFu, incl - c, r.b);
+        const unsigned long long per_head = divide(__shfl_sync(0xFFFFFFFFu, c, r.b), B.kv_heads);
+        s.t0 = __shfl_sync(0xFFFFFFFFu, s.t0, r.b);
+        s.n = __shfl_sync(0xFFFFFFFFu, s.n, r.b);
+        s.m = __shfl_sync(0xFFFFFFFFu, s.m, r.b);
+        r.kvh = static_cast<int>(divide(in, per_head));
+        r.rem = in - r.kvh * per_head;
+        find_item(C, s, r);
+      }
+      if (lane == 0) *out = r;
+    }
+    __syncthreads();
+    return;
+  }
   const int per = (seqs + THREADS - 1) / THREADS;
   const int b0 = min(tid * per, seqs);
   int b1 = min(b0 + per, seqs);
@@ -183,20 +251,15 @@ __device__ __forceinline__ void find_range(const Batch& B, const Cut& C, Range* 
       const unsigned long long c = units_before(C, s, items_of(C, s));
       const unsigned long long in = x0 - at - mine * B.kv_heads;
       if (pass == 1 && in < c * B.kv_heads) {
-        r->b = b;
-        r->kvh = static_cast<int>(in / c);
-        r->rem = in - r->kvh * c;
+        out->b = b;
+        out->kvh = static_cast<int>(divide(in, c));
+        out->rem = in - out->kvh * c;
         break;
       }
       mine += c;
     }
     if (pass == 1) break;
-    unsigned long long incl = mine;
-#pragma unroll
-    for (int d = 1; d < 32; d <<= 1) {
-      const unsigned long long o = __shfl_up_sync(0xFFFFFFFFu, incl, d);
-      if (lane >= d) incl += o;
-    }
+    unsigned long long incl = warp_inclusive(mine);
     if (lane == 31) scratch[warp] = incl;
     __syncthreads();
     unsigned long long before = 0, total = 0;
@@ -206,42 +269,20 @@ __device__ __forceinline__ void find_range(const Batch& B, const Cut& C, Range* 
       total += scratch[w];
     }
     incl = (incl + before) * B.kv_heads;
-    total *= B.kv_heads;
-    const unsigned long long quota = (total + gridDim.x - 1) / gridDim.x;
-    x0 = min(quota * blockIdx.x, total);
-    const unsigned long long x1 = min(x0 + quota, total);
-    if (tid == 0) {
-      r->x0 = x0;
-      r->x1 = x1;
-      r->quota = quota;
-      r->b = r->kvh = r->item = r->off = 0;
-    }
+    Range r;
+    share(total * B.kv_heads, r);
+    if (tid == 0) *out = r;
     __syncthreads();
+    x0 = r.x0;
     at = incl - mine * B.kv_heads;
-    if (x0 >= x1 || x0 < at || x0 >= incl) b1 = b0;
+    if (r.x0 >= r.x1 || x0 < at || x0 >= incl) b1 = b0;
   }
   __syncthreads();
-  if (warp == 0 && r->x0 < r->x1) {
-    // the item that holds unit `rem` of its sequence and head: 32 trials at a time
-    if (load_seq(B, C, r->b, s)) {
-      const unsigned long long rem = r->rem;
-      int a = 0, e = items_of(C, s);  // units_before(a) <= rem < units_before(e)
-      unsigned long long base = 0;    // units_before(a)
-      do {
-        const int step = (e - a + 31) / 32;
-        const int k = a + lane * step;
-        const unsigned long long u = k < e ? units_before(C, s, k) : ~0ull;
-        const int last = 31 - __clz(__ballot_sync(0xFFFFFFFFu, u <= rem));
-        base = __shfl_sync(0xFFFFFFFFu, u, last);
-        a += last * step;
-        e = min(e, a + step);
-      } while (e - a > 1);
-      __syncwarp();
-      if (lane == 0) {
-        r->item = a;
-        r->off = static_cast<int>(rem - base);
-      }
-    }
+  if (warp == 0 && out->x0 < out->x1 && load_seq(B, C, out->b, s)) {
+    Range r = *out;
+    find_item(C, s, r);
+    __syncwarp();
+    if (lane == 0) *out = r;
   }
   __syncthreads();
 }
