@@ -25,6 +25,8 @@ struct cs_kv_s {
   uint32_t* ctrl = nullptr;  // error words, then the counters
   size_t ctrl_words = 0;
   float* part = nullptr;    // pieces of items that several CTAs share
+  float4* other = nullptr;  // halves of items inside a CTA
+  cskv::Split* splits = nullptr;
   float* flat_o = nullptr;  // desc.shared: the prefix's output and log-sum-exp
   bool error_latched = false;
 };
@@ -219,6 +221,8 @@ cs_status check_attn(const cs_kv_s* p, const cs_kv_batch* b, const cs_kv_attn_ar
   const double scale = d.scale > 0.0f ? d.scale : 1.0 / std::sqrt(static_cast<double>(d.head_dim));
   k.scale_log2 = static_cast<float>(scale * 1.4426950408889634);
   k.part = p->part;
+  k.other = p->other;
+  k.splits = p->splits;
   k.arrivals = p->ctrl + cskv::CTRL_COUNTERS;
   k.q_raw = a->q;
   k.k_raw = a->k_cache;
@@ -226,6 +230,13 @@ cs_status check_attn(const cs_kv_s* p, const cs_kv_batch* b, const cs_kv_attn_ar
   k.q_stride = q_stride;
   k.out_wide = reinterpret_cast<uintptr_t>(a->out) % 32 == 0 && k.out_stride % 16 == 0;
   return CS_OK;
+}
+
+const void* join_kernel(const cs_kv_desc& d) {
+  if (d.dtype == CS_BF16)
+    return d.head_dim == 128 ? (const void*)cskv::cs_kv_join_kernel<__nv_bfloat16, 128>
+                             : (const void*)cskv::cs_kv_join_kernel<__nv_bfloat16, 64>;
+  return d.head_dim == 128 ? (const void*)cskv::cs_kv_join_kernel<__half, 128> : (const void*)cskv::cs_kv_join_kernel<__half, 64>;
 }
 
 const void* rows_kernel(const cs_kv_desc& d) {
@@ -280,7 +291,8 @@ cs_status run_attention(cs_kv_s* p, cskv::AttnP& k, int max_rows, cudaStream_t s
   if (s != CS_OK) return s;
   int smem = 0;
   const void* fn = attn_kernel(d, &smem);
-  return launch(fn, dim3(p->num_sms), cskv::ATTN_THREADS, smem, &k, st);
+  if ((s = launch(fn, dim3(p->num_sms), cskv::ATTN_THREADS, smem, &k, st)) != CS_OK) return s;
+  return launch(join_kernel(d), dim3(p->num_sms, 2, 4), cskv::JOIN_THREADS, 0, &k, st);
 }
 
 cs_status append(cs_kv_s* p, const cs_kv_batch* b, const cs_kv_append_args* a, cudaStream_t st) {
@@ -330,8 +342,8 @@ cs_status append(cs_kv_s* p, const cs_kv_batch* b, const cs_kv_append_args* a, c
   return launch(fn, grid, cskv::APPEND_THREADS, 0, &k, st);
 }
 
-// Rows of one key head that a sequence of n new tokens has.
-int rows_of(const cskv::AttnP& k, int n) {
+// Rows of one key head that n new tokens have.
+int rows_of(const cskv::AttnP& k, long long n) {
   const long long tokens = n < k.b.tokens ? n : k.b.tokens;
   return static_cast<int>(tokens * k.b.group);
 }
@@ -345,6 +357,8 @@ cs_status begin(cs_kv_s* p, const cs_kv_batch* b) {
 void free_plan(cs_kv_s* p) {
   cudaFree(p->ctrl);
   cudaFree(p->part);
+  cudaFree(p->other);
+  cudaFree(p->splits);
   cudaFree(p->flat_o);
   delete p;
 }
@@ -381,8 +395,7 @@ cs_status cs_kv_plan(const cs_kv_desc* desc, cs_kv_t* out) {
   p->d = *desc;
   p->device = dev;
   p->num_sms = desc->num_sms > 0 && desc->num_sms < sms ? desc->num_sms : sms;
-  const size_t counters = 2 * static_cast<size_t>(p->num_sms), rows_counters = rows_grid(p);
-  p->ctrl_words = cskv::CTRL_COUNTERS + (counters > rows_counters ? counters : rows_counters);
+  p->ctrl_words = cskv::CTRL_COUNTERS + static_cast<size_t>(rows_grid(p));
   int smem = 0;
   const void* fn = attn_kernel(p->d, &smem);
   if (cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess ||
@@ -391,12 +404,15 @@ cs_status cs_kv_plan(const cs_kv_desc* desc, cs_kv_t* out) {
     free_plan(p);
     return cs_fail(CS_ERR_CUDA, "the attention kernels need %d bytes of shared memory", smem);
   }
-  // states of both kernels: the tensor-core kernel's are the larger
-  const size_t part = static_cast<size_t>(p->num_sms) * 6 * (desc->head_dim / 4 + 1) * 128 * 16;
-  static_assert(cskv::ROWS_CTAS * 2 * cskv::ROWS * (64 + 2) * 4 <= 6 * (64 / 4 + 1) * 128 * 16, "workspace");
+  // states of pieces: the tensor-core kernel's are larger than the rows kernel's
+  const size_t part = static_cast<size_t>(p->num_sms) * 4 * 128 * (desc->head_dim + 8) * 4;
+  static_assert(cskv::ROWS_CTAS * 2 * cskv::ROWS * (64 + 2) <= 4 * 128 * (64 + 8), "workspace");
+  const size_t other = static_cast<size_t>(p->num_sms) * (desc->head_dim / 4 + 1) * 128 * 16;
   const size_t flat = static_cast<size_t>(desc->max_tokens) * desc->heads * (desc->head_dim + 1) * 4;
   if (cudaMalloc(reinterpret_cast<void**>(&p->ctrl), p->ctrl_words * 4) != cudaSuccess ||
       cudaMalloc(reinterpret_cast<void**>(&p->part), part) != cudaSuccess ||
+      cudaMalloc(reinterpret_cast<void**>(&p->other), other) != cudaSuccess ||
+      cudaMalloc(reinterpret_cast<void**>(&p->splits), p->num_sms * sizeof(cskv::Split)) != cudaSuccess ||
       (desc->shared && cudaMalloc(reinterpret_cast<void**>(&p->flat_o), flat) != cudaSuccess)) {
     cudaGetLastError();
     free_plan(p);
@@ -456,7 +472,7 @@ cs_status cs_kv_attention_shared(cs_kv_t p, const cs_kv_batch* b, const int32_t*
     k.pages = prefix_pages;
     k.c.flat = 1;
     k.c.flat_len = prefix_len;
-    if ((s = run_attention(p, k, rows_of(k, b->tokens), static_cast<cudaStream_t>(stream))) != CS_OK) return s;
+    if ((s = run_attention(p, k, rows_of(k, b->seqs * static_cast<long long>(b->max_q)), static_cast<cudaStream_t>(stream))) != CS_OK) return s;
     k.c.flat = 0;
   }
   return run_attention(p, k, rows_of(k, b->max_q), static_cast<cudaStream_t>(stream));

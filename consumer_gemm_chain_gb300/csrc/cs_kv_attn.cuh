@@ -5,13 +5,20 @@
 // and sum, P = 2^(c S - max), O += P V, and O / sum at the end.
 //
 // Work.  An item is 2 x 128 such rows (whole tokens), its tiles have 128 keys; one CTA
-// per SM (cs_kv_sched.cuh).
+// per SM (cs_kv_sched.cuh).  Pieces of items are joined by a kernel of their own.
 #pragma once
 #include "cs_kv_sched.cuh"
 
 namespace cskv {
 
 constexpr int KT = 128;  // keys per tile (Cut.shift 7)
+
+// An item whose tiles several CTAs share.
+struct Split {
+  int pieces;     // 0: none
+  int first;      // its first piece is the CTA's last piece (1) or only (0)
+  int token, tokens, kvh;
+};
 
 struct AttnP {
   CUtensorMap q, k, v;    // for cs_kv_attn_kernel
@@ -24,8 +31,10 @@ struct AttnP {
   float* lse;
   long long out_stride;   // elements
   float scale_log2;       // scale * log2(e): exponents in base 2
-  float* part;            // states: [CTA][first piece, last piece, other half][tile][D / 4 + 1][128 rows] float4
-  uint32_t* arrivals;     // [CTA][tile] pieces of the item that starts there and ends elsewhere
+  float* part;            // pieces' states: [CTA][first piece, last piece][tile][128 rows][O, max, sum, 6 unused]
+  float4* other;          // warpgroup 1's half of an item of one row tile: [CTA][D / 4 + 1][128 rows]
+  Split* splits;          // [CTA] the item that starts there and ends elsewhere
+  uint32_t* arrivals;     // cs_kv_rows_kernel: [CTA] its pieces that are stored
   float* flat_o;          // [tokens][heads][D], [tokens][heads]: a prefix's normalised output and
   float* flat_lse;        // base-2 log-sum-exp; written with c.flat, else joined in if not null
   int per_tile;           // tokens of a 128-row tile: 128 / group, rounded down; an item has two
@@ -67,14 +76,12 @@ struct AttnCtl {
   uint64_t full[SLOTS], empty[SLOTS];
   uint64_t q_full[2], q_empty[2], s_full[2], p_full[2][2], o_full[2];
   uint64_t v_ready[2];                 // the values of the buffer's tile are there
-  uint64_t stored[2], counted[2];      // a piece is stored; its arrival is counted
   uint64_t other_full, other_empty;    // warpgroup 1's half of an item of one row tile
   uint64_t drained;
   unsigned long long scratch[ATTN_THREADS / 32];
   Range range;
   uint32_t tmem;
   volatile int abort;
-  volatile int last[2];
   int turn;               // an MMA warp has the tensor core
   int loads, q_loads[2];  // tiles and queries whose copies were issued
 };
@@ -382,6 +389,20 @@ __device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
   return d;
 }
 
+// A row's state in a piece: O against the maximum, the maximum and the sum.
+template <int D>
+__device__ __forceinline__ float* piece_state(float* part, unsigned cta, int which, int tile, int r) {
+  return part + (((static_cast<size_t>(cta) * 2 + which) * 2 + tile) * 128 + r) * (D + 8);
+}
+
+// The log-sum-exp (base 2) of an output row.
+__device__ __forceinline__ void put_lse(const AttnP& p, long long row, float lse2) {
+  if (p.c.flat)
+    p.flat_lse[row] = lse2;
+  else if (p.lse)
+    p.lse[row] = lse2 * 0.6931471805599453f;
+}
+
 // x += f * the 32 values of 8 float4s `stride` apart (written by this grid or an earlier one).
 __device__ __forceinline__ void axpy(float (&x)[32], const float4* src, int stride, float f) {
   float4 y[8];
@@ -410,14 +431,12 @@ template <typename T, int D>
 __device__ bool softmax_role(const AttnP& p, AttnCtl<AttnShape<D>::SLOTS>* sc, uint8_t* ring, int w) {
   using Sh = AttnShape<D>;
   constexpr int CH = D / 32;                                      // chunks of 32 columns of O
-  constexpr size_t STATE = static_cast<size_t>(D / 4 + 1) * 128;  // float4s
   const Batch& B = p.b;
   const int r = threadIdx.x & 127, lane = threadIdx.x & 31;
   const uint32_t lanes = static_cast<uint32_t>(r & ~31) << 16;
   const uint32_t s_tm = sc->tmem + lanes + COL_S + w * 128, o_tm = sc->tmem + lanes + COL_O + w * D;
   const int row_tok = r / B.group, row_head = r - row_tok * B.group;
-  float4* states = reinterpret_cast<float4*>(p.part) + r;
-  auto state = [&](unsigned cta, int which, int tile) { return states + ((static_cast<size_t>(cta) * 3 + which) * 2 + tile) * STATE; };
+  float4* const shared_half = p.other + static_cast<size_t>(blockIdx.x) * (D / 4 + 1) * 128 + r;
   auto read_o = [&](int c, uint32_t (&o)[32]) {
     cs::tmem_ld32(o_tm + c * 32, o);
     cs::tc_wait_ld();
@@ -427,7 +446,7 @@ __device__ bool softmax_role(const AttnP& p, AttnCtl<AttnShape<D>::SLOTS>* sc, u
   Walk walk(B, p.c, sc->range);
   Seg g;
   uint32_t tiles_done = 0;  // key tiles of the segments before this one
-  uint32_t s_phase = 0, o_phase = 0, j_phase = 0, x_phase = 0;
+  uint32_t s_phase = 0, o_phase = 0, x_phase = 0;
   while (walk.next(B, p.c, g)) {
     const int count = g.k1 - g.k0;
     const uint32_t ring0 = 2 * tiles_done;
@@ -552,7 +571,7 @@ __device__ bool softmax_role(const AttnP& p, AttnCtl<AttnShape<D>::SLOTS>* sc, u
       // the other key tiles of buffer 0's rows, which joins them
       if (!wait_warp(&sc->other_empty, x_phase ^ 1u, sc)) return false;
       x_phase ^= 1u;
-      float4* to = state(blockIdx.x, 2, 0);
+      float4* to = shared_half;
 #pragma unroll 1
       for (int c = 0; c < CH; ++c) {
         uint32_t o[32];
@@ -574,7 +593,7 @@ __device__ bool softmax_role(const AttnP& p, AttnCtl<AttnShape<D>::SLOTS>* sc, u
       if (!wait_warp(&sc->other_full, x_phase, sc)) return false;
       x_phase ^= 1u;
       if (live) {
-        other = state(blockIdx.x, 2, 0);
+        other = shared_half;
         const float4 ml = __ldcg(other + D / 4 * 128);
         const float m_new = fmaxf(m_ref, ml.x);
         f_own = m_ref == -INFINITY ? 0.0f : cs::ex2_approx(m_ref - m_new);
@@ -585,130 +604,141 @@ __device__ bool softmax_role(const AttnP& p, AttnCtl<AttnShape<D>::SLOTS>* sc, u
     }
     const long long row = static_cast<long long>(g.s.t0 + tok) * B.heads + g.kvh * B.group + row_head;
     const bool whole = g.whole();
-    auto starts_before = [&](unsigned cta) { return sc->range.quota * cta < g.x ? 1 : 0; };
-    unsigned c0 = 0, c1 = 0;  // the CTAs that hold pieces of the item
-    float f = f_own, fold = 0.0f, inv = 1.0f;
+    float f = f_own, fold = 0.0f;
     const float4* pre = nullptr;
-#pragma unroll 1
-    for (int pass = whole ? 1 : 0; pass < 2; ++pass) {  // 0: store this piece; 1: the output
-      if (pass == 1) {
-        if (!whole) {
-          // every thread's stores come before the one arrival at gpu scope; the other
-          // pieces are read after it
-          cs::mbar_arrive(&sc->stored[w]);
-          if (r < 32) {
-            if (!wait_warp(&sc->stored[w], j_phase, sc)) return false;
-            if (r == 0) {
-              uint32_t* ctr = p.arrivals + c0 * 2 + tile;
-              const uint32_t old = cs::atom_add_acq_rel_gpu(ctr, 1u);
-              sc->last[w] = old == c1 - c0;
-              if (old == c1 - c0) *ctr = 0u;  // for the next call
-              cs::mbar_arrive(&sc->counted[w]);
-            }
-            __syncwarp();
-          }
-          if (!wait_warp(&sc->counted[w], j_phase, sc)) return false;
-          j_phase ^= 1u;
-          if (!sc->last[w]) break;
-          // the last to arrive joins the pieces in their order
-          m_ref = -INFINITY;
-          l = 0.0f;
-          if (live) {
-#pragma unroll 1
-            for (unsigned c = c0; c <= c1; ++c) m_ref = fmaxf(m_ref, __ldcg(state(c, starts_before(c), tile) + D / 4 * 128).x);
-#pragma unroll 1
-            for (unsigned c = c0; c <= c1; ++c) {
-              const float4 ml = __ldcg(state(c, starts_before(c), tile) + D / 4 * 128);
-              l = fmaf(ml.y, ml.x == -INFINITY ? 0.0f : cs::ex2_approx(ml.x - m_ref), l);
-            }
-          }
-        }
-        if (live && !p.c.flat && p.flat_o) {  // join the prefix's output
-          pre = reinterpret_cast<const float4*>(p.flat_o + row * D);
-          const float z = p.flat_lse[row];
-          const float m_new = fmaxf(m_ref, z);
-          const float own = m_ref == -INFINITY ? 0.0f : cs::ex2_approx(m_ref - m_new);
-          fold = z == -INFINITY ? 0.0f : cs::ex2_approx(z - m_new);
-          l = l * own + fold;
-          f *= own;
-          f_other *= own;
-          m_ref = m_new;
-        }
-        inv = l == 0.0f ? 0.0f : 1.0f / l;
-      } else {
-        const unsigned me = blockIdx.x, q = static_cast<unsigned>(min(sc->range.quota, 0x80000000ull));
-        const unsigned long long end_x = g.x + g.tiles - 1;
-        c0 = sc->range.x0 > g.x ? me - (static_cast<unsigned>(sc->range.x0 - g.x) + q - 1) / q : me;
-        c1 = end_x >= sc->range.x1 ? me + static_cast<unsigned>(end_x - sc->range.x1) / q + 1 : me;
+    float* to = piece_state<D>(p.part, blockIdx.x, sc->range.x0 < g.x, tile, r);
+    if (whole) {
+      if (live && !p.c.flat && p.flat_o) {  // join the prefix's output
+        pre = reinterpret_cast<const float4*>(p.flat_o + row * D);
+        const float z = p.flat_lse[row];
+        const float m_new = fmaxf(m_ref, z);
+        const float own = m_ref == -INFINITY ? 0.0f : cs::ex2_approx(m_ref - m_new);
+        fold = z == -INFINITY ? 0.0f : cs::ex2_approx(z - m_new);
+        l = l * own + fold;
+        f *= own;
+        f_other *= own;
+        m_ref = m_new;
       }
-      float4* to = state(blockIdx.x, sc->range.x0 < g.x, tile);
+      const float inv = l == 0.0f ? 0.0f : 1.0f / l;
+      f *= inv;
+      f_other *= inv;
+      fold *= inv;
+    }
 #pragma unroll 1
-      for (int c = 0; c < CH; ++c) {
-        float x[32];
-        if (pass == 0 || whole) {
-          uint32_t o[32];
-          read_o(c, o);
+    for (int c = 0; c < CH; ++c) {
+      float x[32];
+      uint32_t o[32];
+      read_o(c, o);
 #pragma unroll
-          for (int t = 0; t < 32; ++t) x[t] = __uint_as_float(o[t]) * f;
-          if (other) axpy(x, other + c * 8 * 128, 128, f_other);
-        } else if (live) {
-#pragma unroll
-          for (int t = 0; t < 32; ++t) x[t] = 0.0f;
-#pragma unroll 1
-          for (unsigned i = c0; i <= c1; ++i) {
-            const float4* src = state(i, starts_before(i), tile);
-            const float m_i = __ldcg(src + D / 4 * 128).x;
-            axpy(x, src + c * 8 * 128, 128, m_i == -INFINITY ? 0.0f : cs::ex2_approx(m_i - m_ref));
-          }
-        }
-        if (!live) continue;
-        if (pass == 0) {
-#pragma unroll
-          for (int t = 0; t < 8; ++t) to[(c * 8 + t) * 128] = make_float4(x[4 * t], x[4 * t + 1], x[4 * t + 2], x[4 * t + 3]);
-          continue;
-        }
-        if (pre) axpy(x, pre + c * 8, 1, fold);
-#pragma unroll
-        for (int t = 0; t < 32; ++t) x[t] *= inv;
-        if (p.c.flat) {
-          float4* dst = reinterpret_cast<float4*>(p.flat_o + row * D) + c * 8;
-#pragma unroll
-          for (int t = 0; t < 8; ++t) dst[t] = make_float4(x[4 * t], x[4 * t + 1], x[4 * t + 2], x[4 * t + 3]);
-        } else {
-          uint4* dst = reinterpret_cast<uint4*>(static_cast<T*>(p.out) + (g.s.t0 + tok) * p.out_stride +
-                                                (g.kvh * B.group + row_head) * D + c * 32);
-          uint32_t y[16];
-#pragma unroll
-          for (int t = 0; t < 16; ++t) y[t] = Pair<T>::put(x[2 * t], x[2 * t + 1]);
-          if (p.out_wide) {
-            // a lane's row is another line than its neighbours': whole 32-byte sectors at least
-            st32(dst, y);
-            st32(dst + 2, y + 8);
-          } else {
-#pragma unroll
-            for (int t = 0; t < 4; ++t) dst[t] = make_uint4(y[4 * t], y[4 * t + 1], y[4 * t + 2], y[4 * t + 3]);
-          }
-        }
-      }
-      __syncwarp();
-      if (pass == 0 || whole) {  // O and the other buffer's state are read
-        cs::tc_fence_before();
-        if (!two && count > 1) cs::mbar_arrive(&sc->other_empty);
-      }
+      for (int t = 0; t < 32; ++t) x[t] = __uint_as_float(o[t]) * f;
+      if (other) axpy(x, other + c * 8 * 128, 128, f_other);
       if (!live) continue;
-      if (pass == 0) {
-        to[D / 4 * 128] = make_float4(m_ref, l, 0.0f, 0.0f);
+      if (pre) axpy(x, pre + c * 8, 1, fold);
+      if (!whole || p.c.flat) {  // 32-bit values: a piece's state, or a prefix's output
+        float* dst = whole ? p.flat_o + row * D + c * 32 : to + c * 32;
+#pragma unroll
+        for (int t = 0; t < 4; ++t) st32(dst + 8 * t, reinterpret_cast<uint32_t*>(x) + 8 * t);
       } else {
-        const float lse2 = l == 0.0f ? -INFINITY : m_ref + log2f(l);
-        if (p.c.flat)
-          p.flat_lse[row] = lse2;
-        else if (p.lse)
-          p.lse[row] = lse2 * 0.6931471805599453f;
+        uint4* dst = reinterpret_cast<uint4*>(static_cast<T*>(p.out) + (g.s.t0 + tok) * p.out_stride +
+                                              (g.kvh * B.group + row_head) * D + c * 32);
+        uint32_t y[16];
+#pragma unroll
+        for (int t = 0; t < 16; ++t) y[t] = Pair<T>::put(x[2 * t], x[2 * t + 1]);
+        if (p.out_wide) {
+          // a lane's row is another line than its neighbours': whole 32-byte sectors at least
+          st32(dst, y);
+          st32(dst + 2, y + 8);
+        } else {
+#pragma unroll
+          for (int t = 0; t < 4; ++t) dst[t] = make_uint4(y[4 * t], y[4 * t + 1], y[4 * t + 2], y[4 * t + 3]);
+        }
       }
     }
     __syncwarp();
+    cs::tc_fence_before();
+    if (!two && count > 1) cs::mbar_arrive(&sc->other_empty);  // the other buffer's state is read
+    if (whole) {
+      if (live) put_lse(p, row, l == 0.0f ? -INFINITY : m_ref + log2f(l));
+    } else {
+      if (live) *reinterpret_cast<float2*>(to + D) = make_float2(m_ref, l);
+      if (threadIdx.x == 0 && sc->range.x0 <= g.x) {  // the item starts here: what its joining needs to know
+        const unsigned q = static_cast<unsigned>(min(sc->range.quota, 0x80000000ull));
+        const unsigned long long end_x = g.x + g.tiles - 1;
+        Split sp;
+        sp.pieces = static_cast<unsigned>(end_x - sc->range.x1) / q + 2;
+        sp.first = sc->range.x0 < g.x;
+        sp.token = g.s.t0 + g.item * p.c.per_item;
+        sp.tokens = min(p.c.per_item, g.s.n - g.item * p.c.per_item);
+        sp.kvh = g.kvh;
+        p.splits[blockIdx.x] = sp;
+      }
+      __syncwarp();
+    }
   }
   return true;
+}
+
+// Joins the pieces of the items that several CTAs of cs_kv_attn_kernel share: block (c, tile, z)
+// 32 rows of a row tile of the item that starts in CTA c, a warp four rows, a lane
+// D / 32 dimensions.  A kernel of its own, because one SM joining ten pieces of 256 rows took
+// 20 us and more while the others were done.
+constexpr int JOIN_THREADS = 256;
+template <typename T, int D>
+__global__ void __launch_bounds__(JOIN_THREADS) cs_kv_join_kernel(const __grid_constant__ AttnP p) {
+  cs::grid_dep_wait();
+  cs::grid_dep_launch_dependents();
+  const Split sp = p.splits[blockIdx.x];
+  if (sp.pieces == 0) return;
+  const Batch& B = p.b;
+  const int tile = blockIdx.y, lane = threadIdx.x & 31;
+  const int rows = min(p.per_tile, sp.tokens - tile * p.per_tile) * B.group;
+  for (int i = 0; i < 4; ++i) {
+    const int r = blockIdx.z * 32 + i * 8 + (threadIdx.x >> 5);
+    if (r >= rows) return;
+    auto piece = [&](int c) { return piece_state<D>(p.part, blockIdx.x + c, c == 0 && sp.first, tile, r); };
+    // the row's maximum over all pieces, then the sum of the pieces in their order
+    float m = -INFINITY;
+    for (int c = lane; c < sp.pieces; c += 32) m = fmaxf(m, __ldcg(piece(c) + D));
+#pragma unroll
+    for (int d = 16; d; d >>= 1) m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, d));
+    constexpr int W = D / 32;
+    float x[W] = {}, l = 0.0f;
+#pragma unroll 8
+    for (int c = 0; c < sp.pieces; ++c) {
+      const float* src = piece(c);
+      const float2 ml = __ldcg(reinterpret_cast<const float2*>(src + D));
+      const float f = ml.x == -INFINITY ? 0.0f : cs::ex2_approx(ml.x - m);
+      l = fmaf(ml.y, f, l);
+      if constexpr (W == 4) {
+        const float4 y = __ldcg(reinterpret_cast<const float4*>(src) + lane);
+        x[0] = fmaf(y.x, f, x[0]), x[1] = fmaf(y.y, f, x[1]), x[2] = fmaf(y.z, f, x[2]), x[3] = fmaf(y.w, f, x[3]);
+      } else {
+        const float2 y = __ldcg(reinterpret_cast<const float2*>(src) + lane);
+        x[0] = fmaf(y.x, f, x[0]), x[1] = fmaf(y.y, f, x[1]);
+      }
+    }
+    const int t = r / B.group;
+    const long long tok = sp.token + tile * p.per_tile + t, row = tok * B.heads + sp.kvh * B.group + r - t * B.group;
+    if (!p.c.flat && p.flat_o) {  // join the prefix's output
+      const float z = p.flat_lse[row], top = fmaxf(m, z);
+      const float own = m == -INFINITY ? 0.0f : cs::ex2_approx(m - top), fold = z == -INFINITY ? 0.0f : cs::ex2_approx(z - top);
+#pragma unroll
+      for (int w = 0; w < W; ++w) x[w] = x[w] * own + p.flat_o[row * D + lane * W + w] * fold;
+      l = l * own + fold;
+      m = top;
+    }
+    const float inv = l == 0.0f ? 0.0f : 1.0f / l;
+    if (p.c.flat) {
+#pragma unroll
+      for (int w = 0; w < W; ++w) p.flat_o[row * D + lane * W + w] = x[w] * inv;
+    } else {
+      uint32_t* dst = reinterpret_cast<uint32_t*>(static_cast<T*>(p.out) + tok * p.out_stride +
+                                                  (sp.kvh * B.group + r - t * B.group) * D) + lane * (W / 2);
+#pragma unroll
+      for (int w = 0; w < W; w += 2) dst[w / 2] = Pair<T>::put(x[w] * inv, x[w + 1] * inv);
+    }
+    if (lane == 0) put_lse(p, row, l == 0.0f ? -INFINITY : m + log2f(l));
+  }
 }
 
 template <typename T, int D>
@@ -734,8 +764,6 @@ __global__ void __launch_bounds__(ATTN_THREADS, 1) cs_kv_attn_kernel(const __gri
       for (int h = 0; h < 2; ++h) cs::mbar_init(&sc->p_full[w][h], 4);  // the warps of its warpgroup
       cs::mbar_init(&sc->o_full[w], 1);
       cs::mbar_init(&sc->v_ready[w], 1);
-      cs::mbar_init(&sc->stored[w], 128);
-      cs::mbar_init(&sc->counted[w], 1);
     }
     cs::mbar_init(&sc->other_full, 128);
     cs::mbar_init(&sc->other_empty, 128);
@@ -755,6 +783,7 @@ __global__ void __launch_bounds__(ATTN_THREADS, 1) cs_kv_attn_kernel(const __gri
   cs::tc_fence_after();
   cs::grid_dep_wait();
   cs::grid_dep_launch_dependents();
+  if (threadIdx.x == 0) p.splits[blockIdx.x].pieces = 0;
   find_range<ATTN_THREADS>(p.b, p.c, &sc->range, sc->scratch);
   constexpr int bf16 = sizeof(T) == 2 && !std::is_same<T, __half>::value;
   if (warp < 8) {

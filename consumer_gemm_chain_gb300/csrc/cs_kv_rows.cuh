@@ -8,7 +8,8 @@
 // free as long as both operands agree on it, so each lane's part of the m16n8k16
 // fragments is 16 consecutive bytes: of K, of the key that is its column; of V, of
 // its four keys.  Each warp has its own running maximum and sum; the four are joined
-// in shared memory at the end, pieces of an item as in cs_kv_sched.cuh.
+// in shared memory at the end, and the pieces of an item by the last of its CTAs to
+// store one (in their order, so that the result does not depend on which that is).
 #pragma once
 #include <climits>
 

@@ -4,9 +4,8 @@
 // and key head; it needs one or more tiles of keys.  The tiles of all items, laid
 // end to end, are cut into one equal range per CTA: long and short sequences, one or
 // many, prompts and single tokens all load the SMs alike, without a launch per kind.
-// Items cut by a range's border leave their state (O, max, sum) in the workspace,
-// and the last CTA to arrive joins the pieces in their order, so the result
-// does not depend on who is last.
+// Items cut by a range's border leave their state (O, max, sum) in the workspace, and
+// the pieces are joined in their order.
 #pragma once
 #include "cs_kv_append.cuh"
 
