@@ -223,6 +223,7 @@ cs_status check_attn(const cs_kv_s* p, const cs_kv_batch* b, const cs_kv_attn_ar
   k.part = p->part;
   k.other = p->other;
   k.splits = p->splits;
+  k.num_splits = p->num_sms;
   k.arrivals = p->ctrl + cskv::CTRL_COUNTERS;
   k.q_raw = a->q;
   k.k_raw = a->k_cache;
@@ -251,8 +252,7 @@ int rows_smem(const cs_kv_desc& d) {
 }
 
 int rows_grid(const cs_kv_s* p) {
-  const int n = p->num_sms * cskv::ROWS_CTAS;
-  return n < cskv::ROWS_MAX_GRID ? n : cskv::ROWS_MAX_GRID;
+  return p->num_sms * cskv::ROWS_CTAS;
 }
 
 const void* attn_kernel(const cs_kv_desc& d, int* smem) {
@@ -292,7 +292,7 @@ cs_status run_attention(cs_kv_s* p, cskv::AttnP& k, int max_rows, cudaStream_t s
   int smem = 0;
   const void* fn = attn_kernel(d, &smem);
   if ((s = launch(fn, dim3(p->num_sms), cskv::ATTN_THREADS, smem, &k, st)) != CS_OK) return s;
-  return launch(join_kernel(d), dim3(p->num_sms, 2, 4), cskv::JOIN_THREADS, 0, &k, st);
+  return launch(join_kernel(d), dim3(4 * p->num_sms), cskv::JOIN_THREADS, 0, &k, st);
 }
 
 cs_status append(cs_kv_s* p, const cs_kv_batch* b, const cs_kv_append_args* a, cudaStream_t st) {
@@ -395,6 +395,7 @@ cs_status cs_kv_plan(const cs_kv_desc* desc, cs_kv_t* out) {
   p->d = *desc;
   p->device = dev;
   p->num_sms = desc->num_sms > 0 && desc->num_sms < sms ? desc->num_sms : sms;
+  if (p->num_sms > cskv::JOIN_THREADS) p->num_sms = cskv::JOIN_THREADS;
   p->ctrl_words = cskv::CTRL_COUNTERS + static_cast<size_t>(rows_grid(p));
   int smem = 0;
   const void* fn = attn_kernel(p->d, &smem);

@@ -34,6 +34,7 @@ struct AttnP {
   float* part;            // pieces' states: [CTA][first piece, last piece][tile][128 rows][O, max, sum, 6 unused]
   float4* other;          // warpgroup 1's half of an item of one row tile: [CTA][D / 4 + 1][128 rows]
   Split* splits;          // [CTA] the item that starts there and ends elsewhere
+  int num_splits;
   uint32_t* arrivals;     // cs_kv_rows_kernel: [CTA] its pieces that are stored
   float* flat_o;          // [tokens][heads][D], [tokens][heads]: a prefix's normalised output and
   float* flat_lse;        // base-2 log-sum-exp; written with c.flat, else joined in if not null
@@ -678,24 +679,45 @@ __device__ bool softmax_role(const AttnP& p, AttnCtl<AttnShape<D>::SLOTS>* sc, u
   return true;
 }
 
-// Joins the pieces of the items that several CTAs of cs_kv_attn_kernel share: block (c, tile, z)
-// 32 rows of a row tile of the item that starts in CTA c, a warp four rows, a lane
-// D / 32 dimensions.  A kernel of its own, because one SM joining ten pieces of 256 rows took
-// 20 us and more while the others were done.
-constexpr int JOIN_THREADS = 256;
+// Joins the pieces of the items that several CTAs of cs_kv_attn_kernel share, a row to a
+// warp, D / 32 dimensions to a lane.  A kernel of its own, because one SM joining ten
+// pieces of 256 rows took 20 us and more while the others were done.
+constexpr int JOIN_THREADS = 256;  // at least the grid of cs_kv_attn_kernel
 template <typename T, int D>
 __global__ void __launch_bounds__(JOIN_THREADS) cs_kv_join_kernel(const __grid_constant__ AttnP p) {
+  __shared__ int before[JOIN_THREADS + 1], sums[JOIN_THREADS / 32];
   cs::grid_dep_wait();
   cs::grid_dep_launch_dependents();
-  const Split sp = p.splits[blockIdx.x];
-  if (sp.pieces == 0) return;
   const Batch& B = p.b;
-  const int tile = blockIdx.y, lane = threadIdx.x & 31;
-  const int rows = min(p.per_tile, sp.tokens - tile * p.per_tile) * B.group;
-  for (int i = 0; i < 4; ++i) {
-    const int r = blockIdx.z * 32 + i * 8 + (threadIdx.x >> 5);
-    if (r >= rows) return;
-    auto piece = [&](int c) { return piece_state<D>(p.part, blockIdx.x + c, c == 0 && sp.first, tile, r); };
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  // rows of the items that are split, in the order of the CTAs that they start in
+  const int mine = tid < p.num_splits && p.splits[tid].pieces ? p.splits[tid].tokens * B.group : 0;
+  int incl = mine;
+#pragma unroll
+  for (int d = 1; d < 32; d <<= 1) {
+    const int o = __shfl_up_sync(0xFFFFFFFFu, incl, d);
+    if (lane >= d) incl += o;
+  }
+  if (lane == 31) sums[warp] = incl;
+  __syncthreads();
+  for (int w = 0; w < warp; ++w) incl += sums[w];
+  before[tid + 1] = incl;
+  if (tid == 0) before[0] = 0;
+  __syncthreads();
+  const int total = before[JOIN_THREADS];
+  for (int n = blockIdx.x * (JOIN_THREADS / 32) + warp; n < total; n += gridDim.x * (JOIN_THREADS / 32)) {
+    int c0 = 0, e = JOIN_THREADS;  // before[c0] <= n < before[e]
+    while (e - c0 > 1) {
+      const int mid = (c0 + e) >> 1;
+      if (before[mid] <= n)
+        c0 = mid;
+      else
+        e = mid;
+    }
+    const Split sp = p.splits[c0];
+    const int t = (n - before[c0]) / B.group, h = n - before[c0] - t * B.group;  // token of the item, head of the group
+    const int tile = t >= p.per_tile, r = (t - tile * p.per_tile) * B.group + h;
+    auto piece = [&](int c) { return piece_state<D>(p.part, c0 + c, c == 0 && sp.first, tile, r); };
     // the row's maximum over all pieces, then the sum of the pieces in their order
     float m = -INFINITY;
     for (int c = lane; c < sp.pieces; c += 32) m = fmaxf(m, __ldcg(piece(c) + D));
@@ -717,8 +739,7 @@ __global__ void __launch_bounds__(JOIN_THREADS) cs_kv_join_kernel(const __grid_c
         x[0] = fmaf(y.x, f, x[0]), x[1] = fmaf(y.y, f, x[1]);
       }
     }
-    const int t = r / B.group;
-    const long long tok = sp.token + tile * p.per_tile + t, row = tok * B.heads + sp.kvh * B.group + r - t * B.group;
+    const long long tok = sp.token + t, row = tok * B.heads + sp.kvh * B.group + h;
     if (!p.c.flat && p.flat_o) {  // join the prefix's output
       const float z = p.flat_lse[row], top = fmaxf(m, z);
       const float own = m == -INFINITY ? 0.0f : cs::ex2_approx(m - top), fold = z == -INFINITY ? 0.0f : cs::ex2_approx(z - top);
@@ -733,7 +754,7 @@ __global__ void __launch_bounds__(JOIN_THREADS) cs_kv_join_kernel(const __grid_c
       for (int w = 0; w < W; ++w) p.flat_o[row * D + lane * W + w] = x[w] * inv;
     } else {
       uint32_t* dst = reinterpret_cast<uint32_t*>(static_cast<T*>(p.out) + tok * p.out_stride +
-                                                  (sp.kvh * B.group + r - t * B.group) * D) + lane * (W / 2);
+                                                  (sp.kvh * B.group + h) * D) + lane * (W / 2);
 #pragma unroll
       for (int w = 0; w < W; w += 2) dst[w / 2] = Pair<T>::put(x[w] * inv, x[w + 1] * inv);
     }

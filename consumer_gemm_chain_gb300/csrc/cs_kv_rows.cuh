@@ -3,11 +3,11 @@
 // values' bytes bound it, and for short contexts the latency.
 //
 // An item is the rows of one sequence and key head, a tile 64 keys: 16 for each of a
-// CTA's four warps, which has them copied (one TMA box for K, one for V) for itself, so that no
+// CTA's warps, which has them copied (one TMA box for K, one for V) for itself, so that no
 // barrier of the CTA lies on the way.  The order of the contracted dimensions of a product is
 // free as long as both operands agree on it, so each lane's part of the m16n8k16
 // fragments is 16 consecutive bytes: of K, of the key that is its column; of V, of
-// its four keys.  Each warp has its own running maximum and sum; the four are joined
+// its four keys.  Each warp has its own running maximum and sum; they are joined
 // in shared memory at the end, and the pieces of an item by the last of its CTAs to
 // store one (in their order, so that the result does not depend on which that is).
 #pragma once
@@ -18,10 +18,10 @@
 namespace cskv {
 
 constexpr int ROWS = 16;         // rows of an item
-constexpr int ROWS_THREADS = 128;
-constexpr int ROWS_CTAS = 3;     // per SM: 12 warps with up to 16 KB in flight each
-constexpr int ROWS_MAX_GRID = 512;
-constexpr int ROWS_SHIFT = 6;    // keys of a tile
+constexpr int ROWS_SHIFT = 6;     // keys of a tile: 64
+constexpr int ROWS_WARPS = (1 << ROWS_SHIFT) / 16;  // 16 keys each
+constexpr int ROWS_THREADS = 32 * ROWS_WARPS;
+constexpr int ROWS_CTAS = 12 / ROWS_WARPS;  // per SM: 12 warps (168 registers a thread) with up to 16 KB in flight each
 
 template <typename T>
 __device__ __forceinline__ void mma16816(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
@@ -41,15 +41,15 @@ struct alignas(1024) RowsShared {
   static constexpr int STAGES = D == 128 ? 2 : 4;  // tiles on their way
   union {
     // [warp][stage][K, V][8-key group][64-dimension half][key][16-byte piece, at its index ^ key]
-    uint4 kv[4][STAGES][2][2][D / 64][8][8];
-    float o[4][ROWS][D + 4];                 // each warp's output
-    float weight[ROWS_MAX_GRID][ROWS];       // of the pieces of an item
+    uint4 kv[ROWS_WARPS][STAGES][2][2][D / 64][8][8];
+    float o[ROWS_WARPS][ROWS][D + 4];        // each warp's output
+    float sum[ROWS_WARPS][ROWS][D + 2];      // of a part of an item's pieces: output, sum
   };
   Range range;
   unsigned long long scratch[ROWS_THREADS / 32];
   int last, failed;
-  uint64_t full[4][STAGES][2];  // [warp][stage][K, V]
-  float2 ml[4][ROWS];           // each warp's maximum and sum of a row
+  uint64_t full[ROWS_WARPS][STAGES][2];  // [warp][stage][K, V]
+  float2 ml[ROWS_WARPS][ROWS];  // each warp's maximum and sum of a row
   float top[ROWS_THREADS];
   uint4 q[ROWS][D / 8 + 1];
 };
@@ -61,7 +61,7 @@ __global__ void __launch_bounds__(ROWS_THREADS, ROWS_CTAS) cs_kv_rows_kernel(con
       *reinterpret_cast<RowsShared<D>*>((reinterpret_cast<uintptr_t>(rows_smem) + 1023) & ~uintptr_t(1023));
   constexpr int ST = RowsShared<D>::STAGES;
   if (threadIdx.x == 0) {
-    for (int i = 0; i < 4 * ST * 2; ++i) cs::mbar_init(&sm.full[0][0][0] + i, 1);
+    for (int i = 0; i < ROWS_WARPS * ST * 2; ++i) cs::mbar_init(&sm.full[0][0][0] + i, 1);
     sm.failed = 0;
     cs::fence_mbar_init();
     cs::prefetch_tmap(&p.k);
@@ -259,7 +259,7 @@ __global__ void __launch_bounds__(ROWS_THREADS, ROWS_CTAS) cs_kv_rows_kernel(con
       ++done;
     }
     __syncthreads();  // every warp is done with its operands' memory
-    // the four warps' states to shared memory
+    // the warps' states to shared memory
 #pragma unroll
     for (int x = 0; x < 2; ++x) {
       l[x] += __shfl_xor_sync(0xFFFFFFFFu, l[x], 1);
@@ -278,10 +278,9 @@ __global__ void __launch_bounds__(ROWS_THREADS, ROWS_CTAS) cs_kv_rows_kernel(con
       }
     }
     __syncthreads();
-    const int d = tid % D;
     auto state = [&](unsigned cta, int which, int r) { return p.part + ((static_cast<size_t>(cta) * 2 + which) * ROWS + r) * (D + 2); };
     // dimension d of row r from its state
-    auto finish = [&](int r, float x, float m, float l) {
+    auto finish = [&](int r, int d, float x, float m, float l) {
       const int t = r / B.group;
       const long long row = static_cast<long long>(g.s.t0 + first + t) * B.heads + g.kvh * B.group + r - t * B.group;
       if (!p.c.flat && p.flat_o) {  // join the prefix's output
@@ -306,19 +305,20 @@ __global__ void __launch_bounds__(ROWS_THREADS, ROWS_CTAS) cs_kv_rows_kernel(con
       }
     };
     const bool whole = g.whole();
-    for (int r = tid / D; r < rows; r += ROWS_THREADS / D) {
+    for (int i = tid; i < rows * D; i += ROWS_THREADS) {
+      const int r = i / D, d = i % D;
       float m = -INFINITY, sum = 0.0f, x = 0.0f;
 #pragma unroll
-      for (int w = 0; w < 4; ++w) m = fmaxf(m, sm.ml[w][r].x);
+      for (int w = 0; w < ROWS_WARPS; ++w) m = fmaxf(m, sm.ml[w][r].x);
 #pragma unroll
-      for (int w = 0; w < 4; ++w) {
+      for (int w = 0; w < ROWS_WARPS; ++w) {
         const float2 ml = sm.ml[w][r];
         const float f = ml.x == -INFINITY ? 0.0f : cs::ex2_approx(ml.x - m);
         sum = fmaf(ml.y, f, sum);
         x = fmaf(sm.o[w][r][d], f, x);
       }
       if (whole) {
-        finish(r, x, m, sum);
+        finish(r, d, x, m, sum);
       } else {
         float* to = state(blockIdx.x, sm.range.x0 < g.x, r);
         to[d] = x;
@@ -351,24 +351,43 @@ __global__ void __launch_bounds__(ROWS_THREADS, ROWS_CTAS) cs_kv_rows_kernel(con
     __syncthreads();
 #pragma unroll
     for (int i = 0; i < ROWS_THREADS / ROWS; ++i) m = fmaxf(m, sm.top[i * ROWS + wr]);
-    if (wr < rows)
-      for (int i = tid / ROWS; i < pieces; i += ROWS_THREADS / ROWS) {
-        const float x = __ldcg(piece(i, wr) + D);
-        sm.weight[i][wr] = x == -INFINITY ? 0.0f : cs::ex2_approx(x - m);
-      }
     __syncthreads();
     if (tid < ROWS) sm.top[tid] = m;
     __syncthreads();
-    for (int r = tid / D; r < rows; r += ROWS_THREADS / D) {
-      float x = 0.0f, sum = 0.0f;
+    // a warp sums a row over all pieces, or with few rows over a part of them; a lane D / 32
+    // dimensions
+    constexpr int W = D / 32;
+    const int parts = rows >= ROWS_WARPS ? 1 : ROWS_WARPS / rows, per = (pieces + parts - 1) / parts;
+    for (int u = warp; u < rows * parts; u += ROWS_WARPS) {
+      const int r = u % rows, part = u / rows, to = min(pieces, (part + 1) * per);
+      float x[W] = {}, sum = 0.0f;
+      const float top = sm.top[r];
 #pragma unroll 8
-      for (int i = 0; i < pieces; ++i) {
+      for (int i = part * per; i < to; ++i) {
         const float* from = piece(i, r);
-        const float f = sm.weight[i][r];
-        x = fmaf(__ldcg(from + d), f, x);
-        sum = fmaf(__ldcg(from + D + 1), f, sum);
+        const float2 ml = __ldcg(reinterpret_cast<const float2*>(from + D));
+        const float f = ml.x == -INFINITY ? 0.0f : cs::ex2_approx(ml.x - top);
+        sum = fmaf(ml.y, f, sum);
+#pragma unroll
+        for (int v = 0; v < W; v += 2) {
+          const float2 y = __ldcg(reinterpret_cast<const float2*>(from + lane * 2 + 32 * v));
+          x[v] = fmaf(y.x, f, x[v]);
+          x[v + 1] = fmaf(y.y, f, x[v + 1]);
+        }
       }
-      finish(r, x, sm.top[r], sum);
+#pragma unroll
+      for (int v = 0; v < W; v += 2) *reinterpret_cast<float2*>(&sm.sum[part][r][lane * 2 + 32 * v]) = make_float2(x[v], x[v + 1]);
+      if (lane == 0) sm.sum[part][r][D] = sum;
+    }
+    __syncthreads();
+    for (int i = tid; i < rows * D; i += ROWS_THREADS) {
+      const int r = i / D, d = i % D;
+      float y = 0.0f, l = 0.0f;
+      for (int part = 0; part < parts; ++part) {
+        y += sm.sum[part][r][d];
+        l += sm.sum[part][r][D];
+      }
+      finish(r, d, y, sm.top[r], l);
     }
   }
 }
