@@ -28,6 +28,9 @@ struct cs_kv_s {
   float4* other = nullptr;  // halves of items inside a CTA
   cskv::Split* splits = nullptr;
   float* flat_o = nullptr;  // desc.shared: the prefix's output and log-sum-exp
+  // copies of a cache (its address is put in by each call): a whole page's slots of a
+  // head, and 16 slots
+  CUtensorMap page_map, slots_map;
   bool error_latched = false;
 };
 
@@ -158,25 +161,32 @@ cs_status check_caches(const void* k, const void* v) {
   return CS_OK;
 }
 
-PFN_cuTensorMapEncodeTiled_v12000 get_encode() {
-  static PFN_cuTensorMapEncodeTiled_v12000 fn = nullptr;
+struct Driver {
+  PFN_cuTensorMapEncodeTiled_v12000 encode = nullptr;
+  PFN_cuTensorMapReplaceAddress_v12000 replace = nullptr;
+};
+
+const Driver& driver() {
+  static Driver d;
   static std::once_flag once;
   std::call_once(once, [] {
-    void* f = nullptr;
-    cudaDriverEntryPointQueryResult q;
-    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &f, 12000, cudaEnableDefault, &q) == cudaSuccess &&
-        q == cudaDriverEntryPointSuccess)
-      fn = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(f);
+    auto entry = [](const char* name) {
+      void* f = nullptr;
+      cudaDriverEntryPointQueryResult q;
+      const bool ok = cudaGetDriverEntryPointByVersion(name, &f, 12000, cudaEnableDefault, &q) == cudaSuccess &&
+                      q == cudaDriverEntryPointSuccess;
+      return ok ? f : nullptr;
+    };
+    d.encode = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(entry("cuTensorMapEncodeTiled"));
+    d.replace = reinterpret_cast<PFN_cuTensorMapReplaceAddress_v12000>(entry("cuTensorMapReplaceAddress"));
   });
-  return fn;
+  return d;
 }
 
 cs_status encode(CUtensorMap* map, int bf16, const void* ptr, int rank, const cuuint64_t* dims, const cuuint64_t* strides,
                  const cuuint32_t* box, const char* name) {
-  auto enc = get_encode();
-  if (!enc) return cs_fail(CS_ERR_CUDA, "cuTensorMapEncodeTiled is unavailable (driver too old?)");
   const cuuint32_t ones[5] = {1, 1, 1, 1, 1};
-  const CUresult r = enc(map, bf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, rank,
+  const CUresult r = driver().encode(map, bf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, rank,
                          const_cast<void*>(ptr), dims, strides, box, ones, CU_TENSOR_MAP_INTERLEAVE_NONE,
                          CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
   if (r != CUDA_SUCCESS) return cs_fail(CS_ERR_CUDA, "cuTensorMapEncodeTiled failed (%d) for %s", static_cast<int>(r), name);
@@ -185,8 +195,7 @@ cs_status encode(CUtensorMap* map, int bf16, const void* ptr, int rank, const cu
 
 // A cache as [8-slot group][head][64-dimension half][slot of the group][64]: one box is
 // some slots of a page, of one head.  In the HEAD layout heads are part of the groups' order.
-cs_status encode_cache(const cs_kv_s* p, const cskv::Batch& B, CUtensorMap* map, const void* ptr, int slots, const char* name) {
-  const cs_kv_desc& d = p->d;
+cs_status encode_cache(const cs_kv_desc& d, const cskv::Batch& B, CUtensorMap* map, const void* ptr, int slots) {
   const bool head = d.cache_layout == CS_KV_HEAD;
   const cuuint64_t groups = static_cast<cuuint64_t>(d.num_pages) * (d.page_size / 8);
   const cuuint64_t dims[5] = {64, 8, static_cast<cuuint64_t>(d.head_dim / 64), head ? 1 : static_cast<cuuint64_t>(d.kv_heads),
@@ -194,7 +203,16 @@ cs_status encode_cache(const cs_kv_s* p, const cskv::Batch& B, CUtensorMap* map,
   const cuuint64_t slot = static_cast<cuuint64_t>(B.slot_stride) * 2;
   const cuuint64_t strides[4] = {slot, 128, static_cast<cuuint64_t>(B.head_stride) * 2, 8 * slot};
   const cuuint32_t box[5] = {64, 8, static_cast<cuuint32_t>(d.head_dim / 64), 1, static_cast<cuuint32_t>(slots / 8)};
-  return encode(map, d.dtype == CS_BF16, ptr, 5, dims, strides, box, name);
+  return encode(map, d.dtype == CS_BF16, ptr, 5, dims, strides, box, "a cache");
+}
+
+cs_status map_caches(cskv::AttnP& k, const CUtensorMap& like) {
+  k.k = like;
+  k.v = like;
+  auto replace = driver().replace;
+  if (replace(&k.k, const_cast<void*>(k.k_raw)) != CUDA_SUCCESS || replace(&k.v, const_cast<void*>(k.v_raw)) != CUDA_SUCCESS)
+    return cs_fail(CS_ERR_CUDA, "cuTensorMapReplaceAddress failed");
+  return CS_OK;
 }
 
 cs_status check_attn(const cs_kv_s* p, const cs_kv_batch* b, const cs_kv_attn_args* a, cskv::AttnP& k) {
@@ -274,8 +292,7 @@ cs_status run_attention(cs_kv_s* p, cskv::AttnP& k, int max_rows, cudaStream_t s
   if (max_rows <= cskv::ROWS) {
     k.c.per_item = cskv::ROWS / k.b.group;
     k.c.shift = cskv::ROWS_SHIFT;
-    if ((s = encode_cache(p, k.b, &k.k, k.k_raw, 16, "k_cache")) != CS_OK) return s;
-    if ((s = encode_cache(p, k.b, &k.v, k.v_raw, 16, "v_cache")) != CS_OK) return s;
+    if ((s = map_caches(k, p->slots_map)) != CS_OK) return s;
     return launch(rows_kernel(d), dim3(rows_grid(p)), cskv::ROWS_THREADS, rows_smem(d), &k, st);
   }
   k.per_tile = 128 / k.b.group;
@@ -286,8 +303,7 @@ cs_status run_attention(cs_kv_s* p, cskv::AttnP& k, int max_rows, cudaStream_t s
   const cuuint64_t strides[2] = {static_cast<cuuint64_t>(d.head_dim) * 2, static_cast<cuuint64_t>(k.q_stride) * 2};
   const cuuint32_t box[3] = {64, static_cast<cuuint32_t>(k.b.group), static_cast<cuuint32_t>(k.per_tile)};
   s = encode(&k.q, bf16, k.q_raw, 3, dims, strides, box, "q");
-  if (s == CS_OK) s = encode_cache(p, k.b, &k.k, k.k_raw, d.page_size, "k_cache");
-  if (s == CS_OK) s = encode_cache(p, k.b, &k.v, k.v_raw, d.page_size, "v_cache");
+  if (s == CS_OK) s = map_caches(k, p->page_map);
   if (s != CS_OK) return s;
   int smem = 0;
   const void* fn = attn_kernel(d, &smem);
@@ -422,6 +438,15 @@ cs_status cs_kv_plan(const cs_kv_desc* desc, cs_kv_t* out) {
   if (cudaMemset(p->ctrl, 0, p->ctrl_words * 4) != cudaSuccess || cudaDeviceSynchronize() != cudaSuccess) {
     free_plan(p);
     return cs_fail(CS_ERR_CUDA, "clearing the plan's workspace failed");
+  }
+  if (!driver().encode || !driver().replace) s = cs_fail(CS_ERR_CUDA, "the driver has no tensor maps (too old?)");
+  const cs_kv_batch none{};
+  const cskv::Batch geometry = device_batch(p, &none);
+  if (s == CS_OK) s = encode_cache(p->d, geometry, &p->page_map, p->part, p->d.page_size);
+  if (s == CS_OK) s = encode_cache(p->d, geometry, &p->slots_map, p->part, 16);
+  if (s != CS_OK) {
+    free_plan(p);
+    return s;
   }
   *out = p;
   return CS_OK;

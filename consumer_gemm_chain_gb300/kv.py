@@ -62,6 +62,17 @@ def _declare():
 _declare()
 
 
+# torch's current stream as an integer (what torch.cuda.current_stream().cuda_stream
+# gives, without the stream object: 0.1 us against 3.2 us on a Grace core)
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+
+
+def _stream(stream, device: int):
+    if stream is None and _raw_stream is not None:
+        return _raw_stream(device)
+    return _stream_ptr(stream)
+
+
 def _check(status: int, what: str) -> None:
     if status != CS_OK:
         raise CSError(status, what)
@@ -210,7 +221,7 @@ def cs_kv_append(plan: KVPlan, batch: KVBatch, qkv, q_out, k_cache, v_cache, rop
     if a.q_out == a.qkv and batch.tokens <= 1:
         a.q_stride = a.qkv_stride = plan.qkv_width  # one row: in place, whatever its stride
     _append_args(plan, batch, a, k_cache, v_cache, rope, positions)
-    _check(_lib.cs_kv_append(plan.handle, batch._ref, byref(a), _stream_ptr(stream)), "cs_kv_append")
+    _check(_lib.cs_kv_append(plan.handle, batch._ref, byref(a), _stream(stream, plan.device)), "cs_kv_append")
 
 
 def _kv_attn_args(plan, batch, q, k_cache, v_cache, out, lse):
@@ -227,7 +238,7 @@ def cs_kv_attention(plan: KVPlan, batch: KVBatch, q, k_cache, v_cache, out, lse=
     """Attention of the batch's new tokens over the cache: ``q`` and ``out`` [tokens, heads, head_dim],
     ``lse`` (optional) float32 [tokens, heads]."""
     a = _kv_attn_args(plan, batch, q, k_cache, v_cache, out, lse)
-    _check(_lib.cs_kv_attention(plan.handle, batch._ref, byref(a), _stream_ptr(stream)), "cs_kv_attention")
+    _check(_lib.cs_kv_attention(plan.handle, batch._ref, byref(a), _stream(stream, plan.device)), "cs_kv_attention")
 
 
 def cs_kv_attention_shared(plan: KVPlan, batch: KVBatch, q, k_cache, v_cache, prefix_pages, prefix_len: int, out, lse=None,
@@ -238,7 +249,7 @@ def cs_kv_attention_shared(plan: KVPlan, batch: KVBatch, q, k_cache, v_cache, pr
     if not isinstance(prefix_pages, torch.Tensor) or prefix_pages.dim() != 1 or prefix_pages.shape[0] < need:
         raise _bad("prefix_pages", prefix_pages, f"a 1-D int32 tensor of at least {need} pages")
     pp = _whole(prefix_pages, tuple(prefix_pages.shape), torch.int32, plan.device, "prefix_pages")
-    _check(_lib.cs_kv_attention_shared(plan.handle, batch._ref, pp, prefix_len, byref(a), _stream_ptr(stream)),
+    _check(_lib.cs_kv_attention_shared(plan.handle, batch._ref, pp, prefix_len, byref(a), _stream(stream, plan.device)),
            "cs_kv_attention_shared")
 
 
@@ -248,7 +259,7 @@ def cs_attn_cached_forward(chain: Plan, plan: KVPlan, batch: KVBatch, X, Wqkv, W
     args = _attn_args(chain, X, Wqkv, Wo, Y)
     a = plan._append
     _append_args(plan, batch, a, k_cache, v_cache, rope, positions)
-    _check(_lib.cs_attn_cached_forward(chain.handle, plan.handle, batch._ref, byref(args), byref(a), _stream_ptr(stream)),
+    _check(_lib.cs_attn_cached_forward(chain.handle, plan.handle, batch._ref, byref(args), byref(a), _stream(stream, plan.device)),
            "cs_attn_cached_forward")
 
 
