@@ -273,17 +273,19 @@ int rows_grid(const cs_kv_s* p) {
   return p->num_sms * cskv::ROWS_CTAS;
 }
 
-const void* attn_kernel(const cs_kv_desc& d, int* smem) {
-  *smem = d.head_dim == 128 ? cskv::AttnShape<128>::SMEM : cskv::AttnShape<64>::SMEM;
-  if (d.dtype == CS_BF16)
-    return d.head_dim == 128 ? (const void*)cskv::cs_kv_attn_kernel<__nv_bfloat16, 128>
-                             : (const void*)cskv::cs_kv_attn_kernel<__nv_bfloat16, 64>;
-  return d.head_dim == 128 ? (const void*)cskv::cs_kv_attn_kernel<__half, 128> : (const void*)cskv::cs_kv_attn_kernel<__half, 64>;
+template <typename T, int D>
+const void* attn_kernel_of(bool window) {
+  return window ? (const void*)cskv::cs_kv_attn_kernel<T, D, true> : (const void*)cskv::cs_kv_attn_kernel<T, D, false>;
 }
 
-// Up to 16 rows (tokens x query heads) of a sequence per key head are read by the rows
-// kernel, which is bound by the keys' bytes and has the shorter latency; more by the
-// tensor-core kernel.
+const void* attn_kernel(const cs_kv_desc& d, int* smem) {
+  *smem = d.head_dim == 128 ? cskv::AttnShape<128>::SMEM : cskv::AttnShape<64>::SMEM;
+  const bool window = d.window > 0 && d.window < kMaxKeys;
+  if (d.dtype == CS_BF16)
+    return d.head_dim == 128 ? attn_kernel_of<__nv_bfloat16, 128>(window) : attn_kernel_of<__nv_bfloat16, 64>(window);
+  return d.head_dim == 128 ? attn_kernel_of<__half, 128>(window) : attn_kernel_of<__half, 64>(window);
+}
+
 cs_status run_attention(cs_kv_s* p, cskv::AttnP& k, int max_rows, cudaStream_t st) {
   const cs_kv_desc& d = p->d;
   const bool bf16 = d.dtype == CS_BF16;

@@ -121,10 +121,11 @@ __device__ __forceinline__ bool elect_one() {
 
 // Bounded wait; false when it ran out, here or in another role.  What is waited
 // for is always work of this CTA, microseconds away; a try suspends the thread
-// for a while, so the limit is seconds.  (Kept small: with the slow path's timer and
-// error record inlined everywhere the kernel had 156 KB of code, and its warps
-// waited for instructions.)
-constexpr int WAIT_TRIES = 1 << 22;
+// for some microseconds, so the limit is a second or two.  (Kept small: with a slow path's
+// timer and error record inlined everywhere the kernel had 156 KB of code, and its
+// warps waited for instructions; with a suspend-time hint a prompt of 8192 tokens
+// took 410 us instead of 397.)
+constexpr int WAIT_TRIES = 1 << 18;
 template <typename Ctl>
 __device__ __forceinline__ bool wait(uint64_t* bar, uint32_t parity, Ctl* sc) {
 #pragma unroll 1
@@ -247,6 +248,27 @@ __device__ bool load_role(const AttnP& p, AttnCtl<AttnShape<D>::SLOTS>* sc, uint
   return true;
 }
 
+// Under a window: the key tiles of a segment of an item of two row tiles in which row
+// tile w sees a key, that is its leading sink tiles (k < sinks) and tiles a .. last; if there
+// is none, the segment's first, so that the rows' state exists.  (Without a window only an
+// item's last tile could be left out; that gained nothing.)
+struct Seen {
+  int first, last, sinks, a;
+  __device__ __forceinline__ Seen(const AttnP& p, const Seg& g, int w) {
+    const int tok = g.item * p.c.per_item + w * p.per_tile, base = g.s.m - g.s.n;
+    const int lo = max(0, base + tok - p.c.window + 1), end = base + min(g.s.n, tok + p.per_tile);
+    // (sinks that reach into the window's first tiles are no tiles of their own: k is the tile's place then)
+    sinks = (p.c.sinks + KT - 1) / KT;
+    a = g.sinks + lo / KT - g.lo / KT;
+    const int b = end > 0 ? g.sinks + (end - 1) / KT - g.lo / KT : -1;
+    first = g.k0 >= sinks ? max(g.k0, a) : g.k0;
+    last = min(g.k1 - 1, b);
+    if (last >= sinks && last < a) last = sinks - 1;
+    if (last < first) first = last = g.k0;
+  }
+  __device__ __forceinline__ int next(int k) const { return k + 1 >= sinks && k + 1 < a ? a : k + 1; }
+};
+
 // MMA warp w works for S buffer w: S = Q K^T, then, once the softmax has put P into the
 // first half of S, O += P V.  An item of two row tiles has one for each buffer; of an item
 // of one row tile the buffers take the key tiles in turn (and are joined at the end).
@@ -255,7 +277,7 @@ __device__ bool load_role(const AttnP& p, AttnCtl<AttnShape<D>::SLOTS>* sc, uint
 // buffer's warp is issuing: with one warp for both buffers a step of 1024 cycles took 2300.
 // A buffer's MMAs are issued by one thread and execute in that order, and no
 // MMA reads what the other buffer's write.
-template <int D>
+template <int D, bool WINDOW>
 __device__ bool mma_role(const AttnP& p, AttnCtl<AttnShape<D>::SLOTS>* sc, uint8_t* qbuf, uint8_t* ring, int bf16, int w) {
   using Sh = AttnShape<D>;
   const uint32_t idesc_s = cs::make_idesc_f16(bf16, 0, 128, KT);
@@ -299,58 +321,63 @@ __device__ bool mma_role(const AttnP& p, AttnCtl<AttnShape<D>::SLOTS>* sc, uint8
       for (int kk = 0; kk < 4; ++kk)
         mma_ts(o_tm, s_tm + h * 32 + kk * 8, b + kk * (Sh::HALVES * 2048 >> 4), idesc_o, add || kk > 0);
     };
-    bool issued = false;  // S of this tile was issued right behind the last P V
+    auto segment = [&](auto pair) {
+      constexpr bool TWO = decltype(pair)::value;  // an item of two row tiles
+      // this buffer's tiles: first, and then every one, every second one, or what is seen
+      const Seen seen(p, g, w);
+      const int first = TWO && WINDOW ? seen.first - g.k0 : TWO ? 0 : w;
+      const int last = TWO && WINDOW ? seen.last - g.k0 : TWO ? count - 1 : count - 1 - ((count - 1 - w) & 1);
+      int own = first;
+      bool issued = false;  // S of this tile was issued right behind the last P V
 #pragma unroll 1
-    for (int t = 0; ok && t < count; ++t) {
-      const int next = t + (two ? 1 : 2);  // this warp's next tile
-      if (!two && (t & 1) != w) {
-        for (int i = 0; ok && i < 2; ++i) {
-          ok = wait_warp(&sc->full[r.slot], r.phase, sc);
-          if (leader && ok) cs::mbar_arrive(&sc->empty[r.slot]);
+      for (int t = 0; t < count; ++t) {
+        if ((!TWO || WINDOW) && t != own) {
+          for (int i = 0; i < 2; ++i) {
+            if (!wait_warp(&sc->full[r.slot], r.phase, sc)) return false;
+            if (leader) cs::mbar_arrive(&sc->empty[r.slot]);
+            r.next();
+          }
+          continue;
+        }
+        if (!issued) {
+          if (!wait_warp(&sc->full[r.slot], r.phase, sc)) return false;
+          cs::tc_fence_after();
+          if (leader) scores(r.slot, t == last);
           r.next();
         }
-        continue;
-      }
-      if (!issued) {
-        ok = wait_warp(&sc->full[r.slot], r.phase, sc);
-        if (!ok) break;
-        cs::tc_fence_after();
-        if (leader) scores(r.slot, next >= count);
+        if (!wait_warp(&sc->full[r.slot], r.phase, sc)) return false;
+        const int sv = r.slot;
         r.next();
-      }
-      ok = wait_warp(&sc->full[r.slot], r.phase, sc);
-      if (!ok) break;
-      const int sv = r.slot;
-      r.next();
-      if (leader) cs::mbar_arrive(&sc->v_ready[w]);
-      // with the next tile's keys there, nothing comes between this P V and its S
-      issued = two && next < count && __all_sync(0xFFFFFFFFu, cs::mbar_test_wait(&sc->full[r.slot], r.phase));
-      const int sk = r.slot;
-      const bool add = t >= (two ? 1 : 2);
-      ok = wait_warp(&sc->p_full[w][0], p_phase, sc);  // the weights of the first 64 keys come before the rest
-      if (!ok) break;
-      cs::tc_fence_after();
-      if (leader) values(sv, 0, add);
-      ok = wait_warp(&sc->p_full[w][1], p_phase, sc);
-      if (!ok) break;
-      cs::tc_fence_after();
-      if (leader) {
-        // one buffer's twelve MMAs after the other's: issued side by side, both S would
-        // be done late, both softmaxes run at a time, and the tensor core wait for them
-        // (64 dimensions: an MMA of P V takes half the time and the softmax bounds the rest;
-        // taking turns cost 4 %)
-        if (D == 128 && issued) take_turn(sc);
-        values(sv, 1, true);
-        if (issued) {
-          scores(sk, next + 1 >= count);
-          if (D == 128) atomicExch(&sc->turn, 0);
+        if (leader) cs::mbar_arrive(&sc->v_ready[w]);
+        own = t == last ? -1 : !TWO ? t + 2 : WINDOW ? seen.next(t + g.k0) - g.k0 : t + 1;
+        // with the next tile's keys there, nothing comes between this P V and its S
+        issued = TWO && t != last && (!WINDOW || own == t + 1) &&
+                 __all_sync(0xFFFFFFFFu, cs::mbar_test_wait(&sc->full[r.slot], r.phase));
+        const int sk = r.slot;
+        if (!wait_warp(&sc->p_full[w][0], p_phase, sc)) return false;  // the weights of the first 64 keys come before the rest
+        cs::tc_fence_after();
+        if (leader) values(sv, 0, t != first);
+        if (!wait_warp(&sc->p_full[w][1], p_phase, sc)) return false;
+        cs::tc_fence_after();
+        if (leader) {
+          // one buffer's twelve MMAs after the other's: issued side by side, both S would
+          // be done late, both softmaxes run at a time, and the tensor core wait for them
+          // (64 dimensions: an MMA of P V takes half the time and the softmax bounds the rest)
+          if (D == 128 && issued) take_turn(sc);
+          values(sv, 1, true);
+          if (issued) {
+            scores(sk, t + 1 == last);
+            if (D == 128) atomicExch(&sc->turn, 0);
+          }
+          cs::tc_commit<1>(&sc->empty[sv]);
+          if (t == last) cs::tc_commit<1>(&sc->o_full[w]);
         }
-        cs::tc_commit<1>(&sc->empty[sv]);
-        if (next >= count) cs::tc_commit<1>(&sc->o_full[w]);
+        p_phase ^= 1u;
+        if (issued) r.next();
       }
-      p_phase ^= 1u;
-      if (issued) r.next();
-    }
+      return true;
+    };
+    ok = two ? segment(std::true_type()) : segment(std::false_type());
   }
   if (leader) cs::tc_commit<1>(&sc->drained);  // all MMAs of this warp are done
   return ok;
@@ -428,7 +455,7 @@ __device__ __forceinline__ void st32(void* p, const uint32_t* v) {
 __device__ __forceinline__ uint32_t below(int n) { return n >= 32 ? 0xFFFFFFFFu : n <= 0 ? 0u : (1u << n) - 1u; }
 
 // Warpgroup w: the softmax of the steps with S buffer w, one row per thread, and the output.
-template <typename T, int D>
+template <typename T, int D, bool WINDOW>
 __device__ bool softmax_role(const AttnP& p, AttnCtl<AttnShape<D>::SLOTS>* sc, uint8_t* ring, int w) {
   using Sh = AttnShape<D>;
   constexpr int CH = D / 32;                                      // chunks of 32 columns of O
@@ -460,18 +487,20 @@ __device__ bool softmax_role(const AttnP& p, AttnCtl<AttnShape<D>::SLOTS>* sc, u
     const int tok = first + row_tok;
     const bool live = row_tok < p.per_tile && tok < g.s.n;
     const int end = p.c.flat ? g.s.m : live ? base + tok + 1 : 0;  // keys [.., end) are seen
-    const int lo = p.c.window > 0 ? max(0, base + tok + 1 - p.c.window) : 0;
+    const int lo = WINDOW ? max(0, base + tok + 1 - p.c.window) : 0;
     // keys below `some` and from `all_lo` on are seen by every live row
     const int some = p.c.flat ? g.s.m : base + first + 1;
-    const int all_lo = p.c.window > 0 ? max(0, base + first + p.per_tile - p.c.window) : 0;
+    const int all_lo = WINDOW ? max(0, base + first + p.per_tile - p.c.window) : 0;
     float m_ref = -INFINITY, l = 0.0f;
 #pragma unroll 1
-    for (int k = g.k0 + (two ? 0 : w); k < g.k1; k += two ? 1 : 2) {
+    const Seen seen(p, g, w);
+    const int k_first = two ? WINDOW ? seen.first : g.k0 : g.k0 + w, k_end = WINDOW && two ? seen.last + 1 : g.k1;
+    for (int k = k_first; k < k_end; k = WINDOW && two ? seen.next(k) : k + (two ? 1 : 2)) {
       // what the tile needs, known before its scores are there
-      const bool fresh = k - g.k0 < (two ? 1 : 2);  // O of this buffer holds nothing yet
-      const int j0 = g.key0(p.c, k);
-      const bool mask = !(j0 + KT <= some && (j0 >= all_lo || j0 + KT <= p.c.sinks));  // some key is hidden from some row
-      const bool unseen = j0 + KT > g.hi || (j0 < g.lo && j0 + KT > p.c.sinks);       // from every row of the item
+      const bool fresh = k == k_first;  // O of this buffer holds nothing yet
+      const int j0 = WINDOW ? g.key0(p.c, k) : k * KT;
+      const bool mask = !(j0 + KT <= some && (!WINDOW || j0 >= all_lo || j0 + KT <= p.c.sinks));  // some key is hidden from some row
+      const bool unseen = j0 + KT > g.hi || (WINDOW && j0 < g.lo && j0 + KT > p.c.sinks);       // from every row of the item
       if (!wait_warp(&sc->s_full[w], s_phase, sc)) return false;
       s_phase ^= 1u;
       cs::tc_fence_after();
@@ -479,7 +508,7 @@ __device__ bool softmax_role(const AttnP& p, AttnCtl<AttnShape<D>::SLOTS>* sc, u
 #pragma unroll 1
         for (int c = 0; c < 4; ++c) {  // hidden scores become -inf in place
           const int j1 = j0 + 32 * c;
-          const uint32_t seen = below(end - j1) & (~below(lo - j1) | below(p.c.sinks - j1));
+          const uint32_t seen = below(end - j1) & (WINDOW ? ~below(lo - j1) | below(p.c.sinks - j1) : 0xFFFFFFFFu);
           uint32_t v[32];
           cs::tmem_ld32(s_tm + c * 32, v);
           cs::tc_wait_ld();
@@ -510,7 +539,7 @@ __device__ bool softmax_role(const AttnP& p, AttnCtl<AttnShape<D>::SLOTS>* sc, u
       const bool raise = m_tile > m_ref + RAISE_LOG2 || (m_ref == -INFINITY && m_tile > -INFINITY);
       const float m_new = raise ? m_tile : m_ref;
       if (__builtin_expect(!fresh && __any_sync(0xFFFFFFFFu, raise), 0)) {
-        // S of this step was issued after P V of the buffer's last one: O is complete
+        // S of this tile was issued after P V of the buffer's last one: O is complete
         const float f = raise ? cs::ex2_approx(m_ref - m_new) : 1.0f;
         l *= f;
 #pragma unroll 1
@@ -529,7 +558,7 @@ __device__ bool softmax_role(const AttnP& p, AttnCtl<AttnShape<D>::SLOTS>* sc, u
         const uint32_t slot = (ring0 + 2 * (k - g.k0) + 1) % Sh::SLOTS;
         if (!wait_warp(&sc->v_ready[w], s_phase ^ 1u, sc)) return false;
         const int j = j0 + r;
-        if (j >= g.hi || (j < g.lo && j >= p.c.sinks)) {
+        if (j >= g.hi || (WINDOW && j < g.lo && j >= p.c.sinks)) {
           uint8_t* row = ring + slot * Sh::TILE + (r >> 3) * (Sh::HALVES * 1024) + (r & 7) * 128;
           for (int h = 0; h < Sh::HALVES; ++h)
 #pragma unroll
@@ -762,7 +791,9 @@ __global__ void __launch_bounds__(JOIN_THREADS) cs_kv_join_kernel(const __grid_c
   }
 }
 
-template <typename T, int D>
+// WINDOW: whether keys may be hidden behind a row's window (without, what deals with it is
+// not in the code of the inner loops)
+template <typename T, int D, bool WINDOW>
 __global__ void __launch_bounds__(ATTN_THREADS, 1) cs_kv_attn_kernel(const __grid_constant__ AttnP p) {
   using Sh = AttnShape<D>;
   using Ctl = AttnCtl<Sh::SLOTS>;
@@ -809,11 +840,11 @@ __global__ void __launch_bounds__(ATTN_THREADS, 1) cs_kv_attn_kernel(const __gri
   constexpr int bf16 = sizeof(T) == 2 && !std::is_same<T, __half>::value;
   if (warp < 8) {
     regs_inc<SOFTMAX_REGS>();
-    softmax_role<T, D>(p, sc, ring, warp >> 2);
+    softmax_role<T, D, WINDOW>(p, sc, ring, warp >> 2);
   } else {
     regs_dec<OTHER_REGS>();
     if (warp == 8) load_role<D>(p, sc, qbuf, ring);
-    if (warp == 9 || warp == 10) mma_role<D>(p, sc, qbuf, ring, bf16, warp - 9);
+    if (warp == 9 || warp == 10) mma_role<D, WINDOW>(p, sc, qbuf, ring, bf16, warp - 9);
   }
   __syncwarp();
   cs::tc_fence_before();
