@@ -27,6 +27,7 @@ struct cs_kv_s {
   float* part = nullptr;    // pieces of items that several CTAs share
   float4* other = nullptr;  // halves of items inside a CTA
   cskv::Split* splits = nullptr;
+  uint8_t* mend = nullptr;  // rows to be computed again
   float* flat_o = nullptr;  // desc.shared: the prefix's output and log-sum-exp
   // copies of a cache (its address is put in by each call): a whole page's slots of a
   // head, and 16 slots
@@ -242,6 +243,7 @@ cs_status check_attn(const cs_kv_s* p, const cs_kv_batch* b, const cs_kv_attn_ar
   k.other = p->other;
   k.splits = p->splits;
   k.num_splits = p->num_sms;
+  k.mend = p->mend;
   k.arrivals = p->ctrl + cskv::CTRL_COUNTERS;
   k.q_raw = a->q;
   k.k_raw = a->k_cache;
@@ -295,7 +297,12 @@ cs_status run_attention(cs_kv_s* p, cskv::AttnP& k, int max_rows, cudaStream_t s
     k.c.per_item = cskv::ROWS / k.b.group;
     k.c.shift = cskv::ROWS_SHIFT;
     if ((s = map_caches(k, p->slots_map)) != CS_OK) return s;
-    return launch(rows_kernel(d), dim3(rows_grid(p)), cskv::ROWS_THREADS, rows_smem(d), &k, st);
+    s = launch(rows_kernel(d), dim3(rows_grid(p)), cskv::ROWS_THREADS, rows_smem(d), &k, st);
+    if (s != CS_OK || max_rows <= k.b.group || k.c.flat) return s;
+    k.num_splits = 0;  // rows of several tokens: some may have to be mended
+    s = launch(join_kernel(d), dim3(p->num_sms), cskv::JOIN_THREADS, 0, &k, st);
+    k.num_splits = p->num_sms;
+    return s;
   }
   k.per_tile = 128 / k.b.group;
   k.c.per_item = 2 * k.per_tile;
@@ -377,6 +384,7 @@ void free_plan(cs_kv_s* p) {
   cudaFree(p->part);
   cudaFree(p->other);
   cudaFree(p->splits);
+  cudaFree(p->mend);
   cudaFree(p->flat_o);
   delete p;
 }
@@ -427,17 +435,20 @@ cs_status cs_kv_plan(const cs_kv_desc* desc, cs_kv_t* out) {
   const size_t part = static_cast<size_t>(p->num_sms) * 4 * 128 * (desc->head_dim + 8) * 4;
   static_assert(cskv::ROWS_CTAS * 2 * cskv::ROWS * (64 + 2) <= 4 * 128 * (64 + 8), "workspace");
   const size_t other = static_cast<size_t>(p->num_sms) * (desc->head_dim / 4 + 1) * 128 * 16;
-  const size_t flat = static_cast<size_t>(desc->max_tokens) * desc->heads * (desc->head_dim + 1) * 4;
+  const size_t rows = static_cast<size_t>(desc->max_tokens) * desc->heads;
+  const size_t flat = rows * (desc->head_dim + 1) * 4;
   if (cudaMalloc(reinterpret_cast<void**>(&p->ctrl), p->ctrl_words * 4) != cudaSuccess ||
       cudaMalloc(reinterpret_cast<void**>(&p->part), part) != cudaSuccess ||
       cudaMalloc(reinterpret_cast<void**>(&p->other), other) != cudaSuccess ||
+      cudaMalloc(reinterpret_cast<void**>(&p->mend), rows) != cudaSuccess ||
       cudaMalloc(reinterpret_cast<void**>(&p->splits), p->num_sms * sizeof(cskv::Split)) != cudaSuccess ||
       (desc->shared && cudaMalloc(reinterpret_cast<void**>(&p->flat_o), flat) != cudaSuccess)) {
     cudaGetLastError();
     free_plan(p);
     return cs_fail(CS_ERR_OOM, "cudaMalloc of the plan's workspace failed");
   }
-  if (cudaMemset(p->ctrl, 0, p->ctrl_words * 4) != cudaSuccess || cudaDeviceSynchronize() != cudaSuccess) {
+  if (cudaMemset(p->ctrl, 0, p->ctrl_words * 4) != cudaSuccess || cudaMemset(p->mend, 0, rows) != cudaSuccess ||
+      cudaDeviceSynchronize() != cudaSuccess) {
     free_plan(p);
     return cs_fail(CS_ERR_CUDA, "clearing the plan's workspace failed");
   }
@@ -566,6 +577,7 @@ cs_status cs_kv_reset(cs_kv_t p) {
   DeviceGuard g(p->device);
   KV_CUDA(cudaDeviceSynchronize());
   KV_CUDA(cudaMemset(p->ctrl, 0, p->ctrl_words * 4));
+  KV_CUDA(cudaMemset(p->mend, 0, static_cast<size_t>(p->d.max_tokens) * p->d.heads));
   KV_CUDA(cudaDeviceSynchronize());
   p->error_latched = false;
   return CS_OK;

@@ -23,8 +23,9 @@ struct Batch {
   uint32_t* ctrl;
 };
 
-// ctrl words: first device error (cs_status), what did not fit, and its index
-enum : int { CTRL_ERROR = 0, CTRL_WHAT = 1, CTRL_INDEX = 2, CTRL_COUNTERS = 16 };
+// ctrl words: first device error (cs_status), what did not fit, and its index; whether rows
+// are to be mended (cs_kv_join_kernel), and the blocks that are through with it
+enum : int { CTRL_ERROR = 0, CTRL_WHAT = 1, CTRL_INDEX = 2, CTRL_MEND = 3, CTRL_MENDED = 4, CTRL_COUNTERS = 16 };
 enum : uint32_t { WHAT_LENGTHS = 1, WHAT_PAGE = 2, WHAT_POSITION = 3, WHAT_WAIT = 4 };
 constexpr uint32_t ERR_INVALID = 1, ERR_WATCHDOG = 6;  // cs_status values
 

@@ -36,6 +36,7 @@ struct AttnP {
   Split* splits;          // [CTA] the item that starts there and ends elsewhere
   int num_splits;
   uint32_t* arrivals;     // cs_kv_rows_kernel: [CTA] its pieces that are stored
+  uint8_t* mend;          // [tokens][heads]: the row is to be computed again (mend_row)
   float* flat_o;          // [tokens][heads][D], [tokens][heads]: a prefix's normalised output and
   float* flat_lse;        // base-2 log-sum-exp; written with c.flat, else joined in if not null
   int per_tile;           // tokens of a 128-row tile: 128 / group, rounded down; an item has two
@@ -431,6 +432,15 @@ __device__ __forceinline__ void put_lse(const AttnP& p, long long row, float lse
     p.lse[row] = lse2 * 0.6931471805599453f;
 }
 
+// A row whose weights are finite and whose output is not: some value of its tiles is
+// not, maybe one at a key that is hidden from this row only (its weight 0 times NaN or
+// infinity is NaN).  The row is computed again from its visible keys alone.
+__device__ __forceinline__ void mark(const AttnP& p, long long row) {
+  if (p.c.flat) return;  // no key is hidden from one row and seen by another
+  p.mend[row] = 1;
+  p.b.ctrl[CTRL_MEND] = 1;
+}
+
 // x += f * the 32 values of 8 float4s `stride` apart (written by this grid or an earlier one).
 __device__ __forceinline__ void axpy(float (&x)[32], const float4* src, int stride, float f) {
   float4 y[8];
@@ -654,13 +664,17 @@ __device__ bool softmax_role(const AttnP& p, AttnCtl<AttnShape<D>::SLOTS>* sc, u
       f_other *= inv;
       fold *= inv;
     }
+    float probe = 0.0f;  // NaN if an element of the row is not finite
 #pragma unroll 1
     for (int c = 0; c < CH; ++c) {
       float x[32];
       uint32_t o[32];
       read_o(c, o);
 #pragma unroll
-      for (int t = 0; t < 32; ++t) x[t] = __uint_as_float(o[t]) * f;
+      for (int t = 0; t < 32; ++t) {
+        x[t] = __uint_as_float(o[t]) * f;
+        probe = fmaf(x[t], 0.0f, probe);
+      }
       if (other) axpy(x, other + c * 8 * 128, 128, f_other);
       if (!live) continue;
       if (pre) axpy(x, pre + c * 8, 1, fold);
@@ -688,7 +702,10 @@ __device__ bool softmax_role(const AttnP& p, AttnCtl<AttnShape<D>::SLOTS>* sc, u
     cs::tc_fence_before();
     if (!two && count > 1) cs::mbar_arrive(&sc->other_empty);  // the other buffer's state is read
     if (whole) {
-      if (live) put_lse(p, row, l == 0.0f ? -INFINITY : m_ref + log2f(l));
+      if (live) {
+        put_lse(p, row, l == 0.0f ? -INFINITY : m_ref + log2f(l));
+        if (probe != 0.0f && isfinite(l)) mark(p, row);
+      }
     } else {
       if (live) *reinterpret_cast<float2*>(to + D) = make_float2(m_ref, l);
       if (threadIdx.x == 0 && sc->range.x0 <= g.x) {  // the item starts here: what its joining needs to know
@@ -708,9 +725,78 @@ __device__ bool softmax_role(const AttnP& p, AttnCtl<AttnShape<D>::SLOTS>* sc, u
   return true;
 }
 
+// One warp: the output of a token and head from its visible keys alone, one key after
+// another with the running maximum.
+template <typename T, int D>
+__device__ __noinline__ void mend_row(const AttnP& p, int t, int h) {
+  const Batch& B = p.b;
+  const int lane = threadIdx.x & 31, b = sequence_of(B, t);
+  int t0, n, m;
+  if (!sequence(B, b, t0, n, m) || t < t0 || t >= t0 + n) return;
+  const int pos = m - n + t - t0, kh = h / B.group;
+  constexpr int W = D / 64;  // 32-bit words per lane
+  float q[2 * W], o[2 * W] = {}, mx = -INFINITY, l = 0.0f;
+  const uint32_t* qr = reinterpret_cast<const uint32_t*>(static_cast<const T*>(p.q_raw) + t * p.q_stride + h * D);
+#pragma unroll
+  for (int w = 0; w < W; ++w) {
+    const float2 v = Pair<T>::get(qr[lane + 32 * w]);
+    q[2 * w] = v.x, q[2 * w + 1] = v.y;
+  }
+  const int* pages = B.table + static_cast<long long>(b) * B.table_cols;
+  const int lo = p.c.window > 0 ? max(0, pos - p.c.window + 1) : 0, sinks = min(p.c.sinks, lo);
+  for (int i = 0; i < sinks + pos + 1 - lo; ++i) {  // the sinks, then the window
+    const int j = i < sinks ? i : lo + i - sinks;
+    const int page = __ldg(pages + (j >> B.page_shift));
+    if (page < 0 || page >= B.num_pages) continue;
+    const long long at = page * B.page_stride + (j & (B.page_size - 1)) * B.slot_stride + kh * B.head_stride;
+    const uint32_t* kr = reinterpret_cast<const uint32_t*>(static_cast<const T*>(p.k_raw) + at);
+    const uint32_t* vr = reinterpret_cast<const uint32_t*>(static_cast<const T*>(p.v_raw) + at);
+    float s = 0.0f;
+#pragma unroll
+    for (int w = 0; w < W; ++w) {
+      const float2 k = Pair<T>::get(kr[lane + 32 * w]);
+      s = fmaf(q[2 * w], k.x, fmaf(q[2 * w + 1], k.y, s));
+    }
+#pragma unroll
+    for (int d = 16; d; d >>= 1) s += __shfl_xor_sync(0xFFFFFFFFu, s, d);
+    s *= p.scale_log2;
+    const float top = fmaxf(mx, s);
+    const float f = mx == -INFINITY ? 0.0f : exp2f(mx - top), e = s == -INFINITY ? 0.0f : exp2f(s - top);
+    l = l * f + e;
+#pragma unroll
+    for (int w = 0; w < W; ++w) {
+      const float2 v = Pair<T>::get(vr[lane + 32 * w]);
+      o[2 * w] = fmaf(o[2 * w], f, e * v.x), o[2 * w + 1] = fmaf(o[2 * w + 1], f, e * v.y);
+    }
+    mx = top;
+  }
+  const long long row = static_cast<long long>(t) * B.heads + h;
+  float fold = 0.0f, f = 1.0f;
+  if (p.flat_o) {
+    const float z = p.flat_lse[row], top = fmaxf(mx, z);
+    f = mx == -INFINITY ? 0.0f : exp2f(mx - top);
+    fold = z == -INFINITY ? 0.0f : exp2f(z - top);
+    l = l * f + fold;
+    mx = top;
+  }
+  const float inv = l == 0.0f ? 0.0f : 1.0f / l;
+  uint32_t* dst = reinterpret_cast<uint32_t*>(static_cast<T*>(p.out) + t * p.out_stride + h * D);
+#pragma unroll
+  for (int w = 0; w < W; ++w) {
+    float x = o[2 * w] * f, y = o[2 * w + 1] * f;
+    if (fold != 0.0f) {
+      const float2 v = *reinterpret_cast<const float2*>(p.flat_o + row * D + 2 * (lane + 32 * w));
+      x = fmaf(v.x, fold, x), y = fmaf(v.y, fold, y);
+    }
+    dst[lane + 32 * w] = Pair<T>::put(x * inv, y * inv);
+  }
+  if (lane == 0) put_lse(p, row, l == 0.0f ? -INFINITY : mx + log2f(l));
+}
+
 // Joins the pieces of the items that several CTAs of cs_kv_attn_kernel share, a row to a
 // warp, D / 32 dimensions to a lane.  A kernel of its own, because one SM joining ten
-// pieces of 256 rows took 20 us and more while the others were done.
+// pieces of 256 rows took 20 us and more while the others were done.  Then it mends the rows
+// that were marked.
 constexpr int JOIN_THREADS = 256;  // at least the grid of cs_kv_attn_kernel
 template <typename T, int D>
 __global__ void __launch_bounds__(JOIN_THREADS) cs_kv_join_kernel(const __grid_constant__ AttnP p) {
@@ -788,6 +874,27 @@ __global__ void __launch_bounds__(JOIN_THREADS) cs_kv_join_kernel(const __grid_c
       for (int w = 0; w < W; w += 2) dst[w / 2] = Pair<T>::put(x[w] * inv, x[w + 1] * inv);
     }
     if (lane == 0) put_lse(p, row, l == 0.0f ? -INFINITY : m + log2f(l));
+    float probe = 0.0f;
+#pragma unroll
+    for (int w = 0; w < W; ++w) probe = fmaf(x[w], 0.0f, probe);
+    if (!p.c.flat && __any_sync(0xFFFFFFFFu, probe != 0.0f) && isfinite(l)) {
+      __syncwarp();
+      mend_row<T, D>(p, static_cast<int>(tok), sp.kvh * B.group + h);
+    }
+  }
+  if (p.c.flat || __ldcg(&B.ctrl[CTRL_MEND]) == 0) return;
+  const long long all = static_cast<long long>(B.tokens) * B.heads;
+  for (long long n = static_cast<long long>(blockIdx.x) * (JOIN_THREADS / 32) + warp; n < all;
+       n += gridDim.x * (JOIN_THREADS / 32)) {
+    if (p.mend[n] == 0) continue;
+    __syncwarp();
+    mend_row<T, D>(p, static_cast<int>(n / B.heads), static_cast<int>(n % B.heads));
+    if (lane == 0) p.mend[n] = 0;
+  }
+  __syncthreads();
+  if (tid == 0 && atomicAdd(&B.ctrl[CTRL_MENDED], 1u) == gridDim.x - 1) {  // every block has read the flag
+    B.ctrl[CTRL_MENDED] = 0;
+    B.ctrl[CTRL_MEND] = 0;
   }
 }
 

@@ -291,6 +291,7 @@ __global__ void __launch_bounds__(ROWS_THREADS, ROWS_CTAS) cs_kv_rows_kernel(con
         m = top;
       }
       const float y = l == 0.0f ? 0.0f : x / l;
+      if (!isfinite(x) && isfinite(l) && g.s.n > 1) mark(p, row);  // several tokens: keys hidden from one only
       const float lse2 = l == 0.0f ? -INFINITY : m + log2f(l);
       if (p.c.flat) {
         p.flat_o[row * D + d] = y;

@@ -127,6 +127,55 @@ def test_many_sequences():
     run(Batch(q, [n + int(x) for n, x in zip(q, r.integers(0, 60, 300))], 4, 2, 64, BF16))
 
 
+@pytest.mark.parametrize("q,kv", [([4, 1], [70, 9]), ([3], [900]), ([200, 30], [300, 30]), ([130], [2000])])
+@pytest.mark.parametrize("window,prefix", [(0, 0), (33, 0), (0, 50)])
+def test_values_that_are_not_finite_at_keys_hidden_from_some_rows(q, kv, window, prefix):
+    """NaN and infinities at keys that only later tokens (or, under a window, only earlier
+    ones) see: every other row is as if they were not there, and those rows are NaN."""
+    for dtype, bad in ((BF16, math.nan), (F16, math.inf)):
+        b = Batch(q, kv, 8, 2, 128, dtype, window=window, sinks=2 if window else 0, prefix=prefix, seed=kv[0])
+        spoilt = []  # (sequence, key): seen by the last token only, and by the first only
+        for s, (n, m) in enumerate(zip(q, kv)):
+            spoilt.append((s, m - 1))
+            if window and m - n - window + 1 >= 2 and n > 1:
+                spoilt.append((s, m - n - window + 1))
+        for s, j in spoilt:
+            page, slot = int(b.table[s, j // 16]), j % 16
+            b.vc[page, slot, :, 5:9] = bad
+            b.v[s][j, :, 5:9] = 0.0  # rows that do not see it never read it
+        d = Device(b)
+        for _ in range(2):  # the marks of the first call are cleared
+            d.out.fill_(7), d.lse.fill_(7)
+            d.attend()
+        d.ok()
+        ref, lse, bound = b.reference()
+        got, t = okv.to64(d.out), 0
+        assert np.abs(okv.to64(d.lse) - lse).max() <= 2.0 ** -11 + 2.0 ** -20 * np.abs(lse).max()
+        for s, (n, m) in enumerate(zip(q, kv)):
+            for i in range(n):
+                p = m - n + i
+                hit = any(x == s and j <= p and (not window or j > p - window) for x, j in spoilt)
+                ok = np.ones(128, dtype=bool)
+                ok[5:9] = not hit
+                assert (np.abs(got[t, :, ok] - ref[t, :, ok]) <= bound[t, :, ok]).all(), (s, i)
+                assert not hit or not np.isfinite(got[t, :, 5:9]).any(), (s, i)
+                t += 1
+
+
+@pytest.mark.parametrize("q,kv", [([4], [70]), ([200], [300])])
+def test_keys_that_are_not_finite_where_hidden(q, kv):
+    b = Batch(q, kv, 8, 2, 64, BF16)
+    n, m = q[0], kv[0]
+    page, slot = int(b.table[0, (m - 1) // 16]), (m - 1) % 16
+    b.kc[page, slot] = math.nan
+    d = Device(b)
+    d.attend()
+    d.ok()
+    ref, _, bound = b.reference(list(range(n - 1)))
+    got = okv.to64(d.out)
+    assert (np.abs(got[:n - 1] - ref) <= bound).all() and np.isnan(got[n - 1]).all()
+
+
 def test_large_scores():
     """Rows whose maximum keeps rising by much, and weights far below the row's largest."""
     for n in (1, 200):
