@@ -20,7 +20,18 @@ struct Cut {
   int flat_len;
 };
 
-__device__ __forceinline__ int kt(const Cut& C) { return 1 << C.shift; }
+#define CS_KV_BOTH __host__ __device__ __forceinline__  // the division's arithmetic also runs in a host test
+
+template <typename A>
+CS_KV_BOTH A kv_min(A a, A b) {
+  return b < a ? b : a;
+}
+template <typename A>
+CS_KV_BOTH A kv_max(A a, A b) {
+  return a < b ? b : a;
+}
+
+CS_KV_BOTH int kt(const Cut& C) { return 1 << C.shift; }
 
 struct Seq {
   int t0, n, m;
@@ -40,24 +51,24 @@ __device__ __forceinline__ bool load_seq(const Batch& B, const Cut& C, int b, Se
 
 // First key of the window of the item's first token (0 without a window), and the
 // end of the keys that its last token sees.
-__device__ __forceinline__ int item_lo(const Cut& C, const Seq& s, int item) {
-  return C.window > 0 ? max(0, s.m - s.n + item * C.per_item - C.window + 1) : 0;
+CS_KV_BOTH int item_lo(const Cut& C, const Seq& s, int item) {
+  return C.window > 0 ? kv_max(0, s.m - s.n + item * C.per_item - C.window + 1) : 0;
 }
-__device__ __forceinline__ int item_hi(const Cut& C, const Seq& s, int item) {
-  return C.flat ? s.m : max(0, s.m - s.n + min(s.n, (item + 1) * C.per_item));
+CS_KV_BOTH int item_hi(const Cut& C, const Seq& s, int item) {
+  return C.flat ? s.m : kv_max(0, s.m - s.n + kv_min(s.n, (item + 1) * C.per_item));
 }
 // Tiles of the sinks before the window's first tile.
-__device__ __forceinline__ int sink_tiles(const Cut& C, int lo) { return min((C.sinks + kt(C) - 1) >> C.shift, lo >> C.shift); }
+CS_KV_BOTH int sink_tiles(const Cut& C, int lo) { return kv_min((C.sinks + kt(C) - 1) >> C.shift, lo >> C.shift); }
 // Key tiles of an item; at least one, so that rows without keys are written too.
-__device__ __forceinline__ int item_tiles(const Cut& C, const Seq& s, int item) {
+CS_KV_BOTH int item_tiles(const Cut& C, const Seq& s, int item) {
   const int lo = item_lo(C, s, item), hi = item_hi(C, s, item);
-  return ((max(1, hi) + kt(C) - 1) >> C.shift) - (lo >> C.shift) + sink_tiles(C, lo);
+  return ((kv_max(1, hi) + kt(C) - 1) >> C.shift) - (lo >> C.shift) + sink_tiles(C, lo);
 }
-__device__ __forceinline__ int items_of(const Cut& C, const Seq& s) { return (s.n + C.per_item - 1) / C.per_item; }
+CS_KV_BOTH int items_of(const Cut& C, const Seq& s) { return (s.n + C.per_item - 1) / C.per_item; }
 
 // sum over i < n of floor((a i + b) / m), a, b >= 0 (the Euclid-like recurrence for
 // lattice points under a line); m a + m fits 32 bits times n
-__device__ __forceinline__ unsigned long long floor_sum(unsigned n, unsigned m, unsigned a, unsigned b) {
+CS_KV_BOTH unsigned long long floor_sum(unsigned n, unsigned m, unsigned a, unsigned b) {
   unsigned long long ans = 0;
 #pragma unroll 1
   while (n > 0) {
@@ -76,20 +87,20 @@ __device__ __forceinline__ unsigned long long floor_sum(unsigned n, unsigned m, 
 
 // Units of the first k items of a sequence (of one key head): their key tiles, and
 // item_cost for each.
-__device__ __forceinline__ unsigned long long units_before(const Cut& C, const Seq& s, int k) {
+CS_KV_BOTH unsigned long long units_before(const Cut& C, const Seq& s, int k) {
   if (k == 0) return 0;
   if (C.flat) return static_cast<unsigned long long>(k) * static_cast<unsigned>(item_tiles(C, s, 0) + C.item_cost);
-  const int full = min(k, items_of(C, s) - 1);  // the last item may hold fewer tokens
+  const int full = kv_min(k, items_of(C, s) - 1);  // the last item may hold fewer tokens
   unsigned long long sum = static_cast<unsigned long long>(k) * C.item_cost;
   if (k > full) sum += item_tiles(C, s, full);
   if (full > 0) {
     const int base = s.m - s.n, P = C.per_item;
     // sum of ceil(max(1, base + (i + 1) P) / tile)
-    const int early = base < 0 ? min(full, -base / P) : 0;
+    const int early = base < 0 ? kv_min(full, -base / P) : 0;
     sum += early + floor_sum(full - early, kt(C), P, base + (early + 1) * P + kt(C) - 1);
     if (C.window > 0) {
       // minus what lies between the sinks' tiles and the window's first tile
-      const int b2 = base - C.window + 1 - (C.sinks + kt(C) - 1) >> C.shift << C.shift;
+      const int b2 = base - C.window + 1 - (((C.sinks + kt(C) - 1) >> C.shift) << C.shift);
       const int k2 = b2 >= 0 ? 0 : (-b2 + P - 1) / P;
       if (full > k2) sum -= floor_sum(full - k2, kt(C), P, b2 + k2 * P);
     }
@@ -141,7 +152,7 @@ struct Walk {
       const unsigned long long left = x1 - x;
       const int to = static_cast<unsigned long long>(units - off) <= left ? units : off + static_cast<int>(left);
       g.x = x - off + C.item_cost;
-      g.k0 = max(0, off - C.item_cost);
+      g.k0 = kv_max(0, off - C.item_cost);
       g.k1 = to - C.item_cost;
       g.item = item;
       x += to - off;
@@ -181,7 +192,7 @@ __device__ __forceinline__ void find_item(const Cut& C, const Seq& s, Range& r) 
     const int last = 31 - __clz(__ballot_sync(0xFFFFFFFFu, u <= r.rem));
     base = __shfl_sync(0xFFFFFFFFu, u, last);
     a += last * step;
-    e = min(e, a + step);
+    e = kv_min(e, a + step);
   }
   r.item = a;
   r.off = static_cast<int>(r.rem - base);
@@ -199,8 +210,8 @@ __device__ __forceinline__ unsigned long long warp_inclusive(unsigned long long 
 // This CTA's share of `total` units.
 __device__ __forceinline__ void share(unsigned long long total, Range& r) {
   r.quota = divide(total + gridDim.x - 1, gridDim.x);
-  r.x0 = min(r.quota * blockIdx.x, total);
-  r.x1 = min(r.x0 + r.quota, total);
+  r.x0 = kv_min(r.quota * blockIdx.x, total);
+  r.x1 = kv_min(r.x0 + r.quota, total);
   r.rem = 0;
   r.b = r.kvh = r.item = r.off = 0;
 }
@@ -235,8 +246,8 @@ __device__ __forceinline__ void find_range(const Batch& B, const Cut& C, Range* 
     return;
   }
   const int per = (seqs + THREADS - 1) / THREADS;
-  const int b0 = min(tid * per, seqs);
-  int b1 = min(b0 + per, seqs);
+  const int b0 = kv_min(tid * per, seqs);
+  int b1 = kv_min(b0 + per, seqs);
   unsigned long long at = 0, x0 = 0;
   Seq s;
   // first the units of all sequences, then, by the thread whose sequences hold unit

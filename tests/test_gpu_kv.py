@@ -95,6 +95,23 @@ def test_window_and_sinks(window, sinks, q, kv):
     run(Batch(q, kv, 6, 6, 64, F16, window=window, sinks=sinks, seed=window, page_size=128, layout="head"))
 
 
+@pytest.mark.parametrize("heads,kv_heads,head_dim,q,kv,window,sinks", [
+    (12, 12, 128, [2226, 1517], [2226, 1517], 1024, 4), (8, 2, 64, [1900, 700, 1], [2500, 700, 3000], 700, 130),
+    (12, 4, 128, [3000], [3000], 0, 0), (16, 1, 128, [640], [5000], 2000, 1)])
+def test_many_items(heads, kv_heads, head_dim, q, kv, window, sinks):
+    """More items than SMs, cut at places that depend on windows and sinks: rows at the
+    borders of tiles and items, and some between."""
+    b = Batch(q, kv, heads, kv_heads, head_dim, F16, window=window, sinks=sinks, seed=window)
+    d = Device(b)
+    d.attend()
+    d.ok()
+    rows, at = [], 0
+    for n in q:
+        rows += [at + i for i in range(n) if i % 128 in (0, 127) or i % 85 == 84]
+        at += n
+    d.check(rows)
+
+
 @pytest.mark.parametrize("prefix", [1, 16, 127, 500, 2049])
 @pytest.mark.parametrize("q,kv", [([1] * 5, [1, 40, 130, 2, 16]), ([1, 0, 3], [9, 0, 3]), ([40, 1, 70], [40, 300, 75]), ([2], [1])])
 def test_shared_prefix(prefix, q, kv):

@@ -6,6 +6,8 @@ import ctypes
 import math
 import os
 import re
+import shutil
+import subprocess
 
 import numpy as np
 import pytest
@@ -77,6 +79,16 @@ def test_null_arguments(cs):
     assert lib.cs_kv_attention_shared(None, None, None, 0, None, None) == cs.CS_ERR_INVALID_ARG
     assert lib.cs_attn_cached_forward(None, None, None, None, None, None) == cs.CS_ERR_INVALID_ARG
     assert "NULL" in cs.cs_last_error_string()
+
+
+def test_the_division_of_the_work_against_counting(tmp_path):
+    """The arithmetic that gives every CTA its range of key tiles, run on the host."""
+    nvcc = shutil.which("nvcc") or "/usr/local/cuda/bin/nvcc"
+    exe = tmp_path / "kv_schedule_check"
+    subprocess.run([nvcc, "-std=c++17", "-O1", "-gencode", "arch=compute_103a,code=sm_103a", "-o", str(exe),
+                    os.path.join(ROOT, "tests", "c", "kv_schedule_check.cu")], check=True, capture_output=True)
+    r = subprocess.run([str(exe)], capture_output=True, text=True, timeout=120)
+    assert r.returncode == 0 and r.stdout.strip() == "ok", r.stdout
 
 
 def test_rotation_is_a_complex_product():
