@@ -502,9 +502,9 @@ __device__ bool softmax_role(const AttnP& p, AttnCtl<AttnShape<D>::SLOTS>* sc, u
     const int some = p.c.flat ? g.s.m : base + first + 1;
     const int all_lo = WINDOW ? max(0, base + first + p.per_tile - p.c.window) : 0;
     float m_ref = -INFINITY, l = 0.0f;
-#pragma unroll 1
     const Seen seen(p, g, w);
     const int k_first = two ? WINDOW ? seen.first : g.k0 : g.k0 + w, k_end = WINDOW && two ? seen.last + 1 : g.k1;
+#pragma unroll 1
     for (int k = k_first; k < k_end; k = WINDOW && two ? seen.next(k) : k + (two ? 1 : 2)) {
       // what the tile needs, known before its scores are there
       const bool fresh = k == k_first;  // O of this buffer holds nothing yet
