@@ -100,6 +100,19 @@ cs_status row_stride(const char* name, long long given, long long width, long lo
   return CS_OK;
 }
 
+// Whether two sets of `rows` rows (16-bit elements) share one: rows of one pitch may lie
+// side by side in a wider buffer.
+bool rows_overlap(const void* a, long long a_stride, long long a_width, const void* b, long long b_stride, long long b_width,
+                  int rows) {
+  const char *a0 = static_cast<const char*>(a), *b0 = static_cast<const char*>(b);
+  const char *a1 = a0 + 2 * ((rows - 1) * a_stride + a_width), *b1 = b0 + 2 * ((rows - 1) * b_stride + b_width);
+  if (rows < 1 || a1 <= b0 || b1 <= a0) return false;
+  if (a_stride != b_stride || rows == 1) return true;
+  const long long pitch = 2 * a_stride;
+  const long long off = ((b0 - a0) % pitch + pitch) % pitch;  // of b's rows inside a's pitch
+  return off < 2 * a_width || off + 2 * b_width > pitch;
+}
+
 cs_status check_batch(const cs_kv_s* p, const cs_kv_batch* b) {
   if (!b) return cs_fail(CS_ERR_INVALID_ARG, "batch is NULL");
   if (b->tokens < 0 || b->tokens > p->d.max_tokens)
@@ -229,7 +242,8 @@ cs_status check_attn(const cs_kv_s* p, const cs_kv_batch* b, const cs_kv_attn_ar
   if (b->tokens == 0) return CS_OK;
   if (!a->q || !a->out) return cs_fail(CS_ERR_INVALID_ARG, "q and out are required");
   if (!aligned16(a->q) || !aligned16(a->out)) return cs_fail(CS_ERR_INVALID_ARG, "q and out must be 16-byte aligned");
-  if (a->q == a->out) return cs_fail(CS_ERR_INVALID_ARG, "out must not be q");
+  if (rows_overlap(a->q, q_stride, width, a->out, k.out_stride, width, b->tokens))
+    return cs_fail(CS_ERR_INVALID_ARG, "out overlaps q");
   k.b = device_batch(p, b);
   // a window as long as any sequence hides nothing
   k.c.window = d.window >= kMaxKeys ? 0 : d.window;
@@ -333,14 +347,9 @@ cs_status append(cs_kv_s* p, const cs_kv_batch* b, const cs_kv_append_args* a, c
   std::memset(&k, 0, sizeof(k));
   if ((s = row_stride("qkv_stride", a->qkv_stride, width, &k.qkv_stride)) != CS_OK) return s;
   if ((s = row_stride("q_stride", a->q_stride, q_width, &k.q_stride)) != CS_OK) return s;
-  if (b->tokens > 0 && !(a->q_out == a->qkv && k.q_stride == k.qkv_stride)) {
-    // not in place: the rows must lie apart
-    const char* x0 = static_cast<const char*>(a->qkv);
-    const char* x1 = x0 + 2 * ((b->tokens - 1) * k.qkv_stride + width);
-    const char* y0 = static_cast<const char*>(a->q_out);
-    const char* y1 = y0 + 2 * ((b->tokens - 1) * k.q_stride + q_width);
-    if (x0 < y1 && y0 < x1) return cs_fail(CS_ERR_INVALID_ARG, "q_out overlaps qkv without being its Q part");
-  }
+  if (!(a->q_out == a->qkv && k.q_stride == k.qkv_stride) &&
+      rows_overlap(a->qkv, k.qkv_stride, width, a->q_out, k.q_stride, q_width, b->tokens))
+    return cs_fail(CS_ERR_INVALID_ARG, "q_out overlaps qkv without being its Q part");
   if (d.rotary_dim > 0) {
     if (!a->rope || a->rope_rows < 1) return cs_fail(CS_ERR_INVALID_ARG, "rope is required (rotary_dim=%d)", d.rotary_dim);
     if (!aligned16(a->rope)) return cs_fail(CS_ERR_INVALID_ARG, "rope must be 16-byte aligned");

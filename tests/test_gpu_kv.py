@@ -68,7 +68,7 @@ def run(b, **desc):
     return d
 
 
-HEADS = [(12, 12, 128), (8, 2, 64), (28, 4, 128), (16, 1, 64), (6, 2, 128), (40, 2, 64)]
+HEADS = [(128, 1, 64), (100, 1, 128), (12, 12, 128), (8, 2, 64), (28, 4, 128), (16, 1, 64), (6, 2, 128), (40, 2, 64)]
 
 
 @pytest.mark.parametrize("heads,kv_heads,head_dim", HEADS)
@@ -137,6 +137,9 @@ def test_long_contexts(q, kv, rows):
 
 
 def test_many_sequences():
+    run(Batch([1] * 3001, [5] * 3000 + [40], 2, 1, 64, F16))
+    run(Batch([0, 1] * 900, [3, 4] * 900, 2, 2, 64, BF16, poison=False))
+    run(Batch([1] * 99 + [30], [7] * 99 + [64], 4, 2, 64, F16))
     r = np.random.default_rng(0)
     kv = [int(x) for x in r.integers(1, 90, 700)]
     run(Batch([1] * 700, kv, 4, 2, 64, F16))
@@ -494,6 +497,9 @@ def test_refused_arguments():
         assert e.value.status == status
 
     refused(cs.CS_ERR_INVALID_ARG, cs.cs_kv_attention, p, b, d.q, d.kc, d.vc, d.q)  # out is q
+    both = torch.zeros(21, 2 * 1024, dtype=BF16, device="cuda")
+    refused(cs.CS_ERR_INVALID_ARG, cs.cs_kv_attention, p, b, both[:, :1024], d.kc, d.vc, both[:, 512:1536])
+    cs.cs_kv_attention(p, b, both[:, :1024], d.kc, d.vc, both[:, 1024:])  # side by side
     refused(cs.CS_ERR_INVALID_ARG, cs.cs_kv_attention_shared, p, b, d.q, d.kc, d.vc, d.prefix_pages, 0, d.out)  # not asked for
     big = cs.cs_kv_batch(p, d.cu_q, d.kv, d.table, tokens=22, max_q=20)
     q22 = torch.zeros(22, 8, 128, dtype=BF16, device="cuda")
