@@ -191,7 +191,7 @@ __device__ bool load_role(const AttnP& p, AttnCtl<AttnShape<D>::SLOTS>* sc, uint
   const Batch& B = p.b;
   const int lane = threadIdx.x & 31;
   const int pages_per_tile = KT >> B.page_shift, groups = B.page_size >> 3;
-  Walk walk(B, p.c, sc->range);
+  Walk walk(p.c, sc->range);
   Seg g;
   Ring<Sh::SLOTS> rp;
   uint32_t q_phase[2] = {1, 1};
@@ -288,7 +288,7 @@ __device__ bool mma_role(const AttnP& p, AttnCtl<AttnShape<D>::SLOTS>* sc, uint8
   const uint64_t k_desc = cs::smem_desc_sw128(cs::smem_u32(ring), 16, Sh::HALVES * 1024);
   const uint64_t v_desc = cs::smem_desc_sw128(cs::smem_u32(ring), 1024, Sh::HALVES * 1024);
   const bool leader = elect_one();
-  Walk walk(p.b, p.c, sc->range);
+  Walk walk(p.c, sc->range);
   Seg g;
   // Both warps watch every tile arrive, and give back the ones they do not read
   // too: a barrier's parity tells two phases apart, so no reader may be two behind.
@@ -424,11 +424,13 @@ __device__ __forceinline__ float* piece_state(float* part, unsigned cta, int whi
   return part + (((static_cast<size_t>(cta) * 2 + which) * 2 + tile) * 128 + r) * (D + 8);
 }
 
-// The log-sum-exp (base 2) of an output row.
-__device__ __forceinline__ void put_lse(const AttnP& p, long long row, float lse2) {
+// The log-sum-exp of an output row from its maximum and sum (base 2).
+__device__ __forceinline__ void put_lse(const AttnP& p, long long row, float m, float l) {
+  if (!p.c.flat && !p.lse) return;
+  const float lse2 = l == 0.0f ? -INFINITY : m + log2f(l);
   if (p.c.flat)
     p.flat_lse[row] = lse2;
-  else if (p.lse)
+  else
     p.lse[row] = lse2 * 0.6931471805599453f;
 }
 
@@ -481,7 +483,7 @@ __device__ bool softmax_role(const AttnP& p, AttnCtl<AttnShape<D>::SLOTS>* sc, u
     cs::tc_wait_ld_regs(o);
   };
   const uint64_t scale2 = pack64(p.scale_log2, p.scale_log2);
-  Walk walk(B, p.c, sc->range);
+  Walk walk(p.c, sc->range);
   Seg g;
   uint32_t tiles_done = 0;  // key tiles of the segments before this one
   uint32_t s_phase = 0, o_phase = 0, x_phase = 0;
@@ -703,7 +705,7 @@ __device__ bool softmax_role(const AttnP& p, AttnCtl<AttnShape<D>::SLOTS>* sc, u
     if (!two && count > 1) cs::mbar_arrive(&sc->other_empty);  // the other buffer's state is read
     if (whole) {
       if (live) {
-        put_lse(p, row, l == 0.0f ? -INFINITY : m_ref + log2f(l));
+        put_lse(p, row, m_ref, l);
         if (probe != 0.0f && isfinite(l)) mark(p, row);
       }
     } else {
@@ -790,7 +792,7 @@ __device__ __noinline__ void mend_row(const AttnP& p, int t, int h) {
     }
     dst[lane + 32 * w] = Pair<T>::put(x * inv, y * inv);
   }
-  if (lane == 0) put_lse(p, row, l == 0.0f ? -INFINITY : mx + log2f(l));
+  if (lane == 0) put_lse(p, row, mx, l);
 }
 
 // Joins the pieces of the items that several CTAs of cs_kv_attn_kernel share, a row to a
@@ -873,7 +875,7 @@ __global__ void __launch_bounds__(JOIN_THREADS) cs_kv_join_kernel(const __grid_c
 #pragma unroll
       for (int w = 0; w < W; w += 2) dst[w / 2] = Pair<T>::put(x[w] * inv, x[w + 1] * inv);
     }
-    if (lane == 0) put_lse(p, row, l == 0.0f ? -INFINITY : m + log2f(l));
+    if (lane == 0) put_lse(p, row, m, l);
     float probe = 0.0f;
 #pragma unroll
     for (int w = 0; w < W; ++w) probe = fmaf(x[w], 0.0f, probe);

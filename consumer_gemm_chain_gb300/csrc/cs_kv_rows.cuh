@@ -43,14 +43,13 @@ struct alignas(1024) RowsShared {
     // [warp][stage][K, V][8-key group][64-dimension half][key][16-byte piece, at its index ^ key]
     uint4 kv[ROWS_WARPS][STAGES][2][2][D / 64][8][8];
     float o[ROWS_WARPS][ROWS][D + 4];        // each warp's output
-    float sum[ROWS_WARPS][ROWS][D + 2];      // of a part of an item's pieces: output, sum
+    float sum[ROWS_WARPS][ROWS][D + 2];      // of a part of an item's pieces: output, maximum, sum
   };
   Range range;
   unsigned long long scratch[ROWS_THREADS / 32];
   int last, failed;
   uint64_t full[ROWS_WARPS][STAGES][2];  // [warp][stage][K, V]
   float2 ml[ROWS_WARPS][ROWS];  // each warp's maximum and sum of a row
-  float top[ROWS_THREADS];
   uint4 q[ROWS][D / 8 + 1];
 };
 
@@ -85,7 +84,7 @@ __global__ void __launch_bounds__(ROWS_THREADS, ROWS_CTAS) cs_kv_rows_kernel(con
         break;
       }
   };
-  Walk walk(B, p.c, sm.range);
+  Walk walk(p.c, sm.range);
   Seg g;
   while (walk.next(B, p.c, g)) {
     const int first = g.item * p.c.per_item;  // the item's first token
@@ -292,17 +291,15 @@ __global__ void __launch_bounds__(ROWS_THREADS, ROWS_CTAS) cs_kv_rows_kernel(con
       }
       const float y = l == 0.0f ? 0.0f : x / l;
       if (!isfinite(x) && isfinite(l) && g.s.n > 1) mark(p, row);  // several tokens: keys hidden from one only
-      const float lse2 = l == 0.0f ? -INFINITY : m + log2f(l);
+      if (d == 0) put_lse(p, row, m, l);
       if (p.c.flat) {
         p.flat_o[row * D + d] = y;
-        if (d == 0) p.flat_lse[row] = lse2;
       } else {
         T* out = static_cast<T*>(p.out) + (g.s.t0 + first + t) * p.out_stride + (g.kvh * B.group + r - t * B.group) * D;
         if constexpr (std::is_same<T, __half>::value)
           out[d] = __float2half(y);
         else
           out[d] = __float2bfloat16(y);
-        if (d == 0 && p.lse) p.lse[row] = lse2 * 0.6931471805599453f;
       }
     };
     const bool whole = g.whole();
@@ -343,52 +340,57 @@ __global__ void __launch_bounds__(ROWS_THREADS, ROWS_CTAS) cs_kv_rows_kernel(con
     // the last to arrive joins the pieces in their order
     const int pieces = static_cast<int>(c1 - c0) + 1;
     auto piece = [&](int i, int r) { return state(c0 + i, sm.range.quota * (c0 + i) < g.x, r); };
-    const int wr = tid % ROWS;  // a row for the weights
-    float m = -INFINITY;
-    if (wr < rows)
-#pragma unroll 4
-      for (int i = tid / ROWS; i < pieces; i += ROWS_THREADS / ROWS) m = fmaxf(m, __ldcg(piece(i, wr) + D));
-    sm.top[tid] = m;
-    __syncthreads();
-#pragma unroll
-    for (int i = 0; i < ROWS_THREADS / ROWS; ++i) m = fmaxf(m, sm.top[i * ROWS + wr]);
-    __syncthreads();
-    if (tid < ROWS) sm.top[tid] = m;
-    __syncthreads();
     // a warp sums a row over all pieces, or with few rows over a part of them; a lane D / 32
-    // dimensions
+    // dimensions.  A lane reads the maximum and sum of one piece of 32; the outputs are
+    // on their way by then.
     constexpr int W = D / 32;
     const int parts = rows >= ROWS_WARPS ? 1 : ROWS_WARPS / rows, per = (pieces + parts - 1) / parts;
     for (int u = warp; u < rows * parts; u += ROWS_WARPS) {
       const int r = u % rows, part = u / rows, to = min(pieces, (part + 1) * per);
-      float x[W] = {}, sum = 0.0f;
-      const float top = sm.top[r];
-#pragma unroll 8
-      for (int i = part * per; i < to; ++i) {
-        const float* from = piece(i, r);
-        const float2 ml = __ldcg(reinterpret_cast<const float2*>(from + D));
-        const float f = ml.x == -INFINITY ? 0.0f : cs::ex2_approx(ml.x - top);
-        sum = fmaf(ml.y, f, sum);
+      float x[W] = {}, sum = 0.0f, top = -INFINITY;
+      for (int i0 = part * per; i0 < to; i0 += 32) {
+        const int here = min(32, to - i0);
+        float2 ml = make_float2(-INFINITY, 0.0f);
+        if (lane < here) ml = __ldcg(reinterpret_cast<const float2*>(piece(i0 + lane, r) + D));
+        float m = ml.x;
 #pragma unroll
-        for (int v = 0; v < W; v += 2) {
-          const float2 y = __ldcg(reinterpret_cast<const float2*>(from + lane * 2 + 32 * v));
-          x[v] = fmaf(y.x, f, x[v]);
-          x[v + 1] = fmaf(y.y, f, x[v + 1]);
+        for (int v = 16; v; v >>= 1) m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, v));
+        m = fmaxf(m, top);
+        const float old = top == -INFINITY ? 0.0f : cs::ex2_approx(top - m);
+        const float weight = ml.x == -INFINITY ? 0.0f : cs::ex2_approx(ml.x - m);
+        top = m;
+        sum *= old;
+#pragma unroll
+        for (int v = 0; v < W; ++v) x[v] *= old;
+        const float part_l = ml.y * weight;
+#pragma unroll 8
+        for (int i = 0; i < here; ++i) {
+          const float* from = piece(i0 + i, r);
+          const float f = __shfl_sync(0xFFFFFFFFu, weight, i);
+          sum += __shfl_sync(0xFFFFFFFFu, part_l, i);
+#pragma unroll
+          for (int v = 0; v < W; v += 2) {
+            const float2 y = __ldcg(reinterpret_cast<const float2*>(from + lane * 2 + 32 * v));
+            x[v] = fmaf(y.x, f, x[v]);
+            x[v + 1] = fmaf(y.y, f, x[v + 1]);
+          }
         }
       }
 #pragma unroll
       for (int v = 0; v < W; v += 2) *reinterpret_cast<float2*>(&sm.sum[part][r][lane * 2 + 32 * v]) = make_float2(x[v], x[v + 1]);
-      if (lane == 0) sm.sum[part][r][D] = sum;
+      if (lane == 0) *reinterpret_cast<float2*>(&sm.sum[part][r][D]) = make_float2(top, sum);
     }
     __syncthreads();
     for (int i = tid; i < rows * D; i += ROWS_THREADS) {
       const int r = i / D, d = i % D;
-      float y = 0.0f, l = 0.0f;
+      float y = 0.0f, l = 0.0f, top = -INFINITY;
+      for (int part = 0; part < parts; ++part) top = fmaxf(top, sm.sum[part][r][D]);
       for (int part = 0; part < parts; ++part) {
-        y += sm.sum[part][r][d];
-        l += sm.sum[part][r][D];
+        const float m = sm.sum[part][r][D], f = m == -INFINITY ? 0.0f : cs::ex2_approx(m - top);
+        y = fmaf(sm.sum[part][r][d], f, y);
+        l = fmaf(sm.sum[part][r][D + 1], f, l);
       }
-      finish(r, d, y, sm.top[r], l);
+      finish(r, d, y, top, l);
     }
   }
 }

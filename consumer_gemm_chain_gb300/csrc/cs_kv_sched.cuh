@@ -123,6 +123,7 @@ struct Seg {
 struct Range {
   unsigned long long x0, x1, rem, quota;
   int b, kvh, item, off;
+  Seq s;  // sequence b
 };
 
 // An item's units are item_cost of overhead and then its tiles; a range that ends
@@ -131,10 +132,8 @@ struct Walk {
   unsigned long long x, x1;
   int b, kvh, item, off, items;
   Seq s;
-  __device__ __forceinline__ Walk(const Batch& B, const Cut& C, const Range& r)
-      : x(r.x0), x1(r.x1), b(r.b), kvh(r.kvh), item(r.item), off(r.off), items(0) {
-    if (x < x1 && load_seq(B, C, b, s)) items = items_of(C, s);
-  }
+  __device__ __forceinline__ Walk(const Cut& C, const Range& r)
+      : x(r.x0), x1(r.x1), b(r.b), kvh(r.kvh), item(r.item), off(r.off), items(items_of(C, r.s)), s(r.s) {}
   __device__ __forceinline__ bool next(const Batch& B, const Cut& C, Seg& g) {
     while (x < x1) {
       if (item == items) {
@@ -214,6 +213,7 @@ __device__ __forceinline__ void share(unsigned long long total, Range& r) {
   r.x1 = kv_min(r.x0 + r.quota, total);
   r.rem = 0;
   r.b = r.kvh = r.item = r.off = 0;
+  r.s = Seq{0, 0, 0};
 }
 
 // Every thread of the block: this CTA's range into *out (shared memory).
@@ -238,6 +238,7 @@ __device__ __forceinline__ void find_range(const Batch& B, const Cut& C, Range* 
         s.m = __shfl_sync(0xFFFFFFFFu, s.m, r.b);
         r.kvh = static_cast<int>(divide(in, per_head));
         r.rem = in - r.kvh * per_head;
+        r.s = s;
         find_item(C, s, r);
       }
       if (lane == 0) *out = r;
@@ -290,6 +291,7 @@ __device__ __forceinline__ void find_range(const Batch& B, const Cut& C, Range* 
   __syncthreads();
   if (warp == 0 && out->x0 < out->x1 && load_seq(B, C, out->b, s)) {
     Range r = *out;
+    r.s = s;
     find_item(C, s, r);
     __syncwarp();
     if (lane == 0) *out = r;
