@@ -285,6 +285,12 @@ int rows_smem(const cs_kv_desc& d) {
   return d.head_dim == 128 ? sizeof(cskv::RowsShared<128>) + 1024 : sizeof(cskv::RowsShared<64>) + 1024;
 }
 
+// States of pieces: the tensor-core kernel's are larger than the rows kernel's.
+size_t part_floats(const cs_kv_desc& d, int num_sms) {
+  static_assert(cskv::ROWS_CTAS * 2 * cskv::ROWS * (64 + 2) <= 4 * 128 * (64 + 8), "workspace");
+  return static_cast<size_t>(num_sms) * 4 * 128 * (d.head_dim + 8);
+}
+
 int rows_grid(const cs_kv_s* p) {
   return p->num_sms * cskv::ROWS_CTAS;
 }
@@ -331,7 +337,7 @@ cs_status run_attention(cs_kv_s* p, cskv::AttnP& k, int max_rows, cudaStream_t s
   int smem = 0;
   const void* fn = attn_kernel(d, &smem);
   if ((s = launch(fn, dim3(p->num_sms), cskv::ATTN_THREADS, smem, &k, st)) != CS_OK) return s;
-  return launch(join_kernel(d), dim3(4 * p->num_sms), cskv::JOIN_THREADS, 0, &k, st);
+  return launch(join_kernel(d), dim3(cskv::JOIN_CTAS * p->num_sms), cskv::JOIN_THREADS, 0, &k, st);
 }
 
 cs_status append(cs_kv_s* p, const cs_kv_batch* b, const cs_kv_append_args* a, cudaStream_t st) {
@@ -431,7 +437,7 @@ cs_status cs_kv_plan(const cs_kv_desc* desc, cs_kv_t* out) {
   p->device = dev;
   p->num_sms = desc->num_sms > 0 && desc->num_sms < sms ? desc->num_sms : sms;
   if (p->num_sms > cskv::JOIN_THREADS) p->num_sms = cskv::JOIN_THREADS;
-  p->ctrl_words = cskv::CTRL_COUNTERS + static_cast<size_t>(rows_grid(p));
+  p->ctrl_words = cskv::CTRL_COUNTERS + (p->d.shared ? 2 : 1) * static_cast<size_t>(rows_grid(p));
   int smem = 0;
   const void* fn = attn_kernel(p->d, &smem);
   if (cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess ||
@@ -440,9 +446,7 @@ cs_status cs_kv_plan(const cs_kv_desc* desc, cs_kv_t* out) {
     free_plan(p);
     return cs_fail(CS_ERR_CUDA, "the attention kernels need %d bytes of shared memory", smem);
   }
-  // states of pieces: the tensor-core kernel's are larger than the rows kernel's
-  const size_t part = static_cast<size_t>(p->num_sms) * 4 * 128 * (desc->head_dim + 8) * 4;
-  static_assert(cskv::ROWS_CTAS * 2 * cskv::ROWS * (64 + 2) <= 4 * 128 * (64 + 8), "workspace");
+  const size_t part = (desc->shared ? 2 : 1) * part_floats(*desc, p->num_sms) * 4;
   const size_t other = static_cast<size_t>(p->num_sms) * (desc->head_dim / 4 + 1) * 128 * 16;
   const size_t rows = static_cast<size_t>(desc->max_tokens) * desc->heads;
   const size_t flat = rows * (desc->head_dim + 1) * 4;
@@ -522,6 +526,8 @@ cs_status cs_kv_attention_shared(cs_kv_t p, const cs_kv_batch* b, const int32_t*
     k.c.flat_len = prefix_len;
     if ((s = run_attention(p, k, rows_of(k, b->seqs * static_cast<long long>(b->max_q)), static_cast<cudaStream_t>(stream))) != CS_OK) return s;
     k.c.flat = 0;
+    k.part += part_floats(p->d, p->num_sms);  // the rows kernel does not wait for the prefix's phase
+    k.arrivals += rows_grid(p);
   }
   return run_attention(p, k, rows_of(k, b->max_q), static_cast<cudaStream_t>(stream));
 }

@@ -800,15 +800,20 @@ __device__ __noinline__ void mend_row(const AttnP& p, int t, int h) {
 // pieces of 256 rows took 20 us and more while the others were done.  Then it mends the rows
 // that were marked.
 constexpr int JOIN_THREADS = 256;  // at least the grid of cs_kv_attn_kernel
+constexpr int JOIN_CTAS = 4;  // per SM
 template <typename T, int D>
-__global__ void __launch_bounds__(JOIN_THREADS) cs_kv_join_kernel(const __grid_constant__ AttnP p) {
+__global__ void __launch_bounds__(JOIN_THREADS, JOIN_CTAS) cs_kv_join_kernel(const __grid_constant__ AttnP p) {
   __shared__ int before[JOIN_THREADS + 1], sums[JOIN_THREADS / 32];
+  __shared__ Split splits[JOIN_THREADS];
   cs::grid_dep_wait();
   cs::grid_dep_launch_dependents();
   const Batch& B = p.b;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   // rows of the items that are split, in the order of the CTAs that they start in
-  const int mine = tid < p.num_splits && p.splits[tid].pieces ? p.splits[tid].tokens * B.group : 0;
+  splits[tid].pieces = 0;
+  if (tid < p.num_splits) splits[tid] = p.splits[tid];
+  const bool mend = !p.c.flat && __ldcg(&B.ctrl[CTRL_MEND]) != 0;
+  const int mine = splits[tid].pieces ? splits[tid].tokens * B.group : 0;
   int incl = mine;
 #pragma unroll
   for (int d = 1; d < 32; d <<= 1) {
@@ -831,30 +836,47 @@ __global__ void __launch_bounds__(JOIN_THREADS) cs_kv_join_kernel(const __grid_c
       else
         e = mid;
     }
-    const Split sp = p.splits[c0];
+    const Split sp = splits[c0];
     const int t = (n - before[c0]) / B.group, h = n - before[c0] - t * B.group;  // token of the item, head of the group
     const int tile = t >= p.per_tile, r = (t - tile * p.per_tile) * B.group + h;
     auto piece = [&](int c) { return piece_state<D>(p.part, c0 + c, c == 0 && sp.first, tile, r); };
-    // the row's maximum over all pieces, then the sum of the pieces in their order
-    float m = -INFINITY;
-    for (int c = lane; c < sp.pieces; c += 32) m = fmaxf(m, __ldcg(piece(c) + D));
+    // the pieces in their order, 32 at a time: a lane reads one's maximum and sum, while
+    // the outputs of the first few are on their way
+    constexpr int W = D / 32, AHEAD = 4;
+    using Part = typename std::conditional<W == 4, float4, float2>::type;
+    float x[W] = {}, l = 0.0f, m = -INFINITY;
+    for (int i0 = 0; i0 < sp.pieces; i0 += 32) {
+      const int here = min(32, sp.pieces - i0);
+      float2 ml = make_float2(-INFINITY, 0.0f);
+      if (lane < here) ml = __ldcg(reinterpret_cast<const float2*>(piece(i0 + lane) + D));
+      auto output = [&](int i) { return __ldcg(reinterpret_cast<const Part*>(piece(i0 + i)) + lane); };
+      Part y[AHEAD];
 #pragma unroll
-    for (int d = 16; d; d >>= 1) m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, d));
-    constexpr int W = D / 32;
-    float x[W] = {}, l = 0.0f;
-#pragma unroll 8
-    for (int c = 0; c < sp.pieces; ++c) {
-      const float* src = piece(c);
-      const float2 ml = __ldcg(reinterpret_cast<const float2*>(src + D));
-      const float f = ml.x == -INFINITY ? 0.0f : cs::ex2_approx(ml.x - m);
-      l = fmaf(ml.y, f, l);
-      if constexpr (W == 4) {
-        const float4 y = __ldcg(reinterpret_cast<const float4*>(src) + lane);
-        x[0] = fmaf(y.x, f, x[0]), x[1] = fmaf(y.y, f, x[1]), x[2] = fmaf(y.z, f, x[2]), x[3] = fmaf(y.w, f, x[3]);
-      } else {
-        const float2 y = __ldcg(reinterpret_cast<const float2*>(src) + lane);
-        x[0] = fmaf(y.x, f, x[0]), x[1] = fmaf(y.y, f, x[1]);
-      }
+      for (int i = 0; i < AHEAD; ++i)
+        if (i < here) y[i] = output(i);
+      float top = ml.x;
+#pragma unroll
+      for (int d = 16; d; d >>= 1) top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, d));
+      top = fmaxf(top, m);
+      const float old = m == -INFINITY ? 0.0f : cs::ex2_approx(m - top);
+      const float weight = ml.x == -INFINITY ? 0.0f : cs::ex2_approx(ml.x - top);
+      m = top;
+      float sum = ml.y * weight;
+#pragma unroll
+      for (int d = 16; d; d >>= 1) sum += __shfl_xor_sync(0xFFFFFFFFu, sum, d);
+      l = fmaf(l, old, sum);
+#pragma unroll
+      for (int w = 0; w < W; ++w) x[w] *= old;
+      auto add = [&](int i, const Part& z) {
+        const float f = __shfl_sync(0xFFFFFFFFu, weight, i);
+#pragma unroll
+        for (int w = 0; w < W; ++w) x[w] = fmaf(reinterpret_cast<const float*>(&z)[w], f, x[w]);
+      };
+#pragma unroll
+      for (int i = 0; i < AHEAD; ++i)
+        if (i < here) add(i, y[i]);
+#pragma unroll 4
+      for (int i = AHEAD; i < here; ++i) add(i, output(i));
     }
     const long long tok = sp.token + t, row = tok * B.heads + sp.kvh * B.group + h;
     if (!p.c.flat && p.flat_o) {  // join the prefix's output
@@ -884,7 +906,7 @@ __global__ void __launch_bounds__(JOIN_THREADS) cs_kv_join_kernel(const __grid_c
       mend_row<T, D>(p, static_cast<int>(tok), sp.kvh * B.group + h);
     }
   }
-  if (p.c.flat || __ldcg(&B.ctrl[CTRL_MEND]) == 0) return;
+  if (!mend) return;
   const long long all = static_cast<long long>(B.tokens) * B.heads;
   for (long long n = static_cast<long long>(blockIdx.x) * (JOIN_THREADS / 32) + warp; n < all;
        n += gridDim.x * (JOIN_THREADS / 32)) {

@@ -66,7 +66,11 @@ __global__ void __launch_bounds__(ROWS_THREADS, ROWS_CTAS) cs_kv_rows_kernel(con
     cs::prefetch_tmap(&p.k);
     cs::prefetch_tmap(&p.v);
   }
-  cs::grid_dep_wait();
+  // After a prefix's phase, all but the folding in of its result goes on beside the end of
+  // that phase: whatever came before it was complete when it let this grid start, and
+  // pieces and counters are other ones.  Every thread waits before it ends.
+  const bool late = !p.c.flat && p.flat_o;
+  if (!late) cs::grid_dep_wait();
   cs::grid_dep_launch_dependents();
   const Batch& B = p.b;
   find_range<ROWS_THREADS>(B, p.c, &sm.range, sm.scratch);
@@ -303,6 +307,7 @@ __global__ void __launch_bounds__(ROWS_THREADS, ROWS_CTAS) cs_kv_rows_kernel(con
       }
     };
     const bool whole = g.whole();
+    if (late && whole) cs::grid_dep_wait();
     for (int i = tid; i < rows * D; i += ROWS_THREADS) {
       const int r = i / D, d = i % D;
       float m = -INFINITY, sum = 0.0f, x = 0.0f;
@@ -337,6 +342,7 @@ __global__ void __launch_bounds__(ROWS_THREADS, ROWS_CTAS) cs_kv_rows_kernel(con
     }
     __syncthreads();
     if (!sm.last) continue;
+    if (late) cs::grid_dep_wait();
     // the last to arrive joins the pieces in their order
     const int pieces = static_cast<int>(c1 - c0) + 1;
     auto piece = [&](int i, int r) { return state(c0 + i, sm.range.quota * (c0 + i) < g.x, r); };
@@ -393,6 +399,7 @@ __global__ void __launch_bounds__(ROWS_THREADS, ROWS_CTAS) cs_kv_rows_kernel(con
       finish(r, d, y, top, l);
     }
   }
+  if (late) cs::grid_dep_wait();
 }
 
 }  // namespace cskv
