@@ -673,11 +673,10 @@ __device__ bool softmax_role(const AttnP& p, AttnCtl<AttnShape<D>::SLOTS>* sc, u
       uint32_t o[32];
       read_o(c, o);
 #pragma unroll
-      for (int t = 0; t < 32; ++t) {
-        x[t] = __uint_as_float(o[t]) * f;
-        probe = fmaf(x[t], 0.0f, probe);
-      }
+      for (int t = 0; t < 32; ++t) x[t] = __uint_as_float(o[t]) * f;
       if (other) axpy(x, other + c * 8 * 128, 128, f_other);
+#pragma unroll
+      for (int t = 0; t < 32; ++t) probe = fmaf(x[t], 0.0f, probe);
       if (!live) continue;
       if (pre) axpy(x, pre + c * 8, 1, fold);
       if (!whole || p.c.flat) {  // 32-bit values: a piece's state, or a prefix's output

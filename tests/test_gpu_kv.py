@@ -147,6 +147,26 @@ def test_many_sequences():
     run(Batch(q, [n + int(x) for n, x in zip(q, r.integers(0, 60, 300))], 4, 2, 64, BF16))
 
 
+def test_values_that_are_not_finite_in_the_other_half_of_a_short_item():
+    """Items of one row tile whose key tiles go to two halves in turn, none of them cut:
+    the spoilt key lies in the second half's tile."""
+    b = Batch([5] * 60, [250] * 60, 8, 2, 128, BF16, seed=3)
+    for s in range(60):
+        page, slot = int(b.table[s, 249 // 16]), 249 % 16
+        b.vc[page, slot, :, 5:9] = math.nan
+        b.v[s][249, :, 5:9] = 0.0  # rows that do not see it never read it
+    d = Device(b)
+    d.attend()
+    d.ok()
+    ref, _, bound = b.reference()
+    got = okv.to64(d.out)
+    for t in range(300):
+        ok = np.ones(128, dtype=bool)
+        ok[5:9] = t % 5 < 4
+        assert (np.abs(got[t, :, ok] - ref[t, :, ok]) <= bound[t, :, ok]).all(), t
+        assert t % 5 < 4 or not np.isfinite(got[t, :, 5:9]).any(), t
+
+
 @pytest.mark.parametrize("q,kv", [([4, 1], [70, 9]), ([3], [900]), ([200, 30], [300, 30]), ([130], [2000])])
 @pytest.mark.parametrize("window,prefix", [(0, 0), (33, 0), (0, 50)])
 def test_values_that_are_not_finite_at_keys_hidden_from_some_rows(q, kv, window, prefix):
