@@ -5,7 +5,8 @@
 // end to end, are cut into one equal range per CTA: long and short sequences, one or
 // many, prompts and single tokens all load the SMs alike, without a launch per kind.
 // Items cut by a range's border leave their state (O, max, sum) in the workspace, and
-// the pieces are joined in their order.
+// the pieces are joined in their order.  Where that would cost more than it evens out,
+// items stay whole (Cut::whole; run_attention in cs_kv.cu has the rule).
 #pragma once
 #include "cs_kv_append.cuh"
 
@@ -18,6 +19,7 @@ struct Cut {
   int item_cost;  // what starting and ending an item costs, in key tiles
   int flat;       // every row sees keys 0 .. flat_len - 1 of one common table (a shared prefix)
   int flat_len;
+  int whole;      // no item is cut: it belongs to the range that holds its middle
 };
 
 #define CS_KV_BOTH __host__ __device__ __forceinline__  // the division's arithmetic also runs in a host test
@@ -133,7 +135,17 @@ struct Walk {
   int b, kvh, item, off, items;
   Seq s;
   __device__ __forceinline__ Walk(const Cut& C, const Range& r)
-      : x(r.x0), x1(r.x1), b(r.b), kvh(r.kvh), item(r.item), off(r.off), items(items_of(C, r.s)), s(r.s) {}
+      : x(r.x0), x1(r.x1), b(r.b), kvh(r.kvh), item(r.item), off(r.off), items(items_of(C, r.s)), s(r.s) {
+    if (C.whole && off > 0) {
+      const int units = item_tiles(C, s, item) + C.item_cost;
+      x -= off;
+      if (2 * off > units) {  // the CTA before has this item
+        x += units;
+        ++item;
+      }
+      off = 0;
+    }
+  }
   __device__ __forceinline__ bool next(const Batch& B, const Cut& C, Seg& g) {
     while (x < x1) {
       if (item == items) {
@@ -149,7 +161,8 @@ struct Walk {
       }
       const int units = item_tiles(C, s, item) + C.item_cost;
       const unsigned long long left = x1 - x;
-      const int to = static_cast<unsigned long long>(units - off) <= left ? units : off + static_cast<int>(left);
+      if (C.whole && 2 * left <= static_cast<unsigned>(units)) return false;  // the next CTA's
+      const int to = C.whole || static_cast<unsigned long long>(units - off) <= left ? units : off + static_cast<int>(left);
       g.x = x - off + C.item_cost;
       g.k0 = kv_max(0, off - C.item_cost);
       g.k1 = to - C.item_cost;

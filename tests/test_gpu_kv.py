@@ -112,6 +112,39 @@ def test_many_items(heads, kv_heads, head_dim, q, kv, window, sinks):
     d.check(rows)
 
 
+@pytest.mark.parametrize("heads,kv_heads,head_dim,q,kv,window,sinks", [
+    (8, 2, 128, [600, 1, 70], [6000, 3900, 4100], 0, 0), (8, 8, 64, [600, 70, 0, 1], [6000, 4100, 0, 3900], 3400, 130),
+    (12, 12, 64, [700, 900], [5000, 7000], 0, 0), (16, 1, 128, [40, 300], [9000, 4000], 3300, 4)])
+@pytest.mark.parametrize("num_sms", [0, 37])
+def test_long_items(heads, kv_heads, head_dim, q, kv, window, sinks, num_sms):
+    """Items long enough to be cut and joined, and shorter ones between them."""
+    b = Batch(q, kv, heads, kv_heads, head_dim, BF16, window=window, sinks=sinks, seed=kv[0], page_size=64)
+    d = Device(b, num_sms=num_sms)
+    d.attend()
+    d.ok()
+    rows, at = [], 0
+    for n in q:
+        rows += [at + i for i in range(n) if i % 64 in (0, 63) or i == n - 1]
+        at += n
+    d.check(rows)
+
+
+@pytest.mark.parametrize("lens", [[512] * 6, [300] * 7, [1024, 90, 700, 2, 511], [256], [20] * 90])
+def test_whole_items(lens):
+    """Prompts short enough for no item to be cut: about as many items as SMs, fewer and more."""
+    b = Batch(lens, lens, 12, 12, 128, F16, seed=len(lens))
+    d = Device(b)
+    for _ in range(2):
+        d.out.fill_(7), d.lse.fill_(7)
+        d.attend()
+    d.ok()
+    rows, at = [], 0
+    for n in lens:
+        rows += [at + i for i in range(n) if i % 128 in (0, 127) or i == n - 1]
+        at += n
+    d.check(rows)
+
+
 @pytest.mark.parametrize("prefix", [1, 16, 127, 500, 2049])
 @pytest.mark.parametrize("q,kv", [([1] * 5, [1, 40, 130, 2, 16]), ([1, 0, 3], [9, 0, 3]), ([40, 1, 70], [40, 300, 75]), ([2], [1])])
 def test_shared_prefix(prefix, q, kv):
