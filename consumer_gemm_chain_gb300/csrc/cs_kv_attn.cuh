@@ -12,8 +12,8 @@
 // the first half of its S as the A operand of O += P V.  So a softmax thread owns a row:
 // its maximum and sum need no exchange, and while one buffer is at its exponentials the
 // other's products run.  Sums, maxima, S and O are fp32; P is rounded to the operands'
-// type (half a step of it, 2^-9 or 2^-12 of a weight that is at most 2^8 times the row's
-// reference), O once at the end.
+// type (off by at most 2^-8 of the weight in bf16, 2^-11 in fp16; a weight is at most 2^8 by
+// the row's reference, so fp16 has room for it), O once at the end.
 //
 // Bound.  Per tile of 128 x 128 weights the tensor core needs 8 x 64 cycles for S and as
 // many for P V at 128 dimensions (half at 64), the two softmax warpgroups together about
@@ -815,8 +815,8 @@ __device__ __noinline__ void mend_row(const AttnP& p, int t, int h) {
 // warp, D / 32 dimensions to a lane:  O = sum_i 2^(m_i - m) O_i / sum_i 2^(m_i - m) l_i.
 // A kernel of its own, because one SM joining ten pieces of 256 rows took 20 us and more
 // while the others were done.  Bound by the latency of a row's reads (L2, mostly), so
-// all of them start at once.  About 8 us behind a prompt of 8192 tokens (304 pieces, 41 MB).
-// Then it mends the rows that were marked.
+// all of them start at once.  304 pieces of 256 rows (41 MB, out of DRAM): 21 us, less right
+// behind the attention, when they lie in L2.  Then it mends the rows that were marked.
 constexpr int JOIN_THREADS = 256;  // at least the grid of cs_kv_attn_kernel
 constexpr int JOIN_CTAS = 4;  // per SM
 template <typename T, int D>

@@ -175,8 +175,9 @@ def _rows(t, tokens, heads, head_dim, dtype, device, name):
 class KVBatch:
     """One batch (see ``cs_kv_batch`` in include/cs_kv.h); keeps its tensors alive."""
 
-    def __init__(self, raw: cs_kv_batch_s, tensors):
+    def __init__(self, raw: cs_kv_batch_s, tensors, device: int):
         self.raw = raw
+        self.device = device
         self.tokens = raw.tokens
         self.tensors = tensors
         self._ref = byref(raw)
@@ -195,10 +196,16 @@ def cs_kv_batch(plan: KVPlan, cu_q, kv_lens, page_table, tokens: int, max_q: int
     b.cu_q = _whole(cu_q, (seqs + 1,), torch.int32, plan.device, "cu_q")
     b.kv_lens = _whole(kv_lens, (seqs,), torch.int32, plan.device, "kv_lens")
     b.page_table = _whole(page_table, (seqs, cols), torch.int32, plan.device, "page_table")
-    return KVBatch(b, (cu_q, kv_lens, page_table))
+    return KVBatch(b, (cu_q, kv_lens, page_table), plan.device)
+
+
+def _same_device(plan, batch) -> None:
+    if batch.device != plan.device:
+        raise ValueError(f"the batch is on cuda:{batch.device}, the plan on cuda:{plan.device}")
 
 
 def _append_args(plan, batch, a, k_cache, v_cache, rope, positions):
+    _same_device(plan, batch)
     a.k_cache = _whole(k_cache, plan.cache_shape, plan.dtype, plan.device, "k_cache")
     a.v_cache = _whole(v_cache, plan.cache_shape, plan.dtype, plan.device, "v_cache")
     if rope is None:
@@ -225,6 +232,7 @@ def cs_kv_append(plan: KVPlan, batch: KVBatch, qkv, q_out, k_cache, v_cache, rop
 
 
 def _kv_attn_args(plan, batch, q, k_cache, v_cache, out, lse):
+    _same_device(plan, batch)
     a, d = plan._attn, plan.desc
     a.q, a.q_stride = _rows(q, batch.tokens, d.heads, d.head_dim, plan.dtype, plan.device, "q")
     a.out, a.out_stride = _rows(out, batch.tokens, d.heads, d.head_dim, plan.dtype, plan.device, "out")

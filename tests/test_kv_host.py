@@ -137,3 +137,13 @@ def test_a_token_that_sees_no_key():
     out, lse, _ = b.reference()
     assert (out[:2] == 0).all() and np.isneginf(lse[:2]).all() and np.isfinite(lse[2:]).all()
     assert np.allclose(out[2, 0], okv.to64(b.v[0][0, 0]))
+
+
+def test_a_batch_of_another_device_is_refused(cs):
+    from types import SimpleNamespace
+    batch = cs.KVBatch(cs.kv.cs_kv_batch_s(), (), 1)
+    plan = SimpleNamespace(device=0, _attn=None, _append=None, desc=None)
+    with pytest.raises(ValueError, match="cuda:1"):
+        cs.kv._kv_attn_args(plan, batch, None, None, None, None, None)
+    with pytest.raises(ValueError, match="cuda:1"):
+        cs.kv._append_args(plan, batch, None, None, None, None, None)
