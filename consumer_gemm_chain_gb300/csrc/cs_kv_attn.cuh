@@ -453,7 +453,7 @@ __device__ __forceinline__ void put_lse(const AttnP& p, long long row, float m, 
 
 // A row whose weights are finite and whose output is not: some value of its tiles is
 // not, maybe one at a key that is hidden from this row only (its weight 0 times NaN or
-// infinity is NaN).  The row is computed again from its visible keys alone.
+// infinity is NaN).  If there is one, the row is computed again from its visible keys alone.
 __device__ __forceinline__ void mark(const AttnP& p, long long row) {
   if (p.c.flat) return;  // no key is hidden from one row and seen by another
   p.mend[row] = 1;
@@ -753,6 +753,34 @@ __device__ __noinline__ void mend_row(const AttnP& p, int t, int h) {
   if (!sequence(B, b, t0, n, m) || t < t0 || t >= t0 + n) return;
   const int pos = m - n + t - t0, kh = h / B.group;
   constexpr int W = D / 64;  // 32-bit words per lane
+  const int* pages = B.table + static_cast<long long>(b) * B.table_cols;
+  const int lo = p.c.window > 0 ? max(0, pos - p.c.window + 1) : 0, sinks = min(p.c.sinks, lo);
+  // element offset of key j's row, negative: its page is not in the pool
+  auto row_of = [&](int j) {
+    const int page = __ldg(pages + (j >> B.page_shift));
+    return page < 0 || page >= B.num_pages
+               ? -1ll
+               : page * B.page_stride + (j & (B.page_size - 1)) * B.slot_stride + kh * B.head_stride;
+  };
+  // is a value not finite at a key of the item that this row does not see?  (Else the row has
+  // what its own keys give, and thousands of rows may see one such value.)
+  const int first = (t - t0) / p.c.per_item * p.c.per_item, last = min(n, first + p.c.per_item) - 1;
+  bool spoilt = false;
+  auto look = [&](int from, int to) {
+#pragma unroll 4
+    for (int j = from; j < to; ++j) {
+      const long long at = row_of(j);
+      if (at < 0) continue;
+#pragma unroll
+      for (int w = 0; w < W; ++w) {
+        const float2 v = Pair<T>::get(reinterpret_cast<const uint32_t*>(static_cast<const T*>(p.v_raw) + at)[lane + 32 * w]);
+        spoilt |= !isfinite(v.x) || !isfinite(v.y);
+      }
+    }
+  };
+  look(max(0, pos + 1), m - n + last + 1);
+  if (p.c.window > 0) look(max(p.c.sinks, m - n + first - p.c.window + 1), lo);
+  if (!__any_sync(0xFFFFFFFFu, spoilt)) return;
   float q[2 * W], o[2 * W] = {}, mx = -INFINITY, l = 0.0f;
   const uint32_t* qr = reinterpret_cast<const uint32_t*>(static_cast<const T*>(p.q_raw) + t * p.q_stride + h * D);
 #pragma unroll
@@ -760,13 +788,10 @@ __device__ __noinline__ void mend_row(const AttnP& p, int t, int h) {
     const float2 v = Pair<T>::get(qr[lane + 32 * w]);
     q[2 * w] = v.x, q[2 * w + 1] = v.y;
   }
-  const int* pages = B.table + static_cast<long long>(b) * B.table_cols;
-  const int lo = p.c.window > 0 ? max(0, pos - p.c.window + 1) : 0, sinks = min(p.c.sinks, lo);
   for (int i = 0; i < sinks + pos + 1 - lo; ++i) {  // the sinks, then the window
     const int j = i < sinks ? i : lo + i - sinks;
-    const int page = __ldg(pages + (j >> B.page_shift));
-    if (page < 0 || page >= B.num_pages) continue;
-    const long long at = page * B.page_stride + (j & (B.page_size - 1)) * B.slot_stride + kh * B.head_stride;
+    const long long at = row_of(j);
+    if (at < 0) continue;
     const uint32_t* kr = reinterpret_cast<const uint32_t*>(static_cast<const T*>(p.k_raw) + at);
     const uint32_t* vr = reinterpret_cast<const uint32_t*>(static_cast<const T*>(p.v_raw) + at);
     float s = 0.0f;

@@ -180,6 +180,32 @@ def test_many_sequences():
     run(Batch(q, [n + int(x) for n, x in zip(q, r.integers(0, 60, 300))], 4, 2, 64, BF16))
 
 
+@pytest.mark.parametrize("window", [0, 600])
+def test_a_value_that_is_not_finite_and_seen_by_many_rows(window):
+    """Rows that see it have it in their results, and no others; the call takes about as long
+    as without it (not as if every one of those rows had been computed again)."""
+    b = Batch([4096], [4096], 16, 4, 64, F16, window=window, seed=window)
+    d = Device(b)
+    d.attend()
+    d.ok()
+    clean = d.out.clone()
+    page, slot = int(b.table[0, 2000 // 16]), 2000 % 16
+    d.vc[page, slot, :, 3] = math.inf
+    a, e = torch.cuda.Event(enable_timing=True), torch.cuda.Event(enable_timing=True)
+    a.record()
+    d.attend()
+    e.record()
+    d.ok()
+    assert a.elapsed_time(e) < 20.0
+    sees = torch.zeros(4096, dtype=torch.bool, device="cuda")
+    sees[2000:2000 + window if window else None] = True
+    assert not torch.isfinite(d.out[sees][:, :, 3]).any()
+    d.out[sees, :, 3] = clean[sees, :, 3]
+    rows = [*range(1980, 2004), *range(2590, 2606), 100, 1900, 2300, 4095]
+    d.check(rows)
+    assert torch.equal(d.out[:1900], clean[:1900])
+
+
 def test_values_that_are_not_finite_in_the_other_half_of_a_short_item():
     """Items of one row tile whose key tiles go to two halves in turn, none of them cut:
     the spoilt key lies in the second half's tile."""
