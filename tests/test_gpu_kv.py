@@ -112,6 +112,50 @@ def test_many_items(heads, kv_heads, head_dim, q, kv, window, sinks):
     d.check(rows)
 
 
+@pytest.mark.parametrize("q,kv,prefix", [([1] * 40, [1 + 9 * i for i in range(40)], 3001), ([1, 3, 2], [400, 90, 2], 700),
+                                         ([1], [200], 40), ([90, 1], [300, 20], 1000)])
+@pytest.mark.parametrize("captured", [False, True])
+def test_calls_right_behind_one_another(q, kv, prefix, captured):
+    """Kernels start while the ones before them end: the same results, bit by bit, as with
+    nothing else running (append, attention behind a prefix, attention; again with other queries)."""
+    b = Batch(q, kv, 8, 2, 128, BF16, prefix=prefix, seed=prefix)
+    d = Device(b, rotary_dim=0)
+    g = torch.Generator().manual_seed(5)
+    n = 6
+    qkv = (torch.randn(n, b.tokens, 12 * 128, generator=g)).to(BF16).cuda()
+    outs = torch.zeros(2, n, 2, b.tokens, 8, 128, dtype=BF16, device="cuda")
+    qs = torch.zeros(2, b.tokens, 8, 128, dtype=BF16, device="cuda")
+
+    def step(i, out, pause):
+        cs.cs_kv_append(d.plan, d.batch, qkv[i], qs[i % 2], d.kc, d.vc)
+        pause()
+        cs.cs_kv_attention_shared(d.plan, d.batch, qs[i % 2], d.kc, d.vc, d.prefix_pages, b.prefix, out[0])
+        pause()
+        cs.cs_kv_attention(d.plan, d.batch, qs[i % 2], d.kc, d.vc, out[1])
+        pause()
+
+    for i in range(n):
+        step(i, outs[0, i], torch.cuda.synchronize)
+    if captured:
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            for i in range(n):
+                step(i, outs[1, i], lambda: None)
+        for _ in range(3):
+            outs[1].fill_(7)
+            graph.replay()
+            torch.cuda.synchronize()
+            assert torch.equal(outs[0], outs[1])
+    else:
+        for _ in range(3):
+            outs[1].fill_(7)
+            for i in range(n):
+                step(i, outs[1, i], lambda: None)
+            torch.cuda.synchronize()
+            assert torch.equal(outs[0], outs[1])
+    d.ok()
+
+
 @pytest.mark.parametrize("heads,kv_heads,head_dim,q,kv,window,sinks", [
     (8, 2, 128, [600, 1, 70], [6000, 3900, 4100], 0, 0), (8, 8, 64, [600, 70, 0, 1], [6000, 4100, 0, 3900], 3400, 130),
     (12, 12, 64, [700, 900], [5000, 7000], 0, 0), (16, 1, 128, [40, 300], [9000, 4000], 3300, 4)])
