@@ -288,7 +288,7 @@ int rows_smem(const cs_kv_desc& d) {
 
 // States of pieces: the tensor-core kernel's are larger than the rows kernel's.
 size_t part_floats(const cs_kv_desc& d, int num_sms) {
-  static_assert(cskv::ROWS_CTAS * 2 * cskv::ROWS * (64 + 2) <= 4 * 128 * (64 + 8), "workspace");
+  static_assert(cskv::ROWS_CTAS * 2 * cskv::ROWS * (64 + 4) <= 4 * 128 * (64 + 8), "workspace");
   return static_cast<size_t>(num_sms) * 4 * 128 * (d.head_dim + 8);
 }
 

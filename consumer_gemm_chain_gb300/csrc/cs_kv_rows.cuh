@@ -53,7 +53,7 @@ struct alignas(1024) RowsShared {
     // [warp][stage][K, V][8-key group][64-dimension half][key][16-byte piece, at its index ^ key]
     uint4 kv[ROWS_WARPS][STAGES][2][2][D / 64][8][8];
     float o[ROWS_WARPS][ROWS][D + 4];        // each warp's output
-    float sum[ROWS_WARPS][ROWS][D + 2];      // of a part of an item's pieces: output, maximum, sum
+    float sum[ROWS][D + 4];                  // of a part of an item's pieces: output, maximum, sum
   };
   Range range;
   unsigned long long scratch[ROWS_THREADS / 32];
@@ -291,36 +291,43 @@ __global__ void __launch_bounds__(ROWS_THREADS, ROWS_CTAS) cs_kv_rows_kernel(con
       }
     }
     __syncthreads();
-    auto state = [&](unsigned cta, int which, int r) { return p.part + ((static_cast<size_t>(cta) * 2 + which) * ROWS + r) * (D + 2); };
-    // dimension d of row r from its state
-    auto finish = [&](int r, int d, float x, float m, float l) {
+    auto state = [&](unsigned cta, int which, int r) { return p.part + ((static_cast<size_t>(cta) * 2 + which) * ROWS + r) * (D + 4); };
+    // dimensions 4 c .. 4 c + 3 of row r from their state
+    auto finish = [&](int r, int c, float4 x, float m, float l) {
       const int t = r / B.group;
       const long long row = static_cast<long long>(g.s.t0 + first + t) * B.heads + g.kvh * B.group + r - t * B.group;
-      if (!p.c.flat && p.flat_o) {  // join the prefix's output
+      float4* const pre = p.flat_o ? reinterpret_cast<float4*>(p.flat_o + row * D) + c : nullptr;
+      if (!p.c.flat && pre) {  // join the prefix's output
         const float z = p.flat_lse[row], top = fmaxf(m, z);
         const float own = m == -INFINITY ? 0.0f : cs::ex2_approx(m - top), fold = z == -INFINITY ? 0.0f : cs::ex2_approx(z - top);
-        x = x * own + p.flat_o[row * D + d] * fold;
+        const float4 y = *pre;
+        x = make_float4(x.x * own + y.x * fold, x.y * own + y.y * fold, x.z * own + y.z * fold, x.w * own + y.w * fold);
         l = l * own + fold;
         m = top;
       }
-      const float y = l == 0.0f ? 0.0f : x / l;
-      if (!isfinite(x) && isfinite(l) && g.s.n > 1) mark(p, row);  // several tokens: keys hidden from one only
-      if (d == 0) put_lse(p, row, m, l);
+      const float inv = l == 0.0f ? 0.0f : 1.0f / l;
+      const float4 y = l == 0.0f ? make_float4(0.0f, 0.0f, 0.0f, 0.0f) : make_float4(x.x * inv, x.y * inv, x.z * inv, x.w * inv);
+      const float probe = fmaf(x.x, 0.0f, fmaf(x.y, 0.0f, fmaf(x.z, 0.0f, x.w * 0.0f)));  // NaN if one is not finite
+      if (probe != 0.0f && isfinite(l) && g.s.n > 1) mark(p, row);  // several tokens: keys hidden from one only
+      if (c == 0) put_lse(p, row, m, l);
       if (p.c.flat) {
-        p.flat_o[row * D + d] = y;
+        *pre = y;
       } else {
-        T* out = static_cast<T*>(p.out) + (g.s.t0 + first + t) * p.out_stride + (g.kvh * B.group + r - t * B.group) * D;
-        if constexpr (std::is_same<T, __half>::value)
-          out[d] = __float2half(y);
-        else
-          out[d] = __float2bfloat16(y);
+        uint2* out = reinterpret_cast<uint2*>(static_cast<T*>(p.out) + (g.s.t0 + first + t) * p.out_stride +
+                                              (g.kvh * B.group + r - t * B.group) * D) + c;
+        *out = make_uint2(Pair<T>::put(y.x, y.y), Pair<T>::put(y.z, y.w));
       }
     };
+    auto add = [](float4& x, const float4& y, float f) {
+      x.x = fmaf(y.x, f, x.x), x.y = fmaf(y.y, f, x.y), x.z = fmaf(y.z, f, x.z), x.w = fmaf(y.w, f, x.w);
+    };
+    constexpr int QUADS = D / 4;
     const bool whole = g.whole();
     if (late && whole) cs::grid_dep_wait();
-    for (int i = tid; i < rows * D; i += ROWS_THREADS) {
-      const int r = i / D, d = i % D;
-      float m = -INFINITY, sum = 0.0f, x = 0.0f;
+    for (int i = tid; i < rows * QUADS; i += ROWS_THREADS) {
+      const int r = i / QUADS, c = i % QUADS;
+      float m = -INFINITY, sum = 0.0f;
+      float4 x = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
 #pragma unroll
       for (int w = 0; w < ROWS_WARPS; ++w) m = fmaxf(m, sm.ml[w][r].x);
 #pragma unroll
@@ -328,14 +335,14 @@ __global__ void __launch_bounds__(ROWS_THREADS, ROWS_CTAS) cs_kv_rows_kernel(con
         const float2 ml = sm.ml[w][r];
         const float f = ml.x == -INFINITY ? 0.0f : cs::ex2_approx(ml.x - m);
         sum = fmaf(ml.y, f, sum);
-        x = fmaf(sm.o[w][r][d], f, x);
+        add(x, *reinterpret_cast<const float4*>(&sm.o[w][r][4 * c]), f);
       }
       if (whole) {
-        finish(r, d, x, m, sum);
+        finish(r, c, x, m, sum);
       } else {
         float* to = state(blockIdx.x, sm.range.x0 < g.x, r);
-        to[d] = x;
-        if (d == 0) *reinterpret_cast<float2*>(to + D) = make_float2(m, sum);
+        reinterpret_cast<float4*>(to)[c] = x;
+        if (c == 0) *reinterpret_cast<float2*>(to + D) = make_float2(m, sum);
       }
     }
     if (whole) continue;
@@ -356,57 +363,61 @@ __global__ void __launch_bounds__(ROWS_THREADS, ROWS_CTAS) cs_kv_rows_kernel(con
     // the last to arrive joins the pieces in their order
     const int pieces = static_cast<int>(c1 - c0) + 1;
     auto piece = [&](int i, int r) { return state(c0 + i, sm.range.quota * (c0 + i) < g.x, r); };
-    // a warp sums a row over all pieces, or with few rows over a part of them; a lane D / 32
-    // dimensions.  A lane reads the maximum and sum of one piece of 32; the outputs are
-    // on their way by then.
-    constexpr int W = D / 32;
-    const int parts = rows >= ROWS_WARPS ? 1 : ROWS_WARPS / rows, per = (pieces + parts - 1) / parts;
-    for (int u = warp; u < rows * parts; u += ROWS_WARPS) {
+    // a warp (64 dimensions: half of one) sums a row over all pieces, or with few rows over a
+    // part of them, a lane four dimensions; every lane knows the weights of 32 (16) pieces at a time
+    constexpr int LANES = QUADS, UNITS = ROWS_THREADS / LANES, AHEAD = 4;
+    static_assert(UNITS <= ROWS, "sums");
+    const unsigned group = LANES == 32 ? 0xFFFFFFFFu : 0xFFFFu << (lane & 16);
+    const int gl = lane % LANES;
+    const int parts = rows >= UNITS ? 1 : UNITS / rows, per = (pieces + parts - 1) / parts;
+    for (int u = tid / LANES; u < rows * parts; u += UNITS) {
       const int r = u % rows, part = u / rows, to = min(pieces, (part + 1) * per);
-      float x[W] = {}, sum = 0.0f, top = -INFINITY;
-      for (int i0 = part * per; i0 < to; i0 += 32) {
-        const int here = min(32, to - i0);
+      float4 x = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+      float sum = 0.0f, top = -INFINITY;
+      for (int i0 = part * per; i0 < to; i0 += LANES) {
+        const int here = min(LANES, to - i0);
+        auto output = [&](int i) { return __ldcg(reinterpret_cast<const float4*>(piece(i0 + i, r)) + gl); };
         float2 ml = make_float2(-INFINITY, 0.0f);
-        if (lane < here) ml = __ldcg(reinterpret_cast<const float2*>(piece(i0 + lane, r) + D));
+        if (gl < here) ml = __ldcg(reinterpret_cast<const float2*>(piece(i0 + gl, r) + D));
+        float4 y[AHEAD];  // on their way with the maxima and sums
+#pragma unroll
+        for (int i = 0; i < AHEAD; ++i)
+          if (i < here) y[i] = output(i);
         float m = ml.x;
 #pragma unroll
-        for (int v = 16; v; v >>= 1) m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, v));
+        for (int v = LANES / 2; v; v >>= 1) m = fmaxf(m, __shfl_xor_sync(group, m, v));
         m = fmaxf(m, top);
         const float old = top == -INFINITY ? 0.0f : cs::ex2_approx(top - m);
         const float weight = ml.x == -INFINITY ? 0.0f : cs::ex2_approx(ml.x - m);
         top = m;
-        sum *= old;
+        float l = ml.y * weight;
 #pragma unroll
-        for (int v = 0; v < W; ++v) x[v] *= old;
-        const float part_l = ml.y * weight;
-#pragma unroll 8
-        for (int i = 0; i < here; ++i) {
-          const float* from = piece(i0 + i, r);
-          const float f = __shfl_sync(0xFFFFFFFFu, weight, i);
-          sum += __shfl_sync(0xFFFFFFFFu, part_l, i);
+        for (int v = LANES / 2; v; v >>= 1) l += __shfl_xor_sync(group, l, v);
+        sum = fmaf(sum, old, l);
+        x.x *= old, x.y *= old, x.z *= old, x.w *= old;
 #pragma unroll
-          for (int v = 0; v < W; v += 2) {
-            const float2 y = __ldcg(reinterpret_cast<const float2*>(from + lane * 2 + 32 * v));
-            x[v] = fmaf(y.x, f, x[v]);
-            x[v + 1] = fmaf(y.y, f, x[v + 1]);
-          }
+        for (int i = 0; i < AHEAD; ++i) {
+          const float f = __shfl_sync(group, weight, i, LANES);
+          if (i < here) add(x, y[i], f);
         }
+#pragma unroll 4
+        for (int i = AHEAD; i < here; ++i) add(x, output(i), __shfl_sync(group, weight, i, LANES));
       }
-#pragma unroll
-      for (int v = 0; v < W; v += 2) *reinterpret_cast<float2*>(&sm.sum[part][r][lane * 2 + 32 * v]) = make_float2(x[v], x[v + 1]);
-      if (lane == 0) *reinterpret_cast<float2*>(&sm.sum[part][r][D]) = make_float2(top, sum);
+      reinterpret_cast<float4*>(sm.sum[u])[gl] = x;
+      if (gl == 0) *reinterpret_cast<float2*>(&sm.sum[u][D]) = make_float2(top, sum);
     }
     __syncthreads();
-    for (int i = tid; i < rows * D; i += ROWS_THREADS) {
-      const int r = i / D, d = i % D;
-      float y = 0.0f, l = 0.0f, top = -INFINITY;
-      for (int part = 0; part < parts; ++part) top = fmaxf(top, sm.sum[part][r][D]);
+    for (int i = tid; i < rows * QUADS; i += ROWS_THREADS) {
+      const int r = i / QUADS, c = i % QUADS;
+      float4 y = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+      float l = 0.0f, top = -INFINITY;
+      for (int part = 0; part < parts; ++part) top = fmaxf(top, sm.sum[part * rows + r][D]);
       for (int part = 0; part < parts; ++part) {
-        const float m = sm.sum[part][r][D], f = m == -INFINITY ? 0.0f : cs::ex2_approx(m - top);
-        y = fmaf(sm.sum[part][r][d], f, y);
-        l = fmaf(sm.sum[part][r][D + 1], f, l);
+        const float m = sm.sum[part * rows + r][D], f = m == -INFINITY ? 0.0f : cs::ex2_approx(m - top);
+        add(y, *reinterpret_cast<const float4*>(&sm.sum[part * rows + r][4 * c]), f);
+        l = fmaf(sm.sum[part * rows + r][D + 1], f, l);
       }
-      finish(r, d, y, top, l);
+      finish(r, c, y, top, l);
     }
   }
   if (late) cs::grid_dep_wait();
