@@ -15,9 +15,11 @@
 //
 // 64 single tokens over 300 to 32000 keys, 64 / 8 heads of 128 (4.26 GB of keys and values):
 // 680 to 698 us, 6.1 to 6.3 TB/s, 0.90 to 0.93 of a plain copy's measured 6.8; DRAM is what
-// bounds it.  128 single tokens under a window of 1024: 95 us, 5.6 TB/s; one user's token
-// over 978 keys, 12 heads: 9.4 us, launch, lookups, a tile's latency and the joining one
-// after another.  Fetching a segment's first tiles while the one before is joined was slower
+// bounds it.  128 single tokens under a window of 1024: 93.5 us, 5.7 TB/s; one user's token
+// over 978 keys, 12 heads: 8.8 us, launch, lookups, a tile's latency and the joining one
+// after another.  With 16 rows the joins count: 8 sequences of up to 4 tokens over up to 2000 keys
+// take 26 us where single tokens take 16 (38 with one dimension a thread; reading all
+// of a thread's rows at once needs 540 bytes of spills, and everything is slower).  Fetching a segment's first tiles while the one before is joined was slower
 // (decode over long contexts 690 -> 703 us, one user's 9.3 -> 10.1): it needs registers
 // that the inner loop has not got, and three CTAs an SM cover for each other already.
 #pragma once
@@ -365,7 +367,7 @@ __global__ void __launch_bounds__(ROWS_THREADS, ROWS_CTAS) cs_kv_rows_kernel(con
     auto piece = [&](int i, int r) { return state(c0 + i, sm.range.quota * (c0 + i) < g.x, r); };
     // a warp (64 dimensions: half of one) sums a row over all pieces, or with few rows over a
     // part of them, a lane four dimensions; every lane knows the weights of 32 (16) pieces at a time
-    constexpr int LANES = QUADS, UNITS = ROWS_THREADS / LANES, AHEAD = 4;
+    constexpr int LANES = QUADS, UNITS = ROWS_THREADS / LANES, AHEAD = 3;  // a fourth is spilled, in the inner loop too
     static_assert(UNITS <= ROWS, "sums");
     const unsigned group = LANES == 32 ? 0xFFFFFFFFu : 0xFFFFu << (lane & 16);
     const int gl = lane % LANES;
