@@ -87,7 +87,8 @@ typedef struct cs_kv_batch {
   int tokens;                 /* rows of the token-indexed tensors, padding included; <= max_tokens */
   int seqs;                   /* <= max_seqs */
   int max_q;                  /* no sequence brings more new tokens than this (it chooses the kernel) */
-  int table_cols;             /* columns of the page table; table_cols * page_size <= 2^22 */
+  int table_cols;             /* columns of the page table; table_cols * page_size <= 2^22.  Of a table no wider
+                                 than the longest sequence needs, short prompts are divided best */
   const int32_t* cu_q;        /* [seqs + 1], not decreasing, within 0 .. tokens */
   const int32_t* kv_lens;     /* [seqs], within n .. table_cols * page_size (below n: the tokens before
                                  position 0 see no key) */
