@@ -161,15 +161,17 @@ def _whole(t, shape, dtype, device, name) -> int:
 
 def _rows(t, tokens, heads, head_dim, dtype, device, name):
     """(pointer, row stride) of a token-indexed tensor: [tokens, width] or
-    [tokens, heads, head_dim], rows contiguous, any row stride."""
+    [tokens, heads, head_dim], each row contiguous, rows at least their width apart
+    (a broadcast row's stride 0 would mean "packed rows" to the library)."""
+    width = heads * head_dim
     if isinstance(t, torch.Tensor) and t.dtype is dtype and t.get_device() == device:
         shape, stride = t.shape, t.stride()
-        if (len(shape) == 2 and shape[0] == tokens and shape[1] == heads * head_dim and stride[1] == 1) or (
+        if ((len(shape) == 2 and shape[0] == tokens and shape[1] == width and stride[1] == 1) or (
                 len(shape) == 3 and shape[0] == tokens and shape[1] == heads and shape[2] == head_dim
-                and stride[2] == 1 and (stride[1] == head_dim or heads == 1)):
+                and stride[2] == 1 and (stride[1] == head_dim or heads == 1))) and (tokens <= 1 or stride[0] >= width):
             return t.data_ptr(), stride[0] if tokens > 1 else 0
-    raise _bad(name, t, f"a [{tokens}, {heads * head_dim}] or [{tokens}, {heads}, {head_dim}] {dtype} tensor on "
-                        f"cuda:{device} with contiguous rows")
+    raise _bad(name, t, f"a [{tokens}, {width}] or [{tokens}, {heads}, {head_dim}] {dtype} tensor on "
+                        f"cuda:{device} with contiguous rows that do not overlap")
 
 
 class KVBatch:
