@@ -143,22 +143,29 @@ __device__ __forceinline__ bool elect_one() {
 // timer and error record inlined everywhere the kernel had 156 KB of code, and its
 // warps waited for instructions; with a suspend-time hint a prompt of 8192 tokens
 // took 410 us instead of 397.)
-constexpr int WAIT_TRIES = 1 << 18;
+#ifndef CS_KV_WAIT_TRIES  // a test lets its waits run out
+#define CS_KV_WAIT_TRIES (1 << 18)
+#endif
+constexpr int SETTLE_TRIES = 1 << 18;  // for copies and MMAs in flight after a wait that ran out
+template <typename Try>
+CS_KV_BOTH bool wait_bounded(volatile int* abort, Try complete) {
+#pragma unroll 1
+  for (int i = 0; i < CS_KV_WAIT_TRIES; ++i) {
+    if (complete()) return true;
+    if (*abort) return false;
+  }
+  *abort = 1;
+  return false;
+}
 template <typename Ctl>
 __device__ __forceinline__ bool wait(uint64_t* bar, uint32_t parity, Ctl* sc) {
-#pragma unroll 1
-  for (int i = 0; i < WAIT_TRIES; ++i) {
-    if (cs::mbar_try_wait(bar, parity)) return true;
-    if (sc->abort) return false;
-  }
-  sc->abort = 1;
-  return false;
+  return wait_bounded(&sc->abort, [&] { return cs::mbar_try_wait(bar, parity); });
 }
 
 // The same for a whole warp, which goes on or gives up together.
 template <typename Ctl>
 __device__ __forceinline__ bool wait_warp(uint64_t* bar, uint32_t parity, Ctl* sc) {
-  if (__all_sync(0xFFFFFFFFu, cs::mbar_try_wait(bar, parity))) return true;
+  if (CS_KV_WAIT_TRIES > 0 && __all_sync(0xFFFFFFFFu, cs::mbar_try_wait(bar, parity))) return true;
   return __all_sync(0xFFFFFFFFu, wait(bar, parity, sc));
 }
 
@@ -169,7 +176,7 @@ __device__ void come_to_rest(AttnCtl<SLOTS>* sc, const AttnP& p) {
   record(p.b.ctrl, ERR_WATCHDOG, WHAT_WAIT, blockIdx.x);
   int tries = 0;
   auto settle = [&](uint64_t* bar, uint32_t parity) {
-    while (!cs::mbar_try_wait(bar, parity) && ++tries < WAIT_TRIES) {
+    while (!cs::mbar_try_wait(bar, parity) && ++tries < SETTLE_TRIES) {
     }
   };
   for (int i = 0; i < SLOTS; ++i) {
@@ -185,7 +192,7 @@ __device__ void come_to_rest(AttnCtl<SLOTS>* sc, const AttnP& p) {
 template <typename Ctl>
 __device__ __forceinline__ void take_turn(Ctl* sc) {
 #pragma unroll 1
-  for (int i = 0; i < WAIT_TRIES && atomicCAS(&sc->turn, 0, 1) != 0 && !sc->abort; ++i) {
+  for (int i = 0; i < CS_KV_WAIT_TRIES && atomicCAS(&sc->turn, 0, 1) != 0 && !sc->abort; ++i) {
   }
 }
 

@@ -59,11 +59,21 @@ struct alignas(1024) RowsShared {
   };
   Range range;
   unsigned long long scratch[ROWS_THREADS / 32];
-  int last, failed;
+  int last;
+  volatile int abort;  // a wait ran out
   uint64_t full[ROWS_WARPS][STAGES][2];  // [warp][stage][K, V]
   float2 ml[ROWS_WARPS][ROWS];  // each warp's maximum and sum of a row
   uint4 q[ROWS][D / 8 + 1];
 };
+
+// How many copies of K (which 0) or V (1) a warp has issued into a stage when it waits for K
+// (or, at_values, V) of its tile number `done`, `left` tiles before its segment's end: ST tiles
+// are on their way, and K of the next one as soon as K of this one is read.
+template <int ST>
+CS_KV_BOTH uint32_t rows_issued(int which, int stage, bool at_values, uint32_t done, int left) {
+  const uint32_t n = done + kv_min(left, ST) + (which == 0 && at_values && left > ST);
+  return (n - stage + ST - 1) / ST;
+}
 
 template <typename T, int D>
 __global__ void __launch_bounds__(ROWS_THREADS, ROWS_CTAS) cs_kv_rows_kernel(const __grid_constant__ AttnP p) {
@@ -73,7 +83,7 @@ __global__ void __launch_bounds__(ROWS_THREADS, ROWS_CTAS) cs_kv_rows_kernel(con
   constexpr int ST = RowsShared<D>::STAGES;
   if (threadIdx.x == 0) {
     for (int i = 0; i < ROWS_WARPS * ST * 2; ++i) cs::mbar_init(&sm.full[0][0][0] + i, 1);
-    sm.failed = 0;
+    sm.abort = 0;
     cs::fence_mbar_init();
     cs::prefetch_tmap(&p.k);
     cs::prefetch_tmap(&p.v);
@@ -89,17 +99,9 @@ __global__ void __launch_bounds__(ROWS_THREADS, ROWS_CTAS) cs_kv_rows_kernel(con
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, gq = lane >> 2, jq = lane & 3;
   constexpr int KB = D / 32, VB = D / 64;  // 16-byte pieces of a key per lane, of each of its four values
   uint32_t done = 0;  // tiles that this warp has read
-  // a copy of this warp; one that never comes (an error: the results mean nothing) is waited
-  // for with a limit, once
-  auto arrived = [&](int which, uint32_t n) {
-    uint64_t* bar = &sm.full[warp][n % ST][which];
-#pragma unroll 1
-    for (int i = 0; !cs::mbar_try_wait(bar, n / ST & 1u); ++i)
-      if (i >= WAIT_TRIES) {
-        if (atomicExch(&sm.failed, 1) == 0) record(B.ctrl, ERR_WATCHDOG, WHAT_WAIT, blockIdx.x);
-        break;
-      }
-  };
+  // a copy of this warp; one that never comes (an error) is waited for with a limit, and
+  // then all warps give up
+  auto arrived = [&](int which, uint32_t n) { return wait_warp(&sm.full[warp][n % ST][which], n / ST & 1u, &sm); };
   Walk walk(p.c, sm.range);
   Seg g;
   while (walk.next(B, p.c, g)) {
@@ -178,13 +180,15 @@ __global__ void __launch_bounds__(ROWS_THREADS, ROWS_CTAS) cs_kv_rows_kernel(con
       sm.q[x / (D / 8)][x % (D / 8)] = qv[i];
     }
     __syncthreads();  // the queries are there
+    int k = g.k0;
+    bool at_values = false;
 #pragma unroll 1
-    for (int k = g.k0; k < g.k1; ++k) {
+    for (; k < g.k1; ++k) {
       const int j0 = g.key0(p.c, k) + warp * 16;
       const int page = checked(next);  // of tile k + ST
       next = table_of(k + ST + 1);
       const int stage = done % ST;
-      arrived(0, done);
+      if (!arrived(0, done)) break;
       float s[2][4] = {};
 #pragma unroll
       for (int i = 0; i < KB; ++i) {
@@ -243,7 +247,10 @@ __global__ void __launch_bounds__(ROWS_THREADS, ROWS_CTAS) cs_kv_rows_kernel(con
       }
       const uint32_t a0 = Pair<T>::put(s[0][0], s[0][1]), a1 = Pair<T>::put(s[0][2], s[0][3]);
       const uint32_t a2 = Pair<T>::put(s[1][0], s[1][1]), a3 = Pair<T>::put(s[1][2], s[1][3]);
-      arrived(1, done);
+      if (!arrived(1, done)) {
+        at_values = true;
+        break;
+      }
       // values of keys that no row sees may be anything: zeros instead
       const bool part = j0 + 16 > g.hi || (j0 < g.lo && j0 + 16 > p.c.sinks);
 #pragma unroll
@@ -273,7 +280,20 @@ __global__ void __launch_bounds__(ROWS_THREADS, ROWS_CTAS) cs_kv_rows_kernel(con
       load(1, k + ST, page, done + ST);
       ++done;
     }
+    if (__builtin_expect(k < g.k1, 0) && lane == 0) {  // gave up: the copies on their way come to rest, with a limit
+      int tries = 0;
+#pragma unroll 1
+      for (int i = 0; i < 2 * ST; ++i) {
+        const uint32_t n = rows_issued<ST>(i & 1, i >> 1, at_values, done, g.k1 - k);
+        while (n > 0 && !cs::mbar_try_wait(&sm.full[warp][i >> 1][i & 1], (n - 1) & 1u) && ++tries < SETTLE_TRIES) {
+        }
+      }
+    }
     __syncthreads();  // every warp is done with its operands' memory
+    if (sm.abort) {  // a warp can set it before this barrier or behind the next one only
+      if (tid == 0) record(B.ctrl, ERR_WATCHDOG, WHAT_WAIT, blockIdx.x);
+      break;
+    }
     // the warps' states to shared memory
 #pragma unroll
     for (int x = 0; x < 2; ++x) {
