@@ -294,6 +294,21 @@ struct Seen {
   __device__ __forceinline__ int next(int k) const { return k + 1 >= sinks && k + 1 < a ? a : k + 1; }
 };
 
+// The phases of the query buffers' barriers.  MMA warp w reads buffer w of an item of two row
+// tiles and buffer 0 of an item of one; it waits for every copy into buffer 0 all the
+// same: a parity tells two phases apart, so a warp that passed one over could take the
+// copy of two items ago for the one it waits for.
+struct Queries {
+  uint32_t phase = 0;  // bit per buffer
+  template <typename Wait>  // wait(buffer, parity)
+  CS_KV_BOTH bool arrived(bool two, int w, Wait wait) {
+    bool ok = wait(0, phase & 1u);
+    if (ok && two && w == 1) ok = wait(1, phase >> 1);
+    phase ^= two ? 3u : 1u;
+    return ok;
+  }
+};
+
 // MMA warp w works for S buffer w: S = Q K^T, then, once the softmax has put P into the
 // first half of S, O += P V.  An item of two row tiles has one for each buffer; of an item
 // of one row tile the buffers take the key tiles in turn (and are joined at the end).
@@ -317,14 +332,14 @@ __device__ bool mma_role(const AttnP& p, AttnCtl<AttnShape<D>::SLOTS>* sc, uint8
   // Both warps watch every tile arrive, and give back the ones they do not read
   // too: a barrier's parity tells two phases apart, so no reader may be two behind.
   Ring<Sh::SLOTS> r;
-  uint32_t q_phase = 0, p_phase = 0;  // q_phase: bit per query buffer
+  Queries queries;
+  uint32_t p_phase = 0;
   bool ok = true;
   while (ok && walk.next(p.b, p.c, g)) {
     const bool two = g.s.n - g.item * p.c.per_item > p.per_tile;
     const int qw = two ? w : 0, count = g.k1 - g.k0;
-    ok = wait_warp(&sc->q_full[qw], (q_phase >> qw) & 1u, sc);
+    ok = queries.arrived(two, w, [&](int b, uint32_t parity) { return wait_warp(&sc->q_full[b], parity, sc); });
     if (!ok) break;
-    q_phase ^= two ? 3u : 1u;
     // both warps give the first queries back, warp 1 at once where it does not read them (the
     // wait above keeps it from doing so for an item before its queries are loaded)
     if (leader && w == 1 && (two || count == 1)) cs::mbar_arrive(&sc->q_empty[0]);
