@@ -153,6 +153,7 @@ struct cs_chain_s {
 };
 
 const cs_chain_desc* cs_chain_desc_of(cs_chain_t plan) { return &plan->d; }
+int cs_chain_device_of(cs_chain_t plan) { return plan->device; }
 
 namespace {
 

@@ -563,6 +563,8 @@ cs_status cs_attn_cached_forward(cs_chain_t chain, cs_kv_t p, const cs_kv_batch*
   if ((s = cs_chain_query(chain, &info)) != CS_OK) return s;
   const cs_chain_desc& cd = *cs_chain_desc_of(chain);
   if (cd.kind != CS_CHAIN_ATTN) return cs_fail(CS_ERR_INVALID_ARG, "chain is not an attention chain");
+  if (cs_chain_device_of(chain) != p->device)
+    return cs_fail(CS_ERR_INVALID_ARG, "the chain's plan is on device %d, the cache's on device %d", cs_chain_device_of(chain), p->device);
   const cs_kv_desc& d = p->d;
   if (d.dtype != cd.dtype || d.heads != cd.heads || d.kv_heads != cd.heads || d.head_dim != 128)
     return cs_fail(CS_ERR_INVALID_ARG, "the plans differ: dtype %d/%d, heads %d/%d, kv_heads %d, head_dim %d", cd.dtype, d.dtype,
@@ -582,6 +584,8 @@ cs_status cs_attn_cached_forward(cs_chain_t chain, cs_kv_t p, const cs_kv_batch*
   at.k_cache = ap.k_cache;
   at.v_cache = ap.v_cache;
   at.out = info.intermediate[1];
+  DeviceGuard g(p->device);
+  if (!g.ok) return cs_fail(CS_ERR_CUDA, "cannot select the plan's device");
   if ((s = cs_chain_forward_stage(chain, args, 0, stream)) != CS_OK) return s;
   if ((s = cs_kv_append(p, b, &ap, stream)) != CS_OK) return s;
   if ((s = cs_kv_attention(p, b, &at, stream)) != CS_OK) return s;

@@ -10,6 +10,9 @@ cs_status cs_fail(cs_status s, const char* fmt, ...);
 // The desc that a plan runs (tuning-table choices applied).
 const cs_chain_desc* cs_chain_desc_of(cs_chain_t plan);
 
+// The device that a plan was made on.
+int cs_chain_device_of(cs_chain_t plan);
+
 // Looks up the tuning-table entry for a desc run on num_sms SMs.  Returns the
 // entry's index, or -1 when the table is not consulted (desc->tuned < 0, or no
 // field it may fill is auto) or holds no entry for this shape.  On a match,

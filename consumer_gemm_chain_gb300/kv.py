@@ -267,6 +267,9 @@ def cs_attn_cached_forward(chain: Plan, plan: KVPlan, batch: KVBatch, X, Wqkv, W
                            positions=None, stream=None) -> None:
     """One attention layer over the cache: QKV = X Wqkv, append with rotation, attention, Y = O Wo."""
     args = _attn_args(chain, X, Wqkv, Wo, Y)
+    for name, t in (("X", X), ("Wqkv", Wqkv), ("Wo", Wo), ("Y", Y)):
+        if t is not None and t.get_device() != plan.device:
+            raise ValueError(f"{name} is on cuda:{t.get_device()}, the plan on cuda:{plan.device}")
     a = plan._append
     _append_args(plan, batch, a, k_cache, v_cache, rope, positions)
     _check(_lib.cs_attn_cached_forward(chain.handle, plan.handle, batch._ref, byref(args), byref(a), _stream(stream, plan.device)),

@@ -146,7 +146,7 @@ cs_status cs_kv_attention_shared(cs_kv_t plan, const cs_kv_batch* batch, const i
 /* An attention chain's forward over the cache: QKV = X Wqkv (stage 0 of `chain`,
  * a plan of kind CS_CHAIN_ATTN), append with rotation (in place in the chain's
  * QKV), attention over the cache into the chain's O, Y = O Wo (stage 2).  The
- * plans' dtypes agree, heads = kv_heads = the chain's heads, head_dim 128, and
+ * plans' devices and dtypes agree, heads = kv_heads = the chain's heads, head_dim 128, and
  * batch->tokens = the chain's M; the chain's plan must not split K (split_k = 1,
  * sk_tiles = -1).  append->qkv, qkv_stride, q_out and q_stride are not used.
  * Rows of Y behind the last sequence are not meaningful. */

@@ -22,6 +22,7 @@ struct cs_chain_s {
   int stages_run = 0;
 };
 const cs_chain_desc* cs_chain_desc_of(cs_chain_t chain) { return &chain->d; }
+int cs_chain_device_of(cs_chain_t chain) { return chain->device; }
 cs_status cs_chain_query(cs_chain_t chain, cs_chain_info* info) {
   *info = chain->info;
   return CS_OK;
