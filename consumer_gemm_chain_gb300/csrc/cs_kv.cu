@@ -357,17 +357,16 @@ cs_status run_attention(cs_kv_s* p, cskv::AttnP& k, int max_rows, cudaStream_t s
   return launch(join_kernel(d), dim3((k.c.whole ? 1 : cskv::JOIN_CTAS) * p->num_sms), cskv::JOIN_THREADS, 0, &k, st);
 }
 
-cs_status append(cs_kv_s* p, const cs_kv_batch* b, const cs_kv_append_args* a, cudaStream_t st) {
+cs_status check_append(const cs_kv_s* p, const cs_kv_batch* b, const cs_kv_append_args* a, cskv::AppendP& k) {
   if (!a) return cs_fail(CS_ERR_INVALID_ARG, "args is NULL");
   const cs_kv_desc& d = p->d;
+  std::memset(&k, 0, sizeof(k));
   cs_status s = check_caches(a->k_cache, a->v_cache);
   if (s != CS_OK) return s;
   if (b->tokens > 0 && (!a->qkv || !a->q_out)) return cs_fail(CS_ERR_INVALID_ARG, "qkv and q_out are required");
   if (!aligned16(a->qkv) || !aligned16(a->q_out)) return cs_fail(CS_ERR_INVALID_ARG, "qkv and q_out must be 16-byte aligned");
   const long long q_width = static_cast<long long>(d.heads) * d.head_dim;
   const long long width = q_width + 2ll * d.kv_heads * d.head_dim;
-  cskv::AppendP k;
-  std::memset(&k, 0, sizeof(k));
   if ((s = row_stride("qkv_stride", a->qkv_stride, width, &k.qkv_stride)) != CS_OK) return s;
   if ((s = row_stride("q_stride", a->q_stride, q_width, &k.q_stride)) != CS_OK) return s;
   if (!(a->q_out == a->qkv && k.q_stride == k.qkv_stride) &&
@@ -377,7 +376,6 @@ cs_status append(cs_kv_s* p, const cs_kv_batch* b, const cs_kv_append_args* a, c
     if (!a->rope || a->rope_rows < 1) return cs_fail(CS_ERR_INVALID_ARG, "rope is required (rotary_dim=%d)", d.rotary_dim);
     if (!aligned16(a->rope)) return cs_fail(CS_ERR_INVALID_ARG, "rope must be 16-byte aligned");
   }
-  if (b->tokens == 0 || b->seqs == 0) return CS_OK;
   k.b = device_batch(p, b);
   k.qkv = static_cast<const uint4*>(a->qkv);
   k.q_out = static_cast<uint4*>(a->q_out);
@@ -392,15 +390,20 @@ cs_status append(cs_kv_s* p, const cs_kv_batch* b, const cs_kv_append_args* a, c
   k.half = d.rotary_pairing == CS_KV_HALF;
   k.head_chunks = d.head_dim / 8;
   k.units = (d.heads + 2 * d.kv_heads) * (d.head_dim / 16);
+  return CS_OK;
+}
+
+cs_status run_append(const cs_kv_s* p, cskv::AppendP& k, cudaStream_t st) {
+  if (k.b.tokens == 0 || k.b.seqs == 0) return CS_OK;
   // The lookups of a block's tokens go side by side, so several tokens cost one chain of
   // them; but not before there are two blocks an SM, and not beyond four or five rounds of
   // a block's threads.  Measured, one token a block and by this rule: 19743 tokens of 384
   // units 83 and 74 us, 1962 of 144 units 6.9 and 5.6 us; 253 of 640 units 4.1 us, two a block 4.6.
-  const int wanted = std::min(b->tokens / (2 * p->num_sms), 1152 / k.units);
+  const int wanted = std::min(k.b.tokens / (2 * p->num_sms), 1152 / k.units);
   k.tokens_per_block = std::max(1, std::min(wanted, cskv::APPEND_MAX_TOKENS));
-  const dim3 grid((b->tokens + k.tokens_per_block - 1) / k.tokens_per_block);
-  const void* fn = d.dtype == CS_BF16 ? (const void*)cskv::cs_kv_append_kernel<__nv_bfloat16>
-                                      : (const void*)cskv::cs_kv_append_kernel<__half>;
+  const dim3 grid((k.b.tokens + k.tokens_per_block - 1) / k.tokens_per_block);
+  const void* fn = p->d.dtype == CS_BF16 ? (const void*)cskv::cs_kv_append_kernel<__nv_bfloat16>
+                                         : (const void*)cskv::cs_kv_append_kernel<__half>;
   return launch(fn, grid, cskv::APPEND_THREADS, 0, &k, st);
 }
 
@@ -511,9 +514,11 @@ cs_status cs_kv_destroy(cs_kv_t p) {
 cs_status cs_kv_append(cs_kv_t p, const cs_kv_batch* b, const cs_kv_append_args* a, void* stream) {
   cs_status s = begin(p, b);
   if (s != CS_OK) return s;
+  cskv::AppendP k;
+  if ((s = check_append(p, b, a, k)) != CS_OK) return s;
   DeviceGuard g(p->device);
   if (!g.ok) return cs_fail(CS_ERR_CUDA, "cannot select the plan's device");
-  return append(p, b, a, static_cast<cudaStream_t>(stream));
+  return run_append(p, k, static_cast<cudaStream_t>(stream));
 }
 
 cs_status cs_kv_attention(cs_kv_t p, const cs_kv_batch* b, const cs_kv_attn_args* a, void* stream) {
@@ -584,11 +589,18 @@ cs_status cs_attn_cached_forward(cs_chain_t chain, cs_kv_t p, const cs_kv_batch*
   at.k_cache = ap.k_cache;
   at.v_cache = ap.v_cache;
   at.out = info.intermediate[1];
+  // what can be refused is, before any stage has run
+  cskv::AppendP ak;
+  cskv::AttnP k;
+  if ((s = check_append(p, b, &ap, ak)) != CS_OK || (s = check_attn(p, b, &at, k)) != CS_OK) return s;
   DeviceGuard g(p->device);
   if (!g.ok) return cs_fail(CS_ERR_CUDA, "cannot select the plan's device");
   if ((s = cs_chain_forward_stage(chain, args, 0, stream)) != CS_OK) return s;
-  if ((s = cs_kv_append(p, b, &ap, stream)) != CS_OK) return s;
-  if ((s = cs_kv_attention(p, b, &at, stream)) != CS_OK) return s;
+  if (b->seqs > 0) {
+    const cudaStream_t st = static_cast<cudaStream_t>(stream);
+    if ((s = run_append(p, ak, st)) != CS_OK) return s;
+    if ((s = run_attention(p, k, rows_of(k, b->max_q), st)) != CS_OK) return s;
+  }
   return cs_chain_forward_stage(chain, args, 2, stream);
 }
 

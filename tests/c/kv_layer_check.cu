@@ -38,6 +38,22 @@ int main() {
   chain.device = 1;
   REQUIRE(refused(append, "device 1"));
   chain.device = 0;
+  // arguments of the append
+  cs_kv_append_args a = append;
+  a.rope = nullptr;
+  REQUIRE(refused(a, "rope is required"));
+  a = append;
+  a.rope_rows = 0;
+  REQUIRE(refused(a, "rope is required"));
+  a = append;
+  a.rope = reinterpret_cast<const float*>(memory + 4);
+  REQUIRE(refused(a, "16-byte aligned"));
+  a = append;
+  a.k_cache = nullptr;
+  REQUIRE(refused(a, "k_cache and v_cache"));
+  a = append;
+  a.v_cache = memory + 8;
+  REQUIRE(refused(a, "16-byte aligned"));
   printf("ok\n");
   return 0;
 }
