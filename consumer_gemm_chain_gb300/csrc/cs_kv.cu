@@ -114,6 +114,19 @@ bool rows_overlap(const void* a, long long a_stride, long long a_width, const vo
   return off < 2 * a_width || off + 2 * b_width > pitch;
 }
 
+// Whether one of `rows` rows (16-bit elements) shares bytes with a contiguous range.
+bool rows_over(const void* a, long long stride, long long width, int rows, const void* range, long long bytes) {
+  if (!range || bytes <= 0) return false;
+  const long long pitch = 2 * stride, from = static_cast<const char*>(range) - static_cast<const char*>(a);
+  const long long r = from >= 0 ? from / pitch : -1;  // the last row that begins at or before the range
+  if (r >= 0 && r < rows && from < r * pitch + 2 * width) return true;
+  return r + 1 < rows && (r + 1) * pitch < from + bytes;
+}
+
+long long cache_bytes(const cs_kv_desc& d) {
+  return 2ll * d.num_pages * d.page_size * d.kv_heads * d.head_dim;
+}
+
 cs_status check_batch(const cs_kv_s* p, const cs_kv_batch* b) {
   if (!b) return cs_fail(CS_ERR_INVALID_ARG, "batch is NULL");
   if (b->tokens < 0 || b->tokens > p->d.max_tokens)
@@ -245,6 +258,15 @@ cs_status check_attn(const cs_kv_s* p, const cs_kv_batch* b, const cs_kv_attn_ar
   if (!aligned16(a->q) || !aligned16(a->out)) return cs_fail(CS_ERR_INVALID_ARG, "q and out must be 16-byte aligned");
   if (rows_overlap(a->q, q_stride, width, a->out, k.out_stride, width, b->tokens))
     return cs_fail(CS_ERR_INVALID_ARG, "out overlaps q");
+  const long long bytes = cache_bytes(d), lse_bytes = 4ll * b->tokens * d.heads;
+  if (rows_over(a->out, k.out_stride, width, b->tokens, a->k_cache, bytes) ||
+      rows_over(a->out, k.out_stride, width, b->tokens, a->v_cache, bytes))
+    return cs_fail(CS_ERR_INVALID_ARG, "out overlaps a cache");
+  if (rows_over(a->out, k.out_stride, width, b->tokens, a->lse, lse_bytes) ||
+      rows_over(a->q, q_stride, width, b->tokens, a->lse, lse_bytes) ||
+      rows_over(a->k_cache, bytes / 2, bytes / 2, 1, a->lse, lse_bytes) ||
+      rows_over(a->v_cache, bytes / 2, bytes / 2, 1, a->lse, lse_bytes))
+    return cs_fail(CS_ERR_INVALID_ARG, "lse overlaps another argument");
   k.b = device_batch(p, b);
   // a window as long as any sequence hides nothing
   k.c.window = d.window >= kMaxKeys ? 0 : d.window;
@@ -376,6 +398,13 @@ cs_status check_append(const cs_kv_s* p, const cs_kv_batch* b, const cs_kv_appen
     if (!a->rope || a->rope_rows < 1) return cs_fail(CS_ERR_INVALID_ARG, "rope is required (rotary_dim=%d)", d.rotary_dim);
     if (!aligned16(a->rope)) return cs_fail(CS_ERR_INVALID_ARG, "rope must be 16-byte aligned");
   }
+  const long long bytes = cache_bytes(d);
+  if (rows_over(a->k_cache, bytes / 2, bytes / 2, 1, a->v_cache, bytes))
+    return cs_fail(CS_ERR_INVALID_ARG, "k_cache and v_cache overlap");
+  for (const void* cache : {a->k_cache, a->v_cache})
+    if (rows_over(a->q_out, k.q_stride, q_width, b->tokens, cache, bytes) ||
+        rows_over(a->qkv, k.qkv_stride, width, b->tokens, cache, bytes))
+      return cs_fail(CS_ERR_INVALID_ARG, "qkv or q_out overlaps a cache");
   k.b = device_batch(p, b);
   k.qkv = static_cast<const uint4*>(a->qkv);
   k.q_out = static_cast<uint4*>(a->q_out);

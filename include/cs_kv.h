@@ -102,7 +102,7 @@ typedef struct cs_kv_append_args {
   void* q_out;                /* rows of heads * head_dim: the rotated queries; may be the Q part of
                                  qkv itself (rotation in place), else must not overlap it */
   long long q_stride;         /* elements between rows of q_out; 0 = heads * head_dim */
-  void* k_cache;
+  void* k_cache;              /* the caches overlap neither each other nor qkv nor q_out */
   void* v_cache;
   const float* rope;          /* [rope_rows, rotary_dim]: row p = rotary_dim / 2 cosines, then as many
                                  sines, of position p's angles.  Unused with rotary_dim 0 */
@@ -123,9 +123,9 @@ typedef struct cs_kv_attn_args {
   long long q_stride;         /* elements between rows; 0 = heads * head_dim */
   const void* k_cache;
   const void* v_cache;
-  void* out;                  /* rows of heads * head_dim; must not overlap q */
+  void* out;                  /* rows of heads * head_dim; must not overlap q or a cache */
   long long out_stride;       /* elements between rows; 0 = heads * head_dim */
-  float* lse;                 /* NULL, or [tokens, heads]: log of the sum of exp(score) */
+  float* lse;                 /* NULL, or [tokens, heads]: log of the sum of exp(score); overlaps nothing else */
 } cs_kv_attn_args;
 
 /* O = softmax(scale Q K^T over the visible keys) V for every new token and head,
