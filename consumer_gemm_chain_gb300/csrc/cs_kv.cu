@@ -391,7 +391,7 @@ cs_status check_append(const cs_kv_s* p, const cs_kv_batch* b, const cs_kv_appen
   const long long width = q_width + 2ll * d.kv_heads * d.head_dim;
   if ((s = row_stride("qkv_stride", a->qkv_stride, width, &k.qkv_stride)) != CS_OK) return s;
   if ((s = row_stride("q_stride", a->q_stride, q_width, &k.q_stride)) != CS_OK) return s;
-  if (!(a->q_out == a->qkv && k.q_stride == k.qkv_stride) &&
+  if (!(a->q_out == a->qkv && (k.q_stride == k.qkv_stride || b->tokens == 1)) &&
       rows_overlap(a->qkv, k.qkv_stride, width, a->q_out, k.q_stride, q_width, b->tokens))
     return cs_fail(CS_ERR_INVALID_ARG, "q_out overlaps qkv without being its Q part");
   if (d.rotary_dim > 0) {

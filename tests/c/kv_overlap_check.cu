@@ -70,6 +70,14 @@ int main() {
   a.q_stride = W;
   REQUIRE(append(a) == CS_OK);
 
+  // one row in place: its stride means nothing
+  const cs_kv_batch single{1, 1, 1, 1, cu, lens, table};
+  a.q_stride = 0;
+  REQUIRE(append(a) == CS_ERR_INVALID_ARG);
+  REQUIRE(check_append(&plan, &single, &a, ak) == CS_OK);
+  a.q_out = mem(0) + 16;
+  REQUIRE(check_append(&plan, &single, &a, ak) == CS_ERR_INVALID_ARG);
+
   cs_kv_attn_args fine{};
   fine.q = mem(0);
   fine.out = mem(1);
