@@ -14,10 +14,17 @@
 #include "cs_kv_rows.cuh"
 #include "cs_tune.h"  // cs_fail
 
-#define KV_CUDA(call)                                                                              \
-  do {                                                                                             \
-    cudaError_t e_ = (call);                                                                       \
-    if (e_ != cudaSuccess) return cs_fail(CS_ERR_CUDA, "%s: %s", #call, cudaGetErrorString(e_));   \
+// A failure of the CUDA runtime that the call reports itself: the runtime keeps no last error,
+// which would fail the next check of whoever calls it after us.
+static cs_status cuda_failed(const char* what, cudaError_t e) {
+  cudaGetLastError();
+  return cs_fail(CS_ERR_CUDA, "%s: %s", what, cudaGetErrorString(e));
+}
+
+#define KV_CUDA(call)                                          \
+  do {                                                         \
+    const cudaError_t e_ = (call);                             \
+    if (e_ != cudaSuccess) return cuda_failed(#call, e_);      \
   } while (0)
 
 struct cs_kv_s {
@@ -52,6 +59,7 @@ struct DeviceGuard {
       ok = cudaSetDevice(device) == cudaSuccess;
       was = cur;
     }
+    if (!ok) cudaGetLastError();
   }
   ~DeviceGuard() {
     if (was >= 0) cudaSetDevice(was);
@@ -179,7 +187,7 @@ cs_status launch(const void* fn, dim3 grid, int threads, int smem, void* params,
   cfg.numAttrs = 1;
   void* args[] = {params};
   const cudaError_t e = cudaLaunchKernelExC(&cfg, fn, args);
-  if (e != cudaSuccess) return cs_fail(CS_ERR_CUDA, "kernel launch: %s", cudaGetErrorString(e));
+  if (e != cudaSuccess) return cuda_failed("kernel launch", e);
   return CS_OK;
 }
 
@@ -203,6 +211,7 @@ const Driver& driver() {
       cudaDriverEntryPointQueryResult q;
       const bool ok = cudaGetDriverEntryPointByVersion(name, &f, 12000, cudaEnableDefault, &q) == cudaSuccess &&
                       q == cudaDriverEntryPointSuccess;
+      if (!ok) cudaGetLastError();
       return ok ? f : nullptr;
     };
     d.encode = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(entry("cuTensorMapEncodeTiled"));
@@ -479,8 +488,9 @@ cs_status cs_kv_plan(const cs_kv_desc* desc, cs_kv_t* out) {
   cs_status s = validate(desc);
   if (s != CS_OK) return s;
   int dev = 0, sms = 0, major = 0, minor = 0;
-  if (cudaGetDevice(&dev) != cudaSuccess || cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
-    return cs_fail(CS_ERR_CUDA, "no CUDA device available");
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
+  if (e != cudaSuccess) return cuda_failed("no CUDA device available", e);
   cudaDeviceGetAttribute(&major, cudaDevAttrComputeCapabilityMajor, dev);
   cudaDeviceGetAttribute(&minor, cudaDevAttrComputeCapabilityMinor, dev);
   if (major * 10 + minor != 103)
@@ -516,6 +526,7 @@ cs_status cs_kv_plan(const cs_kv_desc* desc, cs_kv_t* out) {
   }
   if (cudaMemset(p->ctrl, 0, p->ctrl_words * 4) != cudaSuccess || cudaMemset(p->mend, 0, rows) != cudaSuccess ||
       cudaDeviceSynchronize() != cudaSuccess) {
+    cudaGetLastError();
     free_plan(p);
     return cs_fail(CS_ERR_CUDA, "clearing the plan's workspace failed");
   }
@@ -535,7 +546,7 @@ cs_status cs_kv_plan(const cs_kv_desc* desc, cs_kv_t* out) {
 cs_status cs_kv_destroy(cs_kv_t p) {
   if (!p) return CS_OK;
   DeviceGuard g(p->device);
-  cudaDeviceSynchronize();
+  if (cudaDeviceSynchronize() != cudaSuccess) cudaGetLastError();
   free_plan(p);
   return CS_OK;
 }
