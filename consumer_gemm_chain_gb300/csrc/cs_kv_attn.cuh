@@ -1036,7 +1036,8 @@ __global__ void __launch_bounds__(ATTN_THREADS, 1) cs_kv_attn_kernel(const __gri
   constexpr int bf16 = sizeof(T) == 2 && !std::is_same<T, __half>::value;
   if (warp < 8) {
     regs_inc<SOFTMAX_REGS>();
-    softmax_role<T, D, WINDOW>(p, sc, ring, warp >> 2);
+    // (a softmax that gave up may have stores to tensor memory on their way)
+    if (!softmax_role<T, D, WINDOW>(p, sc, ring, warp >> 2)) cs::tc_wait_st();
   } else {
     regs_dec<OTHER_REGS>();
     if (warp == 8) load_role<D>(p, sc, qbuf, ring);
