@@ -66,6 +66,12 @@ struct DeviceGuard {
   }
 };
 
+// The factor of the scores for exponents in base 2.
+float scale_log2(const cs_kv_desc& d) {
+  const double scale = d.scale > 0.0f ? d.scale : 1.0 / std::sqrt(static_cast<double>(d.head_dim));
+  return static_cast<float>(scale * 1.4426950408889634);
+}
+
 cs_status validate(const cs_kv_desc* d) {
   if (!d) return cs_fail(CS_ERR_INVALID_ARG, "desc is NULL");
   if (d->dtype != CS_F16 && d->dtype != CS_BF16) return cs_fail(CS_ERR_INVALID_ARG, "bad dtype %d", d->dtype);
@@ -89,8 +95,8 @@ cs_status validate(const cs_kv_desc* d) {
     return cs_fail(CS_ERR_INVALID_ARG, "bad rotary_pairing %d", d->rotary_pairing);
   if (d->window < 0) return cs_fail(CS_ERR_INVALID_ARG, "window=%d", d->window);
   if (d->sinks < 0) return cs_fail(CS_ERR_INVALID_ARG, "sinks=%d", d->sinks);
-  if (!(d->scale >= 0.0f) || std::isinf(d->scale))
-    return cs_fail(CS_ERR_INVALID_ARG, "scale=%g (positive, or 0 for 1/sqrt(head_dim))", d->scale);
+  if (!(d->scale >= 0.0f) || std::isinf(scale_log2(*d)))
+    return cs_fail(CS_ERR_INVALID_ARG, "scale=%g (positive and below 2.35e38, or 0 for 1/sqrt(head_dim))", d->scale);
   if (d->shared != 0 && d->shared != 1) return cs_fail(CS_ERR_INVALID_ARG, "shared=%d (0 or 1)", d->shared);
   if (d->shared && d->window > 0) return cs_fail(CS_ERR_UNSUPPORTED, "a shared prefix is built without a window");
   if (static_cast<long long>(d->num_pages) * d->kv_heads * (d->page_size / 8) >= (1ll << 31))
@@ -283,8 +289,7 @@ cs_status check_attn(const cs_kv_s* p, const cs_kv_batch* b, const cs_kv_attn_ar
   k.c.item_cost = 1;
   k.out = a->out;
   k.lse = a->lse;
-  const double scale = d.scale > 0.0f ? d.scale : 1.0 / std::sqrt(static_cast<double>(d.head_dim));
-  k.scale_log2 = static_cast<float>(scale * 1.4426950408889634);
+  k.scale_log2 = scale_log2(d);
   k.part = p->part;
   k.other = p->other;
   k.splits = p->splits;
