@@ -18,11 +18,13 @@
 // Bound.  Per tile of 128 x 128 weights the tensor core needs 8 x 64 cycles for S and as
 // many for P V at 128 dimensions (half at 64), the two softmax warpgroups together about
 // 960 issue cycles per scheduler and pair of tiles.  A prompt of 8192 tokens, 32 / 8 heads of 128:
-// 395 us, 1390 TFLOP/s, 0.72 of the 1925 that a library product of 8192^3 measured;
-// pieces of prompts over 2000 to 20000 keys, 40 / 8 heads of 64: 420 us, 904 TFLOP/s,
-// where the softmax is the longer part.  The counters (4096 tokens) have the tensor core busy
+// 401 us, 1370 TFLOP/s, 0.71 of the 1925 that a library product of 8192^3 measured;
+// pieces of prompts over 2000 to 20000 keys, 40 / 8 heads of 64: 424 us, 895 TFLOP/s.
+// The counters (4096 tokens) have the tensor core busy
 // in 58 % of the cycles (38 % at 64 dimensions), issue slots 32 % (42 %), DRAM 7 %: no
-// unit is full, the chain S -> softmax -> P V of each buffer sets the pace.
+// unit is full, the chain S -> softmax -> P V of each buffer sets the pace.  A pair of tiles
+// takes about 3500 cycles at 128 dimensions and 2500 at 64, where its products are 2048 and
+// 1024: the same 1400 or so of latency in both.
 #pragma once
 #include "cs_kv_sched.cuh"
 
@@ -39,7 +41,7 @@ struct Split {
 
 struct AttnP {
   CUtensorMap q, k, v;    // for cs_kv_attn_kernel
-  const void *q_raw, *k_raw, *v_raw;  // for cs_kv_rows_kernel
+  const void *q_raw, *k_raw, *v_raw;  // the tensors themselves: q for cs_kv_rows_kernel, all for mend_row
   long long q_stride;
   Batch b;
   Cut c;

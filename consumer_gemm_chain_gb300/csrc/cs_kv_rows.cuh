@@ -14,13 +14,17 @@
 // bound here.
 //
 // 64 single tokens over 300 to 32000 keys, 64 / 8 heads of 128 (4.26 GB of keys and values):
-// 680 to 698 us, 6.1 to 6.3 TB/s, 0.90 to 0.93 of a plain copy's measured 6.8; DRAM is what
-// bounds it.  128 single tokens under a window of 1024: 93.5 us, 5.7 TB/s; one user's token
-// over 978 keys, 12 heads: 8.8 us, launch, lookups, a tile's latency and the joining one
-// after another.  With 16 rows the joins count: 8 sequences of up to 4 tokens over up to 2000 keys
+// 664 to 692 us on several cards, 6.2 to 6.4 TB/s, 0.91 to 0.95 of a plain copy's measured 6.8;
+// DRAM bounds it.  (The tensor-core kernel, whose rows are nearly all empty here, measured 662
+// us when it still took this case: over long contexts either is at the memory's rate.  What
+// this kernel is for is the rest: one user's token 31.6 us with that kernel, 135 under the
+// window.)  128 single tokens under a window of 1024: 93 us, 5.7 TB/s; one user's token over
+// 978 keys, 12 heads: 8.9 us, launch, lookups, a tile's latency and the joining one after
+// another.  With 16 rows the joins count: 8 sequences of up to 4 tokens over up to 2000 keys
 // take 26 us where single tokens take 16 (38 with one dimension a thread; reading all
-// of a thread's rows at once needs 540 bytes of spills, and everything is slower).  Fetching a segment's first tiles while the one before is joined was slower
-// (decode over long contexts 690 -> 703 us, one user's 9.3 -> 10.1): it needs registers
+// of a thread's rows at once needs 540 bytes of spills, and everything is slower).
+// Fetching a segment's first tiles while the one before is joined was slower (decode over
+// long contexts 690 -> 703 us, one user's 9.3 -> 10.1): it needs registers
 // that the inner loop has not got, and three CTAs an SM cover for each other already.
 #pragma once
 #include <climits>

@@ -24,8 +24,11 @@
  * stream as void*, calls only enqueue).  The lengths, page tables and positions
  * are read on the device, so a captured call may be replayed with other ones as
  * long as they fit what the call was made with.  Ones that do not fit never
- * cause an access out of bounds: the sequence, token or page is left out and the
- * device error is reported by cs_kv_status.  A plan is not thread-safe and runs
+ * cause an access out of bounds, and cs_kv_status reports the device error.  A
+ * sequence whose lengths do not fit is left out (its rows stay as they were),
+ * and so is an appended token whose page or position does not.  What attention gives a
+ * sequence with such a page means nothing, nor, where the prefix has one or the
+ * lengths under a prefix do not fit, what it gives the batch.  A plan is not thread-safe and runs
  * on one stream at a time (its workspace is per plan): two captured graphs that
  * may run at the same time need a plan each.
  */
@@ -87,8 +90,9 @@ typedef struct cs_kv_batch {
   int tokens;                 /* rows of the token-indexed tensors, padding included; <= max_tokens */
   int seqs;                   /* <= max_seqs */
   int max_q;                  /* no sequence brings more new tokens than this (it chooses the kernel) */
-  int table_cols;             /* columns of the page table; table_cols * page_size <= 2^22.  Of a table no wider
-                                 than the longest sequence needs, short prompts are divided best */
+  int table_cols;             /* columns of the page table; table_cols * page_size <= 2^22.  The width also
+                                 chooses how prompts are divided: with a table no wider than the longest
+                                 sequence needs, short ones take about two thirds of the time */
   const int32_t* cu_q;        /* [seqs + 1], not decreasing, within 0 .. tokens */
   const int32_t* kv_lens;     /* [seqs], within n .. table_cols * page_size (below n: the tokens before
                                  position 0 see no key) */
@@ -131,7 +135,7 @@ typedef struct cs_kv_attn_args {
 /* O = softmax(scale Q K^T over the visible keys) V for every new token and head,
  * scores, sums and O in 32 bits (the weights enter the product with V rounded to
  * the dtype).  A token that sees no key (before position 0) gets O = 0 and
- * lse = -inf.  Nothing that the cache holds at hidden keys changes a result. */
+ * lse = -inf, and so does one whose scores are all -infinity.  Nothing that the cache holds at hidden keys changes a result. */
 cs_status cs_kv_attention(cs_kv_t plan, const cs_kv_batch* batch, const cs_kv_attn_args* args, void* stream);
 
 /* The same where every sequence's keys follow one common prefix of prefix_len
