@@ -15,6 +15,7 @@ with host buffers, and the fp64 CPU oracle timed on the host cores.
 
 Usage:  python bench.py [--gpus N] [--steps K] [--warmup W] [--workload gpt3|stress|llama]
                         [--M M] [--policy tile|row|strided|stream] [--quick] [--impl reference]
+                        [--details FILE]
 """
 from __future__ import annotations
 
@@ -136,6 +137,8 @@ def parse(argv=None):
                     help="profiling aid: launch stage STAGE of the chain alone once, then the cuBLAS GEMM "
                          "of the same shape (via torch) once, and exit; no other kernel runs")
     ap.add_argument("--impl", default="ours", choices=["ours", "reference"])
+    ap.add_argument("--details", default=None, metavar="FILE",
+                    help="write the line with every plan and timeline of the other workloads there")
     ap.add_argument("--cpu-seconds", type=float, default=10.0, help="target CPU-oracle sample time")
     return ap.parse_args(argv)
 
@@ -670,10 +673,31 @@ def main():
                                 "sample": f"first {rows} of {M} rows, {dt:.1f} s, numpy float64 BLAS"}
     cs.cs_chain_destroy(plan)
     if rank == 0:
-        print(json.dumps(line), flush=True)
+        print(json.dumps(shortened(line, args.details)), flush=True)
     if ws > 1:
         import torch.distributed as dist
         dist.destroy_process_group()
+
+
+def short_configs(full):
+    """The other workloads' rows with what a reader of one line wants of them."""
+    def us(rec, *keys):
+        return next((round(rec[k], 2) for k in keys if k in rec), None)
+    return {name: [{"M": r["M"], "us": us(r, "tile_us", "row_us"), "control_us": us(r, "stream_us"),
+                    "roofline_frac": round(r["roofline_frac"], 4) if "roofline_frac" in r else None} for r in rows]
+            for name, rows in full.items()}
+
+
+def shortened(line, details):
+    """The line as printed, a few KB (with every plan and timeline of the other workloads it was
+    33 KB, which its readers cut off); all of it goes to the file `details`, if one is named."""
+    if details:
+        with open(details, "w") as f:
+            json.dump(line, f)
+    extra = line.get("extras", {})
+    if "other_configs" not in extra:
+        return line
+    return {**line, "extras": {**extra, "other_configs": short_configs(extra["other_configs"])}}
 
 
 def solo_vs_cublas(cs, torch, plan, info, dev, Y, inp, lay, stage):
