@@ -255,6 +255,8 @@ def cs_kv_attention_shared(plan: KVPlan, batch: KVBatch, q, k_cache, v_cache, pr
                            stream=None) -> None:
     """The same where every sequence's keys follow the ``prefix_len`` keys of ``prefix_pages`` (int32)."""
     a = _kv_attn_args(plan, batch, q, k_cache, v_cache, out, lse)
+    if prefix_len < 0:
+        raise ValueError(f"prefix_len={prefix_len}")
     need = -(-prefix_len // plan.desc.page_size)
     if not isinstance(prefix_pages, torch.Tensor) or prefix_pages.dim() != 1 or prefix_pages.shape[0] < need:
         raise _bad("prefix_pages", prefix_pages, f"a 1-D int32 tensor of at least {need} pages")

@@ -69,3 +69,14 @@ def test_rows_apart_are_taken(cs, name):
                       (1, torch.zeros(w, dtype=F16).expand(1, w)), (0, torch.zeros(0, w, dtype=F16))):
         with pytest.raises(cs.CSError, match="plan is NULL"):
             calls(cs, tokens)[name](x)
+
+
+@pytest.mark.parametrize("length", [-1, -(1 << 32) + 100, -(1 << 31), 65, 1 << 31, (1 << 32) + 20])
+def test_prefix_lengths_that_do_not_fit_the_pages(cs, length):
+    """A length that 32 bits do not hold must not reach the library as another one."""
+    plan = SimpleNamespace(handle=None, device=-1, dtype=F16, desc=cs.cs_kv_desc_init(heads=HEADS, kv_heads=KV_HEADS, head_dim=DIM),
+                           cache_shape=(4, 16, KV_HEADS, DIM), _attn=cs.kv.cs_kv_attn_args())
+    batch = cs.KVBatch(cs.kv.cs_kv_batch_s(tokens=1), (), -1)
+    cache, row = torch.zeros(plan.cache_shape, dtype=F16), torch.zeros(1, WIDTH, dtype=F16)
+    with pytest.raises(ValueError, match="prefix"):
+        cs.cs_kv_attention_shared(plan, batch, row, cache, cache, torch.zeros(4, dtype=torch.int32), length, row, stream=0)
