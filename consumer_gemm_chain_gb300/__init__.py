@@ -61,3 +61,11 @@ from .kv import (  # noqa: F401
     cs_kv_reset,
     cs_kv_status,
 )
+from .kv4 import (  # noqa: F401
+    cs_attn_cached4_forward,
+    cs_kv4_append,
+    cs_kv4_attention,
+    cs_kv4_attention_shared,
+    cs_kv4_read,
+    cs_kv4_shapes,
+)

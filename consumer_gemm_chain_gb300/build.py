@@ -20,8 +20,9 @@ LIB = os.path.join(LIBDIR, "libcs_chain.so")
 LIB_NOMC = os.path.join(LIBDIR, "libcs_chain_nomc.so")
 # (library, extra nvcc defines)
 VARIANTS = ((LIB, []), (LIB_NOMC, ["-DCS_NO_CLUSTER_MULTICAST"]))
-SOURCES = ["cs_chain.cu", "cs_kv.cu", "cs_tune.cpp"]
-DEPS = ["cs_chain.cu", "cs_kernel.cuh", "cs_kv.cu", "cs_kv_append.cuh", "cs_kv_sched.cuh", "cs_kv_attn.cuh", "cs_kv_rows.cuh", "cs_ptx.cuh", "cs_sched.cuh", "cs_tune.cpp", "cs_tune.h"]
+SOURCES = ["cs_chain.cu", "cs_kv.cu", "cs_kv4.cu", "cs_tune.cpp"]
+DEPS = ["cs_chain.cu", "cs_kernel.cuh", "cs_kv.cu", "cs_kv_host.cuh", "cs_kv_append.cuh", "cs_kv_sched.cuh", "cs_kv_attn.cuh", "cs_kv_rows.cuh", "cs_kv4.cu", "cs_kv4_codes.cuh",
+        "cs_kv4_append.cuh", "cs_kv4_rows.cuh", "cs_ptx.cuh", "cs_sched.cuh", "cs_tune.cpp", "cs_tune.h"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
 
@@ -36,7 +37,7 @@ def _stale(lib: str) -> bool:
     if not os.path.exists(lib):
         return True
     t = os.path.getmtime(lib)
-    deps = [os.path.join(CSRC, d) for d in DEPS] + [os.path.join(ROOT, "include", h) for h in ("cs_chain.h", "cs_kv.h")]
+    deps = [os.path.join(CSRC, d) for d in DEPS] + [os.path.join(ROOT, "include", h) for h in ("cs_chain.h", "cs_kv.h", "cs_kv4.h")]
     return any(os.path.exists(d) and os.path.getmtime(d) > t for d in deps)
 
 
@@ -50,7 +51,7 @@ def build(force: bool = False, verbose: bool = False) -> str:
     procs = []
     for lib, defs in todo:
         tmp = lib + f".tmp{os.getpid()}"
-        cmd = [_nvcc(), *ARCH, *defs, "-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC,-O2", "-shared",
+        cmd = [_nvcc(), *ARCH, *defs, "-O3", "-lineinfo", "-std=c++17", "--threads", str(len(SOURCES)), "-Xcompiler", "-fPIC,-O2", "-shared",
                "-I", os.path.join(ROOT, "include"), "-o", tmp] + [os.path.join(CSRC, s) for s in SOURCES]
         if verbose:
             cmd.insert(1, "-Xptxas=-v")

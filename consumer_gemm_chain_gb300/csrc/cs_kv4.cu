@@ -1,0 +1,252 @@
+// Host side of the paged key/value cache held in 4 bits (include/cs_kv4.h): argument
+// checks and launches.
+#include "../../include/cs_kv4.h"
+#include "cs_kv4_append.cuh"
+#include "cs_kv4_rows.cuh"
+#include "cs_kv_host.cuh"
+
+namespace {
+
+static_assert(cskv::ROWS4_CTAS<1> <= kRowsCtas && cskv::ROWS4_CTAS<2> <= kRowsCtas, "counters and pieces");
+
+long long code_bytes(const cs_kv_desc& d) {
+  return static_cast<long long>(d.num_pages) * d.page_size * d.kv_heads * d.head_dim / 2;
+}
+long long scale_bytes(const cs_kv_desc& d) { return code_bytes(d) / (cskv::GROUP4 / 2); }
+
+// The parts of the caches that are used, K's and V's.
+struct Parts {
+  Held held[4];
+  int count = 0;
+};
+
+cs_status add_cache(const cs_kv_desc& d, const char* name, const cs_kv4_cache& c, Parts& parts) {
+  if (!c.codes || !c.scales) return cs_fail(CS_ERR_INVALID_ARG, "the codes and scales of %s are required", name);
+  if (!aligned16(c.codes) || !aligned16(c.scales))
+    return cs_fail(CS_ERR_INVALID_ARG, "the codes and scales of %s must be 16-byte aligned", name);
+  parts.held[parts.count++] = {c.codes, code_bytes(d)};
+  parts.held[parts.count++] = {c.scales, scale_bytes(d)};
+  return CS_OK;
+}
+
+cs_status add_caches(const cs_kv_desc& d, const cs_kv4_cache& k, const cs_kv4_cache& v, Parts& parts) {
+  const cs_status s = add_cache(d, "k", k, parts);
+  return s != CS_OK ? s : add_cache(d, "v", v, parts);
+}
+
+template <typename T, int D>
+Kernels kernels_of(const cs_kv_s* p, int max_rows) {
+  const bool window = p->d.window > 0 && p->d.window < kMaxKeys, narrow = max_rows <= 8;
+  Kernels u;
+  u.rows = narrow ? (const void*)cskv::cs_kv4_rows_kernel<T, D, 1> : (const void*)cskv::cs_kv4_rows_kernel<T, D, 2>;
+  u.attn = window ? (const void*)cskv::cs_kv_attn_kernel<T, D, true, true> : (const void*)cskv::cs_kv_attn_kernel<T, D, false, true>;
+  u.join = (const void*)cskv::cs_kv_join_kernel<T, D, true>;
+  u.rows_grid = p->num_sms * (narrow ? cskv::ROWS4_CTAS<1> : cskv::ROWS4_CTAS<2>);
+  u.rows_smem = sizeof(cskv::Rows4Shared<D>);
+  u.attn_smem = cskv::AttnShape<D>::SMEM;
+  u.rows_map = u.attn_map = nullptr;
+  return u;
+}
+
+Kernels kernels(const cs_kv_s* p, int max_rows) {
+  if (p->d.dtype == CS_BF16)
+    return p->d.head_dim == 128 ? kernels_of<__nv_bfloat16, 128>(p, max_rows) : kernels_of<__nv_bfloat16, 64>(p, max_rows);
+  return p->d.head_dim == 128 ? kernels_of<__half, 128>(p, max_rows) : kernels_of<__half, 64>(p, max_rows);
+}
+
+// Once for a plan, on its device: the shared memory of its kernels.
+cs_status make_ready(cs_kv_s* p) {
+  if (p->four_ready) return CS_OK;
+  for (int rows : {1, 16}) {
+    const Kernels u = kernels(p, rows);
+    cudaError_t e = cudaFuncSetAttribute(u.rows, cudaFuncAttributeMaxDynamicSharedMemorySize, u.rows_smem);
+    if (e == cudaSuccess) e = cudaFuncSetAttribute(u.attn, cudaFuncAttributeMaxDynamicSharedMemorySize, u.attn_smem);
+    if (e != cudaSuccess) return cuda_failed("shared memory of the attention kernels", e);
+  }
+  p->four_ready = true;
+  return CS_OK;
+}
+
+cs_status check_attn4(const cs_kv_s* p, const cs_kv_batch* b, const cs_kv4_attn_args* a, cskv::AttnP& k) {
+  if (!a) return cs_fail(CS_ERR_INVALID_ARG, "args is NULL");
+  std::memset(&k, 0, sizeof(k));
+  Parts parts;
+  cs_status s = add_caches(p->d, a->k, a->v, parts);
+  if (s != CS_OK) return s;
+  k.k_raw = a->k.codes;
+  k.v_raw = a->v.codes;
+  k.k_scales = static_cast<const uint8_t*>(a->k.scales);
+  k.v_scales = static_cast<const uint8_t*>(a->v.scales);
+  return check_attn_rows(p, b, a->q, a->q_stride, a->out, a->out_stride, a->lse, parts.held, parts.count, k);
+}
+
+void fill_places(const cs_kv_s* p, const cs_kv_batch* b, const cs_kv4_cache& k, const cs_kv4_cache& v, cskv::Four4P& f) {
+  f.b = device_batch(p, b);
+  f.k_codes = static_cast<uint8_t*>(k.codes);
+  f.v_codes = static_cast<uint8_t*>(v.codes);
+  f.k_scales = static_cast<uint8_t*>(k.scales);
+  f.v_scales = static_cast<uint8_t*>(v.scales);
+  f.head_chunks = p->d.head_dim / 8;
+}
+
+cs_status check_append4(const cs_kv_s* p, const cs_kv_batch* b, const cs_kv4_append_args* a, cskv::Four4P& f) {
+  if (!a) return cs_fail(CS_ERR_INVALID_ARG, "args is NULL");
+  const cs_kv_desc& d = p->d;
+  std::memset(&f, 0, sizeof(f));
+  Parts parts;
+  cs_status s = add_caches(d, a->k, a->v, parts);
+  if (s != CS_OK) return s;
+  cs_kv_append_args rows{};
+  rows.qkv = a->qkv;
+  rows.qkv_stride = a->qkv_stride;
+  rows.q_out = a->q_out;
+  rows.q_stride = a->q_stride;
+  rows.rope = a->rope;
+  rows.rope_rows = a->rope_rows;
+  if ((s = check_append_rows(p, b, &rows, parts.held, parts.count, &f.qkv_stride, &f.q_stride)) != CS_OK) return s;
+  fill_places(p, b, a->k, a->v, f);
+  f.qkv = static_cast<const uint4*>(a->qkv);
+  f.q_out = static_cast<uint4*>(a->q_out);
+  f.rope = reinterpret_cast<const float4*>(a->rope);
+  f.positions = a->positions;
+  f.qkv_stride >>= 3;
+  f.q_stride >>= 3;
+  f.rope_rows = a->rope_rows;
+  f.rotary_dim = d.rotary_dim;
+  f.half = d.rotary_pairing == CS_KV_HALF;
+  f.units = (d.heads + 2 * d.kv_heads) * f.head_chunks;
+  return CS_OK;
+}
+
+// The rule of run_append (cs_kv.cu): several tokens a block once there are two blocks an SM, up to some
+// rounds of its threads.
+cs_status run_places(const cs_kv_s* p, const void* fn, cskv::Four4P& f, int rounds, cudaStream_t st) {
+  if (f.b.tokens == 0 || f.b.seqs == 0) return CS_OK;
+  const int wanted = std::min(f.b.tokens / (2 * p->num_sms), rounds * cskv::FOUR_THREADS / f.units);
+  f.tokens_per_block = std::max(1, std::min(wanted, cskv::FOUR_MAX_TOKENS));
+  const dim3 grid((f.b.tokens + f.tokens_per_block - 1) / f.tokens_per_block);
+  return launch(fn, grid, cskv::FOUR_THREADS, 0, &f, st);
+}
+
+cs_status run_append4(const cs_kv_s* p, cskv::Four4P& f, cudaStream_t st) {
+  const void* fn = p->d.dtype == CS_BF16 ? (const void*)cskv::cs_kv4_append_kernel<__nv_bfloat16>
+                                         : (const void*)cskv::cs_kv4_append_kernel<__half>;
+  return run_places(p, fn, f, 9, st);
+}
+
+cs_status check_read4(const cs_kv_s* p, const cs_kv_batch* b, const cs_kv4_read_args* a, cskv::Four4P& f) {
+  if (!a) return cs_fail(CS_ERR_INVALID_ARG, "args is NULL");
+  const cs_kv_desc& d = p->d;
+  std::memset(&f, 0, sizeof(f));
+  const long long width = static_cast<long long>(d.kv_heads) * d.head_dim;
+  cs_status s;
+  if (b->tokens > 0 && !a->k_out && !a->v_out) return cs_fail(CS_ERR_INVALID_ARG, "k_out or v_out is required");
+  if (!aligned16(a->k_out) || !aligned16(a->v_out)) return cs_fail(CS_ERR_INVALID_ARG, "k_out and v_out must be 16-byte aligned");
+  Parts parts;
+  if (a->k_out && (s = add_cache(d, "k", a->k, parts)) != CS_OK) return s;
+  if (a->v_out && (s = add_cache(d, "v", a->v, parts)) != CS_OK) return s;
+  if ((s = row_stride("k_stride", a->k_stride, width, &f.k_stride)) != CS_OK) return s;
+  if ((s = row_stride("v_stride", a->v_stride, width, &f.v_stride)) != CS_OK) return s;
+  if (a->k_out && a->v_out && rows_overlap(a->k_out, f.k_stride, width, a->v_out, f.v_stride, width, b->tokens))
+    return cs_fail(CS_ERR_INVALID_ARG, "k_out overlaps v_out");
+  for (int i = 0; i < parts.count; ++i)
+    if ((a->k_out && rows_over(a->k_out, f.k_stride, width, b->tokens, parts.held[i].at, parts.held[i].bytes)) ||
+        (a->v_out && rows_over(a->v_out, f.v_stride, width, b->tokens, parts.held[i].at, parts.held[i].bytes)))
+      return cs_fail(CS_ERR_INVALID_ARG, "k_out or v_out overlaps a cache");
+  fill_places(p, b, a->k, a->v, f);
+  f.k_out = static_cast<uint4*>(a->k_out);
+  f.v_out = static_cast<uint4*>(a->v_out);
+  f.k_stride >>= 3;
+  f.v_stride >>= 3;
+  f.units = ((a->k_out ? 1 : 0) + (a->v_out ? 1 : 0)) * d.kv_heads * (f.head_chunks / 2);
+  return CS_OK;
+}
+
+}  // namespace
+
+extern "C" {
+
+cs_status cs_kv4_append(cs_kv_t p, const cs_kv_batch* b, const cs_kv4_append_args* a, void* stream) {
+  cs_status s = begin(p, b);
+  if (s != CS_OK) return s;
+  cskv::Four4P f;
+  if ((s = check_append4(p, b, a, f)) != CS_OK) return s;
+  DeviceGuard g(p->device);
+  if (!g.ok) return cs_fail(CS_ERR_CUDA, "cannot select the plan's device");
+  return run_append4(p, f, static_cast<cudaStream_t>(stream));
+}
+
+cs_status cs_kv4_read(cs_kv_t p, const cs_kv_batch* b, const cs_kv4_read_args* a, void* stream) {
+  cs_status s = begin(p, b);
+  if (s != CS_OK) return s;
+  cskv::Four4P f;
+  if ((s = check_read4(p, b, a, f)) != CS_OK) return s;
+  DeviceGuard g(p->device);
+  if (!g.ok) return cs_fail(CS_ERR_CUDA, "cannot select the plan's device");
+  const void* fn = p->d.dtype == CS_BF16 ? (const void*)cskv::cs_kv4_read_kernel<__nv_bfloat16>
+                                         : (const void*)cskv::cs_kv4_read_kernel<__half>;
+  return run_places(p, fn, f, 9, static_cast<cudaStream_t>(stream));
+}
+
+cs_status cs_kv4_attention(cs_kv_t p, const cs_kv_batch* b, const cs_kv4_attn_args* a, void* stream) {
+  cs_status s = begin(p, b);
+  if (s != CS_OK) return s;
+  cskv::AttnP k;
+  if ((s = check_attn4(p, b, a, k)) != CS_OK) return s;
+  DeviceGuard g(p->device);
+  if (!g.ok) return cs_fail(CS_ERR_CUDA, "cannot select the plan's device");
+  if (b->tokens == 0 || b->seqs == 0) return CS_OK;
+  if ((s = make_ready(p)) != CS_OK) return s;
+  const int rows = rows_of(k, b->max_q);
+  return run_attention(p, k, kernels(p, rows), rows, static_cast<cudaStream_t>(stream));
+}
+
+cs_status cs_kv4_attention_shared(cs_kv_t p, const cs_kv_batch* b, const int32_t* prefix_pages, int prefix_len,
+                                  const cs_kv4_attn_args* a, void* stream) {
+  cs_status s = begin(p, b);
+  if (s != CS_OK) return s;
+  if ((s = check_prefix(p, prefix_pages, prefix_len)) != CS_OK) return s;
+  cskv::AttnP k;
+  if ((s = check_attn4(p, b, a, k)) != CS_OK) return s;
+  DeviceGuard g(p->device);
+  if (!g.ok) return cs_fail(CS_ERR_CUDA, "cannot select the plan's device");
+  if (b->tokens == 0 || b->seqs == 0) return CS_OK;
+  if ((s = make_ready(p)) != CS_OK) return s;
+  return run_shared(p, k, b, prefix_pages, prefix_len, [&](int rows) { return kernels(p, rows); }, static_cast<cudaStream_t>(stream));
+}
+
+cs_status cs_attn_cached4_forward(cs_chain_t chain, cs_kv_t p, const cs_kv_batch* b, const cs_attn_args* args,
+                                  const cs_kv4_append_args* append_args, void* stream) {
+  cs_status s = begin(p, b);
+  if (s != CS_OK) return s;
+  if (!chain || !args || !append_args) return cs_fail(CS_ERR_INVALID_ARG, "chain, args and append are required");
+  cs_chain_info info;
+  if ((s = check_layer(chain, p, b, info)) != CS_OK) return s;
+  cs_kv4_append_args ap = *append_args;
+  ap.qkv = info.intermediate[0];
+  ap.q_out = info.intermediate[0];
+  ap.qkv_stride = ap.q_stride = 3ll * p->d.heads * p->d.head_dim;
+  cs_kv4_attn_args at{};
+  at.q = info.intermediate[0];
+  at.q_stride = ap.qkv_stride;
+  at.k = ap.k;
+  at.v = ap.v;
+  at.out = info.intermediate[1];
+  // what can be refused is, before any stage has run
+  cskv::Four4P f;
+  cskv::AttnP k;
+  if ((s = check_append4(p, b, &ap, f)) != CS_OK || (s = check_attn4(p, b, &at, k)) != CS_OK) return s;
+  DeviceGuard g(p->device);
+  if (!g.ok) return cs_fail(CS_ERR_CUDA, "cannot select the plan's device");
+  if ((s = make_ready(p)) != CS_OK) return s;
+  if ((s = cs_chain_forward_stage(chain, args, 0, stream)) != CS_OK) return s;
+  if (b->seqs > 0) {
+    const cudaStream_t st = static_cast<cudaStream_t>(stream);
+    const int rows = rows_of(k, b->max_q);
+    if ((s = run_append4(p, f, st)) != CS_OK) return s;
+    if ((s = run_attention(p, k, kernels(p, rows), rows, st)) != CS_OK) return s;
+  }
+  return cs_chain_forward_stage(chain, args, 2, stream);
+}
+
+}  // extern "C"

@@ -1,0 +1,96 @@
+// Keys and values in 4 bits (include/cs_kv4.h): the format, and the instructions that make
+// 16-bit operands of it.
+//
+// A group is 32 consecutive dimensions of one key (value) of one head: a scale s, an unsigned
+// byte of 5 exponent and 3 mantissa bits (so a half has the byte at its bits 7 .. 14), and
+// 4-bit codes c + 8 with c in -7 .. 7.  A value is s c: 4 and 3 significant bits make at most
+// 7, which both 16-bit types hold, so what follows works with the values themselves and
+// rounds nothing.  Of the 8 values in a 32-bit word, value 2 j lies at bit 4 j and value
+// 2 j + 1 at bit 16 + 4 j: a mask then picks a pair in its 16-bit halves, in order.
+#pragma once
+#include "cs_kv_append.cuh"
+
+namespace cskv {
+
+constexpr int GROUP4 = 32;            // dimensions of a scale
+constexpr uint32_t SCALE_MOST = 0xF7;  // the largest finite scale, 61440
+constexpr uint32_t SCALE_NAN = 0xFF;
+
+// The row of a key's scales, [pages, kv_heads, page_size] (in units of head_dim / 32 bytes).
+__device__ __forceinline__ long long scale_row(const Batch& B, int page, int slot, int kh) {
+  return (static_cast<long long>(page) * B.kv_heads + kh) * B.page_size + slot;
+}
+
+__device__ __forceinline__ float scale_value(uint32_t byte) {
+  return __half2float(__ushort_as_half(static_cast<unsigned short>(byte << 7)));
+}
+
+// The byte of the scale nearest to a finite x >= 0 (ties to the even byte), at most the largest.
+__device__ __forceinline__ uint32_t scale_byte(float x) {
+  if (x < 6.103515625e-05f) return __float2uint_rn(x * 131072.0f);  // below 2^-14: steps of 2^-17
+  const uint32_t b = __float_as_uint(x);
+  const uint32_t r = ((b + 0x7FFFFu + (b >> 20 & 1u)) >> 20) - ((127 - 15) << 3);
+  return min(r, SCALE_MOST);
+}
+
+// Values 2 i, 2 i + 1 of a key's row of codes and scales.
+__device__ __forceinline__ float2 four_pair(const uint8_t* codes, const uint8_t* scales, int i) {
+  const uint32_t w = reinterpret_cast<const uint32_t*>(codes)[i >> 2] >> 4 * (i & 3);
+  const float s = scale_value(scales[i >> 4]);
+  return make_float2(s * (static_cast<int>(w & 15u) - 8), s * (static_cast<int>(w >> 16 & 15u) - 8));
+}
+
+// Two scales, and what turns codes into values.
+template <typename T>
+struct Four;
+
+// f16: code bits under the exponent of 1024 are 1024 + (c + 8), those of the next 4 bits 1024 + 16 (c + 8);
+// c is exact, and so is s c.  (One multiply-add from there would need 1032 s, which overflows for s > 63.)
+template <>
+struct Four<__half> {
+  __half2 s;
+  // the bytes at bits 0 and 16
+  __device__ __forceinline__ explicit Four(uint32_t bytes) {
+    bytes <<= 7;
+    s = *reinterpret_cast<__half2*>(&bytes);
+  }
+  static __device__ __forceinline__ __half2 low(uint32_t w) {
+    const uint32_t x = (w & 0x000F000Fu) | 0x64006400u, bias = 0x64086408u;  // 1032
+    return __hsub2(*reinterpret_cast<const __half2*>(&x), *reinterpret_cast<const __half2*>(&bias));
+  }
+  static __device__ __forceinline__ __half2 high(uint32_t w) {
+    const uint32_t x = (w & 0x00F000F0u) | 0x64006400u, by = 0x2C002C00u, bias = 0xD480D480u;  // 1/16, -72
+    return __hfma2(*reinterpret_cast<const __half2*>(&x), *reinterpret_cast<const __half2*>(&by),
+                   *reinterpret_cast<const __half2*>(&bias));
+  }
+  // the four pairs of a word
+  __device__ __forceinline__ void pairs(uint32_t w, uint32_t (&x)[4]) const {
+    __half2* y = reinterpret_cast<__half2*>(x);
+    y[0] = __hmul2(low(w), s);
+    y[1] = __hmul2(high(w), s);
+    y[2] = __hmul2(low(w >> 8), s);
+    y[3] = __hmul2(high(w >> 8), s);
+  }
+};
+
+// bf16: code bits under the exponent of 128 are 128 + (c + 8), and one multiply-add leaves s c: 136 s = 17 * 8 s
+// has 8 significant bits at most, and nothing is near the type's limits.
+template <>
+struct Four<__nv_bfloat16> {
+  __nv_bfloat162 s, off;
+  __device__ __forceinline__ explicit Four(uint32_t bytes) {
+    bytes <<= 7;
+    s = __float22bfloat162_rn(__half22float2(*reinterpret_cast<__half2*>(&bytes)));
+    const uint32_t bias = 0xC308C308u;  // -136
+    off = __hmul2(s, *reinterpret_cast<const __nv_bfloat162*>(&bias));
+  }
+  __device__ __forceinline__ void pairs(uint32_t w, uint32_t (&x)[4]) const {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const uint32_t y = (w >> 4 * i & 0x000F000Fu) | 0x43004300u;
+      *reinterpret_cast<__nv_bfloat162*>(&x[i]) = __hfma2(*reinterpret_cast<const __nv_bfloat162*>(&y), s, off);
+    }
+  }
+};
+
+}  // namespace cskv

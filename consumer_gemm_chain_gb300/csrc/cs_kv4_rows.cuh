@@ -1,0 +1,305 @@
+// Attention over a paged cache in 4 bits for few rows per key head (single tokens, or a few):
+// at most 16 (token, query head) rows of a sequence read each key.
+//
+// Items, tiles and joins are those of cs_kv_rows.cuh.  What differs: a key and its value are
+// 2 x (head_dim / 2 + head_dim / 32) bytes, so that making operands of codes costs
+// more than bringing them, and the products are turned round, S^T = K Q^T and O^T = V^T P^T:
+// the cache is the operand of 16 rows, the queries' 8 columns are all that single tokens need,
+// and each code is made an operand once for 8 (16) rows.
+//
+// Operands.  The order of the contracted dimensions is free as long as both operands agree on it.
+// A lane (g, t) of S^T's first operand has 32 (16) consecutive dimensions of two keys, under one
+// scale each; of V^T's it has 16 (8) dimensions of four keys: two keys' words, taken apart in
+// 16-bit halves and put together by dimension, make pairs along the keys.  P^T is the second operand of O^T:
+// an 8 x 8 transposition of S^T's accumulators (movmatrix).
+//
+// Row r of S^T's 8-row half is key r / 2 (r even) or 7 - r / 2 (r odd) of 8: with it all reads
+// of the codes from shared memory are free of bank conflicts.
+#pragma once
+#include "cs_kv_rows.cuh"
+
+namespace cskv {
+
+// Per SM: as many CTAs of four warps as registers allow with 8 (16) columns.
+template <int NT>
+constexpr int ROWS4_CTAS = NT == 1 ? 4 : 3;
+
+template <int D>
+struct Stage4 {  // 16 keys: codes of K and V, their scales
+  uint8_t codes[2][16][D / 2];
+  uint8_t scales[2][16][D / GROUP4];
+};
+
+template <int D>
+struct alignas(16) Rows4Shared {
+  static constexpr int STAGES = D == 128 ? 6 : 12;  // 12 KB on their way for each warp
+  union {
+    Stage4<D> ring[ROWS_WARPS][STAGES];
+    float o[ROWS_WARPS][ROWS][D + 4];  // each warp's output
+    float sum[ROWS][D + 4];            // of a part of an item's pieces: output, maximum, sum
+  };
+  Range range;
+  unsigned long long scratch[ROWS_THREADS / 32];
+  int last;
+  float2 ml[ROWS_WARPS][ROWS];  // each warp's maximum and sum of a row
+};
+
+// 16 bytes to shared memory, zeros where nothing is to be read.
+__device__ __forceinline__ void copy16(void* dst, const void* src, bool read) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(cs::smem_u32(dst)), "l"(src), "r"(read ? 16 : 0) : "memory");
+}
+__device__ __forceinline__ void copies_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void copies_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+// 8 x 8 transposition of 16-bit values
+__device__ __forceinline__ uint32_t transposed(uint32_t x) {
+  uint32_t y;
+  asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
+  return y;
+}
+
+// NT: groups of 8 rows
+template <typename T, int D, int NT>
+__global__ void __launch_bounds__(ROWS_THREADS, ROWS4_CTAS<NT>) cs_kv4_rows_kernel(const __grid_constant__ AttnP p) {
+  extern __shared__ __align__(1024) uint8_t rows_smem[];
+  Rows4Shared<D>& sm = *reinterpret_cast<Rows4Shared<D>*>(rows_smem);
+  constexpr int ST = Rows4Shared<D>::STAGES;
+  constexpr int KW = D / 32, VW = D / 64;  // 32-bit words of a key per lane, of each of its four values
+  const bool late = !p.c.flat && p.flat_o;  // as in cs_kv_rows_kernel
+  if (!late) cs::grid_dep_wait();
+  cs::grid_dep_launch_dependents();
+  const Batch& B = p.b;
+  find_range<ROWS_THREADS>(B, p.c, &sm.range, sm.scratch);
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, gq = lane >> 2, jq = lane & 3;
+  const int key0 = gq & 1 ? 7 - (gq >> 1) : gq >> 1;  // this lane's key of K, the other is 8 behind
+  const int key1 = jq, key2 = 7 - jq;                 // its keys of V, two more are 8 behind
+  Stage4<D>* const ring = sm.ring[warp];
+  // 16-byte piece `c` of key j lies at c ^ turn(j) in its row of 64 bytes (32 bytes: where it is)
+  auto turn = [](int j) { return D == 128 ? j & 2 : 0; };
+  Walk walk(p.c, sm.range);
+  Seg g;
+  while (walk.next(B, p.c, g)) {
+    const int first = g.item * p.c.per_item;  // the item's first token
+    const int tokens = min(p.c.per_item, g.s.n - first), rows = tokens * B.group;
+    const int* table = p.c.flat ? p.pages : B.table + static_cast<long long>(g.b) * B.table_cols;
+    const int base = g.s.m - g.s.n + first;  // position of its first token
+    // this warp's page of tile k, -1 if none of its keys is seen
+    auto table_of = [&](int k) {
+      if (k >= g.k1) return -1;
+      const int j0 = g.key0(p.c, k) + warp * 16;
+      if (j0 >= g.hi || (j0 + 16 <= g.lo && j0 >= p.c.sinks)) return -1;
+      const int page = __ldg(table + (j0 >> B.page_shift));
+      return page < 0 ? INT_MAX : page;
+    };
+    auto checked = [&](int page) {
+      if (page < B.num_pages) return page;
+      record(B.ctrl, ERR_INVALID, WHAT_PAGE, p.c.flat ? 0xFFFFFFFFu : static_cast<uint32_t>(g.b));
+      return -1;
+    };
+    auto load = [&](int k, int page, Stage4<D>& to) {
+      if (k < g.k1) {
+        const bool read = page >= 0;
+        const int slot = read ? (g.key0(p.c, k) + warp * 16) & (B.page_size - 1) : 0;
+        const long long at = read ? page * B.page_stride + slot * B.slot_stride + g.kvh * B.head_stride : 0;
+        constexpr int PIECES = D / GROUP4;  // of 16 bytes in a key's row
+#pragma unroll
+        for (int i = 0; i < 16 * PIECES / 32; ++i) {
+          const int x = lane + 32 * i, j = x / PIECES, c = x % PIECES;
+          const long long from = (at + j * B.slot_stride) / 2 + c * 16;
+          copy16(&to.codes[0][j][(c ^ turn(j)) * 16], static_cast<const uint8_t*>(p.k_raw) + from, read);
+          copy16(&to.codes[1][j][(c ^ turn(j)) * 16], static_cast<const uint8_t*>(p.v_raw) + from, read);
+        }
+        if (lane < 2 * PIECES) {  // 16 keys' scales lie side by side
+          const int v = lane / PIECES, c = lane % PIECES;
+          const long long from = read ? scale_row(B, page, slot, g.kvh) * PIECES + c * 16 : 0;
+          copy16(&to.scales[v][0][0] + c * 16, (v ? p.v_scales : p.k_scales) + from, read);
+        }
+      }
+      copies_commit();
+    };
+    int ahead[ST];
+#pragma unroll
+    for (int i = 0; i < ST; ++i) ahead[i] = table_of(g.k0 + i);
+    __syncthreads();  // shared memory of the segment before is read
+#pragma unroll
+    for (int i = 0; i < ST - 1; ++i) load(g.k0 + i, checked(ahead[i]), ring[i]);
+    int next = ahead[ST - 1];
+    // the queries, in the order of a key's words
+    uint4 q[NT][KW];
+#pragma unroll
+    for (int n = 0; n < NT; ++n) {
+      const int r = 8 * n + gq, t = r / B.group;
+      const uint4* from = reinterpret_cast<const uint4*>(static_cast<const T*>(p.q_raw) + (g.s.t0 + first + t) * p.q_stride +
+                                                         (g.kvh * B.group + r - t * B.group) * D) + jq * KW;
+#pragma unroll
+      for (int w = 0; w < KW; ++w) q[n][w] = r < rows ? from[w] : make_uint4(0, 0, 0, 0);
+    }
+    // keys [.., end) and from lo on, or below the sinks, are seen by rows 8 n + 2 jq + e
+    int end[NT][2], lo[NT][2];
+#pragma unroll
+    for (int n = 0; n < NT; ++n)
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        const int r = 8 * n + 2 * jq + e, pos = base + r / B.group;
+        end[n][e] = r >= rows ? 0 : p.c.flat ? g.s.m : pos + 1;
+        lo[n][e] = p.c.window > 0 ? max(0, pos + 1 - p.c.window) : 0;
+      }
+    // keys below all_end and from all_lo on are seen by every row
+    const int all_end = p.c.flat ? g.s.m : base + 1, all_lo = p.c.window > 0 ? max(0, base + tokens - p.c.window) : 0;
+    float o[NT][4 * VW][4];
+#pragma unroll
+    for (int n = 0; n < NT; ++n)
+#pragma unroll
+      for (int i = 0; i < 4 * VW; ++i)
+#pragma unroll
+        for (int c = 0; c < 4; ++c) o[n][i][c] = 0.0f;
+    float m_ref[NT][2], l[NT][2];
+#pragma unroll
+    for (int n = 0; n < NT; ++n) m_ref[n][0] = m_ref[n][1] = -INFINITY, l[n][0] = l[n][1] = 0.0f;
+    int at = 0;  // the stage of tile k
+#pragma unroll 1
+    for (int k = g.k0; k < g.k1; ++k) {
+      const int j0 = g.key0(p.c, k) + warp * 16;
+      copies_wait<ST - 2>();
+      __syncwarp();  // every lane's copies are there, and the stage before is read
+      load(k + ST - 1, checked(next), ring[at == 0 ? ST - 1 : at - 1]);
+      next = table_of(k + ST);
+      const Stage4<D>& st = ring[at];
+      at = at == ST - 1 ? 0 : at + 1;
+      float s[NT][4] = {}, s2[NT][4] = {};
+      {
+        uint32_t ka[KW], kb[KW];
+        const uint8_t* row = st.codes[0][key0] + (D == 128 ? (jq ^ turn(key0)) * 16 : jq * 8);
+        if constexpr (D == 128) {
+          *reinterpret_cast<uint4*>(ka) = *reinterpret_cast<const uint4*>(row);
+          *reinterpret_cast<uint4*>(kb) = *reinterpret_cast<const uint4*>(row + 8 * (D / 2));
+        } else {
+          *reinterpret_cast<uint2*>(ka) = *reinterpret_cast<const uint2*>(row);
+          *reinterpret_cast<uint2*>(kb) = *reinterpret_cast<const uint2*>(row + 8 * (D / 2));
+        }
+        const int group = D == 128 ? jq : jq >> 1;
+        const Four<T> fa(st.scales[0][key0][group] * 0x10001u), fb(st.scales[0][key0 + 8][group] * 0x10001u);
+#pragma unroll
+        for (int w = 0; w < KW; ++w) {
+          uint32_t a[4], b[4];
+          fa.pairs(ka[w], a);
+          fb.pairs(kb[w], b);
+#pragma unroll
+          for (int n = 0; n < NT; ++n) {
+            mma16816<T>(s[n], a[0], b[0], a[1], b[1], q[n][w].x, q[n][w].y);
+            mma16816<T>(s2[n], a[2], b[2], a[3], b[3], q[n][w].z, q[n][w].w);
+          }
+        }
+      }
+      const bool mask = !(j0 + 16 <= all_end && (j0 >= all_lo || j0 + 16 <= p.c.sinks));  // some key is hidden from some row
+      bool raise = false;
+      float mx[NT][2];
+#pragma unroll
+      for (int n = 0; n < NT; ++n) {
+#pragma unroll
+        for (int c = 0; c < 4; ++c) s[n][c] = (s[n][c] + s2[n][c]) * p.scale_log2;
+        if (mask) {
+#pragma unroll
+          for (int c = 0; c < 4; ++c) {
+            const int key = j0 + key0 + 8 * (c >> 1), e = c & 1;
+            if (!(key < end[n][e] && (key >= lo[n][e] || key < p.c.sinks))) s[n][c] = -INFINITY;
+          }
+        }
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          mx[n][e] = fmaxf(s[n][e], s[n][2 + e]);
+          // the reference is raised only when it is exceeded by more than 2^8
+          raise |= mx[n][e] > m_ref[n][e] + RAISE_LOG2 || (m_ref[n][e] == -INFINITY && mx[n][e] > -INFINITY);
+        }
+      }
+      if (__any_sync(0xFFFFFFFFu, raise)) {
+#pragma unroll
+        for (int n = 0; n < NT; ++n)
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            float top = mx[n][e];
+#pragma unroll
+            for (int d = 4; d < 32; d <<= 1) top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, d));
+            const bool up = top > m_ref[n][e] + RAISE_LOG2 || (m_ref[n][e] == -INFINITY && top > -INFINITY);
+            const float f = up ? cs::ex2_approx(m_ref[n][e] - top) : 1.0f;
+            if (up) m_ref[n][e] = top;
+            l[n][e] *= f;
+#pragma unroll
+            for (int i = 0; i < 4 * VW; ++i) o[n][i][e] *= f, o[n][i][2 + e] *= f;
+          }
+      }
+      uint32_t pt[NT][2];
+#pragma unroll
+      for (int n = 0; n < NT; ++n) {
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          const float sub = m_ref[n][e] == -INFINITY ? 0.0f : m_ref[n][e];
+          s[n][e] = cs::ex2_approx(s[n][e] - sub);
+          s[n][2 + e] = cs::ex2_approx(s[n][2 + e] - sub);
+          l[n][e] += s[n][e] + s[n][2 + e];
+        }
+        pt[n][0] = transposed(Pair<T>::put(s[n][0], s[n][1]));
+        pt[n][1] = transposed(Pair<T>::put(s[n][2], s[n][3]));
+      }
+      // V: words of keys key1, key2, key1 + 8 and key2 + 8
+      uint32_t v[4][VW];
+      uint32_t sv[4];
+#pragma unroll
+      for (int x = 0; x < 4; ++x) {
+        const int key = (x & 1 ? key2 : key1) + 8 * (x >> 1);
+        const uint8_t* row = st.codes[1][key] + (D == 128 ? (((gq >> 1) ^ turn(key)) * 16 + (gq & 1) * 8) : gq * 4);
+        if constexpr (D == 128)
+          *reinterpret_cast<uint2*>(v[x]) = *reinterpret_cast<const uint2*>(row);
+        else
+          v[x][0] = *reinterpret_cast<const uint32_t*>(row);
+        sv[x] = st.scales[1][key][D == 128 ? gq >> 1 : gq >> 2];
+      }
+      if (mask) {  // a scale of a key that no row sees may be anything
+#pragma unroll
+        for (int x = 0; x < 4; ++x) {
+          const int key = j0 + (x & 1 ? key2 : key1) + 8 * (x >> 1);
+          if (!(key < g.hi && (key >= g.lo || key < p.c.sinks))) sv[x] = 0;
+        }
+      }
+      const Four<T> fa(sv[0] | sv[1] << 16), fb(sv[2] | sv[3] << 16);
+#pragma unroll
+      for (int w = 0; w < VW; ++w) {
+        uint32_t a0[4], a1[4], a2[4], a3[4];  // even and odd dimensions of keys key1, key2; of those 8 behind
+        fa.pairs(__byte_perm(v[0][w], v[1][w], 0x5410), a0);
+        fa.pairs(__byte_perm(v[0][w], v[1][w], 0x7632), a1);
+        fb.pairs(__byte_perm(v[2][w], v[3][w], 0x5410), a2);
+        fb.pairs(__byte_perm(v[2][w], v[3][w], 0x7632), a3);
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+#pragma unroll
+          for (int n = 0; n < NT; ++n) mma16816<T>(o[n][4 * w + i], a0[i], a1[i], a2[i], a3[i], pt[n][0], pt[n][1]);
+      }
+    }
+    copies_wait<0>();
+    __syncthreads();  // every warp is done with the ring's memory
+    // the warps' states to shared memory: this lane has 8 VW dimensions of rows 8 n + 2 jq and 8 n + 2 jq + 1
+#pragma unroll
+    for (int n = 0; n < NT; ++n)
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        const int r = 8 * n + 2 * jq + e;
+        float sum = l[n][e];
+#pragma unroll
+        for (int d = 4; d < 32; d <<= 1) sum += __shfl_xor_sync(0xFFFFFFFFu, sum, d);
+        if (r < rows) {
+          if (gq == 0) sm.ml[warp][r] = make_float2(m_ref[n][e], sum);
+          float4* to = reinterpret_cast<float4*>(&sm.o[warp][r][8 * VW * gq]);
+#pragma unroll
+          for (int i = 0; i < 4 * VW; i += 2)
+            to[i / 2] = make_float4(o[n][i][e], o[n][i][2 + e], o[n][i + 1][e], o[n][i + 1][2 + e]);
+        }
+      }
+    __syncthreads();
+    rows_join<T, D>(p, g, first, rows, late, sm.o, sm.sum, sm.ml, sm.range, sm.last);
+  }
+  if (late) cs::grid_dep_wait();
+}
+
+}  // namespace cskv

@@ -26,6 +26,7 @@
 // takes about 3500 cycles at 128 dimensions and 2500 at 64, where its products are 2048 and
 // 1024: the same 1400 or so of latency in both.
 #pragma once
+#include "cs_kv4_codes.cuh"
 #include "cs_kv_sched.cuh"
 
 namespace cskv {
@@ -61,6 +62,7 @@ struct AttnP {
   int per_tile;           // tokens of a 128-row tile: 128 / group, rounded down; an item has two
   int out_wide;           // rows of out start on 32-byte boundaries
   int head_groups;        // 8-slot groups between heads (HEAD layout), 0: heads are a dimension of their own
+  const uint8_t *k_scales, *v_scales;  // of a cache in 4 bits, whose codes k_raw and v_raw are
 };
 
 // Two softmax warpgroups, one per S buffer with a row per thread, and one with the
@@ -270,6 +272,101 @@ __device__ bool load_role(const AttnP& p, AttnCtl<AttnShape<D>::SLOTS>* sc, uint
         if (two && k == g.k0 && half == 0 && !queries(1)) return false;
       }
       page = after;
+    }
+  }
+  return true;
+}
+
+// A cache in 4 bits: two warps make the tiles that load_role's copies bring, each 64 keys of
+// every tile, straight into the swizzled layout; the first one also has the queries copied.  A lane
+// has 32 dimensions of a key (16 bytes and their scale), the lanes of a store 8 keys, so that their
+// 16-byte pieces fall into different banks.  A few loads are on their way in registers.
+constexpr int LOAD4_WARPS = 2;
+template <typename T, int D>
+__device__ bool load4_role(const AttnP& p, AttnCtl<AttnShape<D>::SLOTS>* sc, uint8_t* qbuf, uint8_t* ring, int second) {
+  using Sh = AttnShape<D>;
+  constexpr int PIECES = D / GROUP4, ROWS_OF = 32 / PIECES, LOADS = 64 / ROWS_OF, AHEAD = 4;  // rows of a load, loads of a tile
+  const Batch& B = p.b;
+  const int lane = threadIdx.x & 31, row = lane % ROWS_OF, piece = lane / ROWS_OF;
+  Walk walk(p.c, sc->range);
+  Seg g;
+  Ring<Sh::SLOTS> rp;
+  uint32_t q_phase[2] = {1, 1};
+  uint4 codes[AHEAD];
+  uint32_t scale[AHEAD];
+  while (walk.next(B, p.c, g)) {
+    const int* table = p.c.flat ? p.pages : B.table + static_cast<long long>(g.b) * B.table_cols;
+    const bool two = g.s.n - g.item * p.c.per_item > p.per_tile;
+    auto queries = [&](int w) {
+      if (!wait_warp(&sc->q_empty[w], q_phase[w], sc)) return false;
+      q_phase[w] ^= 1u;
+      if (lane == 0) {
+        cs::mbar_arrive_expect_tx(&sc->q_full[w], static_cast<uint32_t>(p.per_tile) * B.group * D * 2);
+        for (int h = 0; h < Sh::HALVES; ++h)
+          tma_3d(qbuf + w * Sh::TILE + h * (KT * 128), &p.q, h * 64, g.kvh * B.group,
+                 g.s.t0 + g.item * p.c.per_item + w * p.per_tile, &sc->q_full[w]);
+        ++sc->q_loads[w];
+      }
+      return true;
+    };
+    if (!second && !queries(0)) return false;
+    // lane i < 4: the page of this warp's keys 16 i .. 16 i + 15 of tile k, -1: none of them is seen
+    auto page_of = [&](int k) {
+      if (k >= g.k1 || lane >= 4) return -1;
+      const int j0 = g.key0(p.c, k) + second * 64 + lane * 16;
+      if (j0 >= g.hi || (j0 + 16 <= g.lo && j0 >= p.c.sinks)) return -1;
+      const int page = __ldg(table + (j0 >> B.page_shift));
+      if (page >= 0 && page < B.num_pages) return page;
+      record(B.ctrl, ERR_INVALID, WHAT_PAGE, p.c.flat ? 0xFFFFFFFFu : static_cast<uint32_t>(g.b));
+      return -1;
+    };
+    // load i of K or V of tile k; zeros for keys that no row of the item sees
+    auto fetch = [&](int into, int half, int pages, int k, int i) {
+      const int page = __shfl_sync(0xFFFFFFFFu, pages, i * ROWS_OF / 16);
+      const int key = g.key0(p.c, k) + second * 64 + i * ROWS_OF + row, slot = key & (B.page_size - 1);
+      codes[into] = make_uint4(0, 0, 0, 0);
+      scale[into] = 0;
+      if (page >= 0 && key < g.hi && (key >= g.lo || key < p.c.sinks)) {
+        const long long at = page * B.page_stride + slot * B.slot_stride + g.kvh * B.head_stride;
+        codes[into] = __ldg(reinterpret_cast<const uint4*>(static_cast<const uint8_t*>(half ? p.v_raw : p.k_raw) + at / 2) + piece);
+        scale[into] = __ldg((half ? p.v_scales : p.k_scales) + scale_row(B, page, slot, g.kvh) * PIECES + piece);
+      }
+    };
+    int pages = page_of(g.k0);
+#pragma unroll
+    for (int i = 0; i < AHEAD; ++i) fetch(i, 0, pages, g.k0, i);
+#pragma unroll 1
+    for (int k = g.k0; k < g.k1; ++k) {
+      const int after = page_of(k + 1);
+#pragma unroll 1
+      for (int half = 0; half < 2; ++half) {  // K, then V
+        if (!wait_warp(&sc->empty[rp.slot], rp.phase ^ 1u, sc)) return false;
+        uint8_t* const tile = ring + rp.slot * Sh::TILE + (second * 8 + (row >> 3)) * (Sh::HALVES * 1024) +
+                              (piece >> 1) * 1024 + (row & 7) * 128;
+#pragma unroll
+        for (int i = 0; i < LOADS; ++i) {
+          const Four<T> four(scale[i % AHEAD] * 0x10001u);
+          const uint32_t words[4] = {codes[i % AHEAD].x, codes[i % AHEAD].y, codes[i % AHEAD].z, codes[i % AHEAD].w};
+#pragma unroll
+          for (int w = 0; w < 4; ++w) {
+            uint32_t x[4];
+            four.pairs(words[w], x);
+            *reinterpret_cast<uint4*>(tile + i * ROWS_OF / 8 * (Sh::HALVES * 1024) + ((((piece & 1) * 4 + w) ^ (row & 7)) << 4)) =
+                make_uint4(x[0], x[1], x[2], x[3]);
+          }
+          const int next = i + AHEAD;
+          if (next < LOADS)
+            fetch(i % AHEAD, half, pages, k, next);
+          else
+            fetch(i % AHEAD, half ^ 1, half ? after : pages, k + half, next - LOADS);
+        }
+        cs::fence_proxy_async_shared();
+        __syncwarp();
+        if (lane == 0) cs::mbar_arrive(&sc->full[rp.slot]);
+        rp.next();
+        if (!second && two && k == g.k0 && half == 0 && !queries(1)) return false;
+      }
+      pages = after;
     }
   }
   return true;
@@ -508,7 +605,8 @@ __device__ __forceinline__ void st32(void* p, const uint32_t* v) {
 __device__ __forceinline__ uint32_t below(int n) { return n >= 32 ? 0xFFFFFFFFu : n <= 0 ? 0u : (1u << n) - 1u; }
 
 // Warpgroup w: the softmax of the steps with S buffer w, one row per thread, and the output.
-template <typename T, int D, bool WINDOW>
+// FOUR: the tiles come from a cache in 4 bits (load4_role), with zeros where no row of the item sees a key.
+template <typename T, int D, bool WINDOW, bool FOUR>
 __device__ bool softmax_role(const AttnP& p, AttnCtl<AttnShape<D>::SLOTS>* sc, uint8_t* ring, int w) {
   using Sh = AttnShape<D>;
   constexpr int CH = D / 32;                                      // chunks of 32 columns of O
@@ -553,7 +651,7 @@ __device__ bool softmax_role(const AttnP& p, AttnCtl<AttnShape<D>::SLOTS>* sc, u
       const bool fresh = k == k_first;  // O of this buffer holds nothing yet
       const int j0 = WINDOW ? g.key0(p.c, k) : k * KT;
       const bool mask = !(j0 + KT <= some && (!WINDOW || j0 >= all_lo || j0 + KT <= p.c.sinks));  // some key is hidden from some row
-      const bool unseen = j0 + KT > g.hi || (WINDOW && j0 < g.lo && j0 + KT > p.c.sinks);       // from every row of the item
+      const bool unseen = !FOUR && (j0 + KT > g.hi || (WINDOW && j0 < g.lo && j0 + KT > p.c.sinks));  // from every row of the item
       if (!wait_warp(&sc->s_full[w], s_phase, sc)) return false;
       s_phase ^= 1u;
       cs::tc_fence_after();
@@ -769,7 +867,7 @@ __device__ bool softmax_role(const AttnP& p, AttnCtl<AttnShape<D>::SLOTS>* sc, u
 
 // One warp: the output of a token and head from its visible keys alone, one key after
 // another with the running maximum.
-template <typename T, int D>
+template <typename T, int D, bool FOUR>
 __device__ __noinline__ void mend_row(const AttnP& p, int t, int h) {
   const Batch& B = p.b;
   const int lane = threadIdx.x & 31, b = sequence_of(B, t);
@@ -779,12 +877,19 @@ __device__ __noinline__ void mend_row(const AttnP& p, int t, int h) {
   constexpr int W = D / 64;  // 32-bit words per lane
   const int* pages = B.table + static_cast<long long>(b) * B.table_cols;
   const int lo = p.c.window > 0 ? max(0, pos - p.c.window + 1) : 0, sinks = min(p.c.sinks, lo);
-  // element offset of key j's row, negative: its page is not in the pool
-  auto row_of = [&](int j) {
-    const int page = __ldg(pages + (j >> B.page_shift));
-    return page < 0 || page >= B.num_pages
-               ? -1ll
-               : page * B.page_stride + (j & (B.page_size - 1)) * B.slot_stride + kh * B.head_stride;
+  // element offset of key j's row (and that of its scales), negative: its page is not in the pool
+  auto row_of = [&](int j, long long& scales) {
+    const int page = __ldg(pages + (j >> B.page_shift)), slot = j & (B.page_size - 1);
+    if (page < 0 || page >= B.num_pages) return -1ll;
+    scales = scale_row(B, page, slot, kh) * (D / 32);
+    return page * B.page_stride + slot * B.slot_stride + kh * B.head_stride;
+  };
+  // two values of a row
+  auto pair_of = [&](const void* cache, const uint8_t* scales, long long at, long long scales_at, int i) {
+    if constexpr (FOUR)
+      return four_pair(static_cast<const uint8_t*>(cache) + at / 2, scales + scales_at, i);
+    else
+      return Pair<T>::get(reinterpret_cast<const uint32_t*>(static_cast<const T*>(cache) + at)[i]);
   };
   // is a value not finite at a key of the item that this row does not see?  (Else the row has
   // what its own keys give, and thousands of rows may see one such value.)
@@ -793,11 +898,12 @@ __device__ __noinline__ void mend_row(const AttnP& p, int t, int h) {
   auto look = [&](int from, int to) {
 #pragma unroll 4
     for (int j = from; j < to; ++j) {
-      const long long at = row_of(j);
+      long long scales;
+      const long long at = row_of(j, scales);
       if (at < 0) continue;
 #pragma unroll
       for (int w = 0; w < W; ++w) {
-        const float2 v = Pair<T>::get(reinterpret_cast<const uint32_t*>(static_cast<const T*>(p.v_raw) + at)[lane + 32 * w]);
+        const float2 v = pair_of(p.v_raw, p.v_scales, at, scales, lane + 32 * w);
         spoilt |= !isfinite(v.x) || !isfinite(v.y);
       }
     }
@@ -814,14 +920,13 @@ __device__ __noinline__ void mend_row(const AttnP& p, int t, int h) {
   }
   for (int i = 0; i < sinks + pos + 1 - lo; ++i) {  // the sinks, then the window
     const int j = i < sinks ? i : lo + i - sinks;
-    const long long at = row_of(j);
+    long long scales;
+    const long long at = row_of(j, scales);
     if (at < 0) continue;
-    const uint32_t* kr = reinterpret_cast<const uint32_t*>(static_cast<const T*>(p.k_raw) + at);
-    const uint32_t* vr = reinterpret_cast<const uint32_t*>(static_cast<const T*>(p.v_raw) + at);
     float s = 0.0f;
 #pragma unroll
     for (int w = 0; w < W; ++w) {
-      const float2 k = Pair<T>::get(kr[lane + 32 * w]);
+      const float2 k = pair_of(p.k_raw, p.k_scales, at, scales, lane + 32 * w);
       s = fmaf(q[2 * w], k.x, fmaf(q[2 * w + 1], k.y, s));
     }
 #pragma unroll
@@ -832,7 +937,7 @@ __device__ __noinline__ void mend_row(const AttnP& p, int t, int h) {
     l = l * f + e;
 #pragma unroll
     for (int w = 0; w < W; ++w) {
-      const float2 v = Pair<T>::get(vr[lane + 32 * w]);
+      const float2 v = pair_of(p.v_raw, p.v_scales, at, scales, lane + 32 * w);
       o[2 * w] = fmaf(o[2 * w], f, e * v.x), o[2 * w + 1] = fmaf(o[2 * w + 1], f, e * v.y);
     }
     mx = top;
@@ -868,7 +973,7 @@ __device__ __noinline__ void mend_row(const AttnP& p, int t, int h) {
 // behind the attention, when they lie in L2.  Then it mends the rows that were marked.
 constexpr int JOIN_THREADS = 256;  // at least the grid of cs_kv_attn_kernel
 constexpr int JOIN_CTAS = 4;  // per SM
-template <typename T, int D>
+template <typename T, int D, bool FOUR = false>
 __global__ void __launch_bounds__(JOIN_THREADS, JOIN_CTAS) cs_kv_join_kernel(const __grid_constant__ AttnP p) {
   __shared__ int before[JOIN_THREADS + 1], sums[JOIN_THREADS / 32];
   __shared__ Split splits[JOIN_THREADS];
@@ -970,7 +1075,7 @@ __global__ void __launch_bounds__(JOIN_THREADS, JOIN_CTAS) cs_kv_join_kernel(con
     for (int w = 0; w < W; ++w) probe = fmaf(x[w], 0.0f, probe);
     if (!p.c.flat && __any_sync(0xFFFFFFFFu, probe != 0.0f) && isfinite(l)) {
       __syncwarp();
-      mend_row<T, D>(p, static_cast<int>(tok), sp.kvh * B.group + h);
+      mend_row<T, D, FOUR>(p, static_cast<int>(tok), sp.kvh * B.group + h);
     }
   }
   if (!mend) return;
@@ -979,7 +1084,7 @@ __global__ void __launch_bounds__(JOIN_THREADS, JOIN_CTAS) cs_kv_join_kernel(con
        n += gridDim.x * (JOIN_THREADS / 32)) {
     if (p.mend[n] == 0) continue;
     __syncwarp();
-    mend_row<T, D>(p, static_cast<int>(n / B.heads), static_cast<int>(n % B.heads));
+    mend_row<T, D, FOUR>(p, static_cast<int>(n / B.heads), static_cast<int>(n % B.heads));
     if (lane == 0) p.mend[n] = 0;
   }
   __syncthreads();
@@ -990,8 +1095,8 @@ __global__ void __launch_bounds__(JOIN_THREADS, JOIN_CTAS) cs_kv_join_kernel(con
 }
 
 // WINDOW: whether keys may be hidden behind a row's window (without, what deals with it is
-// not in the code of the inner loops)
-template <typename T, int D, bool WINDOW>
+// not in the code of the inner loops).  FOUR: the cache is in 4 bits, and two warps make tiles of it
+template <typename T, int D, bool WINDOW, bool FOUR = false>
 __global__ void __launch_bounds__(ATTN_THREADS, 1) cs_kv_attn_kernel(const __grid_constant__ AttnP p) {
   using Sh = AttnShape<D>;
   using Ctl = AttnCtl<Sh::SLOTS>;
@@ -1004,7 +1109,7 @@ __global__ void __launch_bounds__(ATTN_THREADS, 1) cs_kv_attn_kernel(const __gri
   const int warp = threadIdx.x >> 5;
   if (threadIdx.x == 0) {
     for (int i = 0; i < Sh::SLOTS; ++i) {
-      cs::mbar_init(&sc->full[i], 1);
+      cs::mbar_init(&sc->full[i], FOUR ? LOAD4_WARPS : 1);
       cs::mbar_init(&sc->empty[i], 2);  // both MMA warps
     }
     for (int w = 0; w < 2; ++w) {
@@ -1021,8 +1126,10 @@ __global__ void __launch_bounds__(ATTN_THREADS, 1) cs_kv_attn_kernel(const __gri
     sc->abort = sc->turn = sc->loads = sc->q_loads[0] = sc->q_loads[1] = 0;
     cs::fence_mbar_init();
     cs::prefetch_tmap(&p.q);
-    cs::prefetch_tmap(&p.k);
-    cs::prefetch_tmap(&p.v);
+    if (!FOUR) {
+      cs::prefetch_tmap(&p.k);
+      cs::prefetch_tmap(&p.v);
+    }
   }
   if (warp == 9) {
     cs::tmem_alloc<1>(&sc->tmem, 512);
@@ -1039,10 +1146,14 @@ __global__ void __launch_bounds__(ATTN_THREADS, 1) cs_kv_attn_kernel(const __gri
   if (warp < 8) {
     regs_inc<SOFTMAX_REGS>();
     // (a softmax that gave up may have stores to tensor memory on their way)
-    if (!softmax_role<T, D, WINDOW>(p, sc, ring, warp >> 2)) cs::tc_wait_st();
+    if (!softmax_role<T, D, WINDOW, FOUR>(p, sc, ring, warp >> 2)) cs::tc_wait_st();
   } else {
     regs_dec<OTHER_REGS>();
-    if (warp == 8) load_role<D>(p, sc, qbuf, ring);
+    if constexpr (FOUR) {
+      if (warp == 8 || warp == 11) load4_role<T, D>(p, sc, qbuf, ring, warp == 11);
+    } else {
+      if (warp == 8) load_role<D>(p, sc, qbuf, ring);
+    }
     if (warp == 9 || warp == 10) mma_role<D, WINDOW>(p, sc, qbuf, ring, bf16, warp - 9);
   }
   __syncwarp();

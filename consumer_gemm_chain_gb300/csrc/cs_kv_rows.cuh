@@ -79,6 +79,145 @@ CS_KV_BOTH uint32_t rows_issued(int which, int stage, bool at_values, uint32_t d
   return (n - stage + ST - 1) / ST;
 }
 
+// All threads of a CTA, behind a barrier: the state of a segment from those of its warps (o: outputs, ml:
+// maxima and sums), and where an item has several pieces, the last CTA to store one joins them.
+// `sum_of` may share o's memory.  tid runs over ROWS_THREADS.
+template <typename T, int D>
+__device__ __forceinline__ void rows_join(const AttnP& p, const Seg& g, int first, int rows, bool late,
+                                          float (*o)[ROWS][D + 4], float (*sum_of)[D + 4], float2 (*ml_of)[ROWS],
+                                          const Range& range, int& last) {
+  const Batch& B = p.b;
+  const int tid = threadIdx.x, lane = tid & 31;
+  auto state = [&](unsigned cta, int which, int r) { return p.part + ((static_cast<size_t>(cta) * 2 + which) * ROWS + r) * (D + 4); };
+  // dimensions 4 c .. 4 c + 3 of row r from their state
+  auto finish = [&](int r, int c, float4 x, float m, float l) {
+    const int t = r / B.group;
+    const long long row = static_cast<long long>(g.s.t0 + first + t) * B.heads + g.kvh * B.group + r - t * B.group;
+    float4* const pre = p.flat_o ? reinterpret_cast<float4*>(p.flat_o + row * D) + c : nullptr;
+    if (!p.c.flat && pre) {  // join the prefix's output
+      const float z = p.flat_lse[row], top = fmaxf(m, z);
+      const float own = m == -INFINITY ? 0.0f : cs::ex2_approx(m - top), fold = z == -INFINITY ? 0.0f : cs::ex2_approx(z - top);
+      const float4 y = *pre;
+      x = make_float4(x.x * own + y.x * fold, x.y * own + y.y * fold, x.z * own + y.z * fold, x.w * own + y.w * fold);
+      l = l * own + fold;
+      m = top;
+    }
+    const float inv = l == 0.0f ? 0.0f : 1.0f / l;
+    const float4 y = l == 0.0f ? make_float4(0.0f, 0.0f, 0.0f, 0.0f) : make_float4(x.x * inv, x.y * inv, x.z * inv, x.w * inv);
+    const float probe = fmaf(x.x, 0.0f, fmaf(x.y, 0.0f, fmaf(x.z, 0.0f, x.w * 0.0f)));  // NaN if one is not finite
+    if (probe != 0.0f && isfinite(l) && g.s.n > 1) mark(p, row);  // several tokens: keys hidden from one only
+    if (c == 0) put_lse(p, row, m, l);
+    if (p.c.flat) {
+      *pre = y;
+    } else {
+      uint2* out = reinterpret_cast<uint2*>(static_cast<T*>(p.out) + (g.s.t0 + first + t) * p.out_stride +
+                                            (g.kvh * B.group + r - t * B.group) * D) + c;
+      *out = make_uint2(Pair<T>::put(y.x, y.y), Pair<T>::put(y.z, y.w));
+    }
+  };
+  auto add = [](float4& x, const float4& y, float f) {
+    x.x = fmaf(y.x, f, x.x), x.y = fmaf(y.y, f, x.y), x.z = fmaf(y.z, f, x.z), x.w = fmaf(y.w, f, x.w);
+  };
+  constexpr int QUADS = D / 4;
+  const bool whole = g.whole();
+  if (late && whole) cs::grid_dep_wait();
+  for (int i = tid; i < rows * QUADS; i += ROWS_THREADS) {
+    const int r = i / QUADS, c = i % QUADS;
+    float m = -INFINITY, sum = 0.0f;
+    float4 x = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+#pragma unroll
+    for (int w = 0; w < ROWS_WARPS; ++w) m = fmaxf(m, ml_of[w][r].x);
+#pragma unroll
+    for (int w = 0; w < ROWS_WARPS; ++w) {
+      const float2 ml = ml_of[w][r];
+      const float f = ml.x == -INFINITY ? 0.0f : cs::ex2_approx(ml.x - m);
+      sum = fmaf(ml.y, f, sum);
+      add(x, *reinterpret_cast<const float4*>(&o[w][r][4 * c]), f);
+    }
+    if (whole) {
+      finish(r, c, x, m, sum);
+    } else {
+      float* to = state(blockIdx.x, range.x0 < g.x, r);
+      reinterpret_cast<float4*>(to)[c] = x;
+      if (c == 0) *reinterpret_cast<float2*>(to + D) = make_float2(m, sum);
+    }
+  }
+  if (whole) return;
+  const unsigned me = blockIdx.x, quota = static_cast<unsigned>(min(range.quota, 0x80000000ull));
+  const unsigned long long end_x = g.x + g.tiles - 1;
+  const unsigned c0 = range.x0 > g.x ? me - (static_cast<unsigned>(range.x0 - g.x) + quota - 1) / quota : me;
+  const unsigned c1 = end_x >= range.x1 ? me + static_cast<unsigned>(end_x - range.x1) / quota + 1 : me;
+  __syncthreads();  // all stores come before the one arrival at gpu scope
+  if (tid == 0) {
+    uint32_t* ctr = p.arrivals + c0;
+    const uint32_t old = cs::atom_add_acq_rel_gpu(ctr, 1u);
+    last = old == c1 - c0;
+    if (old == c1 - c0) *ctr = 0u;  // for the next call
+  }
+  __syncthreads();
+  if (!last) return;
+  if (late) cs::grid_dep_wait();
+  // the last to arrive joins the pieces in their order
+  const int pieces = static_cast<int>(c1 - c0) + 1;
+  auto piece = [&](int i, int r) { return state(c0 + i, range.quota * (c0 + i) < g.x, r); };
+  // a warp (64 dimensions: half of one) sums a row over all pieces, or with few rows over a
+  // part of them, a lane four dimensions; every lane knows the weights of 32 (16) pieces at a time
+  constexpr int LANES = QUADS, UNITS = ROWS_THREADS / LANES, AHEAD = 3;  // a fourth is spilled, in the inner loop too
+  static_assert(UNITS <= ROWS, "sums");
+  const unsigned group = LANES == 32 ? 0xFFFFFFFFu : 0xFFFFu << (lane & 16);
+  const int gl = lane % LANES;
+  const int parts = rows >= UNITS ? 1 : UNITS / rows, per = (pieces + parts - 1) / parts;
+  for (int u = tid / LANES; u < rows * parts; u += UNITS) {
+    const int r = u % rows, part = u / rows, to = min(pieces, (part + 1) * per);
+    float4 x = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+    float sum = 0.0f, top = -INFINITY;
+    for (int i0 = part * per; i0 < to; i0 += LANES) {
+      const int here = min(LANES, to - i0);
+      auto output = [&](int i) { return __ldcg(reinterpret_cast<const float4*>(piece(i0 + i, r)) + gl); };
+      float2 ml = make_float2(-INFINITY, 0.0f);
+      if (gl < here) ml = __ldcg(reinterpret_cast<const float2*>(piece(i0 + gl, r) + D));
+      float4 y[AHEAD];  // on their way with the maxima and sums
+#pragma unroll
+      for (int i = 0; i < AHEAD; ++i)
+        if (i < here) y[i] = output(i);
+      float m = ml.x;
+#pragma unroll
+      for (int v = LANES / 2; v; v >>= 1) m = fmaxf(m, __shfl_xor_sync(group, m, v));
+      m = fmaxf(m, top);
+      const float old = top == -INFINITY ? 0.0f : cs::ex2_approx(top - m);
+      const float weight = ml.x == -INFINITY ? 0.0f : cs::ex2_approx(ml.x - m);
+      top = m;
+      float l = ml.y * weight;
+#pragma unroll
+      for (int v = LANES / 2; v; v >>= 1) l += __shfl_xor_sync(group, l, v);
+      sum = fmaf(sum, old, l);
+      x.x *= old, x.y *= old, x.z *= old, x.w *= old;
+#pragma unroll
+      for (int i = 0; i < AHEAD; ++i) {
+        const float f = __shfl_sync(group, weight, i, LANES);
+        if (i < here) add(x, y[i], f);
+      }
+#pragma unroll 4
+      for (int i = AHEAD; i < here; ++i) add(x, output(i), __shfl_sync(group, weight, i, LANES));
+    }
+    reinterpret_cast<float4*>(sum_of[u])[gl] = x;
+    if (gl == 0) *reinterpret_cast<float2*>(&sum_of[u][D]) = make_float2(top, sum);
+  }
+  __syncthreads();
+  for (int i = tid; i < rows * QUADS; i += ROWS_THREADS) {
+    const int r = i / QUADS, c = i % QUADS;
+    float4 y = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+    float l = 0.0f, top = -INFINITY;
+    for (int part = 0; part < parts; ++part) top = fmaxf(top, sum_of[part * rows + r][D]);
+    for (int part = 0; part < parts; ++part) {
+      const float m = sum_of[part * rows + r][D], f = m == -INFINITY ? 0.0f : cs::ex2_approx(m - top);
+      add(y, *reinterpret_cast<const float4*>(&sum_of[part * rows + r][4 * c]), f);
+      l = fmaf(sum_of[part * rows + r][D + 1], f, l);
+    }
+    finish(r, c, y, top, l);
+  }
+}
+
 template <typename T, int D>
 __global__ void __launch_bounds__(ROWS_THREADS, ROWS_CTAS) cs_kv_rows_kernel(const __grid_constant__ AttnP p) {
   extern __shared__ __align__(1024) uint8_t rows_smem[];
@@ -317,134 +456,7 @@ __global__ void __launch_bounds__(ROWS_THREADS, ROWS_CTAS) cs_kv_rows_kernel(con
       }
     }
     __syncthreads();
-    auto state = [&](unsigned cta, int which, int r) { return p.part + ((static_cast<size_t>(cta) * 2 + which) * ROWS + r) * (D + 4); };
-    // dimensions 4 c .. 4 c + 3 of row r from their state
-    auto finish = [&](int r, int c, float4 x, float m, float l) {
-      const int t = r / B.group;
-      const long long row = static_cast<long long>(g.s.t0 + first + t) * B.heads + g.kvh * B.group + r - t * B.group;
-      float4* const pre = p.flat_o ? reinterpret_cast<float4*>(p.flat_o + row * D) + c : nullptr;
-      if (!p.c.flat && pre) {  // join the prefix's output
-        const float z = p.flat_lse[row], top = fmaxf(m, z);
-        const float own = m == -INFINITY ? 0.0f : cs::ex2_approx(m - top), fold = z == -INFINITY ? 0.0f : cs::ex2_approx(z - top);
-        const float4 y = *pre;
-        x = make_float4(x.x * own + y.x * fold, x.y * own + y.y * fold, x.z * own + y.z * fold, x.w * own + y.w * fold);
-        l = l * own + fold;
-        m = top;
-      }
-      const float inv = l == 0.0f ? 0.0f : 1.0f / l;
-      const float4 y = l == 0.0f ? make_float4(0.0f, 0.0f, 0.0f, 0.0f) : make_float4(x.x * inv, x.y * inv, x.z * inv, x.w * inv);
-      const float probe = fmaf(x.x, 0.0f, fmaf(x.y, 0.0f, fmaf(x.z, 0.0f, x.w * 0.0f)));  // NaN if one is not finite
-      if (probe != 0.0f && isfinite(l) && g.s.n > 1) mark(p, row);  // several tokens: keys hidden from one only
-      if (c == 0) put_lse(p, row, m, l);
-      if (p.c.flat) {
-        *pre = y;
-      } else {
-        uint2* out = reinterpret_cast<uint2*>(static_cast<T*>(p.out) + (g.s.t0 + first + t) * p.out_stride +
-                                              (g.kvh * B.group + r - t * B.group) * D) + c;
-        *out = make_uint2(Pair<T>::put(y.x, y.y), Pair<T>::put(y.z, y.w));
-      }
-    };
-    auto add = [](float4& x, const float4& y, float f) {
-      x.x = fmaf(y.x, f, x.x), x.y = fmaf(y.y, f, x.y), x.z = fmaf(y.z, f, x.z), x.w = fmaf(y.w, f, x.w);
-    };
-    constexpr int QUADS = D / 4;
-    const bool whole = g.whole();
-    if (late && whole) cs::grid_dep_wait();
-    for (int i = tid; i < rows * QUADS; i += ROWS_THREADS) {
-      const int r = i / QUADS, c = i % QUADS;
-      float m = -INFINITY, sum = 0.0f;
-      float4 x = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-#pragma unroll
-      for (int w = 0; w < ROWS_WARPS; ++w) m = fmaxf(m, sm.ml[w][r].x);
-#pragma unroll
-      for (int w = 0; w < ROWS_WARPS; ++w) {
-        const float2 ml = sm.ml[w][r];
-        const float f = ml.x == -INFINITY ? 0.0f : cs::ex2_approx(ml.x - m);
-        sum = fmaf(ml.y, f, sum);
-        add(x, *reinterpret_cast<const float4*>(&sm.o[w][r][4 * c]), f);
-      }
-      if (whole) {
-        finish(r, c, x, m, sum);
-      } else {
-        float* to = state(blockIdx.x, sm.range.x0 < g.x, r);
-        reinterpret_cast<float4*>(to)[c] = x;
-        if (c == 0) *reinterpret_cast<float2*>(to + D) = make_float2(m, sum);
-      }
-    }
-    if (whole) continue;
-    const unsigned me = blockIdx.x, quota = static_cast<unsigned>(min(sm.range.quota, 0x80000000ull));
-    const unsigned long long end_x = g.x + g.tiles - 1;
-    const unsigned c0 = sm.range.x0 > g.x ? me - (static_cast<unsigned>(sm.range.x0 - g.x) + quota - 1) / quota : me;
-    const unsigned c1 = end_x >= sm.range.x1 ? me + static_cast<unsigned>(end_x - sm.range.x1) / quota + 1 : me;
-    __syncthreads();  // all stores come before the one arrival at gpu scope
-    if (tid == 0) {
-      uint32_t* ctr = p.arrivals + c0;
-      const uint32_t old = cs::atom_add_acq_rel_gpu(ctr, 1u);
-      sm.last = old == c1 - c0;
-      if (old == c1 - c0) *ctr = 0u;  // for the next call
-    }
-    __syncthreads();
-    if (!sm.last) continue;
-    if (late) cs::grid_dep_wait();
-    // the last to arrive joins the pieces in their order
-    const int pieces = static_cast<int>(c1 - c0) + 1;
-    auto piece = [&](int i, int r) { return state(c0 + i, sm.range.quota * (c0 + i) < g.x, r); };
-    // a warp (64 dimensions: half of one) sums a row over all pieces, or with few rows over a
-    // part of them, a lane four dimensions; every lane knows the weights of 32 (16) pieces at a time
-    constexpr int LANES = QUADS, UNITS = ROWS_THREADS / LANES, AHEAD = 3;  // a fourth is spilled, in the inner loop too
-    static_assert(UNITS <= ROWS, "sums");
-    const unsigned group = LANES == 32 ? 0xFFFFFFFFu : 0xFFFFu << (lane & 16);
-    const int gl = lane % LANES;
-    const int parts = rows >= UNITS ? 1 : UNITS / rows, per = (pieces + parts - 1) / parts;
-    for (int u = tid / LANES; u < rows * parts; u += UNITS) {
-      const int r = u % rows, part = u / rows, to = min(pieces, (part + 1) * per);
-      float4 x = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-      float sum = 0.0f, top = -INFINITY;
-      for (int i0 = part * per; i0 < to; i0 += LANES) {
-        const int here = min(LANES, to - i0);
-        auto output = [&](int i) { return __ldcg(reinterpret_cast<const float4*>(piece(i0 + i, r)) + gl); };
-        float2 ml = make_float2(-INFINITY, 0.0f);
-        if (gl < here) ml = __ldcg(reinterpret_cast<const float2*>(piece(i0 + gl, r) + D));
-        float4 y[AHEAD];  // on their way with the maxima and sums
-#pragma unroll
-        for (int i = 0; i < AHEAD; ++i)
-          if (i < here) y[i] = output(i);
-        float m = ml.x;
-#pragma unroll
-        for (int v = LANES / 2; v; v >>= 1) m = fmaxf(m, __shfl_xor_sync(group, m, v));
-        m = fmaxf(m, top);
-        const float old = top == -INFINITY ? 0.0f : cs::ex2_approx(top - m);
-        const float weight = ml.x == -INFINITY ? 0.0f : cs::ex2_approx(ml.x - m);
-        top = m;
-        float l = ml.y * weight;
-#pragma unroll
-        for (int v = LANES / 2; v; v >>= 1) l += __shfl_xor_sync(group, l, v);
-        sum = fmaf(sum, old, l);
-        x.x *= old, x.y *= old, x.z *= old, x.w *= old;
-#pragma unroll
-        for (int i = 0; i < AHEAD; ++i) {
-          const float f = __shfl_sync(group, weight, i, LANES);
-          if (i < here) add(x, y[i], f);
-        }
-#pragma unroll 4
-        for (int i = AHEAD; i < here; ++i) add(x, output(i), __shfl_sync(group, weight, i, LANES));
-      }
-      reinterpret_cast<float4*>(sm.sum[u])[gl] = x;
-      if (gl == 0) *reinterpret_cast<float2*>(&sm.sum[u][D]) = make_float2(top, sum);
-    }
-    __syncthreads();
-    for (int i = tid; i < rows * QUADS; i += ROWS_THREADS) {
-      const int r = i / QUADS, c = i % QUADS;
-      float4 y = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-      float l = 0.0f, top = -INFINITY;
-      for (int part = 0; part < parts; ++part) top = fmaxf(top, sm.sum[part * rows + r][D]);
-      for (int part = 0; part < parts; ++part) {
-        const float m = sm.sum[part * rows + r][D], f = m == -INFINITY ? 0.0f : cs::ex2_approx(m - top);
-        add(y, *reinterpret_cast<const float4*>(&sm.sum[part * rows + r][4 * c]), f);
-        l = fmaf(sm.sum[part * rows + r][D + 1], f, l);
-      }
-      finish(r, c, y, top, l);
-    }
+    rows_join<T, D>(p, g, first, rows, late, sm.o, sm.sum, sm.ml, sm.range, sm.last);
   }
   if (late) cs::grid_dep_wait();
 }
