@@ -109,8 +109,10 @@ Kernels kernels(const cs_kv_s* p) {
   Kernels u;
   u.rows = rows_kernel(p->d);
   u.attn = attn_kernel(p->d, &u.attn_smem);
+  u.attn_threads = cskv::ATTN_THREADS;
   u.join = join_kernel(p->d);
   u.rows_grid = p->num_sms * cskv::ROWS_CTAS;
+  u.rows_shift = cskv::ROWS_SHIFT;
   u.rows_smem = rows_smem(p->d);
   u.rows_map = &p->slots_map;
   u.attn_map = &p->page_map;

@@ -42,9 +42,12 @@ Kernels kernels_of(const cs_kv_s* p, int max_rows) {
   u.attn = window ? (const void*)cskv::cs_kv_attn_kernel<T, D, true, true> : (const void*)cskv::cs_kv_attn_kernel<T, D, false, true>;
   u.join = (const void*)cskv::cs_kv_join_kernel<T, D, true>;
   u.rows_grid = p->num_sms * (narrow ? cskv::ROWS4_CTAS<1> : cskv::ROWS4_CTAS<2>);
+  u.rows_shift = cskv::ROWS4_SHIFT;
   u.rows_smem = sizeof(cskv::Rows4Shared<D>);
-  u.attn_smem = cskv::AttnShape<D>::SMEM;
-  u.rows_map = u.attn_map = nullptr;
+  u.attn_smem = cskv::AttnShape<D, true>::SMEM;
+  u.attn_threads = cskv::ATTN_THREADS_OF<true>;
+  u.rows_map = nullptr;
+  u.attn_map = &p->codes_map;
   return u;
 }
 
@@ -54,9 +57,30 @@ Kernels kernels(const cs_kv_s* p, int max_rows) {
   return p->d.head_dim == 128 ? kernels_of<__half, 128>(p, max_rows) : kernels_of<__half, 64>(p, max_rows);
 }
 
-// Once for a plan, on its device: the shared memory of its kernels.
+// A cache's codes as [8-slot group][head][slot of the group][head_dim / 2 bytes]: one box is a page's slots of a
+// head.  In the HEAD layout heads are part of the groups' order.
+cs_status encode_codes(const cs_kv_s* p, CUtensorMap* map) {
+  const cs_kv_desc& d = p->d;
+  const cs_kv_batch none{};
+  const cskv::Batch B = device_batch(p, &none);
+  const bool head = d.cache_layout == CS_KV_HEAD;
+  const cuuint64_t groups = static_cast<cuuint64_t>(d.num_pages) * (d.page_size / 8), width = d.head_dim / 2;
+  const cuuint64_t dims[4] = {width, 8, head ? 1 : static_cast<cuuint64_t>(d.kv_heads), head ? groups * d.kv_heads : groups};
+  const cuuint64_t slot = static_cast<cuuint64_t>(B.slot_stride) / 2;
+  const cuuint64_t strides[3] = {slot, static_cast<cuuint64_t>(B.head_stride) / 2, 8 * slot};
+  const cuuint32_t box[4] = {static_cast<cuuint32_t>(width), 8, 1, static_cast<cuuint32_t>(d.page_size / 8)}, ones[4] = {1, 1, 1, 1};
+  const CUresult r = driver().encode(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 4, p->part, dims, strides, box, ones,
+                                     CU_TENSOR_MAP_INTERLEAVE_NONE, width == 64 ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_32B,
+                                     CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  if (r != CUDA_SUCCESS) return cs_fail(CS_ERR_CUDA, "cuTensorMapEncodeTiled failed (%d) for a cache's codes", static_cast<int>(r));
+  return CS_OK;
+}
+
+// Once for a plan, on its device: the shared memory of its kernels, and the map of its copies.
 cs_status make_ready(cs_kv_s* p) {
   if (p->four_ready) return CS_OK;
+  const cs_status s = encode_codes(p, &p->codes_map);
+  if (s != CS_OK) return s;
   for (int rows : {1, 16}) {
     const Kernels u = kernels(p, rows);
     cudaError_t e = cudaFuncSetAttribute(u.rows, cudaFuncAttributeMaxDynamicSharedMemorySize, u.rows_smem);
@@ -114,7 +138,7 @@ cs_status check_append4(const cs_kv_s* p, const cs_kv_batch* b, const cs_kv4_app
   f.rope_rows = a->rope_rows;
   f.rotary_dim = d.rotary_dim;
   f.half = d.rotary_pairing == CS_KV_HALF;
-  f.units = (d.heads + 2 * d.kv_heads) * f.head_chunks;
+  f.units = d.heads * (f.head_chunks / 2) + 2 * d.kv_heads * f.head_chunks;
   return CS_OK;
 }
 

@@ -59,37 +59,73 @@ __device__ __forceinline__ void find_places(const Four4P& p, int first, int coun
 
 // Appends: (a, b) -> (a cos - b sin, b cos + a sin) for every rotated pair of Q and K, each product and each sum
 // rounded to 32 bits (no multiply-add: what is kept does not depend on how it is compiled) and the result to the dtype;
-// then the 4-bit form of K and V.  A lane has 8 values of a head; the other half of its pairs
-// comes from the lane that holds it, a group's maximum from its four lanes.
+// then the 4-bit form of K and V.  Queries go 16 values a thread, both halves of a pair (so that they can be
+// rotated in place); keys and values 8 a lane, with the other half of a pair from the lane
+// that holds it and a group's maximum from its four lanes.
 template <typename T>
-__global__ void __launch_bounds__(FOUR_THREADS) cs_kv4_append_kernel(const __grid_constant__ Four4P p) {
+struct Turn {
+  static __device__ __forceinline__ float minus(float a, float c, float b, float s) {  // a c - b s
+    return __fsub_rn(__fmul_rn(a, c), __fmul_rn(b, s));
+  }
+  static __device__ __forceinline__ float plus(float a, float c, float b, float s) {  // a c + b s
+    return __fadd_rn(__fmul_rn(a, c), __fmul_rn(b, s));
+  }
+  // Pairs of neighbouring values: one chunk by four angles.
+  static __device__ __forceinline__ void adjacent(uint32_t* x, const float4& c, const float4& s) {
+    const float co[4] = {c.x, c.y, c.z, c.w}, si[4] = {s.x, s.y, s.z, s.w};
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      const float2 a = Pair<T>::get(x[e]);
+      x[e] = Pair<T>::put(minus(a.x, co[e], a.y, si[e]), plus(a.y, co[e], a.x, si[e]));
+    }
+  }
+};
+
+// c + 8 for c = x / s rounded to the nearest, ties to even, within -7 .. 7.  inv is 1 / s rounded, so x inv may miss
+// a tie by a part in 2^23; a quotient that is no tie is at least 2^-13 away from one (x has at most 11 significant
+// bits, s has 4), so rounding to steps of 2^-16 first puts it right: a sum with 192 does, and one with 1.5 2^23 + 8 rounds.
+__device__ __forceinline__ uint32_t code_of(float x, float inv) {
+  const float y = __fsub_rn(__fadd_rn(__fmul_rn(x, inv), 192.0f), 192.0f);
+  return __float_as_uint(__fadd_rn(fminf(fmaxf(y, -7.0f), 7.0f), 12582920.0f)) & 15u;
+}
+
+template <typename T>
+__global__ void __launch_bounds__(FOUR_THREADS, 5) cs_kv4_append_kernel(const __grid_constant__ Four4P p) {
   __shared__ Places places;
   cs::grid_dep_wait();
   cs::grid_dep_launch_dependents();
   const Batch& B = p.b;
   const int first = blockIdx.x * p.tokens_per_block;
-  const int count = min(p.tokens_per_block, B.tokens - first), total = count * p.units;
+  const int count = min(p.tokens_per_block, B.tokens - first);
   const int turned = p.rotary_dim >> 4;    // chunks that hold one half of the pairs
-  const int heads = B.heads + B.kv_heads;  // heads that are rotated
   const int lane = threadIdx.x & 31;
+  // keys and values: chunk c of head h (V's behind K's), this lane's of the warp's 32 from i0 on
+  const int kv_units = 2 * B.kv_heads * p.head_chunks, kv_total = count * kv_units;
+  int k, h, c;
+  uint4 x4;
+  auto fetch = [&](int i0) {
+    if (i0 >= kv_total) return;
+    const int i = min(i0 + lane, kv_total - 1);  // (lanes behind the end go along)
+    k = i / kv_units;
+    h = (i - k * kv_units) / p.head_chunks;
+    c = i - k * kv_units - h * p.head_chunks;
+    x4 = p.qkv[(first + k) * p.qkv_stride + (B.heads + h) * p.head_chunks + c];
+  };
+  fetch(threadIdx.x - lane);
   find_places<true>(p, first, count, places);
   __syncthreads();
-  for (int i0 = threadIdx.x - lane; i0 < total; i0 += FOUR_THREADS) {
-    const int i = min(i0 + lane, total - 1);  // (lanes behind the end go along)
-    const int k = i / p.units, h = (i - k * p.units) / p.head_chunks, c = i - k * p.units - h * p.head_chunks;
-    uint4 x4 = p.qkv[(first + k) * p.qkv_stride + h * p.head_chunks + c];
+  for (int i0 = threadIdx.x - lane; i0 < kv_total;) {
     uint32_t* x = reinterpret_cast<uint32_t*>(&x4);
-    const long long at = i0 + lane < total ? places.codes[k] : -1;
-    const bool rotate = c < 2 * turned && h < heads;
+    const long long at = i0 + lane < kv_total ? places.codes[k] : -1;
+    const bool key = h < B.kv_heads, rotate = key && c < 2 * turned;
     const float4* angles = p.rope + static_cast<long long>(places.angle[k]) * (p.rotary_dim >> 2);
     if (p.half && turned > 0) {
       const bool upper = c >= turned;
-      const int other = rotate ? (upper ? c - turned : c + turned) : c, from = (lane - c + other) & 31;
+      const int j = upper ? c - turned : c, from = rotate ? lane - c + (upper ? j : c + turned) : lane;
       uint32_t y[4];
 #pragma unroll
       for (int e = 0; e < 4; ++e) y[e] = __shfl_sync(0xFFFFFFFFu, x[e], from);
       if (rotate && at >= 0) {
-        const int j = upper ? c - turned : c;
         const float4 ca = __ldg(angles + 2 * j), cb = __ldg(angles + 2 * j + 1);
         const float4 sa = __ldg(angles + 2 * turned + 2 * j), sb = __ldg(angles + 2 * turned + 2 * j + 1);
         const float co[8] = {ca.x, ca.y, ca.z, ca.w, cb.x, cb.y, cb.z, cb.w};
@@ -97,20 +133,12 @@ __global__ void __launch_bounds__(FOUR_THREADS) cs_kv4_append_kernel(const __gri
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
           const float2 a = Pair<T>::get(x[e]), b = Pair<T>::get(y[e]);
-          const float u = __fmul_rn(b.x, si[2 * e]), w = __fmul_rn(b.y, si[2 * e + 1]);
-          x[e] = Pair<T>::put(__fadd_rn(__fmul_rn(a.x, co[2 * e]), upper ? u : -u),
-                              __fadd_rn(__fmul_rn(a.y, co[2 * e + 1]), upper ? w : -w));
+          const float u = upper ? b.x : -b.x, w = upper ? b.y : -b.y;  // (a sign changes no rounding)
+          x[e] = Pair<T>::put(Turn<T>::plus(a.x, co[2 * e], u, si[2 * e]), Turn<T>::plus(a.y, co[2 * e + 1], w, si[2 * e + 1]));
         }
       }
     } else if (rotate && at >= 0) {
-      const float4 ca = __ldg(angles + c), sa = __ldg(angles + turned * 2 + c);
-      const float co[4] = {ca.x, ca.y, ca.z, ca.w}, si[4] = {sa.x, sa.y, sa.z, sa.w};
-#pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        const float2 a = Pair<T>::get(x[e]);
-        x[e] = Pair<T>::put(__fsub_rn(__fmul_rn(a.x, co[e]), __fmul_rn(a.y, si[e])),
-                            __fadd_rn(__fmul_rn(a.y, co[e]), __fmul_rn(a.x, si[e])));
-      }
+      Turn<T>::adjacent(x, __ldg(angles + c), __ldg(angles + 2 * turned + c));
     }
     // the greatest magnitude of the group (as bits: what is not finite is greater than what is)
     float y[8];
@@ -123,30 +151,59 @@ __global__ void __launch_bounds__(FOUR_THREADS) cs_kv4_append_kernel(const __gri
     }
     top = max(top, __shfl_xor_sync(0xFFFFFFFFu, top, 1));
     top = max(top, __shfl_xor_sync(0xFFFFFFFFu, top, 2));
-    if (at < 0) continue;
-    if (h < B.heads) {
-      p.q_out[(first + k) * p.q_stride + h * p.head_chunks + c] = x4;
-      continue;
-    }
-    const bool key = h < heads;
-    const int kh = h - B.heads - (key ? 0 : B.kv_heads);
-    const bool finite = top < 0x7F800000u;
-    const uint32_t byte = finite ? scale_byte(__fdiv_rn(__uint_as_float(top), 7.0f)) : SCALE_NAN;
-    const float scale = scale_value(byte);
-    uint32_t word = 0x88888888u;  // zeros
-    if (finite && byte != 0) {
-      word = 0;
+    if (at >= 0) {
+      const int kh = key ? h : h - B.kv_heads;
+      const bool finite = top < 0x7F800000u;
+      const uint32_t byte = finite ? scale_byte(__fdiv_rn(__uint_as_float(top), 7.0f)) : SCALE_NAN;
+      uint32_t word = 0x88888888u;  // zeros
+      if (finite && byte != 0) {
+        const float inv = __frcp_rn(scale_value(byte));
+        word = 0;
 #pragma unroll
-      for (int e = 0; e < 8; ++e) {
-        const float r = fminf(fmaxf(rintf(__fdiv_rn(y[e], scale)), -7.0f), 7.0f);
-        word |= static_cast<uint32_t>(static_cast<int>(r) + 8) << (4 * (e >> 1) + 16 * (e & 1));
+        for (int e = 0; e < 8; ++e) word |= code_of(y[e], inv) << (4 * (e >> 1) + 16 * (e & 1));
+      }
+      *reinterpret_cast<uint32_t*>((key ? p.k_codes : p.v_codes) + (at + kh * B.head_stride) / 2 + 4 * c) = word;
+      if ((c & 3) == 0) {
+        const long long row = places.scales[k] + static_cast<long long>(kh) * B.page_size;
+        (key ? p.k_scales : p.v_scales)[row * (p.head_chunks >> 2) + (c >> 2)] = static_cast<uint8_t>(byte);
       }
     }
-    *reinterpret_cast<uint32_t*>((key ? p.k_codes : p.v_codes) + (at + kh * B.head_stride) / 2 + 4 * c) = word;
-    if ((c & 3) == 0) {
-      const long long row = places.scales[k] + static_cast<long long>(kh) * B.page_size;
-      (key ? p.k_scales : p.v_scales)[row * (p.head_chunks >> 2) + (c >> 2)] = static_cast<uint8_t>(byte);
+    i0 += FOUR_THREADS;
+    fetch(i0);
+  }
+  // queries: two chunks of a head, those that are rotated together, or neighbours
+  const int per_head = p.head_chunks >> 1, q_units = B.heads * per_head;
+  for (int i = threadIdx.x; i < count * q_units; i += FOUR_THREADS) {
+    const int t = i / q_units, qh = (i - t * q_units) / per_head, j = i - t * q_units - qh * per_head;
+    if (places.codes[t] < 0) continue;
+    const bool rotate = j < turned, apart = p.half && rotate;
+    const int c0 = apart ? j : 2 * j, c1 = apart ? j + turned : 2 * j + 1;
+    const uint4* src = p.qkv + (first + t) * p.qkv_stride + qh * p.head_chunks;
+    uint4 a4 = src[c0], b4 = src[c1];
+    uint32_t *x = reinterpret_cast<uint32_t*>(&a4), *y = reinterpret_cast<uint32_t*>(&b4);
+    if (rotate) {
+      // 8 cosines, 8 sines: HALF rotates (x[e], y[e]), ADJACENT neighbouring values
+      const float4* angles = p.rope + static_cast<long long>(places.angle[t]) * (p.rotary_dim >> 2);
+      const float4 ca = __ldg(angles + 2 * j), cb = __ldg(angles + 2 * j + 1);
+      const float4 sa = __ldg(angles + 2 * turned + 2 * j), sb = __ldg(angles + 2 * turned + 2 * j + 1);
+      if (apart) {
+        const float co[8] = {ca.x, ca.y, ca.z, ca.w, cb.x, cb.y, cb.z, cb.w};
+        const float si[8] = {sa.x, sa.y, sa.z, sa.w, sb.x, sb.y, sb.z, sb.w};
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const float2 a = Pair<T>::get(x[e]), b = Pair<T>::get(y[e]);
+          const int u = 2 * e, w = 2 * e + 1;
+          x[e] = Pair<T>::put(Turn<T>::minus(a.x, co[u], b.x, si[u]), Turn<T>::minus(a.y, co[w], b.y, si[w]));
+          y[e] = Pair<T>::put(Turn<T>::plus(b.x, co[u], a.x, si[u]), Turn<T>::plus(b.y, co[w], a.y, si[w]));
+        }
+      } else {
+        Turn<T>::adjacent(x, ca, sa);
+        Turn<T>::adjacent(y, cb, sb);
+      }
     }
+    uint4* dst = p.q_out + (first + t) * p.q_stride + qh * p.head_chunks;
+    dst[c0] = a4;
+    dst[c1] = b4;
   }
 }
 
@@ -170,7 +227,7 @@ __global__ void __launch_bounds__(FOUR_THREADS) cs_kv4_read_kernel(const __grid_
     if (at < 0) continue;
     const uint2 w = *reinterpret_cast<const uint2*>((key ? p.k_codes : p.v_codes) + (at + kh * B.head_stride) / 2 + 8 * j);
     const long long row = places.scales[k] + static_cast<long long>(kh) * B.page_size;
-    const Four<T> four((key ? p.k_scales : p.v_scales)[row * (p.head_chunks >> 2) + (j >> 1)] * 0x10001u);
+    const Four<T> four(scale_pair((key ? p.k_scales : p.v_scales)[row * (p.head_chunks >> 2) + (j >> 1)]));
     uint32_t x[4], y[4];
     four.pairs(w.x, x);
     four.pairs(w.y, y);

@@ -40,6 +40,10 @@ __device__ __forceinline__ float2 four_pair(const uint8_t* codes, const uint8_t*
   return make_float2(s * (static_cast<int>(w & 15u) - 8), s * (static_cast<int>(w >> 16 & 15u) - 8));
 }
 
+// One scale twice, and two scales, as halves (products, because the pipe of shifts is the busy one).
+__device__ __forceinline__ uint32_t scale_pair(uint32_t byte) { return byte * 0x00800080u; }
+__device__ __forceinline__ uint32_t scale_pair(uint32_t low, uint32_t high) { return high * 0x00800000u + low * 0x80u; }
+
 // Two scales, and what turns codes into values.
 template <typename T>
 struct Four;
@@ -49,11 +53,8 @@ struct Four;
 template <>
 struct Four<__half> {
   __half2 s;
-  // the bytes at bits 0 and 16
-  __device__ __forceinline__ explicit Four(uint32_t bytes) {
-    bytes <<= 7;
-    s = *reinterpret_cast<__half2*>(&bytes);
-  }
+  // bits: the scales as halves (scale_pair)
+  __device__ __forceinline__ explicit Four(uint32_t bits) { s = *reinterpret_cast<__half2*>(&bits); }
   static __device__ __forceinline__ __half2 low(uint32_t w) {
     const uint32_t x = (w & 0x000F000Fu) | 0x64006400u, bias = 0x64086408u;  // 1032
     return __hsub2(*reinterpret_cast<const __half2*>(&x), *reinterpret_cast<const __half2*>(&bias));
@@ -78,9 +79,8 @@ struct Four<__half> {
 template <>
 struct Four<__nv_bfloat16> {
   __nv_bfloat162 s, off;
-  __device__ __forceinline__ explicit Four(uint32_t bytes) {
-    bytes <<= 7;
-    s = __float22bfloat162_rn(__half22float2(*reinterpret_cast<__half2*>(&bytes)));
+  __device__ __forceinline__ explicit Four(uint32_t bits) {
+    s = __float22bfloat162_rn(__half22float2(*reinterpret_cast<__half2*>(&bits)));
     const uint32_t bias = 0xC308C308u;  // -136
     off = __hmul2(s, *reinterpret_cast<const __nv_bfloat162*>(&bias));
   }

@@ -24,15 +24,17 @@ namespace cskv {
 template <int NT>
 constexpr int ROWS4_CTAS = NT == 1 ? 4 : 3;
 
+constexpr int ROWS4_SHIFT = 7;  // keys of a tile: 128, two runs of 16 for each warp, 64 apart
+
 template <int D>
-struct Stage4 {  // 16 keys: codes of K and V, their scales
-  uint8_t codes[2][16][D / 2];
-  uint8_t scales[2][16][D / GROUP4];
+struct Stage4 {  // a warp's keys of a tile: codes of K and V, their scales
+  uint8_t codes[2][32][D / 2];
+  uint8_t scales[2][32][D / GROUP4];
 };
 
 template <int D>
 struct alignas(16) Rows4Shared {
-  static constexpr int STAGES = D == 128 ? 6 : 12;  // 12 KB on their way for each warp
+  static constexpr int STAGES = D == 128 ? 3 : 6;  // 9 to 11 KB on their way for each warp
   union {
     Stage4<D> ring[ROWS_WARPS][STAGES];
     float o[ROWS_WARPS][ROWS][D + 4];  // each warp's output
@@ -66,7 +68,8 @@ __global__ void __launch_bounds__(ROWS_THREADS, ROWS4_CTAS<NT>) cs_kv4_rows_kern
   extern __shared__ __align__(1024) uint8_t rows_smem[];
   Rows4Shared<D>& sm = *reinterpret_cast<Rows4Shared<D>*>(rows_smem);
   constexpr int ST = Rows4Shared<D>::STAGES;
-  constexpr int KW = D / 32, VW = D / 64;  // 32-bit words of a key per lane, of each of its four values
+  constexpr int KW = D / 32, VW = D / 64;   // 32-bit words of a key per lane, of each of its four values
+  constexpr int XS = NT == 1 ? 2 : 1;       // runs of 16 keys whose scores are computed together (16 rows: registers)
   const bool late = !p.c.flat && p.flat_o;  // as in cs_kv_rows_kernel
   if (!late) cs::grid_dep_wait();
   cs::grid_dep_launch_dependents();
@@ -78,6 +81,12 @@ __global__ void __launch_bounds__(ROWS_THREADS, ROWS4_CTAS<NT>) cs_kv4_rows_kern
   Stage4<D>* const ring = sm.ring[warp];
   // 16-byte piece `c` of key j lies at c ^ turn(j) in its row of 64 bytes (32 bytes: where it is)
   auto turn = [](int j) { return D == 128 ? j & 2 : 0; };
+  // What a lane copies: of one of the warp's two runs of 16 keys a piece of every STEP-th key, and maybe 16
+  // bytes of scales (which lie side by side).
+  constexpr int PIECES = D / GROUP4, STEP = 16 / PIECES;
+  const int run = lane >> 4, piece = lane & (PIECES - 1), first_key = (lane & 15) / PIECES;
+  const uint32_t slot_bytes = static_cast<uint32_t>(B.slot_stride >> 1);
+  const bool has_scales = (lane & 15) < 2 * PIECES, of_v = (lane & 15) >= PIECES;
   Walk walk(p.c, sm.range);
   Seg g;
   while (walk.next(B, p.c, g)) {
@@ -85,12 +94,14 @@ __global__ void __launch_bounds__(ROWS_THREADS, ROWS4_CTAS<NT>) cs_kv4_rows_kern
     const int tokens = min(p.c.per_item, g.s.n - first), rows = tokens * B.group;
     const int* table = p.c.flat ? p.pages : B.table + static_cast<long long>(g.b) * B.table_cols;
     const int base = g.s.m - g.s.n + first;  // position of its first token
-    // this warp's page of tile k, -1 if none of its keys is seen
+    const int mine = warp * 16 + run * 64;   // this lane's run of a tile
+    const int skip = (g.lo >> ROWS4_SHIFT) - g.sinks;  // tiles between the sinks' and the window's
+    auto tile_at = [&](int k) { return (k < g.sinks ? k : k + skip) << ROWS4_SHIFT; };  // Seg::key0
+    // the page of this lane's run of tile k, -1 if none of its keys is seen
     auto table_of = [&](int k) {
-      if (k >= g.k1) return -1;
-      const int j0 = g.key0(p.c, k) + warp * 16;
-      if (j0 >= g.hi || (j0 + 16 <= g.lo && j0 >= p.c.sinks)) return -1;
-      const int page = __ldg(table + (j0 >> B.page_shift));
+      const int j = tile_at(k) + mine;
+      if (k >= g.k1 || j >= g.hi || (j + 16 <= g.lo && j >= p.c.sinks)) return -1;
+      const int page = __ldg(table + (j >> B.page_shift));
       return page < 0 ? INT_MAX : page;
     };
     auto checked = [&](int page) {
@@ -98,24 +109,25 @@ __global__ void __launch_bounds__(ROWS_THREADS, ROWS4_CTAS<NT>) cs_kv4_rows_kern
       record(B.ctrl, ERR_INVALID, WHAT_PAGE, p.c.flat ? 0xFFFFFFFFu : static_cast<uint32_t>(g.b));
       return -1;
     };
+    // this lane's part of the codes of K, and V's offset from it; of the scales, K's or V's
+    const uint8_t* const codes = static_cast<const uint8_t*>(p.k_raw) + (g.kvh * B.head_stride >> 1) + first_key * slot_bytes + piece * 16;
+    const long long to_v = static_cast<const uint8_t*>(p.v_raw) - static_cast<const uint8_t*>(p.k_raw);
+    const uint8_t* const scales = (of_v ? p.v_scales : p.k_scales) + piece * 16;
     auto load = [&](int k, int page, Stage4<D>& to) {
       if (k < g.k1) {
         const bool read = page >= 0;
-        const int slot = read ? (g.key0(p.c, k) + warp * 16) & (B.page_size - 1) : 0;
-        const long long at = read ? page * B.page_stride + slot * B.slot_stride + g.kvh * B.head_stride : 0;
-        constexpr int PIECES = D / GROUP4;  // of 16 bytes in a key's row
+        const uint32_t from = read ? page : 0, slot = (tile_at(k) + mine) & (B.page_size - 1);
+        const uint8_t* at = codes + from * (B.page_stride >> 1) + slot * slot_bytes;
+        uint8_t* into = &to.codes[0][run * 16 + first_key][(piece ^ turn(first_key)) * 16];
 #pragma unroll
-        for (int i = 0; i < 16 * PIECES / 32; ++i) {
-          const int x = lane + 32 * i, j = x / PIECES, c = x % PIECES;
-          const long long from = (at + j * B.slot_stride) / 2 + c * 16;
-          copy16(&to.codes[0][j][(c ^ turn(j)) * 16], static_cast<const uint8_t*>(p.k_raw) + from, read);
-          copy16(&to.codes[1][j][(c ^ turn(j)) * 16], static_cast<const uint8_t*>(p.v_raw) + from, read);
+        for (int i = 0; i < PIECES; ++i) {  // (STEP is a multiple of 4, so the piece is turned alike)
+          copy16(into + i * STEP * (D / 2), at, read);
+          copy16(into + i * STEP * (D / 2) + sizeof(to.codes[0]), at + to_v, read);
+          at += STEP * slot_bytes;
         }
-        if (lane < 2 * PIECES) {  // 16 keys' scales lie side by side
-          const int v = lane / PIECES, c = lane % PIECES;
-          const long long from = read ? scale_row(B, page, slot, g.kvh) * PIECES + c * 16 : 0;
-          copy16(&to.scales[v][0][0] + c * 16, (v ? p.v_scales : p.k_scales) + from, read);
-        }
+        if (has_scales)
+          copy16(&to.scales[of_v][run * 16][0] + piece * 16,
+                 scales + ((static_cast<long long>(from) * B.kv_heads + g.kvh) * B.page_size + slot) * PIECES, read);
       }
       copies_commit();
     };
@@ -136,18 +148,14 @@ __global__ void __launch_bounds__(ROWS_THREADS, ROWS4_CTAS<NT>) cs_kv4_rows_kern
 #pragma unroll
       for (int w = 0; w < KW; ++w) q[n][w] = r < rows ? from[w] : make_uint4(0, 0, 0, 0);
     }
-    // keys [.., end) and from lo on, or below the sinks, are seen by rows 8 n + 2 jq + e
-    int end[NT][2], lo[NT][2];
-#pragma unroll
-    for (int n = 0; n < NT; ++n)
-#pragma unroll
-      for (int e = 0; e < 2; ++e) {
-        const int r = 8 * n + 2 * jq + e, pos = base + r / B.group;
-        end[n][e] = r >= rows ? 0 : p.c.flat ? g.s.m : pos + 1;
-        lo[n][e] = p.c.window > 0 ? max(0, pos + 1 - p.c.window) : 0;
-      }
     // keys below all_end and from all_lo on are seen by every row
     const int all_end = p.c.flat ? g.s.m : base + 1, all_lo = p.c.window > 0 ? max(0, base + tokens - p.c.window) : 0;
+    // is key j seen by row 8 n + 2 jq + e?  (Rows behind the last see none.)
+    auto seen_by = [&](int n, int e, int j) {
+      const int r = 8 * n + 2 * jq + e, pos = base + r / B.group;
+      const int end = r >= rows ? 0 : p.c.flat ? g.s.m : pos + 1;
+      return j < end && (p.c.window <= 0 || j > pos - p.c.window || j < p.c.sinks);
+    };
     float o[NT][4 * VW][4];
 #pragma unroll
     for (int n = 0; n < NT; ++n)
@@ -155,126 +163,146 @@ __global__ void __launch_bounds__(ROWS_THREADS, ROWS4_CTAS<NT>) cs_kv4_rows_kern
       for (int i = 0; i < 4 * VW; ++i)
 #pragma unroll
         for (int c = 0; c < 4; ++c) o[n][i][c] = 0.0f;
-    float m_ref[NT][2], l[NT][2];
+    // of a row: the reference times the scale's factor, the score from which it is raised (by 2^8), the sum
+    float m_ref[NT][2], limit[NT][2], l[NT][2];
+    const float room = RAISE_LOG2 / p.scale_log2;
 #pragma unroll
-    for (int n = 0; n < NT; ++n) m_ref[n][0] = m_ref[n][1] = -INFINITY, l[n][0] = l[n][1] = 0.0f;
+    for (int n = 0; n < NT; ++n)
+#pragma unroll
+      for (int e = 0; e < 2; ++e) m_ref[n][e] = limit[n][e] = -INFINITY, l[n][e] = 0.0f;
     int at = 0;  // the stage of tile k
 #pragma unroll 1
     for (int k = g.k0; k < g.k1; ++k) {
-      const int j0 = g.key0(p.c, k) + warp * 16;
       copies_wait<ST - 2>();
       __syncwarp();  // every lane's copies are there, and the stage before is read
       load(k + ST - 1, checked(next), ring[at == 0 ? ST - 1 : at - 1]);
       next = table_of(k + ST);
       const Stage4<D>& st = ring[at];
       at = at == ST - 1 ? 0 : at + 1;
-      float s[NT][4] = {}, s2[NT][4] = {};
-      {
-        uint32_t ka[KW], kb[KW];
-        const uint8_t* row = st.codes[0][key0] + (D == 128 ? (jq ^ turn(key0)) * 16 : jq * 8);
-        if constexpr (D == 128) {
-          *reinterpret_cast<uint4*>(ka) = *reinterpret_cast<const uint4*>(row);
-          *reinterpret_cast<uint4*>(kb) = *reinterpret_cast<const uint4*>(row + 8 * (D / 2));
-        } else {
-          *reinterpret_cast<uint2*>(ka) = *reinterpret_cast<const uint2*>(row);
-          *reinterpret_cast<uint2*>(kb) = *reinterpret_cast<const uint2*>(row + 8 * (D / 2));
-        }
-        const int group = D == 128 ? jq : jq >> 1;
-        const Four<T> fa(st.scales[0][key0][group] * 0x10001u), fb(st.scales[0][key0 + 8][group] * 0x10001u);
+      const int tile0 = tile_at(k) + warp * 16;
+      // some key is hidden from some row
+      const bool mask = !(tile0 + 80 <= all_end && (tile0 >= all_lo || tile0 + 80 <= p.c.sinks));
+#pragma unroll 1
+      for (int x0 = 0; x0 < 2; x0 += XS) {
+        float s[XS][NT][4] = {};
 #pragma unroll
-        for (int w = 0; w < KW; ++w) {
-          uint32_t a[4], b[4];
-          fa.pairs(ka[w], a);
-          fb.pairs(kb[w], b);
+        for (int x = 0; x < XS; ++x) {
+          uint32_t ka[KW], kb[KW];
+          const int j = (x0 + x) * 16 + key0;
+          const uint8_t* row = st.codes[0][j] + (D == 128 ? (jq ^ turn(key0)) * 16 : jq * 8);
+          if constexpr (D == 128) {
+            *reinterpret_cast<uint4*>(ka) = *reinterpret_cast<const uint4*>(row);
+            *reinterpret_cast<uint4*>(kb) = *reinterpret_cast<const uint4*>(row + 8 * (D / 2));
+          } else {
+            *reinterpret_cast<uint2*>(ka) = *reinterpret_cast<const uint2*>(row);
+            *reinterpret_cast<uint2*>(kb) = *reinterpret_cast<const uint2*>(row + 8 * (D / 2));
+          }
+          const uint8_t* scale = st.scales[0][j] + (D == 128 ? jq : jq >> 1);
+          const Four<T> fa(scale_pair(scale[0])), fb(scale_pair(scale[8 * PIECES]));
 #pragma unroll
-          for (int n = 0; n < NT; ++n) {
-            mma16816<T>(s[n], a[0], b[0], a[1], b[1], q[n][w].x, q[n][w].y);
-            mma16816<T>(s2[n], a[2], b[2], a[3], b[3], q[n][w].z, q[n][w].w);
+          for (int w = 0; w < KW; ++w) {
+            uint32_t a[4], b[4];
+            fa.pairs(ka[w], a);
+            fb.pairs(kb[w], b);
+#pragma unroll
+            for (int n = 0; n < NT; ++n) {
+              mma16816<T>(s[x][n], a[0], b[0], a[1], b[1], q[n][w].x, q[n][w].y);
+              mma16816<T>(s[x][n], a[2], b[2], a[3], b[3], q[n][w].z, q[n][w].w);
+            }
           }
         }
-      }
-      const bool mask = !(j0 + 16 <= all_end && (j0 >= all_lo || j0 + 16 <= p.c.sinks));  // some key is hidden from some row
-      bool raise = false;
-      float mx[NT][2];
+        if (__builtin_expect(mask, 0)) {
 #pragma unroll
-      for (int n = 0; n < NT; ++n) {
+          for (int x = 0; x < XS; ++x)
 #pragma unroll
-        for (int c = 0; c < 4; ++c) s[n][c] = (s[n][c] + s2[n][c]) * p.scale_log2;
-        if (mask) {
+            for (int n = 0; n < NT; ++n)
 #pragma unroll
-          for (int c = 0; c < 4; ++c) {
-            const int key = j0 + key0 + 8 * (c >> 1), e = c & 1;
-            if (!(key < end[n][e] && (key >= lo[n][e] || key < p.c.sinks))) s[n][c] = -INFINITY;
-          }
+              for (int c = 0; c < 4; ++c)
+                if (!seen_by(n, c & 1, tile0 + (x0 + x) * 64 + key0 + 8 * (c >> 1))) s[x][n][c] = -INFINITY;
         }
-#pragma unroll
-        for (int e = 0; e < 2; ++e) {
-          mx[n][e] = fmaxf(s[n][e], s[n][2 + e]);
-          // the reference is raised only when it is exceeded by more than 2^8
-          raise |= mx[n][e] > m_ref[n][e] + RAISE_LOG2 || (m_ref[n][e] == -INFINITY && mx[n][e] > -INFINITY);
-        }
-      }
-      if (__any_sync(0xFFFFFFFFu, raise)) {
+        bool raise = false;
+        float top[NT][2];
 #pragma unroll
         for (int n = 0; n < NT; ++n)
 #pragma unroll
           for (int e = 0; e < 2; ++e) {
-            float top = mx[n][e];
-#pragma unroll
-            for (int d = 4; d < 32; d <<= 1) top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, d));
-            const bool up = top > m_ref[n][e] + RAISE_LOG2 || (m_ref[n][e] == -INFINITY && top > -INFINITY);
-            const float f = up ? cs::ex2_approx(m_ref[n][e] - top) : 1.0f;
-            if (up) m_ref[n][e] = top;
-            l[n][e] *= f;
-#pragma unroll
-            for (int i = 0; i < 4 * VW; ++i) o[n][i][e] *= f, o[n][i][2 + e] *= f;
+            top[n][e] = fmaxf(s[0][n][e], s[0][n][2 + e]);
+            if (XS == 2) top[n][e] = max3(top[n][e], s[XS - 1][n][e], s[XS - 1][n][2 + e]);
+            raise |= top[n][e] > limit[n][e];
           }
-      }
-      uint32_t pt[NT][2];
+        if (__any_sync(0xFFFFFFFFu, raise)) {
 #pragma unroll
-      for (int n = 0; n < NT; ++n) {
+          for (int n = 0; n < NT; ++n)
 #pragma unroll
-        for (int e = 0; e < 2; ++e) {
-          const float sub = m_ref[n][e] == -INFINITY ? 0.0f : m_ref[n][e];
-          s[n][e] = cs::ex2_approx(s[n][e] - sub);
-          s[n][2 + e] = cs::ex2_approx(s[n][2 + e] - sub);
-          l[n][e] += s[n][e] + s[n][2 + e];
+            for (int e = 0; e < 2; ++e) {
+              float m = top[n][e];
+#pragma unroll
+              for (int d = 4; d < 32; d <<= 1) m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, d));
+              if (m > limit[n][e]) {
+                limit[n][e] = m + room;
+                m *= p.scale_log2;
+                const float f = cs::ex2_approx(m_ref[n][e] - m);
+                m_ref[n][e] = m;
+                l[n][e] *= f;
+#pragma unroll
+                for (int i = 0; i < 4 * VW; ++i) o[n][i][e] *= f, o[n][i][2 + e] *= f;
+              }
+            }
         }
-        pt[n][0] = transposed(Pair<T>::put(s[n][0], s[n][1]));
-        pt[n][1] = transposed(Pair<T>::put(s[n][2], s[n][3]));
-      }
-      // V: words of keys key1, key2, key1 + 8 and key2 + 8
-      uint32_t v[4][VW];
-      uint32_t sv[4];
+        uint32_t pt[XS][NT][2];
 #pragma unroll
-      for (int x = 0; x < 4; ++x) {
-        const int key = (x & 1 ? key2 : key1) + 8 * (x >> 1);
-        const uint8_t* row = st.codes[1][key] + (D == 128 ? (((gq >> 1) ^ turn(key)) * 16 + (gq & 1) * 8) : gq * 4);
-        if constexpr (D == 128)
-          *reinterpret_cast<uint2*>(v[x]) = *reinterpret_cast<const uint2*>(row);
-        else
-          v[x][0] = *reinterpret_cast<const uint32_t*>(row);
-        sv[x] = st.scales[1][key][D == 128 ? gq >> 1 : gq >> 2];
-      }
-      if (mask) {  // a scale of a key that no row sees may be anything
+        for (int n = 0; n < NT; ++n) {
 #pragma unroll
-        for (int x = 0; x < 4; ++x) {
-          const int key = j0 + (x & 1 ? key2 : key1) + 8 * (x >> 1);
-          if (!(key < g.hi && (key >= g.lo || key < p.c.sinks))) sv[x] = 0;
+          for (int e = 0; e < 2; ++e) {
+            const float sub = m_ref[n][e] == -INFINITY ? 0.0f : -m_ref[n][e];
+#pragma unroll
+            for (int x = 0; x < XS; ++x) {
+              s[x][n][e] = cs::ex2_approx(fmaf(s[x][n][e], p.scale_log2, sub));
+              s[x][n][2 + e] = cs::ex2_approx(fmaf(s[x][n][2 + e], p.scale_log2, sub));
+              l[n][e] += s[x][n][e] + s[x][n][2 + e];
+            }
+          }
+#pragma unroll
+          for (int x = 0; x < XS; ++x) {
+            pt[x][n][0] = transposed(Pair<T>::put(s[x][n][0], s[x][n][1]));
+            pt[x][n][1] = transposed(Pair<T>::put(s[x][n][2], s[x][n][3]));
+          }
         }
-      }
-      const Four<T> fa(sv[0] | sv[1] << 16), fb(sv[2] | sv[3] << 16);
 #pragma unroll
-      for (int w = 0; w < VW; ++w) {
-        uint32_t a0[4], a1[4], a2[4], a3[4];  // even and odd dimensions of keys key1, key2; of those 8 behind
-        fa.pairs(__byte_perm(v[0][w], v[1][w], 0x5410), a0);
-        fa.pairs(__byte_perm(v[0][w], v[1][w], 0x7632), a1);
-        fb.pairs(__byte_perm(v[2][w], v[3][w], 0x5410), a2);
-        fb.pairs(__byte_perm(v[2][w], v[3][w], 0x7632), a3);
+        for (int x = 0; x < XS; ++x) {
+          // V: words of keys key1, key2, key1 + 8 and key2 + 8 of the run
+          uint32_t v[4][VW], sv[4];
 #pragma unroll
-        for (int i = 0; i < 4; ++i)
+          for (int y = 0; y < 4; ++y) {
+            const int of = y & 1 ? key2 : key1, j = (x0 + x) * 16 + of + 8 * (y >> 1);
+            const uint8_t* row = st.codes[1][j] + (D == 128 ? (((gq >> 1) ^ turn(of)) * 16 + (gq & 1) * 8) : gq * 4);
+            if constexpr (D == 128)
+              *reinterpret_cast<uint2*>(v[y]) = *reinterpret_cast<const uint2*>(row);
+            else
+              v[y][0] = *reinterpret_cast<const uint32_t*>(row);
+            sv[y] = st.scales[1][j][D == 128 ? gq >> 1 : gq >> 2];
+          }
+          if (__builtin_expect(mask, 0)) {  // a scale of a key that no row sees may be anything
 #pragma unroll
-          for (int n = 0; n < NT; ++n) mma16816<T>(o[n][4 * w + i], a0[i], a1[i], a2[i], a3[i], pt[n][0], pt[n][1]);
+            for (int y = 0; y < 4; ++y) {
+              const int key = tile0 + (x0 + x) * 64 + (y & 1 ? key2 : key1) + 8 * (y >> 1);
+              if (!(key < g.hi && (key >= g.lo || key < p.c.sinks))) sv[y] = 0;
+            }
+          }
+          const Four<T> fa(scale_pair(sv[0], sv[1])), fb(scale_pair(sv[2], sv[3]));
+#pragma unroll
+          for (int w = 0; w < VW; ++w) {
+            uint32_t a0[4], a1[4], a2[4], a3[4];  // even and odd dimensions of keys key1, key2; of those 8 behind
+            fa.pairs(__byte_perm(v[0][w], v[1][w], 0x5410), a0);
+            fa.pairs(__byte_perm(v[0][w], v[1][w], 0x7632), a1);
+            fb.pairs(__byte_perm(v[2][w], v[3][w], 0x5410), a2);
+            fb.pairs(__byte_perm(v[2][w], v[3][w], 0x7632), a3);
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+#pragma unroll
+              for (int n = 0; n < NT; ++n) mma16816<T>(o[n][4 * w + i], a0[i], a1[i], a2[i], a3[i], pt[x][n][0], pt[x][n][1]);
+          }
+        }
       }
     }
     copies_wait<0>();

@@ -66,14 +66,20 @@ struct AttnP {
 };
 
 // Two softmax warpgroups, one per S buffer with a row per thread, and one with the
-// TMA warp, two MMA warps and an idle one.
-constexpr int ATTN_THREADS = 384;
+// TMA warp, two MMA warps and an idle one; over a cache in 4 bits one more, which makes the tiles.
+template <bool FOUR>
+constexpr int ATTN_THREADS_OF = FOUR ? 512 : 384;
+constexpr int ATTN_THREADS = ATTN_THREADS_OF<false>;
 // Registers: 65536 / 384 gives every thread 168 at launch; a softmax thread holds a
 // row of S, so the third warpgroup hands over what it does not need
-// (2 x 216 + 72 = 3 x 168).  Nothing may spill: next to 226 KB of shared memory the
-// L1 holds nearly nothing, and a spilled register comes back from L2.
-constexpr int SOFTMAX_REGS = 216, OTHER_REGS = 72;
-static_assert(2 * SOFTMAX_REGS + OTHER_REGS <= 3 * 168, "more registers than the launch holds");
+// (2 x 216 + 72 = 3 x 168; with a fourth 2 x 200 + 2 x 56 = 4 x 128).  Nothing may spill: next to
+// 226 KB of shared memory the L1 holds nearly nothing, and a spilled register comes back from L2.
+template <bool FOUR>
+constexpr int SOFTMAX_REGS = FOUR ? 200 : 216;
+template <bool FOUR>
+constexpr int OTHER_REGS = FOUR ? 56 : 72;
+static_assert(2 * SOFTMAX_REGS<false> + OTHER_REGS<false> <= 3 * 168 && 2 * SOFTMAX_REGS<true> + 2 * OTHER_REGS<true> <= 4 * 128,
+              "more registers than the launch holds");
 template <int N>
 __device__ __forceinline__ void regs_inc() {
   asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
@@ -86,22 +92,27 @@ constexpr uint32_t COL_S = 0, COL_O = 256;
 constexpr int CTL = 1024;  // bytes of the control block
 constexpr float RAISE_LOG2 = 8.0f;  // the reference maximum follows a row's when it is exceeded by more than 2^8
 
-template <int D>
+template <int D, bool FOUR = false>
 struct AttnShape {
   static constexpr int HALVES = D / 64;
   static constexpr int TILE = KT * D * 2;              // bytes of a 128-row tile of Q, K or V
-  static constexpr int SLOTS = D == 128 ? 5 : 10;      // ring of K and V tiles: 160 KB in flight
-  static constexpr int SMEM = 2 * TILE + SLOTS * TILE + 1024 + CTL;
+  // ring of K and V tiles: 160 KB in flight, or 128 KB and 25 KB of codes and scales
+  static constexpr int SLOTS = FOUR ? (D == 128 ? 4 : 8) : (D == 128 ? 5 : 10);
+  static constexpr int STAGES = FOUR ? (D == 128 ? 3 : 6) : 0;
+  static constexpr int CODES = KT * D / 2, STAGE = CODES + KT * D / GROUP4;  // bytes of a tile's codes, and with its scales
+  static constexpr int SMEM = 2 * TILE + SLOTS * TILE + STAGES * STAGE + 1024 + CTL;
 };
 
-template <int SLOTS>
+template <typename Sh>
 struct AttnCtl {
+  static constexpr int SLOTS = Sh::SLOTS, STAGES = Sh::STAGES;
   uint64_t full[SLOTS], empty[SLOTS];
+  uint64_t stage_full[STAGES + 1], stage_empty[STAGES + 1];  // (one more than there are, for there may be none)
   uint64_t q_full[2], q_empty[2], s_full[2], p_full[2][2], o_full[2];
   uint64_t v_ready[2];                 // the values of the buffer's tile are there
   uint64_t other_full, other_empty;    // warpgroup 1's half of an item of one row tile
   uint64_t drained;
-  unsigned long long scratch[ATTN_THREADS / 32];
+  unsigned long long scratch[512 / 32];
   Range range;
   uint32_t tmem;
   volatile int abort;
@@ -123,6 +134,19 @@ __device__ __forceinline__ void tma_3d(void* dst, const CUtensorMap* map, int x,
           cs::smem_u32(dst)),
       "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(c1), "r"(c2), "r"(cs::smem_u32(bar))
       : "memory");
+}
+__device__ __forceinline__ void tma_4d(void* dst, const CUtensorMap* map, int x, int c1, int c2, int c3, uint64_t* bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4, %5}], [%6];" ::"r"(
+          cs::smem_u32(dst)),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(c1), "r"(c2), "r"(c3), "r"(cs::smem_u32(bar))
+      : "memory");
+}
+// both addresses and the size multiples of 16 bytes
+__device__ __forceinline__ void bulk_copy(void* dst, const void* src, uint32_t bytes, uint64_t* bar) {
+  asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(cs::smem_u32(dst)),
+               "l"(src), "r"(bytes), "r"(cs::smem_u32(bar))
+               : "memory");
 }
 // D(tmem) (+)= A(tmem) * B(smem): the 16-bit A operand holds two K values per 32-bit column.
 __device__ __forceinline__ void mma_ts(uint32_t d_tmem, uint32_t a_tmem, uint64_t b_desc, uint32_t idesc, uint32_t acc) {
@@ -175,17 +199,19 @@ __device__ __forceinline__ bool wait_warp(uint64_t* bar, uint32_t parity, Ctl* s
 
 // After a wait that ran out, one thread: this CTA's copies and MMAs in flight
 // come to rest (again with a limit) before its memory is given back.
-template <int SLOTS>
-__device__ void come_to_rest(AttnCtl<SLOTS>* sc, const AttnP& p) {
+template <typename Sh>
+__device__ void come_to_rest(AttnCtl<Sh>* sc, const AttnP& p) {
   record(p.b.ctrl, ERR_WATCHDOG, WHAT_WAIT, blockIdx.x);
   int tries = 0;
   auto settle = [&](uint64_t* bar, uint32_t parity) {
     while (!cs::mbar_try_wait(bar, parity) && ++tries < SETTLE_TRIES) {
     }
   };
-  for (int i = 0; i < SLOTS; ++i) {
-    const int n = (sc->loads - i + SLOTS - 1) / SLOTS;  // loads into slot i
-    if (n > 0) settle(&sc->full[i], (n - 1) & 1);
+  constexpr int COUNT = Sh::STAGES > 0 ? Sh::STAGES : Sh::SLOTS;
+  uint64_t* const copied = Sh::STAGES > 0 ? sc->stage_full : sc->full;
+  for (int i = 0; i < COUNT; ++i) {
+    const int n = (sc->loads - i + COUNT - 1) / COUNT;  // loads into slot i
+    if (n > 0) settle(&copied[i], (n - 1) & 1);
   }
   for (int w = 0; w < 2; ++w)
     if (sc->q_loads[w] > 0) settle(&sc->q_full[w], (sc->q_loads[w] - 1) & 1);
@@ -214,7 +240,7 @@ struct Ring {
 // tile lies in shared memory as [8-key group][64-dimension half][8 x 128 bytes],
 // so that one box brings a page's slots of a head with all dimensions.
 template <int D>
-__device__ bool load_role(const AttnP& p, AttnCtl<AttnShape<D>::SLOTS>* sc, uint8_t* qbuf, uint8_t* ring) {
+__device__ bool load_role(const AttnP& p, AttnCtl<AttnShape<D>>* sc, uint8_t* qbuf, uint8_t* ring) {
   using Sh = AttnShape<D>;
   const Batch& B = p.b;
   const int lane = threadIdx.x & 31;
@@ -277,23 +303,19 @@ __device__ bool load_role(const AttnP& p, AttnCtl<AttnShape<D>::SLOTS>* sc, uint
   return true;
 }
 
-// A cache in 4 bits: two warps make the tiles that load_role's copies bring, each 64 keys of
-// every tile, straight into the swizzled layout; the first one also has the queries copied.  A lane
-// has 32 dimensions of a key (16 bytes and their scale), the lanes of a store 8 keys, so that their
-// 16-byte pieces fall into different banks.  A few loads are on their way in registers.
-constexpr int LOAD4_WARPS = 2;
-template <typename T, int D>
-__device__ bool load4_role(const AttnP& p, AttnCtl<AttnShape<D>::SLOTS>* sc, uint8_t* qbuf, uint8_t* ring, int second) {
-  using Sh = AttnShape<D>;
-  constexpr int PIECES = D / GROUP4, ROWS_OF = 32 / PIECES, LOADS = 64 / ROWS_OF, AHEAD = 4;  // rows of a load, loads of a tile
+// A cache in 4 bits, TMA warp: the item's queries, and codes and scales of K and V of each key tile, page by
+// page.  Codes lie by key, 64 (32) bytes each, their 16-byte pieces swizzled by the copy.
+template <int D>
+__device__ bool load4_role(const AttnP& p, AttnCtl<AttnShape<D, true>>* sc, uint8_t* qbuf, uint8_t* stages) {
+  using Sh = AttnShape<D, true>;
   const Batch& B = p.b;
-  const int lane = threadIdx.x & 31, row = lane % ROWS_OF, piece = lane / ROWS_OF;
+  const int lane = threadIdx.x & 31;
+  const int pages_per_tile = KT >> B.page_shift, groups = B.page_size >> 3;
+  const uint32_t code_bytes = B.page_size * (D / 2), scale_bytes = B.page_size * (D / GROUP4);
   Walk walk(p.c, sc->range);
   Seg g;
-  Ring<Sh::SLOTS> rp;
+  Ring<Sh::STAGES> rp;
   uint32_t q_phase[2] = {1, 1};
-  uint4 codes[AHEAD];
-  uint32_t scale[AHEAD];
   while (walk.next(B, p.c, g)) {
     const int* table = p.c.flat ? p.pages : B.table + static_cast<long long>(g.b) * B.table_cols;
     const bool two = g.s.n - g.item * p.c.per_item > p.per_tile;
@@ -309,64 +331,115 @@ __device__ bool load4_role(const AttnP& p, AttnCtl<AttnShape<D>::SLOTS>* sc, uin
       }
       return true;
     };
-    if (!second && !queries(0)) return false;
-    // lane i < 4: the page of this warp's keys 16 i .. 16 i + 15 of tile k, -1: none of them is seen
+    if (!queries(0)) return false;
+    // the page that this lane brings of tile k, -1: none of its keys is seen
     auto page_of = [&](int k) {
-      if (k >= g.k1 || lane >= 4) return -1;
-      const int j0 = g.key0(p.c, k) + second * 64 + lane * 16;
-      if (j0 >= g.hi || (j0 + 16 <= g.lo && j0 >= p.c.sinks)) return -1;
+      if (k >= g.k1 || lane >= pages_per_tile) return -1;
+      const int j0 = g.key0(p.c, k) + (lane << B.page_shift), j1 = j0 + B.page_size;
+      if (j0 >= g.hi || (j1 <= g.lo && j0 >= p.c.sinks)) return -1;
       const int page = __ldg(table + (j0 >> B.page_shift));
       if (page >= 0 && page < B.num_pages) return page;
       record(B.ctrl, ERR_INVALID, WHAT_PAGE, p.c.flat ? 0xFFFFFFFFu : static_cast<uint32_t>(g.b));
       return -1;
     };
-    // load i of K or V of tile k; zeros for keys that no row of the item sees
-    auto fetch = [&](int into, int half, int pages, int k, int i) {
-      const int page = __shfl_sync(0xFFFFFFFFu, pages, i * ROWS_OF / 16);
-      const int key = g.key0(p.c, k) + second * 64 + i * ROWS_OF + row, slot = key & (B.page_size - 1);
-      codes[into] = make_uint4(0, 0, 0, 0);
-      scale[into] = 0;
-      if (page >= 0 && key < g.hi && (key >= g.lo || key < p.c.sinks)) {
-        const long long at = page * B.page_stride + slot * B.slot_stride + g.kvh * B.head_stride;
-        codes[into] = __ldg(reinterpret_cast<const uint4*>(static_cast<const uint8_t*>(half ? p.v_raw : p.k_raw) + at / 2) + piece);
-        scale[into] = __ldg((half ? p.v_scales : p.k_scales) + scale_row(B, page, slot, g.kvh) * PIECES + piece);
-      }
-    };
-    int pages = page_of(g.k0);
-#pragma unroll
-    for (int i = 0; i < AHEAD; ++i) fetch(i, 0, pages, g.k0, i);
+    int page = page_of(g.k0);
 #pragma unroll 1
     for (int k = g.k0; k < g.k1; ++k) {
+      const uint32_t boxes = __popc(__ballot_sync(0xFFFFFFFFu, page >= 0));
       const int after = page_of(k + 1);
+      const int c2 = p.head_groups ? 0 : g.kvh;
+      const int c3 = page * (p.head_groups ? p.head_groups * B.kv_heads : groups) + g.kvh * p.head_groups;
+      const long long scales = scale_row(B, page, 0, g.kvh) * (D / GROUP4);
 #pragma unroll 1
       for (int half = 0; half < 2; ++half) {  // K, then V
-        if (!wait_warp(&sc->empty[rp.slot], rp.phase ^ 1u, sc)) return false;
-        uint8_t* const tile = ring + rp.slot * Sh::TILE + (second * 8 + (row >> 3)) * (Sh::HALVES * 1024) +
-                              (piece >> 1) * 1024 + (row & 7) * 128;
+        uint64_t* bar = &sc->stage_full[rp.slot];
+        if (!wait_warp(&sc->stage_empty[rp.slot], rp.phase ^ 1u, sc)) return false;
+        if (lane == 0) {
+          cs::mbar_arrive_expect_tx(bar, boxes * (code_bytes + scale_bytes));
+          ++sc->loads;
+        }
+        __syncwarp();
+        if (page >= 0) {
+          uint8_t* to = stages + rp.slot * Sh::STAGE;
+          tma_4d(to + lane * code_bytes, half ? &p.v : &p.k, 0, 0, c2, c3, bar);
+          bulk_copy(to + Sh::CODES + lane * scale_bytes, (half ? p.v_scales : p.k_scales) + scales, scale_bytes, bar);
+        }
+        rp.next();
+        // the second row tile's queries, which the last item may still hold, after the first keys
+        if (two && k == g.k0 && half == 0 && !queries(1)) return false;
+      }
+      page = after;
+    }
+  }
+  return true;
+}
+
+// A cache in 4 bits, a warpgroup: tiles of the operands, in the layout that load_role's copies have, from codes and
+// scales.  Warp w has 32 keys of every tile.  A lane has 32 dimensions of a key, the lanes of a load
+// and of a store (8 at a time) 8 keys, so that their 16-byte pieces fall into different banks.
+constexpr int MAKE4_WARPS = 4;
+template <typename T, int D>
+__device__ bool make4_role(const AttnP& p, AttnCtl<AttnShape<D, true>>* sc, const uint8_t* stages, uint8_t* ring, int w) {
+  using Sh = AttnShape<D, true>;
+  constexpr int PIECES = D / GROUP4, ROWS_OF = 32 / PIECES, LOADS = 32 / ROWS_OF;  // keys of a load, loads of a tile
+  const int lane = threadIdx.x & 31, row = lane % ROWS_OF, piece = lane / ROWS_OF;
+  const int first = w * 32 + row;  // this lane's first key
+  const int turn = D == 128 ? row >> 1 & 3 : row >> 2 & 1;  // of the copies' swizzle
+  const uint8_t* const codes = stages + first * (D / 2) + ((piece ^ turn) << 4);
+  const uint8_t* const scales = stages + Sh::CODES + first * PIECES + piece;
+  uint8_t* const tile = ring + (first >> 3) * (Sh::HALVES * 1024) + (piece >> 1) * 1024 + (row & 7) * 128;
+  Walk walk(p.c, sc->range);
+  Seg g;
+  Ring<Sh::STAGES> from;
+  Ring<Sh::SLOTS> to;
+  while (walk.next(p.b, p.c, g)) {
+#pragma unroll 1
+    for (int k = g.k0; k < g.k1; ++k) {
+      const int j0 = g.key0(p.c, k);
+      // some key is seen by no row of the item: zeros in its place, whatever its scale (or what it was copied over) is
+      const bool edge = j0 + KT > g.hi || (j0 < g.lo && j0 + KT > p.c.sinks);
+#pragma unroll 1
+      for (int half = 0; half < 2; ++half) {  // K, then V
+        if (!wait_warp(&sc->stage_full[from.slot], from.phase, sc)) return false;
+        if (!wait_warp(&sc->empty[to.slot], to.phase ^ 1u, sc)) return false;
+        const uint8_t* c = codes + from.slot * Sh::STAGE;
+        const uint8_t* s = scales + from.slot * Sh::STAGE;
+        uint4 words[LOADS];
+        uint32_t byte[LOADS];
 #pragma unroll
         for (int i = 0; i < LOADS; ++i) {
-          const Four<T> four(scale[i % AHEAD] * 0x10001u);
-          const uint32_t words[4] = {codes[i % AHEAD].x, codes[i % AHEAD].y, codes[i % AHEAD].z, codes[i % AHEAD].w};
+          words[i] = *reinterpret_cast<const uint4*>(c + i * ROWS_OF * (D / 2));
+          byte[i] = s[i * ROWS_OF * PIECES];
+        }
+        if (edge) {
 #pragma unroll
-          for (int w = 0; w < 4; ++w) {
+          for (int i = 0; i < LOADS; ++i) {
+            const int key = j0 + first + i * ROWS_OF;
+            if (!(key < g.hi && (key >= g.lo || key < p.c.sinks))) byte[i] = 0;
+          }
+        }
+        uint8_t* d = tile + to.slot * Sh::TILE;
+#pragma unroll
+        for (int i = 0; i < LOADS; ++i) {
+          const Four<T> four(scale_pair(byte[i]));
+          const uint32_t ws[4] = {words[i].x, words[i].y, words[i].z, words[i].w};
+#pragma unroll
+          for (int v = 0; v < 4; ++v) {
             uint32_t x[4];
-            four.pairs(words[w], x);
-            *reinterpret_cast<uint4*>(tile + i * ROWS_OF / 8 * (Sh::HALVES * 1024) + ((((piece & 1) * 4 + w) ^ (row & 7)) << 4)) =
+            four.pairs(ws[v], x);
+            *reinterpret_cast<uint4*>(d + i * ROWS_OF / 8 * (Sh::HALVES * 1024) + ((((piece & 1) * 4 + v) ^ (row & 7)) << 4)) =
                 make_uint4(x[0], x[1], x[2], x[3]);
           }
-          const int next = i + AHEAD;
-          if (next < LOADS)
-            fetch(i % AHEAD, half, pages, k, next);
-          else
-            fetch(i % AHEAD, half ^ 1, half ? after : pages, k + half, next - LOADS);
         }
         cs::fence_proxy_async_shared();
         __syncwarp();
-        if (lane == 0) cs::mbar_arrive(&sc->full[rp.slot]);
-        rp.next();
-        if (!second && two && k == g.k0 && half == 0 && !queries(1)) return false;
+        if (lane == 0) {
+          cs::mbar_arrive(&sc->full[to.slot]);
+          cs::mbar_arrive(&sc->stage_empty[from.slot]);
+        }
+        from.next();
+        to.next();
       }
-      pages = after;
     }
   }
   return true;
@@ -416,9 +489,9 @@ struct Queries {
 // buffer's warp is issuing: with one warp for both buffers a step of 1024 cycles took 2300.
 // A buffer's MMAs are issued by one thread and execute in that order, and no
 // MMA reads what the other buffer's write.
-template <int D, bool WINDOW>
-__device__ bool mma_role(const AttnP& p, AttnCtl<AttnShape<D>::SLOTS>* sc, uint8_t* qbuf, uint8_t* ring, int bf16, int w) {
-  using Sh = AttnShape<D>;
+template <int D, bool WINDOW, bool FOUR>
+__device__ bool mma_role(const AttnP& p, AttnCtl<AttnShape<D, FOUR>>* sc, uint8_t* qbuf, uint8_t* ring, int bf16, int w) {
+  using Sh = AttnShape<D, FOUR>;
   const uint32_t idesc_s = cs::make_idesc_f16(bf16, 0, 128, KT);
   const uint32_t idesc_o = cs::make_idesc_f16(bf16, 1, 128, D);
   const uint32_t s_tm = sc->tmem + COL_S + w * 128, o_tm = sc->tmem + COL_O + w * D;
@@ -605,10 +678,10 @@ __device__ __forceinline__ void st32(void* p, const uint32_t* v) {
 __device__ __forceinline__ uint32_t below(int n) { return n >= 32 ? 0xFFFFFFFFu : n <= 0 ? 0u : (1u << n) - 1u; }
 
 // Warpgroup w: the softmax of the steps with S buffer w, one row per thread, and the output.
-// FOUR: the tiles come from a cache in 4 bits (load4_role), with zeros where no row of the item sees a key.
+// FOUR: the tiles come from a cache in 4 bits (make4_role), with zeros where no row of the item sees a key.
 template <typename T, int D, bool WINDOW, bool FOUR>
-__device__ bool softmax_role(const AttnP& p, AttnCtl<AttnShape<D>::SLOTS>* sc, uint8_t* ring, int w) {
-  using Sh = AttnShape<D>;
+__device__ bool softmax_role(const AttnP& p, AttnCtl<AttnShape<D, FOUR>>* sc, uint8_t* ring, int w) {
+  using Sh = AttnShape<D, FOUR>;
   constexpr int CH = D / 32;                                      // chunks of 32 columns of O
   const Batch& B = p.b;
   const int r = threadIdx.x & 127, lane = threadIdx.x & 31;
@@ -1095,22 +1168,27 @@ __global__ void __launch_bounds__(JOIN_THREADS, JOIN_CTAS) cs_kv_join_kernel(con
 }
 
 // WINDOW: whether keys may be hidden behind a row's window (without, what deals with it is
-// not in the code of the inner loops).  FOUR: the cache is in 4 bits, and two warps make tiles of it
+// not in the code of the inner loops).  FOUR: the cache is in 4 bits, and a warpgroup makes tiles of it
 template <typename T, int D, bool WINDOW, bool FOUR = false>
-__global__ void __launch_bounds__(ATTN_THREADS, 1) cs_kv_attn_kernel(const __grid_constant__ AttnP p) {
-  using Sh = AttnShape<D>;
-  using Ctl = AttnCtl<Sh::SLOTS>;
+__global__ void __launch_bounds__(ATTN_THREADS_OF<FOUR>, 1) cs_kv_attn_kernel(const __grid_constant__ AttnP p) {
+  using Sh = AttnShape<D, FOUR>;
+  using Ctl = AttnCtl<Sh>;
   static_assert(sizeof(Ctl) <= CTL, "control block");
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   uint8_t* qbuf = smem;
   uint8_t* ring = smem + 2 * Sh::TILE;
-  Ctl* sc = reinterpret_cast<Ctl*>(ring + Sh::SLOTS * Sh::TILE);
+  uint8_t* stages = ring + Sh::SLOTS * Sh::TILE;
+  Ctl* sc = reinterpret_cast<Ctl*>(stages + Sh::STAGES * Sh::STAGE);
   const int warp = threadIdx.x >> 5;
   if (threadIdx.x == 0) {
     for (int i = 0; i < Sh::SLOTS; ++i) {
-      cs::mbar_init(&sc->full[i], FOUR ? LOAD4_WARPS : 1);
+      cs::mbar_init(&sc->full[i], FOUR ? MAKE4_WARPS : 1);
       cs::mbar_init(&sc->empty[i], 2);  // both MMA warps
+    }
+    for (int i = 0; i < Sh::STAGES; ++i) {
+      cs::mbar_init(&sc->stage_full[i], 1);
+      cs::mbar_init(&sc->stage_empty[i], MAKE4_WARPS);
     }
     for (int w = 0; w < 2; ++w) {
       cs::mbar_init(&sc->q_full[w], 1);
@@ -1126,10 +1204,8 @@ __global__ void __launch_bounds__(ATTN_THREADS, 1) cs_kv_attn_kernel(const __gri
     sc->abort = sc->turn = sc->loads = sc->q_loads[0] = sc->q_loads[1] = 0;
     cs::fence_mbar_init();
     cs::prefetch_tmap(&p.q);
-    if (!FOUR) {
-      cs::prefetch_tmap(&p.k);
-      cs::prefetch_tmap(&p.v);
-    }
+    cs::prefetch_tmap(&p.k);
+    cs::prefetch_tmap(&p.v);
   }
   if (warp == 9) {
     cs::tmem_alloc<1>(&sc->tmem, 512);
@@ -1141,20 +1217,21 @@ __global__ void __launch_bounds__(ATTN_THREADS, 1) cs_kv_attn_kernel(const __gri
   cs::grid_dep_wait();
   cs::grid_dep_launch_dependents();
   if (threadIdx.x == 0) p.splits[blockIdx.x].pieces = 0;
-  find_range<ATTN_THREADS>(p.b, p.c, &sc->range, sc->scratch);
+  find_range<ATTN_THREADS_OF<FOUR>>(p.b, p.c, &sc->range, sc->scratch);
   constexpr int bf16 = sizeof(T) == 2 && !std::is_same<T, __half>::value;
   if (warp < 8) {
-    regs_inc<SOFTMAX_REGS>();
+    regs_inc<SOFTMAX_REGS<FOUR>>();
     // (a softmax that gave up may have stores to tensor memory on their way)
     if (!softmax_role<T, D, WINDOW, FOUR>(p, sc, ring, warp >> 2)) cs::tc_wait_st();
   } else {
-    regs_dec<OTHER_REGS>();
+    regs_dec<OTHER_REGS<FOUR>>();
     if constexpr (FOUR) {
-      if (warp == 8 || warp == 11) load4_role<T, D>(p, sc, qbuf, ring, warp == 11);
+      if (warp == 8) load4_role<D>(p, sc, qbuf, stages);
+      if (warp >= 12) make4_role<T, D>(p, sc, stages, ring, warp - 12);
     } else {
       if (warp == 8) load_role<D>(p, sc, qbuf, ring);
     }
-    if (warp == 9 || warp == 10) mma_role<D, WINDOW>(p, sc, qbuf, ring, bf16, warp - 9);
+    if (warp == 9 || warp == 10) mma_role<D, WINDOW, FOUR>(p, sc, qbuf, ring, bf16, warp - 9);
   }
   __syncwarp();
   cs::tc_fence_before();

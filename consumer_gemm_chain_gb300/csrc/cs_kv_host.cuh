@@ -40,6 +40,7 @@ struct cs_kv_s {
   // copies of a cache (its address is put in by each call): a whole page's slots of a
   // head, and 16 slots
   CUtensorMap page_map, slots_map;
+  CUtensorMap codes_map;  // of a cache's codes: a whole page's slots of a head
   bool error_latched = false;
   bool four_ready = false;  // the kernels of caches in 4 bits have their shared memory
 };
@@ -310,7 +311,8 @@ inline cs_status map_caches(cskv::AttnP& k, const CUtensorMap& like) {
 // The kernels of a call with at most `max_rows` rows per key head, and the maps of their caches' copies.
 struct Kernels {
   const void *rows, *attn, *join;
-  int rows_grid, rows_smem, attn_smem;
+  int rows_shift;  // keys of a tile of the kernel for few rows
+  int rows_grid, rows_smem, attn_smem, attn_threads;
   const CUtensorMap *rows_map, *attn_map;  // nullptr: read through pointers
 };
 
@@ -321,7 +323,7 @@ inline cs_status run_attention(cs_kv_s* p, cskv::AttnP& k, const Kernels& use, i
   cs_status s;
   if (max_rows <= cskv::ROWS) {
     k.c.per_item = cskv::ROWS / k.b.group;
-    k.c.shift = cskv::ROWS_SHIFT;
+    k.c.shift = use.rows_shift;
     if (use.rows_map && (s = map_caches(k, *use.rows_map)) != CS_OK) return s;
     s = launch(use.rows, dim3(use.rows_grid), cskv::ROWS_THREADS, use.rows_smem, &k, st);
     if (s != CS_OK || max_rows <= k.b.group || k.c.flat) return s;
@@ -356,7 +358,7 @@ inline cs_status run_attention(cs_kv_s* p, cskv::AttnP& k, const Kernels& use, i
     k.c.whole = 1;
     k.num_splits = 0;
   }
-  if ((s = launch(use.attn, dim3(p->num_sms), cskv::ATTN_THREADS, use.attn_smem, &k, st)) != CS_OK) return s;
+  if ((s = launch(use.attn, dim3(p->num_sms), use.attn_threads, use.attn_smem, &k, st)) != CS_OK) return s;
   return launch(use.join, dim3((k.c.whole ? 1 : cskv::JOIN_CTAS) * p->num_sms), cskv::JOIN_THREADS, 0, &k, st);
 }
 
