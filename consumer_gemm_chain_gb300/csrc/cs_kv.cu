@@ -113,6 +113,7 @@ Kernels kernels(const cs_kv_s* p) {
   u.join = join_kernel(p->d);
   u.rows_grid = p->num_sms * cskv::ROWS_CTAS;
   u.rows_shift = cskv::ROWS_SHIFT;
+  u.head_ctas = 0;
   u.rows_smem = rows_smem(p->d);
   u.rows_map = &p->slots_map;
   u.attn_map = &p->page_map;

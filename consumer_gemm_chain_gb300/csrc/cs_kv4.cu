@@ -34,14 +34,22 @@ cs_status add_caches(const cs_kv_desc& d, const cs_kv4_cache& k, const cs_kv4_ca
   return s != CS_OK ? s : add_cache(d, "v", v, parts);
 }
 
+template <typename T, int D, int NT>
+const void* rows_kernel_of(bool by_head) {
+  return by_head ? (const void*)cskv::cs_kv4_rows_kernel<T, D, NT, true> : (const void*)cskv::cs_kv4_rows_kernel<T, D, NT, false>;
+}
+
 template <typename T, int D>
 Kernels kernels_of(const cs_kv_s* p, int max_rows) {
   const bool window = p->d.window > 0 && p->d.window < kMaxKeys, narrow = max_rows <= 8;
   Kernels u;
-  u.rows = narrow ? (const void*)cskv::cs_kv4_rows_kernel<T, D, 1> : (const void*)cskv::cs_kv4_rows_kernel<T, D, 2>;
+  u.rows_grid = p->num_sms * (narrow ? cskv::ROWS4_CTAS<1> : cskv::ROWS4_CTAS<2>);
+  // with the heads' rows side by side, and at least eight CTAs for each, by heads
+  const bool by_head = p->d.cache_layout == CS_KV_TOKEN && p->d.kv_heads > 1 && u.rows_grid >= 8 * p->d.kv_heads;
+  u.head_ctas = by_head ? u.rows_grid / p->d.kv_heads : 0;
+  u.rows = narrow ? rows_kernel_of<T, D, 1>(by_head) : rows_kernel_of<T, D, 2>(by_head);
   u.attn = window ? (const void*)cskv::cs_kv_attn_kernel<T, D, true, true> : (const void*)cskv::cs_kv_attn_kernel<T, D, false, true>;
   u.join = (const void*)cskv::cs_kv_join_kernel<T, D, true>;
-  u.rows_grid = p->num_sms * (narrow ? cskv::ROWS4_CTAS<1> : cskv::ROWS4_CTAS<2>);
   u.rows_shift = cskv::ROWS4_SHIFT;
   u.rows_smem = sizeof(cskv::Rows4Shared<D>);
   u.attn_smem = cskv::AttnShape<D, true>::SMEM;

@@ -44,6 +44,13 @@ __device__ __forceinline__ float2 four_pair(const uint8_t* codes, const uint8_t*
 __device__ __forceinline__ uint32_t scale_pair(uint32_t byte) { return byte * 0x00800080u; }
 __device__ __forceinline__ uint32_t scale_pair(uint32_t low, uint32_t high) { return high * 0x00800000u + low * 0x80u; }
 
+// (w & mask) | bits, in one instruction (the compiler makes two of it, with an immediate each).
+__device__ __forceinline__ uint32_t masked(uint32_t w, uint32_t mask, uint32_t bits) {
+  uint32_t x;
+  asm("lop3.b32 %0, %1, %2, %3, 0xEA;" : "=r"(x) : "r"(w), "r"(mask), "r"(bits));
+  return x;
+}
+
 // Two scales, and what turns codes into values.
 template <typename T>
 struct Four;
@@ -56,11 +63,11 @@ struct Four<__half> {
   // bits: the scales as halves (scale_pair)
   __device__ __forceinline__ explicit Four(uint32_t bits) { s = *reinterpret_cast<__half2*>(&bits); }
   static __device__ __forceinline__ __half2 low(uint32_t w) {
-    const uint32_t x = (w & 0x000F000Fu) | 0x64006400u, bias = 0x64086408u;  // 1032
+    const uint32_t x = masked(w, 0x000F000Fu, 0x64006400u), bias = 0x64086408u;  // 1032
     return __hsub2(*reinterpret_cast<const __half2*>(&x), *reinterpret_cast<const __half2*>(&bias));
   }
   static __device__ __forceinline__ __half2 high(uint32_t w) {
-    const uint32_t x = (w & 0x00F000F0u) | 0x64006400u, by = 0x2C002C00u, bias = 0xD480D480u;  // 1/16, -72
+    const uint32_t x = masked(w, 0x00F000F0u, 0x64006400u), by = 0x2C002C00u, bias = 0xD480D480u;  // 1/16, -72
     return __hfma2(*reinterpret_cast<const __half2*>(&x), *reinterpret_cast<const __half2*>(&by),
                    *reinterpret_cast<const __half2*>(&bias));
   }
@@ -87,7 +94,7 @@ struct Four<__nv_bfloat16> {
   __device__ __forceinline__ void pairs(uint32_t w, uint32_t (&x)[4]) const {
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-      const uint32_t y = (w >> 4 * i & 0x000F000Fu) | 0x43004300u;
+      const uint32_t y = masked(w >> 4 * i, 0x000F000Fu, 0x43004300u);
       *reinterpret_cast<__nv_bfloat162*>(&x[i]) = __hfma2(*reinterpret_cast<const __nv_bfloat162*>(&y), s, off);
     }
   }

@@ -63,7 +63,7 @@ __device__ __forceinline__ uint32_t transposed(uint32_t x) {
 }
 
 // NT: groups of 8 rows
-template <typename T, int D, int NT>
+template <typename T, int D, int NT, bool BY_HEAD>
 __global__ void __launch_bounds__(ROWS_THREADS, ROWS4_CTAS<NT>) cs_kv4_rows_kernel(const __grid_constant__ AttnP p) {
   extern __shared__ __align__(1024) uint8_t rows_smem[];
   Rows4Shared<D>& sm = *reinterpret_cast<Rows4Shared<D>*>(rows_smem);
@@ -74,7 +74,7 @@ __global__ void __launch_bounds__(ROWS_THREADS, ROWS4_CTAS<NT>) cs_kv4_rows_kern
   if (!late) cs::grid_dep_wait();
   cs::grid_dep_launch_dependents();
   const Batch& B = p.b;
-  find_range<ROWS_THREADS>(B, p.c, &sm.range, sm.scratch);
+  find_range<ROWS_THREADS, BY_HEAD>(B, p.c, &sm.range, sm.scratch);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, gq = lane >> 2, jq = lane & 3;
   const int key0 = gq & 1 ? 7 - (gq >> 1) : gq >> 1;  // this lane's key of K, the other is 8 behind
   const int key1 = jq, key2 = 7 - jq;                 // its keys of V, two more are 8 behind
@@ -87,7 +87,7 @@ __global__ void __launch_bounds__(ROWS_THREADS, ROWS4_CTAS<NT>) cs_kv4_rows_kern
   const int run = lane >> 4, piece = lane & (PIECES - 1), first_key = (lane & 15) / PIECES;
   const uint32_t slot_bytes = static_cast<uint32_t>(B.slot_stride >> 1);
   const bool has_scales = (lane & 15) < 2 * PIECES, of_v = (lane & 15) >= PIECES;
-  Walk walk(p.c, sm.range);
+  WalkOf<BY_HEAD> walk(p.c, sm.range);
   Seg g;
   while (walk.next(B, p.c, g)) {
     const int first = g.item * p.c.per_item;  // the item's first token

@@ -311,7 +311,7 @@ inline cs_status map_caches(cskv::AttnP& k, const CUtensorMap& like) {
 // The kernels of a call with at most `max_rows` rows per key head, and the maps of their caches' copies.
 struct Kernels {
   const void *rows, *attn, *join;
-  int rows_shift;  // keys of a tile of the kernel for few rows
+  int rows_shift, head_ctas;  // few rows: keys of a tile; CTAs of a key head where items go by heads, or 0
   int rows_grid, rows_smem, attn_smem, attn_threads;
   const CUtensorMap *rows_map, *attn_map;  // nullptr: read through pointers
 };
@@ -324,6 +324,7 @@ inline cs_status run_attention(cs_kv_s* p, cskv::AttnP& k, const Kernels& use, i
   if (max_rows <= cskv::ROWS) {
     k.c.per_item = cskv::ROWS / k.b.group;
     k.c.shift = use.rows_shift;
+    k.c.head_ctas = use.head_ctas;
     if (use.rows_map && (s = map_caches(k, *use.rows_map)) != CS_OK) return s;
     s = launch(use.rows, dim3(use.rows_grid), cskv::ROWS_THREADS, use.rows_smem, &k, st);
     if (s != CS_OK || max_rows <= k.b.group || k.c.flat) return s;

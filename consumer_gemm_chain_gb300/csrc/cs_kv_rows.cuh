@@ -159,7 +159,7 @@ __device__ __forceinline__ void rows_join(const AttnP& p, const Seg& g, int firs
   if (late) cs::grid_dep_wait();
   // the last to arrive joins the pieces in their order
   const int pieces = static_cast<int>(c1 - c0) + 1;
-  auto piece = [&](int i, int r) { return state(c0 + i, range.quota * (c0 + i) < g.x, r); };
+  auto piece = [&](int i, int r) { return state(c0 + i, range.quota * (c0 + i - range.cta) < g.x, r); };
   // a warp (64 dimensions: half of one) sums a row over all pieces, or with few rows over a
   // part of them, a lane four dimensions; every lane knows the weights of 32 (16) pieces at a time
   constexpr int LANES = QUADS, UNITS = ROWS_THREADS / LANES, AHEAD = 3;  // a fourth is spilled, in the inner loop too

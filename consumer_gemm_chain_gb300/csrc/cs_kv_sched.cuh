@@ -6,7 +6,11 @@
 // many, prompts and single tokens all load the SMs alike, without a launch per kind.
 // Items cut by a range's border leave their state (O, max, sum) in the workspace, and
 // the pieces are joined in their order.  Where that would cost more than it evens out,
-// items stay whole (Cut::whole; run_attention in cs_kv.cu has the rule).
+// items stay whole (Cut::whole; run_attention in cs_kv_host.cuh has the rule).
+//
+// BY_HEAD: every key head has as many CTAs, and its items alone are their order: then the CTAs of all
+// heads come to the same keys at the same time.  A row of codes is 64 or 32 bytes, and where the rows of the
+// heads lie side by side a line that one head's CTA brings serves the next one's, if it is not much later.
 #pragma once
 #include "cs_kv_append.cuh"
 
@@ -20,6 +24,7 @@ struct Cut {
   int flat;       // every row sees keys 0 .. flat_len - 1 of one common table (a shared prefix)
   int flat_len;
   int whole;      // no item is cut: it belongs to the range that holds its middle
+  int head_ctas;  // with BY_HEAD: CTAs of a key head
 };
 
 #define CS_KV_BOTH __host__ __device__ __forceinline__  // the division's arithmetic also runs in a host test
@@ -125,16 +130,18 @@ struct Seg {
 struct Range {
   unsigned long long x0, x1, rem, quota;
   int b, kvh, item, off;
-  Seq s;  // sequence b
+  int head, cta;  // the first head and CTA of the order
+  Seq s;          // sequence b
 };
 
 // An item's units are item_cost of overhead and then its tiles; a range that ends
 // in the overhead leaves all tiles to the next CTA.
-struct Walk {
+template <bool BY_HEAD>
+struct WalkOf {
   unsigned long long x, x1;
   int b, kvh, item, off, items;
   Seq s;
-  __device__ __forceinline__ Walk(const Cut& C, const Range& r)
+  __device__ __forceinline__ WalkOf(const Cut& C, const Range& r)
       : x(r.x0), x1(r.x1), b(r.b), kvh(r.kvh), item(r.item), off(r.off), items(items_of(C, r.s)), s(r.s) {
     if (C.whole && off > 0) {
       const int units = item_tiles(C, s, item) + C.item_cost;
@@ -150,8 +157,8 @@ struct Walk {
     while (x < x1) {
       if (item == items) {
         item = 0;
-        if (++kvh == B.kv_heads) {
-          kvh = 0;
+        if (BY_HEAD || ++kvh == B.kv_heads) {
+          if (!BY_HEAD) kvh = 0;
           const int seqs = C.flat ? 1 : B.seqs;
           do {
             if (++b >= seqs) return false;
@@ -183,6 +190,8 @@ struct Walk {
     return false;
   }
 };
+
+using Walk = WalkOf<false>;
 
 // a / b; nearly always both fit 32 bits, where the division is much the shorter
 __device__ __forceinline__ unsigned long long divide(unsigned long long a, unsigned long long b) {
@@ -220,37 +229,45 @@ __device__ __forceinline__ unsigned long long warp_inclusive(unsigned long long 
 }
 
 // This CTA's share of `total` units.
-__device__ __forceinline__ void share(unsigned long long total, Range& r) {
-  r.quota = divide(total + gridDim.x - 1, gridDim.x);
-  r.x0 = kv_min(r.quota * blockIdx.x, total);
+template <bool BY_HEAD>
+__device__ __forceinline__ void share(const Batch& B, const Cut& C, unsigned long long total, Range& r) {
+  const unsigned ctas = BY_HEAD ? C.head_ctas : gridDim.x;
+  r.head = BY_HEAD ? blockIdx.x / ctas : 0;
+  r.cta = r.head * ctas;
+  if (BY_HEAD && r.head >= B.kv_heads) total = 0;  // one CTA too many
+  r.quota = divide(total + ctas - 1, ctas);
+  r.x0 = kv_min(r.quota * (blockIdx.x - r.cta), total);
   r.x1 = kv_min(r.x0 + r.quota, total);
   r.rem = 0;
-  r.b = r.kvh = r.item = r.off = 0;
+  r.b = r.item = r.off = 0;
+  r.kvh = r.head;
   r.s = Seq{0, 0, 0};
 }
 
 // Every thread of the block: this CTA's range into *out (shared memory).
-template <int THREADS>
+template <int THREADS, bool BY_HEAD = false>
 __device__ __forceinline__ void find_range(const Batch& B, const Cut& C, Range* out, unsigned long long* scratch) {
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int seqs = C.flat ? 1 : B.seqs;
+  const int heads = BY_HEAD ? 1 : B.kv_heads;  // of the order
   if (seqs <= 32) {  // one sequence per lane of one warp: no barrier but the last
     if (warp == 0) {
       Seq s{0, 0, 0};
       const bool ok = lane < seqs && load_seq(B, C, lane, s);
-      const unsigned long long c = ok ? units_before(C, s, items_of(C, s)) * B.kv_heads : 0;
+      const unsigned long long c = ok ? units_before(C, s, items_of(C, s)) * heads : 0;
       const unsigned long long incl = warp_inclusive(c);
       Range r;
-      share(__shfl_sync(0xFFFFFFFFu, incl, 31), r);
+      share<BY_HEAD>(B, C, __shfl_sync(0xFFFFFFFFu, incl, 31), r);
       if (r.x0 < r.x1) {
         r.b = __ffs(__ballot_sync(0xFFFFFFFFu, r.x0 < incl)) - 1;
         const unsigned long long in = r.x0 - __shfl_sync(0xFFFFFFFFu, incl - c, r.b);
-        const unsigned long long per_head = divide(__shfl_sync(0xFFFFFFFFu, c, r.b), B.kv_heads);
+        const unsigned long long per_head = divide(__shfl_sync(0xFFFFFFFFu, c, r.b), heads);
         s.t0 = __shfl_sync(0xFFFFFFFFu, s.t0, r.b);
         s.n = __shfl_sync(0xFFFFFFFFu, s.n, r.b);
         s.m = __shfl_sync(0xFFFFFFFFu, s.m, r.b);
-        r.kvh = static_cast<int>(divide(in, per_head));
-        r.rem = in - r.kvh * per_head;
+        const int h = static_cast<int>(divide(in, per_head));
+        r.kvh = r.head + h;
+        r.rem = in - h * per_head;
         r.s = s;
         find_item(C, s, r);
       }
@@ -273,11 +290,12 @@ __device__ __forceinline__ void find_range(const Batch& B, const Cut& C, Range* 
     for (int b = b0; b < b1; ++b) {
       if (!load_seq(B, C, b, s)) continue;
       const unsigned long long c = units_before(C, s, items_of(C, s));
-      const unsigned long long in = x0 - at - mine * B.kv_heads;
-      if (pass == 1 && in < c * B.kv_heads) {
+      const unsigned long long in = x0 - at - mine * heads;
+      if (pass == 1 && in < c * heads) {
         out->b = b;
-        out->kvh = static_cast<int>(divide(in, c));
-        out->rem = in - out->kvh * c;
+        const int h = static_cast<int>(divide(in, c));
+        out->kvh += h;
+        out->rem = in - h * c;
         break;
       }
       mine += c;
@@ -292,13 +310,13 @@ __device__ __forceinline__ void find_range(const Batch& B, const Cut& C, Range* 
       if (w < warp) before += scratch[w];
       total += scratch[w];
     }
-    incl = (incl + before) * B.kv_heads;
+    incl = (incl + before) * heads;
     Range r;
-    share(total * B.kv_heads, r);
+    share<BY_HEAD>(B, C, total * heads, r);
     if (tid == 0) *out = r;
     __syncthreads();
     x0 = r.x0;
-    at = incl - mine * B.kv_heads;
+    at = incl - mine * heads;
     if (r.x0 >= r.x1 || x0 < at || x0 >= incl) b1 = b0;
   }
   __syncthreads();
