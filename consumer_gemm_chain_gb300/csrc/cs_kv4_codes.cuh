@@ -100,4 +100,36 @@ struct Four<__nv_bfloat16> {
   }
 };
 
+// Operands of products in f16, whatever the cache's type is: values times 2^-7, numbers of f16 for all scales (from
+// 2^-24 on).  Code bits under the exponent of 1024 are 1024 + (c + 8), those of the next four 64 + (c + 8) under the
+// exponent of 64, and one multiply-add makes either a value: 1032 s and 72 s have at most 11 significant
+// bits.  Only where 1032 s overflows (BIG: bytes from 0xE0 on, values of some 55000) c is made first.
+struct FourScaled {
+  static constexpr uint32_t BIG_BYTE = 0xE0;
+  __half2 s, low, high;
+  __device__ __forceinline__ explicit FourScaled(uint32_t bits) {
+    const uint32_t unit = 0x20002000u, lo = 0xE408E408u, hi = 0xD480D480u;  // 2^-7, -1032, -72
+    s = __hmul2(*reinterpret_cast<__half2*>(&bits), *reinterpret_cast<const __half2*>(&unit));
+    low = __hmul2(s, *reinterpret_cast<const __half2*>(&lo));
+    high = __hmul2(s, *reinterpret_cast<const __half2*>(&hi));
+  }
+  template <bool BIG>
+  __device__ __forceinline__ uint32_t one(uint32_t w, uint32_t mask, uint32_t magic, uint32_t minus, __half2 off) const {
+    const uint32_t x = masked(w, mask, magic);
+    const __half2 h = *reinterpret_cast<const __half2*>(&x);
+    const __half2 y = BIG ? __hmul2(__hadd2(h, *reinterpret_cast<const __half2*>(&minus)), s) : __hfma2(h, s, off);
+    return *reinterpret_cast<const uint32_t*>(&y);
+  }
+  // the four pairs of a word
+  template <bool BIG>
+  __device__ __forceinline__ void pairs(uint32_t w, uint32_t (&x)[4]) const {
+    const uint32_t v = w >> 8;
+    x[0] = one<BIG>(w, 0x000F000Fu, 0x64006400u, 0xE408E408u, low);
+    x[1] = one<BIG>(w, 0x00F000F0u, 0x54005400u, 0xD480D480u, high);
+    x[2] = one<BIG>(v, 0x000F000Fu, 0x64006400u, 0xE408E408u, low);
+    x[3] = one<BIG>(v, 0x00F000F0u, 0x54005400u, 0xD480D480u, high);
+  }
+};
+constexpr float FOUR_UNIT = 0.0078125f;
+
 }  // namespace cskv

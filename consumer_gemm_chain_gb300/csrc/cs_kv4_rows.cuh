@@ -138,15 +138,39 @@ __global__ void __launch_bounds__(ROWS_THREADS, ROWS4_CTAS<NT>) cs_kv4_rows_kern
 #pragma unroll
     for (int i = 0; i < ST - 1; ++i) load(g.k0 + i, checked(ahead[i]), ring[i]);
     int next = ahead[ST - 1];
-    // the queries, in the order of a key's words
-    uint4 q[NT][KW];
+    // the queries, in the order of a key's words, in f16: rows of bf16 times a power of two that puts their largest
+    // value to 2^14 .. 2^15 (what is lost below 2^-25 is 2^-39 of it); `unit` undoes both operands' factors
+    uint32_t q[NT][KW][4];
+    float unit[NT][2];
 #pragma unroll
     for (int n = 0; n < NT; ++n) {
       const int r = 8 * n + gq, t = r / B.group;
       const uint4* from = reinterpret_cast<const uint4*>(static_cast<const T*>(p.q_raw) + (g.s.t0 + first + t) * p.q_stride +
                                                          (g.kvh * B.group + r - t * B.group) * D) + jq * KW;
 #pragma unroll
-      for (int w = 0; w < KW; ++w) q[n][w] = r < rows ? from[w] : make_uint4(0, 0, 0, 0);
+      for (int w = 0; w < KW; ++w) *reinterpret_cast<uint4*>(q[n][w]) = r < rows ? from[w] : make_uint4(0, 0, 0, 0);
+      float f = 1.0f;
+      if constexpr (!std::is_same<T, __half>::value) {
+        uint32_t top = 0;
+#pragma unroll
+        for (int i = 0; i < 4 * KW; ++i) {
+          const uint32_t lo = q[n][i / 4][i % 4] << 16 & 0x7F800000u, hi = q[n][i / 4][i % 4] & 0x7F800000u;  // exponents
+          top = max(top, max(lo == 0x7F800000u ? 0u : lo, hi == 0x7F800000u ? 0u : hi));
+        }
+        top = max(top, __shfl_xor_sync(0xFFFFFFFFu, top, 1));
+        top = max(top, __shfl_xor_sync(0xFFFFFFFFu, top, 2));
+        const int shift = min(max(14 - (static_cast<int>(top >> 23) - 127), -112), 126);
+        const float by = __uint_as_float(static_cast<uint32_t>(127 + shift) << 23);
+        f = __uint_as_float(static_cast<uint32_t>(127 - shift) << 23);
+#pragma unroll
+        for (int i = 0; i < 4 * KW; ++i) {
+          const float2 v = Pair<T>::get(q[n][i / 4][i % 4]);
+          q[n][i / 4][i % 4] = Pair<__half>::put(v.x * by, v.y * by);
+        }
+      }
+#pragma unroll
+      for (int e = 0; e < 2; ++e)
+        unit[n][e] = __shfl_sync(0xFFFFFFFFu, f, 4 * (2 * jq + e)) * (p.scale_log2 / FOUR_UNIT);
     }
     // keys below all_end and from all_lo on are seen by every row
     const int all_end = p.c.flat ? g.s.m : base + 1, all_lo = p.c.window > 0 ? max(0, base + tokens - p.c.window) : 0;
@@ -163,13 +187,11 @@ __global__ void __launch_bounds__(ROWS_THREADS, ROWS4_CTAS<NT>) cs_kv4_rows_kern
       for (int i = 0; i < 4 * VW; ++i)
 #pragma unroll
         for (int c = 0; c < 4; ++c) o[n][i][c] = 0.0f;
-    // of a row: the reference times the scale's factor, the score from which it is raised (by 2^8), the sum
-    float m_ref[NT][2], limit[NT][2], l[NT][2];
-    const float room = RAISE_LOG2 / p.scale_log2;
+    float m_ref[NT][2], l[NT][2];  // of a row: the reference (of scores times unit) and the sum
 #pragma unroll
     for (int n = 0; n < NT; ++n)
 #pragma unroll
-      for (int e = 0; e < 2; ++e) m_ref[n][e] = limit[n][e] = -INFINITY, l[n][e] = 0.0f;
+      for (int e = 0; e < 2; ++e) m_ref[n][e] = -INFINITY, l[n][e] = 0.0f;
     int at = 0;  // the stage of tile k
 #pragma unroll 1
     for (int k = g.k0; k < g.k1; ++k) {
@@ -184,6 +206,31 @@ __global__ void __launch_bounds__(ROWS_THREADS, ROWS4_CTAS<NT>) cs_kv4_rows_kern
       const bool mask = !(tile0 + 80 <= all_end && (tile0 >= all_lo || tile0 + 80 <= p.c.sinks));
 #pragma unroll 1
       for (int x0 = 0; x0 < 2; x0 += XS) {
+        // the scales of this lane's keys, two of K and two pairs of V, and whether one of the warp's is big
+        uint32_t sk[XS], sv[XS][2];
+        bool big = false;
+#pragma unroll
+        for (int x = 0; x < XS; ++x) {
+          const uint8_t* of_k = st.scales[0][(x0 + x) * 16 + key0] + (D == 128 ? jq : jq >> 1);
+          const uint32_t k0 = of_k[0], k1 = of_k[8 * PIECES];
+          uint32_t v[4];
+#pragma unroll
+          for (int y = 0; y < 4; ++y)
+            v[y] = st.scales[1][(x0 + x) * 16 + (y & 1 ? key2 : key1) + 8 * (y >> 1)][D == 128 ? gq >> 1 : gq >> 2];
+          if (__builtin_expect(mask, 0)) {  // a scale of a key that no row sees may be anything
+#pragma unroll
+            for (int y = 0; y < 4; ++y) {
+              const int key = tile0 + (x0 + x) * 64 + (y & 1 ? key2 : key1) + 8 * (y >> 1);
+              if (!(key < g.hi && (key >= g.lo || key < p.c.sinks))) v[y] = 0;
+            }
+          }
+          big |= max(max(k0, k1), max(max(v[0], v[1]), max(v[2], v[3]))) >= FourScaled::BIG_BYTE;
+          sk[x] = k0 | k1 << 16;
+          sv[x][0] = scale_pair(v[0], v[1]);
+          sv[x][1] = scale_pair(v[2], v[3]);
+        }
+        auto keys = [&](auto is_big) {
+        constexpr bool BIG = decltype(is_big)::value;
         float s[XS][NT][4] = {};
 #pragma unroll
         for (int x = 0; x < XS; ++x) {
@@ -197,17 +244,16 @@ __global__ void __launch_bounds__(ROWS_THREADS, ROWS4_CTAS<NT>) cs_kv4_rows_kern
             *reinterpret_cast<uint2*>(ka) = *reinterpret_cast<const uint2*>(row);
             *reinterpret_cast<uint2*>(kb) = *reinterpret_cast<const uint2*>(row + 8 * (D / 2));
           }
-          const uint8_t* scale = st.scales[0][j] + (D == 128 ? jq : jq >> 1);
-          const Four<T> fa(scale_pair(scale[0])), fb(scale_pair(scale[8 * PIECES]));
+          const FourScaled fa(scale_pair(sk[x] & 0xFFu)), fb(scale_pair(sk[x] >> 16));
 #pragma unroll
           for (int w = 0; w < KW; ++w) {
             uint32_t a[4], b[4];
-            fa.pairs(ka[w], a);
-            fb.pairs(kb[w], b);
+            fa.pairs<BIG>(ka[w], a);
+            fb.pairs<BIG>(kb[w], b);
 #pragma unroll
             for (int n = 0; n < NT; ++n) {
-              mma16816<T>(s[x][n], a[0], b[0], a[1], b[1], q[n][w].x, q[n][w].y);
-              mma16816<T>(s[x][n], a[2], b[2], a[3], b[3], q[n][w].z, q[n][w].w);
+              mma16816<__half>(s[x][n], a[0], b[0], a[1], b[1], q[n][w][0], q[n][w][1]);
+              mma16816<__half>(s[x][n], a[2], b[2], a[3], b[3], q[n][w][2], q[n][w][3]);
             }
           }
         }
@@ -228,7 +274,8 @@ __global__ void __launch_bounds__(ROWS_THREADS, ROWS4_CTAS<NT>) cs_kv4_rows_kern
           for (int e = 0; e < 2; ++e) {
             top[n][e] = fmaxf(s[0][n][e], s[0][n][2 + e]);
             if (XS == 2) top[n][e] = max3(top[n][e], s[XS - 1][n][e], s[XS - 1][n][2 + e]);
-            raise |= top[n][e] > limit[n][e];
+            // raised only when it is exceeded by more than 2^8 (from -infinity by anything but that)
+            raise |= fmaf(top[n][e], unit[n][e], -m_ref[n][e]) > RAISE_LOG2;
           }
         if (__any_sync(0xFFFFFFFFu, raise)) {
 #pragma unroll
@@ -238,9 +285,8 @@ __global__ void __launch_bounds__(ROWS_THREADS, ROWS4_CTAS<NT>) cs_kv4_rows_kern
               float m = top[n][e];
 #pragma unroll
               for (int d = 4; d < 32; d <<= 1) m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, d));
-              if (m > limit[n][e]) {
-                limit[n][e] = m + room;
-                m *= p.scale_log2;
+              if (fmaf(m, unit[n][e], -m_ref[n][e]) > RAISE_LOG2) {
+                m *= unit[n][e];
                 const float f = cs::ex2_approx(m_ref[n][e] - m);
                 m_ref[n][e] = m;
                 l[n][e] *= f;
@@ -257,21 +303,21 @@ __global__ void __launch_bounds__(ROWS_THREADS, ROWS4_CTAS<NT>) cs_kv4_rows_kern
             const float sub = m_ref[n][e] == -INFINITY ? 0.0f : -m_ref[n][e];
 #pragma unroll
             for (int x = 0; x < XS; ++x) {
-              s[x][n][e] = cs::ex2_approx(fmaf(s[x][n][e], p.scale_log2, sub));
-              s[x][n][2 + e] = cs::ex2_approx(fmaf(s[x][n][2 + e], p.scale_log2, sub));
+              s[x][n][e] = cs::ex2_approx(fmaf(s[x][n][e], unit[n][e], sub));
+              s[x][n][2 + e] = cs::ex2_approx(fmaf(s[x][n][2 + e], unit[n][e], sub));
               l[n][e] += s[x][n][e] + s[x][n][2 + e];
             }
           }
 #pragma unroll
           for (int x = 0; x < XS; ++x) {
-            pt[x][n][0] = transposed(Pair<T>::put(s[x][n][0], s[x][n][1]));
-            pt[x][n][1] = transposed(Pair<T>::put(s[x][n][2], s[x][n][3]));
+            pt[x][n][0] = transposed(Pair<__half>::put(s[x][n][0], s[x][n][1]));
+            pt[x][n][1] = transposed(Pair<__half>::put(s[x][n][2], s[x][n][3]));
           }
         }
 #pragma unroll
         for (int x = 0; x < XS; ++x) {
           // V: words of keys key1, key2, key1 + 8 and key2 + 8 of the run
-          uint32_t v[4][VW], sv[4];
+          uint32_t v[4][VW];
 #pragma unroll
           for (int y = 0; y < 4; ++y) {
             const int of = y & 1 ? key2 : key1, j = (x0 + x) * 16 + of + 8 * (y >> 1);
@@ -280,29 +326,26 @@ __global__ void __launch_bounds__(ROWS_THREADS, ROWS4_CTAS<NT>) cs_kv4_rows_kern
               *reinterpret_cast<uint2*>(v[y]) = *reinterpret_cast<const uint2*>(row);
             else
               v[y][0] = *reinterpret_cast<const uint32_t*>(row);
-            sv[y] = st.scales[1][j][D == 128 ? gq >> 1 : gq >> 2];
           }
-          if (__builtin_expect(mask, 0)) {  // a scale of a key that no row sees may be anything
-#pragma unroll
-            for (int y = 0; y < 4; ++y) {
-              const int key = tile0 + (x0 + x) * 64 + (y & 1 ? key2 : key1) + 8 * (y >> 1);
-              if (!(key < g.hi && (key >= g.lo || key < p.c.sinks))) sv[y] = 0;
-            }
-          }
-          const Four<T> fa(scale_pair(sv[0], sv[1])), fb(scale_pair(sv[2], sv[3]));
+          const FourScaled fa(sv[x][0]), fb(sv[x][1]);
 #pragma unroll
           for (int w = 0; w < VW; ++w) {
             uint32_t a0[4], a1[4], a2[4], a3[4];  // even and odd dimensions of keys key1, key2; of those 8 behind
-            fa.pairs(__byte_perm(v[0][w], v[1][w], 0x5410), a0);
-            fa.pairs(__byte_perm(v[0][w], v[1][w], 0x7632), a1);
-            fb.pairs(__byte_perm(v[2][w], v[3][w], 0x5410), a2);
-            fb.pairs(__byte_perm(v[2][w], v[3][w], 0x7632), a3);
+            fa.pairs<BIG>(__byte_perm(v[0][w], v[1][w], 0x5410), a0);
+            fa.pairs<BIG>(__byte_perm(v[0][w], v[1][w], 0x7632), a1);
+            fb.pairs<BIG>(__byte_perm(v[2][w], v[3][w], 0x5410), a2);
+            fb.pairs<BIG>(__byte_perm(v[2][w], v[3][w], 0x7632), a3);
 #pragma unroll
             for (int i = 0; i < 4; ++i)
 #pragma unroll
-              for (int n = 0; n < NT; ++n) mma16816<T>(o[n][4 * w + i], a0[i], a1[i], a2[i], a3[i], pt[x][n][0], pt[x][n][1]);
+              for (int n = 0; n < NT; ++n) mma16816<__half>(o[n][4 * w + i], a0[i], a1[i], a2[i], a3[i], pt[x][n][0], pt[x][n][1]);
           }
         }
+        };
+        if (__builtin_expect(__any_sync(0xFFFFFFFFu, big), 0))
+          keys(std::true_type());
+        else
+          keys(std::false_type());
       }
     }
     copies_wait<0>();
@@ -321,7 +364,8 @@ __global__ void __launch_bounds__(ROWS_THREADS, ROWS4_CTAS<NT>) cs_kv4_rows_kern
           float4* to = reinterpret_cast<float4*>(&sm.o[warp][r][8 * VW * gq]);
 #pragma unroll
           for (int i = 0; i < 4 * VW; i += 2)
-            to[i / 2] = make_float4(o[n][i][e], o[n][i][2 + e], o[n][i + 1][e], o[n][i + 1][2 + e]);
+            to[i / 2] = make_float4(o[n][i][e] / FOUR_UNIT, o[n][i][2 + e] / FOUR_UNIT, o[n][i + 1][e] / FOUR_UNIT,
+                                    o[n][i + 1][2 + e] / FOUR_UNIT);
         }
       }
     __syncthreads();
