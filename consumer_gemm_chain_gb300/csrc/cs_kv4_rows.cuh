@@ -38,7 +38,7 @@ struct alignas(16) Rows4Shared {
   union {
     Stage4<D> ring[ROWS_WARPS][STAGES];
     float o[ROWS_WARPS][ROWS][D + 4];  // each warp's output
-    float sum[ROWS][D + 4];            // of a part of an item's pieces: output, maximum, sum
+    float piece[6][ROWS][D + 4];       // pieces of an item on their way: outputs, maxima, sums
   };
   Range range;
   unsigned long long scratch[ROWS_THREADS / 32];
@@ -60,6 +60,62 @@ __device__ __forceinline__ uint32_t transposed(uint32_t x) {
   uint32_t y;
   asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
   return y;
+}
+
+// Joins the pieces of an item in their order, two at a time while four more are on their way to shared memory.
+// (With loads into registers, few at a time because the loop over the keys spills what more of them would need,
+// 63 pieces of 8 rows took over 20 us.)  A thread has some quads of dimensions, with the maximum and sum of their rows.
+template <typename T, int D, int NT>
+__device__ __forceinline__ void join4(const AttnP& p, const Seg& g, int first, int rows, const Pieces& of, Rows4Shared<D>& sm) {
+  constexpr int QUADS = D / 4, MINE = NT * 8 * QUADS / ROWS_THREADS, CHUNKS = QUADS + 1;
+  const int tid = threadIdx.x;
+  auto load = [&](int i) {  // pieces i and i + 1
+#pragma unroll
+    for (int j = 0; j < 2; ++j)
+      if (i + j < of.count) {
+        const unsigned cta = of.first + i + j;
+        const float* from = rows_state<D>(p, cta, sm.range.quota * (cta - sm.range.cta) < g.x, 0);
+        float* to = sm.piece[(i + j) % 6][0];
+        for (int x = tid; x < rows * CHUNKS; x += ROWS_THREADS) copy16(to + 4 * x, from + 4 * x, true);
+      }
+    copies_commit();
+  };
+  float4 x[MINE];
+  float m[MINE], l[MINE];
+#pragma unroll
+  for (int n = 0; n < MINE; ++n) x[n] = make_float4(0.0f, 0.0f, 0.0f, 0.0f), m[n] = -INFINITY, l[n] = 0.0f;
+  load(0);
+  load(2);
+  for (int i = 0; i < of.count; i += 2) {
+    load(i + 4);
+    copies_wait<2>();
+    __syncthreads();
+#pragma unroll
+    for (int j = 0; j < 2; ++j)
+      if (i + j < of.count) {
+#pragma unroll
+        for (int n = 0; n < MINE; ++n) {
+          const int at = tid + n * ROWS_THREADS, r = at / QUADS, c = at % QUADS;
+          if (r >= rows) continue;
+          const float* state = sm.piece[(i + j) % 6][r];
+          const float2 ml = *reinterpret_cast<const float2*>(state + D);
+          const float top = fmaxf(m[n], ml.x);
+          const float old = m[n] == -INFINITY ? 0.0f : cs::ex2_approx(m[n] - top);
+          const float weight = ml.x == -INFINITY ? 0.0f : cs::ex2_approx(ml.x - top);
+          m[n] = top;
+          l[n] = fmaf(ml.y, weight, l[n] * old);
+          x[n].x *= old, x[n].y *= old, x[n].z *= old, x[n].w *= old;
+          add_weighted(x[n], reinterpret_cast<const float4*>(state)[c], weight);
+        }
+      }
+    __syncthreads();  // before the next copies over them
+  }
+  copies_wait<0>();
+#pragma unroll
+  for (int n = 0; n < MINE; ++n) {
+    const int at = tid + n * ROWS_THREADS, r = at / QUADS;
+    if (r < rows) rows_finish<T, D>(p, g, first, r, at % QUADS, x[n], m[n], l[n]);
+  }
 }
 
 // NT: groups of 8 rows
@@ -369,7 +425,8 @@ __global__ void __launch_bounds__(ROWS_THREADS, ROWS4_CTAS<NT>) cs_kv4_rows_kern
         }
       }
     __syncthreads();
-    rows_join<T, D>(p, g, first, rows, late, sm.o, sm.sum, sm.ml, sm.range, sm.last);
+    const Pieces of = rows_store<T, D>(p, g, first, rows, late, sm.o, sm.ml, sm.range, sm.last);
+    if (of.count > 0) join4<T, D, NT>(p, g, first, rows, of, sm);
   }
   if (late) cs::grid_dep_wait();
 }

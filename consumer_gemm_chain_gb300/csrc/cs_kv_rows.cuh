@@ -79,45 +79,57 @@ CS_KV_BOTH uint32_t rows_issued(int which, int stage, bool at_values, uint32_t d
   return (n - stage + ST - 1) / ST;
 }
 
-// All threads of a CTA, behind a barrier: the state of a segment from those of its warps (o: outputs, ml:
-// maxima and sums), and where an item has several pieces, the last CTA to store one joins them.
-// `sum_of` may share o's memory.  tid runs over ROWS_THREADS.
+__device__ __forceinline__ void add_weighted(float4& x, const float4& y, float f) {
+  x.x = fmaf(y.x, f, x.x), x.y = fmaf(y.y, f, x.y), x.z = fmaf(y.z, f, x.z), x.w = fmaf(y.w, f, x.w);
+}
+
+// The state of row r in a piece: D values of the output, the maximum and the sum.
+template <int D>
+__device__ __forceinline__ float* rows_state(const AttnP& p, unsigned cta, int which, int r) {
+  return p.part + ((static_cast<size_t>(cta) * 2 + which) * ROWS + r) * (D + 4);
+}
+
+// Dimensions 4 c .. 4 c + 3 of row r of an item from their state.
 template <typename T, int D>
-__device__ __forceinline__ void rows_join(const AttnP& p, const Seg& g, int first, int rows, bool late,
-                                          float (*o)[ROWS][D + 4], float (*sum_of)[D + 4], float2 (*ml_of)[ROWS],
-                                          const Range& range, int& last) {
+__device__ __forceinline__ void rows_finish(const AttnP& p, const Seg& g, int first, int r, int c, float4 x, float m, float l) {
   const Batch& B = p.b;
-  const int tid = threadIdx.x, lane = tid & 31;
-  auto state = [&](unsigned cta, int which, int r) { return p.part + ((static_cast<size_t>(cta) * 2 + which) * ROWS + r) * (D + 4); };
-  // dimensions 4 c .. 4 c + 3 of row r from their state
-  auto finish = [&](int r, int c, float4 x, float m, float l) {
-    const int t = r / B.group;
-    const long long row = static_cast<long long>(g.s.t0 + first + t) * B.heads + g.kvh * B.group + r - t * B.group;
-    float4* const pre = p.flat_o ? reinterpret_cast<float4*>(p.flat_o + row * D) + c : nullptr;
-    if (!p.c.flat && pre) {  // join the prefix's output
-      const float z = p.flat_lse[row], top = fmaxf(m, z);
-      const float own = m == -INFINITY ? 0.0f : cs::ex2_approx(m - top), fold = z == -INFINITY ? 0.0f : cs::ex2_approx(z - top);
-      const float4 y = *pre;
-      x = make_float4(x.x * own + y.x * fold, x.y * own + y.y * fold, x.z * own + y.z * fold, x.w * own + y.w * fold);
-      l = l * own + fold;
-      m = top;
-    }
-    const float inv = l == 0.0f ? 0.0f : 1.0f / l;
-    const float4 y = l == 0.0f ? make_float4(0.0f, 0.0f, 0.0f, 0.0f) : make_float4(x.x * inv, x.y * inv, x.z * inv, x.w * inv);
-    const float probe = fmaf(x.x, 0.0f, fmaf(x.y, 0.0f, fmaf(x.z, 0.0f, x.w * 0.0f)));  // NaN if one is not finite
-    if (probe != 0.0f && isfinite(l) && g.s.n > 1) mark(p, row);  // several tokens: keys hidden from one only
-    if (c == 0) put_lse(p, row, m, l);
-    if (p.c.flat) {
-      *pre = y;
-    } else {
-      uint2* out = reinterpret_cast<uint2*>(static_cast<T*>(p.out) + (g.s.t0 + first + t) * p.out_stride +
-                                            (g.kvh * B.group + r - t * B.group) * D) + c;
-      *out = make_uint2(Pair<T>::put(y.x, y.y), Pair<T>::put(y.z, y.w));
-    }
-  };
-  auto add = [](float4& x, const float4& y, float f) {
-    x.x = fmaf(y.x, f, x.x), x.y = fmaf(y.y, f, x.y), x.z = fmaf(y.z, f, x.z), x.w = fmaf(y.w, f, x.w);
-  };
+  const int t = r / B.group;
+  const long long row = static_cast<long long>(g.s.t0 + first + t) * B.heads + g.kvh * B.group + r - t * B.group;
+  float4* const pre = p.flat_o ? reinterpret_cast<float4*>(p.flat_o + row * D) + c : nullptr;
+  if (!p.c.flat && pre) {  // join the prefix's output
+    const float z = p.flat_lse[row], top = fmaxf(m, z);
+    const float own = m == -INFINITY ? 0.0f : cs::ex2_approx(m - top), fold = z == -INFINITY ? 0.0f : cs::ex2_approx(z - top);
+    const float4 y = *pre;
+    x = make_float4(x.x * own + y.x * fold, x.y * own + y.y * fold, x.z * own + y.z * fold, x.w * own + y.w * fold);
+    l = l * own + fold;
+    m = top;
+  }
+  const float inv = l == 0.0f ? 0.0f : 1.0f / l;
+  const float4 y = l == 0.0f ? make_float4(0.0f, 0.0f, 0.0f, 0.0f) : make_float4(x.x * inv, x.y * inv, x.z * inv, x.w * inv);
+  const float probe = fmaf(x.x, 0.0f, fmaf(x.y, 0.0f, fmaf(x.z, 0.0f, x.w * 0.0f)));  // NaN if one is not finite
+  if (probe != 0.0f && isfinite(l) && g.s.n > 1) mark(p, row);  // several tokens: keys hidden from one only
+  if (c == 0) put_lse(p, row, m, l);
+  if (p.c.flat) {
+    *pre = y;
+  } else {
+    uint2* out = reinterpret_cast<uint2*>(static_cast<T*>(p.out) + (g.s.t0 + first + t) * p.out_stride +
+                                          (g.kvh * B.group + r - t * B.group) * D) + c;
+    *out = make_uint2(Pair<T>::put(y.x, y.y), Pair<T>::put(y.z, y.w));
+  }
+}
+
+// The pieces of an item that this CTA has to join, being the last to store one: CTAs from `first` on.
+struct Pieces {
+  unsigned first;
+  int count;  // 0: none
+};
+
+// All threads of a CTA, behind a barrier: the state of a segment from those of its warps (o: outputs, ml:
+// maxima and sums), and the output where that is a whole item.  tid runs over ROWS_THREADS.
+template <typename T, int D>
+__device__ __forceinline__ Pieces rows_store(const AttnP& p, const Seg& g, int first, int rows, bool late, float (*o)[ROWS][D + 4],
+                                             float2 (*ml_of)[ROWS], const Range& range, int& last) {
+  const int tid = threadIdx.x;
   constexpr int QUADS = D / 4;
   const bool whole = g.whole();
   if (late && whole) cs::grid_dep_wait();
@@ -132,17 +144,17 @@ __device__ __forceinline__ void rows_join(const AttnP& p, const Seg& g, int firs
       const float2 ml = ml_of[w][r];
       const float f = ml.x == -INFINITY ? 0.0f : cs::ex2_approx(ml.x - m);
       sum = fmaf(ml.y, f, sum);
-      add(x, *reinterpret_cast<const float4*>(&o[w][r][4 * c]), f);
+      add_weighted(x, *reinterpret_cast<const float4*>(&o[w][r][4 * c]), f);
     }
     if (whole) {
-      finish(r, c, x, m, sum);
+      rows_finish<T, D>(p, g, first, r, c, x, m, sum);
     } else {
-      float* to = state(blockIdx.x, range.x0 < g.x, r);
+      float* to = rows_state<D>(p, blockIdx.x, range.x0 < g.x, r);
       reinterpret_cast<float4*>(to)[c] = x;
       if (c == 0) *reinterpret_cast<float2*>(to + D) = make_float2(m, sum);
     }
   }
-  if (whole) return;
+  if (whole) return {0, 0};
   const unsigned me = blockIdx.x, quota = static_cast<unsigned>(min(range.quota, 0x80000000ull));
   const unsigned long long end_x = g.x + g.tiles - 1;
   const unsigned c0 = range.x0 > g.x ? me - (static_cast<unsigned>(range.x0 - g.x) + quota - 1) / quota : me;
@@ -155,11 +167,19 @@ __device__ __forceinline__ void rows_join(const AttnP& p, const Seg& g, int firs
     if (old == c1 - c0) *ctr = 0u;  // for the next call
   }
   __syncthreads();
-  if (!last) return;
+  if (!last) return {0, 0};
   if (late) cs::grid_dep_wait();
-  // the last to arrive joins the pieces in their order
-  const int pieces = static_cast<int>(c1 - c0) + 1;
-  auto piece = [&](int i, int r) { return state(c0 + i, range.quota * (c0 + i - range.cta) < g.x, r); };
+  return {c0, static_cast<int>(c1 - c0) + 1};
+}
+
+// Joins the pieces in their order.
+template <typename T, int D>
+__device__ __forceinline__ void rows_join(const AttnP& p, const Seg& g, int first, int rows, const Pieces& of, float (*sum_of)[D + 4],
+                                          const Range& range) {
+  constexpr int QUADS = D / 4;
+  const int tid = threadIdx.x, lane = tid & 31, pieces = of.count;
+  const unsigned c0 = of.first;
+  auto piece = [&](int i, int r) { return rows_state<D>(p, c0 + i, range.quota * (c0 + i - range.cta) < g.x, r); };
   // a warp (64 dimensions: half of one) sums a row over all pieces, or with few rows over a
   // part of them, a lane four dimensions; every lane knows the weights of 32 (16) pieces at a time
   constexpr int LANES = QUADS, UNITS = ROWS_THREADS / LANES, AHEAD = 3;  // a fourth is spilled, in the inner loop too
@@ -195,10 +215,10 @@ __device__ __forceinline__ void rows_join(const AttnP& p, const Seg& g, int firs
 #pragma unroll
       for (int i = 0; i < AHEAD; ++i) {
         const float f = __shfl_sync(group, weight, i, LANES);
-        if (i < here) add(x, y[i], f);
+        if (i < here) add_weighted(x, y[i], f);
       }
 #pragma unroll 4
-      for (int i = AHEAD; i < here; ++i) add(x, output(i), __shfl_sync(group, weight, i, LANES));
+      for (int i = AHEAD; i < here; ++i) add_weighted(x, output(i), __shfl_sync(group, weight, i, LANES));
     }
     reinterpret_cast<float4*>(sum_of[u])[gl] = x;
     if (gl == 0) *reinterpret_cast<float2*>(&sum_of[u][D]) = make_float2(top, sum);
@@ -211,10 +231,10 @@ __device__ __forceinline__ void rows_join(const AttnP& p, const Seg& g, int firs
     for (int part = 0; part < parts; ++part) top = fmaxf(top, sum_of[part * rows + r][D]);
     for (int part = 0; part < parts; ++part) {
       const float m = sum_of[part * rows + r][D], f = m == -INFINITY ? 0.0f : cs::ex2_approx(m - top);
-      add(y, *reinterpret_cast<const float4*>(&sum_of[part * rows + r][4 * c]), f);
+      add_weighted(y, *reinterpret_cast<const float4*>(&sum_of[part * rows + r][4 * c]), f);
       l = fmaf(sum_of[part * rows + r][D + 1], f, l);
     }
-    finish(r, c, y, top, l);
+    rows_finish<T, D>(p, g, first, r, c, y, top, l);
   }
 }
 
@@ -456,7 +476,8 @@ __global__ void __launch_bounds__(ROWS_THREADS, ROWS_CTAS) cs_kv_rows_kernel(con
       }
     }
     __syncthreads();
-    rows_join<T, D>(p, g, first, rows, late, sm.o, sm.sum, sm.ml, sm.range, sm.last);
+    const Pieces of = rows_store<T, D>(p, g, first, rows, late, sm.o, sm.ml, sm.range, sm.last);
+    if (of.count > 0) rows_join<T, D>(p, g, first, rows, of, sm.sum, sm.range);
   }
   if (late) cs::grid_dep_wait();
 }

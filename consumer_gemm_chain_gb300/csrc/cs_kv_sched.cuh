@@ -25,6 +25,7 @@ struct Cut {
   int flat_len;
   int whole;      // no item is cut: it belongs to the range that holds its middle
   int head_ctas;  // with BY_HEAD: CTAs of a key head
+  int least;      // fewest units of a range
 };
 
 #define CS_KV_BOTH __host__ __device__ __forceinline__  // the division's arithmetic also runs in a host test
@@ -235,7 +236,7 @@ __device__ __forceinline__ void share(const Batch& B, const Cut& C, unsigned lon
   r.head = BY_HEAD ? blockIdx.x / ctas : 0;
   r.cta = r.head * ctas;
   if (BY_HEAD && r.head >= B.kv_heads) total = 0;  // one CTA too many
-  r.quota = divide(total + ctas - 1, ctas);
+  r.quota = kv_max<unsigned long long>(divide(total + ctas - 1, ctas), C.least);
   r.x0 = kv_min(r.quota * (blockIdx.x - r.cta), total);
   r.x1 = kv_min(r.x0 + r.quota, total);
   r.rem = 0;
