@@ -114,6 +114,8 @@ Kernels kernels(const cs_kv_s* p) {
   u.rows_grid = p->num_sms * cskv::ROWS_CTAS;
   u.rows_shift = cskv::ROWS_SHIFT;
   u.head_ctas = 0;
+  u.least = 1;
+  u.spare = 0;
   u.rows_smem = rows_smem(p->d);
   u.rows_map = &p->slots_map;
   u.attn_map = &p->page_map;

@@ -50,6 +50,13 @@ Kernels kernels_of(const cs_kv_s* p, int max_rows) {
   u.rows = narrow ? rows_kernel_of<T, D, 1>(by_head) : rows_kernel_of<T, D, 2>(by_head);
   u.attn = window ? (const void*)cskv::cs_kv_attn_kernel<T, D, true, true> : (const void*)cskv::cs_kv_attn_kernel<T, D, false, true>;
   u.join = (const void*)cskv::cs_kv_join_kernel<T, D, true>;
+  // one token over 16000 keys 34 us with ranges of one tile at least, 29.5 with two, and 8 sequences of it the same
+  u.least = 2;
+  // Whole items save the pieces' stores and joins.  Measured, cut and whole, 32 / 8 heads of 128: 128 sequences of 500 keys
+  // (1.6 tiles more on the longest CTA) 38.3 and 33.4 us, 256 of them (3.2) 60.0 and 61.9, 64 of 2000 keys (2.7)
+  // 53.5 and 50.6, 128 of them (5.4) 86.0 and 90.0; 40 / 8 heads of 64, 1024 keys: 128 sequences (3.2) 41.2 and
+  // 38.5, 256 (6.3) 67.7 and 71.2.
+  u.spare = 3;
   u.rows_shift = cskv::ROWS4_SHIFT;
   u.rows_smem = sizeof(cskv::Rows4Shared<D>);
   u.attn_smem = cskv::AttnShape<D, true>::SMEM;

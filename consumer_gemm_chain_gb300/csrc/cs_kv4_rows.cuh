@@ -38,7 +38,7 @@ struct alignas(16) Rows4Shared {
   union {
     Stage4<D> ring[ROWS_WARPS][STAGES];
     float o[ROWS_WARPS][ROWS][D + 4];  // each warp's output
-    float piece[6][ROWS][D + 4];       // pieces of an item on their way: outputs, maxima, sums
+    float piece[6 * ROWS][D + 4];      // rows of pieces of an item on their way: outputs, maxima, sums
   };
   Range range;
   unsigned long long scratch[ROWS_THREADS / 32];
@@ -62,59 +62,75 @@ __device__ __forceinline__ uint32_t transposed(uint32_t x) {
   return y;
 }
 
-// Joins the pieces of an item in their order, two at a time while four more are on their way to shared memory.
-// (With loads into registers, few at a time because the loop over the keys spills what more of them would need,
-// 63 pieces of 8 rows took over 20 us.)  A thread has some quads of dimensions, with the maximum and sum of their rows.
+// Joins the pieces of an item in their order: outputs go by way of shared memory, four (two) at a time while eight
+// (four) more are on their way, and the lanes of a row know the weights of 32 (16) pieces at a time, so that a
+// piece costs a read and four multiply-adds.  (With loads into registers, few at a time because the loop over the
+// keys spills what more of them would need, and a running maximum, 63 pieces of 8 rows took over 20 us.)
 template <typename T, int D, int NT>
 __device__ __forceinline__ void join4(const AttnP& p, const Seg& g, int first, int rows, const Pieces& of, Rows4Shared<D>& sm) {
-  constexpr int QUADS = D / 4, MINE = NT * 8 * QUADS / ROWS_THREADS, CHUNKS = QUADS + 1;
-  const int tid = threadIdx.x;
-  auto load = [&](int i) {  // pieces i and i + 1
+  constexpr int QUADS = D / 4, MINE = NT * 8 * QUADS / ROWS_THREADS;  // QUADS lanes for a row, MINE rows for a lane
+  constexpr int BATCH = 4 / NT, SLOTS = 3 * BATCH;
+  const int tid = threadIdx.x, lane = tid & 31, gl = lane % QUADS, r0 = tid / QUADS;
+  const unsigned group = QUADS == 32 ? 0xFFFFFFFFu : 0xFFFFu << (lane & 16);
+  auto piece = [&](int i, int r) {
+    const unsigned cta = of.first + i;
+    return rows_state<D>(p, cta, sm.range.quota * (cta - sm.range.cta) < g.x, r);
+  };
+  auto load = [&](int i) {  // a batch from piece i on: a lane copies what it reads
+#pragma unroll 1
+    for (int j = i; j < min(i + BATCH, of.count); ++j)
 #pragma unroll
-    for (int j = 0; j < 2; ++j)
-      if (i + j < of.count) {
-        const unsigned cta = of.first + i + j;
-        const float* from = rows_state<D>(p, cta, sm.range.quota * (cta - sm.range.cta) < g.x, 0);
-        float* to = sm.piece[(i + j) % 6][0];
-        for (int x = tid; x < rows * CHUNKS; x += ROWS_THREADS) copy16(to + 4 * x, from + 4 * x, true);
+      for (int n = 0; n < MINE; ++n) {
+        const int r = r0 + n * (ROWS_THREADS / QUADS);
+        if (r < rows) copy16(&sm.piece[j % SLOTS * 8 * NT + r][4 * gl], piece(j, r) + 4 * gl, true);
       }
     copies_commit();
   };
   float4 x[MINE];
-  float m[MINE], l[MINE];
+  float m[MINE], l[MINE], weight[MINE];
 #pragma unroll
   for (int n = 0; n < MINE; ++n) x[n] = make_float4(0.0f, 0.0f, 0.0f, 0.0f), m[n] = -INFINITY, l[n] = 0.0f;
   load(0);
-  load(2);
-  for (int i = 0; i < of.count; i += 2) {
-    load(i + 4);
-    copies_wait<2>();
-    __syncthreads();
+  load(BATCH);
+#pragma unroll 1
+  for (int i = 0; i < of.count; i += BATCH) {
+    if (i % QUADS == 0) {  // the weights of the next pieces
 #pragma unroll
-    for (int j = 0; j < 2; ++j)
-      if (i + j < of.count) {
+      for (int n = 0; n < MINE; ++n) {
+        const int r = r0 + n * (ROWS_THREADS / QUADS);
+        float2 ml = make_float2(-INFINITY, 0.0f);
+        if (r < rows && i + gl < of.count) ml = __ldcg(reinterpret_cast<const float2*>(piece(i + gl, r) + D));
+        float top = ml.x;
 #pragma unroll
-        for (int n = 0; n < MINE; ++n) {
-          const int at = tid + n * ROWS_THREADS, r = at / QUADS, c = at % QUADS;
-          if (r >= rows) continue;
-          const float* state = sm.piece[(i + j) % 6][r];
-          const float2 ml = *reinterpret_cast<const float2*>(state + D);
-          const float top = fmaxf(m[n], ml.x);
-          const float old = m[n] == -INFINITY ? 0.0f : cs::ex2_approx(m[n] - top);
-          const float weight = ml.x == -INFINITY ? 0.0f : cs::ex2_approx(ml.x - top);
-          m[n] = top;
-          l[n] = fmaf(ml.y, weight, l[n] * old);
-          x[n].x *= old, x[n].y *= old, x[n].z *= old, x[n].w *= old;
-          add_weighted(x[n], reinterpret_cast<const float4*>(state)[c], weight);
-        }
+        for (int v = QUADS / 2; v; v >>= 1) top = fmaxf(top, __shfl_xor_sync(group, top, v));
+        top = fmaxf(top, m[n]);
+        const float old = m[n] == -INFINITY ? 0.0f : cs::ex2_approx(m[n] - top);
+        weight[n] = ml.x == -INFINITY ? 0.0f : cs::ex2_approx(ml.x - top);
+        m[n] = top;
+        float sum = ml.y * weight[n];
+#pragma unroll
+        for (int v = QUADS / 2; v; v >>= 1) sum += __shfl_xor_sync(group, sum, v);
+        l[n] = fmaf(l[n], old, sum);
+        x[n].x *= old, x[n].y *= old, x[n].z *= old, x[n].w *= old;
       }
-    __syncthreads();  // before the next copies over them
+    }
+    load(i + 2 * BATCH);
+    copies_wait<2>();  // this lane's own copies: no barrier
+#pragma unroll
+    for (int j = 0; j < BATCH; ++j)
+#pragma unroll
+      for (int n = 0; n < MINE; ++n) {
+        const int r = r0 + n * (ROWS_THREADS / QUADS);
+        const float f = __shfl_sync(group, weight[n], (i + j) % QUADS, QUADS);
+        if (r < rows && i + j < of.count)
+          add_weighted(x[n], *reinterpret_cast<const float4*>(&sm.piece[(i + j) % SLOTS * 8 * NT + r][4 * gl]), f);
+      }
   }
   copies_wait<0>();
 #pragma unroll
   for (int n = 0; n < MINE; ++n) {
-    const int at = tid + n * ROWS_THREADS, r = at / QUADS;
-    if (r < rows) rows_finish<T, D>(p, g, first, r, at % QUADS, x[n], m[n], l[n]);
+    const int r = r0 + n * (ROWS_THREADS / QUADS);
+    if (r < rows) rows_finish<T, D>(p, g, first, r, gl, x[n], m[n], l[n]);
   }
 }
 

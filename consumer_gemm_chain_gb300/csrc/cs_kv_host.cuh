@@ -311,7 +311,9 @@ inline cs_status map_caches(cskv::AttnP& k, const CUtensorMap& like) {
 // The kernels of a call with at most `max_rows` rows per key head, and the maps of their caches' copies.
 struct Kernels {
   const void *rows, *attn, *join;
-  int rows_shift, head_ctas;  // few rows: keys of a tile; CTAs of a key head where items go by heads, or 0
+  // few rows: keys of a tile; CTAs of a key head where items go by heads, or 0; fewest units of a CTA; how many
+  // tiles more a CTA may get so that items stay whole
+  int rows_shift, head_ctas, least, spare;
   int rows_grid, rows_smem, attn_smem, attn_threads;
   const CUtensorMap *rows_map, *attn_map;  // nullptr: read through pointers
 };
@@ -325,6 +327,17 @@ inline cs_status run_attention(cs_kv_s* p, cskv::AttnP& k, const Kernels& use, i
     k.c.per_item = cskv::ROWS / k.b.group;
     k.c.shift = use.rows_shift;
     k.c.head_ctas = use.head_ctas;
+    k.c.least = use.least;
+    // The longest CTA's tiles with whole items, one a sequence and head and as long as the page table (or the
+    // window) lets it be, against those of equal ranges.
+    if (!k.c.flat && use.spare > 0) {
+      const int tile = 1 << k.c.shift;
+      long long keys = static_cast<long long>(k.b.table_cols) * d.page_size;
+      if (k.c.window > 0) keys = std::min<long long>(keys, k.c.window + k.c.per_item + tile + (k.c.sinks + tile - 1) / tile * tile);
+      const long long units = (keys + tile - 1) / tile + k.c.item_cost, seqs = std::min(k.b.seqs, k.b.tokens);
+      const long long ctas = use.head_ctas ? use.head_ctas : use.rows_grid, items = use.head_ctas ? seqs : seqs * d.kv_heads;
+      k.c.whole = (items + ctas - 1) / ctas * units * ctas - items * units <= use.spare * ctas;
+    }
     if (use.rows_map && (s = map_caches(k, *use.rows_map)) != CS_OK) return s;
     s = launch(use.rows, dim3(use.rows_grid), cskv::ROWS_THREADS, use.rows_smem, &k, st);
     if (s != CS_OK || max_rows <= k.b.group || k.c.flat) return s;
@@ -336,6 +349,7 @@ inline cs_status run_attention(cs_kv_s* p, cskv::AttnP& k, const Kernels& use, i
   k.per_tile = 128 / k.b.group;
   k.c.per_item = 2 * k.per_tile;
   k.c.shift = 7;
+  k.c.least = 1;
   const cuuint64_t dims[3] = {static_cast<cuuint64_t>(d.head_dim), static_cast<cuuint64_t>(d.heads),
                               static_cast<cuuint64_t>(k.b.tokens)};
   const cuuint64_t strides[2] = {static_cast<cuuint64_t>(d.head_dim) * 2, static_cast<cuuint64_t>(k.q_stride) * 2};
