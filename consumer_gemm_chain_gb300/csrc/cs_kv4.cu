@@ -126,6 +126,17 @@ void fill_places(const cs_kv_s* p, const cs_kv_batch* b, const cs_kv4_cache& k, 
   f.k_scales = static_cast<uint8_t*>(k.scales);
   f.v_scales = static_cast<uint8_t*>(v.scales);
   f.head_chunks = p->d.head_dim / 8;
+  f.head_shift = p->d.head_dim == 128 ? 4 : 3;
+}
+
+// (The products of a block's units fit 32 bits: several tokens a block have some thousands together, one has up to
+// 2 x 1024 x 16.)
+void set_units(cskv::Four4P& f, int units, int q_units) {
+  auto reciprocal = [](uint32_t n) { return n < 2 ? 0u : static_cast<uint32_t>(((1ull << 32) + n - 1) / n); };
+  f.units = units;
+  f.per_unit = reciprocal(units);
+  f.q_units = q_units;
+  f.per_q_unit = reciprocal(q_units);
 }
 
 cs_status check_append4(const cs_kv_s* p, const cs_kv_batch* b, const cs_kv4_append_args* a, cskv::Four4P& f) {
@@ -153,7 +164,7 @@ cs_status check_append4(const cs_kv_s* p, const cs_kv_batch* b, const cs_kv4_app
   f.rope_rows = a->rope_rows;
   f.rotary_dim = d.rotary_dim;
   f.half = d.rotary_pairing == CS_KV_HALF;
-  f.units = d.heads * (f.head_chunks / 2) + 2 * d.kv_heads * f.head_chunks;
+  set_units(f, 2 * d.kv_heads * f.head_chunks, d.heads * (f.head_chunks / 2));
   return CS_OK;
 }
 
@@ -161,7 +172,7 @@ cs_status check_append4(const cs_kv_s* p, const cs_kv_batch* b, const cs_kv4_app
 // rounds of its threads.
 cs_status run_places(const cs_kv_s* p, const void* fn, cskv::Four4P& f, int rounds, cudaStream_t st) {
   if (f.b.tokens == 0 || f.b.seqs == 0) return CS_OK;
-  const int wanted = std::min(f.b.tokens / (2 * p->num_sms), rounds * cskv::FOUR_THREADS / f.units);
+  const int wanted = std::min(f.b.tokens / (2 * p->num_sms), rounds * cskv::FOUR_THREADS / static_cast<int>(f.units + f.q_units));
   f.tokens_per_block = std::max(1, std::min(wanted, cskv::FOUR_MAX_TOKENS));
   const dim3 grid((f.b.tokens + f.tokens_per_block - 1) / f.tokens_per_block);
   return launch(fn, grid, cskv::FOUR_THREADS, 0, &f, st);
@@ -197,7 +208,8 @@ cs_status check_read4(const cs_kv_s* p, const cs_kv_batch* b, const cs_kv4_read_
   f.v_out = static_cast<uint4*>(a->v_out);
   f.k_stride >>= 3;
   f.v_stride >>= 3;
-  f.units = ((a->k_out ? 1 : 0) + (a->v_out ? 1 : 0)) * d.kv_heads * (f.head_chunks / 2);
+  f.wide = ((reinterpret_cast<uintptr_t>(a->k_out) | reinterpret_cast<uintptr_t>(a->v_out)) % 32 == 0) && (f.k_stride | f.v_stride) % 2 == 0;
+  set_units(f, ((a->k_out ? 1 : 0) + (a->v_out ? 1 : 0)) * d.kv_heads * (f.head_chunks / 2), 0);
   return CS_OK;
 }
 

@@ -79,6 +79,11 @@ struct Four<__half> {
     y[2] = __hmul2(low(w >> 8), s);
     y[3] = __hmul2(high(w >> 8), s);
   }
+  __device__ __forceinline__ void pairs(uint32_t w, uint32_t& a, uint32_t& b, uint32_t& c, uint32_t& d) const {
+    uint32_t x[4];
+    pairs(w, x);
+    a = x[0], b = x[1], c = x[2], d = x[3];
+  }
 };
 
 // bf16: code bits under the exponent of 128 are 128 + (c + 8), and one multiply-add leaves s c: 136 s = 17 * 8 s
@@ -97,6 +102,11 @@ struct Four<__nv_bfloat16> {
       const uint32_t y = masked(w >> 4 * i, 0x000F000Fu, 0x43004300u);
       *reinterpret_cast<__nv_bfloat162*>(&x[i]) = __hfma2(*reinterpret_cast<const __nv_bfloat162*>(&y), s, off);
     }
+  }
+  __device__ __forceinline__ void pairs(uint32_t w, uint32_t& a, uint32_t& b, uint32_t& c, uint32_t& d) const {
+    uint32_t x[4];
+    pairs(w, x);
+    a = x[0], b = x[1], c = x[2], d = x[3];
   }
 };
 

@@ -83,6 +83,13 @@ struct Pair<__nv_bfloat16> {
   }
 };
 
+// 32 bytes, on a 32-byte boundary
+__device__ __forceinline__ void st32(void* p, const uint32_t* v) {
+  asm volatile("st.global.v8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"l"(p), "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]),
+               "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7])
+               : "memory");
+}
+
 // ---------------------------------------------------------------- append
 // (a, b) -> (a cos - b sin, b cos + a sin) for the rotated pairs of Q and K, a copy
 // for the rest.  A unit is 16 values of one head: the two 8-value chunks whose
