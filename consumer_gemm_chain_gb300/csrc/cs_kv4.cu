@@ -181,7 +181,7 @@ cs_status run_places(const cs_kv_s* p, const void* fn, cskv::Four4P& f, int roun
 cs_status run_append4(const cs_kv_s* p, cskv::Four4P& f, cudaStream_t st) {
   const void* fn = p->d.dtype == CS_BF16 ? (const void*)cskv::cs_kv4_append_kernel<__nv_bfloat16>
                                          : (const void*)cskv::cs_kv4_append_kernel<__half>;
-  return run_places(p, fn, f, 9, st);
+  return run_places(p, fn, f, 5, st);
 }
 
 cs_status check_read4(const cs_kv_s* p, const cs_kv_batch* b, const cs_kv4_read_args* a, cskv::Four4P& f) {
@@ -236,7 +236,7 @@ cs_status cs_kv4_read(cs_kv_t p, const cs_kv_batch* b, const cs_kv4_read_args* a
   if (!g.ok) return cs_fail(CS_ERR_CUDA, "cannot select the plan's device");
   const void* fn = p->d.dtype == CS_BF16 ? (const void*)cskv::cs_kv4_read_kernel<__nv_bfloat16>
                                          : (const void*)cskv::cs_kv4_read_kernel<__half>;
-  return run_places(p, fn, f, 9, static_cast<cudaStream_t>(stream));
+  return run_places(p, fn, f, 3, static_cast<cudaStream_t>(stream));
 }
 
 cs_status cs_kv4_attention(cs_kv_t p, const cs_kv_batch* b, const cs_kv4_attn_args* a, void* stream) {

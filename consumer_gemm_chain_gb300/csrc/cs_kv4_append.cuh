@@ -105,7 +105,7 @@ __device__ __forceinline__ uint32_t code_word(const float (&y)[8], float inv, bo
 }
 
 template <typename T>
-__global__ void __launch_bounds__(FOUR_THREADS, 5) cs_kv4_append_kernel(const __grid_constant__ Four4P p) {
+__global__ void __launch_bounds__(FOUR_THREADS, 6) cs_kv4_append_kernel(const __grid_constant__ Four4P p) {
   __shared__ Places places;
   cs::grid_dep_wait();
   cs::grid_dep_launch_dependents();

@@ -74,12 +74,12 @@ constexpr int ATTN_THREADS = ATTN_THREADS_OF<false>;
 // row of S, so the third warpgroup hands over what it does not need
 // (2 x 216 + 72 = 3 x 168; with a fourth 2 x 200 + 2 x 56 = 4 x 128).  Nothing may spill: next to
 // 226 KB of shared memory the L1 holds nearly nothing, and a spilled register comes back from L2.
-template <bool FOUR>
-constexpr int SOFTMAX_REGS = FOUR ? 200 : 216;
-template <bool FOUR>
-constexpr int OTHER_REGS = FOUR ? 56 : 72;
-static_assert(2 * SOFTMAX_REGS<false> + OTHER_REGS<false> <= 3 * 168 && 2 * SOFTMAX_REGS<true> + 2 * OTHER_REGS<true> <= 4 * 128,
-              "more registers than the launch holds");
+template <int D, bool FOUR>
+struct AttnRegs {
+  static constexpr int SOFTMAX = FOUR ? (D == 128 ? 192 : 200) : 216;
+  static constexpr int ISSUE = FOUR ? (D == 128 ? 64 : 56) : 72, MAKE = FOUR ? (D == 128 ? 64 : 56) : 0;
+  static_assert(2 * SOFTMAX + ISSUE + MAKE <= (FOUR ? 4 * 128 : 3 * 168), "more registers than the launch holds");
+};
 template <int N>
 __device__ __forceinline__ void regs_inc() {
   asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
@@ -377,7 +377,21 @@ __device__ bool load4_role(const AttnP& p, AttnCtl<AttnShape<D, true>>* sc, uint
 // A cache in 4 bits, a warpgroup: tiles of the operands, in the layout that load_role's copies have, from codes and
 // scales.  Warp w has 32 keys of every tile.  A lane has 32 dimensions of a key, the lanes of a load
 // and of a store (8 at a time) 8 keys, so that their 16-byte pieces fall into different banks.
+// (Shared memory by 32-bit addresses: the registers are few.)
 constexpr int MAKE4_WARPS = 4;
+__device__ __forceinline__ uint4 lds128(uint32_t at) {
+  uint4 v;
+  asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(at) : "memory");
+  return v;
+}
+__device__ __forceinline__ uint32_t lds8(uint32_t at) {
+  uint32_t v;
+  asm volatile("ld.shared.u8 %0, [%1];" : "=r"(v) : "r"(at) : "memory");
+  return v;
+}
+__device__ __forceinline__ void sts128(uint32_t at, const uint32_t (&v)[4]) {
+  asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(at), "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]) : "memory");
+}
 template <typename T, int D>
 __device__ bool make4_role(const AttnP& p, AttnCtl<AttnShape<D, true>>* sc, const uint8_t* stages, uint8_t* ring, int w) {
   using Sh = AttnShape<D, true>;
@@ -385,9 +399,11 @@ __device__ bool make4_role(const AttnP& p, AttnCtl<AttnShape<D, true>>* sc, cons
   const int lane = threadIdx.x & 31, row = lane % ROWS_OF, piece = lane / ROWS_OF;
   const int first = w * 32 + row;  // this lane's first key
   const int turn = D == 128 ? row >> 1 & 3 : row >> 2 & 1;  // of the copies' swizzle
-  const uint8_t* const codes = stages + first * (D / 2) + ((piece ^ turn) << 4);
-  const uint8_t* const scales = stages + Sh::CODES + first * PIECES + piece;
-  uint8_t* const tile = ring + (first >> 3) * (Sh::HALVES * 1024) + (piece >> 1) * 1024 + (row & 7) * 128;
+  const uint32_t codes = cs::smem_u32(stages) + first * (D / 2) + ((piece ^ turn) << 4);
+  const uint32_t scales = cs::smem_u32(stages) + Sh::CODES + first * PIECES + piece;
+  // piece 4 (piece & 1) + v of a row lies at its index ^ (row & 7)
+  const uint32_t tile = cs::smem_u32(ring) + (first >> 3) * (Sh::HALVES * 1024) + (piece >> 1) * 1024 + (row & 7) * 128 +
+                        (((piece & 1) * 4 ^ (row & 4)) << 4);
   Walk walk(p.c, sc->range);
   Seg g;
   Ring<Sh::STAGES> from;
@@ -402,33 +418,31 @@ __device__ bool make4_role(const AttnP& p, AttnCtl<AttnShape<D, true>>* sc, cons
       for (int half = 0; half < 2; ++half) {  // K, then V
         if (!wait_warp(&sc->stage_full[from.slot], from.phase, sc)) return false;
         if (!wait_warp(&sc->empty[to.slot], to.phase ^ 1u, sc)) return false;
-        const uint8_t* c = codes + from.slot * Sh::STAGE;
-        const uint8_t* s = scales + from.slot * Sh::STAGE;
-        uint4 words[LOADS];
-        uint32_t byte[LOADS];
+        const uint32_t c = codes + from.slot * Sh::STAGE, s = scales + from.slot * Sh::STAGE, d = tile + to.slot * Sh::TILE;
+        constexpr int AT_A_TIME = 2;
 #pragma unroll
-        for (int i = 0; i < LOADS; ++i) {
-          words[i] = *reinterpret_cast<const uint4*>(c + i * ROWS_OF * (D / 2));
-          byte[i] = s[i * ROWS_OF * PIECES];
-        }
-        if (edge) {
+        for (int i0 = 0; i0 < LOADS; i0 += AT_A_TIME) {
+          uint4 words[AT_A_TIME];
+          uint32_t byte[AT_A_TIME];
 #pragma unroll
-          for (int i = 0; i < LOADS; ++i) {
-            const int key = j0 + first + i * ROWS_OF;
-            if (!(key < g.hi && (key >= g.lo || key < p.c.sinks))) byte[i] = 0;
+          for (int i = 0; i < AT_A_TIME; ++i) {
+            words[i] = lds128(c + (i0 + i) * ROWS_OF * (D / 2));
+            byte[i] = lds8(s + (i0 + i) * ROWS_OF * PIECES);
+            if (edge) {
+              const int key = j0 + first + (i0 + i) * ROWS_OF;
+              if (!(key < g.hi && (key >= g.lo || key < p.c.sinks))) byte[i] = 0;
+            }
           }
-        }
-        uint8_t* d = tile + to.slot * Sh::TILE;
 #pragma unroll
-        for (int i = 0; i < LOADS; ++i) {
-          const Four<T> four(scale_pair(byte[i]));
-          const uint32_t ws[4] = {words[i].x, words[i].y, words[i].z, words[i].w};
+          for (int i = 0; i < AT_A_TIME; ++i) {
+            const Four<T> four(scale_pair(byte[i]));
+            const uint32_t ws[4] = {words[i].x, words[i].y, words[i].z, words[i].w};
 #pragma unroll
-          for (int v = 0; v < 4; ++v) {
-            uint32_t x[4];
-            four.pairs(ws[v], x);
-            *reinterpret_cast<uint4*>(d + i * ROWS_OF / 8 * (Sh::HALVES * 1024) + ((((piece & 1) * 4 + v) ^ (row & 7)) << 4)) =
-                make_uint4(x[0], x[1], x[2], x[3]);
+            for (int v = 0; v < 4; ++v) {
+              uint32_t x[4];
+              four.pairs(ws[v], x);
+              sts128(d + (i0 + i) * ROWS_OF / 8 * (Sh::HALVES * 1024) + ((v ^ (row & 3)) << 4), x);
+            }
           }
         }
         cs::fence_proxy_async_shared();
@@ -1214,16 +1228,21 @@ __global__ void __launch_bounds__(ATTN_THREADS_OF<FOUR>, 1) cs_kv_attn_kernel(co
   find_range<ATTN_THREADS_OF<FOUR>>(p.b, p.c, &sc->range, sc->scratch);
   constexpr int bf16 = sizeof(T) == 2 && !std::is_same<T, __half>::value;
   if (warp < 8) {
-    regs_inc<SOFTMAX_REGS<FOUR>>();
+    regs_inc<AttnRegs<D, FOUR>::SOFTMAX>();
     // (a softmax that gave up may have stores to tensor memory on their way)
     if (!softmax_role<T, D, WINDOW, FOUR>(p, sc, ring, warp >> 2)) cs::tc_wait_st();
-  } else {
-    regs_dec<OTHER_REGS<FOUR>>();
+  } else if (FOUR && warp >= 12) {
     if constexpr (FOUR) {
-      if (warp == 8) load4_role<D>(p, sc, qbuf, stages);
-      if (warp >= 12) make4_role<T, D>(p, sc, stages, ring, warp - 12);
-    } else {
-      if (warp == 8) load_role<D>(p, sc, qbuf, ring);
+      regs_dec<AttnRegs<D, FOUR>::MAKE>();
+      make4_role<T, D>(p, sc, stages, ring, warp - 12);
+    }
+  } else {
+    regs_dec<AttnRegs<D, FOUR>::ISSUE>();
+    if (warp == 8) {
+      if constexpr (FOUR)
+        load4_role<D>(p, sc, qbuf, stages);
+      else
+        load_role<D>(p, sc, qbuf, ring);
     }
     if (warp == 9 || warp == 10) mma_role<D, WINDOW, FOUR>(p, sc, qbuf, ring, bf16, warp - 9);
   }
