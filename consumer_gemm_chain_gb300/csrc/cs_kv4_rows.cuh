@@ -157,7 +157,8 @@ __global__ void __launch_bounds__(ROWS_THREADS, ROWS4_CTAS<NT>) cs_kv4_rows_kern
   // bytes of scales (which lie side by side).
   constexpr int PIECES = D / GROUP4, STEP = 16 / PIECES;
   const int run = lane >> 4, piece = lane & (PIECES - 1), first_key = (lane & 15) / PIECES;
-  const uint32_t slot_bytes = static_cast<uint32_t>(B.slot_stride >> 1);
+  const uint32_t slot_bytes = static_cast<uint32_t>(B.slot_stride >> 1), page_bytes = static_cast<uint32_t>(B.page_stride >> 1);
+  const uint32_t page_scales = B.kv_heads * B.page_size * PIECES;
   const bool has_scales = (lane & 15) < 2 * PIECES, of_v = (lane & 15) >= PIECES;
   WalkOf<BY_HEAD> walk(p.c, sm.range);
   Seg g;
@@ -184,12 +185,12 @@ __global__ void __launch_bounds__(ROWS_THREADS, ROWS4_CTAS<NT>) cs_kv4_rows_kern
     // this lane's part of the codes of K, and V's offset from it; of the scales, K's or V's
     const uint8_t* const codes = static_cast<const uint8_t*>(p.k_raw) + (g.kvh * B.head_stride >> 1) + first_key * slot_bytes + piece * 16;
     const long long to_v = static_cast<const uint8_t*>(p.v_raw) - static_cast<const uint8_t*>(p.k_raw);
-    const uint8_t* const scales = (of_v ? p.v_scales : p.k_scales) + piece * 16;
+    const uint8_t* const scales = (of_v ? p.v_scales : p.k_scales) + g.kvh * (B.page_size * PIECES) + piece * 16;
     auto load = [&](int k, int page, Stage4<D>& to) {
       if (k < g.k1) {
         const bool read = page >= 0;
         const uint32_t from = read ? page : 0, slot = (tile_at(k) + mine) & (B.page_size - 1);
-        const uint8_t* at = codes + from * (B.page_stride >> 1) + slot * slot_bytes;
+        const uint8_t* at = codes + static_cast<uint64_t>(from) * page_bytes + slot * slot_bytes;
         uint8_t* into = &to.codes[0][run * 16 + first_key][(piece ^ turn(first_key)) * 16];
 #pragma unroll
         for (int i = 0; i < PIECES; ++i) {  // (STEP is a multiple of 4, so the piece is turned alike)
@@ -199,7 +200,7 @@ __global__ void __launch_bounds__(ROWS_THREADS, ROWS4_CTAS<NT>) cs_kv4_rows_kern
         }
         if (has_scales)
           copy16(&to.scales[of_v][run * 16][0] + piece * 16,
-                 scales + ((static_cast<long long>(from) * B.kv_heads + g.kvh) * B.page_size + slot) * PIECES, read);
+                 scales + static_cast<uint64_t>(from) * page_scales + slot * PIECES, read);
       }
       copies_commit();
     };

@@ -16,22 +16,20 @@ from .kv import CS_KV_TOKEN, KVBatch, KVPlan, _bad, _check, _I, _L, _P, _rows, _
 KV4_EXPORTED = ("cs_kv4_append", "cs_kv4_read", "cs_kv4_attention", "cs_kv4_attention_shared", "cs_attn_cached4_forward")
 
 
-class cs_kv4_cache(ctypes.Structure):
-    _fields_ = [("codes", _P), ("scales", _P)]
+_K, _V = [("k_codes", _P), ("k_scales", _P)], [("v_codes", _P), ("v_scales", _P)]  # a cs_kv4_cache each
 
 
 class cs_kv4_append_args(ctypes.Structure):
-    _fields_ = [("qkv", _P), ("qkv_stride", _L), ("q_out", _P), ("q_stride", _L), ("k", cs_kv4_cache), ("v", cs_kv4_cache),
+    _fields_ = [("qkv", _P), ("qkv_stride", _L), ("q_out", _P), ("q_stride", _L), *_K, *_V,
                 ("rope", _P), ("rope_rows", _I), ("positions", _P)]
 
 
 class cs_kv4_read_args(ctypes.Structure):
-    _fields_ = [("k", cs_kv4_cache), ("v", cs_kv4_cache), ("k_out", _P), ("k_stride", _L), ("v_out", _P), ("v_stride", _L)]
+    _fields_ = [*_K, *_V, ("k_out", _P), ("k_stride", _L), ("v_out", _P), ("v_stride", _L)]
 
 
 class cs_kv4_attn_args(ctypes.Structure):
-    _fields_ = [("q", _P), ("q_stride", _L), ("k", cs_kv4_cache), ("v", cs_kv4_cache), ("out", _P), ("out_stride", _L),
-                ("lse", _P)]
+    _fields_ = [("q", _P), ("q_stride", _L), *_K, *_V, ("out", _P), ("out_stride", _L), ("lse", _P)]
 
 
 def _declare():
@@ -57,26 +55,31 @@ def cs_kv4_shapes(plan: KVPlan):
     return codes, (pages, hk, ps, d.head_dim // 32)
 
 
-def _shapes(plan):
-    s = plan.__dict__.get("_four_shapes")
-    if s is None:
-        s = plan._four_shapes = cs_kv4_shapes(plan)
-    return s
+_U8 = torch.uint8
 
 
-def _cache(plan, c, pair, name) -> None:
+def _cache(plan, pair, name):
+    """(pointer of the codes, pointer of the scales) of a cache."""
+    try:
+        codes_shape, scales_shape = plan._four_shapes
+    except AttributeError:
+        codes_shape, scales_shape = plan._four_shapes = cs_kv4_shapes(plan)
     if not isinstance(pair, (tuple, list)) or len(pair) != 2:
         raise TypeError(f"{name} must be a pair (codes, scales); got {type(pair).__name__}")
-    codes, scales = _shapes(plan)
-    c.codes = _whole(pair[0], codes, torch.uint8, plan.device, f"{name} codes")
-    c.scales = _whole(pair[1], scales, torch.uint8, plan.device, f"{name} scales")
+    c, s = pair
+    if (isinstance(c, torch.Tensor) and isinstance(s, torch.Tensor) and c.dtype is _U8 and s.dtype is _U8
+            and c.shape == codes_shape and s.shape == scales_shape and c.get_device() == s.get_device() == plan.device
+            and c.is_contiguous() and s.is_contiguous()):
+        return c.data_ptr(), s.data_ptr()
+    _whole(c, codes_shape, _U8, plan.device, name + " codes")  # one of them says what is wrong
+    _whole(s, scales_shape, _U8, plan.device, name + " scales")
 
 
 def _append_args(plan, batch, k, v, rope, positions) -> cs_kv4_append_args:
     _same_device(plan, batch)
     a = cs_kv4_append_args()
-    _cache(plan, a.k, k, "k")
-    _cache(plan, a.v, v, "v")
+    a.k_codes, a.k_scales = _cache(plan, k, "k")
+    a.v_codes, a.v_scales = _cache(plan, v, "v")
     if rope is not None:
         if not isinstance(rope, torch.Tensor) or rope.dim() != 2:
             raise _bad("rope", rope, "a 2-D float32 tensor")
@@ -103,10 +106,10 @@ def cs_kv4_read(plan: KVPlan, batch: KVBatch, k, v, k_out, v_out, stream=None) -
     _same_device(plan, batch)
     a, d = cs_kv4_read_args(), plan.desc
     if k_out is not None:
-        _cache(plan, a.k, k, "k")
+        a.k_codes, a.k_scales = _cache(plan, k, "k")
         a.k_out, a.k_stride = _rows(k_out, batch.tokens, d.kv_heads, d.head_dim, plan.dtype, plan.device, "k_out")
     if v_out is not None:
-        _cache(plan, a.v, v, "v")
+        a.v_codes, a.v_scales = _cache(plan, v, "v")
         a.v_out, a.v_stride = _rows(v_out, batch.tokens, d.kv_heads, d.head_dim, plan.dtype, plan.device, "v_out")
     _check(_lib.cs_kv4_read(plan.handle, batch._ref, byref(a), _stream(stream, plan.device)), "cs_kv4_read")
 
@@ -116,8 +119,8 @@ def _attn4_args(plan, batch, q, k, v, out, lse) -> cs_kv4_attn_args:
     a, d = cs_kv4_attn_args(), plan.desc
     a.q, a.q_stride = _rows(q, batch.tokens, d.heads, d.head_dim, plan.dtype, plan.device, "q")
     a.out, a.out_stride = _rows(out, batch.tokens, d.heads, d.head_dim, plan.dtype, plan.device, "out")
-    _cache(plan, a.k, k, "k")
-    _cache(plan, a.v, v, "v")
+    a.k_codes, a.k_scales = _cache(plan, k, "k")
+    a.v_codes, a.v_scales = _cache(plan, v, "v")
     a.lse = None if lse is None else _whole(lse, (batch.tokens, d.heads), torch.float32, plan.device, "lse")
     return a
 
