@@ -58,7 +58,8 @@ typedef struct cs_kv4_append_args {
 
 /* cs_kv_append into a cache in 4 bits.  The rotation rounds each product and each sum
  * to 32 bits (no fused multiply-add) and the result to the dtype, and what is
- * quantised is that result: the same inputs give the same bytes. */
+ * quantised is that result: the same inputs give the same bytes.  Two tokens sent to one
+ * slot leave a mixture of their codes and scales there. */
 cs_status cs_kv4_append(cs_kv_t plan, const cs_kv_batch* batch, const cs_kv4_append_args* args, void* stream);
 
 typedef struct cs_kv4_read_args {

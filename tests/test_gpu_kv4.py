@@ -204,6 +204,87 @@ def test_values_of_other_sizes(dtype, size, n):
     d.check()
 
 
+def scaled_batch(q, kv, dtype, sizes_k, sizes_v, head_dim=64, **kw):
+    """A batch whose keys' and values' groups are of the sizes given, in turn."""
+    from kv4_util import parts
+    b = Batch4(q, kv, 8, 2, head_dim, dtype, **kw)
+
+    def scaled(cache, sizes):
+        groups = cache.float().unflatten(-1, (-1, 32))
+        s = torch.tensor(sizes)[torch.arange(groups[..., 0].numel()) % len(sizes)].view(groups.shape[:-1])
+        x = (groups * s[..., None]).flatten(-2)
+        return x.clamp(-6e4, 6e4).to(dtype) if dtype == F16 else x.to(dtype)  # (f16 ends at 65504)
+
+    for name, cache, sizes, seqs in (("k4", b.kc, sizes_k, b.k), ("v4", b.vc, sizes_v, b.v)):
+        x = scaled(cache, sizes)
+        setattr(b, name, parts(x, b.layout))
+        held = torch.from_numpy(o4.held(x)).to(dtype)
+        for i, m in enumerate(kv):
+            for j in range(m):
+                if int(b.table[i, j // 16]) != BAD_PAGE:
+                    seqs[i][j] = held[int(b.table[i, j // 16]), j % 16]
+    return b
+
+
+@pytest.mark.parametrize("n", [1, 3, 40])
+@pytest.mark.parametrize("dtype,big", [(F16, 1.4e4), (BF16, 9e4), (BF16, 1.3e4)])
+def test_scales_of_all_sizes_beside_one_another(n, dtype, big):
+    """Groups of values near the ends of the scales' range, of usual ones and of zeros, in one key and in neighbouring ones."""
+    sizes = [big, 1.0, 1e-5, 300.0, 0.0, 1e-4, big, 3e-6, 0.03, 1e3, 20.0]
+    run(scaled_batch([n, 1], [200, 90], dtype, [1.0], sizes, seed=n))
+    run(scaled_batch([n, 1], [200, 90], dtype, [1.0, 0.3], sizes, head_dim=128, seed=n))
+    # keys of such sizes: scores of a few units by the scale, weights over the keys with large groups only
+    b = scaled_batch([n], [150], dtype, sizes, [1.0], seed=n, scale=2.0 ** -19, spread=1.0)
+    d = Device(b)
+    d.attend()
+    d.ok()
+    ref, lse, bound = b.reference()
+    # 64 products in 32 bits: a score is off by up to 2^-24 * 64 * sum |q k| scale
+    worst = 2 * 2.0 ** -24 * 64 * 64 * float(b.q.float().abs().amax() * b.k[0].float().abs().amax()) * 2.0 ** -19
+    assert (np.abs(okv.to64(d.out) - ref) <= bound * (1 + worst / 2.0 ** -11)).all()
+
+
+def test_large_scores():
+    """Rows whose maximum keeps rising by much, and weights far below the row's largest."""
+    for n in (1, 2, 200):
+        for dtype in (BF16, F16):
+            b = scaled_batch([n], [600], dtype, [float(x) for x in np.linspace(0.02, 3, 61)], [1.0], head_dim=128, scale=1.0, seed=5)
+            d = Device(b)
+            d.attend()
+            d.ok()
+            ref, _, bound = b.reference()
+            worst = 2 * 2.0 ** -24 * 128 * 128 * float(b.q.float().abs().amax() * b.k[0].float().abs().amax())
+            assert (np.abs(okv.to64(d.out) - ref) <= bound * (1 + worst / 2.0 ** -11)).all()
+
+
+@pytest.mark.parametrize("size", [1e-30, 1e-6, 3e4, 1e30])
+@pytest.mark.parametrize("n", [1, 4])
+def test_queries_of_other_sizes(n, size):
+    """Rows of bf16 queries far from 1, the scale undoing it; rows of one call differ, and values within a row too."""
+    b = Batch4([n, 1], [300, 80], 8, 2, 128, BF16, seed=n, scale=float(np.float32(0.09 / size)))
+    b.q = (b.q.float() * size).to(BF16)
+    b.q[..., 1::7] *= 2.0 ** -20
+    b.q[0, 1::2] *= 2.0 ** -12
+    run(b)
+
+
+def test_a_query_that_is_not_finite():
+    """Its rows are NaN; the others of the call are as without it."""
+    for n in (1, 2, 30):
+        for dtype in (F16, BF16):
+            b = Batch4([n, n], [200, 100], 8, 2, 128, dtype, seed=n)
+            d = Device(b)
+            d.attend()
+            d.ok()
+            clean = d.out.clone()
+            d.q[0, 1, 5], d.q[n, 6, 7] = math.nan, math.inf
+            d.attend()
+            d.ok()
+            assert torch.isnan(d.out[0, 1]).all() and torch.isnan(d.out[n, 6]).all()
+            d.out[0, 1], d.out[n, 6] = clean[0, 1], clean[n, 6]
+            assert torch.equal(d.out, clean)
+
+
 @pytest.mark.parametrize("q,kv", [([4, 1], [70, 9]), ([3], [900]), ([200, 30], [300, 30]), ([130], [2000]), ([2], [40])])
 @pytest.mark.parametrize("window,prefix", [(0, 0), (33, 0), (0, 50)])
 def test_scales_that_are_no_number_at_keys_hidden_from_some_rows(q, kv, window, prefix):
@@ -658,6 +739,25 @@ def test_calls_right_behind_one_another(q, kv, prefix, captured):
         torch.cuda.synchronize()
         assert torch.equal(outs[0], outs[1]) and torch.equal(read[0], read[1])
     d.ok()
+
+
+def test_a_plans_first_call_captured():
+    """Nothing of a plan is made in a way that a capture forbids; graphs of a plan each may run side by side."""
+    graphs, ds, streams = [], [], [torch.cuda.Stream() for _ in range(3)]
+    for s, n in enumerate((1, 4, 60)):
+        d = Device(Batch4([n, n], [900, 300], 8, 2, 128, BF16, seed=s))
+        torch.cuda.synchronize()
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            d.attend()
+        graphs.append(graph), ds.append(d)
+    for _ in range(10):
+        for graph, s in zip(graphs, streams):
+            with torch.cuda.stream(s):
+                graph.replay()
+    for d in ds:
+        d.ok()
+        d.check()
 
 
 def test_two_plans_on_two_streams():
