@@ -11,11 +11,26 @@
 // A lane (g, t) of S^T's first operand has 32 (16) consecutive dimensions of two keys, under one
 // scale each; of V^T's it has 16 (8) dimensions of four keys: two keys' words, taken apart in
 // 16-bit halves and put together by dimension, make pairs along the keys.  P^T is the second operand of O^T:
-// an 8 x 8 transposition of S^T's accumulators (movmatrix).
+// an 8 x 8 transposition of S^T's accumulators (movmatrix).  All operands are f16, whatever the
+// cache's type is: a code is then a value after a mask and a multiply-add (FourScaled; bf16 takes more
+// shifts), values times 2^-7 are f16 numbers for every scale, queries of bf16 are put to f16's range row by row, and
+// weights are rounded to 11 bits instead of 8.
 //
 // Row r of S^T's 8-row half is key r / 2 (r even) or 7 - r / 2 (r odd) of 8: with it all reads
 // of the codes from shared memory are free of bank conflicts.
+//
+// Bound.  Instructions: 350 for 16 keys of 128 dimensions and a warp, about half of them to make operands of codes,
+// at 2.4 of 4 a cycle (shifts, masks and byte selections, at half a warp a cycle and scheduler, keep their pipe busy in
+// 54 % of the cycles, DRAM is at 54 %).  64 single tokens over 300 to 32000 keys, 64 / 8 heads of 128 (1.13 GB):
+// 260 us, 4.3 TB/s, 0.64 of a plain copy's measured 6.8; the 16-bit cache (4.26 GB) takes 664 to 692.  256000 keys of
+// 8 heads: 80 us from L2, 81 from DRAM.  One user's token over 978 keys, 12 heads: 9.3 us, the latency of
+// its steps, as over the 16-bit cache; over 16000 keys, 8 heads: 29.5.  128 tokens under a window of 1024,
+// 40 / 8 heads of 64: 37.5 us, of which the start of a launch, its division and its last joins are about 13.
+// Slower or no faster: items' first copies sent off while the item before is stored (81 and 81 us), runs one by one in half
+// the code (84), right shifts as products' upper halves (96), prefetches of whole lines, two CTAs an SM with 16 columns.
 #pragma once
+#include <cfloat>
+
 #include "cs_kv_rows.cuh"
 
 namespace cskv {
@@ -243,7 +258,7 @@ __global__ void __launch_bounds__(ROWS_THREADS, ROWS4_CTAS<NT>) cs_kv4_rows_kern
       }
 #pragma unroll
       for (int e = 0; e < 2; ++e)
-        unit[n][e] = __shfl_sync(0xFFFFFFFFu, f, 4 * (2 * jq + e)) * (p.scale_log2 / FOUR_UNIT);
+        unit[n][e] = fminf(__shfl_sync(0xFFFFFFFFu, f, 4 * (2 * jq + e)) / FOUR_UNIT * p.scale_log2, FLT_MAX);
     }
     // keys below all_end and from all_lo on are seen by every row
     const int all_end = p.c.flat ? g.s.m : base + 1, all_lo = p.c.window > 0 ? max(0, base + tokens - p.c.window) : 0;
@@ -280,8 +295,7 @@ __global__ void __launch_bounds__(ROWS_THREADS, ROWS4_CTAS<NT>) cs_kv4_rows_kern
 #pragma unroll 1
       for (int x0 = 0; x0 < 2; x0 += XS) {
         // the scales of this lane's keys, two of K and two pairs of V, and whether one of the warp's is big
-        uint32_t sk[XS], sv[XS][2];
-        bool big = false;
+        uint32_t sk[XS], sv[XS][2], most = 0;
 #pragma unroll
         for (int x = 0; x < XS; ++x) {
           const uint8_t* of_k = st.scales[0][(x0 + x) * 16 + key0] + (D == 128 ? jq : jq >> 1);
@@ -297,123 +311,125 @@ __global__ void __launch_bounds__(ROWS_THREADS, ROWS4_CTAS<NT>) cs_kv4_rows_kern
               if (!(key < g.hi && (key >= g.lo || key < p.c.sinks))) v[y] = 0;
             }
           }
-          big |= max(max(k0, k1), max(max(v[0], v[1]), max(v[2], v[3]))) >= FourScaled::BIG_BYTE;
-          sk[x] = k0 | k1 << 16;
-          sv[x][0] = scale_pair(v[0], v[1]);
-          sv[x][1] = scale_pair(v[2], v[3]);
+          const uint32_t v01 = v[1] * 0x10000u + v[0], v23 = v[3] * 0x10000u + v[2];
+          sk[x] = k1 * 0x10000u + k0;
+          sv[x][0] = v01 * 0x80u;
+          sv[x][1] = v23 * 0x80u;
+          most = __vmaxu2(most, __vmaxu2(sk[x], __vmaxu2(v01, v23)));
         }
+        const bool big = (most + (0x100u - FourScaled::BIG_BYTE) * 0x10001u & 0x01000100u) != 0;
         auto keys = [&](auto is_big) {
-        constexpr bool BIG = decltype(is_big)::value;
-        float s[XS][NT][4] = {};
+          constexpr bool BIG = decltype(is_big)::value;
+          float s[XS][NT][4] = {};
 #pragma unroll
-        for (int x = 0; x < XS; ++x) {
-          uint32_t ka[KW], kb[KW];
-          const int j = (x0 + x) * 16 + key0;
-          const uint8_t* row = st.codes[0][j] + (D == 128 ? (jq ^ turn(key0)) * 16 : jq * 8);
-          if constexpr (D == 128) {
-            *reinterpret_cast<uint4*>(ka) = *reinterpret_cast<const uint4*>(row);
-            *reinterpret_cast<uint4*>(kb) = *reinterpret_cast<const uint4*>(row + 8 * (D / 2));
-          } else {
-            *reinterpret_cast<uint2*>(ka) = *reinterpret_cast<const uint2*>(row);
-            *reinterpret_cast<uint2*>(kb) = *reinterpret_cast<const uint2*>(row + 8 * (D / 2));
-          }
-          const FourScaled fa(scale_pair(sk[x] & 0xFFu)), fb(scale_pair(sk[x] >> 16));
+          for (int x = 0; x < XS; ++x) {
+            uint32_t ka[KW], kb[KW];
+            const int j = (x0 + x) * 16 + key0;
+            const uint8_t* row = st.codes[0][j] + (D == 128 ? (jq ^ turn(key0)) * 16 : jq * 8);
+            if constexpr (D == 128) {
+              *reinterpret_cast<uint4*>(ka) = *reinterpret_cast<const uint4*>(row);
+              *reinterpret_cast<uint4*>(kb) = *reinterpret_cast<const uint4*>(row + 8 * (D / 2));
+            } else {
+              *reinterpret_cast<uint2*>(ka) = *reinterpret_cast<const uint2*>(row);
+              *reinterpret_cast<uint2*>(kb) = *reinterpret_cast<const uint2*>(row + 8 * (D / 2));
+            }
+            const FourScaled fa(scale_pair(sk[x] & 0xFFu)), fb(scale_pair(sk[x] >> 16));
 #pragma unroll
-          for (int w = 0; w < KW; ++w) {
-            uint32_t a[4], b[4];
-            fa.pairs<BIG>(ka[w], a);
-            fb.pairs<BIG>(kb[w], b);
+            for (int w = 0; w < KW; ++w) {
+              uint32_t a[4], b[4];
+              fa.pairs<BIG>(ka[w], a);
+              fb.pairs<BIG>(kb[w], b);
 #pragma unroll
-            for (int n = 0; n < NT; ++n) {
-              mma16816<__half>(s[x][n], a[0], b[0], a[1], b[1], q[n][w][0], q[n][w][1]);
-              mma16816<__half>(s[x][n], a[2], b[2], a[3], b[3], q[n][w][2], q[n][w][3]);
+              for (int n = 0; n < NT; ++n) {
+                mma16816<__half>(s[x][n], a[0], b[0], a[1], b[1], q[n][w][0], q[n][w][1]);
+                mma16816<__half>(s[x][n], a[2], b[2], a[3], b[3], q[n][w][2], q[n][w][3]);
+              }
             }
           }
-        }
-        if (__builtin_expect(mask, 0)) {
+          if (__builtin_expect(mask, 0)) {
 #pragma unroll
-          for (int x = 0; x < XS; ++x)
+            for (int x = 0; x < XS; ++x)
 #pragma unroll
-            for (int n = 0; n < NT; ++n)
+              for (int n = 0; n < NT; ++n)
 #pragma unroll
-              for (int c = 0; c < 4; ++c)
-                if (!seen_by(n, c & 1, tile0 + (x0 + x) * 64 + key0 + 8 * (c >> 1))) s[x][n][c] = -INFINITY;
-        }
-        bool raise = false;
-        float top[NT][2];
-#pragma unroll
-        for (int n = 0; n < NT; ++n)
-#pragma unroll
-          for (int e = 0; e < 2; ++e) {
-            top[n][e] = fmaxf(s[0][n][e], s[0][n][2 + e]);
-            if (XS == 2) top[n][e] = max3(top[n][e], s[XS - 1][n][e], s[XS - 1][n][2 + e]);
-            // raised only when it is exceeded by more than 2^8 (from -infinity by anything but that)
-            raise |= fmaf(top[n][e], unit[n][e], -m_ref[n][e]) > RAISE_LOG2;
+                for (int c = 0; c < 4; ++c)
+                  if (!seen_by(n, c & 1, tile0 + (x0 + x) * 64 + key0 + 8 * (c >> 1))) s[x][n][c] = -INFINITY;
           }
-        if (__any_sync(0xFFFFFFFFu, raise)) {
+          bool raise = false;
+          float top[NT][2];
 #pragma unroll
           for (int n = 0; n < NT; ++n)
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
-              float m = top[n][e];
+              top[n][e] = fmaxf(s[0][n][e], s[0][n][2 + e]);
+              if (XS == 2) top[n][e] = max3(top[n][e], s[XS - 1][n][e], s[XS - 1][n][2 + e]);
+              // raised only when it is exceeded by more than 2^8 (from -infinity by anything but that)
+              raise |= fmaf(top[n][e], unit[n][e], -m_ref[n][e]) > RAISE_LOG2;
+            }
+          if (__any_sync(0xFFFFFFFFu, raise)) {
 #pragma unroll
-              for (int d = 4; d < 32; d <<= 1) m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, d));
-              if (fmaf(m, unit[n][e], -m_ref[n][e]) > RAISE_LOG2) {
-                m *= unit[n][e];
-                const float f = cs::ex2_approx(m_ref[n][e] - m);
-                m_ref[n][e] = m;
-                l[n][e] *= f;
+            for (int n = 0; n < NT; ++n)
 #pragma unroll
-                for (int i = 0; i < 4 * VW; ++i) o[n][i][e] *= f, o[n][i][2 + e] *= f;
+              for (int e = 0; e < 2; ++e) {
+                float m = top[n][e];
+#pragma unroll
+                for (int d = 4; d < 32; d <<= 1) m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, d));
+                if (fmaf(m, unit[n][e], -m_ref[n][e]) > RAISE_LOG2) {
+                  m *= unit[n][e];
+                  const float f = cs::ex2_approx(m_ref[n][e] - m);
+                  m_ref[n][e] = m;
+                  l[n][e] *= f;
+#pragma unroll
+                  for (int i = 0; i < 4 * VW; ++i) o[n][i][e] *= f, o[n][i][2 + e] *= f;
+                }
+              }
+          }
+          uint32_t pt[XS][NT][2];
+#pragma unroll
+          for (int n = 0; n < NT; ++n) {
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+              const float sub = m_ref[n][e] == -INFINITY ? 0.0f : -m_ref[n][e];
+#pragma unroll
+              for (int x = 0; x < XS; ++x) {
+                s[x][n][e] = cs::ex2_approx(fmaf(s[x][n][e], unit[n][e], sub));
+                s[x][n][2 + e] = cs::ex2_approx(fmaf(s[x][n][2 + e], unit[n][e], sub));
+                l[n][e] += s[x][n][e] + s[x][n][2 + e];
               }
             }
-        }
-        uint32_t pt[XS][NT][2];
-#pragma unroll
-        for (int n = 0; n < NT; ++n) {
-#pragma unroll
-          for (int e = 0; e < 2; ++e) {
-            const float sub = m_ref[n][e] == -INFINITY ? 0.0f : -m_ref[n][e];
 #pragma unroll
             for (int x = 0; x < XS; ++x) {
-              s[x][n][e] = cs::ex2_approx(fmaf(s[x][n][e], unit[n][e], sub));
-              s[x][n][2 + e] = cs::ex2_approx(fmaf(s[x][n][2 + e], unit[n][e], sub));
-              l[n][e] += s[x][n][e] + s[x][n][2 + e];
+              pt[x][n][0] = transposed(Pair<__half>::put(s[x][n][0], s[x][n][1]));
+              pt[x][n][1] = transposed(Pair<__half>::put(s[x][n][2], s[x][n][3]));
             }
           }
 #pragma unroll
           for (int x = 0; x < XS; ++x) {
-            pt[x][n][0] = transposed(Pair<__half>::put(s[x][n][0], s[x][n][1]));
-            pt[x][n][1] = transposed(Pair<__half>::put(s[x][n][2], s[x][n][3]));
+            // V: words of keys key1, key2, key1 + 8 and key2 + 8 of the run
+            uint32_t v[4][VW];
+#pragma unroll
+            for (int y = 0; y < 4; ++y) {
+              const int of = y & 1 ? key2 : key1, j = (x0 + x) * 16 + of + 8 * (y >> 1);
+              const uint8_t* row = st.codes[1][j] + (D == 128 ? (((gq >> 1) ^ turn(of)) * 16 + (gq & 1) * 8) : gq * 4);
+              if constexpr (D == 128)
+                *reinterpret_cast<uint2*>(v[y]) = *reinterpret_cast<const uint2*>(row);
+              else
+                v[y][0] = *reinterpret_cast<const uint32_t*>(row);
+            }
+            const FourScaled fa(sv[x][0]), fb(sv[x][1]);
+#pragma unroll
+            for (int w = 0; w < VW; ++w) {
+              uint32_t a0[4], a1[4], a2[4], a3[4];  // even and odd dimensions of keys key1, key2; of those 8 behind
+              fa.pairs<BIG>(__byte_perm(v[0][w], v[1][w], 0x5410), a0);
+              fa.pairs<BIG>(__byte_perm(v[0][w], v[1][w], 0x7632), a1);
+              fb.pairs<BIG>(__byte_perm(v[2][w], v[3][w], 0x5410), a2);
+              fb.pairs<BIG>(__byte_perm(v[2][w], v[3][w], 0x7632), a3);
+#pragma unroll
+              for (int i = 0; i < 4; ++i)
+#pragma unroll
+                for (int n = 0; n < NT; ++n) mma16816<__half>(o[n][4 * w + i], a0[i], a1[i], a2[i], a3[i], pt[x][n][0], pt[x][n][1]);
+            }
           }
-        }
-#pragma unroll
-        for (int x = 0; x < XS; ++x) {
-          // V: words of keys key1, key2, key1 + 8 and key2 + 8 of the run
-          uint32_t v[4][VW];
-#pragma unroll
-          for (int y = 0; y < 4; ++y) {
-            const int of = y & 1 ? key2 : key1, j = (x0 + x) * 16 + of + 8 * (y >> 1);
-            const uint8_t* row = st.codes[1][j] + (D == 128 ? (((gq >> 1) ^ turn(of)) * 16 + (gq & 1) * 8) : gq * 4);
-            if constexpr (D == 128)
-              *reinterpret_cast<uint2*>(v[y]) = *reinterpret_cast<const uint2*>(row);
-            else
-              v[y][0] = *reinterpret_cast<const uint32_t*>(row);
-          }
-          const FourScaled fa(sv[x][0]), fb(sv[x][1]);
-#pragma unroll
-          for (int w = 0; w < VW; ++w) {
-            uint32_t a0[4], a1[4], a2[4], a3[4];  // even and odd dimensions of keys key1, key2; of those 8 behind
-            fa.pairs<BIG>(__byte_perm(v[0][w], v[1][w], 0x5410), a0);
-            fa.pairs<BIG>(__byte_perm(v[0][w], v[1][w], 0x7632), a1);
-            fb.pairs<BIG>(__byte_perm(v[2][w], v[3][w], 0x5410), a2);
-            fb.pairs<BIG>(__byte_perm(v[2][w], v[3][w], 0x7632), a3);
-#pragma unroll
-            for (int i = 0; i < 4; ++i)
-#pragma unroll
-              for (int n = 0; n < NT; ++n) mma16816<__half>(o[n][4 * w + i], a0[i], a1[i], a2[i], a3[i], pt[x][n][0], pt[x][n][1]);
-          }
-        }
         };
         if (__builtin_expect(__any_sync(0xFFFFFFFFu, big), 0))
           keys(std::true_type());
