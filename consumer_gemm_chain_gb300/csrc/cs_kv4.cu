@@ -7,7 +7,7 @@
 
 namespace {
 
-static_assert(cskv::ROWS4_CTAS<1> <= kRowsCtas && cskv::ROWS4_CTAS<2> <= kRowsCtas, "counters and pieces");
+static_assert(cskv::ROWS4_CTAS<64, 1> <= kRowsCtas && cskv::ROWS4_CTAS<128, 1> <= kRowsCtas, "counters and pieces");
 
 long long code_bytes(const cs_kv_desc& d) {
   return static_cast<long long>(d.num_pages) * d.page_size * d.kv_heads * d.head_dim / 2;
@@ -43,7 +43,7 @@ template <typename T, int D>
 Kernels kernels_of(const cs_kv_s* p, int max_rows) {
   const bool window = p->d.window > 0 && p->d.window < kMaxKeys, narrow = max_rows <= 8;
   Kernels u;
-  u.rows_grid = p->num_sms * (narrow ? cskv::ROWS4_CTAS<1> : cskv::ROWS4_CTAS<2>);
+  u.rows_grid = p->num_sms * (narrow ? cskv::ROWS4_CTAS<D, 1> : cskv::ROWS4_CTAS<D, 2>);
   // with the heads' rows side by side, and at least eight CTAs for each, by heads
   const bool by_head = p->d.cache_layout == CS_KV_TOKEN && p->d.kv_heads > 1 && u.rows_grid >= 8 * p->d.kv_heads;
   u.head_ctas = by_head ? u.rows_grid / p->d.kv_heads : 0;

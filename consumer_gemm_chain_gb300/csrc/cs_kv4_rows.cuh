@@ -35,9 +35,11 @@
 
 namespace cskv {
 
-// Per SM: as many CTAs of four warps as registers allow with 8 (16) columns.
-template <int NT>
-constexpr int ROWS4_CTAS = NT == 1 ? 4 : 3;
+// CTAs of four warps per SM.  Three leave a thread 168 registers, four 128, into which 8 columns just fit; at 128 dimensions
+// independent work is worth more than warps (64 sequences of 16000 keys 247 us with three, 261 with four), at 64 it
+// is not (182 and 171).
+template <int D, int NT>
+constexpr int ROWS4_CTAS = D == 64 && NT == 1 ? 4 : 3;
 
 constexpr int ROWS4_SHIFT = 7;  // keys of a tile: 128, two runs of 16 for each warp, 64 apart
 
@@ -151,7 +153,7 @@ __device__ __forceinline__ void join4(const AttnP& p, const Seg& g, int first, i
 
 // NT: groups of 8 rows
 template <typename T, int D, int NT, bool BY_HEAD>
-__global__ void __launch_bounds__(ROWS_THREADS, ROWS4_CTAS<NT>) cs_kv4_rows_kernel(const __grid_constant__ AttnP p) {
+__global__ void __launch_bounds__(ROWS_THREADS, ROWS4_CTAS<D, NT>) cs_kv4_rows_kernel(const __grid_constant__ AttnP p) {
   extern __shared__ __align__(1024) uint8_t rows_smem[];
   Rows4Shared<D>& sm = *reinterpret_cast<Rows4Shared<D>*>(rows_smem);
   constexpr int ST = Rows4Shared<D>::STAGES;
