@@ -129,16 +129,6 @@ void fill_places(const cs_kv_s* p, const cs_kv_batch* b, const cs_kv4_cache& k, 
   f.head_shift = p->d.head_dim == 128 ? 4 : 3;
 }
 
-// (The products of a block's units fit 32 bits: several tokens a block have some thousands together, one has up to
-// 2 x 1024 x 16.)
-void set_units(cskv::Four4P& f, int units, int q_units) {
-  auto reciprocal = [](uint32_t n) { return n < 2 ? 0u : static_cast<uint32_t>(((1ull << 32) + n - 1) / n); };
-  f.units = units;
-  f.per_unit = reciprocal(units);
-  f.q_units = q_units;
-  f.per_q_unit = reciprocal(q_units);
-}
-
 cs_status check_append4(const cs_kv_s* p, const cs_kv_batch* b, const cs_kv4_append_args* a, cskv::Four4P& f) {
   if (!a) return cs_fail(CS_ERR_INVALID_ARG, "args is NULL");
   const cs_kv_desc& d = p->d;
@@ -164,24 +154,26 @@ cs_status check_append4(const cs_kv_s* p, const cs_kv_batch* b, const cs_kv4_app
   f.rope_rows = a->rope_rows;
   f.rotary_dim = d.rotary_dim;
   f.half = d.rotary_pairing == CS_KV_HALF;
-  set_units(f, 2 * d.kv_heads * f.head_chunks, d.heads * (f.head_chunks / 2));
+  f.units = 2 * d.kv_heads * f.head_chunks;
+  f.q_units = d.heads * (f.head_chunks / 2);
   return CS_OK;
 }
 
-// The rule of run_append (cs_kv.cu): several tokens a block once there are two blocks an SM, up to some
-// rounds of its threads.
-cs_status run_places(const cs_kv_s* p, const void* fn, cskv::Four4P& f, int rounds, cudaStream_t st) {
+// A token's values are shared out to eight warps, or fewer once there are more than eight times as many of them as the SMs hold: each
+// of a token's warps looks its place up.
+cs_status run_places(const cs_kv_s* p, const void* fn, cskv::Four4P& f, cudaStream_t st) {
   if (f.b.tokens == 0 || f.b.seqs == 0) return CS_OK;
-  const int wanted = std::min(f.b.tokens / (2 * p->num_sms), rounds * cskv::FOUR_THREADS / static_cast<int>(f.units + f.q_units));
-  f.tokens_per_block = std::max(1, std::min(wanted, cskv::FOUR_MAX_TOKENS));
-  const dim3 grid((f.b.tokens + f.tokens_per_block - 1) / f.tokens_per_block);
+  constexpr int WARPS = cskv::FOUR_THREADS / 32;
+  f.warps_shift = 3;
+  while (f.warps_shift > 0 && (static_cast<long long>(f.b.tokens) << f.warps_shift) > 8ll * 48 * p->num_sms) --f.warps_shift;
+  const dim3 grid(static_cast<unsigned>(((static_cast<long long>(f.b.tokens) << f.warps_shift) + WARPS - 1) / WARPS));
   return launch(fn, grid, cskv::FOUR_THREADS, 0, &f, st);
 }
 
 cs_status run_append4(const cs_kv_s* p, cskv::Four4P& f, cudaStream_t st) {
   const void* fn = p->d.dtype == CS_BF16 ? (const void*)cskv::cs_kv4_append_kernel<__nv_bfloat16>
                                          : (const void*)cskv::cs_kv4_append_kernel<__half>;
-  return run_places(p, fn, f, 5, st);
+  return run_places(p, fn, f, st);
 }
 
 cs_status check_read4(const cs_kv_s* p, const cs_kv_batch* b, const cs_kv4_read_args* a, cskv::Four4P& f) {
@@ -209,7 +201,7 @@ cs_status check_read4(const cs_kv_s* p, const cs_kv_batch* b, const cs_kv4_read_
   f.k_stride >>= 3;
   f.v_stride >>= 3;
   f.wide = ((reinterpret_cast<uintptr_t>(a->k_out) | reinterpret_cast<uintptr_t>(a->v_out)) % 32 == 0) && (f.k_stride | f.v_stride) % 2 == 0;
-  set_units(f, ((a->k_out ? 1 : 0) + (a->v_out ? 1 : 0)) * d.kv_heads * (f.head_chunks / 2), 0);
+  f.units = ((a->k_out ? 1 : 0) + (a->v_out ? 1 : 0)) * d.kv_heads * (f.head_chunks / 2);
   return CS_OK;
 }
 
@@ -236,7 +228,7 @@ cs_status cs_kv4_read(cs_kv_t p, const cs_kv_batch* b, const cs_kv4_read_args* a
   if (!g.ok) return cs_fail(CS_ERR_CUDA, "cannot select the plan's device");
   const void* fn = p->d.dtype == CS_BF16 ? (const void*)cskv::cs_kv4_read_kernel<__nv_bfloat16>
                                          : (const void*)cskv::cs_kv4_read_kernel<__half>;
-  return run_places(p, fn, f, 3, static_cast<cudaStream_t>(stream));
+  return run_places(p, fn, f, static_cast<cudaStream_t>(stream));
 }
 
 cs_status cs_kv4_attention(cs_kv_t p, const cs_kv_batch* b, const cs_kv4_attn_args* a, void* stream) {
