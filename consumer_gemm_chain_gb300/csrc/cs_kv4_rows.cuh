@@ -19,15 +19,15 @@
 // Row r of S^T's 8-row half is key r / 2 (r even) or 7 - r / 2 (r odd) of 8: with it all reads
 // of the codes from shared memory are free of bank conflicts.
 //
-// Bound.  Instructions: 350 for 16 keys of 128 dimensions and a warp, about half of them to make operands of codes,
-// at 2.4 of 4 a cycle (shifts, masks and byte selections, at half a warp a cycle and scheduler, keep their pipe busy in
-// 54 % of the cycles, DRAM is at 54 %).  64 single tokens over 300 to 32000 keys, 64 / 8 heads of 128 (1.13 GB):
-// 260 us, 4.3 TB/s, 0.64 of a plain copy's measured 6.8; the 16-bit cache (4.26 GB) takes 664 to 692.  256000 keys of
-// 8 heads: 80 us from L2, 81 from DRAM.  One user's token over 978 keys, 12 heads: 9.3 us, the latency of
-// its steps, as over the 16-bit cache; over 16000 keys, 8 heads: 29.5.  128 tokens under a window of 1024,
-// 40 / 8 heads of 64: 37.5 us, of which the start of a launch, its division and its last joins are about 13.
-// Slower or no faster: items' first copies sent off while the item before is stored (81 and 81 us), runs one by one in half
-// the code (84), right shifts as products' upper halves (96), prefetches of whole lines, two CTAs an SM with 16 columns.
+// Bound.  Instructions: 350 for 16 keys of 128 dimensions and a warp, about half of them to make operands of codes, at
+// 2.3 of 4 a cycle (the pipe of shifts, masks and byte selections is busy in 47 % of the cycles, DRAM in 54 %).
+// 62 single tokens over 300 to 32000 keys, 64 / 8 heads of 128 (1.13 GB): 243 us, 4.7 TB/s, 0.69 of a plain copy's
+// measured 6.8; the 16-bit cache (4.26 GB) takes 664 to 692.  128 tokens under a window of 1024, 40 / 8 heads of 64:
+// 37.5 us, of which the start of a launch, its division and its last joins are about 13.  One user's token over 978
+// keys, 12 heads: 9.1 us, the latency of its steps, as over the 16-bit cache; over 16000 keys, 8 heads: 25.5.
+// Slower or no faster: items' first copies sent off while the item before is stored (81 and 81 us for 256000 keys), runs
+// one by one in half the code (84), right shifts as products' upper halves (96), prefetches of whole lines, five
+// CTAs an SM (98), two with 16 columns (118 and 114).
 #pragma once
 #include <cfloat>
 
