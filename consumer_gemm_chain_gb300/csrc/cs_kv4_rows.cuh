@@ -19,7 +19,7 @@
 // Row r of S^T's 8-row half is key r / 2 (r even) or 7 - r / 2 (r odd) of 8: with it all reads
 // of the codes from shared memory are free of bank conflicts.
 //
-// Bound.  Instructions: 350 for 16 keys of 128 dimensions and a warp, about half of them to make operands of codes, at
+// Bound.  Instructions: 318 for 16 keys of 128 dimensions and a warp, about half of them to make operands of codes, at
 // 2.3 of 4 a cycle (the pipe of shifts, masks and byte selections is busy in 47 % of the cycles, DRAM in 54 %).
 // 62 single tokens over 300 to 32000 keys, 64 / 8 heads of 128 (1.13 GB): 243 us, 4.7 TB/s, 0.69 of a plain copy's
 // measured 6.8; the 16-bit cache (4.26 GB) takes 664 to 692.  128 tokens under a window of 1024, 40 / 8 heads of 64:
