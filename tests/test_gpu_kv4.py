@@ -148,6 +148,14 @@ def test_whole_items(lens):
     d.check(rows)
 
 
+@pytest.mark.parametrize("heads,kv_heads,num_sms", [(14, 7, 0), (14, 7, 15), (64, 64, 20), (64, 32, 0), (9, 3, 6)])
+@pytest.mark.parametrize("q,kv", [([1] * 3, [700, 5, 1300]), ([1] * 35, [9 * i + 1 for i in range(35)]), ([2, 0, 1], [400, 9, 90])])
+def test_division_by_heads(heads, kv_heads, num_sms, q, kv):
+    """Key heads that share the CTAs out evenly, with some left over, and more heads than CTAs."""
+    for head_dim, dtype in ((64, BF16), (128, F16)):
+        run(Batch4(q, kv, heads, kv_heads, head_dim, dtype, seed=heads), num_sms=num_sms)
+
+
 @pytest.mark.parametrize("prefix", [1, 16, 127, 500, 2049])
 @pytest.mark.parametrize("q,kv", [([1] * 5, [1, 40, 130, 2, 16]), ([1, 0, 3], [9, 0, 3]), ([40, 1, 70], [40, 300, 75]), ([2], [1])])
 def test_shared_prefix(prefix, q, kv):

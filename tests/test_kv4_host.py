@@ -76,6 +76,23 @@ def test_quantising_against_search():
         assert o4.quantise(np.full(32, 7 * (o4.SCALES[b] + o4.SCALES[b + 1]) / 2))[1][0] == b + (b & 1)
 
 
+def test_rounding_by_sums():
+    """The kernel's quotients, in the same steps: x times the rounded reciprocal plus 192 (one rounding), plus 1.5 2^23 + 8 - 192.
+    Every scale against every value of both types that it can meet."""
+    f = np.float32
+    values = {16: np.arange(0x7C00, dtype=np.uint16).view(np.float16).astype(np.float64),
+              8: (np.arange(0x7F80, dtype=np.uint32) << 16).view(np.float32).astype(np.float64)}
+    for byte in range(1, 0xF8):
+        s = o4.SCALES[byte]
+        for x in values.values():
+            x = x[x <= 60 * s]
+            x = np.concatenate([x, -x])
+            inv = np.float64(f(1) / f(s))
+            r = (x * inv + 192.0).astype(f) + f(12582728)  # (the product and sum fit 53 bits)
+            code = np.clip(r, f(12582913), f(12582927)).view(np.uint32) & 15
+            assert np.array_equal(code, np.clip(np.rint(x / s), -7, 7) + 8)
+
+
 def test_the_stated_error():
     g = np.random.default_rng(1)
     x = g.standard_normal((2000, 32)) * 2.0 ** g.uniform(-11, 15, (2000, 1))
