@@ -40,9 +40,8 @@ __device__ __forceinline__ float2 four_pair(const uint8_t* codes, const uint8_t*
   return make_float2(s * (static_cast<int>(w & 15u) - 8), s * (static_cast<int>(w >> 16 & 15u) - 8));
 }
 
-// One scale twice, and two scales, as halves (products, because the pipe of shifts is the busy one).
+// One scale twice, as halves (a product, because the pipe of shifts is the busy one).
 __device__ __forceinline__ uint32_t scale_pair(uint32_t byte) { return byte * 0x00800080u; }
-__device__ __forceinline__ uint32_t scale_pair(uint32_t low, uint32_t high) { return high * 0x00800000u + low * 0x80u; }
 
 // (w & mask) | bits, in one instruction (the compiler makes two of it, with an immediate each).
 __device__ __forceinline__ uint32_t masked(uint32_t w, uint32_t mask, uint32_t bits) {

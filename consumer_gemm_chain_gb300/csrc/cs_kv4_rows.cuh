@@ -25,9 +25,10 @@
 // measured 6.8; the 16-bit cache (4.26 GB) takes 664 to 692.  128 tokens under a window of 1024, 40 / 8 heads of 64:
 // 37.5 us, of which the start of a launch, its division and its last joins are about 13.  One user's token over 978
 // keys, 12 heads: 9.1 us, the latency of its steps, as over the 16-bit cache; over 16000 keys, 8 heads: 25.5.
-// Slower or no faster: items' first copies sent off while the item before is stored (81 and 81 us for 256000 keys), runs
-// one by one in half the code (84), right shifts as products' upper halves (96), prefetches of whole lines, five
-// CTAs an SM (98), two with 16 columns (118 and 114).
+// Slower or no faster: the next keys' scores before the softmax of these (267 us for 64 sequences of 16000 keys instead
+// of 243), leaving out runs that no row sees (251), items' first copies sent off while the item before is stored (81
+// and 81 us for 256000 keys), runs one by one in half the code (84), right shifts as products' upper halves (96),
+// prefetches of whole lines, five CTAs an SM (98), two with 16 columns (118 and 114).
 #pragma once
 #include <cfloat>
 
