@@ -109,12 +109,13 @@ struct Four<__nv_bfloat16> {
   }
 };
 
-// Operands of products in f16, whatever the cache's type is: values times 2^-7, numbers of f16 for all scales (from
+// Operands of products in f16, of keys whatever the cache's type is: values times 2^-7, numbers of f16 for all scales (from
 // 2^-24 on).  Code bits under the exponent of 1024 are 1024 + (c + 8), those of the next four 64 + (c + 8) under the
 // exponent of 64, and one multiply-add makes either a value: 1032 s and 72 s have at most 11 significant
 // bits.  Only where 1032 s overflows (BIG: bytes from 0xE0 on, values of some 55000) c is made first.
 struct FourScaled {
   static constexpr uint32_t BIG_BYTE = 0xE0;
+  static constexpr bool HAS_BIG = true;
   __half2 s, low, high;
   __device__ __forceinline__ explicit FourScaled(uint32_t bits) {
     const uint32_t unit = 0x20002000u, lo = 0xE408E408u, hi = 0xD480D480u;  // 2^-7, -1032, -72
@@ -140,5 +141,41 @@ struct FourScaled {
   }
 };
 constexpr float FOUR_UNIT = 0.0078125f;
+
+// The same values as operands of products in bf16.  The f16 number 1024 + u has u in its lowest bits, and the same
+// bits are 2^66 (128 + u) in bf16: one multiply-add makes it s c 2^-7, 136 s having 8 significant bits.  The second code of a
+// byte is 64 + u in f16 after the mask, and a sum there (+ 960) puts it in place: the pipe of shifts is the busy one
+// (with a shift for each of three codes 64 sequences of 16000 keys took 248 us, so 244).
+struct FourScaledBf16 {
+  static constexpr bool HAS_BIG = false;
+  __nv_bfloat162 s, off;
+  __device__ __forceinline__ explicit FourScaledBf16(uint32_t bits) {
+    const uint32_t unit = 0x1B001B00u, bias = 0xE408E408u;  // 2^-73, -136 2^66
+    const __nv_bfloat162 h = __float22bfloat162_rn(__half22float2(*reinterpret_cast<__half2*>(&bits)));
+    s = __hmul2(h, *reinterpret_cast<const __nv_bfloat162*>(&unit));
+    off = __hmul2(s, *reinterpret_cast<const __nv_bfloat162*>(&bias));
+  }
+  __device__ __forceinline__ uint32_t value(uint32_t x) const {
+    const __nv_bfloat162 y = __hfma2(*reinterpret_cast<const __nv_bfloat162*>(&x), s, off);
+    return *reinterpret_cast<const uint32_t*>(&y);
+  }
+  __device__ __forceinline__ uint32_t high(uint32_t w) const {
+    const uint32_t x = masked(w, 0x00F000F0u, 0x54005400u), up = 0x63806380u;  // 960
+    const __half2 y = __hadd2(*reinterpret_cast<const __half2*>(&x), *reinterpret_cast<const __half2*>(&up));
+    return value(*reinterpret_cast<const uint32_t*>(&y));
+  }
+  // the four pairs of a word
+  template <bool>
+  __device__ __forceinline__ void pairs(uint32_t w, uint32_t (&x)[4]) const {
+    const uint32_t v = w >> 8;
+    x[0] = value(masked(w, 0x000F000Fu, 0x64006400u));
+    x[1] = high(w);
+    x[2] = value(masked(v, 0x000F000Fu, 0x64006400u));
+    x[3] = high(v);
+  }
+};
+
+template <typename T>
+using OperandsOf = std::conditional_t<std::is_same<T, __half>::value, FourScaled, FourScaledBf16>;
 
 }  // namespace cskv

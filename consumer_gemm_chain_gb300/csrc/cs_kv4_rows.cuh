@@ -11,10 +11,12 @@
 // A lane (g, t) of S^T's first operand has 32 (16) consecutive dimensions of two keys, under one
 // scale each; of V^T's it has 16 (8) dimensions of four keys: two keys' words, taken apart in
 // 16-bit halves and put together by dimension, make pairs along the keys.  P^T is the second operand of O^T:
-// an 8 x 8 transposition of S^T's accumulators (movmatrix).  All operands are f16, whatever the
-// cache's type is: a code is then a value after a mask and a multiply-add (FourScaled; bf16 takes more
-// shifts), values times 2^-7 are f16 numbers for every scale, queries of bf16 are put to f16's range row by row, and
-// weights are rounded to 11 bits instead of 8.
+// an 8 x 8 transposition of S^T's accumulators (movmatrix).  The scores' operands are f16, whatever the
+// cache's type is: a code is then a value after a mask and a multiply-add (FourScaled), values times 2^-7 are f16 numbers
+// for every scale, and queries of bf16 are put to f16's range row by row.  The weights and V are of the cache's type:
+// beside a key that takes nearly all the weight and whose value is about 0 (an attention sink) the others are the
+// output, and f16 has no bits for weights below 2^-25 of the largest.  (With f16 for both types 64 sequences of 16000 keys
+// took 239 us, now 244; 16000 keys 18 nats below one of value 0 on one SM lost those of that key's warp, 8 % of the output.)
 //
 // Row r of S^T's 8-row half is key r / 2 (r even) or 7 - r / 2 (r odd) of 8: with it all reads
 // of the codes from shared memory are free of bank conflicts.
@@ -43,6 +45,10 @@ template <int D, int NT>
 constexpr int ROWS4_CTAS = D == 64 && NT == 1 ? 4 : 3;
 
 constexpr int ROWS4_SHIFT = 7;  // keys of a tile: 128, two runs of 16 for each warp, 64 apart
+
+// A row's reference lies 2^7 below a score of its own, so its weights are at most 2^15: as far from f16's end as that
+// goes, and 2^7 more of what f16 has at its other end.
+constexpr float WEIGHT_LOG2 = 7.0f;
 
 template <int D>
 struct Stage4 {  // a warp's keys of a tile: codes of K and V, their scales
@@ -279,6 +285,7 @@ __global__ void __launch_bounds__(ROWS_THREADS, ROWS4_CTAS<D, NT>) cs_kv4_rows_k
 #pragma unroll
         for (int c = 0; c < 4; ++c) o[n][i][c] = 0.0f;
     float m_ref[NT][2], l[NT][2];  // of a row: the reference (of scores times unit) and the sum
+    using Values = OperandsOf<T>;
 #pragma unroll
     for (int n = 0; n < NT; ++n)
 #pragma unroll
@@ -318,7 +325,8 @@ __global__ void __launch_bounds__(ROWS_THREADS, ROWS4_CTAS<D, NT>) cs_kv4_rows_k
           sk[x] = k1 * 0x10000u + k0;
           sv[x][0] = v01 * 0x80u;
           sv[x][1] = v23 * 0x80u;
-          most = __vmaxu2(most, __vmaxu2(sk[x], __vmaxu2(v01, v23)));
+          most = __vmaxu2(most, sk[x]);
+          if (Values::HAS_BIG) most = __vmaxu2(most, __vmaxu2(v01, v23));
         }
         const bool big = (most + (0x100u - FourScaled::BIG_BYTE) * 0x10001u & 0x01000100u) != 0;
         auto keys = [&](auto is_big) {
@@ -367,7 +375,7 @@ __global__ void __launch_bounds__(ROWS_THREADS, ROWS4_CTAS<D, NT>) cs_kv4_rows_k
               top[n][e] = fmaxf(s[0][n][e], s[0][n][2 + e]);
               if (XS == 2) top[n][e] = max3(top[n][e], s[XS - 1][n][e], s[XS - 1][n][2 + e]);
               // raised only when it is exceeded by more than 2^8 (from -infinity by anything but that)
-              raise |= fmaf(top[n][e], unit[n][e], -m_ref[n][e]) > RAISE_LOG2;
+              raise |= fmaf(top[n][e], unit[n][e], -m_ref[n][e]) > RAISE_LOG2 + WEIGHT_LOG2;
             }
           if (__any_sync(0xFFFFFFFFu, raise)) {
 #pragma unroll
@@ -377,8 +385,8 @@ __global__ void __launch_bounds__(ROWS_THREADS, ROWS4_CTAS<D, NT>) cs_kv4_rows_k
                 float m = top[n][e];
 #pragma unroll
                 for (int d = 4; d < 32; d <<= 1) m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, d));
-                if (fmaf(m, unit[n][e], -m_ref[n][e]) > RAISE_LOG2) {
-                  m *= unit[n][e];
+                if (fmaf(m, unit[n][e], -m_ref[n][e]) > RAISE_LOG2 + WEIGHT_LOG2) {
+                  m = fmaf(m, unit[n][e], -WEIGHT_LOG2);
                   const float f = cs::ex2_approx(m_ref[n][e] - m);
                   m_ref[n][e] = m;
                   l[n][e] *= f;
@@ -402,8 +410,8 @@ __global__ void __launch_bounds__(ROWS_THREADS, ROWS4_CTAS<D, NT>) cs_kv4_rows_k
             }
 #pragma unroll
             for (int x = 0; x < XS; ++x) {
-              pt[x][n][0] = transposed(Pair<__half>::put(s[x][n][0], s[x][n][1]));
-              pt[x][n][1] = transposed(Pair<__half>::put(s[x][n][2], s[x][n][3]));
+              pt[x][n][0] = transposed(Pair<T>::put(s[x][n][0], s[x][n][1]));
+              pt[x][n][1] = transposed(Pair<T>::put(s[x][n][2], s[x][n][3]));
             }
           }
 #pragma unroll
@@ -419,18 +427,18 @@ __global__ void __launch_bounds__(ROWS_THREADS, ROWS4_CTAS<D, NT>) cs_kv4_rows_k
               else
                 v[y][0] = *reinterpret_cast<const uint32_t*>(row);
             }
-            const FourScaled fa(sv[x][0]), fb(sv[x][1]);
+            const Values fa(sv[x][0]), fb(sv[x][1]);
 #pragma unroll
             for (int w = 0; w < VW; ++w) {
               uint32_t a0[4], a1[4], a2[4], a3[4];  // even and odd dimensions of keys key1, key2; of those 8 behind
-              fa.pairs<BIG>(__byte_perm(v[0][w], v[1][w], 0x5410), a0);
-              fa.pairs<BIG>(__byte_perm(v[0][w], v[1][w], 0x7632), a1);
-              fb.pairs<BIG>(__byte_perm(v[2][w], v[3][w], 0x5410), a2);
-              fb.pairs<BIG>(__byte_perm(v[2][w], v[3][w], 0x7632), a3);
+              fa.template pairs<BIG>(__byte_perm(v[0][w], v[1][w], 0x5410), a0);
+              fa.template pairs<BIG>(__byte_perm(v[0][w], v[1][w], 0x7632), a1);
+              fb.template pairs<BIG>(__byte_perm(v[2][w], v[3][w], 0x5410), a2);
+              fb.template pairs<BIG>(__byte_perm(v[2][w], v[3][w], 0x7632), a3);
 #pragma unroll
               for (int i = 0; i < 4; ++i)
 #pragma unroll
-                for (int n = 0; n < NT; ++n) mma16816<__half>(o[n][4 * w + i], a0[i], a1[i], a2[i], a3[i], pt[x][n][0], pt[x][n][1]);
+                for (int n = 0; n < NT; ++n) mma16816<T>(o[n][4 * w + i], a0[i], a1[i], a2[i], a3[i], pt[x][n][0], pt[x][n][1]);
             }
           }
         };

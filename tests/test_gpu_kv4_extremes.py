@@ -1,0 +1,70 @@
+"""The paged cache in 4 bits on the GPU where numbers come near the ends of their types."""
+from __future__ import annotations
+
+import numpy as np
+import pytest
+import torch
+
+import consumer_gemm_chain_gb300 as cs
+from kv4_util import parts
+from oracle import kv as okv
+from oracle import kv4 as o4
+
+pytestmark = pytest.mark.gpu
+F16, BF16 = torch.float16, torch.bfloat16
+
+
+def attend(q, k, v, dtype, **desc):
+    """(out, lse) of the last len(q) tokens of one sequence over keys k and values v [keys, key heads, d], held as they are
+    quantised or given as pairs of codes and scales; q [tokens, heads, d].  Pages of 16, TOKEN layout."""
+    tokens, heads, d = q.shape
+    keys, hk = len(k), k.shape[1]
+    pages = -(-keys // 16)
+
+    def cache(x):
+        whole = torch.zeros(pages * 16, hk, d, dtype=torch.float64)
+        whole[:keys] = x
+        return tuple(y.cuda() for y in parts(whole.view(pages, 16, hk, d), "token"))
+
+    plan = cs.cs_kv_plan(cs.cs_kv_desc_init(dtype=dtype, heads=heads, kv_heads=hk, head_dim=d, num_pages=pages, max_tokens=tokens,
+                                            max_seqs=1, **desc))
+    batch = cs.cs_kv_batch(plan, torch.tensor([0, tokens], dtype=torch.int32, device="cuda"),
+                           torch.tensor([keys], dtype=torch.int32, device="cuda"),
+                           torch.arange(pages, dtype=torch.int32, device="cuda")[None], tokens=tokens, max_q=tokens)
+    out = torch.full((tokens, heads, d), 7.0, dtype=dtype, device="cuda")
+    lse = torch.full((tokens, heads), 7.0, device="cuda")
+    cs.cs_kv4_attention(plan, batch, q.to(dtype).cuda(), cache(k), cache(v), out, lse)
+    torch.cuda.synchronize()
+    assert cs.cs_kv_status(plan) == cs.CS_OK
+    return okv.to64(out), okv.to64(lse)
+
+
+# ------------------------------------------------------------------ weights
+@pytest.mark.parametrize("dtype,nats", [(BF16, 12), (BF16, 16), (BF16, 18), (BF16, 30), (BF16, 60), (F16, 10), (F16, 14)])
+@pytest.mark.parametrize("heads,tokens,d", [(8, 1, 128), (8, 1, 64), (16, 1, 128), (4, 4, 64), (4, 40, 128)])
+def test_a_key_of_nearly_all_the_weight_and_value_zero(dtype, nats, heads, tokens, d):
+    """The output is that of thousands of keys whose weights are e^-nats each: as exact as these are, rounded to the dtype.
+
+    One SM, so that a warp has many of the keys beside the one.  u |O| for the output's rounding, u sum(w |v|) for the weights', and 2^-11 sum(w |v|) for their errors from the scores (which
+    are exact but for a factor in 32 bits) and the sums in 32 bits.  In f16 a tile of 128 rows rounds weights to steps of
+    2^-24 of the reference, few rows 2^7 finer: half of one for each key."""
+    if dtype == F16 and tokens == 40:
+        nats -= 6
+    g = torch.Generator().manual_seed(nats)
+    keys = 4000
+    q = torch.zeros(tokens, heads, d, dtype=torch.float64)
+    k, v = torch.zeros(keys, 1, d, dtype=torch.float64), torch.randn(keys, 1, d, generator=g).double()
+    q[..., 1], k[0, 0, 1], v[0] = 4.0, 7.0, 0.0
+    scale = float(np.float32(nats / 28))
+    out, lse = attend(q, k, v, dtype, scale=scale, num_sms=1)
+    held_k, held_v = o4.held(k), o4.held(v)
+    assert held_k[0, 0, 1] == 7.0
+    u = torch.finfo(dtype).eps / 2
+    for t in range(tokens):
+        seen = np.arange(keys) <= keys - tokens + t
+        o, z, a = okv.attend(q[t, 0], held_k[:, 0], held_v[:, 0], seen, scale)
+        bound = u * np.abs(o) + (u + 2.0 ** -11) * a
+        if dtype == F16:
+            bound = bound + keys * 2.0 ** (-25 if tokens == 40 else -32) * np.abs(held_v).max() + 2.0 ** -25
+        assert (np.abs(out[t] - o) <= bound).all(), float((np.abs(out[t] - o) / bound).max())
+        assert np.abs(lse[t] - z).max() <= 2.0 ** -20 * abs(z)
