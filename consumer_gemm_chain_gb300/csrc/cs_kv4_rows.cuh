@@ -267,7 +267,8 @@ __global__ void __launch_bounds__(ROWS_THREADS, ROWS4_CTAS<D, NT>) cs_kv4_rows_k
       }
 #pragma unroll
       for (int e = 0; e < 2; ++e)
-        unit[n][e] = fminf(__shfl_sync(0xFFFFFFFFu, f, 4 * (2 * jq + e)) / FOUR_UNIT * p.scale_log2, FLT_MAX);
+        // (neither infinite nor, for a row of zeros and a small scale, 0: hidden scores are -infinity before it)
+        unit[n][e] = fmaxf(fminf(__shfl_sync(0xFFFFFFFFu, f, 4 * (2 * jq + e)) / FOUR_UNIT * p.scale_log2, FLT_MAX), FLT_MIN);
     }
     // keys below all_end and from all_lo on are seen by every row
     const int all_end = p.c.flat ? g.s.m : base + 1, all_lo = p.c.window > 0 ? max(0, base + tokens - p.c.window) : 0;

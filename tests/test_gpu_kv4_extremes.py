@@ -68,3 +68,32 @@ def test_a_key_of_nearly_all_the_weight_and_value_zero(dtype, nats, heads, token
             bound = bound + keys * 2.0 ** (-25 if tokens == 40 else -32) * np.abs(held_v).max() + 2.0 ** -25
         assert (np.abs(out[t] - o) <= bound).all(), float((np.abs(out[t] - o) / bound).max())
         assert np.abs(lse[t] - z).max() <= 2.0 ** -20 * abs(z)
+
+
+# ------------------------------------------------------------------ scores
+@pytest.mark.parametrize("dtype", [F16, BF16])
+@pytest.mark.parametrize("size", [1.0, 1e4, 1e12, 1e30])
+@pytest.mark.parametrize("heads,tokens", [(8, 1), (8, 3), (8, 40)])
+def test_queries_of_zeros_under_a_small_scale(dtype, size, heads, tokens):
+    """Rows of zeros see all their keys alike, whatever the scale is; beside them are rows of `size`, which the scale undoes.
+    Bounds: u |O|, u sum(w |v|) for the weights, 2^-11 sum(w |v|) for scores (sums of 64 products in 32 bits) and sums."""
+    if dtype == F16 and size > 1e4:
+        size_of_q = 1e4  # (scores of nearly 0)
+    else:
+        size_of_q = size
+    g = torch.Generator().manual_seed(tokens)
+    keys, d = 150, 64
+    q = (torch.randn(tokens, heads, d, generator=g).double() * size_of_q).to(dtype).double()
+    q[:, 1::2] = 0.0
+    q[0, 3] = -0.0
+    k, v = (torch.randn(keys, 2, d, generator=g).double() for _ in range(2))
+    scale = float(np.float32(0.125 / size))
+    out, lse = attend(q, k, v, dtype, scale=scale)
+    held_k, held_v = o4.held(k), o4.held(v)
+    u = torch.finfo(dtype).eps / 2
+    for t in range(tokens):
+        seen = np.arange(keys) <= keys - tokens + t
+        for h in range(heads):
+            o, z, a = okv.attend(q[t, h].numpy(), held_k[:, h // 4], held_v[:, h // 4], seen, scale)
+            assert (np.abs(out[t, h] - o) <= u * np.abs(o) + (u + 2.0 ** -11) * a + 1e-30).all(), (t, h)
+            assert abs(lse[t, h] - z) <= 2.0 ** -11 + 2.0 ** -20 * abs(z)
