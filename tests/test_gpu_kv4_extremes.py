@@ -97,3 +97,43 @@ def test_queries_of_zeros_under_a_small_scale(dtype, size, heads, tokens):
             o, z, a = okv.attend(q[t, h].numpy(), held_k[:, h // 4], held_v[:, h // 4], seen, scale)
             assert (np.abs(out[t, h] - o) <= u * np.abs(o) + (u + 2.0 ** -11) * a + 1e-30).all(), (t, h)
             assert abs(lse[t, h] - z) <= 2.0 ** -11 + 2.0 ** -20 * abs(z)
+
+
+@pytest.mark.parametrize("dtype", [F16, BF16])
+@pytest.mark.parametrize("heads,tokens", [(8, 1), (16, 1), (8, 3)])
+@pytest.mark.parametrize("d", [64, 128])
+def test_scores_that_overflow(dtype, heads, tokens, d):
+    """Scores beyond 32 bits are infinities: a key at -infinity has no weight, a row of them alone gets zeros and an lse of
+    -infinity, and a row with infinity, whose softmax is no number, is NaN: as over a cache in 16 bits."""
+    keys, scale = 300, 1e36
+    q, k = torch.zeros(tokens, heads, d, dtype=torch.float64), torch.zeros(keys, 1, d, dtype=torch.float64)
+    g = torch.Generator().manual_seed(1)
+    v = torch.randn(keys, 1, d, generator=g).double()
+    k[:, 0, 0] = 7.0
+    k[5, 0], k[17, 0] = 0.0, 0.0
+    k[5, 0, 40] = k[17, 0, 40] = 7.0
+    q[..., 0] = -1e3  # -infinity but for two keys, at 0
+    q[:, 1, 40] = -1e3  # everywhere
+    q[:, 2, 0] = 1e3  # infinity
+    out, lse = attend(q, k, v, dtype, scale=scale)
+    held = o4.held(v)[:, 0]
+    u = torch.finfo(dtype).eps / 2
+    want = (held[5] + held[17]) / 2
+    for h in [0] + list(range(3, heads)):
+        assert (np.abs(out[:, h] - want) <= u * np.abs(want) + 2.0 ** -20).all()
+        assert (np.abs(lse[:, h] - np.log(2)) <= 2.0 ** -20).all()
+    assert (out[:, 1] == 0).all() and np.isneginf(lse[:, 1]).all()
+    assert np.isnan(out[:, 2]).all() and np.isnan(lse[:, 2]).all()
+    # the same through a cache in 16 bits
+    plan = cs.cs_kv_plan(cs.cs_kv_desc_init(dtype=dtype, heads=heads, kv_heads=1, head_dim=d, page_size=16, num_pages=19,
+                                            max_tokens=tokens, max_seqs=1, scale=scale))
+    batch = cs.cs_kv_batch(plan, torch.tensor([0, tokens], dtype=torch.int32, device="cuda"), torch.tensor([keys], dtype=torch.int32,
+                           device="cuda"), torch.arange(19, dtype=torch.int32, device="cuda")[None], tokens=tokens, max_q=tokens)
+    kc, vc = (torch.zeros(19 * 16, 1, d, dtype=dtype, device="cuda") for _ in range(2))
+    kc[:keys], vc[:keys] = torch.from_numpy(o4.held(k)).to(dtype).cuda(), torch.from_numpy(o4.held(v)).to(dtype).cuda()
+    out16, lse16 = torch.empty(tokens, heads, d, dtype=dtype, device="cuda"), torch.empty(tokens, heads, device="cuda")
+    cs.cs_kv_attention(plan, batch, q.to(dtype).cuda(), kc.view(19, 16, 1, d), vc.view(19, 16, 1, d), out16, lse16)
+    torch.cuda.synchronize()
+    out16, lse16 = okv.to64(out16), okv.to64(lse16)
+    assert (np.isnan(out16) == np.isnan(out)).all() and (np.isnan(lse16) == np.isnan(lse)).all()
+    assert (out16[:, 1] == 0).all() and (np.isneginf(lse16) == np.isneginf(lse)).all()
