@@ -992,7 +992,8 @@ __device__ __noinline__ void mend_row(const AttnP& p, int t, int h) {
       if (at < 0) continue;
 #pragma unroll
       for (int w = 0; w < W; ++w) {
-        const float2 v = pair_of(p.v_raw, p.v_scales, at, scales, lane + 32 * w);
+        float2 v = pair_of(p.v_raw, p.v_scales, at, scales, lane + 32 * w);
+        if constexpr (FOUR) v = Pair<T>::get(Pair<T>::put(v.x, v.y));  // as make4_role's operands: f16 ends at 65504
         spoilt |= !isfinite(v.x) || !isfinite(v.y);
       }
     }

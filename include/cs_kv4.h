@@ -19,7 +19,8 @@
  *     NaN (infinite scales make infinite values or NaN);
  *   32 codes c + 8 of 4 bits, c in -7 .. 7 (-8 is never written, and is read as -8).
  * The value is s c, a number of both 16-bit types: reading rounds nothing.  (Caches that are
- * not written here may hold values beyond f16's 65504; a plan of that type may give infinities for them.)
+ * not written here may hold values beyond f16's 65504; a plan of that type may give infinities, or NaN, for them and
+ * to rows that see them.)
  * Written: s = the scale nearest to max |x| / 7 (ties to the even byte), c = x / s rounded to
  * the nearest (ties to even), within -7 .. 7, where x is what cs_kv_append would
  * have stored.  So |x - s c| <= 0.54 s while 2^-14 <= max |x| / 7 <= 61440; below, the

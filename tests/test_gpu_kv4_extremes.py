@@ -6,9 +6,10 @@ import pytest
 import torch
 
 import consumer_gemm_chain_gb300 as cs
-from kv4_util import parts
+from kv4_util import Batch4, parts
 from oracle import kv as okv
 from oracle import kv4 as o4
+from test_gpu_kv4 import Device
 
 pytestmark = pytest.mark.gpu
 F16, BF16 = torch.float16, torch.bfloat16
@@ -137,3 +138,41 @@ def test_scores_that_overflow(dtype, heads, tokens, d):
     out16, lse16 = okv.to64(out16), okv.to64(lse16)
     assert (np.isnan(out16) == np.isnan(out)).all() and (np.isnan(lse16) == np.isnan(lse)).all()
     assert (out16[:, 1] == 0).all() and (np.isneginf(lse16) == np.isneginf(lse)).all()
+
+
+# ------------------------------------------------------------------ values
+@pytest.mark.parametrize("q,kv", [([4, 1], [70, 9]), ([6], [300]), ([200, 30], [300, 30]), ([130], [2000])])
+@pytest.mark.parametrize("head_dim", [64, 128])
+@pytest.mark.parametrize("window,prefix", [(0, 0), (33, 0), (0, 50)])
+def test_values_beyond_f16_at_keys_hidden_from_some_rows(q, kv, head_dim, window, prefix):
+    """A plan of f16 over values that only a bf16 one writes, 7 times the largest scale, at keys that only the last token (or, under a
+    window, only the first ones) see: every other row is as if they were not there, and rows that see one are infinite, no
+    number, or right, in the group's dimensions, and right elsewhere."""
+    b = Batch4(q, kv, 8, 2, head_dim, F16, window=window, sinks=2 if window else 0, prefix=prefix, seed=kv[0])
+    group, spoilt = head_dim // 32 - 1, []
+    dims = slice(32 * group, 32 * group + 32)
+    for s, (n, m) in enumerate(zip(q, kv)):
+        spoilt.append((s, m - 1))
+        if window and m - n - window + 1 >= 2 and n > 1:
+            spoilt.append((s, m - n - window + 1))
+    for s, j in spoilt:
+        page = int(b.table[s, j // 16])
+        b.v4[1][page, :, j % 16, group] = 0xF7
+        b.v4[0][page, j % 16, :, 16 * group:16 * group + 16] = 0xFF  # codes of 7
+        b.v[s][j, :, dims] = 0.0  # rows that do not see it never read it
+    d = Device(b)
+    for _ in range(2):  # the marks of the first call are cleared
+        d.out.fill_(7), d.lse.fill_(7)
+        d.attend()
+    d.ok()
+    ref, lse, bound = b.reference()
+    got, t = okv.to64(d.out), 0
+    assert np.abs(okv.to64(d.lse) - lse).max() <= 2.0 ** -11 + 2.0 ** -20 * np.abs(lse).max()
+    for s, (n, m) in enumerate(zip(q, kv)):
+        for i in range(n):
+            p = m - n + i
+            hit = any(x == s and j <= p and (not window or j > p - window) for x, j in spoilt)
+            ok = np.ones(head_dim, dtype=bool)
+            ok[dims] = not hit
+            assert (np.abs(got[t, :, ok] - ref[t, :, ok]) <= bound[t, :, ok]).all(), (s, i)
+            t += 1
