@@ -387,11 +387,12 @@ __global__ void __launch_bounds__(ROWS_THREADS, ROWS4_CTAS<D, NT>) cs_kv4_rows_k
 #pragma unroll
                 for (int d = 4; d < 32; d <<= 1) m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, d));
                 m = fmaf(m, unit[n][e], -WEIGHT_LOG2);
-                // scores that overflow: -infinity raises nothing (it is like a hidden key), and with infinity the sum is NaN
+                // (scores that overflow: -infinity raises nothing, as a hidden key; a reference of infinity makes the row NaN
+                // when the warps' states are joined)
                 if (m - m_ref[n][e] > RAISE_LOG2) {
                   const float f = cs::ex2_approx(m_ref[n][e] - m);
                   m_ref[n][e] = m;
-                  l[n][e] = fmaf(l[n][e], f, m - m);
+                  l[n][e] *= f;
 #pragma unroll
                   for (int i = 0; i < 4 * VW; ++i) o[n][i][e] *= f, o[n][i][2 + e] *= f;
                 }
