@@ -115,6 +115,7 @@ Kernels kernels(const cs_kv_s* p) {
   u.rows_shift = cskv::ROWS_SHIFT;
   u.head_ctas = 0;
   u.least = 1;
+  u.uncut = 0;
   u.spare = 0;
   u.rows_smem = rows_smem(p->d);
   u.rows_map = &p->slots_map;

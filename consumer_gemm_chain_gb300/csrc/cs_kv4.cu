@@ -53,10 +53,13 @@ Kernels kernels_of(const cs_kv_s* p, int max_rows) {
   // Ranges of one, two and four tiles at least: one token over 16000 keys 35.8, 34.4 and 31.0 us, 128 of them over 100
   // keys 19.9, 20.0 and 23.1.
   u.least = 2;
-  // Whole items save the pieces' stores and joins.  Measured, cut and whole, 32 / 8 heads of 128: 128 sequences of 500 keys
-  // (1.6 tiles more on the longest CTA) 38.3 and 33.4 us, 256 of them (3.2) 60.0 and 61.9, 64 of 2000 keys (2.7)
-  // 53.5 and 50.6, 128 of them (5.4) 86.0 and 90.0; 40 / 8 heads of 64, 1024 keys: 128 sequences (3.2) 41.2 and
-  // 38.5, 256 (6.3) 67.7 and 71.2.
+  // Whole items save the pieces' stores and joins, and load the CTAs less evenly.  Measured, whole and cut, 32 / 8 heads of 128,
+  // keys of each sequence between the numbers given: 57 sequences (a CTA each) 1..500 16.7 and 18.0 us, 250..500 19.8 and
+  // 19.8, 1..760 18.7 and 20.8, 380..760 24.7 and 23.0, 510..1020 28.5 and 24.9, one of 1020 beside 1..100 14.6 and 12.4, one of
+  // 32000 beside 500 277 and 30; 114 of them 1..500 25.7 and 26.2, 250..500 29.7 and 29.2, 510..1020 43.5 and 40.8; 6
+  // sequences of 250 7.2 and 8.7, 50 of 250..500 14.4 and 18.3.  40 / 8 heads of 64, 76 sequences: 1..500 15.3 and 16.4, 510..1020
+  // 26.6 and 23.6.  So up to four tiles, where whole costs at most 2 %.
+  u.uncut = 4;
   u.spare = 3;
   u.rows_shift = cskv::ROWS4_SHIFT;
   u.rows_smem = sizeof(cskv::Rows4Shared<D>);

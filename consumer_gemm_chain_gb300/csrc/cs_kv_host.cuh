@@ -311,12 +311,25 @@ inline cs_status map_caches(cskv::AttnP& k, const CUtensorMap& like) {
 // The kernels of a call with at most `max_rows` rows per key head, and the maps of their caches' copies.
 struct Kernels {
   const void *rows, *attn, *join;
-  // few rows: keys of a tile; CTAs of a key head where items go by heads, or 0; fewest units of a CTA; how many
-  // tiles more a CTA may get so that items stay whole
-  int rows_shift, head_ctas, least, spare;
+  // few rows: keys of a tile; CTAs of a key head where items go by heads, or 0; fewest units of a CTA; items of up to
+  // `uncut` tiles stay whole if that gives a CTA up to `spare` tiles more
+  int rows_shift, head_ctas, least, uncut, spare;
   int rows_grid, rows_smem, attn_smem, attn_threads;
   const CUtensorMap *rows_map, *attn_map;  // nullptr: read through pointers
 };
+
+// Few rows: do items stay whole?  With as many tiles as the page table (or the window) lets an item have, and one a
+// sequence and head: the longest CTA's tiles against those of equal ranges.  That says nothing of batches of long and short
+// items, where a CTA may get nearly an item's tiles more than an equal range, so items that may be long are cut.
+inline bool rows_uncut(const cskv::AttnP& k, const Kernels& use, const cs_kv_desc& d) {
+  const int tile = 1 << k.c.shift;
+  long long keys = static_cast<long long>(k.b.table_cols) * d.page_size;
+  if (k.c.window > 0) keys = std::min<long long>(keys, k.c.window + k.c.per_item + tile + (k.c.sinks + tile - 1) / tile * tile);
+  const long long tiles = std::max<long long>(1, (keys + tile - 1) / tile), units = tiles + k.c.item_cost;
+  const long long seqs = std::min(k.b.seqs, k.b.tokens);
+  const long long ctas = use.head_ctas ? use.head_ctas : use.rows_grid, items = use.head_ctas ? seqs : seqs * d.kv_heads;
+  return !k.c.flat && tiles <= use.uncut && (items + ctas - 1) / ctas * units * ctas - items * units <= use.spare * ctas;
+}
 
 inline cs_status run_attention(cs_kv_s* p, cskv::AttnP& k, const Kernels& use, int max_rows, cudaStream_t st) {
   const cs_kv_desc& d = p->d;
@@ -328,16 +341,7 @@ inline cs_status run_attention(cs_kv_s* p, cskv::AttnP& k, const Kernels& use, i
     k.c.shift = use.rows_shift;
     k.c.head_ctas = use.head_ctas;
     k.c.least = use.least;
-    // The longest CTA's tiles with whole items, one a sequence and head and as long as the page table (or the
-    // window) lets it be, against those of equal ranges.
-    if (!k.c.flat && use.spare > 0) {
-      const int tile = 1 << k.c.shift;
-      long long keys = static_cast<long long>(k.b.table_cols) * d.page_size;
-      if (k.c.window > 0) keys = std::min<long long>(keys, k.c.window + k.c.per_item + tile + (k.c.sinks + tile - 1) / tile * tile);
-      const long long units = (keys + tile - 1) / tile + k.c.item_cost, seqs = std::min(k.b.seqs, k.b.tokens);
-      const long long ctas = use.head_ctas ? use.head_ctas : use.rows_grid, items = use.head_ctas ? seqs : seqs * d.kv_heads;
-      k.c.whole = (items + ctas - 1) / ctas * units * ctas - items * units <= use.spare * ctas;
-    }
+    if (rows_uncut(k, use, d)) k.c.whole = 1;
     if (use.rows_map && (s = map_caches(k, *use.rows_map)) != CS_OK) return s;
     s = launch(use.rows, dim3(use.rows_grid), cskv::ROWS_THREADS, use.rows_smem, &k, st);
     if (s != CS_OK || max_rows <= k.b.group || k.c.flat) return s;

@@ -234,3 +234,7 @@ def test_another_device_and_bad_prefixes(cs):
     for pages in (None, torch.zeros(4), torch.zeros(2, 2, dtype=torch.int32)):
         with pytest.raises((TypeError, ValueError), match="prefix_pages"):
             cs.cs_kv4_attention_shared(plan, batch, row, pair, pair, pages, 20, row, stream=0)
+
+
+def test_long_items_of_few_rows_are_cut(tmp_path):
+    assert kv_programs.run("kv4_uncut_check", tmp_path) == (0, "ok")
