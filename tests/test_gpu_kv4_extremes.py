@@ -176,3 +176,32 @@ def test_values_beyond_f16_at_keys_hidden_from_some_rows(q, kv, head_dim, window
             ok[dims] = not hit
             assert (np.abs(got[t, :, ok] - ref[t, :, ok]) <= bound[t, :, ok]).all(), (s, i)
             t += 1
+
+
+@pytest.mark.parametrize("dtype,d", [(F16, 64), (F16, 128), (BF16, 64), (BF16, 128)])
+def test_no_byte_reads_back_as_what_it_does_not_stand_for(dtype, d):
+    """Every scale under every code: what the dtype holds is exact, what it does not hold is infinite with its sign, and under the
+    eight scales that stand for no number nothing is finite."""
+    scale = np.repeat(np.arange(256), 16).reshape(-1, 1)  # [rows, 1]: each scale under 16 rotations of the codes
+    code = (np.arange(d) % 16 - 8 + np.tile(np.arange(16), 256).reshape(-1, 1) + 8) % 16 - 8
+    rows = len(scale)
+    codes = torch.from_numpy(o4.pack(code.astype(np.int8))).view(rows // 16, 16, 1, d // 2).cuda()
+    scales = torch.from_numpy(np.repeat(scale, d // 32, 1).astype(np.uint8)).view(rows // 16, 1, 16, d // 32).cuda()
+    plan = cs.cs_kv_plan(cs.cs_kv_desc_init(dtype=dtype, heads=1, kv_heads=1, head_dim=d, num_pages=rows // 16, max_tokens=rows,
+                                            max_seqs=1))
+    batch = cs.cs_kv_batch(plan, torch.tensor([0, rows], dtype=torch.int32, device="cuda"),
+                           torch.tensor([rows], dtype=torch.int32, device="cuda"),
+                           torch.arange(rows // 16, dtype=torch.int32, device="cuda")[None], tokens=rows, max_q=rows)
+    k, v = (torch.empty(rows, 1, d, dtype=dtype, device="cuda") for _ in range(2))
+    cs.cs_kv4_read(plan, batch, (codes, scales), (codes, scales), k, v)
+    torch.cuda.synchronize()
+    assert cs.cs_kv_status(plan) == cs.CS_OK
+    with np.errstate(invalid="ignore"):
+        want = code * o4.SCALES[scale]
+    named = np.isfinite(want)
+    fits = named & (np.abs(np.where(named, want, 0)) <= torch.finfo(dtype).max)
+    for got in (okv.to64(k)[:, 0], okv.to64(v)[:, 0]):
+        assert (got[fits] == want[fits]).all()
+        assert (got[named & ~fits] == np.sign(want[named & ~fits]) * np.inf).all()
+        assert not np.isfinite(got[~named]).any()
+    assert (named & ~fits).any() == (dtype == F16)
