@@ -99,7 +99,8 @@ __device__ __forceinline__ uint32_t code_word(const float (&y)[8], float inv, bo
 // the lane that holds it and a group's maximum from its four lanes.  A warp has a token (or part of one) and looks its
 // place up for itself: lookups by some warps of a block for all its tokens, behind a barrier, were slower (82.8 and 77.6 us).
 // Bound by instructions and DRAM alike: 19743 tokens of 32 + 2 x 8 heads of 128 (435 MB): 77.6 us, 5.6 TB/s, 0.83 of a
-// plain copy's measured 6.8; issue slots are 74 % busy, DRAM 55 %.  (The 16-bit cache's append, which moves 495 MB and
+// plain copy's measured 6.8.  (16000 of them, 66 us: 2.8 of 4 instructions a cycle, the busiest pipe 48 %, DRAM 60 %; warps
+// wait for loads most.  A sixth block an SM makes it 12 bytes of spills a thread.)  (The 16-bit cache's append, which moves 495 MB and
 // makes nothing of them, takes 74.)  247 single tokens of 40 + 2 x 8 heads of 64: 3.2 us, one token alone 3.1, launch and lookups.
 template <typename T>
 __global__ void __launch_bounds__(FOUR_THREADS, 6) cs_kv4_append_kernel(const __grid_constant__ Four4P p) {

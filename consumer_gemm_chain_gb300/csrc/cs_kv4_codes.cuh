@@ -7,6 +7,9 @@
 // 7, which both 16-bit types hold, so what follows works with the values themselves and
 // rounds nothing.  Of the 8 values in a 32-bit word, value 2 j lies at bit 4 j and value
 // 2 j + 1 at bit 16 + 4 j: a mask then picks a pair in its 16-bit halves, in order.
+//
+// Code bits put under a constant exponent are a number without a conversion: the method of Kim, Henry, Fahim and
+// Hassan Awadalla, "Who Says Elephants Can't Run: Bringing Large Scale MoE Models into Cloud Scale Production" (2022).
 #pragma once
 #include "cs_kv_append.cuh"
 

@@ -21,14 +21,16 @@
 // Row r of S^T's 8-row half is key r / 2 (r even) or 7 - r / 2 (r odd) of 8: with it all reads
 // of the codes from shared memory are free of bank conflicts.
 //
-// Bound.  Instructions: 318 for 16 keys of 128 dimensions and a warp, about half of them to make operands of codes, at
-// 2.3 of 4 a cycle (the pipe of shifts, masks and byte selections is busy in 47 % of the cycles, DRAM in 54 %).
-// 62 single tokens over 300 to 32000 keys, 64 / 8 heads of 128 (1.13 GB): 243 us, 4.7 TB/s, 0.69 of a plain copy's
-// measured 6.8; the 16-bit cache (4.26 GB) takes 664 to 692.  128 tokens under a window of 1024, 40 / 8 heads of 64:
-// 37.5 us, of which the start of a launch, its division and its last joins are about 13.  One user's token over 978
+// Bound.  Instructions and their latency together: 338 (f16 318) for 16 keys of 128 dimensions and a warp, about half of them
+// to make operands of codes, at 2.3 of 4 a cycle; no unit is full (the pipe of shifts, masks and byte selections is busy in 47 %
+// of the cycles, DRAM in 53 %), and 12 warps an SM leave waits uncovered.
+// 62 single tokens over 300 to 32000 keys, 64 / 8 heads of 128 (1.13 GB): 247 us, 4.6 TB/s, 0.68 of a plain copy's
+// measured 6.8; the 16-bit cache (4.26 GB) takes 664 to 692.  32 x 4 tokens over 8000 keys, 32 / 8 heads of 128: 112 us (f16
+// 107), over 16 bits 191.  128 tokens under a window of 1024, 40 / 8 heads of 64:
+// 37.7 us, of which the start of a launch, its division and its last joins are about 13.  One user's token over 978
 // keys, 12 heads: 9.1 us, the latency of its steps, as over the 16-bit cache; over 16000 keys, 8 heads: 25.5.
-// Slower or no faster: the next keys' scores before the softmax of these (267 us for 64 sequences of 16000 keys instead
-// of 243), leaving out runs that no row sees (251), items' first copies sent off while the item before is stored (81
+// Slower or no faster: the next keys' scores before the softmax of these (267 us for 64 sequences of 16000 keys where it
+// took 243), leaving out runs that no row sees (251), items' first copies sent off while the item before is stored (81
 // and 81 us for 256000 keys), runs one by one in half the code (84), right shifts as products' upper halves (96),
 // prefetches of whole lines, five CTAs an SM (98), two with 16 columns (118 and 114).
 #pragma once
@@ -40,7 +42,8 @@ namespace cskv {
 
 // CTAs of four warps per SM.  Three leave a thread 168 registers, four 128, into which 8 columns just fit; at 128 dimensions
 // independent work is worth more than warps (64 sequences of 16000 keys 247 us with three, 261 with four), at 64 it
-// is not (182 and 171).
+// is not (182 and 171).  With 16 columns at 128 dimensions three CTAs spill 70 to 120 bytes a thread, and are
+// faster than two without spills (114 and 118).
 template <int D, int NT>
 constexpr int ROWS4_CTAS = D == 64 && NT == 1 ? 4 : 3;
 

@@ -80,8 +80,11 @@ constexpr int ATTN_THREADS_OF = FOUR ? 512 : 384;
 constexpr int ATTN_THREADS = ATTN_THREADS_OF<false>;
 // Registers: 65536 / 384 gives every thread 168 at launch; a softmax thread holds a
 // row of S, so the third warpgroup hands over what it does not need
-// (2 x 216 + 72 = 3 x 168; with a fourth 2 x 200 + 2 x 56 = 4 x 128).  Nothing may spill: next to
-// 226 KB of shared memory the L1 holds nearly nothing, and a spilled register comes back from L2.
+// (2 x 216 + 72 = 3 x 168; with a fourth 2 x 192 + 2 x 64 or 2 x 200 + 2 x 56 = 4 x 128).  Next to 226 KB of shared memory
+// the L1 holds nearly nothing, and a spilled register comes back from L2: what spilled the prefetch of a loop cost 10 to 200 %.
+// Over 4 bits some variants still spill a few bytes a thread (64 wide 16, under a window 60, 128 wide under a window 44), which
+// cannot be seen in their times: prompts of 8192 tokens, 64 wide 438 us, over 16 bits 403; under a window of 1024 180 and 173,
+// 128 wide 174 and 168; 128 wide without a window, which spills nothing, 431 and 408.
 template <int D, bool FOUR>
 struct AttnRegs {
   static constexpr int SOFTMAX = FOUR ? (D == 128 ? 192 : 200) : 216;
