@@ -90,7 +90,8 @@ typedef struct cs_kv4_attn_args {
 
 /* cs_kv_attention (cs_kv_attention_shared) over a cache in 4 bits: scores, sums and
  * O in 32 bits of the exact values, the weights rounded to the dtype for the product with V.  (f16 has
- * no weights below 2^-25 of a row's largest, with at most 16 rows per key head 2^-32.) */
+ * no weights below 2^-25 of a row's largest, with at most 16 rows per key head 2^-32.  There lse is too small where a row's
+ * largest query times the scale is beyond 2^134, scores that nearly always overflow.) */
 cs_status cs_kv4_attention(cs_kv_t plan, const cs_kv_batch* batch, const cs_kv4_attn_args* args, void* stream);
 cs_status cs_kv4_attention_shared(cs_kv_t plan, const cs_kv_batch* batch, const int32_t* prefix_pages, int prefix_len,
                                   const cs_kv4_attn_args* args, void* stream);
