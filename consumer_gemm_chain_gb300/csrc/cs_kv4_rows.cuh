@@ -52,6 +52,9 @@ constexpr int ROWS4_SHIFT = 7;  // keys of a tile: 128, two runs of 16 for each 
 // A row's reference lies 2^7 below a score of its own, so its weights are at most 2^15: as far from f16's end as that
 // goes, and 2^7 more of what f16 has at its other end.
 constexpr float WEIGHT_LOG2 = 7.0f;
+// Beyond +-2^20 a reference in 32 bits is off by more than a sixteenth, and the multiply-add, which rounds once, would show it
+// in the weights: there scores are taken off one another before the factor.
+constexpr float FAR_LOG2 = 1048576.0f;
 
 template <int D>
 struct Stage4 {  // a warp's keys of a tile: codes of K and V, their scales
@@ -379,17 +382,18 @@ __global__ void __launch_bounds__(ROWS_THREADS, ROWS4_CTAS<D, NT>) cs_kv4_rows_k
               top[n][e] = fmaxf(s[0][n][e], s[0][n][2 + e]);
               if (XS == 2) top[n][e] = max3(top[n][e], s[XS - 1][n][e], s[XS - 1][n][2 + e]);
               // raised only when it is exceeded by more than 2^8 (from -infinity by anything but that)
-              raise |= fmaf(top[n][e], unit[n][e], -m_ref[n][e]) > RAISE_LOG2 + WEIGHT_LOG2;
+              raise |= fmaf(top[n][e], unit[n][e], -m_ref[n][e]) > RAISE_LOG2 + WEIGHT_LOG2 || fabsf(m_ref[n][e]) > FAR_LOG2;
             }
+          float sub[NT][2];
           if (__any_sync(0xFFFFFFFFu, raise)) {
 #pragma unroll
             for (int n = 0; n < NT; ++n)
 #pragma unroll
               for (int e = 0; e < 2; ++e) {
-                float m = top[n][e];
+                float t = top[n][e];
 #pragma unroll
-                for (int d = 4; d < 32; d <<= 1) m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, d));
-                m = fmaf(m, unit[n][e], -WEIGHT_LOG2);
+                for (int d = 4; d < 32; d <<= 1) t = fmaxf(t, __shfl_xor_sync(0xFFFFFFFFu, t, d));
+                const float m = fmaf(t, unit[n][e], -WEIGHT_LOG2);
                 // (scores that overflow: -infinity raises nothing, as a hidden key; a reference of infinity makes the row NaN
                 // when the warps' states are joined)
                 if (m - m_ref[n][e] > RAISE_LOG2) {
@@ -399,18 +403,28 @@ __global__ void __launch_bounds__(ROWS_THREADS, ROWS4_CTAS<D, NT>) cs_kv4_rows_k
 #pragma unroll
                   for (int i = 0; i < 4 * VW; ++i) o[n][i][e] *= f, o[n][i][2 + e] *= f;
                 }
+                sub[n][e] = m_ref[n][e] == -INFINITY ? 0.0f : -m_ref[n][e];
+                if (fabsf(m) > FAR_LOG2 && fabsf(m) < INFINITY) {  // differences before the factor
+                  sub[n][e] = m - m_ref[n][e] + WEIGHT_LOG2;
+#pragma unroll
+                  for (int x = 0; x < XS; ++x) s[x][n][e] -= t, s[x][n][2 + e] -= t;
+                }
               }
+          } else {
+#pragma unroll
+            for (int n = 0; n < NT; ++n)
+#pragma unroll
+              for (int e = 0; e < 2; ++e) sub[n][e] = -m_ref[n][e];
           }
           uint32_t pt[XS][NT][2];
 #pragma unroll
           for (int n = 0; n < NT; ++n) {
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
-              const float sub = m_ref[n][e] == -INFINITY ? 0.0f : -m_ref[n][e];
 #pragma unroll
               for (int x = 0; x < XS; ++x) {
-                s[x][n][e] = cs::ex2_approx(fmaf(s[x][n][e], unit[n][e], sub));
-                s[x][n][2 + e] = cs::ex2_approx(fmaf(s[x][n][2 + e], unit[n][e], sub));
+                s[x][n][e] = cs::ex2_approx(fmaf(s[x][n][e], unit[n][e], sub[n][e]));
+                s[x][n][2 + e] = cs::ex2_approx(fmaf(s[x][n][2 + e], unit[n][e], sub[n][e]));
                 l[n][e] += s[x][n][e] + s[x][n][2 + e];
               }
             }

@@ -205,3 +205,33 @@ def test_no_byte_reads_back_as_what_it_does_not_stand_for(dtype, d):
         assert (got[named & ~fits] == np.sign(want[named & ~fits]) * np.inf).all()
         assert not np.isfinite(got[~named]).any()
     assert (named & ~fits).any() == (dtype == F16)
+
+
+@pytest.mark.parametrize("dtype", [F16, BF16])
+@pytest.mark.parametrize("exponent", [0, 18, 22, 24, 26, 28, 30, 40, 70, 110])
+@pytest.mark.parametrize("heads,tokens,d", [(8, 1, 128), (8, 1, 64), (16, 1, 128), (4, 3, 64)])
+def test_scores_far_from_zero(dtype, exponent, heads, tokens, d):
+    """Scores of up to 2^exponent times 40, where a step of 32 bits is many units: keys with the largest share the weight, the others have
+    none of it.  Positive and negative ones, and some that rise from tile to tile.
+
+    u |O| and u sum(w |v|) for roundings, 2^-11 sum(w |v|) for the sums; scores are products of one dimension each."""
+    keys, scale = 400, 2.0 ** exponent
+    g = torch.Generator().manual_seed(exponent)
+    q, k = torch.zeros(tokens, heads, d, dtype=torch.float64), torch.zeros(keys, 1, d, dtype=torch.float64)
+    v = torch.randn(keys, 1, d, generator=g).double()
+    j = torch.arange(keys)
+    k[:, 0, 0] = 3.5 + 0.25 * (j % 3)
+    k[:, 0, 32] = 1.0 + (j // 32) * 0.125
+    q[:, 0, 0], q[:, 1, 0], q[:, 2, 32], q[:, 3, 32] = 5.3125, -5.3125, 4.6875, -4.6875
+    if exponent == 0:
+        q *= 8
+    q = q.to(dtype).double()
+    out, lse = attend(q, k, v, dtype, scale=scale)
+    held_k, held_v = o4.held(k), o4.held(v)
+    u = torch.finfo(dtype).eps / 2
+    for t in range(tokens):
+        seen = np.arange(keys) <= keys - tokens + t
+        for h in range(heads):
+            o, z, a = okv.attend(q[t, h].numpy(), held_k[:, 0], held_v[:, 0], seen, scale)
+            assert (np.abs(out[t, h] - o) <= u * np.abs(o) + (u + 2.0 ** -11) * a).all(), (t, h)
+            assert abs(lse[t, h] - z) <= 2.0 ** -11 + 2.0 ** -20 * abs(z), (t, h)
