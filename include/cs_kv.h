@@ -135,7 +135,8 @@ typedef struct cs_kv_attn_args {
 /* O = softmax(scale Q K^T over the visible keys) V for every new token and head,
  * scores, sums and O in 32 bits (the weights enter the product with V rounded to
  * the dtype).  A token that sees no key (before position 0) gets O = 0 and
- * lse = -inf, and so does one whose scores are all -infinity.  Nothing that the cache holds at hidden keys changes a result. */
+ * lse = -inf, and so does one whose scores are all -infinity.  With more than 16 rows per key
+ * head a row whose scores lie beyond 9e7 (f16) or 1.4e9 (bf16) from 0 is NaN.  Nothing that the cache holds at hidden keys changes a result. */
 cs_status cs_kv_attention(cs_kv_t plan, const cs_kv_batch* batch, const cs_kv_attn_args* args, void* stream);
 
 /* The same where every sequence's keys follow one common prefix of prefix_len

@@ -1,6 +1,8 @@
 """The paged cache in 4 bits on the GPU where numbers come near the ends of their types."""
 from __future__ import annotations
 
+import math
+
 import numpy as np
 import pytest
 import torch
@@ -207,15 +209,10 @@ def test_no_byte_reads_back_as_what_it_does_not_stand_for(dtype, d):
     assert (named & ~fits).any() == (dtype == F16)
 
 
-@pytest.mark.parametrize("dtype", [F16, BF16])
-@pytest.mark.parametrize("exponent", [0, 18, 22, 24, 26, 28, 30, 40, 70, 110])
-@pytest.mark.parametrize("heads,tokens,d", [(8, 1, 128), (8, 1, 64), (16, 1, 128), (4, 3, 64)])
-def test_scores_far_from_zero(dtype, exponent, heads, tokens, d):
-    """Scores of up to 2^exponent times 40, where a step of 32 bits is many units: keys with the largest share the weight, the others have
-    none of it.  Positive and negative ones, and some that rise from tile to tile.
-
-    u |O| and u sum(w |v|) for roundings, 2^-11 sum(w |v|) for the sums; scores are products of one dimension each."""
-    keys, scale = 400, 2.0 ** exponent
+def far_case(dtype, exponent, heads, tokens, d):
+    """(q, k, v, scale): scores of up to 2^exponent times 40, where a step of 32 bits is many units: keys with the largest share the
+    weight, the others have none of it.  Positive and negative ones, and some that rise from tile to tile."""
+    keys = 400
     g = torch.Generator().manual_seed(exponent)
     q, k = torch.zeros(tokens, heads, d, dtype=torch.float64), torch.zeros(keys, 1, d, dtype=torch.float64)
     v = torch.randn(keys, 1, d, generator=g).double()
@@ -225,7 +222,14 @@ def test_scores_far_from_zero(dtype, exponent, heads, tokens, d):
     q[:, 0, 0], q[:, 1, 0], q[:, 2, 32], q[:, 3, 32] = 5.3125, -5.3125, 4.6875, -4.6875
     if exponent == 0:
         q *= 8
-    q = q.to(dtype).double()
+    return q.to(dtype).double(), k, v, 2.0 ** exponent
+
+
+def far_rows(q, k, v, dtype, scale):
+    """(row, head, is right, lse) of each: within u |O| and u sum(w |v|) for roundings and 2^-11 sum(w |v|) for the sums; scores are
+    products of one dimension each."""
+    tokens, heads, _ = q.shape
+    keys = len(k)
     out, lse = attend(q, k, v, dtype, scale=scale)
     held_k, held_v = o4.held(k), o4.held(v)
     u = torch.finfo(dtype).eps / 2
@@ -233,5 +237,28 @@ def test_scores_far_from_zero(dtype, exponent, heads, tokens, d):
         seen = np.arange(keys) <= keys - tokens + t
         for h in range(heads):
             o, z, a = okv.attend(q[t, h].numpy(), held_k[:, 0], held_v[:, 0], seen, scale)
-            assert (np.abs(out[t, h] - o) <= u * np.abs(o) + (u + 2.0 ** -11) * a).all(), (t, h)
-            assert abs(lse[t, h] - z) <= 2.0 ** -11 + 2.0 ** -20 * abs(z), (t, h)
+            right = (np.abs(out[t, h] - o) <= u * np.abs(o) + (u + 2.0 ** -11) * a).all() and \
+                abs(lse[t, h] - z) <= 2.0 ** -11 + 2.0 ** -20 * abs(z)
+            yield right, np.isnan(out[t, h]).all() and np.isnan(lse[t, h]), abs(z) / math.log(2)
+
+
+EXPONENTS = [0, 18, 20, 22, 24, 26, 28, 30, 40, 70, 110]
+
+
+@pytest.mark.parametrize("dtype", [F16, BF16])
+@pytest.mark.parametrize("exponent", EXPONENTS)
+@pytest.mark.parametrize("heads,tokens,d", [(8, 1, 128), (8, 1, 64), (16, 1, 128), (4, 3, 64)])
+def test_scores_far_from_zero(dtype, exponent, heads, tokens, d):
+    q, k, v, scale = far_case(dtype, exponent, heads, tokens, d)
+    assert all(right for right, _, _ in far_rows(q, k, v, dtype, scale))
+
+
+@pytest.mark.parametrize("dtype,limit", [(F16, 2.0 ** 27), (BF16, 2.0 ** 31)])
+@pytest.mark.parametrize("exponent", EXPONENTS)
+@pytest.mark.parametrize("heads,tokens,d", [(4, 40, 128), (4, 150, 64), (4, 300, 128)])
+def test_scores_far_from_zero_of_many_rows(dtype, limit, exponent, heads, tokens, d):
+    """Beyond the limit (of base-2 scores, whose largest in a tile is within a third of the row's here) rows are NaN."""
+    q, k, v, scale = far_case(dtype, exponent, heads, tokens, d)
+    for right, nan, size in far_rows(q, k, v, dtype, scale):
+        assert right or (nan and size >= 0.6 * limit), size
+        assert nan or size <= limit, size
