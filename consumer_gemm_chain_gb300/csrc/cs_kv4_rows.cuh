@@ -27,7 +27,7 @@
 // 62 single tokens over 300 to 32000 keys, 64 / 8 heads of 128 (1.13 GB): 247 us, 4.6 TB/s, 0.68 of a plain copy's
 // measured 6.8; the 16-bit cache (4.26 GB) takes 664 to 692.  32 x 4 tokens over 8000 keys, 32 / 8 heads of 128: 112 us (f16
 // 107), over 16 bits 191.  128 tokens under a window of 1024, 40 / 8 heads of 64:
-// 37.7 us, of which the start of a launch, its division and its last joins are about 13.  One user's token over 978
+// 38.2 us, of which the start of a launch, its division and its last joins are about 13.  One user's token over 978
 // keys, 12 heads: 9.1 us, the latency of its steps, as over the 16-bit cache; over 16000 keys, 8 heads: 25.5.
 // Slower or no faster: the next keys' scores before the softmax of these (267 us for 64 sequences of 16000 keys where it
 // took 243), leaving out runs that no row sees (251), items' first copies sent off while the item before is stored (81
